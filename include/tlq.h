@@ -569,6 +569,170 @@ tlq_status tl_loop_block_forward_static_scratch(float* x, const tl_block* block,
 tlq_status tl_probe_read_bandwidth(const void* buf, size_t bytes, int reps, uint32_t* sink, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Multi-request serving beside the quantized projections: a paged cache of
+ * keys and values in 4 bits with the attention that reads it, the tables of a
+ * step's requests, and low-rank adapters per request.
+ *
+ * Source: "Model", section "VRAM cost" (INT4 cache mode) and "Chunked
+ * prefill" (queries of a chunk over everything cached before it);
+ * "Prefix pool" (requests of different lengths over shared cached pages).
+ * The pages fix neither layout nor formulas; the ones below are this
+ * library's.  Activations are FP16 like those of every GEMM here.
+ *
+ * Cache blocks.  `blocks` is [num_pages][heads][tl_kv4_block_bytes] bytes; the
+ * block of one page and key head holds, one after another,
+ *   key codes    [page_size][head_dim/2] bytes
+ *   value codes  [page_size][head_dim/2] bytes
+ *   key parameters   [page_size][head_dim/group] pairs of FP16 (scale, minimum)
+ *   value parameters [page_size][head_dim/group] pairs of FP16 (scale, minimum)
+ * Code rows pack channels as tl_pack_weights packs a weight row (least
+ * significant first); a channel stands for code * scale + minimum.  A token's
+ * slot is page * page_size + offset.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct {
+  void* blocks;      /* device, 16-byte aligned */
+  int64_t num_pages; /* 1 .. 2^31 - 1 */
+  int heads;         /* key (and value) heads, 1 .. 4096 */
+  int head_dim;      /* 64 or 128 */
+  int page_size;     /* tokens of a page: 16, 32, 64, 128 or 256 */
+  int group;         /* channels that share a scale and a minimum: 64 or 128, dividing head_dim */
+} tl_kv4_cache;
+
+/* Bytes of one page and head of the cache; 0 for a geometry the library does
+ * not take (tl_last_error says why). */
+size_t tl_kv4_block_bytes(int page_size, int head_dim, int group);
+
+/*
+ * tl_kv_plan -- block tables, slots and positions of one step's tokens, from
+ * the requests' lengths, on the GPU (no host copy of a length is needed).
+ *
+ *   Request b has cached[b] tokens in the cache and brings added[b] (either
+ *   may be 0; negative counts as 0).  The step's tokens are laid out request
+ *   after request.  Pages that a request does not hold yet are taken from
+ *   free_pages in request order, beginning at *free_head:
+ *     held = ceil(cached/page_size), need = ceil((cached+added)/page_size) - held
+ *     table[b][held + i] = free_pages[*free_head + (need of earlier requests) + i]
+ *
+ *   cached, added  int32 [requests]
+ *   table          int32 [requests][ld_table], read for pages held, written
+ *                  for new ones (other entries are left as they are)
+ *   free_pages     int32 [num_free] page ids; free_head: device int32 or NULL (0)
+ *   num_pages      pages of the cache; a page id outside it gives slot -1
+ *   q_start        out int32 [requests + 1], exclusive sums of added
+ *   seq_lens       out int32 [requests], cached + added
+ *   token_req, token_pos, slots   out [capacity] (int32, int32, int64): each
+ *                  token's request, its position in the request and its slot;
+ *                  -1 behind the last token
+ *   counts         out int32 [4]: tokens, pages taken, the free list's next
+ *                  head, and pages that were needed but not to be had (the
+ *                  list ended, or the table row did): their entries and slots
+ *                  are -1
+ *   Tokens beyond capacity are left out of the token arrays.  Outputs overlap
+ *   neither an input nor each other (free_head may not point into counts: two
+ *   counts buffers in turn carry the head from step to step).  page_size: a
+ *   power of two.  Deterministic; the same inputs give the same tables, so a
+ *   call can be repeated.  Returns TLQ_OK, TLQ_EINVAL or TLQ_ECUDA.
+ */
+tlq_status tl_kv_plan(const int32_t* cached, const int32_t* added, int requests, int32_t* table, int ld_table,
+                      const int32_t* free_pages, int num_free, const int32_t* free_head, int page_size,
+                      int64_t num_pages, int32_t* q_start, int32_t* seq_lens, int32_t* token_req, int32_t* token_pos,
+                      int64_t* slots, int capacity, int32_t* counts, void* stream);
+
+/*
+ * tl_kv4_append -- keys and values of `tokens` tokens quantized into the cache.
+ *
+ *   Per token, head and group of channels (binary32, rounded to nearest even
+ *   after every step):
+ *     minimum = fp16(min x), scale = max(fp16((max x - min x) / 15), 2^-24)
+ *     code = clamp(rint((x - minimum) / scale), 0, 15)
+ *   k, v   FP16 [tokens][heads][head_dim] with token strides ldk, ldv (in
+ *          elements, multiples of 8; the columns of a fused qkv projection's
+ *          rows are taken as they lie); 16-byte aligned; finite
+ *   slots  int64 [tokens]; slots outside the cache (-1) are passed over; a
+ *          call's slots are distinct
+ *   Bit-exact; deterministic.  Returns TLQ_OK, TLQ_EINVAL, TLQ_EUNSUPPORTED
+ *   (a head_dim or group that is not taken) or TLQ_ECUDA.
+ */
+tlq_status tl_kv4_append(const tl_kv4_cache* cache, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                         const int64_t* slots, int tokens, void* stream);
+
+/*
+ * tl_kv4_read -- the values that cached tokens stand for: k, v FP16
+ * [tokens][heads][head_dim] compact, fp16(code * scale + minimum) rounded once
+ * more from binary32; zeros for slots outside the cache.  Errors as
+ * tl_kv4_append.
+ */
+tlq_status tl_kv4_read(const tl_kv4_cache* cache, const int64_t* slots, int tokens, uint16_t* k, uint16_t* v,
+                       void* stream);
+
+/*
+ * tl_kv4_attention -- causal attention of a step's queries over the cache.
+ *
+ *   Request b's queries are rows q_start[b] .. q_start[b+1] - 1; the last of
+ *   them sits at position seq_lens[b] - 1, and a query at position p sees the
+ *   request's tokens 0 .. p (window > 0: the last `window` of them).  Query
+ *   head i reads key head i / (q_heads / heads).
+ *     out = softmax(scale * q . k) v
+ *   Sums and softmax statistics are FP32; weights are rounded to FP16 for the
+ *   second product.  A query that sees no key (seq_lens[b] smaller than the
+ *   request's queries, or none of its pages in the cache) gives zeros.
+ *
+ *   q, out    FP16 [tokens][q_heads][head_dim], token strides ldq, ldo
+ *             (elements, multiples of 8), 16-byte aligned; out overlaps no
+ *             other buffer
+ *   q_start   int32 [requests + 1], seq_lens int32 [requests], table int32
+ *             [requests][ld_table]: page ids of each request's tokens (device;
+ *             what tl_kv_plan writes).  seq_lens counts the step's own tokens,
+ *             which tl_kv4_append has put into the cache.  Entries that no
+ *             visible token lies in are not read as pages; a page id outside
+ *             the cache counts as holding no tokens
+ *   tokens    rows of q; queries outside [0, tokens) count as none, rows of
+ *             no request are not written
+ *   max_q     the most queries that a request has (an upper bound will do;
+ *             a request's further queries are left out)
+ *   workspace device, 16-byte aligned, of tl_kv4_attention_workspace_size
+ *             bytes or more; undefined afterwards, no contents needed before.
+ *             Calls whose executions overlap need separate workspaces
+ *   Lengths are read on the GPU only, so a captured call can be replayed as
+ *   requests grow.  Deterministic.  Returns TLQ_OK, TLQ_EINVAL,
+ *   TLQ_EUNSUPPORTED or TLQ_ECUDA.
+ */
+tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_t ldq, int q_heads, uint16_t* out,
+                            int64_t ldo, const int32_t* q_start, const int32_t* seq_lens, const int32_t* table,
+                            int ld_table, int requests, int tokens, int max_q, float scale, int window,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that tl_kv4_attention takes (the same for every batch of
+ * up to max_q queries a request); 0 for arguments it would not take. */
+size_t tl_kv4_attention_workspace_size(int q_heads, int heads, int head_dim, int max_q);
+
+/*
+ * tl_lora_add -- low-rank adapters of many requests beside a shared projection:
+ *
+ *   out[t] = fp16( y[t] + scales[a] * B[a] (A[a] x[t]) ),  a = adapters[b] of
+ *   the token's request b; both products in FP32, one rounding.
+ *
+ *   x        FP16 [tokens][K], stride ldx; the projection's input
+ *   y, out   FP16 [tokens][N], strides ldy, ldo; the projection's output; out
+ *            may be exactly y, else overlaps no input
+ *   A        FP16 [num_adapters][rank][K];  B  FP16 [num_adapters][N][rank]
+ *   scales   FP32 [num_adapters]
+ *   q_start  int32 [requests + 1] as in tl_kv4_attention; adapters int32
+ *            [requests], outside 0 .. num_adapters - 1: none (out = y)
+ *   K, N     multiples of 8; rank a multiple of 8 up to 64
+ *   x, A, B, y and out 16-byte aligned, strides multiples of 8 elements.
+ *   max_q as in tl_kv4_attention; rows of no request are not written.
+ *   Deterministic.  Returns TLQ_OK, TLQ_EINVAL, TLQ_EUNSUPPORTED (rank above
+ *   64) or TLQ_ECUDA.
+ */
+tlq_status tl_lora_add(const uint16_t* x, int64_t ldx, const uint16_t* A, const uint16_t* B, const float* scales,
+                       const int32_t* q_start, const int32_t* adapters, int requests, int tokens, int max_q, int K,
+                       int N, int rank, int num_adapters, const uint16_t* y, int64_t ldy, uint16_t* out, int64_t ldo,
+                       void* stream);
+
+/*
  * Synchronize `stream` and report the device status word: TLQ_OK, or
  * TLQ_ETIMEOUT if a kernel gave up on a bounded wait since the last
  * tl_reset_status().  Also returns TLQ_ECUDA on an asynchronous CUDA error.

@@ -26,6 +26,8 @@ __all__ = [
     "tl_quant_gemm_ws", "tl_quant_gemm_workspace_size", "tl_quant_gemm_swiglu_ws", "tl_loop_block_to_int2",
     "tl_swiglu_block_to_int2", "gemm_workspace", "requant_descs", "tl_probe_read_bandwidth",
     "tl_loop_block_l2_plan", "tl_prefill_plan",
+    "tl_kv4_block_bytes", "tl_kv_plan", "tl_kv4_append", "tl_kv4_read", "tl_kv4_attention",
+    "tl_kv4_attention_workspace_size", "tl_lora_add", "KV4Cache", "kv4_attention", "lora_add",
 ]
 
 # every symbol include/tlq.h declares
@@ -37,7 +39,8 @@ EXPORTED = (
     "tl_dequant_fp16", "tl_loop_block_forward_chunked", "tl_swiglu_block_forward_chunked",
     "tl_quant_gemm_batched_host", "tl_quant_gemm_ws", "tl_quant_gemm_workspace_size", "tl_quant_gemm_swiglu_ws",
     "tl_loop_block_to_int2", "tl_swiglu_block_to_int2", "tl_probe_read_bandwidth", "tl_loop_block_l2_plan",
-    "tl_prefill_plan",
+    "tl_prefill_plan", "tl_kv4_block_bytes", "tl_kv_plan", "tl_kv4_append", "tl_kv4_read", "tl_kv4_attention",
+    "tl_kv4_attention_workspace_size", "tl_lora_add",
 )
 
 TLQ_OK, TLQ_EINVAL, TLQ_EUNSUPPORTED, TLQ_ECUDA, TLQ_ETIMEOUT = 0, 1, 2, 3, 4
@@ -83,6 +86,11 @@ class _SwigluBlock(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class _KV4Cache(ctypes.Structure):
+    _fields_ = [("blocks", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int), ("group", ctypes.c_int)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -107,6 +115,8 @@ def load():
                                % _LIB_PATH)
         lib = ctypes.CDLL(_LIB_PATH)
         P, I, U = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint
+        L, Z, F = ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+        KV = ctypes.POINTER(_KV4Cache)
         sigs = {
             "tl_last_error": ([], ctypes.c_char_p),
             "tl_version": ([], ctypes.c_char_p),
@@ -138,6 +148,13 @@ def load():
             "tl_probe_read_bandwidth": ([P, ctypes.c_size_t, I, P, P], I),
             "tl_loop_block_l2_plan": ([ctypes.POINTER(_Block), I, ctypes.POINTER(ctypes.c_int),
                                        ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)], I),
+            "tl_kv4_block_bytes": ([I, I, I], Z),
+            "tl_kv_plan": ([P, P, I, P, I, P, I, P, I, L, P, P, P, P, P, I, P, P], I),
+            "tl_kv4_append": ([KV, P, L, P, L, P, I, P], I),
+            "tl_kv4_read": ([KV, P, I, P, P, P], I),
+            "tl_kv4_attention": ([KV, P, L, I, P, L, P, P, P, I, I, I, I, F, I, P, Z, P], I),
+            "tl_kv4_attention_workspace_size": ([I, I, I, I], Z),
+            "tl_lora_add": ([P, L, P, P, P, P, P, I, I, I, I, I, I, I, P, L, P, L, P], I),
         }
         for name, (args, res) in sigs.items():
             f = getattr(lib, name)
@@ -474,6 +491,182 @@ def tl_selftest_wait_timeout(limit_us: int, stream=None) -> None:
 
 
 # ---------------------------------------------------------------------------
+# multi-request serving: paged 4-bit cache, attention, tables, adapters
+# ---------------------------------------------------------------------------
+
+def _rows(t, dtype, name, dims):
+    """Data pointer and token stride of a [tokens, ...] CUDA tensor whose rows
+    are contiguous (a token stride of its own is taken as it is)."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.dim() != len(dims) + 1 or any(d is not None and n != d for n, d in zip(t.shape[1:], dims)):
+        raise ValueError("%s has shape %s, expected [tokens%s]" % (name, tuple(t.shape),
+                                                                   "".join(", %s" % d for d in dims)))
+    inner = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if t.numel() > 0 and n != 1 and s != inner:
+            raise ValueError("%s: a token's values must be contiguous" % name)
+        inner *= n
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(inner, 8))
+
+
+def _ints(t, dtype, name, n=None):
+    p = _dev(t, (dtype,), name)
+    if n is not None and t.numel() != n:
+        raise ValueError("%s has %d elements, expected %d" % (name, t.numel(), n))
+    return p
+
+
+def _table(table, requests):
+    import torch
+
+    if not isinstance(table, torch.Tensor) or not table.is_cuda or table.dtype != torch.int32:
+        raise ValueError("table must be an int32 CUDA tensor")
+    if table.dim() != 2 or table.shape[0] != requests:
+        raise ValueError("table has shape %s, expected [%d, pages]" % (tuple(table.shape), requests))
+    if not table.is_contiguous():
+        raise ValueError("table must be contiguous")
+    return table.data_ptr(), table.shape[1]
+
+
+def tl_kv4_block_bytes(page_size: int, head_dim: int, group: int) -> int:
+    """Bytes of one page and head of a 4-bit cache."""
+    n = int(load().tl_kv4_block_bytes(page_size, head_dim, group))
+    if n == 0:
+        raise TLQError(TLQ_EINVAL, tl_last_error())
+    return n
+
+
+def tl_kv_plan(cached, added, table, free_pages, q_start, seq_lens, token_req, token_pos, slots, counts,
+               page_size: int, num_pages: int, free_head=None, stream=None) -> None:
+    """Block tables, slots and positions of a step's tokens (see include/tlq.h);
+    table and the arrays from q_start to counts are written."""
+    import torch
+
+    i32 = torch.int32
+    n = cached.numel()
+    room = slots.numel()
+    tp, width = _table(table, n)
+    _raise_if(load().tl_kv_plan(_ints(cached, i32, "cached"), _ints(added, i32, "added", n), n, tp, width,
+                                _ints(free_pages, i32, "free_pages"), free_pages.numel(),
+                                _ints(free_head, i32, "free_head", 1) if free_head is not None else None, page_size,
+                                num_pages, _ints(q_start, i32, "q_start", n + 1), _ints(seq_lens, i32, "seq_lens", n),
+                                _ints(token_req, i32, "token_req", room), _ints(token_pos, i32, "token_pos", room),
+                                _ints(slots, torch.int64, "slots"), room, _ints(counts, i32, "counts", 4),
+                                _stream(stream)))
+
+
+class KV4Cache:
+    """A paged cache of keys and values in 4 bits.
+
+    ``blocks`` (uint8 CUDA tensor [num_pages, heads, block bytes], allocated
+    here when not given) holds codes, scales and minima as include/tlq.h lays
+    them out; a page holds ``page_size`` tokens of every head."""
+
+    def __init__(self, num_pages: int, heads: int, head_dim: int, page_size: int = 16, group: int = 128,
+                 blocks=None, device="cuda"):
+        import torch
+
+        nb = tl_kv4_block_bytes(page_size, head_dim, group)
+        if blocks is None:
+            blocks = torch.empty((num_pages, heads, nb), dtype=torch.uint8, device=device)
+        if tuple(blocks.shape) != (num_pages, heads, nb):
+            raise ValueError("blocks has shape %s, expected %s" % (tuple(blocks.shape), (num_pages, heads, nb)))
+        self.blocks = blocks
+        self.num_pages, self.heads, self.head_dim = num_pages, heads, head_dim
+        self.page_size, self.group = page_size, group
+        self._c = _KV4Cache(_dev(blocks, (torch.uint8,), "blocks"), num_pages, heads, head_dim, page_size, group)
+
+    def attention_workspace(self, q_heads: int, max_q: int):
+        """A workspace tensor for tl_kv4_attention with up to max_q queries a
+        request (allocated by torch; keep it for all steps)."""
+        import torch
+
+        n = tl_kv4_attention_workspace_size(q_heads, self.heads, self.head_dim, max_q)
+        return torch.empty(n, dtype=torch.uint8, device=self.blocks.device)
+
+
+def tl_kv4_append(cache: KV4Cache, k, v, slots, stream=None) -> None:
+    """Quantize k, v [tokens, heads, head_dim] into the cache's slots."""
+    import torch
+
+    dims = (cache.heads, cache.head_dim)
+    kp, ldk = _rows(k, torch.float16, "k", dims)
+    vp, ldv = _rows(v, torch.float16, "v", dims)
+    n = slots.numel()
+    if k.shape[0] != n or v.shape[0] != n:
+        raise ValueError("k and v have %d and %d tokens, slots %d" % (k.shape[0], v.shape[0], n))
+    _raise_if(load().tl_kv4_append(ctypes.byref(cache._c), kp, ldk, vp, ldv, _ints(slots, torch.int64, "slots"), n,
+                                   _stream(stream)))
+
+
+def tl_kv4_read(cache: KV4Cache, slots, k, v, stream=None) -> None:
+    """The FP16 values of cached tokens into k, v [tokens, heads, head_dim]."""
+    import torch
+
+    n = slots.numel()
+    shape = (n, cache.heads, cache.head_dim)
+    for t, name in ((k, "k"), (v, "v")):
+        if tuple(t.shape) != shape:
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+    _raise_if(load().tl_kv4_read(ctypes.byref(cache._c), _ints(slots, torch.int64, "slots"), n,
+                                 _dev(k, (torch.float16,), "k"), _dev(v, (torch.float16,), "v"), _stream(stream)))
+
+
+def tl_kv4_attention_workspace_size(q_heads: int, heads: int, head_dim: int, max_q: int) -> int:
+    """Bytes of workspace tl_kv4_attention takes."""
+    return int(load().tl_kv4_attention_workspace_size(q_heads, heads, head_dim, max_q))
+
+
+def tl_kv4_attention(cache: KV4Cache, q, out, q_start, seq_lens, table, max_q: int, scale: float, window: int = 0,
+                     workspace=None, stream=None) -> None:
+    """Causal attention of q [tokens, q_heads, head_dim] over the cache into
+    out; workspace: cache.attention_workspace(q_heads, max_q)."""
+    import torch
+
+    qp, ldq = _rows(q, torch.float16, "q", (None, cache.head_dim))
+    op, ldo = _rows(out, torch.float16, "out", (q.shape[1], cache.head_dim))
+    if out.shape[0] != q.shape[0]:
+        raise ValueError("out has %d tokens, q %d" % (out.shape[0], q.shape[0]))
+    n = seq_lens.numel()
+    tp, width = _table(table, n)
+    ws = _dev(workspace, (torch.uint8,), "workspace") if workspace is not None else None
+    nb = workspace.numel() if workspace is not None else 0
+    _raise_if(load().tl_kv4_attention(ctypes.byref(cache._c), qp, ldq, q.shape[1], op, ldo,
+                                      _ints(q_start, torch.int32, "q_start", n + 1),
+                                      _ints(seq_lens, torch.int32, "seq_lens"), tp, width, n, q.shape[0], max_q,
+                                      scale, window, ws, nb, _stream(stream)))
+
+
+def tl_lora_add(x, A, B, scales, q_start, adapters, max_q: int, y, out, stream=None) -> None:
+    """out = y + scale * B[a] (A[a] x) per token, a the adapter of the token's
+    request; A [adapters, rank, K], B [adapters, N, rank], out may be y."""
+    import torch
+
+    f16 = torch.float16
+    if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
+        raise ValueError("A %s and B %s: expected [adapters, rank, K] and [adapters, N, rank]"
+                         % (tuple(A.shape), tuple(B.shape)))
+    num, rank, K = A.shape
+    N = B.shape[1]
+    xp, ldx = _rows(x, f16, "x", (K,))
+    yp, ldy = _rows(y, f16, "y", (N,))
+    op, ldo = _rows(out, f16, "out", (N,))
+    if y.shape[0] != x.shape[0] or out.shape[0] != x.shape[0]:
+        raise ValueError("x, y and out have %d, %d and %d tokens" % (x.shape[0], y.shape[0], out.shape[0]))
+    n = adapters.numel()
+    _raise_if(load().tl_lora_add(xp, ldx, _dev(A, (f16,), "A"), _dev(B, (f16,), "B"),
+                                 _ints(scales, torch.float32, "scales", num),
+                                 _ints(q_start, torch.int32, "q_start", n + 1),
+                                 _ints(adapters, torch.int32, "adapters"), n, x.shape[0], max_q, K, N, rank, num, yp,
+                                 ldy, op, ldo, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
 # conveniences that allocate their outputs with torch
 # ---------------------------------------------------------------------------
 
@@ -524,6 +717,27 @@ def requant_int4_to_int2(W4, s4, z4, group: int, in_place_scales: bool = False, 
     s2, z2 = (s4, z4) if in_place_scales else (torch.empty_like(s4), torch.empty_like(z4))
     tl_requant_int4_to_int2(W4, s4, z4, W2, s2, z2, group, stream)
     return W2, s2, z2
+
+
+def kv4_attention(cache: KV4Cache, q, q_start, seq_lens, table, max_q: int, scale=None, window: int = 0, stream=None):
+    """Attention output [tokens, q_heads, head_dim]; scale defaults to
+    head_dim ** -0.5."""
+    import torch
+
+    out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+    tl_kv4_attention(cache, q, out, q_start, seq_lens, table, max_q,
+                     cache.head_dim ** -0.5 if scale is None else scale, window,
+                     cache.attention_workspace(q.shape[1], max_q), stream)
+    return out
+
+
+def lora_add(x, A, B, scales, q_start, adapters, max_q: int, y, stream=None):
+    """y + the requests' adapters applied to x."""
+    import torch
+
+    out = torch.empty(y.shape, dtype=torch.float16, device=y.device)
+    tl_lora_add(x, A, B, scales, q_start, adapters, max_q, y, out, stream)
+    return out
 
 
 def unpack_weights(W, K: int, bits: int, stream=None):

@@ -1,0 +1,697 @@
+// Attention of few query rows over the paged 4-bit cache (decode, drafts).
+//
+//   k = s c + b, v = s' c' + b',  O = softmax(scale q . k) v
+//
+// Both products run on the codes.  With p_t the softmax weight of token t,
+//   q . k_t      = s_t (q . c_t) + b_t sum(q)
+//   sum_t p_t v_t = sum_t (p_t s'_t) c'_t + sum_t p_t b'_t
+// so scales and minima are folded outside and a code enters the matrix
+// instruction as the FP16 subnormal c * 2^-24: one AND per pair of codes, no
+// conversion (16 c * 2^-24 for the odd nibbles, paid back by q / 16 and by the
+// output rows).  Products and sums are exact in FP32 to its own rounding.
+//
+// Layout: mma.sync m16n8k16 with the cache on the M side, eight (query, head)
+// rows of one key head on the N side (NT = 1 or 2 such tiles):
+//   S^T [16 tokens x 8 rows] = K [16 x D] Q^T,  O^T [D x 8] += V^T [D x 16] P^T.
+// K fragments are 8-byte reads of a token's row, V fragments pairs of tokens
+// interleaved by PRMT, P^T comes from S^T by movmatrix: no tile is transposed
+// or dequantized through shared memory.
+//
+// The running reference m of the softmax is kept per row in log2 units of
+// p * s' (not p), so that the FP16 weights p s' use FP16's whole range
+// whatever the scales: they lie below 2^14 and the largest is at least 2^6.
+// m moves only when a weight would pass that.  Sums of p and of p b' use the
+// rounded weights too, so the result is an exact weighted mean under them.
+//
+// Work: a unit is 16 tokens per warp.  All units of the batch (requests x key
+// heads x row blocks x units) lie on one line that the blocks cut into equal
+// spans, so ragged lengths balance whatever they are; a block that begins or
+// ends inside an item leaves a partial (FP32) in the workspace and a second,
+// small kernel joins an item's partials in order (no atomics: repeatable).
+// Each warp streams its tiles through its own ring of bulk copies.
+#include <algorithm>
+#include <cmath>
+
+#include "serve.cuh"
+
+namespace tlq {
+namespace {
+
+constexpr int kTile = 16;     // tokens per tile
+constexpr int kDepth = 4;     // ring slots per warp
+constexpr float kHeadroom = 6.0f;   // a new reference puts the largest weight at 2^6
+constexpr float kTrigger = 14.0f;   // weights stay at or below 2^14
+
+template <int D, int NG, int NT>
+struct DCfg {
+  static constexpr int WARPS = 8;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int CTAS = NT == 1 ? 2 : 1;  // resident per SM
+  static constexpr int H = D / 64;        // 64-channel halves
+  static constexpr int R = 8 * NT;        // rows of an item
+  static constexpr int CODES = kTile * D / 2;
+  static constexpr int PAR = kTile * NG * 4;
+  static constexpr int TILE_BYTES = 2 * CODES + 2 * PAR;
+  static constexpr int RING = WARPS * kDepth * TILE_BYTES;
+  static constexpr int OSTRIDE = D + 4;   // floats per row of the merge buffer
+  static constexpr int MERGE = WARPS * 8 * OSTRIDE * 4;
+  static constexpr int STATS = WARPS * R * (2 + NG) * 4;
+  static constexpr int SMEM = RING + MERGE + STATS + WARPS * kDepth * 8 + 256;
+};
+
+// A partial of the workspace: O [R][D], then m [R], l [R].
+template <int D, int R>
+struct Partial {
+  static constexpr int FLOATS = R * (D + 2);
+};
+
+// What the joining kernel needs of an item that a block began but did not end.
+struct Header {
+  int followers;  // blocks after this one that hold a part of the item; 0: nothing to join
+  int q0;         // first query of the request
+  int row0;       // first (query, head) row of the item
+  int rows;
+  int head;       // key head
+};
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
+struct DecodeParams {
+  KvCache cache;
+  KvBatch batch;
+  const __half* q;
+  long long ldq;
+  __half* out;
+  long long ldo;
+  float scale_log2;  // softmax scale * log2(e)
+  int window, share;  // share: query heads per key head
+  float* partials;
+  Header* headers;
+};
+
+// Units of one request, the same for each of its items (key head, row block).
+struct ItemShape {
+  int items, units;
+};
+
+template <int R, int UNIT>
+__device__ __forceinline__ ItemShape item_shape(const DecodeParams& p, const KvRequest& r) {
+  ItemShape s;
+  s.items = p.cache.heads * ((r.q_len * p.share + R - 1) / R);
+  int span = r.len;
+  if (p.window > 0) {
+    const int queries = min(r.q_len, (R + p.share - 2) / p.share + 1);  // a row block's queries
+    span = (int)min((long long)r.len, (long long)p.window + queries + kTile);
+  }
+  s.units = max(1, (span + UNIT - 1) / UNIT);
+  return s;
+}
+
+template <int D, int NG, int NT>
+__global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTAS) decode_attention_kernel(
+    const DecodeParams p) {
+  using C = DCfg<D, NG, NT>;
+  constexpr int H = C::H, R = C::R, W = C::WARPS;
+  constexpr int UNIT = W * kTile;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* merge = reinterpret_cast<float*>(smem + C::RING);
+  float* stats = reinterpret_cast<float*>(smem + C::RING + C::MERGE);  // [W][R][m, l, beta...]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING + C::MERGE + C::STATS);
+  __shared__ UnitSearch<C::THREADS> search;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = lane >> 2, qd = lane & 3;
+  pdl_launch_dependents();
+  if (lane == 0) {
+    for (int i = 0; i < kDepth; ++i) mbar_init(&bars[warp * kDepth + i], 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  Header* const header = &p.headers[blockIdx.x];
+  if (tid == 0) header->followers = 0;
+
+  auto count = [&](int i) -> long long {
+    const ItemShape s = item_shape<R, UNIT>(p, kv_request(p.batch, p.cache.page, i));
+    return (long long)s.items * s.units;
+  };
+  long long own, mine;
+  search.count_all(p.batch.requests, count, &own, &mine);
+  const long long U = search.total;
+  const long long n = min((long long)gridDim.x, U);
+  if ((long long)blockIdx.x >= n) return;
+  long long u = U * blockIdx.x / n;
+  const long long u_end = U * (blockIdx.x + 1) / n;
+  search.find(p.batch.requests, count, u, own, mine);
+  int req = search.request;
+  long long req_u = search.first;
+  if (req < 0) return;  // not reached: u < U
+
+  const uint32_t ring = smem_u32(smem) + warp * kDepth * C::TILE_BYTES;
+  uint64_t* const bar = bars + warp * kDepth;
+  uint32_t phase = 0;  // parity of each ring slot
+
+  while (u < u_end) {
+    const KvRequest rq = kv_request(p.batch, p.cache.page, req);
+    const ItemShape shape = item_shape<R, UNIT>(p, rq);
+    const long long req_units = (long long)shape.items * shape.units;
+    if (u >= req_u + req_units) {  // on to the next request (of no units: passed over)
+      req_u += req_units;
+      if (++req >= p.batch.requests) return;  // not reached
+      continue;
+    }
+    const int item = (int)((u - req_u) / shape.units);
+    const int c0 = (int)((u - req_u) - (long long)item * shape.units);
+    const int c1 = (int)min((long long)shape.units, c0 + (u_end - u));
+    const int blocks_of = shape.items / p.cache.heads;
+    const int head = item / blocks_of, row0 = (item - head * blocks_of) * R;
+    const int rows = min(R, rq.q_len * p.share - row0);
+
+    // keys that any row of the item sees: [lo, hi)
+    const int first_q = row0 / p.share, last_q = (row0 + rows - 1) / p.share;
+    const int base_pos = rq.len - rq.q_len;
+    const int hi = max(0, base_pos + last_q + 1);
+    const int lo = p.window > 0 ? max(0, base_pos + first_q - p.window + 1) : 0;
+    const int all_see_hi = base_pos + first_q + 1;                                    // every row sees keys below it
+    const int all_see_lo = p.window > 0 ? base_pos + last_q - p.window + 1 : 0;       // and from it
+    const int tile0 = lo / kTile + c0 * W;
+    const int tile1 = min((hi + kTile - 1) / kTile, lo / kTile + c1 * W);
+    const int my_tiles = tile1 > tile0 + warp ? (tile1 - tile0 - warp + W - 1) / W : 0;
+
+    // page of this warp's tile i, 32 tiles at a time, a tile to a lane
+    const int* row_table = p.batch.table + (size_t)req * p.batch.ld_table;
+    auto load_pages = [&](int i0) {
+      const int i = i0 + lane;
+      return i < my_tiles ? __ldg(row_table + (((tile0 + warp + i * W) * kTile) >> p.cache.page_shift)) : -1;
+    };
+    int pages = load_pages(0), pages_next = -1;
+    uint32_t sent = 0;  // ring slots with a copy under way
+    auto issue = [&](int i) {  // tile i of this warp into slot i % kDepth; all lanes
+      if (i > 0 && (i & 31) == 0) pages = pages_next;
+      if ((i & 31) == 16) pages_next = load_pages((i & ~31) + 32);
+      const int page = __shfl_sync(0xffffffffu, pages, i & 31);
+      const int slot = i % kDepth;
+      sent &= ~(1u << slot);
+      if (page < 0 || page >= p.cache.num_pages) return;
+      sent |= 1u << slot;
+      const int off = ((tile0 + warp + i * W) * kTile) & (p.cache.page - 1);
+      const uint8_t* blk =
+          p.cache.blocks + ((long long)page * p.cache.heads + head) * (long long)p.cache.block_bytes;
+      const uint32_t dst = ring + slot * C::TILE_BYTES;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar[slot], C::TILE_BYTES);
+        const int half = p.cache.page * (D / 2);
+        bulk_load(dst, blk + off * (D / 2), C::CODES, &bar[slot]);
+        bulk_load(dst + C::CODES, blk + half + off * (D / 2), C::CODES, &bar[slot]);
+        bulk_load(dst + 2 * C::CODES, blk + 2 * half + off * (NG * 4), C::PAR, &bar[slot]);
+        bulk_load(dst + 2 * C::CODES + C::PAR, blk + 2 * half + (p.cache.page + off) * (NG * 4), C::PAR, &bar[slot]);
+      }
+    };
+    for (int i = 0; i < kDepth - 1 && i < my_tiles; ++i) issue(i);
+
+    // Query fragments: row n = 8 nt + r, channels 64 h + 16 qd .. + 15, scaled
+    // by a power of two so that the row's largest value lies in [2^14, 2^15)
+    // (an exact product; q / 16 for the odd nibbles then stays normal).
+    uint32_t qf[NT][4 * H][2];
+    float f[NT][2], qs[NT][2][NG];  // of this thread's columns (rows 2 qd, 2 qd + 1)
+    int pos[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = 8 * nt + r;
+      const bool on = row < rows;
+      const int gr = row0 + (on ? row : 0);
+      const int t = gr / p.share, g = gr - t * p.share;
+      const __half* src = p.q + (long long)(rq.q0 + t) * p.ldq + (long long)(head * p.share + g) * D;
+      uint4 raw[H][2];
+      float sum[H], big = 0.f;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        sum[h] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          raw[h][j] = on ? *reinterpret_cast<const uint4*>(src + 64 * h + 16 * qd + 8 * j) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {raw[h][j].x, raw[h][j].y, raw[h][j].z, raw[h][j].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+            sum[h] += v.x + v.y;
+            big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+#pragma unroll
+        for (int h = 0; h < H; ++h) sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], o);
+      }
+      int e = 0;  // 2^e * big in [2^14, 2^15); 0 for zero, infinite and NaN rows
+      if (big > 0.f && big < 65536.f) e = 14 + 127 - (int)(__float_as_uint(big) >> 23);
+      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+      const float up16 = __uint_as_float((uint32_t)(127 + e - 4) << 23);
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t w[4] = {raw[h][j].x, raw[h][j].y, raw[h][j].z, raw[h][j].w};
+          // pairs (ch 0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16 of the code word
+          float2 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+          const __half2 a0 = __floats2half2_rn(v[0].x * up, v[2].x * up);
+          const __half2 a1 = __floats2half2_rn(v[0].y * up16, v[2].y * up16);
+          const __half2 a2 = __floats2half2_rn(v[1].x * up, v[3].x * up);
+          const __half2 a3 = __floats2half2_rn(v[1].y * up16, v[3].y * up16);
+          qf[nt][4 * h + 2 * j][0] = *reinterpret_cast<const uint32_t*>(&a0);
+          qf[nt][4 * h + 2 * j][1] = *reinterpret_cast<const uint32_t*>(&a1);
+          qf[nt][4 * h + 2 * j + 1][0] = *reinterpret_cast<const uint32_t*>(&a2);
+          qf[nt][4 * h + 2 * j + 1][1] = *reinterpret_cast<const uint32_t*>(&a3);
+        }
+      }
+      const float down = p.scale_log2 * __uint_as_float((uint32_t)(127 + 24 - e) << 23);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int src_lane = (2 * qd + c) * 4;
+        f[nt][c] = __shfl_sync(0xffffffffu, down, src_lane);
+        float s0 = __shfl_sync(0xffffffffu, sum[0], src_lane);
+        if constexpr (H == 2) {
+          const float s1 = __shfl_sync(0xffffffffu, sum[1], src_lane);
+          if constexpr (NG == 1)
+            s0 += s1;
+          else
+            qs[nt][c][1] = s1 * p.scale_log2;
+        }
+        qs[nt][c][0] = s0 * p.scale_log2;
+        const int col = 8 * nt + 2 * qd + c;
+        pos[nt][c] = base_pos + (row0 + min(col, rows - 1)) / p.share;
+      }
+    }
+
+    float o[NT][4 * H][4];
+    float m[NT][2], mu[NT][2], l[NT][2], beta[NT][2][NG];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[nt][c] = -INFINITY;  // reference so far; mu is what is subtracted (0 while there is none)
+        mu[nt][c] = 0.f;
+        l[nt][c] = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) beta[nt][c][g] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4 * H; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[nt][j][k] = 0.f;
+    }
+
+    for (int i = 0; i < my_tiles; ++i) {
+      __syncwarp();  // the slot that is refilled next has been read by every lane
+      if (i + kDepth - 1 < my_tiles) issue(i + kDepth - 1);
+      const int slot = i % kDepth;
+      if (!(sent >> slot & 1u)) continue;  // a page outside the cache: its tokens do not exist
+      if (!mbar_wait(&bar[slot], (phase >> slot) & 1u, 0x301)) break;
+      phase ^= 1u << slot;
+      const int tok0 = (tile0 + warp + i * W) * kTile;
+      const uint32_t kb = ring + slot * C::TILE_BYTES, vb = kb + C::CODES;
+      const uint32_t kp = kb + 2 * C::CODES, vp = kp + C::PAR;
+      const bool edge = tok0 < all_see_lo || tok0 + kTile > all_see_hi;  // some row does not see some key
+
+      // S^T = K Q^T on the codes, per group of channels
+      float s[NT][NG][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[nt][g][k] = 0.f;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const uint2 ka = lds64(kb + r * (D / 2) + 32 * h + 8 * qd);
+        const uint2 kc = lds64(kb + (r + 8) * (D / 2) + 32 * h + 8 * qd);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t wa = j ? ka.y : ka.x, wc = j ? kc.y : kc.x;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t xa = e ? wa >> 8 : wa, xc = e ? wc >> 8 : wc;
+            const uint32_t a0 = xa & 0x000F000Fu, a1 = xc & 0x000F000Fu;
+            const uint32_t a2 = xa & 0x00F000F0u, a3 = xc & 0x00F000F0u;
+            const int ks = 4 * h + 2 * j + e;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_16816(s[nt][NG == 1 ? 0 : h], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+          }
+        }
+      }
+
+      // parameters of tokens r and r + 8
+      float ksc[2][NG], kmi[2][NG], vlg[2][NG], vrc[2], vmi[2][NG];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int tk = r + 8 * y;
+        const bool in = !edge || (tok0 + tk >= lo && tok0 + tk < hi);  // else what lies there is not a token of ours
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          uint32_t a = lds32(kp + (tk * NG + g) * 4), b = lds32(vp + (tk * NG + g) * 4);
+          a = in ? a : 0x00003C00u;  // scale 1, minimum 0
+          b = in ? b : 0x00003C00u;
+          const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
+          const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
+          ksc[y][g] = fa.x;
+          kmi[y][g] = fa.y;
+          const float vs = fmaxf(fb.x, 5.9604644775390625e-8f);
+          vlg[y][g] = lg2(vs);
+          vmi[y][g] = fb.y;
+          if (g == 0) vrc[y] = __fdividef(1.0f, vs);
+        }
+      }
+
+      // logits in log2 units of p (lw) and of p s' (a)
+      float lw[NT][2][2];  // [token half][column]
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x = fmaf(s[nt][0][2 * y + c] * f[nt][c], ksc[y][0], kmi[y][0] * qs[nt][c][0]);
+            if constexpr (NG == 2)
+              x = fmaf(s[nt][1][2 * y + c] * f[nt][c], ksc[y][1], fmaf(kmi[y][1], qs[nt][c][1], x));
+            if (edge) {
+              const int key = tok0 + r + 8 * y;
+              const bool see = key <= pos[nt][c] && key < hi && (p.window <= 0 || key > pos[nt][c] - p.window);
+              x = see ? x : -INFINITY;
+            }
+            lw[nt][y][c] = x;
+            float a = x + vlg[y][0];
+            if constexpr (NG == 2) a = x + fmaxf(vlg[y][0], vlg[y][1]);
+            over |= a > m[nt][c] + kTrigger;
+          }
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float lg = vlg[y][0];
+              if constexpr (NG == 2) lg = fmaxf(lg, vlg[y][1]);
+              x = fmaxf(x, lw[nt][y][c] + lg);
+            }
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float next = fmaxf(m[nt][c], x - kHeadroom);
+            if (next > m[nt][c]) {
+              const float w = ex2(m[nt][c] - next);  // 0 for the first reference
+              m[nt][c] = next;
+              mu[nt][c] = next;
+              l[nt][c] *= w;
+#pragma unroll
+              for (int g = 0; g < NG; ++g) beta[nt][c][g] *= w;
+#pragma unroll
+              for (int j = 0; j < 4 * H; ++j) {
+                o[nt][j][c] *= w;
+                o[nt][j][2 + c] *= w;
+              }
+            }
+          }
+      }
+
+      // weights p s' as FP16, their sums, and P^T fragments
+      uint32_t pf[NT][NG][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float w0[2];
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const __half2 h2 = __floats2half2_rn(ex2(lw[nt][y][0] + (vlg[y][g] - mu[nt][0])),
+                                                 ex2(lw[nt][y][1] + (vlg[y][g] - mu[nt][1])));
+            if (g == 0) {
+              const float2 back = __half22float2(h2);
+              w0[0] = back.x * vrc[y];
+              w0[1] = back.y * vrc[y];
+              l[nt][0] += w0[0];
+              l[nt][1] += w0[1];
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              // a minimum that this row does not see is left out, whatever it holds
+              const float mi = edge && w0[c] == 0.f ? 0.f : vmi[y][g];
+              beta[nt][c][g] = fmaf(w0[c], mi, beta[nt][c][g]);
+            }
+            pf[nt][g][y] = movmatrix(*reinterpret_cast<const uint32_t*>(&h2));
+          }
+        }
+
+      // O^T += V^T P^T: word 8 h + r of tokens 2 qd, 2 qd + 1, + 8, + 9.  Odd
+      // lanes of a quad read their two tokens in the other order (banks), the
+      // byte selectors put them back.
+      const int sw = qd & 1;
+      const uint32_t sel_lo = sw ? 0x1054u : 0x5410u, sel_hi = sw ? 0x3276u : 0x7632u;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const uint32_t at = vb + 32 * h + 4 * r + (2 * qd) * (D / 2);
+        const uint32_t t0 = lds32(at + sw * (D / 2)), t1 = lds32(at + (sw ^ 1) * (D / 2));
+        const uint32_t t8 = lds32(at + (8 + sw) * (D / 2)), t9 = lds32(at + (8 + (sw ^ 1)) * (D / 2));
+        const uint32_t wl[2] = {prmt(t0, t1, sel_lo), prmt(t0, t1, sel_hi)};
+        const uint32_t wh[2] = {prmt(t8, t9, sel_lo), prmt(t8, t9, sel_hi)};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t xa = e ? wl[j] >> 8 : wl[j], xc = e ? wh[j] >> 8 : wh[j];
+            const uint32_t a0 = xa & 0x000F000Fu, a1 = xa & 0x00F000F0u;  // channels 4 j + 2 e, + 1 of the word
+            const uint32_t a2 = xc & 0x000F000Fu, a3 = xc & 0x00F000F0u;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_16816(o[nt][4 * h + 2 * j + e], a0, a1, a2, a3, pf[nt][NG == 1 ? 0 : h][0],
+                        pf[nt][NG == 1 ? 0 : h][1]);
+          }
+      }
+    }
+
+    // ---------------- join the warps ----------------
+    __syncthreads();  // the merge buffer and statistics of the last item have been read
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) beta[nt][c][g] += __shfl_xor_sync(0xffffffffu, beta[nt][c][g], x);
+        }
+        if (r == 0) {
+          float* st = stats + (warp * R + 8 * nt + 2 * qd + c) * (2 + NG);
+          st[0] = m[nt][c];
+          st[1] = l[nt][c];
+#pragma unroll
+          for (int g = 0; g < NG; ++g) st[2 + g] = beta[nt][c][g];
+        }
+      }
+    const bool whole = c0 == 0 && c1 == shape.units;
+    float* part = nullptr;
+    if (!whole)
+      part = p.partials + ((size_t)blockIdx.x * 2 + (c0 == 0 ? 1 : 0)) * Partial<D, R>::FLOATS;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (nt > 0) __syncthreads();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float* dst = merge + (warp * 8 + 2 * qd + c) * C::OSTRIDE + 8 * r;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float k24 = 16777216.0f, k20 = 1048576.0f;
+            *reinterpret_cast<float4*>(dst + 64 * h + 4 * j) =
+                make_float4(o[nt][4 * h + 2 * j][c] * k24, o[nt][4 * h + 2 * j][2 + c] * k20,
+                            o[nt][4 * h + 2 * j + 1][c] * k24, o[nt][4 * h + 2 * j + 1][2 + c] * k20);
+          }
+      }
+      __syncthreads();
+      for (int e = tid; e < 8 * (D / 4); e += C::THREADS) {
+        const int row8 = e / (D / 4), ch = (e - row8 * (D / 4)) * 4;
+        const int row = 8 * nt + row8;
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < W; ++w) mm = fmaxf(mm, stats[(w * R + row) * (2 + NG)]);
+        float ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float* st = stats + (w * R + row) * (2 + NG);
+          const float wm = st[0] == -INFINITY ? 0.f : ex2(st[0] - mm);
+          ll = fmaf(wm, st[1], ll);
+          const float bt = st[2 + (NG == 2 ? ch / 64 : 0)];
+          const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + row8) * C::OSTRIDE + ch);
+          acc[0] = fmaf(wm, v.x + bt, acc[0]);
+          acc[1] = fmaf(wm, v.y + bt, acc[1]);
+          acc[2] = fmaf(wm, v.z + bt, acc[2]);
+          acc[3] = fmaf(wm, v.w + bt, acc[3]);
+        }
+        if (whole) {
+          if (row < rows) {
+            const float inv = ll == 0.f ? 0.f : 1.0f / ll;  // no key seen: zeros
+            const int gr = row0 + row, t = gr / p.share, g = gr - t * p.share;
+            const __half2 a = __floats2half2_rn(acc[0] * inv, acc[1] * inv);
+            const __half2 b = __floats2half2_rn(acc[2] * inv, acc[3] * inv);
+            *reinterpret_cast<uint2*>(p.out + (long long)(rq.q0 + t) * p.ldo +
+                                      (long long)(head * p.share + g) * D + ch) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+          }
+        } else {
+          *reinterpret_cast<float4*>(part + row * D + ch) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          if (ch == 0) {
+            part[R * D + row] = mm;
+            part[R * D + R + row] = ll;
+          }
+        }
+      }
+    }
+    if (!whole && c0 == 0 && tid == 0) {
+      // the block that holds the item's last unit
+      const long long last_u = req_u + (long long)(item + 1) * shape.units - 1;
+      long long b = ((last_u + 1) * n - 1) / U;
+      while (U * b / n > last_u) --b;
+      while (U * (b + 1) / n <= last_u) ++b;
+      *header = Header{(int)(b - blockIdx.x), rq.q0, row0, rows, head};
+    }
+    u += c1 - c0;
+  }
+}
+
+// Joins the partials of the items that were cut: block x looks at what main
+// block x began, block y takes every gridDim.y-th set of 128 four-channel pieces.
+template <int D, int R>
+__global__ void __launch_bounds__(128) decode_join_kernel(const DecodeParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const Header h = p.headers[blockIdx.x];
+  if (h.followers <= 0) return;
+  const int e = blockIdx.y * 128 + threadIdx.x;
+  const int row = e / (D / 4), ch = (e - row * (D / 4)) * 4;
+  if (row >= h.rows) return;
+  constexpr int F = Partial<D, R>::FLOATS;
+  const float* first = p.partials + ((size_t)blockIdx.x * 2 + 1) * F;
+  const float* rest = p.partials + ((size_t)blockIdx.x + 1) * 2 * F;  // follower i at i * 2 F
+  float m = first[R * D + row];
+  for (int i = 0; i < h.followers; ++i) m = fmaxf(m, rest[(size_t)i * 2 * F + R * D + row]);
+  float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = -1; i < h.followers; ++i) {
+    const float* part = i < 0 ? first : rest + (size_t)i * 2 * F;
+    const float mi = part[R * D + row];
+    const float w = mi == -INFINITY ? 0.f : ex2(mi - m);
+    const float4 v = *reinterpret_cast<const float4*>(part + row * D + ch);
+    l = fmaf(w, part[R * D + R + row], l);
+    acc[0] = fmaf(w, v.x, acc[0]);
+    acc[1] = fmaf(w, v.y, acc[1]);
+    acc[2] = fmaf(w, v.z, acc[2]);
+    acc[3] = fmaf(w, v.w, acc[3]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  const int gr = h.row0 + row, t = gr / p.share, g = gr - t * p.share;
+  const __half2 a = __floats2half2_rn(acc[0] * inv, acc[1] * inv);
+  const __half2 b = __floats2half2_rn(acc[2] * inv, acc[3] * inv);
+  *reinterpret_cast<uint2*>(p.out + (long long)(h.q0 + t) * p.ldo + (long long)(h.head * p.share + g) * D + ch) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+template <int D, int NG, int NT>
+tlq_status launch_one(const DecodeParams& base, cudaStream_t stream) {
+  using C = DCfg<D, NG, NT>;
+  auto kernel = decode_attention_kernel<D, NG, NT>;
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (attr != cudaSuccess) return cuda_error(attr, "kv4 attention: shared memory");
+  const int blocks = device_info().sms * C::CTAS;
+  DecodeParams p = base;
+  p.headers = reinterpret_cast<Header*>(p.partials);
+  p.partials = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.partials) +
+                                        ((blocks * sizeof(Header) + 255) & ~size_t(255)));
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)blocks, 1, 1);
+  lc.blockDim = dim3(C::THREADS, 1, 1);
+  lc.dynamicSmemBytes = C::SMEM;
+  lc.stream = stream;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = &at;
+  lc.numAttrs = pdl_enabled() ? 1 : 0;
+  tlq_status st = cuda_error(cudaLaunchKernelEx(&lc, kernel, p), "kv4 attention: launch");
+  if (st != TLQ_OK) return st;
+  lc.gridDim = dim3((unsigned)blocks, (unsigned)((C::R * D / 4 + 127) / 128), 1);
+  lc.blockDim = dim3(128, 1, 1);
+  lc.dynamicSmemBytes = 0;
+  return cuda_error(cudaLaunchKernelEx(&lc, decode_join_kernel<D, C::R>, p), "kv4 attention join: launch");
+}
+
+template <int D, int NG>
+tlq_status launch_rows(const DecodeParams& p, int rows, cudaStream_t stream) {
+  return rows <= 8 ? launch_one<D, NG, 1>(p, stream) : launch_one<D, NG, 2>(p, stream);
+}
+
+}  // namespace
+
+// The most that any form of the kernel takes at this head size, so that one
+// workspace serves steps of every shape.
+size_t kv4_decode_workspace(int head_dim) {
+  const size_t sms = (size_t)device_info().sms;
+  auto bytes = [&](size_t blocks, size_t R) {
+    return ((blocks * sizeof(Header) + 255) & ~size_t(255)) + blocks * 2 * R * (head_dim + 2) * sizeof(float);
+  };
+  return std::max(bytes(2 * sms, 8), bytes(sms, 16));
+}
+
+tlq_status launch_kv4_decode(const KvAttention& a, cudaStream_t stream) {
+  DecodeParams p{};
+  p.cache = a.cache;
+  p.batch = a.batch;
+  p.q = a.q;
+  p.ldq = a.ldq;
+  p.out = a.out;
+  p.ldo = a.ldo;
+  p.scale_log2 = (float)((double)a.scale * M_LOG2E);
+  p.window = a.window;
+  p.share = a.q_heads / a.cache.heads;
+  p.partials = static_cast<float*>(a.ws);
+  const int rows = (int)std::min<long long>((long long)a.batch.max_q * p.share, 1 << 20);
+  if (a.head_dim == 64) return launch_rows<64, 1>(p, rows, stream);
+  return a.cache.group == 64 ? launch_rows<128, 2>(p, rows, stream) : launch_rows<128, 1>(p, rows, stream);
+}
+
+}  // namespace tlq

@@ -1,0 +1,249 @@
+// Low-rank adapters of many requests beside a shared projection:
+//
+//   out[t] = fp16(y[t] + scale_a * B_a (A_a x[t])),  a = the adapter of token t's request
+//
+// One launch.  A cluster of eight blocks takes a tile of one request's tokens:
+// each block contracts an eighth of K, the partial A x (FP32) are summed over
+// the cluster through shared memory in rank order, and each block then makes
+// an eighth of N.  So x, y and out cross DRAM once, A x never does, and no
+// workspace or second launch is needed.  At rank 16 there are 2 * 16 flops to
+// every 2 bytes: memory bounds long batches, latency short ones.
+//
+// Both products run on mma.sync m16n8k16 with operands straight from global
+// memory: the order of k (and of the output columns) inside a fragment is
+// free, so each thread takes 8 (4) neighbouring values in one load.  A x is
+// normalised by a power of two per token and split into two FP16 parts
+// (22 bits together), so nothing is lost of the FP32 sums and none overflows.
+#include <algorithm>
+
+#include "serve.cuh"
+
+namespace tlq {
+namespace {
+
+constexpr int kRanks = 8;  // blocks of a cluster
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxRank = 64;
+
+__device__ __forceinline__ float peer_f32(const float* p, uint32_t rank) {
+  uint32_t a = smem_u32(p), r;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+  return v;
+}
+
+// MT: 16-token tiles of a cluster
+template <int MT>
+__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads) lora_kernel(const LoraArgs a) {
+  constexpr int TT = 16 * MT;
+  __shared__ UnitSearch<kThreads> search;
+  __shared__ float part[kWarps][16][kMaxRank + 1];   // A x of each warp's share of k, one 16-token tile at a time
+  __shared__ float sums[TT][kMaxRank];               // this block's A x, then the cluster's
+  __shared__ __half th[2][TT][kMaxRank + 8];         // the high and low parts
+  __shared__ float back[TT];                         // 2^e * scale of each token
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, qd = lane & 3;
+  const uint32_t rank = cluster_ctarank();
+  pdl_launch_dependents();
+  pdl_wait();
+
+  auto length = [&](int i) {
+    const int s = a.q_start[i], e = a.q_start[i + 1];
+    return s >= 0 && e >= s && e <= a.tokens ? min(e - s, a.max_q) : 0;
+  };
+  auto count = [&](int i) -> long long { return (length(i) + TT - 1) / TT; };
+  long long own, mine;
+  search.count_all(a.requests, count, &own, &mine);
+  const long long u = blockIdx.x / kRanks;
+  if (u >= search.total) return;  // the same for the whole cluster
+  search.find(a.requests, count, u, own, mine);
+  const int req = search.request;
+  const int off = (int)(u - search.first) * TT;
+  const int t0 = a.q_start[req] + off;
+  const int rows = min(TT, length(req) - off);
+  int w = a.adapters[req];
+  if (w < 0 || w >= a.num_adapters) w = -1;  // no adapter: y goes through as it is
+  const int NR = a.rank, KS = (NR + 15) / 16;
+
+  if (w >= 0) {
+    // ---- A x: this block's k, 32 at a time to a warp ----
+    const int chunks = (a.K + 31) / 32;
+    const int k_lo = (int)((long long)chunks * rank / kRanks), k_hi = (int)((long long)chunks * (rank + 1) / kRanks);
+    const __half* A = a.A + (size_t)w * NR * a.K;
+    for (int mt = 0; mt < MT; ++mt) {
+      float acc[kMaxRank / 8][4];
+#pragma unroll
+      for (int j = 0; j < kMaxRank / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+      const int ra = 16 * mt + r, rb = ra + 8;
+      const __half* xa = a.x + (long long)(t0 + min(ra, rows - 1)) * a.ldx;
+      const __half* xb = a.x + (long long)(t0 + min(rb, rows - 1)) * a.ldx;
+      if (16 * mt < rows) {
+        for (int c = k_lo + warp; c < k_hi; c += kWarps) {
+          const int k = 32 * c + 8 * qd;
+          const bool in = k < a.K;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          const uint4 va = in ? *reinterpret_cast<const uint4*>(xa + k) : zero;
+          const uint4 vb = in ? *reinterpret_cast<const uint4*>(xb + k) : zero;
+#pragma unroll
+          for (int j = 0; j < kMaxRank / 8; ++j) {
+            if (8 * j < NR) {
+              const uint4 b = in ? __ldg(reinterpret_cast<const uint4*>(A + (size_t)(8 * j + r) * a.K + k)) : zero;
+              mma_16816(acc[j], va.x, vb.x, va.y, vb.y, b.x, b.y);
+              mma_16816(acc[j], va.z, vb.z, va.w, vb.w, b.z, b.w);
+            }
+          }
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kMaxRank / 8; ++j) {
+        if (8 * j < NR) {
+          part[warp][r][8 * j + 2 * qd] = acc[j][0];
+          part[warp][r][8 * j + 2 * qd + 1] = acc[j][1];
+          part[warp][r + 8][8 * j + 2 * qd] = acc[j][2];
+          part[warp][r + 8][8 * j + 2 * qd + 1] = acc[j][3];
+        }
+      }
+      __syncthreads();
+      for (int e = tid; e < 16 * NR; e += kThreads) {
+        const int row = e / NR, col = e - row * NR;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) s += part[i][row][col];
+        sums[16 * mt + row][col] = s;
+      }
+    }
+  }
+  cluster_sync();
+  if (w >= 0) {
+    // ---- the cluster's sums, in rank order; a warp to a token ----
+    const float scale = a.scales[w];
+    for (int row = warp; row < TT; row += kWarps) {
+      float v[2] = {0.f, 0.f}, big = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = lane + 32 * i;
+        if (col < NR && row < rows) {
+          for (uint32_t k = 0; k < kRanks; ++k) v[i] += peer_f32(&sums[row][col], k);
+        }
+        big = fmaxf(big, fabsf(v[i]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      int e = 0;  // big * 2^-e in [2^14, 2^15); exponents whose powers are normal numbers
+      if (big > 0.f && big < INFINITY) e = max(-126, min(126, (int)(__float_as_uint(big) >> 23) - 127 - 14));
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = lane + 32 * i;
+        if (col < 16 * KS) {
+          const float x = v[i] * down;
+          const __half hi = __float2half_rn(x);
+          th[0][row][col] = hi;
+          th[1][row][col] = __float2half_rn(x - __half2float(hi));
+        }
+      }
+      if (lane == 0) back[row] = __uint_as_float((uint32_t)(127 + e) << 23) * scale;
+    }
+  }
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this block has read its peers
+
+  // ---- out = y + B (A x): 32 columns at a time to a warp; thread qd of a quad
+  // holds columns 8 qd .. 8 qd + 7 of its two rows ----
+  const int blocks32 = (a.N + 31) / 32;
+  const int b_lo = (int)((long long)blocks32 * rank / kRanks), b_hi = (int)((long long)blocks32 * (rank + 1) / kRanks);
+  for (int nb = b_lo + warp; nb < b_hi; nb += kWarps) {
+    const int n0 = 32 * nb;
+    uint2 bf[4][kMaxRank / 16];
+    if (w >= 0) {
+      const __half* B = a.B + (size_t)w * a.N * NR;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = n0 + 8 * (r >> 1) + 2 * j + (r & 1);
+#pragma unroll
+        for (int s = 0; s < kMaxRank / 16; ++s) {
+          const int k = 16 * s + 4 * qd;
+          bf[j][s] = n < a.N && k < NR ? __ldg(reinterpret_cast<const uint2*>(B + (size_t)n * NR + k))
+                                       : make_uint2(0, 0);
+        }
+      }
+    }
+    const int col = n0 + 8 * qd;
+    for (int mt = 0; mt < MT; ++mt) {
+      if (16 * mt >= rows) break;
+      float acc[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+      const int ra = 16 * mt + r, rb = ra + 8;
+      if (w >= 0) {
+#pragma unroll
+        for (int s = 0; s < kMaxRank / 16; ++s) {
+          if (s < KS) {
+#pragma unroll
+            for (int part2 = 0; part2 < 2; ++part2) {
+              const uint2 fa = *reinterpret_cast<const uint2*>(&th[part2][ra][16 * s + 4 * qd]);
+              const uint2 fb = *reinterpret_cast<const uint2*>(&th[part2][rb][16 * s + 4 * qd]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma_16816(acc[j], fa.x, fb.x, fa.y, fb.y, bf[j][s].x, bf[j][s].y);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int row = y ? rb : ra;
+        if (row < rows && col < a.N) {
+          const uint4 old = *reinterpret_cast<const uint4*>(a.y + (long long)(t0 + row) * a.ldy + col);
+          uint4 res = old;
+          if (w >= 0) {
+            const float up = back[row];
+            const uint32_t in[4] = {old.x, old.y, old.z, old.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&in[j]));
+              const __half2 h = __floats2half2_rn(fmaf(acc[j][2 * y], up, f.x), fmaf(acc[j][2 * y + 1], up, f.y));
+              o[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            res = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          *reinterpret_cast<uint4*>(a.out + (long long)(t0 + row) * a.ldo + col) = res;
+        }
+      }
+    }
+  }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no block leaves while a peer reads it
+}
+
+template <int MT>
+tlq_status launch_tiles(const LoraArgs& a, cudaStream_t stream) {
+  // at most this many tiles whatever the requests' lengths are
+  const long long tiles =
+      std::min<long long>((long long)a.tokens / (16 * MT) + a.requests,
+                          (long long)a.requests * ((a.max_q + 16 * MT - 1) / (16 * MT)));
+  if (tiles * kRanks > 0x7fffffffll) return set_error(TLQ_EUNSUPPORTED, "lora: %lld token tiles", tiles);
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(tiles * kRanks), 1, 1);
+  lc.blockDim = dim3(kThreads, 1, 1);
+  lc.stream = stream;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = &at;
+  lc.numAttrs = pdl_enabled() ? 1 : 0;
+  return cuda_error(cudaLaunchKernelEx(&lc, lora_kernel<MT>, a), "lora: launch");
+}
+
+}  // namespace
+
+tlq_status launch_lora(const LoraArgs& a, cudaStream_t stream) {
+  return launch_tiles<1>(a, stream);
+}
+
+}  // namespace tlq

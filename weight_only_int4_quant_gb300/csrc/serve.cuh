@@ -1,0 +1,183 @@
+// Shared parts of the multi-request serving operators: the geometry of the
+// paged 4-bit cache, the batch a kernel is given, and the search that turns a
+// position in the batch's work into a request.
+#pragma once
+
+#include "common.cuh"
+
+namespace tlq {
+
+// The cache: blocks is [pages][heads][block_bytes]; a block holds the key
+// codes [page][D/2], the value codes [page][D/2], the key parameters
+// [page][D/group][2] and the value parameters (FP16 scale, minimum).  Keys and
+// values of one page and head are one contiguous piece, so a 16-token page
+// moves with a single bulk copy.
+struct KvCache {
+  uint8_t* blocks;
+  long long num_pages;
+  int heads, page, group;  // page: tokens, a power of two >= 16
+  int page_shift;
+  int block_bytes;
+};
+
+__host__ __device__ inline int kv_block_bytes(int page, int head_dim, int group) {
+  return page * head_dim + 8 * page * (head_dim / group);
+}
+
+// The step's requests.  Request b has queries [q_start[b], q_start[b+1]) and
+// seq_lens[b] tokens in the cache, the queries' own among them.
+struct KvBatch {
+  const int* q_start;
+  const int* seq_lens;
+  const int* table;
+  int ld_table;
+  int requests, tokens, max_q;
+};
+
+struct KvRequest {
+  int q0, q_len, len;
+};
+
+// Lengths as the kernels use them: queries outside [0, tokens) and lengths
+// beyond the table's row count as none.
+__device__ __forceinline__ KvRequest kv_request(const KvBatch& b, int page, int i) {
+  KvRequest r;
+  r.q0 = b.q_start[i];
+  const int q1 = b.q_start[i + 1];
+  r.q_len = (r.q0 >= 0 && q1 >= r.q0 && q1 <= b.tokens) ? min(q1 - r.q0, b.max_q) : 0;
+  const long long room = (long long)b.ld_table * page;
+  r.len = (int)max(0ll, min((long long)b.seq_lens[i], min(room, 0x7fffff00ll)));
+  return r;
+}
+
+// Where unit `u` of the batch's work lies: requests have count(i) units each,
+// in order.  All THREADS threads of a block call it together; the totals and
+// the request found come back through shared memory.
+template <int THREADS>
+struct UnitSearch {
+  long long warp_sum[THREADS / 32];
+  long long total;
+  long long first;  // first unit of the request found
+  int request;      // -1: none
+
+  __device__ long long scan(long long v, long long* sum) {  // inclusive scan over the block
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long n = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += n;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = v;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      all += warp_sum[w];
+    }
+    *sum = all;
+    return v + before;
+  }
+
+  // total units of the batch; with one chunk of requests *own is this thread's
+  // inclusive prefix and *mine its count, which find() takes again
+  template <class F>
+  __device__ void count_all(int requests, F count, long long* own, long long* mine) {
+    long long v = 0;
+    for (int i = threadIdx.x; i < requests; i += THREADS) v += count(i);
+    long long sum;
+    *own = scan(v, &sum);
+    *mine = v;
+    if (threadIdx.x == 0) {
+      total = sum;
+      request = -1;
+    }
+    __syncthreads();
+  }
+
+  template <class F>
+  __device__ void find(int requests, F count, long long u, long long own, long long mine) {
+    if (requests <= THREADS) {
+      if (mine > 0 && own - mine <= u && u < own) {
+        request = threadIdx.x;
+        first = own - mine;
+      }
+    } else {
+      long long base = 0;
+      for (int c = 0; c < requests; c += THREADS) {
+        const int i = c + threadIdx.x;
+        const long long n = i < requests ? count(i) : 0;
+        long long sum;
+        const long long upto = scan(n, &sum) + base;
+        if (n > 0 && upto - n <= u && u < upto) {
+          request = i;
+          first = upto - n;
+        }
+        base += sum;
+        if (base > u) break;  // the same for every thread
+      }
+    }
+    __syncthreads();
+  }
+};
+
+// Launchers (arguments validated by the entry points).
+struct KvPlanArgs {
+  const int* cached;
+  const int* added;
+  int requests;
+  int* table;
+  int ld_table;
+  const int* free_pages;
+  int num_free;
+  const int* free_head;
+  int page;
+  long long num_pages;
+  int* q_start;
+  int* seq_lens;
+  int* token_req;
+  int* token_pos;
+  long long* slots;
+  int capacity;
+  int* counts;
+};
+tlq_status launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream);
+tlq_status launch_kv4_append(const KvCache& c, int head_dim, const __half* k, long long ldk, const __half* v,
+                             long long ldv, const long long* slots, int tokens, cudaStream_t stream);
+tlq_status launch_kv4_read(const KvCache& c, int head_dim, const long long* slots, int tokens, __half* k, __half* v,
+                           cudaStream_t stream);
+
+struct KvAttention {
+  KvCache cache;
+  KvBatch batch;
+  int head_dim, q_heads;
+  const __half* q;
+  long long ldq;
+  __half* out;
+  long long ldo;
+  float scale;
+  int window;
+  void* ws;
+};
+size_t kv4_decode_workspace(int head_dim);
+tlq_status launch_kv4_decode(const KvAttention& a, cudaStream_t stream);
+
+struct LoraArgs {
+  const __half* x;
+  long long ldx;
+  const __half* A;
+  const __half* B;
+  const float* scales;
+  const int* q_start;
+  const int* adapters;
+  int requests, tokens, max_q;
+  int K, N, rank, num_adapters;
+  const __half* y;
+  long long ldy;
+  __half* out;
+  long long ldo;
+};
+tlq_status launch_lora(const LoraArgs& a, cudaStream_t stream);
+
+}  // namespace tlq
