@@ -103,6 +103,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 def load():
     """Load libtlq.so; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -173,7 +175,8 @@ def _stream(stream):
     import torch
 
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle: torch.cuda.current_stream() builds a Stream object, 3 us of every call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -494,6 +497,21 @@ def tl_selftest_wait_timeout(limit_us: int, stream=None) -> None:
 # multi-request serving: paged 4-bit cache, attention, tables, adapters
 # ---------------------------------------------------------------------------
 
+# These calls are made per step, several to a step, so their checks take the
+# short way through for arguments that are as they should be (a serving step's
+# kernels run for a few microseconds); what is not goes on to the full checks
+# and their messages.
+
+def _ptr(t, dtype, name):
+    """Data pointer of a contiguous CUDA tensor of one dtype."""
+    try:
+        if t.is_cuda and t.dtype is dtype and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _dev(t, (dtype,), name)
+
+
 def _rows(t, dtype, name, dims):
     """Data pointer and token stride of a [tokens, ...] CUDA tensor whose rows
     are contiguous (a token stride of its own is taken as it is)."""
@@ -501,21 +519,23 @@ def _rows(t, dtype, name, dims):
 
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.dim() != len(dims) + 1 or any(d is not None and n != d for n, d in zip(t.shape[1:], dims)):
-        raise ValueError("%s has shape %s, expected [tokens%s]" % (name, tuple(t.shape),
+    shape = t.shape
+    if len(shape) != len(dims) + 1 or shape[1:] != dims:
+        raise ValueError("%s has shape %s, expected [tokens%s]" % (name, tuple(shape),
                                                                    "".join(", %s" % d for d in dims)))
+    stride = t.stride()
     inner = 1
-    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if t.numel() > 0 and n != 1 and s != inner:
+    for i in range(len(dims), 0, -1):
+        if stride[i] != inner and shape[i] != 1 and t.numel() > 0:
             raise ValueError("%s: a token's values must be contiguous" % name)
-        inner *= n
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(inner, 8))
+        inner *= shape[i]
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else max(inner, 8))
 
 
 def _ints(t, dtype, name, n=None):
-    p = _dev(t, (dtype,), name)
+    p = _ptr(t, dtype, name)
     if n is not None and t.numel() != n:
         raise ValueError("%s has %d elements, expected %d" % (name, t.numel(), n))
     return p
@@ -524,13 +544,11 @@ def _ints(t, dtype, name, n=None):
 def _table(table, requests):
     import torch
 
-    if not isinstance(table, torch.Tensor) or not table.is_cuda or table.dtype != torch.int32:
-        raise ValueError("table must be an int32 CUDA tensor")
-    if table.dim() != 2 or table.shape[0] != requests:
-        raise ValueError("table has shape %s, expected [%d, pages]" % (tuple(table.shape), requests))
-    if not table.is_contiguous():
-        raise ValueError("table must be contiguous")
-    return table.data_ptr(), table.shape[1]
+    p = _ptr(table, torch.int32, "table")
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != requests:
+        raise ValueError("table has shape %s, expected [%d, pages]" % (tuple(shape), requests))
+    return p, shape[1]
 
 
 def tl_kv4_block_bytes(page_size: int, head_dim: int, group: int) -> int:
@@ -580,6 +598,8 @@ class KV4Cache:
         self.num_pages, self.heads, self.head_dim = num_pages, heads, head_dim
         self.page_size, self.group = page_size, group
         self._c = _KV4Cache(_dev(blocks, (torch.uint8,), "blocks"), num_pages, heads, head_dim, page_size, group)
+        self._ref = ctypes.byref(self._c)
+        self._dims = (heads, head_dim)
 
     def attention_workspace(self, q_heads: int, max_q: int):
         """A workspace tensor for tl_kv4_attention with up to max_q queries a
@@ -594,13 +614,13 @@ def tl_kv4_append(cache: KV4Cache, k, v, slots, stream=None) -> None:
     """Quantize k, v [tokens, heads, head_dim] into the cache's slots."""
     import torch
 
-    dims = (cache.heads, cache.head_dim)
+    dims = cache._dims
     kp, ldk = _rows(k, torch.float16, "k", dims)
     vp, ldv = _rows(v, torch.float16, "v", dims)
     n = slots.numel()
     if k.shape[0] != n or v.shape[0] != n:
         raise ValueError("k and v have %d and %d tokens, slots %d" % (k.shape[0], v.shape[0], n))
-    _raise_if(load().tl_kv4_append(ctypes.byref(cache._c), kp, ldk, vp, ldv, _ints(slots, torch.int64, "slots"), n,
+    _raise_if(load().tl_kv4_append(cache._ref, kp, ldk, vp, ldv, _ints(slots, torch.int64, "slots"), n,
                                    _stream(stream)))
 
 
@@ -609,12 +629,12 @@ def tl_kv4_read(cache: KV4Cache, slots, k, v, stream=None) -> None:
     import torch
 
     n = slots.numel()
-    shape = (n, cache.heads, cache.head_dim)
+    shape = (n,) + cache._dims
     for t, name in ((k, "k"), (v, "v")):
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
-    _raise_if(load().tl_kv4_read(ctypes.byref(cache._c), _ints(slots, torch.int64, "slots"), n,
-                                 _dev(k, (torch.float16,), "k"), _dev(v, (torch.float16,), "v"), _stream(stream)))
+    _raise_if(load().tl_kv4_read(cache._ref, _ptr(slots, torch.int64, "slots"), n, _ptr(k, torch.float16, "k"),
+                                 _ptr(v, torch.float16, "v"), _stream(stream)))
 
 
 def tl_kv4_attention_workspace_size(q_heads: int, heads: int, head_dim: int, max_q: int) -> int:
@@ -628,15 +648,17 @@ def tl_kv4_attention(cache: KV4Cache, q, out, q_start, seq_lens, table, max_q: i
     out; workspace: cache.attention_workspace(q_heads, max_q)."""
     import torch
 
-    qp, ldq = _rows(q, torch.float16, "q", (None, cache.head_dim))
+    if q.dim() != 3:
+        raise ValueError("q has shape %s, expected [tokens, q_heads, %d]" % (tuple(q.shape), cache.head_dim))
+    qp, ldq = _rows(q, torch.float16, "q", (q.shape[1], cache.head_dim))
     op, ldo = _rows(out, torch.float16, "out", (q.shape[1], cache.head_dim))
     if out.shape[0] != q.shape[0]:
         raise ValueError("out has %d tokens, q %d" % (out.shape[0], q.shape[0]))
     n = seq_lens.numel()
     tp, width = _table(table, n)
-    ws = _dev(workspace, (torch.uint8,), "workspace") if workspace is not None else None
+    ws = _ptr(workspace, torch.uint8, "workspace") if workspace is not None else None
     nb = workspace.numel() if workspace is not None else 0
-    _raise_if(load().tl_kv4_attention(ctypes.byref(cache._c), qp, ldq, q.shape[1], op, ldo,
+    _raise_if(load().tl_kv4_attention(cache._ref, qp, ldq, q.shape[1], op, ldo,
                                       _ints(q_start, torch.int32, "q_start", n + 1),
                                       _ints(seq_lens, torch.int32, "seq_lens"), tp, width, n, q.shape[0], max_q,
                                       scale, window, ws, nb, _stream(stream)))
@@ -659,7 +681,7 @@ def tl_lora_add(x, A, B, scales, q_start, adapters, max_q: int, y, out, stream=N
     if y.shape[0] != x.shape[0] or out.shape[0] != x.shape[0]:
         raise ValueError("x, y and out have %d, %d and %d tokens" % (x.shape[0], y.shape[0], out.shape[0]))
     n = adapters.numel()
-    _raise_if(load().tl_lora_add(xp, ldx, _dev(A, (f16,), "A"), _dev(B, (f16,), "B"),
+    _raise_if(load().tl_lora_add(xp, ldx, _ptr(A, f16, "A"), _ptr(B, f16, "B"),
                                  _ints(scales, torch.float32, "scales", num),
                                  _ints(q_start, torch.int32, "q_start", n + 1),
                                  _ints(adapters, torch.int32, "adapters"), n, x.shape[0], max_q, K, N, rank, num, yp,

@@ -23,12 +23,14 @@
 // m moves only when a weight would pass that.  Sums of p and of p b' use the
 // rounded weights too, so the result is an exact weighted mean under them.
 //
-// Work: a unit is 16 tokens per warp.  All units of the batch (requests x key
-// heads x row blocks x units) lie on one line that the blocks cut into equal
-// spans, so ragged lengths balance whatever they are; a block that begins or
-// ends inside an item leaves a partial (FP32) in the workspace and a second,
-// small kernel joins an item's partials in order (no atomics: repeatable).
-// Each warp streams its tiles through its own ring of bulk copies.
+// Work: a unit is a stage of 128 tokens, 32 to each of a block's four warps.
+// All units of the batch (requests x key heads x row blocks x stages) lie on
+// one line that the blocks cut into equal spans, so ragged lengths balance
+// whatever they are; a block that begins or ends inside an item leaves a
+// partial (FP32) in the workspace and a second, small kernel joins an item's
+// partials in order (no atomics: repeatable).  A fifth warp streams the stages
+// through a ring of bulk copies, one per page (a page and head is one
+// contiguous piece), and runs ahead over the ends of items.
 #include <algorithm>
 #include <cmath>
 
@@ -37,26 +39,28 @@
 namespace tlq {
 namespace {
 
-constexpr int kTile = 16;     // tokens per tile
-constexpr int kDepth = 4;     // ring slots per warp
+constexpr int kStage = 128;  // tokens of a stage
+constexpr int kTile = 16;    // tokens of a matrix instruction
+constexpr int kTiles = 2;    // tiles of a warp in a stage
 constexpr float kHeadroom = 6.0f;   // a new reference puts the largest weight at 2^6
 constexpr float kTrigger = 14.0f;   // weights stay at or below 2^14
+constexpr float kNone = -1e30f;     // the reference of a row that has seen no key (finite: differences stay numbers)
 
 template <int D, int NG, int NT>
 struct DCfg {
-  static constexpr int WARPS = 8;
-  static constexpr int THREADS = 32 * WARPS;
-  static constexpr int CTAS = NT == 1 ? 2 : 1;  // resident per SM
+  static constexpr int WARPS = 4;  // that compute; one more loads
+  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int CTAS = NT == 1 ? 3 : 2;  // resident per SM
+  static constexpr int JOINT = NT * NG == 1 ? 2 : 1;  // tiles whose steps are interleaved (registers)
+  static constexpr int DEPTH = 3;         // stages of the ring
   static constexpr int H = D / 64;        // 64-channel halves
   static constexpr int R = 8 * NT;        // rows of an item
-  static constexpr int CODES = kTile * D / 2;
-  static constexpr int PAR = kTile * NG * 4;
-  static constexpr int TILE_BYTES = 2 * CODES + 2 * PAR;
-  static constexpr int RING = WARPS * kDepth * TILE_BYTES;
+  static constexpr int STAGE_BYTES = kStage * (D + 8 * NG);
+  static constexpr int RING = DEPTH * STAGE_BYTES;
   static constexpr int OSTRIDE = D + 4;   // floats per row of the merge buffer
   static constexpr int MERGE = WARPS * 8 * OSTRIDE * 4;
   static constexpr int STATS = WARPS * R * (2 + NG) * 4;
-  static constexpr int SMEM = RING + MERGE + STATS + WARPS * kDepth * 8 + 256;
+  static constexpr int SMEM = RING + MERGE + STATS + DEPTH * 20 + 64;
 };
 
 // A partial of the workspace: O [R][D], then m [R], l [R].
@@ -121,36 +125,98 @@ struct ItemShape {
   int items, units;
 };
 
-template <int R, int UNIT>
+template <int R>
 __device__ __forceinline__ ItemShape item_shape(const DecodeParams& p, const KvRequest& r) {
   ItemShape s;
   s.items = p.cache.heads * ((r.q_len * p.share + R - 1) / R);
   int span = r.len;
   if (p.window > 0) {
     const int queries = min(r.q_len, (R + p.share - 2) / p.share + 1);  // a row block's queries
-    span = (int)min((long long)r.len, (long long)p.window + queries + kTile);
+    // window + queries - 1 keys, wherever they lie in their stages
+    span = (int)min((long long)r.len, (long long)p.window + queries + kStage);
   }
-  s.units = max(1, (span + UNIT - 1) / UNIT);
+  s.units = max(1, (span + kStage - 1) / kStage);
   return s;
 }
+
+// A block's share of an item: stages [s0, s1) of one request, key head and row block.
+struct Segment {
+  KvRequest rq;
+  int req, head, row0, rows;
+  int lo, hi;             // keys that any row sees
+  int all_lo, all_hi;     // keys that every row sees
+  int s0, s1;             // stages (absolute: token / kStage)
+  bool first, last;       // holds the item's first, last unit
+  long long item_end;     // unit behind the item
+  int units;              // units of the share
+};
+
+// Walks a block's span of units; every thread walks by itself.
+template <int R>
+struct Walk {
+  long long u, u_end, req_u;
+  int req;
+
+  __device__ __forceinline__ bool next(const DecodeParams& p, Segment* s) {
+    while (u < u_end && req < p.batch.requests) {
+      const KvRequest rq = kv_request(p.batch, p.cache.page, req);
+      const ItemShape shape = item_shape<R>(p, rq);
+      const long long units = (long long)shape.items * shape.units;
+      if (u >= req_u + units) {  // on to the next request (one without queries is passed over)
+        req_u += units;
+        ++req;
+        continue;
+      }
+      const int item = (int)((u - req_u) / shape.units);
+      const int c0 = (int)((u - req_u) - (long long)item * shape.units);
+      const int c1 = (int)min((long long)shape.units, c0 + (u_end - u));
+      const int row_blocks = shape.items / p.cache.heads;
+      s->rq = rq;
+      s->req = req;
+      s->head = item / row_blocks;
+      s->row0 = (item - s->head * row_blocks) * R;
+      s->rows = min(R, rq.q_len * p.share - s->row0);
+      const int first_q = s->row0 / p.share, last_q = (s->row0 + s->rows - 1) / p.share;
+      const int base = rq.len - rq.q_len;
+      s->hi = max(0, base + last_q + 1);
+      s->lo = p.window > 0 ? max(0, base + first_q - p.window + 1) : 0;
+      s->all_hi = base + first_q + 1;
+      s->all_lo = p.window > 0 ? base + last_q - p.window + 1 : 0;
+      const int stage = s->lo / kStage;
+      s->s0 = stage + c0;
+      s->s1 = min(stage + c1, (s->hi + kStage - 1) / kStage);
+      s->first = c0 == 0;
+      s->last = c1 == shape.units;
+      s->item_end = req_u + (long long)(item + 1) * shape.units;
+      s->units = c1 - c0;
+      u += c1 - c0;
+      return true;
+    }
+    return false;
+  }
+};
 
 template <int D, int NG, int NT>
 __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTAS) decode_attention_kernel(
     const DecodeParams p) {
   using C = DCfg<D, NG, NT>;
-  constexpr int H = C::H, R = C::R, W = C::WARPS;
-  constexpr int UNIT = W * kTile;
+  constexpr int H = C::H, R = C::R, W = C::WARPS, DEPTH = C::DEPTH;
   extern __shared__ __align__(128) uint8_t smem[];
   float* merge = reinterpret_cast<float*>(smem + C::RING);
   float* stats = reinterpret_cast<float*>(smem + C::RING + C::MERGE);  // [W][R][m, l, beta...]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING + C::MERGE + C::STATS);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING + C::MERGE + C::STATS);  // [DEPTH]
+  uint64_t* empty = full + DEPTH;                                                    // [DEPTH]
+  uint32_t* there = reinterpret_cast<uint32_t*>(empty + DEPTH);  // [DEPTH] 16-token tiles whose page exists
   __shared__ UnitSearch<C::THREADS> search;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, qd = lane & 3;
   pdl_launch_dependents();
-  if (lane == 0) {
-    for (int i = 0; i < kDepth; ++i) mbar_init(&bars[warp * kDepth + i], 1);
+  if (tid == 0) {
+    for (int i = 0; i < DEPTH; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], W);
+    }
     fence_mbar_init();
   }
   pdl_wait();
@@ -158,89 +224,102 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
   if (tid == 0) header->followers = 0;
 
   auto count = [&](int i) -> long long {
-    const ItemShape s = item_shape<R, UNIT>(p, kv_request(p.batch, p.cache.page, i));
+    const ItemShape s = item_shape<R>(p, kv_request(p.batch, p.cache.page, i));
     return (long long)s.items * s.units;
   };
   long long own, mine;
-  search.count_all(p.batch.requests, count, &own, &mine);
+  search.count_all(p.batch.requests, count, &own, &mine);  // its barriers publish the mbarriers too
   const long long U = search.total;
   const long long n = min((long long)gridDim.x, U);
   if ((long long)blockIdx.x >= n) return;
-  long long u = U * blockIdx.x / n;
-  const long long u_end = U * (blockIdx.x + 1) / n;
-  search.find(p.batch.requests, count, u, own, mine);
-  int req = search.request;
-  long long req_u = search.first;
-  if (req < 0) return;  // not reached: u < U
+  Walk<R> walk;
+  walk.u = U * blockIdx.x / n;
+  walk.u_end = U * (blockIdx.x + 1) / n;
+  search.find(p.batch.requests, count, walk.u, own, mine);
+  walk.req = search.request;
+  walk.req_u = search.first;
+  if (walk.req < 0) return;  // not reached: u < U
+  Segment sg;
+  int stage_i = 0;  // stages of this block so far
 
-  const uint32_t ring = smem_u32(smem) + warp * kDepth * C::TILE_BYTES;
-  uint64_t* const bar = bars + warp * kDepth;
-  uint32_t phase = 0;  // parity of each ring slot
+  // chunk: the tokens of a stage that lie in one page
+  const int chunk = min(p.cache.page, kStage), chunk_shift = min(p.cache.page_shift, 7);
+  const int chunk_bytes = chunk * (D + 8 * NG);
 
-  while (u < u_end) {
-    const KvRequest rq = kv_request(p.batch, p.cache.page, req);
-    const ItemShape shape = item_shape<R, UNIT>(p, rq);
-    const long long req_units = (long long)shape.items * shape.units;
-    if (u >= req_u + req_units) {  // on to the next request (of no units: passed over)
-      req_u += req_units;
-      if (++req >= p.batch.requests) return;  // not reached
-      continue;
-    }
-    const int item = (int)((u - req_u) / shape.units);
-    const int c0 = (int)((u - req_u) - (long long)item * shape.units);
-    const int c1 = (int)min((long long)shape.units, c0 + (u_end - u));
-    const int blocks_of = shape.items / p.cache.heads;
-    const int head = item / blocks_of, row0 = (item - head * blocks_of) * R;
-    const int rows = min(R, rq.q_len * p.share - row0);
-
-    // keys that any row of the item sees: [lo, hi)
-    const int first_q = row0 / p.share, last_q = (row0 + rows - 1) / p.share;
-    const int base_pos = rq.len - rq.q_len;
-    const int hi = max(0, base_pos + last_q + 1);
-    const int lo = p.window > 0 ? max(0, base_pos + first_q - p.window + 1) : 0;
-    const int all_see_hi = base_pos + first_q + 1;                                    // every row sees keys below it
-    const int all_see_lo = p.window > 0 ? base_pos + last_q - p.window + 1 : 0;       // and from it
-    const int tile0 = lo / kTile + c0 * W;
-    const int tile1 = min((hi + kTile - 1) / kTile, lo / kTile + c1 * W);
-    const int my_tiles = tile1 > tile0 + warp ? (tile1 - tile0 - warp + W - 1) / W : 0;
-
-    // page of this warp's tile i, 32 tiles at a time, a tile to a lane
-    const int* row_table = p.batch.table + (size_t)req * p.batch.ld_table;
-    auto load_pages = [&](int i0) {
-      const int i = i0 + lane;
-      return i < my_tiles ? __ldg(row_table + (((tile0 + warp + i * W) * kTile) >> p.cache.page_shift)) : -1;
-    };
-    int pages = load_pages(0), pages_next = -1;
-    uint32_t sent = 0;  // ring slots with a copy under way
-    auto issue = [&](int i) {  // tile i of this warp into slot i % kDepth; all lanes
-      if (i > 0 && (i & 31) == 0) pages = pages_next;
-      if ((i & 31) == 16) pages_next = load_pages((i & ~31) + 32);
-      const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-      const int slot = i % kDepth;
-      sent &= ~(1u << slot);
-      if (page < 0 || page >= p.cache.num_pages) return;
-      sent |= 1u << slot;
-      const int off = ((tile0 + warp + i * W) * kTile) & (p.cache.page - 1);
-      const uint8_t* blk =
-          p.cache.blocks + ((long long)page * p.cache.heads + head) * (long long)p.cache.block_bytes;
-      const uint32_t dst = ring + slot * C::TILE_BYTES;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bar[slot], C::TILE_BYTES);
-        const int half = p.cache.page * (D / 2);
-        bulk_load(dst, blk + off * (D / 2), C::CODES, &bar[slot]);
-        bulk_load(dst + C::CODES, blk + half + off * (D / 2), C::CODES, &bar[slot]);
-        bulk_load(dst + 2 * C::CODES, blk + 2 * half + off * (NG * 4), C::PAR, &bar[slot]);
-        bulk_load(dst + 2 * C::CODES + C::PAR, blk + 2 * half + (p.cache.page + off) * (NG * 4), C::PAR, &bar[slot]);
+  if (warp == W) {
+    // ---------------- loader ----------------
+    const int chunks = kStage >> chunk_shift;
+    bool ok = true;
+    while (ok && walk.next(p, &sg)) {
+      const int* row = p.batch.table + (size_t)sg.req * p.batch.ld_table;
+      const int pages = (sg.hi + p.cache.page - 1) >> p.cache.page_shift;  // pages that hold a visible key
+      auto page_of = [&](int s) {  // lane i: the page of chunk i of stage s
+        const int at = (int)(((long long)s * kStage + lane * chunk) >> p.cache.page_shift);
+        const bool seen = (long long)s * kStage + (lane + 1) * chunk > sg.lo;
+        return s < sg.s1 && lane < chunks && at < pages && seen ? __ldg(row + at) : -1;
+      };
+      int page = page_of(sg.s0);
+      for (int s = sg.s0; s < sg.s1; ++s, ++stage_i) {
+        const int slot = stage_i % DEPTH;
+        const int next = page_of(s + 1);
+        if (!mbar_wait(&empty[slot], ((stage_i / DEPTH) & 1) ^ 1, 0x302)) {
+          ok = false;
+          break;
+        }
+        const bool in = page >= 0 && page < p.cache.num_pages;
+        const uint32_t mask = __ballot_sync(0xffffffffu, in);
+        uint8_t* dst = smem + slot * C::STAGE_BYTES + lane * chunk_bytes;
+        if (lane == 0) {
+          // chunk bit -> bits of its 16-token tiles
+          uint32_t tiles = 0;
+          for (int i = 0; i < chunks; ++i)
+            if (mask >> i & 1u) tiles |= ((1u << (chunk / kTile)) - 1u) << (i * (chunk / kTile));
+          there[slot] = tiles;
+          mbar_arrive_expect_tx(&full[slot], (uint32_t)__popc(mask) * chunk_bytes);
+        }
+        __syncwarp();
+        if (in) {
+          const uint8_t* blk =
+              p.cache.blocks + ((long long)page * p.cache.heads + sg.head) * (long long)p.cache.block_bytes;
+          if (p.cache.page <= kStage) {
+            bulk_load(smem_u32(dst), blk, chunk_bytes, &full[slot]);
+          } else {
+            const int off = (s * kStage) & (p.cache.page - 1), half = p.cache.page * (D / 2);
+            const uint32_t d0 = smem_u32(dst);
+            bulk_load(d0, blk + off * (D / 2), kStage * (D / 2), &full[slot]);
+            bulk_load(d0 + kStage * (D / 2), blk + half + off * (D / 2), kStage * (D / 2), &full[slot]);
+            bulk_load(d0 + kStage * D, blk + 2 * half + off * (NG * 4), kStage * NG * 4, &full[slot]);
+            bulk_load(d0 + kStage * (D + 4 * NG), blk + 2 * half + (p.cache.page + off) * (NG * 4), kStage * NG * 4,
+                      &full[slot]);
+          }
+        }
+        page = next;
       }
-    };
-    for (int i = 0; i < kDepth - 1 && i < my_tiles; ++i) issue(i);
+    }
+    // no copy is under way when the block ends
+    for (int i = max(0, stage_i - DEPTH); i < stage_i; ++i)
+      if (!mbar_wait(&full[i % DEPTH], (i / DEPTH) & 1, 0x303)) break;
+    return;
+  }
 
+  // this warp's tiles inside a stage
+  uint32_t kofs[kTiles], pofs[kTiles];
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) {
+    const int tk = (warp * kTiles + i) * kTile;
+    const uint32_t base = (tk >> chunk_shift) * chunk_bytes;
+    kofs[i] = base + (tk & (chunk - 1)) * (D / 2);
+    pofs[i] = base + chunk * D + (tk & (chunk - 1)) * (NG * 4);
+  }
+  bool ok = true;
+  while (walk.next(p, &sg)) {
+    const KvRequest rq = sg.rq;
+    const int head = sg.head, row0 = sg.row0, rows = sg.rows, base_pos = rq.len - rq.q_len;
     // Query fragments: row n = 8 nt + r, channels 64 h + 16 qd .. + 15, scaled
     // by a power of two so that the row's largest value lies in [2^14, 2^15)
     // (an exact product; q / 16 for the odd nibbles then stays normal).
     uint32_t qf[NT][4 * H][2];
     float f[NT][2], qs[NT][2][NG];  // of this thread's columns (rows 2 qd, 2 qd + 1)
-    int pos[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = 8 * nt + r;
@@ -308,19 +387,16 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
             qs[nt][c][1] = s1 * p.scale_log2;
         }
         qs[nt][c][0] = s0 * p.scale_log2;
-        const int col = 8 * nt + 2 * qd + c;
-        pos[nt][c] = base_pos + (row0 + min(col, rows - 1)) / p.share;
       }
     }
 
     float o[NT][4 * H][4];
-    float m[NT][2], mu[NT][2], l[NT][2], beta[NT][2][NG];
+    float m[NT][2], l[NT][2], beta[NT][2][NG];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        m[nt][c] = -INFINITY;  // reference so far; mu is what is subtracted (0 while there is none)
-        mu[nt][c] = 0.f;
+        m[nt][c] = kNone;
         l[nt][c] = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) beta[nt][c][g] = 0.f;
@@ -331,179 +407,189 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
         for (int k = 0; k < 4; ++k) o[nt][j][k] = 0.f;
     }
 
-    for (int i = 0; i < my_tiles; ++i) {
-      __syncwarp();  // the slot that is refilled next has been read by every lane
-      if (i + kDepth - 1 < my_tiles) issue(i + kDepth - 1);
-      const int slot = i % kDepth;
-      if (!(sent >> slot & 1u)) continue;  // a page outside the cache: its tokens do not exist
-      if (!mbar_wait(&bar[slot], (phase >> slot) & 1u, 0x301)) break;
-      phase ^= 1u << slot;
-      const int tok0 = (tile0 + warp + i * W) * kTile;
-      const uint32_t kb = ring + slot * C::TILE_BYTES, vb = kb + C::CODES;
-      const uint32_t kp = kb + 2 * C::CODES, vp = kp + C::PAR;
-      const bool edge = tok0 < all_see_lo || tok0 + kTile > all_see_hi;  // some row does not see some key
-
-      // S^T = K Q^T on the codes, per group of channels
-      float s[NT][NG][4];
+    for (int s = sg.s0; s < sg.s1; ++s, ++stage_i) {
+      const int slot = stage_i % DEPTH;
+      ok = ok && mbar_wait(&full[slot], (stage_i / DEPTH) & 1, 0x301);
+      if (!ok) break;
+      const int tok0 = s * kStage + warp * (kTiles * kTile);
+      const uint32_t tiles = there[slot] >> (warp * kTiles);
+      const uint32_t sb = smem_u32(smem) + slot * C::STAGE_BYTES;
+      if (tok0 < sg.hi && tok0 + kTiles * kTile > sg.lo && (tiles & ((1u << kTiles) - 1u))) {
+        // some row does not see some key of the tiles, or a page is missing
+        const bool edge = tok0 < sg.all_lo || tok0 + kTiles * kTile > sg.all_hi ||
+                          (~tiles & ((1u << kTiles) - 1u)) != 0;
+        constexpr int JT = C::JOINT;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[nt][g][k] = 0.f;
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        const uint2 ka = lds64(kb + r * (D / 2) + 32 * h + 8 * qd);
-        const uint2 kc = lds64(kb + (r + 8) * (D / 2) + 32 * h + 8 * qd);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t wa = j ? ka.y : ka.x, wc = j ? kc.y : kc.x;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t xa = e ? wa >> 8 : wa, xc = e ? wc >> 8 : wc;
-            const uint32_t a0 = xa & 0x000F000Fu, a1 = xc & 0x000F000Fu;
-            const uint32_t a2 = xa & 0x00F000F0u, a3 = xc & 0x00F000F0u;
-            const int ks = 4 * h + 2 * j + e;
-#pragma unroll
+        for (int i0 = 0; i0 < kTiles; i0 += JT) {
+          float lw[JT][NT][2][2];  // [token half][column]: logits, in log2 units
+          float vlg[JT][2][NG], vrc[JT][2][NG], vmi[JT][2][NG];
+          bool over = false;
+  #pragma unroll
+          for (int i = 0; i < JT; ++i) {
+            // S^T = K Q^T on the codes, per group of channels
+            float sc[NT][NG][4];
+  #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_16816(s[nt][NG == 1 ? 0 : h], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
-          }
-        }
-      }
-
-      // parameters of tokens r and r + 8
-      float ksc[2][NG], kmi[2][NG], vlg[2][NG], vrc[2], vmi[2][NG];
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int tk = r + 8 * y;
-        const bool in = !edge || (tok0 + tk >= lo && tok0 + tk < hi);  // else what lies there is not a token of ours
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          uint32_t a = lds32(kp + (tk * NG + g) * 4), b = lds32(vp + (tk * NG + g) * 4);
-          a = in ? a : 0x00003C00u;  // scale 1, minimum 0
-          b = in ? b : 0x00003C00u;
-          const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
-          const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
-          ksc[y][g] = fa.x;
-          kmi[y][g] = fa.y;
-          const float vs = fmaxf(fb.x, 5.9604644775390625e-8f);
-          vlg[y][g] = lg2(vs);
-          vmi[y][g] = fb.y;
-          if (g == 0) vrc[y] = __fdividef(1.0f, vs);
-        }
-      }
-
-      // logits in log2 units of p (lw) and of p s' (a)
-      float lw[NT][2][2];  // [token half][column]
-      bool over = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x = fmaf(s[nt][0][2 * y + c] * f[nt][c], ksc[y][0], kmi[y][0] * qs[nt][c][0]);
-            if constexpr (NG == 2)
-              x = fmaf(s[nt][1][2 * y + c] * f[nt][c], ksc[y][1], fmaf(kmi[y][1], qs[nt][c][1], x));
-            if (edge) {
-              const int key = tok0 + r + 8 * y;
-              const bool see = key <= pos[nt][c] && key < hi && (p.window <= 0 || key > pos[nt][c] - p.window);
-              x = see ? x : -INFINITY;
-            }
-            lw[nt][y][c] = x;
-            float a = x + vlg[y][0];
-            if constexpr (NG == 2) a = x + fmaxf(vlg[y][0], vlg[y][1]);
-            over |= a > m[nt][c] + kTrigger;
-          }
-      if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x = -INFINITY;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              float lg = vlg[y][0];
-              if constexpr (NG == 2) lg = fmaxf(lg, vlg[y][1]);
-              x = fmaxf(x, lw[nt][y][c] + lg);
-            }
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float next = fmaxf(m[nt][c], x - kHeadroom);
-            if (next > m[nt][c]) {
-              const float w = ex2(m[nt][c] - next);  // 0 for the first reference
-              m[nt][c] = next;
-              mu[nt][c] = next;
-              l[nt][c] *= w;
-#pragma unroll
-              for (int g = 0; g < NG; ++g) beta[nt][c][g] *= w;
-#pragma unroll
-              for (int j = 0; j < 4 * H; ++j) {
-                o[nt][j][c] *= w;
-                o[nt][j][2 + c] *= w;
+  #pragma unroll
+              for (int g = 0; g < NG; ++g)
+  #pragma unroll
+                for (int k = 0; k < 4; ++k) sc[nt][g][k] = 0.f;
+            const uint32_t kb = sb + kofs[i0 + i];
+  #pragma unroll
+            for (int h = 0; h < H; ++h) {
+              const uint2 ka = lds64(kb + r * (D / 2) + 32 * h + 8 * qd);
+              const uint2 kc = lds64(kb + (r + 8) * (D / 2) + 32 * h + 8 * qd);
+  #pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t wa = j ? ka.y : ka.x, wc = j ? kc.y : kc.x;
+  #pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t xa = e ? wa >> 8 : wa, xc = e ? wc >> 8 : wc;
+                  const uint32_t a0 = xa & 0x000F000Fu, a1 = xc & 0x000F000Fu;
+                  const uint32_t a2 = xa & 0x00F000F0u, a3 = xc & 0x00F000F0u;
+                  const int ks = 4 * h + 2 * j + e;
+  #pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+                    mma_16816(sc[nt][NG == 1 ? 0 : h], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+                }
               }
             }
+            // parameters of tokens r and r + 8
+            const uint32_t kp = sb + pofs[i0 + i], vp = kp + chunk * (NG * 4);
+            float ksc[2][NG], kmi[2][NG];
+            bool in[2];
+  #pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int tk = r + 8 * y, key = tok0 + (i0 + i) * kTile + tk;
+              in[y] = !edge || (key >= sg.lo && key < sg.hi && (tiles >> (i0 + i) & 1u));  // else no token of ours lies there
+  #pragma unroll
+              for (int g = 0; g < NG; ++g) {
+                uint32_t a = lds32(kp + (tk * NG + g) * 4), b = lds32(vp + (tk * NG + g) * 4);
+                a = in[y] ? a : 0x00003C00u;  // scale 1, minimum 0
+                b = in[y] ? b : 0x00003C00u;
+                const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
+                const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
+                ksc[y][g] = fa.x;
+                kmi[y][g] = fa.y;
+                const float vs = fmaxf(fb.x, 5.9604644775390625e-8f);
+                vlg[i][y][g] = lg2(vs);
+                vrc[i][y][g] = __fdividef(1.0f, vs);
+                vmi[i][y][g] = fb.y;
+              }
+            }
+  #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+  #pragma unroll
+              for (int y = 0; y < 2; ++y)
+  #pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  float x = fmaf(sc[nt][0][2 * y + c] * f[nt][c], ksc[y][0], kmi[y][0] * qs[nt][c][0]);
+                  if constexpr (NG == 2)
+                    x = fmaf(sc[nt][1][2 * y + c] * f[nt][c], ksc[y][1], fmaf(kmi[y][1], qs[nt][c][1], x));
+                  if (edge) {
+                    const int key = tok0 + (i0 + i) * kTile + r + 8 * y;
+                    const int at = base_pos + (row0 + min(8 * nt + 2 * qd + c, rows - 1)) / p.share;  // the row's position
+                    const bool see = in[y] && key <= at && (p.window <= 0 || key > at - p.window);
+                    x = see ? x : -INFINITY;
+                  }
+                  lw[i][nt][y][c] = x;
+                  float a = x + vlg[i][y][0];
+                  if constexpr (NG == 2) a = x + fmaxf(vlg[i][y][0], vlg[i][y][1]);
+                  over |= a > m[nt][c] + kTrigger;
+                }
           }
-      }
+          if (__any_sync(0xffffffffu, over)) {
+  #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+  #pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float x = -INFINITY;
+  #pragma unroll
+                for (int i = 0; i < JT; ++i)
+  #pragma unroll
+                  for (int y = 0; y < 2; ++y) {
+                    float lg = vlg[i][y][0];
+                    if constexpr (NG == 2) lg = fmaxf(lg, vlg[i][y][1]);
+                    x = fmaxf(x, lw[i][nt][y][c] + lg);
+                  }
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                const float next = fmaxf(m[nt][c], x - kHeadroom);
+                if (next > m[nt][c]) {
+                  const float w = ex2(m[nt][c] - next);  // 0 for the first reference
+                  m[nt][c] = next;
+                  l[nt][c] *= w;
+  #pragma unroll
+                  for (int g = 0; g < NG; ++g) beta[nt][c][g] *= w;
+  #pragma unroll
+                  for (int j = 0; j < 4 * H; ++j) {
+                    o[nt][j][c] *= w;
+                    o[nt][j][2 + c] *= w;
+                  }
+                }
+              }
+          }
 
-      // weights p s' as FP16, their sums, and P^T fragments
-      uint32_t pf[NT][NG][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          float w0[2];
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const __half2 h2 = __floats2half2_rn(ex2(lw[nt][y][0] + (vlg[y][g] - mu[nt][0])),
-                                                 ex2(lw[nt][y][1] + (vlg[y][g] - mu[nt][1])));
-            if (g == 0) {
-              const float2 back = __half22float2(h2);
-              w0[0] = back.x * vrc[y];
-              w0[1] = back.y * vrc[y];
-              l[nt][0] += w0[0];
-              l[nt][1] += w0[1];
+  #pragma unroll
+          for (int i = 0; i < JT; ++i) {
+            // weights p s' as FP16, their sums, and P^T fragments
+            uint32_t pf[NT][NG][2];
+  #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+  #pragma unroll
+              for (int y = 0; y < 2; ++y)
+  #pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                  const __half2 h2 = __floats2half2_rn(ex2(lw[i][nt][y][0] + (vlg[i][y][g] - m[nt][0])),
+                                                       ex2(lw[i][nt][y][1] + (vlg[i][y][g] - m[nt][1])));
+                  const float2 back = __half22float2(h2);
+                  const float w[2] = {back.x * vrc[i][y][g], back.y * vrc[i][y][g]};
+  #pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    if (g == 0) l[nt][c] += w[c];
+                    // a minimum that this row does not see is left out, whatever it holds
+                    const float mi = edge && w[c] == 0.f ? 0.f : vmi[i][y][g];
+                    beta[nt][c][g] = fmaf(w[c], mi, beta[nt][c][g]);
+                  }
+                  pf[nt][g][y] = movmatrix(*reinterpret_cast<const uint32_t*>(&h2));
+                }
+
+            // O^T += V^T P^T: word 8 h + r of tokens 2 qd, 2 qd + 1, + 8, + 9.
+            // Odd lanes of a quad read their two tokens in the other order
+            // (banks), the byte selectors put them back.
+            const uint32_t vb = sb + kofs[i0 + i] + chunk * (D / 2);
+            const int sw = qd & 1;
+            const uint32_t sel_lo = sw ? 0x1054u : 0x5410u, sel_hi = sw ? 0x3276u : 0x7632u;
+  #pragma unroll
+            for (int h = 0; h < H; ++h) {
+              const uint32_t at = vb + 32 * h + 4 * r + (2 * qd) * (D / 2);
+              const uint32_t t0 = lds32(at + sw * (D / 2)), t1 = lds32(at + (sw ^ 1) * (D / 2));
+              const uint32_t t8 = lds32(at + (8 + sw) * (D / 2)), t9 = lds32(at + (8 + (sw ^ 1)) * (D / 2));
+              const uint32_t wl[2] = {prmt(t0, t1, sel_lo), prmt(t0, t1, sel_hi)};
+              const uint32_t wh[2] = {prmt(t8, t9, sel_lo), prmt(t8, t9, sel_hi)};
+  #pragma unroll
+              for (int j = 0; j < 2; ++j)
+  #pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t xa = e ? wl[j] >> 8 : wl[j], xc = e ? wh[j] >> 8 : wh[j];
+                  const uint32_t a0 = xa & 0x000F000Fu, a1 = xa & 0x00F000F0u;  // channels 4 j + 2 e, + 1 of the word
+                  const uint32_t a2 = xc & 0x000F000Fu, a3 = xc & 0x00F000F0u;
+  #pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+                    mma_16816(o[nt][4 * h + 2 * j + e], a0, a1, a2, a3, pf[nt][NG == 1 ? 0 : h][0],
+                              pf[nt][NG == 1 ? 0 : h][1]);
+                }
             }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              // a minimum that this row does not see is left out, whatever it holds
-              const float mi = edge && w0[c] == 0.f ? 0.f : vmi[y][g];
-              beta[nt][c][g] = fmaf(w0[c], mi, beta[nt][c][g]);
-            }
-            pf[nt][g][y] = movmatrix(*reinterpret_cast<const uint32_t*>(&h2));
           }
         }
-
-      // O^T += V^T P^T: word 8 h + r of tokens 2 qd, 2 qd + 1, + 8, + 9.  Odd
-      // lanes of a quad read their two tokens in the other order (banks), the
-      // byte selectors put them back.
-      const int sw = qd & 1;
-      const uint32_t sel_lo = sw ? 0x1054u : 0x5410u, sel_hi = sw ? 0x3276u : 0x7632u;
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        const uint32_t at = vb + 32 * h + 4 * r + (2 * qd) * (D / 2);
-        const uint32_t t0 = lds32(at + sw * (D / 2)), t1 = lds32(at + (sw ^ 1) * (D / 2));
-        const uint32_t t8 = lds32(at + (8 + sw) * (D / 2)), t9 = lds32(at + (8 + (sw ^ 1)) * (D / 2));
-        const uint32_t wl[2] = {prmt(t0, t1, sel_lo), prmt(t0, t1, sel_hi)};
-        const uint32_t wh[2] = {prmt(t8, t9, sel_lo), prmt(t8, t9, sel_hi)};
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t xa = e ? wl[j] >> 8 : wl[j], xc = e ? wh[j] >> 8 : wh[j];
-            const uint32_t a0 = xa & 0x000F000Fu, a1 = xa & 0x00F000F0u;  // channels 4 j + 2 e, + 1 of the word
-            const uint32_t a2 = xc & 0x000F000Fu, a3 = xc & 0x00F000F0u;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_16816(o[nt][4 * h + 2 * j + e], a0, a1, a2, a3, pf[nt][NG == 1 ? 0 : h][0],
-                        pf[nt][NG == 1 ? 0 : h][1]);
-          }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
     }
 
     // ---------------- join the warps ----------------
-    __syncthreads();  // the merge buffer and statistics of the last item have been read
+    named_barrier(1, 32 * W);  // the merge buffer and statistics of the last item have been read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -522,13 +608,13 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
           for (int g = 0; g < NG; ++g) st[2 + g] = beta[nt][c][g];
         }
       }
-    const bool whole = c0 == 0 && c1 == shape.units;
+    const bool whole = sg.first && sg.last;
     float* part = nullptr;
     if (!whole)
-      part = p.partials + ((size_t)blockIdx.x * 2 + (c0 == 0 ? 1 : 0)) * Partial<D, R>::FLOATS;
+      part = p.partials + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * Partial<D, R>::FLOATS;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (nt > 0) __syncthreads();
+      if (nt > 0) named_barrier(1, 32 * W);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float* dst = merge + (warp * 8 + 2 * qd + c) * C::OSTRIDE + 8 * r;
@@ -542,18 +628,18 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
                             o[nt][4 * h + 2 * j + 1][c] * k24, o[nt][4 * h + 2 * j + 1][2 + c] * k20);
           }
       }
-      __syncthreads();
-      for (int e = tid; e < 8 * (D / 4); e += C::THREADS) {
+      named_barrier(1, 32 * W);
+      for (int e = tid; e < 8 * (D / 4); e += 32 * W) {
         const int row8 = e / (D / 4), ch = (e - row8 * (D / 4)) * 4;
         const int row = 8 * nt + row8;
-        float mm = -INFINITY;
+        float mm = kNone;
 #pragma unroll
         for (int w = 0; w < W; ++w) mm = fmaxf(mm, stats[(w * R + row) * (2 + NG)]);
         float ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const float* st = stats + (w * R + row) * (2 + NG);
-          const float wm = st[0] == -INFINITY ? 0.f : ex2(st[0] - mm);
+          const float wm = ex2(st[0] - mm);
           ll = fmaf(wm, st[1], ll);
           const float bt = st[2 + (NG == 2 ? ch / 64 : 0)];
           const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + row8) * C::OSTRIDE + ch);
@@ -581,15 +667,14 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
         }
       }
     }
-    if (!whole && c0 == 0 && tid == 0) {
+    if (!whole && sg.first && tid == 0) {
       // the block that holds the item's last unit
-      const long long last_u = req_u + (long long)(item + 1) * shape.units - 1;
+      const long long last_u = sg.item_end - 1;
       long long b = ((last_u + 1) * n - 1) / U;
       while (U * b / n > last_u) --b;
       while (U * (b + 1) / n <= last_u) ++b;
       *header = Header{(int)(b - blockIdx.x), rq.q0, row0, rows, head};
     }
-    u += c1 - c0;
   }
 }
 
@@ -614,7 +699,7 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const DecodeParams p) 
   for (int i = -1; i < h.followers; ++i) {
     const float* part = i < 0 ? first : rest + (size_t)i * 2 * F;
     const float mi = part[R * D + row];
-    const float w = mi == -INFINITY ? 0.f : ex2(mi - m);
+    const float w = ex2(mi - m);
     const float4 v = *reinterpret_cast<const float4*>(part + row * D + ch);
     l = fmaf(w, part[R * D + R + row], l);
     acc[0] = fmaf(w, v.x, acc[0]);
@@ -674,7 +759,7 @@ size_t kv4_decode_workspace(int head_dim) {
   auto bytes = [&](size_t blocks, size_t R) {
     return ((blocks * sizeof(Header) + 255) & ~size_t(255)) + blocks * 2 * R * (head_dim + 2) * sizeof(float);
   };
-  return std::max(bytes(2 * sms, 8), bytes(sms, 16));
+  return std::max(bytes(3 * sms, 8), bytes(2 * sms, 16));
 }
 
 tlq_status launch_kv4_decode(const KvAttention& a, cudaStream_t stream) {
