@@ -34,15 +34,29 @@ __device__ __forceinline__ float peer_f32(const float* p, uint32_t rank) {
   return v;
 }
 
-// MT: 16-token tiles of a cluster
+// MT: 16-token tiles of a cluster (1 or 4).  A warp takes one tile and one of
+// WK shares of the block's k.
 template <int MT>
-__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads) lora_kernel(const LoraArgs a) {
-  constexpr int TT = 16 * MT;
+struct LCfg {
+  static constexpr int TT = 16 * MT;
+  static constexpr int WK = kWarps / MT;
+  static constexpr int PART = WK * TT * (kMaxRank + 1) * 4;
+  static constexpr int SUMS = TT * kMaxRank * 4;
+  static constexpr int SPLIT = 2 * TT * (kMaxRank + 8) * 2;
+  static constexpr int SMEM = PART + SUMS + SPLIT + TT * 4;
+  static_assert(PART % 16 == 0 && SUMS % 16 == 0, "alignment");
+};
+
+template <int MT>
+__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads, 2) lora_kernel(const LoraArgs a) {
+  using C = LCfg<MT>;
+  constexpr int TT = C::TT, WK = C::WK;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float(*part)[TT][kMaxRank + 1] = reinterpret_cast<float(*)[TT][kMaxRank + 1]>(smem);  // [WK] A x by share of k
+  float(*sums)[kMaxRank] = reinterpret_cast<float(*)[kMaxRank]>(smem + C::PART);        // [TT] of this block's k
+  __half(*th)[TT][kMaxRank + 8] = reinterpret_cast<__half(*)[TT][kMaxRank + 8]>(smem + C::PART + C::SUMS);  // [2]
+  float* back = reinterpret_cast<float*>(smem + C::PART + C::SUMS + C::SPLIT);          // 2^e * scale of each token
   __shared__ UnitSearch<kThreads> search;
-  __shared__ float part[kWarps][16][kMaxRank + 1];   // A x of each warp's share of k, one 16-token tile at a time
-  __shared__ float sums[TT][kMaxRank];               // this block's A x, then the cluster's
-  __shared__ __half th[2][TT][kMaxRank + 8];         // the high and low parts
-  __shared__ float back[TT];                         // 2^e * scale of each token
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, qd = lane & 3;
   const uint32_t rank = cluster_ctarank();
   pdl_launch_dependents();
@@ -66,55 +80,96 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads) lora_
   if (w < 0 || w >= a.num_adapters) w = -1;  // no adapter: y goes through as it is
   const int NR = a.rank, KS = (NR + 15) / 16;
 
+  // Columns of the second product: 32 at a time to a warp; thread qd of a quad
+  // holds columns 8 qd .. 8 qd + 7 of its rows.  The first 32 of y and B are
+  // asked for here, before A x is known.
+  const int blocks32 = (a.N + 31) / 32;
+  const int b_lo = (int)((long long)blocks32 * rank / kRanks), b_hi = (int)((long long)blocks32 * (rank + 1) / kRanks);
+  const __half* const B = a.B + (size_t)max(w, 0) * a.N * NR;
+  uint2 bf[4][kMaxRank / 16];
+  uint4 yv[MT][2];
+  auto load_columns = [&](int nb) {
+    const int n0 = 32 * nb, col = n0 + 8 * qd;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int row = 16 * mt + r + 8 * y;
+        if (row < rows && col < a.N)
+          yv[mt][y] = *reinterpret_cast<const uint4*>(a.y + (long long)(t0 + row) * a.ldy + col);
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + 8 * (r >> 1) + 2 * j + (r & 1);
+#pragma unroll
+      for (int s = 0; s < kMaxRank / 16; ++s) {
+        const int k = 16 * s + 4 * qd;
+        bf[j][s] = w >= 0 && n < a.N && k < NR ? __ldg(reinterpret_cast<const uint2*>(B + (size_t)n * NR + k))
+                                               : make_uint2(0, 0);
+      }
+    }
+  };
+  int nb = b_lo + warp;
+  if (nb < b_hi) load_columns(nb);
+
   if (w >= 0) {
     // ---- A x: this block's k, 32 at a time to a warp ----
     const int chunks = (a.K + 31) / 32;
     const int k_lo = (int)((long long)chunks * rank / kRanks), k_hi = (int)((long long)chunks * (rank + 1) / kRanks);
     const __half* A = a.A + (size_t)w * NR * a.K;
-    for (int mt = 0; mt < MT; ++mt) {
-      float acc[kMaxRank / 8][4];
+    const int mt = warp % MT, wk = warp / MT;
+    float acc[kMaxRank / 8][4];
 #pragma unroll
-      for (int j = 0; j < kMaxRank / 8; ++j)
+    for (int j = 0; j < kMaxRank / 8; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-      const int ra = 16 * mt + r, rb = ra + 8;
-      const __half* xa = a.x + (long long)(t0 + min(ra, rows - 1)) * a.ldx;
-      const __half* xb = a.x + (long long)(t0 + min(rb, rows - 1)) * a.ldx;
-      if (16 * mt < rows) {
-        for (int c = k_lo + warp; c < k_hi; c += kWarps) {
-          const int k = 32 * c + 8 * qd;
-          const bool in = k < a.K;
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-          const uint4 va = in ? *reinterpret_cast<const uint4*>(xa + k) : zero;
-          const uint4 vb = in ? *reinterpret_cast<const uint4*>(xb + k) : zero;
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    const int ra = 16 * mt + r, rb = ra + 8;
+    const __half* xa = a.x + (long long)(t0 + min(ra, rows - 1)) * a.ldx;
+    const __half* xb = a.x + (long long)(t0 + min(rb, rows - 1)) * a.ldx;
+    if (16 * mt < rows) {
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      uint4 na = zero, nc = zero;  // x of the next 32 k
+      auto load_x = [&](int c) {
+        const int k = 32 * c + 8 * qd;
+        const bool in = c < k_hi && k < a.K;
+        na = in ? *reinterpret_cast<const uint4*>(xa + k) : zero;
+        nc = in ? *reinterpret_cast<const uint4*>(xb + k) : zero;
+      };
+      load_x(k_lo + wk);
+      for (int c = k_lo + wk; c < k_hi; c += WK) {
+        const uint4 va = na, vb = nc;
+        const int k = 32 * c + 8 * qd;
+        const bool in = k < a.K;
+        uint4 b[kMaxRank / 8];
 #pragma unroll
-          for (int j = 0; j < kMaxRank / 8; ++j) {
-            if (8 * j < NR) {
-              const uint4 b = in ? __ldg(reinterpret_cast<const uint4*>(A + (size_t)(8 * j + r) * a.K + k)) : zero;
-              mma_16816(acc[j], va.x, vb.x, va.y, vb.y, b.x, b.y);
-              mma_16816(acc[j], va.z, vb.z, va.w, vb.w, b.z, b.w);
-            }
+        for (int j = 0; j < kMaxRank / 8; ++j)
+          b[j] = in && 8 * j < NR ? __ldg(reinterpret_cast<const uint4*>(A + (size_t)(8 * j + r) * a.K + k)) : zero;
+        load_x(c + WK);
+#pragma unroll
+        for (int j = 0; j < kMaxRank / 8; ++j) {
+          if (8 * j < NR) {
+            mma_16816(acc[j], va.x, vb.x, va.y, vb.y, b[j].x, b[j].y);
+            mma_16816(acc[j], va.z, vb.z, va.w, vb.w, b[j].z, b[j].w);
           }
         }
       }
-      __syncthreads();
+    }
 #pragma unroll
-      for (int j = 0; j < kMaxRank / 8; ++j) {
-        if (8 * j < NR) {
-          part[warp][r][8 * j + 2 * qd] = acc[j][0];
-          part[warp][r][8 * j + 2 * qd + 1] = acc[j][1];
-          part[warp][r + 8][8 * j + 2 * qd] = acc[j][2];
-          part[warp][r + 8][8 * j + 2 * qd + 1] = acc[j][3];
-        }
+    for (int j = 0; j < kMaxRank / 8; ++j) {
+      if (8 * j < NR) {
+        part[wk][ra][8 * j + 2 * qd] = acc[j][0];
+        part[wk][ra][8 * j + 2 * qd + 1] = acc[j][1];
+        part[wk][rb][8 * j + 2 * qd] = acc[j][2];
+        part[wk][rb][8 * j + 2 * qd + 1] = acc[j][3];
       }
-      __syncthreads();
-      for (int e = tid; e < 16 * NR; e += kThreads) {
-        const int row = e / NR, col = e - row * NR;
-        float s = 0.f;
+    }
+    __syncthreads();
+    for (int e = tid; e < TT * NR; e += kThreads) {
+      const int row = e / NR, col = e - row * NR;
+      float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) s += part[i][row][col];
-        sums[16 * mt + row][col] = s;
-      }
+      for (int i = 0; i < WK; ++i) s += part[i][row][col];
+      sums[row][col] = s;
     }
   }
   cluster_sync();
@@ -127,7 +182,11 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads) lora_
       for (int i = 0; i < 2; ++i) {
         const int col = lane + 32 * i;
         if (col < NR && row < rows) {
-          for (uint32_t k = 0; k < kRanks; ++k) v[i] += peer_f32(&sums[row][col], k);
+          float got[kRanks];
+#pragma unroll
+          for (uint32_t k = 0; k < kRanks; ++k) got[k] = peer_f32(&sums[row][col], k);
+#pragma unroll
+          for (uint32_t k = 0; k < kRanks; ++k) v[i] += got[k];
         }
         big = fmaxf(big, fabsf(v[i]));
       }
@@ -152,27 +211,10 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads) lora_
   __syncthreads();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this block has read its peers
 
-  // ---- out = y + B (A x): 32 columns at a time to a warp; thread qd of a quad
-  // holds columns 8 qd .. 8 qd + 7 of its two rows ----
-  const int blocks32 = (a.N + 31) / 32;
-  const int b_lo = (int)((long long)blocks32 * rank / kRanks), b_hi = (int)((long long)blocks32 * (rank + 1) / kRanks);
-  for (int nb = b_lo + warp; nb < b_hi; nb += kWarps) {
-    const int n0 = 32 * nb;
-    uint2 bf[4][kMaxRank / 16];
-    if (w >= 0) {
-      const __half* B = a.B + (size_t)w * a.N * NR;
+  // ---- out = y + B (A x) ----
+  for (; nb < b_hi; nb += kWarps) {
+    const int col = 32 * nb + 8 * qd;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + 8 * (r >> 1) + 2 * j + (r & 1);
-#pragma unroll
-        for (int s = 0; s < kMaxRank / 16; ++s) {
-          const int k = 16 * s + 4 * qd;
-          bf[j][s] = n < a.N && k < NR ? __ldg(reinterpret_cast<const uint2*>(B + (size_t)n * NR + k))
-                                       : make_uint2(0, 0);
-        }
-      }
-    }
-    const int col = n0 + 8 * qd;
     for (int mt = 0; mt < MT; ++mt) {
       if (16 * mt >= rows) break;
       float acc[4][4];
@@ -186,9 +228,9 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads) lora_
         for (int s = 0; s < kMaxRank / 16; ++s) {
           if (s < KS) {
 #pragma unroll
-            for (int part2 = 0; part2 < 2; ++part2) {
-              const uint2 fa = *reinterpret_cast<const uint2*>(&th[part2][ra][16 * s + 4 * qd]);
-              const uint2 fb = *reinterpret_cast<const uint2*>(&th[part2][rb][16 * s + 4 * qd]);
+            for (int half = 0; half < 2; ++half) {
+              const uint2 fa = *reinterpret_cast<const uint2*>(&th[half][ra][16 * s + 4 * qd]);
+              const uint2 fb = *reinterpret_cast<const uint2*>(&th[half][rb][16 * s + 4 * qd]);
 #pragma unroll
               for (int j = 0; j < 4; ++j) mma_16816(acc[j], fa.x, fb.x, fa.y, fb.y, bf[j][s].x, bf[j][s].y);
             }
@@ -199,11 +241,10 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads) lora_
       for (int y = 0; y < 2; ++y) {
         const int row = y ? rb : ra;
         if (row < rows && col < a.N) {
-          const uint4 old = *reinterpret_cast<const uint4*>(a.y + (long long)(t0 + row) * a.ldy + col);
-          uint4 res = old;
+          uint4 res = yv[mt][y];
           if (w >= 0) {
             const float up = back[row];
-            const uint32_t in[4] = {old.x, old.y, old.z, old.w};
+            const uint32_t in[4] = {res.x, res.y, res.z, res.w};
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -217,20 +258,28 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads) lora_
         }
       }
     }
+    if (nb + kWarps < b_hi) load_columns(nb + kWarps);
   }
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no block leaves while a peer reads it
 }
 
+// Tiles of 16 MT tokens that the batch can come to, whatever its lengths are.
+long long tile_bound(const LoraArgs& a, int mt) {
+  return std::min<long long>((long long)a.tokens / (16 * mt) + a.requests,
+                             (long long)a.requests * ((a.max_q + 16 * mt - 1) / (16 * mt)));
+}
+
 template <int MT>
 tlq_status launch_tiles(const LoraArgs& a, cudaStream_t stream) {
-  // at most this many tiles whatever the requests' lengths are
-  const long long tiles =
-      std::min<long long>((long long)a.tokens / (16 * MT) + a.requests,
-                          (long long)a.requests * ((a.max_q + 16 * MT - 1) / (16 * MT)));
+  const long long tiles = tile_bound(a, MT);
   if (tiles * kRanks > 0x7fffffffll) return set_error(TLQ_EUNSUPPORTED, "lora: %lld token tiles", tiles);
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(lora_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, LCfg<MT>::SMEM);
+  if (attr != cudaSuccess) return cuda_error(attr, "lora: shared memory");
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(tiles * kRanks), 1, 1);
   lc.blockDim = dim3(kThreads, 1, 1);
+  lc.dynamicSmemBytes = LCfg<MT>::SMEM;
   lc.stream = stream;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -243,7 +292,10 @@ tlq_status launch_tiles(const LoraArgs& a, cudaStream_t stream) {
 }  // namespace
 
 tlq_status launch_lora(const LoraArgs& a, cudaStream_t stream) {
-  return launch_tiles<1>(a, stream);
+  // 64-token tiles read A and B a quarter as often; 16-token tiles spread short
+  // steps over more blocks.
+  if (a.max_q <= 16 || tile_bound(a, 1) * kRanks <= 2 * device_info().sms) return launch_tiles<1>(a, stream);
+  return launch_tiles<4>(a, stream);
 }
 
 }  // namespace tlq
