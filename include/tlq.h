@@ -593,7 +593,7 @@ tlq_status tl_probe_read_bandwidth(const void* buf, size_t bytes, int reps, uint
  */
 typedef struct {
   void* blocks;      /* device, 16-byte aligned */
-  int64_t num_pages; /* 1 .. 2^31 - 1 */
+  int64_t num_pages; /* 1 .. 2^31 - 1, and so num_pages * heads */
   int heads;         /* key (and value) heads, 1 .. 4096 */
   int head_dim;      /* 64 or 128 */
   int page_size;     /* tokens of a page: 16, 32, 64, 128 or 256 */

@@ -7,7 +7,7 @@
 // The smallest FP16 number as the least scale keeps constant rows exact
 // (c = 0) and every scale's logarithm finite for the attention kernels.
 //
-// DRAM traffic bounds both kernels: 16 bytes of activations against 4 bytes of
+// DRAM traffic bounds both kernels: 32 bytes of activations against 8 bytes of
 // codes per thread, one pass, a row's lanes side by side so that loads and
 // stores cover whole sectors.
 #include <algorithm>
@@ -18,7 +18,6 @@ namespace tlq {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kRowsAtOnce = 2;  // rows of a thread under way at a time (16 bytes each)
 
 // n / d for n < 2^31 by one multiplication (d >= 1): m = ceil(2^(31 + s) / d)
 // with 2^s >= d errs by less than 1 / d.
@@ -44,7 +43,7 @@ struct CodeRow {
 template <int D>
 __device__ __forceinline__ CodeRow code_row(const KvCache& c, long long slot, int head, int part) {
   const int P = c.page, off = (int)(slot & (P - 1));
-  uint8_t* blk = c.blocks + ((slot >> c.page_shift) * c.heads + head) * (long long)c.block_bytes;
+  uint8_t* blk = c.blocks + ((uint32_t)(slot >> c.page_shift) * (uint32_t)c.heads + (uint32_t)head) * (uint64_t)c.block_bytes;
   const int half = P * D / 2, pw = c.group == D ? 4 : 8;
   CodeRow r;
   r.codes = blk + part * half + off * (D / 2);
@@ -56,127 +55,159 @@ __device__ __forceinline__ bool in_cache(const KvCache& c, long long slot) {
   return slot >= 0 && slot < c.num_pages << c.page_shift;
 }
 
-// The word of eight codes rint((x - b) / s), and whether all of them are
-// certain.  With inv = fp32(1 / s), t = (x - b) * inv is within 2^-22 of the
-// quotient relative to it, so n = rint(t) can only differ from the rounding of
-// the IEEE quotient where the remainder (x - b) - n s comes within 2^-18 s of
-// half a step (t <= 15: 15 * 2^-22 < 2^-18), or past it; such words are redone
-// with divisions.  x >= b always: b is one of the row's own values.
-__device__ __forceinline__ bool code_word(const float (&x)[8], float s, float b, float inv, uint32_t* word) {
-  const float magic = 8388608.0f;  // 2^23: adding it rounds to whole numbers, kept in the low bits
-  const float limit = s * (0.5f - 3.8147e-6f);
-  float far = 0.f;
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = x[i] - b;
-    const float r = fminf(d * inv, 15.0f) + magic;
-    far = fmaxf(far, fabsf(fmaf(magic - r, s, d)));
-    w |= (__float_as_uint(r) & 15u) << (4 * i);
-  }
-  *word = w;
-  return far < limit;
+// Two FP32 operations in one instruction, each rounded as by itself.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n"
+      " mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
-__device__ __noinline__ uint32_t code_word_by_division(const float (&x)[8], float s, float b) {
+// The word of eight codes rint((x - b) / s), and whether all of them are
+// certain.  inv is 1 / s to one unit in the last place and the product is
+// rounded once, to a whole number n, by adding 2^23; so n - 1/2 <= t <= n + 1/2
+// for a t within 15 * 2^-23 < 2^-19 of the true quotient.  n is the rounding of
+// the IEEE quotient unless the remainder (x - b) - n s comes within 2^-18 s of
+// half a step; such words, and rows whose top passes the last level (scales
+// near 2^-24), are redone with divisions.  x >= b always: b is one of the row's
+// own values.  The whole numbers' bits are 0x4B000000 + n: shifted together
+// they leave a known constant on top of the codes.
+__device__ __forceinline__ bool code_word(const float2 (&x)[4], float s, float b, float inv, uint32_t* word) {
+  const float2 magic = make_float2(8388608.0f, 8388608.0f);
+  const float2 neg_b = make_float2(-b, -b), inv2 = make_float2(inv, inv), s2 = make_float2(s, s);
+  float far = 0.f;
+  uint32_t w = 0, constant = 0;
+#pragma unroll
+  for (int i = 3; i >= 0; --i) {
+    const float2 d = add2(x[i], neg_b);
+    const float2 r = fma2(d, inv2, magic);
+    const float2 e = fma2(fma2(r, make_float2(-1.0f, -1.0f), magic), s2, d);
+    far = fmaxf(far, fmaxf(fabsf(e.x), fabsf(e.y)));
+    w = (((w << 4) + __float_as_uint(r.y)) << 4) + __float_as_uint(r.x);
+    constant = (((constant << 4) + 0x4B000000u) << 4) + 0x4B000000u;
+  }
+  *word = w - constant;
+  return far < s * (0.5f - 3.8147e-6f);
+}
+
+__device__ __noinline__ uint32_t code_word_by_division(float4 lo, float4 hi, float s, float b) {
+  const float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) w |= (uint32_t)fminf(fmaxf(rintf((x[i] - b) / s), 0.0f), 15.0f) << (4 * i);
   return w;
 }
 
-// D / 8 lanes per row of D channels, 8 channels (16 bytes in, 4 out) to a
-// lane; a token's heads follow one another, keys and values are the grid's y.
-template <int D>
-__global__ void __launch_bounds__(kRowThreads)
+// x / 15 as IEEE division gives it: a correctly rounded reciprocal, the
+// product's remainder by FMA and one correction (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990).
+__device__ __forceinline__ float fifteenth(float x) {
+  const float inv = 1.0f / 15.0f;
+  const float q = x * inv;
+  return fmaf(fmaf(-15.0f, q, x), inv, q);
+}
+
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// D / 16 lanes per row of D channels, 16 channels (32 bytes in, 8 out) to a
+// lane, GL lanes to a group; a token's heads follow one another, keys and
+// values are the grid's y.
+template <int D, int GL>
+__global__ void __launch_bounds__(kRowThreads, 4)
     append_kernel(const KvCache c, const __half* __restrict__ k, long long ldk, const __half* __restrict__ v,
                   long long ldv, const long long* __restrict__ slots, uint32_t rows, FastDiv heads) {
-  constexpr int L = D / 8, U = kRowsAtOnce, RPB = kRowThreads / L;
+  constexpr int L = D / 16, RPB = kRowThreads / L;
   pdl_launch_dependents();
   pdl_wait();
   const int part = blockIdx.y;
   const __half* const base = part ? v : k;
   const long long ld = part ? ldv : ldk;
   const int sub = threadIdx.x % L;
-  const int gl = c.group / 8;  // lanes of a group (8 or 16)
   // every lane of a warp takes the same number of turns (the shuffles need all)
-  for (uint32_t r0 = blockIdx.x * (RPB * U); r0 < rows; r0 += gridDim.x * (RPB * U)) {
-    uint4 raw[U];
-    long long slot[U];
-    int head[U];
+  for (uint32_t r0 = blockIdx.x * RPB; r0 < rows; r0 += gridDim.x * RPB) {
+    const uint32_t row = min(r0 + threadIdx.x / L, rows - 1);  // lanes past the end do the last row again
+    const uint32_t t = divide(row, heads);
+    const int head = (int)(row - t * heads.d);
+    const uint4* src = reinterpret_cast<const uint4*>(base + t * ld + head * D + sub * 16);
+    const uint4 raw[2] = {__ldg(src), __ldg(src + 1)};
+    const long long slot = __ldg(slots + t);
+    float2 x[8];
+    __half2 lo2, hi2;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t row = r0 + u * RPB + threadIdx.x / L;
-      const bool on = row < rows;
-      const uint32_t t = divide(on ? row : 0, heads);
-      head[u] = on ? (int)(row - t * heads.d) : 0;
-      raw[u] = on ? __ldg(reinterpret_cast<const uint4*>(base + t * ld + head[u] * D + sub * 8))
-                  : make_uint4(0, 0, 0, 0);
-      slot[u] = on ? __ldg(slots + t) : -1;
+    for (int i = 0; i < 8; ++i) {
+      const uint4& q = raw[i >> 2];
+      const uint32_t w = (i & 2) ? ((i & 1) ? q.w : q.z) : ((i & 1) ? q.y : q.x);
+      const __half2 h = *reinterpret_cast<const __half2*>(&w);
+      x[i] = __half22float2(h);
+      lo2 = i ? __hmin2(lo2, h) : h;
+      hi2 = i ? __hmax2(hi2, h) : h;
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float x[8];
-      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-      __half2 lo2, hi2;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 h = *reinterpret_cast<const __half2*>(&w[i]);
-        const float2 f = __half22float2(h);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-        lo2 = i ? __hmin2(lo2, h) : h;
-        hi2 = i ? __hmax2(hi2, h) : h;
-      }
-      for (int o = 1; o < gl; o <<= 1) {
-        lo2 = __hmin2(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
-        hi2 = __hmax2(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
-      }
-      const __half bh = __hmin(__low2half(lo2), __high2half(lo2)), th = __hmax(__low2half(hi2), __high2half(hi2));
-      const __half tiny = __ushort_as_half((unsigned short)1);
-      const float b = __half2float(bh);
-      const __half sh = __hmax(__float2half_rn((__half2float(th) - b) / 15.0f), tiny);
-      const float s = __half2float(sh);
-      uint32_t word;
-      if (!code_word(x, s, b, 1.0f / s, &word)) word = code_word_by_division(x, s, b);
-      if (in_cache(c, slot[u])) {
-        const CodeRow out = code_row<D>(c, slot[u], head[u], part);
-        reinterpret_cast<uint32_t*>(out.codes)[sub] = word;
-        if (sub % gl == 0)
-          out.par[sub / gl] = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(bh) << 16);
-      }
+    for (int o = 1; o < GL; o <<= 1) {
+      lo2 = __hmin2(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
+      hi2 = __hmax2(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+    }
+    const __half bh = __hmin(__low2half(lo2), __high2half(lo2)), th = __hmax(__low2half(hi2), __high2half(hi2));
+    const __half tiny = __ushort_as_half((unsigned short)1);
+    const float b = __half2float(bh), top = __half2float(th);
+    const __half sh = __hmax(__float2half_rn(fifteenth(top - b)), tiny);
+    const float s = __half2float(sh), inv = reciprocal(s);
+    uint32_t word[2];
+    const float2 x0[4] = {x[0], x[1], x[2], x[3]}, x1[4] = {x[4], x[5], x[6], x[7]};
+    const bool sure0 = code_word(x0, s, b, inv, &word[0]), sure1 = code_word(x1, s, b, inv, &word[1]);
+    if (!(sure0 && sure1 && (top - b) * inv < 15.25f)) {
+      word[0] = code_word_by_division(make_float4(x[0].x, x[0].y, x[1].x, x[1].y),
+                                      make_float4(x[2].x, x[2].y, x[3].x, x[3].y), s, b);
+      word[1] = code_word_by_division(make_float4(x[4].x, x[4].y, x[5].x, x[5].y),
+                                      make_float4(x[6].x, x[6].y, x[7].x, x[7].y), s, b);
+    }
+    if (in_cache(c, slot)) {
+      const CodeRow out = code_row<D>(c, slot, head, part);
+      reinterpret_cast<uint2*>(out.codes)[sub] = make_uint2(word[0], word[1]);
+      if (sub % GL == 0)
+        out.par[sub / GL] = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(bh) << 16);
     }
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kRowThreads)
+template <int D, int GL>
+__global__ void __launch_bounds__(kRowThreads, 4)
     read_kernel(const KvCache c, const long long* __restrict__ slots, uint32_t rows, FastDiv heads,
                 __half* __restrict__ k, __half* __restrict__ v) {
-  constexpr int L = D / 8, U = kRowsAtOnce, RPB = kRowThreads / L;
+  constexpr int L = D / 16, U = 2, RPB = kRowThreads / L;  // U rows of a thread under way at a time
   pdl_launch_dependents();
   pdl_wait();
   const int part = blockIdx.y;
   __half* const base = part ? v : k;
   const int sub = threadIdx.x % L;
-  const int gl = c.group / 8;
   for (uint32_t r0 = blockIdx.x * (RPB * U); r0 < rows; r0 += gridDim.x * (RPB * U)) {
-    uint32_t word[U], par[U];
-    bool there[U];
+    uint2 word[U];
+    uint32_t par[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t row = r0 + u * RPB + threadIdx.x / L;
-      word[u] = par[u] = 0;
-      there[u] = false;
-      if (row < rows) {
-        const uint32_t t = divide(row, heads);
-        const long long slot = __ldg(slots + t);
-        there[u] = in_cache(c, slot);
-        if (there[u]) {
-          const CodeRow in = code_row<D>(c, slot, (int)(row - t * heads.d), part);
-          word[u] = reinterpret_cast<const uint32_t*>(in.codes)[sub];
-          par[u] = in.par[sub / gl];
-        }
+      const uint32_t row = min(r0 + u * RPB + threadIdx.x / L, rows - 1);
+      const uint32_t t = divide(row, heads);
+      const long long slot = __ldg(slots + t);
+      word[u] = make_uint2(0, 0);
+      par[u] = 0;  // scale and minimum 0: zeros
+      if (in_cache(c, slot)) {
+        const CodeRow in = code_row<D>(c, slot, (int)(row - t * heads.d), part);
+        word[u] = reinterpret_cast<const uint2*>(in.codes)[sub];
+        par[u] = in.par[sub / GL];
       }
     }
 #pragma unroll
@@ -184,14 +215,23 @@ __global__ void __launch_bounds__(kRowThreads)
       const uint32_t row = r0 + u * RPB + threadIdx.x / L;
       if (row >= rows) continue;
       const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&par[u]));
-      uint32_t h[4];
+      const float2 s2 = make_float2(sb.x, sb.x);
+      // 2^23 + code, from the bits; the constant goes out again exactly: the
+      // code itself, then one FMA
+      uint32_t h[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 p = __floats2half2_rn(fmaf((float)((word[u] >> (8 * i)) & 15u), sb.x, sb.y),
-                                            fmaf((float)((word[u] >> (8 * i + 4)) & 15u), sb.x, sb.y));
-        h[i] = there[u] ? *reinterpret_cast<const uint32_t*>(&p) : 0u;
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w = (i < 4 ? word[u].x : word[u].y) >> (8 * (i & 3));
+        const float2 q = add2(make_float2(__uint_as_float(0x4B000000u | (w & 15u)),
+                                          __uint_as_float(0x4B000000u | ((w >> 4) & 15u))),
+                              make_float2(-8388608.0f, -8388608.0f));
+        const float2 f = fma2(q, s2, make_float2(sb.y, sb.y));
+        const __half2 p = __floats2half2_rn(f.x, f.y);
+        h[i] = *reinterpret_cast<const uint32_t*>(&p);
       }
-      *reinterpret_cast<uint4*>(base + (long long)row * D + sub * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+      uint4* dst = reinterpret_cast<uint4*>(base + (long long)row * D + sub * 16);
+      dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+      dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
     }
   }
 }
@@ -200,7 +240,7 @@ template <class K, class... Args>
 tlq_status launch_rows(K kernel, long long rows, int lanes, const char* what, cudaStream_t stream, Args... args) {
   if (rows > 0x7fffffffll) return set_error(TLQ_EUNSUPPORTED, "%s: %lld rows (tokens x heads, at most 2^31 - 1)", what, rows);
   const long long per = kRowThreads / lanes;  // a block's first turn, one row a thread group, while blocks are few
-  const long long blocks = std::min<long long>((rows + per - 1) / per, (long long)device_info().sms * 4);
+  const long long blocks = std::min<long long>((rows + per - 1) / per, (long long)device_info().sms * 2);  // with keys and values a full wave
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)std::max<long long>(blocks, 1), 2, 1);
   lc.blockDim = dim3(kRowThreads, 1, 1);
@@ -220,9 +260,9 @@ tlq_status launch_kv4_append(const KvCache& c, int head_dim, const __half* k, lo
   const long long rows = (long long)tokens * c.heads;
   const FastDiv heads = fast_div((uint32_t)c.heads);
   if (head_dim == 128)
-    return launch_rows(append_kernel<128>, rows, 16, "kv4 append: launch", stream, c, k, ldk, v, ldv, slots,
+    return launch_rows(c.group == 64 ? append_kernel<128, 4> : append_kernel<128, 8>, rows, 8, "kv4 append: launch", stream, c, k, ldk, v, ldv, slots,
                        (uint32_t)rows, heads);
-  return launch_rows(append_kernel<64>, rows, 8, "kv4 append: launch", stream, c, k, ldk, v, ldv, slots,
+  return launch_rows(append_kernel<64, 4>, rows, 4, "kv4 append: launch", stream, c, k, ldk, v, ldv, slots,
                      (uint32_t)rows, heads);
 }
 
@@ -231,8 +271,8 @@ tlq_status launch_kv4_read(const KvCache& c, int head_dim, const long long* slot
   const long long rows = (long long)tokens * c.heads;
   const FastDiv heads = fast_div((uint32_t)c.heads);
   if (head_dim == 128)
-    return launch_rows(read_kernel<128>, rows, 16, "kv4 read: launch", stream, c, slots, (uint32_t)rows, heads, k, v);
-  return launch_rows(read_kernel<64>, rows, 8, "kv4 read: launch", stream, c, slots, (uint32_t)rows, heads, k, v);
+    return launch_rows(c.group == 64 ? read_kernel<128, 4> : read_kernel<128, 8>, rows, 8, "kv4 read: launch", stream, c, slots, (uint32_t)rows, heads, k, v);
+  return launch_rows(read_kernel<64, 4>, rows, 4, "kv4 read: launch", stream, c, slots, (uint32_t)rows, heads, k, v);
 }
 
 }  // namespace tlq

@@ -24,7 +24,6 @@ namespace {
 constexpr int kRanks = 8;  // blocks of a cluster
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxRank = 64;
 
 __device__ __forceinline__ float peer_f32(const float* p, uint32_t rank) {
   uint32_t a = smem_u32(p), r;
@@ -36,8 +35,10 @@ __device__ __forceinline__ float peer_f32(const float* p, uint32_t rank) {
 
 // MT: 16-token tiles of a cluster (1 or 4).  A warp takes one tile and one of
 // WK shares of the block's k.
-template <int MT>
+// KR: the most ranks a form takes, in 16s (1, 2 or 4: registers).
+template <int MT, int KR>
 struct LCfg {
+  static constexpr int kMaxRank = 16 * KR;
   static constexpr int TT = 16 * MT;
   static constexpr int WK = kWarps / MT;
   static constexpr int PART = WK * TT * (kMaxRank + 1) * 4;
@@ -47,9 +48,10 @@ struct LCfg {
   static_assert(PART % 16 == 0 && SUMS % 16 == 0, "alignment");
 };
 
-template <int MT>
+template <int MT, int KR>
 __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads, 2) lora_kernel(const LoraArgs a) {
-  using C = LCfg<MT>;
+  using C = LCfg<MT, KR>;
+  constexpr int kMaxRank = C::kMaxRank;
   constexpr int TT = C::TT, WK = C::WK;
   extern __shared__ __align__(16) uint8_t smem[];
   float(*part)[TT][kMaxRank + 1] = reinterpret_cast<float(*)[TT][kMaxRank + 1]>(smem);  // [WK] A x by share of k
@@ -177,9 +179,10 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads, 2) lo
     // ---- the cluster's sums, in rank order; a warp to a token ----
     const float scale = a.scales[w];
     for (int row = warp; row < TT; row += kWarps) {
-      float v[2] = {0.f, 0.f}, big = 0.f;
+      constexpr int VC = (kMaxRank + 31) / 32;  // ranks of a lane
+      float v[VC] = {}, big = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < VC; ++i) {
         const int col = lane + 32 * i;
         if (col < NR && row < rows) {
           float got[kRanks];
@@ -196,7 +199,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads, 2) lo
       if (big > 0.f && big < INFINITY) e = max(-126, min(126, (int)(__float_as_uint(big) >> 23) - 127 - 14));
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < VC; ++i) {
         const int col = lane + 32 * i;
         if (col < 16 * KS) {
           const float x = v[i] * down;
@@ -269,24 +272,31 @@ long long tile_bound(const LoraArgs& a, int mt) {
                              (long long)a.requests * ((a.max_q + 16 * mt - 1) / (16 * mt)));
 }
 
-template <int MT>
-tlq_status launch_tiles(const LoraArgs& a, cudaStream_t stream) {
+template <int MT, int KR>
+tlq_status launch_form(const LoraArgs& a, cudaStream_t stream) {
   const long long tiles = tile_bound(a, MT);
   if (tiles * kRanks > 0x7fffffffll) return set_error(TLQ_EUNSUPPORTED, "lora: %lld token tiles", tiles);
   static const cudaError_t attr =
-      cudaFuncSetAttribute(lora_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, LCfg<MT>::SMEM);
+      cudaFuncSetAttribute(lora_kernel<MT, KR>, cudaFuncAttributeMaxDynamicSharedMemorySize, LCfg<MT, KR>::SMEM);
   if (attr != cudaSuccess) return cuda_error(attr, "lora: shared memory");
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(tiles * kRanks), 1, 1);
   lc.blockDim = dim3(kThreads, 1, 1);
-  lc.dynamicSmemBytes = LCfg<MT>::SMEM;
+  lc.dynamicSmemBytes = LCfg<MT, KR>::SMEM;
   lc.stream = stream;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = &at;
   lc.numAttrs = pdl_enabled() ? 1 : 0;
-  return cuda_error(cudaLaunchKernelEx(&lc, lora_kernel<MT>, a), "lora: launch");
+  return cuda_error(cudaLaunchKernelEx(&lc, lora_kernel<MT, KR>, a), "lora: launch");
+}
+
+template <int MT>
+tlq_status launch_tiles(const LoraArgs& a, cudaStream_t stream) {
+  if (a.rank <= 16) return launch_form<MT, 1>(a, stream);
+  if (a.rank <= 32) return launch_form<MT, 2>(a, stream);
+  return launch_form<MT, 4>(a, stream);
 }
 
 }  // namespace

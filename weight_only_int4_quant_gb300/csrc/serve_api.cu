@@ -41,6 +41,9 @@ tlq_status check_cache(const tl_kv4_cache* c, KvCache* out, const char* who) {
   if (c->heads < 1 || c->heads > 4096) return set_error(TLQ_EINVAL, "%s: heads=%d (1..4096)", who, c->heads);
   if (c->num_pages < 1 || c->num_pages > 0x7fffffffll)
     return set_error(TLQ_EINVAL, "%s: num_pages=%lld (1..2^31-1)", who, (long long)c->num_pages);
+  if (c->num_pages * c->heads > 0x7fffffffll)
+    return set_error(TLQ_EINVAL, "%s: num_pages=%lld x heads=%d (at most 2^31 - 1 blocks)", who, (long long)c->num_pages,
+                     c->heads);
   out->blocks = static_cast<uint8_t*>(c->blocks);
   out->num_pages = c->num_pages;
   out->heads = c->heads;
