@@ -116,6 +116,7 @@ struct DecodeParams {
   long long ldo;
   float scale_log2;  // softmax scale * log2(e)
   int window, share;  // share: query heads per key head
+  int few_rows;       // requests of more rows are not this kernel's
   float* partials;
   Header* headers;
 };
@@ -128,6 +129,7 @@ struct ItemShape {
 template <int R>
 __device__ __forceinline__ ItemShape item_shape(const DecodeParams& p, const KvRequest& r) {
   ItemShape s;
+  if (r.q_len * p.share > p.few_rows) return ItemShape{0, 1};
   s.items = p.cache.heads * ((r.q_len * p.share + R - 1) / R);
   int span = r.len;
   if (p.window > 0) {
@@ -762,7 +764,7 @@ size_t kv4_decode_workspace(int head_dim) {
   return std::max(bytes(3 * sms, 8), bytes(2 * sms, 16));
 }
 
-tlq_status launch_kv4_decode(const KvAttention& a, cudaStream_t stream) {
+tlq_status launch_kv4_decode(const KvAttention& a, int few_rows, cudaStream_t stream) {
   DecodeParams p{};
   p.cache = a.cache;
   p.batch = a.batch;
@@ -773,8 +775,9 @@ tlq_status launch_kv4_decode(const KvAttention& a, cudaStream_t stream) {
   p.scale_log2 = (float)((double)a.scale * M_LOG2E);
   p.window = a.window;
   p.share = a.q_heads / a.cache.heads;
+  p.few_rows = few_rows;
   p.partials = static_cast<float*>(a.ws);
-  const int rows = (int)std::min<long long>((long long)a.batch.max_q * p.share, 1 << 20);
+  const int rows = (int)std::min<long long>((long long)a.batch.max_q * p.share, few_rows);
   if (a.head_dim == 64) return launch_rows<64, 1>(p, rows, stream);
   return a.cache.group == 64 ? launch_rows<128, 2>(p, rows, stream) : launch_rows<128, 1>(p, rows, stream);
 }

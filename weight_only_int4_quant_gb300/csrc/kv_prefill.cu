@@ -1,0 +1,875 @@
+// Attention of many query rows over the paged 4-bit cache (prompts, chunks) on
+// the 5th-generation tensor cores (tcgen05 + TMEM).
+//
+//   S = K Q, O = P V on the codes:  with k = s c + b, v = s' c' + b',
+//   logit_ij = scale (s_j (q_i . c_j) + b_j sum(q_i)),  p' = p s'_j,
+//   o_i = (sum_j p'_ij c'_j + sum_j p_ij b'_j) / sum_j p_ij
+// The codes go to the matrix instructions exactly, as the FP16 subnormals
+// c * 2^-24 (a mask and at most one shift per pair); scales and minima are
+// applied in FP32 in the softmax.  The only roundings to FP16 are those of the
+// weights p' and of the result, as in the kernel for few rows.
+//
+// A block takes two tiles of 128 (query, head) rows of one key head against
+// stages of 128 tokens:
+//   warps 0-3, 4-7  softmax of the first, second tile: S from TMEM, weights
+//                   back to TMEM over it (FP16, the A operand of P V)
+//   warps 8-11      a thread to a token: its codes from global memory to
+//                   registers a stage ahead, then into the K and V tiles; its
+//                   scales and minima into the softmax's tables
+//   warp 12         one thread issues the MMAs:  P V of one tile and S of its
+//                   next stage run while the other tile's softmax works
+// Both operands lie in shared memory as the cache has them, a token to a
+// 128-byte swizzled row: K-major for S, N-major (transposed by descriptor)
+// for P V, so no tile is transposed.  The order of channels inside a code
+// word's eight, (0 4 1 5 2 6 3 7), is that of the masks; Q is stored in the
+// same order and O's columns are put back at the end.
+//
+// TMEM is read in the 16x256b form: a thread holds pairs of columns of four
+// rows, so the five constants of a token are read from shared memory once for
+// four rows.  (With a row to a thread those reads alone, 20 bytes for every
+// element, took longer than the MMAs: shared memory gives 128 bytes a clock.)
+//
+// Work is cut as in the kernel for few rows: all (request, row tile, key head,
+// stage) units lie on one line, each of the persistent blocks takes an equal
+// span, and partial items are joined by a second kernel in a fixed order.
+#include <algorithm>
+#include <cmath>
+
+#include "serve.cuh"
+#include "tc_common.cuh"
+
+namespace tlq {
+namespace {
+
+constexpr int kStage = 128;       // tokens of a stage
+constexpr int kRows = 128;        // rows of a tile
+constexpr int kItemRows = 256;    // rows of an item: two tiles
+constexpr int kThreads = 13 * 32;
+constexpr float kHeadroom = 6.0f;   // a new reference puts the largest weight at 2^6
+constexpr float kTrigger = 14.0f;   // weights stay at or below 2^14
+constexpr float kNone = -1e30f;
+
+template <int D>
+struct PCfg {
+  static constexpr int KD = 2, VD = 2, TD = 2;  // stages of keys, values and tables
+  static constexpr int BLOCK = kStage * 128;    // 128 rows of 64 channels
+  static constexpr int TILE = BLOCK * (D / 64);
+  // tables: per pair of tokens (A0 A1 B0 B1), (lg0 lg1 rc0 rc1), (rb0 rb1)
+  static constexpr int TABLE = kStage * 20;
+  static constexpr int BARS = 8 * 32;
+  static constexpr int SMEM = 1024 + 2 * TILE + KD * TILE + VD * TILE + TD * TABLE + BARS;
+  static_assert(SMEM <= 232448 - 6144, "shared memory");
+};
+
+struct PrefillAttnParams {
+  KvCache cache;
+  KvBatch batch;
+  const __half* q;
+  long long ldq;
+  __half* out;
+  long long ldo;
+  float scale_log2;
+  int window, share, few_rows;
+  float* partials;
+  struct PHeader* headers;
+};
+
+struct PHeader {
+  int followers, q0, row0, rows, head;
+};
+
+template <int D>
+struct PPartial {
+  static constexpr int FLOATS = kItemRows * (D + 2);  // O [rows][D], m [rows], l [rows]
+};
+
+// Bounds of one row tile of a request.
+struct TileShape {
+  int lo, hi;  // keys that any row sees
+  int s0, n;   // first stage, stages (at least one)
+};
+__device__ __forceinline__ TileShape tile_shape(const PrefillAttnParams& p, const KvRequest& r, int rows, int qt) {
+  TileShape t;
+  const int first_q = qt * kItemRows / p.share, last_q = (min(rows, (qt + 1) * kItemRows) - 1) / p.share;
+  const int base = r.len - r.q_len;
+  t.hi = max(0, base + last_q + 1);
+  t.lo = p.window > 0 ? max(0, base + first_q - p.window + 1) : 0;
+  t.s0 = t.lo / kStage;
+  t.n = max(1, (t.hi + kStage - 1) / kStage - t.s0);
+  return t;
+}
+// rows of a request that this kernel takes (0: the kernel for few rows does)
+__device__ __forceinline__ int many_rows(const PrefillAttnParams& p, const KvRequest& r) {
+  const int rows = r.q_len * p.share;
+  return rows > p.few_rows ? rows : 0;
+}
+
+struct PSegment {
+  KvRequest rq;
+  int req, head, row0, rows;
+  int lo, hi;
+  int s0, s1;
+  bool first, last;
+  long long item_end;
+};
+
+struct PWalk {
+  long long u, u_end, item_u;  // item_u: first unit of the item at hand
+  int req, qt, head;
+  int rows, tiles;             // of the request at hand
+  KvRequest rq;
+
+  __device__ __forceinline__ void enter(const PrefillAttnParams& p) {
+    rq = kv_request(p.batch, p.cache.page, req);
+    rows = many_rows(p, rq);
+    tiles = (rows + kItemRows - 1) / kItemRows;
+    qt = head = 0;
+  }
+  __device__ __forceinline__ void start(const PrefillAttnParams& p, int request, long long first) {
+    req = request;
+    item_u = first;
+    enter(p);
+    for (; qt + 1 < tiles; ++qt) {
+      const long long n = (long long)tile_shape(p, rq, rows, qt).n * p.cache.heads;
+      if (u < item_u + n) break;
+      item_u += n;
+    }
+  }
+  __device__ __forceinline__ bool next(const PrefillAttnParams& p, PSegment* s) {
+    while (u < u_end) {
+      if (qt >= tiles) {
+        if (++req >= p.batch.requests) return false;
+        enter(p);
+        continue;
+      }
+      const TileShape t = tile_shape(p, rq, rows, qt);
+      if (u >= item_u + t.n) {
+        const long long skip = min((long long)(p.cache.heads - head), (u - item_u) / t.n);
+        item_u += skip * t.n;
+        head += (int)skip;
+        if (head >= p.cache.heads) {
+          head = 0;
+          ++qt;
+        }
+        continue;
+      }
+      const int c0 = (int)(u - item_u), c1 = (int)min((long long)t.n, c0 + (u_end - u));
+      s->rq = rq;
+      s->req = req;
+      s->head = head;
+      s->row0 = qt * kItemRows;
+      s->rows = min(kItemRows, rows - s->row0);
+      s->lo = t.lo;
+      s->hi = t.hi;
+      s->s0 = t.s0 + c0;
+      s->s1 = t.s0 + c1;
+      s->first = c0 == 0;
+      s->last = c1 == t.n;
+      s->item_end = item_u + t.n;
+      u += c1 - c0;
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---- TMEM in the 16-lane forms.  x4 of 16x256b: 32 columns of 16 rows; thread
+// (r, q) = (lane / 4, lane % 4) holds in v[4 k + 0, 1] columns 8 k + 2 q, + 1 of
+// row r and in v[4 k + 2, 3] those of row r + 8. ----
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t addr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st_16x256(uint32_t addr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"f"(
+          v[0]),
+      "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+      "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "r"(addr)
+      : "memory");
+}
+// x4 of 16x128b: 16 columns of 16 rows; v[2 k] is column 4 k + q of row r, v[2 k + 1] of row r + 8.
+__device__ __forceinline__ void tmem_st_16x128(uint32_t addr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16x128(uint32_t addr, uint32_t* v) {
+  asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// N-major operand, SWIZZLE_128B: rows of 64 channels (128 bytes), 8 tokens to
+// an atom of 1024 bytes (stride offset), 64-channel blocks BLOCK bytes apart
+// (leading offset).
+__device__ __forceinline__ uint64_t sw128_desc_n(uint32_t saddr, uint32_t block_bytes) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(block_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// kind::f16, D = F32, A = B = F16, M = 128; bit 16: B is N-major.
+constexpr uint32_t kIdescS =
+    (1u << 4) | ((uint32_t)(kStage >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+template <int D>
+constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accum)
+      : "memory");
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n"
+      " mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Barriers of a block.
+struct PBars {
+  uint64_t q_full[2];             // Q tile written (4 warps)
+  uint64_t s_full[2];             // S of a stage complete
+  uint64_t p_full[2];             // weights written (4 warps)
+  uint64_t o_done[2];             // P V of a stage complete
+  uint64_t k_full[2], k_empty[2];
+  uint64_t v_full[2], v_empty[2];
+  uint64_t t_empty[2];            // table read (8 warps)
+  uint32_t tmem;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const PrefillAttnParams p) {
+  using C = PCfg<D>;
+  constexpr int KD = C::KD, VD = C::VD, TD = C::TD;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const sq = smem;                       // [2][TILE]
+  uint8_t* const sk = sq + 2 * C::TILE;           // [KD][TILE]
+  uint8_t* const sv = sk + KD * C::TILE;          // [VD][TILE]
+  uint8_t* const st = sv + VD * C::TILE;          // [TD][TABLE]
+  PBars* const bar = reinterpret_cast<PBars*>(st + TD * C::TABLE);
+  static_assert(sizeof(PBars) <= C::BARS, "barriers fit");
+  __shared__ UnitSearch<kThreads> search;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->q_full[i], 4);
+      mbar_init(&bar->s_full[i], 1);
+      mbar_init(&bar->p_full[i], 4);
+      mbar_init(&bar->o_done[i], 1);
+      mbar_init(&bar->k_full[i], 4);
+      mbar_init(&bar->k_empty[i], 1);
+      mbar_init(&bar->v_full[i], 4);
+      mbar_init(&bar->v_empty[i], 1);
+      mbar_init(&bar->t_empty[i], 8);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(&bar->tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem;
+  pdl_wait();
+  PHeader* const header = &p.headers[blockIdx.x];
+  if (tid == 0) header->followers = 0;
+
+  auto count = [&](int i) -> long long {
+    const KvRequest r = kv_request(p.batch, p.cache.page, i);
+    const int rows = many_rows(p, r);
+    long long n = 0;
+    for (int qt = 0; qt * kItemRows < rows; ++qt) n += tile_shape(p, r, rows, qt).n;
+    return n * p.cache.heads;
+  };
+  long long own, mine;
+  search.count_all(p.batch.requests, count, &own, &mine);
+  const long long U = search.total;
+  const long long n = min((long long)gridDim.x, U);
+  const bool busy = (long long)blockIdx.x < n;
+  PWalk walk;
+  walk.u = walk.u_end = 0;
+  if (busy) {
+    walk.u = U * blockIdx.x / n;
+    walk.u_end = U * (blockIdx.x + 1) / n;
+    search.find(p.batch.requests, count, walk.u, own, mine);
+    if (search.request >= 0)
+      walk.start(p, search.request, search.first);
+    else
+      walk.u_end = walk.u;  // not reached: u < U
+  }
+  PSegment sg;
+  uint32_t it = 0;  // stages so far
+
+  if (warp >= 8 && warp < 12) {
+    // ---------------- a thread to a token: codes into the tiles ----------------
+    const int tk = tid - 8 * 32;
+    constexpr int W = D / 32;  // 16-byte pieces of a row of codes
+    uint4 kw[W], vw[W];
+    uint32_t kpar = 0, vpar = 0;
+    bool live = false, live_next = false;
+    auto page_of = [&](const PSegment& s, int stage) {
+      const int key = stage * kStage + tk;
+      return stage < s.s1 && key >= s.lo && key < s.hi
+                 ? __ldg(p.batch.table + (size_t)s.req * p.batch.ld_table + (key >> p.cache.page_shift))
+                 : -1;
+    };
+    const uint8_t* vsrc = nullptr;
+    uint32_t vpar_next = 0;
+    // keys of stage `stage` into kw, and where its values lie
+    auto load_k = [&](const PSegment& s, int stage, int page) {
+      live_next = page >= 0 && page < p.cache.num_pages;
+      if (live_next) {
+        const int P = p.cache.page, off = (stage * kStage + tk) & (P - 1);
+        const uint8_t* blk = p.cache.blocks + ((uint32_t)page * (uint32_t)p.cache.heads + s.head) *
+                                                  (uint64_t)p.cache.block_bytes;
+        const uint4* src = reinterpret_cast<const uint4*>(blk + off * (D / 2));
+#pragma unroll
+        for (int i = 0; i < W; ++i) kw[i] = __ldg(src + i);
+        vsrc = blk + (P + off) * (D / 2);
+        kpar = __ldg(reinterpret_cast<const uint32_t*>(blk + P * D) + off);
+        vpar_next = __ldg(reinterpret_cast<const uint32_t*>(blk + P * D) + P + off);
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) kw[i] = make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto load_v = [&] {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        vw[i] = live_next ? __ldg(reinterpret_cast<const uint4*>(vsrc) + i) : make_uint4(0, 0, 0, 0);
+      vpar = vpar_next;
+      live = live_next;
+    };
+    bool ok = true, more = walk.next(p, &sg);
+    int stage = more ? sg.s0 : 0;
+    int page = -1, page2 = -1;
+    PSegment nx = sg;      // where the stage after this one lies
+    int nstage = stage;
+    auto advance = [&](PSegment& s, int& at) -> bool {  // the next stage of the block's work
+      if (at + 1 < s.s1) {
+        ++at;
+        return true;
+      }
+      if (!walk.next(p, &s)) return false;
+      at = s.s0;
+      return true;
+    };
+    bool have2 = false;
+    if (more) {
+      page = page_of(sg, stage);
+      load_k(sg, stage, page);
+      load_v();
+      have2 = advance(nx, nstage);
+      if (have2) page2 = page_of(nx, nstage);
+    }
+    const uint32_t row = (uint32_t)tk * 128u, sw = (uint32_t)(tk & 7);
+    while (ok && more) {
+      const int ks = it % KD, vs = it % VD, ts = it % TD;
+      // the softmax's constants of this token
+      ok = mbar_wait(&bar->t_empty[ts], ((it / TD) & 1) ^ 1, 0x311) &&
+           mbar_wait(&bar->k_empty[ks], ((it / KD) & 1) ^ 1, 0x312);
+      if (!ok) break;
+      {
+        const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(&kpar));
+        const float2 vp = __half22float2(*reinterpret_cast<const __half2*>(&vpar));
+        const float vsc = fmaxf(vp.x, 5.9604644775390625e-8f), rc = __fdividef(1.0f, vsc);
+        float* tab = reinterpret_cast<float*>(st + ts * C::TABLE);
+        const int pair = tk >> 1, e = tk & 1;
+        float* t1 = tab + pair * 4;
+        float* t2 = tab + kStage * 2 + pair * 4;
+        float* t3 = tab + kStage * 4 + pair * 2;
+        // no token: its logit is -infinity whatever the row
+        t1[e] = live ? kp.x * (p.scale_log2 * 16777216.0f) : 0.f;
+        t1[2 + e] = live ? kp.y * p.scale_log2 : 0.f;
+        t2[e] = live ? lg2(vsc) : -INFINITY;
+        t2[2 + e] = live ? rc : 0.f;
+        t3[e] = live ? rc * vp.y : 0.f;
+      }
+      const uint32_t kb = smem_u32(sk + ks * C::TILE) + row;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const uint32_t w4[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w = w4[j], c = 4 * i + j;  // 8-channel piece c
+          sts128(kb + (c >> 3) * C::BLOCK + (((c & 7) ^ sw) << 4), w & 0x000F000Fu, (w >> 4) & 0x000F000Fu,
+                 (w >> 8) & 0x000F000Fu, (w >> 12) & 0x000F000Fu);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->k_full[ks]);
+      // keys of the next stage, and the page of the one after it
+      more = have2;
+      if (more) {
+        load_k(nx, nstage, page2);
+        have2 = advance(nx, nstage);
+        page2 = have2 ? page_of(nx, nstage) : -1;
+      }
+      ok = mbar_wait(&bar->v_empty[vs], ((it / VD) & 1) ^ 1, 0x313);
+      if (!ok) break;
+      const uint32_t vb = smem_u32(sv + vs * C::TILE) + row;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const uint32_t w4[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w = w4[j], x = w >> 8, c = 4 * i + j;
+          // odd channels enter 16 times too large; the output takes it back
+          sts128(vb + (c >> 3) * C::BLOCK + (((c & 7) ^ sw) << 4), w & 0x000F000Fu, w & 0x00F000F0u, x & 0x000F000Fu,
+                 x & 0x00F000F0u);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->v_full[vs]);
+      if (more) load_v();
+      ++it;
+    }
+  } else if (warp == 12) {
+    // ---------------- MMA issue ----------------
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t tiles_it[2] = {0, 0};  // stages of each tile so far: the phases of p_full
+      uint32_t q_seg[2] = {0, 0};     // segments of each tile so far: the phases of q_full
+      auto issue_s = [&](int i, uint32_t at) {
+        const uint32_t a0 = smem_u32(sq + i * C::TILE), b0 = smem_u32(sk + (at % KD) * C::TILE);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = (kk >> 2) * C::BLOCK + (kk & 3) * 32;
+          mma_ss(tmem + kStage * i, sw128_desc(a0 + o), sw128_desc(b0 + o), kIdescS, kk != 0);
+        }
+        umma_commit(&bar->s_full[i]);
+      };
+      auto issue_o = [&](int i, uint32_t at, bool begin) {
+        const uint32_t b0 = smem_u32(sv + (at % VD) * C::TILE);
+#pragma unroll
+        for (int kk = 0; kk < kStage / 16; ++kk)
+          mma_ts(tmem + 2 * kStage + D * i, tmem + kStage * i + kk * 8, sw128_desc_n(b0 + kk * 2048, C::BLOCK),
+                 kIdescO<D>, !(begin && kk == 0));
+        umma_commit(&bar->o_done[i]);
+      };
+      while (ok && walk.next(p, &sg)) {
+        const int tiles = sg.rows > kRows ? 2 : 1, T = sg.s1 - sg.s0;
+        ok = mbar_wait(&bar->k_full[it % KD], (it / KD) & 1, 0x321);
+        for (int i = 0; i < tiles && ok; ++i) {
+          ok = mbar_wait(&bar->q_full[i], q_seg[i] & 1, 0x322);
+          if (!ok) break;
+          ++q_seg[i];
+          tc_fence_after();
+          issue_s(i, it);
+        }
+        if (!ok) break;
+        umma_commit(&bar->k_empty[it % KD]);
+        for (int s = 0; s < T && ok; ++s, ++it) {
+          const bool next = s + 1 < T;
+          if (next) ok = mbar_wait(&bar->k_full[(it + 1) % KD], ((it + 1) / KD) & 1, 0x323);
+          ok = ok && mbar_wait(&bar->v_full[it % VD], (it / VD) & 1, 0x324);
+          for (int i = 0; i < tiles && ok; ++i) {
+            ok = mbar_wait(&bar->p_full[i], tiles_it[i] & 1, 0x325);
+            if (!ok) break;
+            ++tiles_it[i];
+            tc_fence_after();
+            issue_o(i, it, s == 0);
+            if (next) issue_s(i, it + 1);
+          }
+          if (!ok) break;
+          umma_commit(&bar->v_empty[it % VD]);
+          if (next) umma_commit(&bar->k_empty[(it + 1) % KD]);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---------------- softmax ----------------
+    const int tile = warp >> 2, quarter = warp & 3;
+    const int r = lane >> 2, qd = lane & 3;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+    const uint32_t ts_addr = lanes + kStage * tile;              // S, and the weights over it
+    const uint32_t to_addr = lanes + 2 * kStage + D * tile;      // O
+    uint32_t done = 0;  // stages of this tile so far: the phases of s_full and o_done
+    bool ok = true;
+    while (ok && walk.next(p, &sg)) {
+      const KvRequest rq = sg.rq;
+      const int rows = min(kRows, sg.rows - kRows * tile);  // of this tile; below 1: none
+      const int base_pos = rq.len - rq.q_len;
+      if (rows <= 0) {  // the tile is empty: only let the tables go on
+        for (int s = sg.s0; s < sg.s1 && ok; ++s, ++it) {
+          ok = mbar_wait(&bar->k_full[it % KD], (it / KD) & 1, 0x331);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->t_empty[it % TD]);
+        }
+        continue;
+      }
+      // Q: a thread to a row, in the codes' channel order
+      const int my = 32 * quarter + lane;
+      const int grow = sg.row0 + kRows * tile + my;
+      float qsum = 0.f;
+      {
+        const bool on = my < rows;
+        const int t = grow / p.share, g = grow - t * p.share;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(rq.q0 + (on ? t : 0)) * p.ldq +
+                                                          (long long)(sg.head * p.share + (on ? g : 0)) * D);
+        const uint32_t dst = smem_u32(sq + tile * C::TILE) + my * 128u;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = on ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+            qsum += f.x + f.y;
+          }
+          sts128(dst + (c >> 3) * C::BLOCK + (((c & 7) ^ (my & 7)) << 4), prmt(v.x, v.z, 0x5410), prmt(v.x, v.z, 0x7632),
+                 prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->q_full[tile]);
+      }
+      float qs[4], m[4], l[4], beta[4];
+      int pos[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // rows r + 8 k of this warp's 32
+        qs[k] = __shfl_sync(0xffffffffu, qsum, r + 8 * k);
+        pos[k] = base_pos + (sg.row0 + min(kRows * tile + 32 * quarter + r + 8 * k, sg.rows - 1)) / p.share;
+        m[k] = kNone;
+        l[k] = beta[k] = 0.f;
+      }
+      // keys below all_hi and from all_lo are seen by every row of the tile
+      const int all_hi = base_pos + (sg.row0 + kRows * tile) / p.share + 1;
+      const int all_lo =
+          p.window > 0 ? base_pos + (sg.row0 + kRows * tile + rows - 1) / p.share - p.window + 1 : 0;
+
+      for (int s = sg.s0; s < sg.s1; ++s, ++it, ++done) {
+        ok = mbar_wait(&bar->k_full[it % KD], (it / KD) & 1, 0x332) &&  // the table, written before the keys
+             mbar_wait(&bar->s_full[tile], done & 1, 0x333);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const float* tab = reinterpret_cast<const float*>(st + (it % TD) * C::TABLE);
+        const bool edge = s * kStage < all_lo || (s + 1) * kStage > all_hi;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float v[2][16];  // [rows r, r + 8 | rows r + 16, r + 24]
+          tmem_ld_16x256(ts_addr + 32 * c, v[0]);
+          tmem_ld_16x256(ts_addr + 32 * c + (16u << 16), v[1]);
+          tmem_wait_ld();
+          bool over = false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // column pair 32 c + 8 k + 2 qd
+            const int pair = 16 * c + 4 * k + qd;
+            const float4 ab = *reinterpret_cast<const float4*>(tab + pair * 4);
+            const float2 lg = *reinterpret_cast<const float2*>(tab + kStage * 2 + pair * 4);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              float* x = &v[y >> 1][4 * k + 2 * (y & 1)];
+              float2 z = fma2(make_float2(qs[y], qs[y]), make_float2(ab.z, ab.w), lg);
+              z = fma2(make_float2(x[0], x[1]), make_float2(ab.x, ab.y), z);
+              if (edge) {
+                const int key = s * kStage + 32 * c + 8 * k + 2 * qd;
+                const int from = p.window > 0 ? pos[y] - p.window : -1;
+                if (key > pos[y] || key <= from) z.x = -INFINITY;
+                if (key + 1 > pos[y] || key + 1 <= from) z.y = -INFINITY;
+              }
+              x[0] = z.x;
+              x[1] = z.y;
+              over |= fmaxf(z.x, z.y) > m[y] + kTrigger;
+            }
+          }
+          if (__any_sync(0xffffffffu, over)) {
+            // a new reference: sums, weights already written and O move with it
+            float w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              float x = kNone;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float* a = &v[y >> 1][4 * k + 2 * (y & 1)];
+                x = fmaxf(x, fmaxf(a[0], a[1]));
+              }
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+              const float next = fmaxf(m[y], x - kHeadroom);
+              w[y] = ex2(m[y] - next);
+              m[y] = next;
+              l[y] *= w[y];
+              beta[y] *= w[y];
+            }
+            for (int b = 0; b < c; ++b) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t pw[8];
+                tmem_ld_16x128(ts_addr + 16 * b + ((16u * h) << 16), pw);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float f = w[2 * h + (k & 1)];
+                  float2 x = __half22float2(*reinterpret_cast<const __half2*>(&pw[k]));
+                  const __half2 y = __floats2half2_rn(x.x * f, x.y * f);
+                  pw[k] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                tmem_st_16x128(ts_addr + 16 * b + ((16u * h) << 16), pw);
+              }
+            }
+            if (s > sg.s0) {
+              ok = mbar_wait(&bar->o_done[tile], (done - 1) & 1, 0x334);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int b = 0; b < D / 32; ++b) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float ov[16];
+                  tmem_ld_16x256(to_addr + 32 * b + ((16u * h) << 16), ov);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) ov[k] *= w[2 * h + ((k >> 1) & 1)];
+                  tmem_st_16x256(to_addr + 32 * b + ((16u * h) << 16), ov);
+                }
+              }
+            }
+          }
+          // weights
+          uint32_t pw[2][8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int pair = 16 * c + 4 * k + qd;
+            const float2 rc = *reinterpret_cast<const float2*>(tab + kStage * 2 + pair * 4 + 2);
+            const float2 rb = *reinterpret_cast<const float2*>(tab + kStage * 4 + pair * 2);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float* x = &v[y >> 1][4 * k + 2 * (y & 1)];
+              const float2 a = add2(make_float2(x[0], x[1]), make_float2(-m[y], -m[y]));
+              const float e0 = ex2(a.x), e1 = ex2(a.y);
+              const __half2 h2 = __floats2half2_rn(e0, e1);
+              pw[y >> 1][2 * k + (y & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
+              const float2 back = __half22float2(h2);
+              l[y] = fmaf(back.x, rc.x, fmaf(back.y, rc.y, l[y]));
+              beta[y] = fmaf(back.x, rb.x, fmaf(back.y, rb.y, beta[y]));
+            }
+          }
+          tmem_st_16x128(ts_addr + 16 * c, pw[0]);
+          tmem_st_16x128(ts_addr + 16 * c + (16u << 16), pw[1]);
+        }
+        if (!ok) break;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar->p_full[tile]);
+          mbar_arrive(&bar->t_empty[it % TD]);
+        }
+      }
+      if (!ok) break;
+
+      // ---- the item's end: sums of the quads, then a thread to a row ----
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
+          beta[k] += __shfl_xor_sync(0xffffffffu, beta[k], o);
+        }
+      }
+      float lr = 0.f, br = 0.f, mr = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = __shfl_sync(0xffffffffu, l[k], (lane & 7) * 4);
+        const float b = __shfl_sync(0xffffffffu, beta[k], (lane & 7) * 4);
+        const float c = __shfl_sync(0xffffffffu, m[k], (lane & 7) * 4);
+        if ((lane >> 3) == k) {
+          lr = a;
+          br = b;
+          mr = c;
+        }
+      }
+      ok = mbar_wait(&bar->o_done[tile], (done - 1) & 1, 0x335);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = sg.first && sg.last;
+      const int prow = kRows * tile + my;
+      float* part = whole ? nullptr
+                          : p.partials + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * PPartial<D>::FLOATS;
+      const float inv = whole ? (lr == 0.f ? 0.f : 1.0f / lr) : 1.0f;
+      const int t = grow / p.share, g = grow - t * p.share;
+      __half* const orow = p.out + (long long)(rq.q0 + t) * p.ldo + (long long)(sg.head * p.share + g) * D;
+#pragma unroll 1
+      for (int b = 0; b < D / 32; ++b) {
+        uint32_t raw[32];
+        tmem_ld32(to_addr + 32 * b, raw);
+        if (my < rows) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // positions of channels 0 .. 7: 0 2 4 6 1 3 5 7; odd channels are 16 times too large
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int at = 8 * c + ((j & 3) << 1) + (j >> 2);
+              x[j] = fmaf(__uint_as_float(raw[at]), (j & 1) ? 1048576.0f : 16777216.0f, br) * inv;
+            }
+            if (whole) {
+              uint32_t h[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __half2 y = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+                h[j] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              *reinterpret_cast<uint4*>(orow + 32 * b + 8 * c) = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+              float4* dst = reinterpret_cast<float4*>(part + (size_t)prow * D + 32 * b + 8 * c);
+              dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+              dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+            }
+          }
+        }
+      }
+      if (!whole && my < rows) {
+        part[kItemRows * D + prow] = mr;
+        part[kItemRows * D + kItemRows + prow] = lr;
+      }
+      tc_fence_before();
+      if (!whole && sg.first && tid == 0) {
+        const long long last_u = sg.item_end - 1;  // the block that holds the item's last unit
+        long long b = ((last_u + 1) * n - 1) / U;
+        while (U * b / n > last_u) --b;
+        while (U * (b + 1) / n <= last_u) ++b;
+        *header = PHeader{(int)(b - blockIdx.x), rq.q0, sg.row0, sg.rows, sg.head};
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// Joins the partials of the items that were cut (see the kernel for few rows).
+template <int D>
+__global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillAttnParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const PHeader h = p.headers[blockIdx.x];
+  if (h.followers <= 0) return;
+  constexpr int F = PPartial<D>::FLOATS;
+  const float* first = p.partials + ((size_t)blockIdx.x * 2 + 1) * F;
+  const float* rest = p.partials + ((size_t)blockIdx.x + 1) * 2 * F;  // follower i at i * 2 F
+  for (int e = blockIdx.y * 256 + threadIdx.x; e < h.rows * (D / 4); e += gridDim.y * 256) {
+    const int row = e / (D / 4), ch = (e - row * (D / 4)) * 4;
+    float m = first[kItemRows * D + row];
+    for (int i = 0; i < h.followers; ++i) m = fmaxf(m, rest[(size_t)i * 2 * F + kItemRows * D + row]);
+    float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int i = -1; i < h.followers; ++i) {
+      const float* part = i < 0 ? first : rest + (size_t)i * 2 * F;
+      const float w = ex2(part[kItemRows * D + row] - m);
+      const float4 v = *reinterpret_cast<const float4*>(part + (size_t)row * D + ch);
+      l = fmaf(w, part[kItemRows * D + kItemRows + row], l);
+      acc[0] = fmaf(w, v.x, acc[0]);
+      acc[1] = fmaf(w, v.y, acc[1]);
+      acc[2] = fmaf(w, v.z, acc[2]);
+      acc[3] = fmaf(w, v.w, acc[3]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    const int gr = h.row0 + row, t = gr / p.share, g = gr - t * p.share;
+    const __half2 a = __floats2half2_rn(acc[0] * inv, acc[1] * inv);
+    const __half2 b = __floats2half2_rn(acc[2] * inv, acc[3] * inv);
+    *reinterpret_cast<uint2*>(p.out + (long long)(h.q0 + t) * p.ldo + (long long)(h.head * p.share + g) * D + ch) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+
+template <int D>
+tlq_status launch_one(const PrefillAttnParams& base, cudaStream_t stream) {
+  using C = PCfg<D>;
+  auto kernel = prefill_attention_kernel<D>;
+  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (attr != cudaSuccess) return cuda_error(attr, "kv4 attention: shared memory");
+  const int blocks = device_info().sms;
+  PrefillAttnParams p = base;
+  p.headers = reinterpret_cast<PHeader*>(p.partials);
+  p.partials = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.partials) +
+                                        ((blocks * sizeof(PHeader) + 255) & ~size_t(255)));
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)blocks, 1, 1);
+  lc.blockDim = dim3(kThreads, 1, 1);
+  lc.dynamicSmemBytes = C::SMEM;
+  lc.stream = stream;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = &at;
+  lc.numAttrs = pdl_enabled() ? 1 : 0;
+  tlq_status st = cuda_error(cudaLaunchKernelEx(&lc, kernel, p), "kv4 prompt attention: launch");
+  if (st != TLQ_OK) return st;
+  lc.gridDim = dim3((unsigned)blocks, 8, 1);
+  lc.blockDim = dim3(256, 1, 1);
+  lc.dynamicSmemBytes = 0;
+  return cuda_error(cudaLaunchKernelEx(&lc, prefill_join_kernel<D>, p), "kv4 prompt attention join: launch");
+}
+
+}  // namespace
+
+size_t kv4_prefill_workspace(int head_dim) {
+  const size_t blocks = (size_t)device_info().sms;
+  return ((blocks * sizeof(PHeader) + 255) & ~size_t(255)) + blocks * 2 * kItemRows * (head_dim + 2) * sizeof(float);
+}
+
+tlq_status launch_kv4_prefill(const KvAttention& a, int few_rows, cudaStream_t stream) {
+  PrefillAttnParams p{};
+  p.cache = a.cache;
+  p.batch = a.batch;
+  p.q = a.q;
+  p.ldq = a.ldq;
+  p.out = a.out;
+  p.ldo = a.ldo;
+  p.scale_log2 = (float)((double)a.scale * M_LOG2E);
+  p.window = a.window;
+  p.share = a.q_heads / a.cache.heads;
+  p.few_rows = few_rows;
+  p.partials = static_cast<float*>(a.ws);
+  return a.head_dim == 64 ? launch_one<64>(p, stream) : launch_one<128>(p, stream);
+}
+
+}  // namespace tlq

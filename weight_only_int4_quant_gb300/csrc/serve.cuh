@@ -161,7 +161,11 @@ struct KvAttention {
   void* ws;
 };
 size_t kv4_decode_workspace(int head_dim);
-tlq_status launch_kv4_decode(const KvAttention& a, cudaStream_t stream);
+size_t kv4_prefill_workspace(int head_dim);
+// Requests of up to few_rows (query, head) rows to a key head go through the
+// first, the others through the second; each passes over what is not its own.
+tlq_status launch_kv4_decode(const KvAttention& a, int few_rows, cudaStream_t stream);
+tlq_status launch_kv4_prefill(const KvAttention& a, int few_rows, cudaStream_t stream);
 
 struct LoraArgs {
   const __half* x;

@@ -55,6 +55,10 @@ tlq_status check_cache(const tl_kv4_cache* c, KvCache* out, const char* who) {
   return TLQ_OK;
 }
 
+// Up to this many (query, head) rows to a key head a request's attention runs
+// on the kernel for few rows.
+constexpr int kFewRows = 32;
+
 size_t cache_bytes(const KvCache& c) { return (size_t)c.num_pages * c.heads * c.block_bytes; }
 
 }  // namespace
@@ -175,7 +179,7 @@ tlq_status tl_kv4_read(const tl_kv4_cache* cache, const int64_t* slots, int toke
 size_t tl_kv4_attention_workspace_size(int q_heads, int heads, int head_dim, int max_q) {
   clear_error();
   if (q_heads < 1 || heads < 1 || q_heads % heads || (head_dim != 64 && head_dim != 128) || max_q < 0) return 0;
-  return kv4_decode_workspace(head_dim);
+  return std::max(kv4_decode_workspace(head_dim), kv4_prefill_workspace(head_dim));
 }
 
 tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_t ldq, int q_heads, uint16_t* out,
@@ -205,6 +209,9 @@ tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_
       !aligned(seq_lens, 4) || !aligned(table, 4))
     return set_error(TLQ_EINVAL, "%s: q, out and the workspace must be 16-byte aligned", who);
   max_q = std::min(max_q, tokens);
+  if ((long long)max_q * (q_heads / a.cache.heads) > 0x3fffffff)
+    return set_error(TLQ_EUNSUPPORTED, "%s: max_q=%d x %d query heads to a key head (at most 2^30 rows)", who, max_q,
+                     q_heads / a.cache.heads);
   const size_t need = tl_kv4_attention_workspace_size(q_heads, a.cache.heads, cache->head_dim, max_q);
   if (!workspace || workspace_bytes < need)
     return set_error(TLQ_EINVAL, "%s: workspace of %zu bytes (%zu needed)", who, workspace ? workspace_bytes : size_t(0),
@@ -223,7 +230,13 @@ tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_
   a.scale = scale;
   a.window = window;
   a.ws = workspace;
-  return launch_kv4_decode(a, static_cast<cudaStream_t>(stream));
+  // The tensor-core kernel takes one scale a row, so rows in two groups stay
+  // with the other one whatever their number.
+  const int few = cache->head_dim == cache->group ? kFewRows : 0x7fffffff;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const tlq_status first = launch_kv4_decode(a, few, s);
+  if (first != TLQ_OK || (long long)max_q * (q_heads / a.cache.heads) <= few) return first;
+  return launch_kv4_prefill(a, few, s);
 }
 
 tlq_status tl_lora_add(const uint16_t* x, int64_t ldx, const uint16_t* A, const uint16_t* B, const float* scales,
