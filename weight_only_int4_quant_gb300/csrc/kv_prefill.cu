@@ -16,8 +16,8 @@
 //   warps 8-11      a thread to a token: its codes from global memory to
 //                   registers a stage ahead, then into the K and V tiles; its
 //                   scales and minima into the softmax's tables
-//   warp 12         one thread issues the MMAs:  P V of one tile and S of its
-//                   next stage run while the other tile's softmax works
+// One thread of each softmax group issues its tile's MMAs: P V and S of the next
+// stage run while the other tile's softmax works.
 // Both operands lie in shared memory as the cache has them, a token to a
 // 128-byte swizzled row: K-major for S, N-major (transposed by descriptor)
 // for P V, so no tile is transposed.  The order of channels inside a code
@@ -44,7 +44,7 @@ namespace {
 constexpr int kStage = 128;       // tokens of a stage
 constexpr int kRows = 128;        // rows of a tile
 constexpr int kItemRows = 256;    // rows of an item: two tiles
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 12 * 32;  // three warps to a scheduler: 168 registers a thread
 constexpr float kHeadroom = 6.0f;   // a new reference puts the largest weight at 2^6
 constexpr float kTrigger = 14.0f;   // weights stay at or below 2^14
 constexpr float kNone = -1e30f;
@@ -213,7 +213,20 @@ __device__ __forceinline__ void tmem_ld_16x128(uint32_t addr, uint32_t* v) {
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                : "r"(addr));
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The waits name the registers that the loads fill, so that nothing reads them earlier.
+__device__ __forceinline__ void tmem_wait_ld(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // N-major operand, SWIZZLE_128B: rows of 64 channels (128 bytes), 8 tokens to
@@ -262,13 +275,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Barriers of a block.
 struct PBars {
-  uint64_t q_full[2];             // Q tile written (4 warps)
-  uint64_t s_full[2];             // S of a stage complete
-  uint64_t p_full[2];             // weights written (4 warps)
-  uint64_t o_done[2];             // P V of a stage complete
-  uint64_t k_full[2], k_empty[2];
+  uint64_t s_full[2];             // by tile: S of a stage complete
+  uint64_t o_done[2];             // by tile: P V of a stage complete
+  uint64_t k_full[2], k_empty[2];  // written (4 warps), read (2 tiles)
   uint64_t v_full[2], v_empty[2];
   uint64_t t_empty[2];            // table read (8 warps)
   uint32_t tmem;
@@ -292,14 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar->q_full[i], 4);
       mbar_init(&bar->s_full[i], 1);
-      mbar_init(&bar->p_full[i], 4);
       mbar_init(&bar->o_done[i], 1);
       mbar_init(&bar->k_full[i], 4);
-      mbar_init(&bar->k_empty[i], 1);
+      mbar_init(&bar->k_empty[i], 2);
       mbar_init(&bar->v_full[i], 4);
-      mbar_init(&bar->v_empty[i], 1);
+      mbar_init(&bar->v_empty[i], 2);
       mbar_init(&bar->t_empty[i], 8);
     }
     fence_mbar_init();
@@ -339,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   PSegment sg;
   uint32_t it = 0;  // stages so far
 
-  if (warp >= 8 && warp < 12) {
+  if (warp >= 8) {
     // ---------------- a thread to a token: codes into the tiles ----------------
     const int tk = tid - 8 * 32;
     constexpr int W = D / 32;  // 16-byte pieces of a row of codes
@@ -465,78 +480,60 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       if (more) load_v();
       ++it;
     }
-  } else if (warp == 12) {
-    // ---------------- MMA issue ----------------
-    if (lane == 0) {
-      bool ok = true;
-      uint32_t tiles_it[2] = {0, 0};  // stages of each tile so far: the phases of p_full
-      uint32_t q_seg[2] = {0, 0};     // segments of each tile so far: the phases of q_full
-      auto issue_s = [&](int i, uint32_t at) {
-        const uint32_t a0 = smem_u32(sq + i * C::TILE), b0 = smem_u32(sk + (at % KD) * C::TILE);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * C::BLOCK + (kk & 3) * 32;
-          mma_ss(tmem + kStage * i, sw128_desc(a0 + o), sw128_desc(b0 + o), kIdescS, kk != 0);
-        }
-        umma_commit(&bar->s_full[i]);
-      };
-      auto issue_o = [&](int i, uint32_t at, bool begin) {
-        const uint32_t b0 = smem_u32(sv + (at % VD) * C::TILE);
-#pragma unroll
-        for (int kk = 0; kk < kStage / 16; ++kk)
-          mma_ts(tmem + 2 * kStage + D * i, tmem + kStage * i + kk * 8, sw128_desc_n(b0 + kk * 2048, C::BLOCK),
-                 kIdescO<D>, !(begin && kk == 0));
-        umma_commit(&bar->o_done[i]);
-      };
-      while (ok && walk.next(p, &sg)) {
-        const int tiles = sg.rows > kRows ? 2 : 1, T = sg.s1 - sg.s0;
-        ok = mbar_wait(&bar->k_full[it % KD], (it / KD) & 1, 0x321);
-        for (int i = 0; i < tiles && ok; ++i) {
-          ok = mbar_wait(&bar->q_full[i], q_seg[i] & 1, 0x322);
-          if (!ok) break;
-          ++q_seg[i];
-          tc_fence_after();
-          issue_s(i, it);
-        }
-        if (!ok) break;
-        umma_commit(&bar->k_empty[it % KD]);
-        for (int s = 0; s < T && ok; ++s, ++it) {
-          const bool next = s + 1 < T;
-          if (next) ok = mbar_wait(&bar->k_full[(it + 1) % KD], ((it + 1) / KD) & 1, 0x323);
-          ok = ok && mbar_wait(&bar->v_full[it % VD], (it / VD) & 1, 0x324);
-          for (int i = 0; i < tiles && ok; ++i) {
-            ok = mbar_wait(&bar->p_full[i], tiles_it[i] & 1, 0x325);
-            if (!ok) break;
-            ++tiles_it[i];
-            tc_fence_after();
-            issue_o(i, it, s == 0);
-            if (next) issue_s(i, it + 1);
-          }
-          if (!ok) break;
-          umma_commit(&bar->v_empty[it % VD]);
-          if (next) umma_commit(&bar->k_empty[(it + 1) % KD]);
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp < 8) {
-    // ---------------- softmax ----------------
+  } else {
+    // ---------------- softmax, and its tile's MMAs ----------------
     const int tile = warp >> 2, quarter = warp & 3;
     const int r = lane >> 2, qd = lane & 3;
+    const bool leader = quarter == 0 && lane == 0;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
     const uint32_t ts_addr = lanes + kStage * tile;              // S, and the weights over it
     const uint32_t to_addr = lanes + 2 * kStage + D * tile;      // O
     uint32_t done = 0;  // stages of this tile so far: the phases of s_full and o_done
+    // A wait that gave up ends waiting and issuing for good, but nothing else:
+    // every warp still comes to every barrier.
     bool ok = true;
-    while (ok && walk.next(p, &sg)) {
+    // S of stage `at` (leader only)
+    auto issue_s = [&](uint32_t at) -> bool {
+      if (!mbar_wait(&bar->k_full[at % KD], (at / KD) & 1, 0x321)) return false;
+      tc_fence_after();
+      const uint32_t a0 = smem_u32(sq + tile * C::TILE), b0 = smem_u32(sk + (at % KD) * C::TILE);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t o = (kk >> 2) * C::BLOCK + (kk & 3) * 32;
+        mma_ss(tmem + kStage * tile, sw128_desc(a0 + o), sw128_desc(b0 + o), kIdescS, kk != 0);
+      }
+      umma_commit(&bar->s_full[tile]);
+      umma_commit(&bar->k_empty[at % KD]);
+      return true;
+    };
+    // O += P V of stage `at` (leader only).  MMAs of one thread run in order, so
+    // the S that follows may overwrite the weights this one reads.
+    auto issue_o = [&](uint32_t at, bool begin) -> bool {
+      if (!mbar_wait(&bar->v_full[at % VD], (at / VD) & 1, 0x324)) return false;
+      tc_fence_after();
+      const uint32_t b0 = smem_u32(sv + (at % VD) * C::TILE);
+#pragma unroll
+      for (int kk = 0; kk < kStage / 16; ++kk)
+        mma_ts(tmem + 2 * kStage + D * tile, tmem + kStage * tile + kk * 8, sw128_desc_n(b0 + kk * 2048, C::BLOCK),
+               kIdescO<D>, !(begin && kk == 0));
+      umma_commit(&bar->o_done[tile]);
+      umma_commit(&bar->v_empty[at % VD]);
+      return true;
+    };
+    while (walk.next(p, &sg)) {
       const KvRequest rq = sg.rq;
       const int rows = min(kRows, sg.rows - kRows * tile);  // of this tile; below 1: none
       const int base_pos = rq.len - rq.q_len;
-      if (rows <= 0) {  // the tile is empty: only let the tables go on
-        for (int s = sg.s0; s < sg.s1 && ok; ++s, ++it) {
-          ok = mbar_wait(&bar->k_full[it % KD], (it / KD) & 1, 0x331);
+      if (rows <= 0) {  // the tile is empty: only let the rings go on
+        for (int s = sg.s0; s < sg.s1; ++s, ++it) {
+          ok = ok && mbar_wait(&bar->k_full[it % KD], (it / KD) & 1, 0x331) &&
+               mbar_wait(&bar->v_full[it % VD], (it / VD) & 1, 0x336);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar->t_empty[it % TD]);
+          if (leader) {
+            mbar_arrive(&bar->k_empty[it % KD]);
+            mbar_arrive(&bar->v_empty[it % VD]);
+          }
         }
         continue;
       }
@@ -563,17 +560,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
                  prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
         }
         fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->q_full[tile]);
       }
-      float qs[4], m[4], l[4], beta[4];
+      named_barrier(1 + tile, 128);
+      if (leader && ok) ok = issue_s(it);
+      __syncwarp();
+      float qs[4], m[4];
+      float2 l[4], beta[4];  // by even and odd columns
       int pos[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // rows r + 8 k of this warp's 32
         qs[k] = __shfl_sync(0xffffffffu, qsum, r + 8 * k);
         pos[k] = base_pos + (sg.row0 + min(kRows * tile + 32 * quarter + r + 8 * k, sg.rows - 1)) / p.share;
         m[k] = kNone;
-        l[k] = beta[k] = 0.f;
+        l[k] = beta[k] = make_float2(0.f, 0.f);
       }
       // keys below all_hi and from all_lo are seen by every row of the tile
       const int all_hi = base_pos + (sg.row0 + kRows * tile) / p.share + 1;
@@ -581,70 +580,86 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           p.window > 0 ? base_pos + (sg.row0 + kRows * tile + rows - 1) / p.share - p.window + 1 : 0;
 
       for (int s = sg.s0; s < sg.s1; ++s, ++it, ++done) {
-        ok = mbar_wait(&bar->k_full[it % KD], (it / KD) & 1, 0x332) &&  // the table, written before the keys
+        ok = ok && mbar_wait(&bar->k_full[it % KD], (it / KD) & 1, 0x332) &&  // the table, written before the keys
              mbar_wait(&bar->s_full[tile], done & 1, 0x333);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
         tc_fence_after();
         const float* tab = reinterpret_cast<const float*>(st + (it % TD) * C::TABLE);
         const bool edge = s * kStage < all_lo || (s + 1) * kStage > all_hi;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float v[2][16];  // [rows r, r + 8 | rows r + 16, r + 24]
+
+        // 32 columns: v holds [rows r, r + 8 | rows r + 16, r + 24]
+        auto load = [&](int c, float(&v)[2][16]) {
           tmem_ld_16x256(ts_addr + 32 * c, v[0]);
           tmem_ld_16x256(ts_addr + 32 * c + (16u << 16), v[1]);
-          tmem_wait_ld();
-          bool over = false;
+        };
+        auto wait = [&](float(&v)[2][16]) {
+          tmem_wait_ld(v[0]);
+          tmem_wait_ld(v[1]);
+        };
+        auto work = [&](int c, float(&v)[2][16]) {
+          float2 rc[4];
+          float top[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {  // column pair 32 c + 8 k + 2 qd
             const int pair = 16 * c + 4 * k + qd;
             const float4 ab = *reinterpret_cast<const float4*>(tab + pair * 4);
-            const float2 lg = *reinterpret_cast<const float2*>(tab + kStage * 2 + pair * 4);
+            const float4 lr = *reinterpret_cast<const float4*>(tab + kStage * 2 + pair * 4);
+            rc[k] = make_float2(lr.z, lr.w);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               float* x = &v[y >> 1][4 * k + 2 * (y & 1)];
-              float2 z = fma2(make_float2(qs[y], qs[y]), make_float2(ab.z, ab.w), lg);
-              z = fma2(make_float2(x[0], x[1]), make_float2(ab.x, ab.y), z);
-              if (edge) {
-                const int key = s * kStage + 32 * c + 8 * k + 2 * qd;
-                const int from = p.window > 0 ? pos[y] - p.window : -1;
-                if (key > pos[y] || key <= from) z.x = -INFINITY;
-                if (key + 1 > pos[y] || key + 1 <= from) z.y = -INFINITY;
-              }
+              const float2 z = fma2(make_float2(x[0], x[1]), make_float2(ab.x, ab.y),
+                                    fma2(make_float2(qs[y], qs[y]), make_float2(ab.z, ab.w), make_float2(lr.x, lr.y)));
               x[0] = z.x;
               x[1] = z.y;
-              over |= fmaxf(z.x, z.y) > m[y] + kTrigger;
             }
+          }
+          if (edge) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                float* x = &v[y >> 1][4 * k + 2 * (y & 1)];
+                const int key = s * kStage + 32 * c + 8 * k + 2 * qd;
+                const int from = p.window > 0 ? pos[y] - p.window : -1;
+                if (key > pos[y] || key <= from) x[0] = -INFINITY;
+                if (key + 1 > pos[y] || key + 1 <= from) x[1] = -INFINITY;
+              }
+          }
+          bool over = false;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float* x = &v[y >> 1][2 * (y & 1)];
+            top[y] = max3(max3(max3(x[0], x[1], x[4]), x[5], x[8]), max3(x[9], x[12], x[13]), kNone);
+            over |= top[y] > m[y] + kTrigger;
           }
           if (__any_sync(0xffffffffu, over)) {
             // a new reference: sums, weights already written and O move with it
             float w[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              float x = kNone;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float* a = &v[y >> 1][4 * k + 2 * (y & 1)];
-                x = fmaxf(x, fmaxf(a[0], a[1]));
-              }
+              float x = top[y];
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
               const float next = fmaxf(m[y], x - kHeadroom);
               w[y] = ex2(m[y] - next);
               m[y] = next;
-              l[y] *= w[y];
-              beta[y] *= w[y];
+              l[y].x *= w[y];
+              l[y].y *= w[y];
+              beta[y].x *= w[y];
+              beta[y].y *= w[y];
             }
+#pragma unroll 1
             for (int b = 0; b < c; ++b) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 uint32_t pw[8];
                 tmem_ld_16x128(ts_addr + 16 * b + ((16u * h) << 16), pw);
-                tmem_wait_ld();
+                tmem_wait_ld(pw);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                   const float f = w[2 * h + (k & 1)];
-                  float2 x = __half22float2(*reinterpret_cast<const __half2*>(&pw[k]));
+                  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&pw[k]));
                   const __half2 y = __floats2half2_rn(x.x * f, x.y * f);
                   pw[k] = *reinterpret_cast<const uint32_t*>(&y);
                 }
@@ -652,9 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
               }
             }
             if (s > sg.s0) {
-              ok = mbar_wait(&bar->o_done[tile], (done - 1) & 1, 0x334);
+              ok = ok && mbar_wait(&bar->o_done[tile], (done - 1) & 1, 0x334);
               ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
               for (int b = 0; b < D / 32; ++b) {
@@ -662,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
                 for (int h = 0; h < 2; ++h) {
                   float ov[16];
                   tmem_ld_16x256(to_addr + 32 * b + ((16u * h) << 16), ov);
-                  tmem_wait_ld();
+                  tmem_wait_ld(ov);
 #pragma unroll
                   for (int k = 0; k < 16; ++k) ov[k] *= w[2 * h + ((k >> 1) & 1)];
                   tmem_st_16x256(to_addr + 32 * b + ((16u * h) << 16), ov);
@@ -675,48 +689,61 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int pair = 16 * c + 4 * k + qd;
-            const float2 rc = *reinterpret_cast<const float2*>(tab + kStage * 2 + pair * 4 + 2);
             const float2 rb = *reinterpret_cast<const float2*>(tab + kStage * 4 + pair * 2);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               const float* x = &v[y >> 1][4 * k + 2 * (y & 1)];
               const float2 a = add2(make_float2(x[0], x[1]), make_float2(-m[y], -m[y]));
-              const float e0 = ex2(a.x), e1 = ex2(a.y);
-              const __half2 h2 = __floats2half2_rn(e0, e1);
+              const __half2 h2 = __floats2half2_rn(ex2(a.x), ex2(a.y));
               pw[y >> 1][2 * k + (y & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
               const float2 back = __half22float2(h2);
-              l[y] = fmaf(back.x, rc.x, fmaf(back.y, rc.y, l[y]));
-              beta[y] = fmaf(back.x, rb.x, fmaf(back.y, rb.y, beta[y]));
+              l[y] = fma2(back, rc[k], l[y]);
+              beta[y] = fma2(back, rb, beta[y]);
             }
           }
           tmem_st_16x128(ts_addr + 16 * c, pw[0]);
           tmem_st_16x128(ts_addr + 16 * c + (16u << 16), pw[1]);
+        };
+        float va[2][16], vb[2][16];  // the next 32 columns are on their way while 32 are worked on
+        load(0, va);
+        wait(va);
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          load(c + 1, vb);
+          work(c, va);
+          wait(vb);
+          if (c == 0) load(2, va);
+          work(c + 1, vb);
+          if (c == 0) wait(va);
         }
-        if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar->p_full[tile]);
-          mbar_arrive(&bar->t_empty[it % TD]);
+        if (lane == 0) mbar_arrive(&bar->t_empty[it % TD]);
+        named_barrier(1 + tile, 128);
+        if (leader && ok) {
+          ok = issue_o(it, s == sg.s0);
+          if (ok && s + 1 < sg.s1) ok = issue_s(it + 1);
         }
+        ok = __all_sync(0xffffffffu, ok);
       }
-      if (!ok) break;
 
       // ---- the item's end: sums of the quads, then a thread to a row ----
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        l[k].x += l[k].y;
+        beta[k].x += beta[k].y;
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
-          l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
-          beta[k] += __shfl_xor_sync(0xffffffffu, beta[k], o);
+          l[k].x += __shfl_xor_sync(0xffffffffu, l[k].x, o);
+          beta[k].x += __shfl_xor_sync(0xffffffffu, beta[k].x, o);
         }
       }
       float lr = 0.f, br = 0.f, mr = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float a = __shfl_sync(0xffffffffu, l[k], (lane & 7) * 4);
-        const float b = __shfl_sync(0xffffffffu, beta[k], (lane & 7) * 4);
+        const float a = __shfl_sync(0xffffffffu, l[k].x, (lane & 7) * 4);
+        const float b = __shfl_sync(0xffffffffu, beta[k].x, (lane & 7) * 4);
         const float c = __shfl_sync(0xffffffffu, m[k], (lane & 7) * 4);
         if ((lane >> 3) == k) {
           lr = a;
@@ -724,9 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           mr = c;
         }
       }
-      ok = mbar_wait(&bar->o_done[tile], (done - 1) & 1, 0x335);
+      ok = ok && mbar_wait(&bar->o_done[tile], (done - 1) & 1, 0x335);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
       tc_fence_after();
       const bool whole = sg.first && sg.last;
       const int prow = kRows * tile + my;
