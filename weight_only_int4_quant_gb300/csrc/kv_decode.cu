@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
       for (int s = sg.s0; s < sg.s1; ++s, ++stage_i) {
         const int slot = stage_i % DEPTH;
         const int next = page_of(s + 1);
-        if (!mbar_wait(&empty[slot], ((stage_i / DEPTH) & 1) ^ 1, 0x302)) {
+        if (!mbar_wait_long(&empty[slot], ((stage_i / DEPTH) & 1) ^ 1, 0x302)) {
           ok = false;
           break;
         }
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
     }
     // no copy is under way when the block ends
     for (int i = max(0, stage_i - DEPTH); i < stage_i; ++i)
-      if (!mbar_wait(&full[i % DEPTH], (i / DEPTH) & 1, 0x303)) break;
+      if (!mbar_wait_long(&full[i % DEPTH], (i / DEPTH) & 1, 0x303)) break;
     return;
   }
 
@@ -411,10 +411,10 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
 
     for (int s = sg.s0; s < sg.s1; ++s, ++stage_i) {
       const int slot = stage_i % DEPTH;
-      ok = ok && mbar_wait(&full[slot], (stage_i / DEPTH) & 1, 0x301);
+      ok = ok && mbar_wait_long(&full[slot], (stage_i / DEPTH) & 1, 0x301);
       if (!ok) break;
       const int tok0 = s * kStage + warp * (kTiles * kTile);
-      const uint32_t tiles = there[slot] >> (warp * kTiles);
+      const uint32_t tiles = lds32(smem_u32(&there[slot])) >> (warp * kTiles);
       const uint32_t sb = smem_u32(smem) + slot * C::STAGE_BYTES;
       if (tok0 < sg.hi && tok0 + kTiles * kTile > sg.lo && (tiles & ((1u << kTiles) - 1u))) {
         // some row does not see some key of the tiles, or a page is missing

@@ -7,7 +7,9 @@
 // The codes go to the matrix instructions exactly, as the FP16 subnormals
 // c * 2^-24 (a mask and at most one shift per pair); scales and minima are
 // applied in FP32 in the softmax.  The only roundings to FP16 are those of the
-// weights p' and of the result, as in the kernel for few rows.
+// weights p' and of the result.  Value codes enter as c - 8: a weight's rounding
+// then meets a factor of about the spread of the values (an uncentred code's
+// mean is three times that), with minima b + 8 s beside it in FP32.
 //
 // A block takes two tiles of 128 (query, head) rows of one key head against
 // stages of 128 tokens:
@@ -275,6 +277,20 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float4 lds_f32x4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float2 lds_f32x2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts_f32(uint32_t a, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -420,24 +436,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
     while (ok && more) {
       const int ks = it % KD, vs = it % VD, ts = it % TD;
       // the softmax's constants of this token
-      ok = mbar_wait(&bar->t_empty[ts], ((it / TD) & 1) ^ 1, 0x311) &&
-           mbar_wait(&bar->k_empty[ks], ((it / KD) & 1) ^ 1, 0x312);
+      ok = mbar_wait_long(&bar->t_empty[ts], ((it / TD) & 1) ^ 1, 0x311) &&
+           mbar_wait_long(&bar->k_empty[ks], ((it / KD) & 1) ^ 1, 0x312);
       if (!ok) break;
       {
         const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(&kpar));
         const float2 vp = __half22float2(*reinterpret_cast<const __half2*>(&vpar));
         const float vsc = fmaxf(vp.x, 5.9604644775390625e-8f), rc = __fdividef(1.0f, vsc);
-        float* tab = reinterpret_cast<float*>(st + ts * C::TABLE);
-        const int pair = tk >> 1, e = tk & 1;
-        float* t1 = tab + pair * 4;
-        float* t2 = tab + kStage * 2 + pair * 4;
-        float* t3 = tab + kStage * 4 + pair * 2;
+        const uint32_t tab = smem_u32(st + ts * C::TABLE) + (tk & 1) * 4;
+        const uint32_t t1 = tab + (tk >> 1) * 16, t2 = t1 + kStage * 8, t3 = tab + kStage * 16 + (tk >> 1) * 8;
         // no token: its logit is -infinity whatever the row
-        t1[e] = live ? kp.x * (p.scale_log2 * 16777216.0f) : 0.f;
-        t1[2 + e] = live ? kp.y * p.scale_log2 : 0.f;
-        t2[e] = live ? lg2(vsc) : -INFINITY;
-        t2[2 + e] = live ? rc : 0.f;
-        t3[e] = live ? rc * vp.y : 0.f;
+        sts_f32(t1, live ? kp.x * (p.scale_log2 * 16777216.0f) : 0.f);
+        sts_f32(t1 + 8, live ? kp.y * p.scale_log2 : 0.f);
+        sts_f32(t2, live ? lg2(vsc) : -INFINITY);
+        sts_f32(t2 + 8, live ? rc : 0.f);
+        sts_f32(t3, live ? fmaf(rc, vp.y, 8.0f) : 0.f);  // the value codes are centred: c - 8
       }
       const uint32_t kb = smem_u32(sk + ks * C::TILE) + row;
 #pragma unroll
@@ -460,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
         have2 = advance(nx, nstage);
         page2 = have2 ? page_of(nx, nstage) : -1;
       }
-      ok = mbar_wait(&bar->v_empty[vs], ((it / VD) & 1) ^ 1, 0x313);
+      ok = mbar_wait_long(&bar->v_empty[vs], ((it / VD) & 1) ^ 1, 0x313);
       if (!ok) break;
       const uint32_t vb = smem_u32(sv + vs * C::TILE) + row;
 #pragma unroll
@@ -469,9 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t w = w4[j], x = w >> 8, c = 4 * i + j;
-          // odd channels enter 16 times too large; the output takes it back
-          sts128(vb + (c >> 3) * C::BLOCK + (((c & 7) ^ sw) << 4), w & 0x000F000Fu, w & 0x00F000F0u, x & 0x000F000Fu,
-                 x & 0x00F000F0u);
+          // (c - 8) 2^-24, exact; odd channels enter 16 times too large, which the output takes back
+          sts128(vb + (c >> 3) * C::BLOCK + (((c & 7) ^ sw) << 4), hsub2u(w & 0x000F000Fu, 0x00080008u),
+                 hsub2u(w & 0x00F000F0u, 0x00800080u), hsub2u(x & 0x000F000Fu, 0x00080008u),
+                 hsub2u(x & 0x00F000F0u, 0x00800080u));
         }
       }
       fence_proxy_async_smem();
@@ -494,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
     bool ok = true;
     // S of stage `at` (leader only)
     auto issue_s = [&](uint32_t at) -> bool {
-      if (!mbar_wait(&bar->k_full[at % KD], (at / KD) & 1, 0x321)) return false;
+      if (!mbar_wait_long(&bar->k_full[at % KD], (at / KD) & 1, 0x321)) return false;
       tc_fence_after();
       const uint32_t a0 = smem_u32(sq + tile * C::TILE), b0 = smem_u32(sk + (at % KD) * C::TILE);
 #pragma unroll
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
     // O += P V of stage `at` (leader only).  MMAs of one thread run in order, so
     // the S that follows may overwrite the weights this one reads.
     auto issue_o = [&](uint32_t at, bool begin) -> bool {
-      if (!mbar_wait(&bar->v_full[at % VD], (at / VD) & 1, 0x324)) return false;
+      if (!mbar_wait_long(&bar->v_full[at % VD], (at / VD) & 1, 0x324)) return false;
       tc_fence_after();
       const uint32_t b0 = smem_u32(sv + (at % VD) * C::TILE);
 #pragma unroll
@@ -526,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       const int base_pos = rq.len - rq.q_len;
       if (rows <= 0) {  // the tile is empty: only let the rings go on
         for (int s = sg.s0; s < sg.s1; ++s, ++it) {
-          ok = ok && mbar_wait(&bar->k_full[it % KD], (it / KD) & 1, 0x331) &&
-               mbar_wait(&bar->v_full[it % VD], (it / VD) & 1, 0x336);
+          ok = ok && mbar_wait_long(&bar->k_full[it % KD], (it / KD) & 1, 0x331) &&
+               mbar_wait_long(&bar->v_full[it % VD], (it / VD) & 1, 0x336);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar->t_empty[it % TD]);
           if (leader) {
@@ -580,11 +594,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           p.window > 0 ? base_pos + (sg.row0 + kRows * tile + rows - 1) / p.share - p.window + 1 : 0;
 
       for (int s = sg.s0; s < sg.s1; ++s, ++it, ++done) {
-        ok = ok && mbar_wait(&bar->k_full[it % KD], (it / KD) & 1, 0x332) &&  // the table, written before the keys
-             mbar_wait(&bar->s_full[tile], done & 1, 0x333);
+        ok = ok && mbar_wait_long(&bar->k_full[it % KD], (it / KD) & 1, 0x332) &&  // the table, written before the keys
+             mbar_wait_long(&bar->s_full[tile], done & 1, 0x333);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
-        const float* tab = reinterpret_cast<const float*>(st + (it % TD) * C::TABLE);
+        const uint32_t tab = smem_u32(st + (it % TD) * C::TABLE) + qd * 16, tab3 = tab + kStage * 16 - qd * 8;
         const bool edge = s * kStage < all_lo || (s + 1) * kStage > all_hi;
 
         // 32 columns: v holds [rows r, r + 8 | rows r + 16, r + 24]
@@ -601,9 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           float top[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {  // column pair 32 c + 8 k + 2 qd
-            const int pair = 16 * c + 4 * k + qd;
-            const float4 ab = *reinterpret_cast<const float4*>(tab + pair * 4);
-            const float4 lr = *reinterpret_cast<const float4*>(tab + kStage * 2 + pair * 4);
+            const float4 ab = lds_f32x4(tab + (16 * c + 4 * k) * 16);
+            const float4 lr = lds_f32x4(tab + (16 * c + 4 * k) * 16 + kStage * 8);
             rc[k] = make_float2(lr.z, lr.w);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -667,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
               }
             }
             if (s > sg.s0) {
-              ok = ok && mbar_wait(&bar->o_done[tile], (done - 1) & 1, 0x334);
+              ok = ok && mbar_wait_long(&bar->o_done[tile], (done - 1) & 1, 0x334);
               ok = __all_sync(0xffffffffu, ok);
               tc_fence_after();
 #pragma unroll 1
@@ -688,17 +701,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           uint32_t pw[2][8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int pair = 16 * c + 4 * k + qd;
-            const float2 rb = *reinterpret_cast<const float2*>(tab + kStage * 4 + pair * 2);
+            const float2 rb = lds_f32x2(tab3 + (16 * c + 4 * k) * 8);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               const float* x = &v[y >> 1][4 * k + 2 * (y & 1)];
               const float2 a = add2(make_float2(x[0], x[1]), make_float2(-m[y], -m[y]));
-              const __half2 h2 = __floats2half2_rn(ex2(a.x), ex2(a.y));
+              const float2 e = make_float2(ex2(a.x), ex2(a.y));
+              const __half2 h2 = __floats2half2_rn(e.x, e.y);
               pw[y >> 1][2 * k + (y & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
-              const float2 back = __half22float2(h2);
-              l[y] = fma2(back, rc[k], l[y]);
-              beta[y] = fma2(back, rb, beta[y]);
+              l[y] = fma2(e, rc[k], l[y]);
+              beta[y] = fma2(e, rb, beta[y]);
             }
           }
           tmem_st_16x128(ts_addr + 16 * c, pw[0]);
@@ -751,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           mr = c;
         }
       }
-      ok = ok && mbar_wait(&bar->o_done[tile], (done - 1) & 1, 0x335);
+      ok = ok && mbar_wait_long(&bar->o_done[tile], (done - 1) & 1, 0x335);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const bool whole = sg.first && sg.last;

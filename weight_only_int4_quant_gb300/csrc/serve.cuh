@@ -122,6 +122,31 @@ struct UnitSearch {
   }
 };
 
+// mbar_wait for waits that last a stage or more: the hardware holds the thread
+// for up to 10 us at a try, so a waiting warp leaves the scheduler to the others
+// (without the hint waiting warps issued half of all instructions of the prompt
+// kernel).  Bounded like mbar_wait.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, uint32_t where) {
+  auto held = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
+        : "memory");
+    return ok != 0;
+  };
+  if (held()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!held()) {
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      record_timeout(where);
+      return false;
+    }
+  }
+  return true;
+}
+
 // Launchers (arguments validated by the entry points).
 struct KvPlanArgs {
   const int* cached;
