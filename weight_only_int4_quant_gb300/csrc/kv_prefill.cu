@@ -15,11 +15,15 @@
 // stages of 128 tokens:
 //   warps 0-3, 4-7  softmax of the first, second tile: S from TMEM, weights
 //                   back to TMEM over it (FP16, the A operand of P V)
-//   warps 8-11      a thread to a token: its codes from global memory to
-//                   registers a stage ahead, then into the K and V tiles; its
-//                   scales and minima into the softmax's tables
-// One thread of each softmax group issues its tile's MMAs: P V and S of the next
-// stage run while the other tile's softmax works.
+//   warps 8-10      a thread to a row of codes (a token's key or value): from
+//                   global memory to registers a stage ahead, then into the K
+//                   and V tiles; scales and minima into the softmax's tables
+//   warp 11         issues the MMAs
+// A stage is worked on in two halves of 64 tokens with an S each, so the tensor
+// cores form the next half's S and add the last half's P V while a softmax
+// works.  (With one S a stage, a tile's softmax and its MMAs took turns: 6300
+// clocks a stage, twice the tensor cores' time.)  Twelve warps, three to a
+// scheduler, leave the softmax 168 registers a thread; with thirteen it spilled.
 // Both operands lie in shared memory as the cache has them, a token to a
 // 128-byte swizzled row: K-major for S, N-major (transposed by descriptor)
 // for P V, so no tile is transposed.  The order of channels inside a code
@@ -46,7 +50,9 @@ namespace {
 constexpr int kStage = 128;       // tokens of a stage
 constexpr int kRows = 128;        // rows of a tile
 constexpr int kItemRows = 256;    // rows of an item: two tiles
-constexpr int kThreads = 12 * 32;  // three warps to a scheduler: 168 registers a thread
+constexpr int kHalf = 64;         // tokens of an S
+constexpr int kCodeWarps = 3;     // warps that write the K and V tiles
+constexpr int kThreads = (8 + kCodeWarps + 1) * 32;
 constexpr float kHeadroom = 6.0f;   // a new reference puts the largest weight at 2^6
 constexpr float kTrigger = 14.0f;   // weights stay at or below 2^14
 constexpr float kNone = -1e30f;
@@ -241,24 +247,35 @@ __device__ __forceinline__ uint64_t sw128_desc_n(uint32_t saddr, uint32_t block_
 
 // kind::f16, D = F32, A = B = F16, M = 128; bit 16: B is N-major.
 constexpr uint32_t kIdescS =
-    (1u << 4) | ((uint32_t)(kStage >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+    (1u << 4) | ((uint32_t)(kHalf >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 template <int D>
 constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 
+// The MMAs and commits are executed by a converged warp, of which one elected
+// thread issues (the same one every time): the operands stay in uniform
+// registers.  Issued from a one-thread branch, each MMA's operands were moved
+// there one by one, 2 us for the sixteen of a stage and tile.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accum)
       : "memory");
 }
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -299,11 +316,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // Barriers of a block.
 struct PBars {
-  uint64_t s_full[2];             // by tile: S of a stage complete
-  uint64_t o_done[2];             // by tile: P V of a stage complete
-  uint64_t k_full[2], k_empty[2];  // written (4 warps), read (2 tiles)
+  uint64_t q_full[2];              // by tile: Q written (4 warps)
+  uint64_t s_full[2][2];           // by tile and half: S complete
+  uint64_t p_full[2][2];           // by tile and half: the weights written (4 warps)
+  uint64_t o_done[2][2];           // by tile and half: P V complete
+  uint64_t k_full[2], k_empty[2];  // written (4 warps), read
   uint64_t v_full[2], v_empty[2];
-  uint64_t t_empty[2];            // table read (8 warps)
+  uint64_t t_empty[2];             // table read (8 warps)
   uint32_t tmem;
 };
 
@@ -321,16 +340,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   static_assert(sizeof(PBars) <= C::BARS, "barriers fit");
   __shared__ UnitSearch<kThreads> search;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = (int)uniform(tid >> 5), lane = tid & 31;
   pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar->s_full[i], 1);
-      mbar_init(&bar->o_done[i], 1);
+      mbar_init(&bar->q_full[i], 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&bar->s_full[i][h], 1);
+        mbar_init(&bar->p_full[i][h], 4);
+        mbar_init(&bar->o_done[i][h], 1);
+      }
       mbar_init(&bar->k_full[i], 4);
-      mbar_init(&bar->k_empty[i], 2);
+      mbar_init(&bar->k_empty[i], 1);
       mbar_init(&bar->v_full[i], 4);
-      mbar_init(&bar->v_empty[i], 2);
+      mbar_init(&bar->v_empty[i], 1);
       mbar_init(&bar->t_empty[i], 8);
     }
     fence_mbar_init();
@@ -339,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bar->tmem;
+  const uint32_t tmem = uniform(bar->tmem);
   pdl_wait();
   PHeader* const header = &p.headers[blockIdx.x];
   if (tid == 0) header->followers = 0;
@@ -370,184 +393,207 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   PSegment sg;
   uint32_t it = 0;  // stages so far
 
-  if (warp >= 8) {
-    // ---------------- a thread to a token: codes into the tiles ----------------
-    const int tk = tid - 8 * 32;
+  if (warp >= 8 && warp < 8 + kCodeWarps) {
+    // ---------------- codes into the tiles ----------------
+    // The 256 rows of a stage, keys then values, go round the 96 threads: row
+    // 96 j + (thread) in round j; a warp's rows are all keys or all values.
     constexpr int W = D / 32;  // 16-byte pieces of a row of codes
-    uint4 kw[W], vw[W];
-    uint32_t kpar = 0, vpar = 0;
-    bool live = false, live_next = false;
-    auto page_of = [&](const PSegment& s, int stage) {
-      const int key = stage * kStage + tk;
-      return stage < s.s1 && key >= s.lo && key < s.hi
-                 ? __ldg(p.batch.table + (size_t)s.req * p.batch.ld_table + (key >> p.cache.page_shift))
-                 : -1;
-    };
-    const uint8_t* vsrc = nullptr;
-    uint32_t vpar_next = 0;
-    // keys of stage `stage` into kw, and where its values lie
-    auto load_k = [&](const PSegment& s, int stage, int page) {
-      live_next = page >= 0 && page < p.cache.num_pages;
-      if (live_next) {
-        const int P = p.cache.page, off = (stage * kStage + tk) & (P - 1);
-        const uint8_t* blk = p.cache.blocks + ((uint32_t)page * (uint32_t)p.cache.heads + s.head) *
-                                                  (uint64_t)p.cache.block_bytes;
-        const uint4* src = reinterpret_cast<const uint4*>(blk + off * (D / 2));
+    constexpr int ROUNDS = 3, N = 32 * kCodeWarps;
+    static_assert(ROUNDS * N >= 2 * kStage && (2 * kStage) % 32 == 0, "rounds");
+    const int me = tid - 8 * 32;
+    uint4 cw[ROUNDS][W];  // codes of the stage at hand, and of the next as rounds pass
+    uint32_t par[ROUNDS];
+    bool live[ROUNDS];
+    int page[ROUNDS];     // of the next stage's rows
+    auto rows_page = [&](const PSegment& s, int stage, bool have) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) kw[i] = __ldg(src + i);
-        vsrc = blk + (P + off) * (D / 2);
-        kpar = __ldg(reinterpret_cast<const uint32_t*>(blk + P * D) + off);
-        vpar_next = __ldg(reinterpret_cast<const uint32_t*>(blk + P * D) + P + off);
-      } else {
-#pragma unroll
-        for (int i = 0; i < W; ++i) kw[i] = make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < ROUNDS; ++j) {
+        const int t = j * N + me, key = stage * kStage + (t & (kStage - 1));
+        page[j] = have && t < 2 * kStage && key >= s.lo && key < s.hi
+                      ? __ldg(p.batch.table + (size_t)s.req * p.batch.ld_table + (key >> p.cache.page_shift))
+                      : -1;
       }
     };
-    auto load_v = [&] {
+    auto load = [&](int j, const PSegment& s, int stage) {
+      live[j] = page[j] >= 0 && page[j] < p.cache.num_pages;
+      par[j] = 0;
+      if (live[j]) {
+        const int t = j * N + me, part = t >> 7;
+        const int P = p.cache.page, off = (stage * kStage + (t & (kStage - 1))) & (P - 1);
+        const uint8_t* blk = p.cache.blocks + ((uint32_t)page[j] * (uint32_t)p.cache.heads + s.head) *
+                                                  (uint64_t)p.cache.block_bytes;
+        const uint4* src = reinterpret_cast<const uint4*>(blk + (part * P + off) * (D / 2));
 #pragma unroll
-      for (int i = 0; i < W; ++i)
-        vw[i] = live_next ? __ldg(reinterpret_cast<const uint4*>(vsrc) + i) : make_uint4(0, 0, 0, 0);
-      vpar = vpar_next;
-      live = live_next;
+        for (int i = 0; i < W; ++i) cw[j][i] = __ldg(src + i);
+        par[j] = __ldg(reinterpret_cast<const uint32_t*>(blk + P * D) + part * P + off);
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) cw[j][i] = make_uint4(0, 0, 0, 0);
+      }
     };
     bool ok = true, more = walk.next(p, &sg);
     int stage = more ? sg.s0 : 0;
-    int page = -1, page2 = -1;
-    PSegment nx = sg;      // where the stage after this one lies
-    int nstage = stage;
-    auto advance = [&](PSegment& s, int& at) -> bool {  // the next stage of the block's work
-      if (at + 1 < s.s1) {
-        ++at;
+    auto advance = [&]() -> bool {  // to the next stage of the block's work
+      if (stage + 1 < sg.s1) {
+        ++stage;
         return true;
       }
-      if (!walk.next(p, &s)) return false;
-      at = s.s0;
+      if (!walk.next(p, &sg)) return false;
+      stage = sg.s0;
       return true;
     };
-    bool have2 = false;
     if (more) {
-      page = page_of(sg, stage);
-      load_k(sg, stage, page);
-      load_v();
-      have2 = advance(nx, nstage);
-      if (have2) page2 = page_of(nx, nstage);
+      rows_page(sg, stage, true);
+#pragma unroll
+      for (int j = 0; j < ROUNDS; ++j) load(j, sg, stage);
     }
-    const uint32_t row = (uint32_t)tk * 128u, sw = (uint32_t)(tk & 7);
-    while (ok && more) {
+    while (more) {
+      // (sg, stage) move on to the stage after the one whose codes are here
+      more = advance();
+      rows_page(sg, stage, more);
       const int ks = it % KD, vs = it % VD, ts = it % TD;
-      // the softmax's constants of this token
       ok = mbar_wait_long(&bar->t_empty[ts], ((it / TD) & 1) ^ 1, 0x311) &&
            mbar_wait_long(&bar->k_empty[ks], ((it / KD) & 1) ^ 1, 0x312);
-      if (!ok) break;
-      {
-        const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(&kpar));
-        const float2 vp = __half22float2(*reinterpret_cast<const __half2*>(&vpar));
-        const float vsc = fmaxf(vp.x, 5.9604644775390625e-8f), rc = __fdividef(1.0f, vsc);
+      bool vok = false;
+#pragma unroll
+      for (int j = 0; j < ROUNDS; ++j) {
+        const int t = j * N + me, tk = t & (kStage - 1);
+        if (!ok || (t & ~31) >= 2 * kStage) break;
+        const bool val = t >= kStage;
+        if (val && !vok) {
+          ok = vok = mbar_wait_long(&bar->v_empty[vs], ((it / VD) & 1) ^ 1, 0x313);
+          if (!ok) break;
+        }
+        // the softmax's constants of this token; no token: its logit is
+        // -infinity whatever the row
+        const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&par[j]));
         const uint32_t tab = smem_u32(st + ts * C::TABLE) + (tk & 1) * 4;
         const uint32_t t1 = tab + (tk >> 1) * 16, t2 = t1 + kStage * 8, t3 = tab + kStage * 16 + (tk >> 1) * 8;
-        // no token: its logit is -infinity whatever the row
-        sts_f32(t1, live ? kp.x * (p.scale_log2 * 16777216.0f) : 0.f);
-        sts_f32(t1 + 8, live ? kp.y * p.scale_log2 : 0.f);
-        sts_f32(t2, live ? lg2(vsc) : -INFINITY);
-        sts_f32(t2 + 8, live ? rc : 0.f);
-        sts_f32(t3, live ? fmaf(rc, vp.y, 8.0f) : 0.f);  // the value codes are centred: c - 8
-      }
-      const uint32_t kb = smem_u32(sk + ks * C::TILE) + row;
+        const uint32_t dst = smem_u32((val ? sv + vs * C::TILE : sk + ks * C::TILE)) + (uint32_t)tk * 128u;
+        const uint32_t sw = (uint32_t)(tk & 7);
+        if (!val) {
+          sts_f32(t1, sb.x * (p.scale_log2 * 16777216.0f));
+          sts_f32(t1 + 8, sb.y * p.scale_log2);
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const uint32_t w4[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
+          for (int i = 0; i < W; ++i) {
+            const uint32_t w4[4] = {cw[j][i].x, cw[j][i].y, cw[j][i].z, cw[j][i].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w = w4[j], c = 4 * i + j;  // 8-channel piece c
-          sts128(kb + (c >> 3) * C::BLOCK + (((c & 7) ^ sw) << 4), w & 0x000F000Fu, (w >> 4) & 0x000F000Fu,
-                 (w >> 8) & 0x000F000Fu, (w >> 12) & 0x000F000Fu);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t w = w4[k], c = 4 * i + k;  // 8-channel piece c
+              sts128(dst + (c >> 3) * C::BLOCK + (((c & 7) ^ sw) << 4), w & 0x000F000Fu, (w >> 4) & 0x000F000Fu,
+                     (w >> 8) & 0x000F000Fu, (w >> 12) & 0x000F000Fu);
+            }
+          }
+        } else {
+          const float vsc = fmaxf(sb.x, 5.9604644775390625e-8f), rc = __fdividef(1.0f, vsc);
+          sts_f32(t2, live[j] ? lg2(vsc) : -INFINITY);
+          sts_f32(t2 + 8, live[j] ? rc : 0.f);
+          sts_f32(t3, live[j] ? fmaf(rc, sb.y, 8.0f) : 0.f);  // the value codes are centred: c - 8
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            const uint32_t w4[4] = {cw[j][i].x, cw[j][i].y, cw[j][i].z, cw[j][i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t w = w4[k], x = w >> 8, c = 4 * i + k;
+              // (c - 8) 2^-24, exact; odd channels enter 16 times too large, which the output takes back
+              sts128(dst + (c >> 3) * C::BLOCK + (((c & 7) ^ sw) << 4), hsub2u(w & 0x000F000Fu, 0x00080008u),
+                     hsub2u(w & 0x00F000F0u, 0x00800080u), hsub2u(x & 0x000F000Fu, 0x00080008u),
+                     hsub2u(x & 0x00F000F0u, 0x00800080u));
+            }
+          }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(val ? &bar->v_full[vs] : &bar->k_full[ks]);
+        load(j, sg, stage);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->k_full[ks]);
-      // keys of the next stage, and the page of the one after it
-      more = have2;
-      if (more) {
-        load_k(nx, nstage, page2);
-        have2 = advance(nx, nstage);
-        page2 = have2 ? page_of(nx, nstage) : -1;
-      }
-      ok = mbar_wait_long(&bar->v_empty[vs], ((it / VD) & 1) ^ 1, 0x313);
       if (!ok) break;
-      const uint32_t vb = smem_u32(sv + vs * C::TILE) + row;
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const uint32_t w4[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w = w4[j], x = w >> 8, c = 4 * i + j;
-          // (c - 8) 2^-24, exact; odd channels enter 16 times too large, which the output takes back
-          sts128(vb + (c >> 3) * C::BLOCK + (((c & 7) ^ sw) << 4), hsub2u(w & 0x000F000Fu, 0x00080008u),
-                 hsub2u(w & 0x00F000F0u, 0x00800080u), hsub2u(x & 0x000F000Fu, 0x00080008u),
-                 hsub2u(x & 0x00F000F0u, 0x00800080u));
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->v_full[vs]);
-      if (more) load_v();
       ++it;
     }
+  } else if (warp >= 8) {
+    // ---------------- MMA issue (one warp, converged) ----------------
+    {
+      bool ok = true;
+      uint32_t q_seg[2] = {0, 0}, stages[2] = {0, 0};  // of each tile so far: the phases of q_full, p_full
+      auto wait = [&](uint64_t* b, uint32_t parity, uint32_t where) -> bool {
+        const bool there = mbar_wait_long(b, parity, where);
+        return __all_sync(0xffffffffu, there);
+      };
+      auto issue_s = [&](uint32_t tile, uint32_t slot, uint32_t half) {
+        const uint64_t a0 = sw128_desc(smem_u32(sq) + tile * C::TILE);
+        const uint64_t b0 = sw128_desc(smem_u32(sk) + slot * C::TILE + half * (kHalf * 128));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = ((kk >> 2) * C::BLOCK + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + kStage * tile + kHalf * half, a0 + o, b0 + o, kIdescS, kk != 0);
+        }
+        commit(smem_u32(&bar->s_full[0][0]) + 16 * tile + 8 * half);
+      };
+      // MMAs of one thread run in order, so the S issued next may overwrite the weights this one reads
+      auto issue_o = [&](uint32_t tile, uint32_t slot, uint32_t half, uint32_t accum) {
+        const uint64_t b0 = sw128_desc_n(smem_u32(sv) + slot * C::TILE + half * (kHalf * 128), C::BLOCK);
+#pragma unroll
+        for (int kk = 0; kk < kHalf / 16; ++kk)
+          mma_ts(tmem + 2 * kStage + D * tile, tmem + kStage * tile + kHalf * half + kk * 8, b0 + kk * (2048 >> 4),
+                 kIdescO<D>, kk ? 1u : accum);
+        commit(smem_u32(&bar->o_done[0][0]) + 16 * tile + 8 * half);
+      };
+      while (ok && walk.next(p, &sg)) {
+        const uint32_t tiles = uniform(sg.rows > kRows ? 2 : 1), T = uniform(sg.s1 - sg.s0);
+        it = uniform(it);
+        ok = wait(&bar->k_full[it % KD], (it / KD) & 1, 0x321);
+        for (uint32_t i = 0; i < tiles && ok; ++i) {
+          ok = wait(&bar->q_full[i], q_seg[i] & 1, 0x322);
+          ++q_seg[i];
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(i, it % KD, 0);
+          issue_s(i, it % KD, 1);
+        }
+        if (!ok) break;
+        commit(smem_u32(&bar->k_empty[0]) + 8 * (it % KD));
+        for (uint32_t s = 0; s < T && ok; ++s, ++it) {
+          const bool next = s + 1 < T;
+          ok = wait(&bar->v_full[it % VD], (it / VD) & 1, 0x324) &&
+               (!next || wait(&bar->k_full[(it + 1) % KD], ((it + 1) / KD) & 1, 0x323));
+#pragma unroll 1
+          for (uint32_t half = 0; half < 2; ++half) {
+#pragma unroll 1
+            for (uint32_t i = 0; i < tiles && ok; ++i) {
+              ok = wait(&bar->p_full[i][half], stages[i] & 1, 0x325);
+              stages[i] += half;
+              if (!ok) break;
+              tc_fence_after();
+              issue_o(i, it % VD, half, s || half ? 1u : 0u);
+              if (next) issue_s(i, (it + 1) % KD, half);
+            }
+          }
+          if (!ok) break;
+          commit(smem_u32(&bar->v_empty[0]) + 8 * (it % VD));
+          if (next) commit(smem_u32(&bar->k_empty[0]) + 8 * ((it + 1) % KD));
+        }
+      }
+    }
   } else {
-    // ---------------- softmax, and its tile's MMAs ----------------
+    // ---------------- softmax ----------------
     const int tile = warp >> 2, quarter = warp & 3;
     const int r = lane >> 2, qd = lane & 3;
-    const bool leader = quarter == 0 && lane == 0;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-    const uint32_t ts_addr = lanes + kStage * tile;              // S, and the weights over it
+    const uint32_t ts_tile = lanes + kStage * tile;              // S of the two halves, and the weights over them
     const uint32_t to_addr = lanes + 2 * kStage + D * tile;      // O
-    uint32_t done = 0;  // stages of this tile so far: the phases of s_full and o_done
-    // A wait that gave up ends waiting and issuing for good, but nothing else:
-    // every warp still comes to every barrier.
+    uint32_t done = 0;  // halves of this tile so far: two give the barriers of a half their next phase
+    // A wait that gave up ends waiting for good, but nothing else.
     bool ok = true;
-    // S of stage `at` (leader only)
-    auto issue_s = [&](uint32_t at) -> bool {
-      if (!mbar_wait_long(&bar->k_full[at % KD], (at / KD) & 1, 0x321)) return false;
-      tc_fence_after();
-      const uint32_t a0 = smem_u32(sq + tile * C::TILE), b0 = smem_u32(sk + (at % KD) * C::TILE);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t o = (kk >> 2) * C::BLOCK + (kk & 3) * 32;
-        mma_ss(tmem + kStage * tile, sw128_desc(a0 + o), sw128_desc(b0 + o), kIdescS, kk != 0);
-      }
-      umma_commit(&bar->s_full[tile]);
-      umma_commit(&bar->k_empty[at % KD]);
-      return true;
-    };
-    // O += P V of stage `at` (leader only).  MMAs of one thread run in order, so
-    // the S that follows may overwrite the weights this one reads.
-    auto issue_o = [&](uint32_t at, bool begin) -> bool {
-      if (!mbar_wait_long(&bar->v_full[at % VD], (at / VD) & 1, 0x324)) return false;
-      tc_fence_after();
-      const uint32_t b0 = smem_u32(sv + (at % VD) * C::TILE);
-#pragma unroll
-      for (int kk = 0; kk < kStage / 16; ++kk)
-        mma_ts(tmem + 2 * kStage + D * tile, tmem + kStage * tile + kk * 8, sw128_desc_n(b0 + kk * 2048, C::BLOCK),
-               kIdescO<D>, !(begin && kk == 0));
-      umma_commit(&bar->o_done[tile]);
-      umma_commit(&bar->v_empty[at % VD]);
-      return true;
-    };
     while (walk.next(p, &sg)) {
       const KvRequest rq = sg.rq;
       const int rows = min(kRows, sg.rows - kRows * tile);  // of this tile; below 1: none
       const int base_pos = rq.len - rq.q_len;
-      if (rows <= 0) {  // the tile is empty: only let the rings go on
+      if (rows <= 0) {  // the tile is empty: only let the tables go on
         for (int s = sg.s0; s < sg.s1; ++s, ++it) {
           ok = ok && mbar_wait_long(&bar->k_full[it % KD], (it / KD) & 1, 0x331) &&
-               mbar_wait_long(&bar->v_full[it % VD], (it / VD) & 1, 0x336);
+               mbar_wait_long(&bar->v_full[it % VD], (it / VD) & 1, 0x337);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar->t_empty[it % TD]);
-          if (leader) {
-            mbar_arrive(&bar->k_empty[it % KD]);
-            mbar_arrive(&bar->v_empty[it % VD]);
-          }
         }
         continue;
       }
@@ -574,10 +620,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
                  prmt(v.y, v.w, 0x5410), prmt(v.y, v.w, 0x7632));
         }
         fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->q_full[tile]);
       }
-      named_barrier(1 + tile, 128);
-      if (leader && ok) ok = issue_s(it);
-      __syncwarp();
       float qs[4], m[4];
       float2 l[4], beta[4];  // by even and odd columns
       int pos[4];
@@ -593,13 +638,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       const int all_lo =
           p.window > 0 ? base_pos + (sg.row0 + kRows * tile + rows - 1) / p.share - p.window + 1 : 0;
 
-      for (int s = sg.s0; s < sg.s1; ++s, ++it, ++done) {
-        ok = ok && mbar_wait_long(&bar->k_full[it % KD], (it / KD) & 1, 0x332) &&  // the table, written before the keys
-             mbar_wait_long(&bar->s_full[tile], done & 1, 0x333);
+      const int h1 = 2 * sg.s1;
+      for (int h = 2 * sg.s0; h < h1; ++h, ++done) {  // halves of stages
+        const int half = h & 1, key0 = h * kHalf;
+        ok = ok && mbar_wait_long(&bar->k_full[it % KD], (it / KD) & 1, 0x332) &&  // the table is written with the tiles
+             mbar_wait_long(&bar->v_full[it % VD], (it / VD) & 1, 0x336) &&
+             mbar_wait_long(&bar->s_full[tile][half], (done >> 1) & 1, 0x333);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
-        const uint32_t tab = smem_u32(st + (it % TD) * C::TABLE) + qd * 16, tab3 = tab + kStage * 16 - qd * 8;
-        const bool edge = s * kStage < all_lo || (s + 1) * kStage > all_hi;
+        const uint32_t tab = smem_u32(st + (it % TD) * C::TABLE) + half * (kHalf * 8) + qd * 16;
+        const uint32_t tab3 = smem_u32(st + (it % TD) * C::TABLE) + kStage * 16 + half * (kHalf * 4) + qd * 8;
+        const uint32_t ts_addr = ts_tile + kHalf * half;
+        const bool edge = key0 < all_lo || key0 + kHalf > all_hi;
 
         // 32 columns: v holds [rows r, r + 8 | rows r + 16, r + 24]
         auto load = [&](int c, float(&v)[2][16]) {
@@ -633,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 float* x = &v[y >> 1][4 * k + 2 * (y & 1)];
-                const int key = s * kStage + 32 * c + 8 * k + 2 * qd;
+                const int key = key0 + 32 * c + 8 * k + 2 * qd;
                 const int from = p.window > 0 ? pos[y] - p.window : -1;
                 if (key > pos[y] || key <= from) x[0] = -INFINITY;
                 if (key + 1 > pos[y] || key + 1 <= from) x[1] = -INFINITY;
@@ -679,8 +729,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
                 tmem_st_16x128(ts_addr + 16 * b + ((16u * h) << 16), pw);
               }
             }
-            if (s > sg.s0) {
-              ok = ok && mbar_wait_long(&bar->o_done[tile], (done - 1) & 1, 0x334);
+            if (h > 2 * sg.s0) {
+              ok = ok && mbar_wait_long(&bar->o_done[tile][half ^ 1], ((done - 1) >> 1) & 1, 0x334);
               ok = __all_sync(0xffffffffu, ok);
               tc_fence_after();
 #pragma unroll 1
@@ -716,28 +766,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           tmem_st_16x128(ts_addr + 16 * c, pw[0]);
           tmem_st_16x128(ts_addr + 16 * c + (16u << 16), pw[1]);
         };
-        float va[2][16], vb[2][16];  // the next 32 columns are on their way while 32 are worked on
+        float va[2][16], vb[2][16];  // the second 32 columns are on their way while the first are worked on
         load(0, va);
         wait(va);
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          load(c + 1, vb);
-          work(c, va);
-          wait(vb);
-          if (c == 0) load(2, va);
-          work(c + 1, vb);
-          if (c == 0) wait(va);
-        }
+        load(1, vb);
+        work(0, va);
+        wait(vb);
+        work(1, vb);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->t_empty[it % TD]);
-        named_barrier(1 + tile, 128);
-        if (leader && ok) {
-          ok = issue_o(it, s == sg.s0);
-          if (ok && s + 1 < sg.s1) ok = issue_s(it + 1);
+        if (lane == 0) {
+          mbar_arrive(&bar->p_full[tile][half]);
+          if (half) mbar_arrive(&bar->t_empty[it % TD]);
         }
-        ok = __all_sync(0xffffffffu, ok);
+        it += half;
       }
 
       // ---- the item's end: sums of the quads, then a thread to a row ----
@@ -763,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           mr = c;
         }
       }
-      ok = ok && mbar_wait_long(&bar->o_done[tile], (done - 1) & 1, 0x335);
+      ok = ok && mbar_wait_long(&bar->o_done[tile][1], ((done - 1) >> 1) & 1, 0x335);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const bool whole = sg.first && sg.last;
