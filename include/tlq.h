@@ -688,6 +688,7 @@ tlq_status tl_kv4_read(const tl_kv4_cache* cache, const int64_t* slots, int toke
  *             which tl_kv4_append has put into the cache.  Entries that no
  *             visible token lies in are not read as pages; a page id outside
  *             the cache counts as holding no tokens
+ *             A request's context is at most 2^30 tokens
  *   tokens    rows of q; queries outside [0, tokens) count as none, rows of
  *             no request are not written
  *   max_q     the most queries that a request has (an upper bound will do;

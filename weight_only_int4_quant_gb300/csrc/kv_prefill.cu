@@ -59,7 +59,7 @@ constexpr float kNone = -1e30f;
 
 template <int D>
 struct PCfg {
-  static constexpr int KD = 2, VD = 2, TD = 2;  // stages of keys, values and tables
+  static constexpr int KD = 2, VD = 2, TD = 3;  // stages of keys, values and tables
   static constexpr int BLOCK = kStage * 128;    // 128 rows of 64 channels
   static constexpr int TILE = BLOCK * (D / 64);
   // tables: per pair of tokens (A0 A1 B0 B1), (lg0 lg1 rc0 rc1), (rb0 rb1)
@@ -216,22 +216,11 @@ __device__ __forceinline__ void tmem_st_16x128(uint32_t addr, const uint32_t* v)
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void tmem_ld_16x128(uint32_t addr, uint32_t* v) {
-  asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "r"(addr));
-}
 // The waits name the registers that the loads fill, so that nothing reads them earlier.
 __device__ __forceinline__ void tmem_wait_ld(float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
                  "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld(uint32_t* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
                :
                : "memory");
 }
@@ -322,7 +311,7 @@ struct PBars {
   uint64_t o_done[2][2];           // by tile and half: P V complete
   uint64_t k_full[2], k_empty[2];  // written (4 warps), read
   uint64_t v_full[2], v_empty[2];
-  uint64_t t_empty[2];             // table read (8 warps)
+  uint64_t t_empty[3];             // table read (8 warps)
   uint32_t tmem;
 };
 
@@ -354,8 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       mbar_init(&bar->k_empty[i], 1);
       mbar_init(&bar->v_full[i], 4);
       mbar_init(&bar->v_empty[i], 1);
-      mbar_init(&bar->t_empty[i], 8);
     }
+    for (int i = 0; i < TD; ++i) mbar_init(&bar->t_empty[i], 8);
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(&bar->tmem, 512);
@@ -452,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       more = advance();
       rows_page(sg, stage, more);
       const int ks = it % KD, vs = it % VD, ts = it % TD;
-      ok = mbar_wait_long(&bar->t_empty[ts], ((it / TD) & 1) ^ 1, 0x311) &&
-           mbar_wait_long(&bar->k_empty[ks], ((it / KD) & 1) ^ 1, 0x312);
+      ok = mbar_wait_long(&bar->t_empty[ts], ((it / TD) & 1) ^ 1, 0x311, 100) &&
+           mbar_wait_long(&bar->k_empty[ks], ((it / KD) & 1) ^ 1, 0x312, 100);
       bool vok = false;
 #pragma unroll
       for (int j = 0; j < ROUNDS; ++j) {
@@ -461,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
         if (!ok || (t & ~31) >= 2 * kStage) break;
         const bool val = t >= kStage;
         if (val && !vok) {
-          ok = vok = mbar_wait_long(&bar->v_empty[vs], ((it / VD) & 1) ^ 1, 0x313);
+          ok = vok = mbar_wait_long(&bar->v_empty[vs], ((it / VD) & 1) ^ 1, 0x313, 100);
           if (!ok) break;
         }
         // the softmax's constants of this token; no token: its logit is
@@ -638,66 +627,72 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       const int all_lo =
           p.window > 0 ? base_pos + (sg.row0 + kRows * tile + rows - 1) / p.share - p.window + 1 : 0;
 
-      const int h1 = 2 * sg.s1;
-      for (int h = 2 * sg.s0; h < h1; ++h, ++done) {  // halves of stages
-        const int half = h & 1, key0 = h * kHalf;
+      for (int s = sg.s0; s < sg.s1; ++s, ++it) {
         ok = ok && mbar_wait_long(&bar->k_full[it % KD], (it / KD) & 1, 0x332) &&  // the table is written with the tiles
-             mbar_wait_long(&bar->v_full[it % VD], (it / VD) & 1, 0x336) &&
-             mbar_wait_long(&bar->s_full[tile][half], (done >> 1) & 1, 0x333);
-        ok = __all_sync(0xffffffffu, ok);
-        tc_fence_after();
-        const uint32_t tab = smem_u32(st + (it % TD) * C::TABLE) + half * (kHalf * 8) + qd * 16;
-        const uint32_t tab3 = smem_u32(st + (it % TD) * C::TABLE) + kStage * 16 + half * (kHalf * 4) + qd * 8;
-        const uint32_t ts_addr = ts_tile + kHalf * half;
-        const bool edge = key0 < all_lo || key0 + kHalf > all_hi;
-
-        // 32 columns: v holds [rows r, r + 8 | rows r + 16, r + 24]
-        auto load = [&](int c, float(&v)[2][16]) {
-          tmem_ld_16x256(ts_addr + 32 * c, v[0]);
-          tmem_ld_16x256(ts_addr + 32 * c + (16u << 16), v[1]);
-        };
-        auto wait = [&](float(&v)[2][16]) {
-          tmem_wait_ld(v[0]);
-          tmem_wait_ld(v[1]);
-        };
-        auto work = [&](int c, float(&v)[2][16]) {
-          float2 rc[4];
+             mbar_wait_long(&bar->v_full[it % VD], (it / VD) & 1, 0x336);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half, ++done) {
+          const int key0 = s * kStage + half * kHalf;
+          ok = ok && mbar_wait_long(&bar->s_full[tile][half], (done >> 1) & 1, 0x333);
+          ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+          const uint32_t tab = smem_u32(st + (it % TD) * C::TABLE) + half * (kHalf * 8) + qd * 16;
+          const uint32_t tab3 = smem_u32(st + (it % TD) * C::TABLE) + kStage * 16 + half * (kHalf * 4) + qd * 8;
+          const uint32_t ts_addr = ts_tile + kHalf * half;
+          // v[c][0]: columns 32 c .. of rows r, r + 8; v[c][1]: of rows r + 16, r + 24
+          float v[2][2][16];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld_16x256(ts_addr + 32 * c, v[c][0]);
+            tmem_ld_16x256(ts_addr + 32 * c + (16u << 16), v[c][1]);
+          }
+          float2 rc[2][4];
           float top[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {  // column pair 32 c + 8 k + 2 qd
-            const float4 ab = lds_f32x4(tab + (16 * c + 4 * k) * 16);
-            const float4 lr = lds_f32x4(tab + (16 * c + 4 * k) * 16 + kStage * 8);
-            rc[k] = make_float2(lr.z, lr.w);
+          for (int c = 0; c < 2; ++c) {
+            tmem_wait_ld(v[c][0]);
+            tmem_wait_ld(v[c][1]);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              float* x = &v[y >> 1][4 * k + 2 * (y & 1)];
-              const float2 z = fma2(make_float2(x[0], x[1]), make_float2(ab.x, ab.y),
-                                    fma2(make_float2(qs[y], qs[y]), make_float2(ab.z, ab.w), make_float2(lr.x, lr.y)));
-              x[0] = z.x;
-              x[1] = z.y;
-            }
-          }
-          if (edge) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 4; ++k) {  // column pair 32 c + 8 k + 2 qd
+              const float4 ab = lds_f32x4(tab + (16 * c + 4 * k) * 16);
+              const float4 lr = lds_f32x4(tab + (16 * c + 4 * k) * 16 + kStage * 8);
+              rc[c][k] = make_float2(lr.z, lr.w);
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                float* x = &v[y >> 1][4 * k + 2 * (y & 1)];
-                const int key = key0 + 32 * c + 8 * k + 2 * qd;
-                const int from = p.window > 0 ? pos[y] - p.window : -1;
-                if (key > pos[y] || key <= from) x[0] = -INFINITY;
-                if (key + 1 > pos[y] || key + 1 <= from) x[1] = -INFINITY;
+                float* x = &v[c][y >> 1][4 * k + 2 * (y & 1)];
+                const float2 z =
+                    fma2(make_float2(x[0], x[1]), make_float2(ab.x, ab.y),
+                         fma2(make_float2(qs[y], qs[y]), make_float2(ab.z, ab.w), make_float2(lr.x, lr.y)));
+                x[0] = z.x;
+                x[1] = z.y;
               }
+            }
+          }
+          if (key0 < all_lo || key0 + kHalf > all_hi) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int to = pos[y] - key0 - 2 * qd;  // the last column that row y sees, counted from this thread's first
+              const int from = p.window > 0 ? to - p.window : -kStage;  // and the one before the first
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int col = 8 * (e >> 1) + (e & 1);
+                float* x = &v[e >> 3][y >> 1][4 * ((e >> 1) & 3) + 2 * (y & 1) + (e & 1)];
+                if (col > to || col <= from) *x = -INFINITY;
+              }
+            }
           }
           bool over = false;
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const float* x = &v[y >> 1][2 * (y & 1)];
-            top[y] = max3(max3(max3(x[0], x[1], x[4]), x[5], x[8]), max3(x[9], x[12], x[13]), kNone);
+            const float* x = &v[0][y >> 1][2 * (y & 1)];
+            const float* z = &v[1][y >> 1][2 * (y & 1)];
+            top[y] = max3(max3(max3(x[0], x[1], x[4]), max3(x[5], x[8], x[9]), max3(x[12], x[13], z[0])),
+                          max3(z[1], z[4], z[5]), max3(max3(z[8], z[9], z[12]), z[13], kNone));
             over |= top[y] > m[y] + kTrigger;
           }
           if (__any_sync(0xffffffffu, over)) {
-            // a new reference: sums, weights already written and O move with it
+            // a new reference: the sums and O move with it (the weights of the
+            // other half are in O by now, or will have been added before it moves)
             float w[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -712,24 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
               beta[y].x *= w[y];
               beta[y].y *= w[y];
             }
-#pragma unroll 1
-            for (int b = 0; b < c; ++b) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t pw[8];
-                tmem_ld_16x128(ts_addr + 16 * b + ((16u * h) << 16), pw);
-                tmem_wait_ld(pw);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float f = w[2 * h + (k & 1)];
-                  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&pw[k]));
-                  const __half2 y = __floats2half2_rn(x.x * f, x.y * f);
-                  pw[k] = *reinterpret_cast<const uint32_t*>(&y);
-                }
-                tmem_st_16x128(ts_addr + 16 * b + ((16u * h) << 16), pw);
-              }
-            }
-            if (h > 2 * sg.s0) {
+            if (s > sg.s0 || half) {
               ok = ok && mbar_wait_long(&bar->o_done[tile][half ^ 1], ((done - 1) >> 1) & 1, 0x334);
               ok = __all_sync(0xffffffffu, ok);
               tc_fence_after();
@@ -748,39 +726,32 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
             }
           }
           // weights
-          uint32_t pw[2][8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 rb = lds_f32x2(tab3 + (16 * c + 4 * k) * 8);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pw[2][8];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float* x = &v[y >> 1][4 * k + 2 * (y & 1)];
-              const float2 a = add2(make_float2(x[0], x[1]), make_float2(-m[y], -m[y]));
-              const float2 e = make_float2(ex2(a.x), ex2(a.y));
-              const __half2 h2 = __floats2half2_rn(e.x, e.y);
-              pw[y >> 1][2 * k + (y & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
-              l[y] = fma2(e, rc[k], l[y]);
-              beta[y] = fma2(e, rb, beta[y]);
+            for (int k = 0; k < 4; ++k) {
+              const float2 rb = lds_f32x2(tab3 + (16 * c + 4 * k) * 8);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float* x = &v[c][y >> 1][4 * k + 2 * (y & 1)];
+                const float2 a = add2(make_float2(x[0], x[1]), make_float2(-m[y], -m[y]));
+                const float2 e = make_float2(ex2(a.x), ex2(a.y));
+                const __half2 h2 = __floats2half2_rn(e.x, e.y);
+                pw[y >> 1][2 * k + (y & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
+                l[y] = fma2(e, rc[c][k], l[y]);
+                beta[y] = fma2(e, rb, beta[y]);
+              }
             }
+            tmem_st_16x128(ts_addr + 16 * c, pw[0]);
+            tmem_st_16x128(ts_addr + 16 * c + (16u << 16), pw[1]);
           }
-          tmem_st_16x128(ts_addr + 16 * c, pw[0]);
-          tmem_st_16x128(ts_addr + 16 * c + (16u << 16), pw[1]);
-        };
-        float va[2][16], vb[2][16];  // the second 32 columns are on their way while the first are worked on
-        load(0, va);
-        wait(va);
-        load(1, vb);
-        work(0, va);
-        wait(vb);
-        work(1, vb);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar->p_full[tile][half]);
-          if (half) mbar_arrive(&bar->t_empty[it % TD]);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->p_full[tile][half]);
         }
-        it += half;
+        if (lane == 0) mbar_arrive(&bar->t_empty[it % TD]);
       }
 
       // ---- the item's end: sums of the quads, then a thread to a row ----

@@ -34,6 +34,9 @@ struct KvBatch {
   int requests, tokens, max_q;
 };
 
+// The longest context (positions and windows stay far from 32-bit limits).
+constexpr long long kMaxContext = 1ll << 30;
+
 struct KvRequest {
   int q0, q_len, len;
 };
@@ -46,7 +49,7 @@ __device__ __forceinline__ KvRequest kv_request(const KvBatch& b, int page, int 
   const int q1 = b.q_start[i + 1];
   r.q_len = (r.q0 >= 0 && q1 >= r.q0 && q1 <= b.tokens) ? min(q1 - r.q0, b.max_q) : 0;
   const long long room = (long long)b.ld_table * page;
-  r.len = (int)max(0ll, min((long long)b.seq_lens[i], min(room, 0x7fffff00ll)));
+  r.len = (int)max(0ll, min((long long)b.seq_lens[i], min(room, kMaxContext)));
   return r;
 }
 
@@ -122,29 +125,20 @@ struct UnitSearch {
   }
 };
 
-// mbar_wait for waits that last a stage or more: the hardware holds the thread
-// for up to 10 us at a try, so a waiting warp leaves the scheduler to the others
-// (without the hint waiting warps issued half of all instructions of the prompt
-// kernel).  Bounded like mbar_wait.
-__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, uint32_t where) {
-  auto held = [&] {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
-        : "memory");
-    return ok != 0;
-  };
-  if (held()) return true;
+// mbar_wait for waits that last a stage or more, with a pause between tries, so
+// that a waiting warp leaves the scheduler to the others (waiting warps issued a
+// third of the prompt kernel's instructions).  Bounded like mbar_wait.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, uint32_t where, uint32_t pause_ns = 20) {
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
-  while (!held()) {
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+  for (uint32_t i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    __nanosleep(pause_ns);
+    if ((i & 63u) == 63u && globaltimer_ns() - t0 > kWaitLimitNs) {
       record_timeout(where);
       return false;
     }
   }
-  return true;
 }
 
 // Launchers (arguments validated by the entry points).
