@@ -311,7 +311,7 @@ struct PBars {
   uint64_t o_done[2][2];           // by tile and half: P V complete
   uint64_t k_full[2], k_empty[2];  // written (4 warps), read
   uint64_t v_full[2], v_empty[2];
-  uint64_t t_empty[3];             // table read (8 warps)
+  uint64_t t_full[3], t_empty[3];  // table written (4 warps), read (8 warps)
   uint32_t tmem;
 };
 
@@ -328,6 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   PBars* const bar = reinterpret_cast<PBars*>(st + TD * C::TABLE);
   static_assert(sizeof(PBars) <= C::BARS, "barriers fit");
   __shared__ UnitSearch<kThreads> search;
+  // each warp's place in the block's work: in shared memory, since it is needed
+  // once an item and the softmax has no registers to spare
+  __shared__ PWalk walks[kThreads / 32];
+  __shared__ PSegment segments[kThreads / 32];
 
   const int tid = threadIdx.x, warp = (int)uniform(tid >> 5), lane = tid & 31;
   pdl_launch_dependents();
@@ -344,7 +348,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       mbar_init(&bar->v_full[i], 4);
       mbar_init(&bar->v_empty[i], 1);
     }
-    for (int i = 0; i < TD; ++i) mbar_init(&bar->t_empty[i], 8);
+    for (int i = 0; i < TD; ++i) {
+      mbar_init(&bar->t_full[i], 4);
+      mbar_init(&bar->t_empty[i], 8);
+    }
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(&bar->tmem, 512);
@@ -368,101 +375,125 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   const long long U = search.total;
   const long long n = min((long long)gridDim.x, U);
   const bool busy = (long long)blockIdx.x < n;
-  PWalk walk;
-  walk.u = walk.u_end = 0;
-  if (busy) {
-    walk.u = U * blockIdx.x / n;
-    walk.u_end = U * (blockIdx.x + 1) / n;
-    search.find(p.batch.requests, count, walk.u, own, mine);
-    if (search.request >= 0)
+  if (busy) search.find(p.batch.requests, count, U * blockIdx.x / n, own, mine);
+  if (lane == 0) {
+    PWalk& walk = walks[warp];
+    walk.u = walk.u_end = 0;
+    if (busy && search.request >= 0) {
+      walk.u = U * blockIdx.x / n;
+      walk.u_end = U * (blockIdx.x + 1) / n;
       walk.start(p, search.request, search.first);
-    else
-      walk.u_end = walk.u;  // not reached: u < U
+    }
   }
-  PSegment sg;
+  const PSegment& sg = segments[warp];
+  auto next_segment = [&]() -> bool {  // all lanes of a warp
+    __syncwarp();
+    const int there = lane == 0 ? (int)walks[warp].next(p, &segments[warp]) : 0;
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, there, 0) != 0;
+  };
   uint32_t it = 0;  // stages so far
 
   if (warp >= 8 && warp < 8 + kCodeWarps) {
     // ---------------- codes into the tiles ----------------
-    // The 256 rows of a stage, keys then values, go round the 96 threads: row
-    // 96 j + (thread) in round j; a warp's rows are all keys or all values.
+    // A step writes the keys of one stage and the values of the stage before it
+    // (S of a stage is formed during the softmax of the one before, its values
+    // are needed a stage later).  Their 256 rows, keys then values, go round the
+    // 96 threads: row 96 j + (thread) in round j; a warp's rows are all keys or
+    // all values.
     constexpr int W = D / 32;  // 16-byte pieces of a row of codes
     constexpr int ROUNDS = 3, N = 32 * kCodeWarps;
     static_assert(ROUNDS * N >= 2 * kStage && (2 * kStage) % 32 == 0, "rounds");
     const int me = tid - 8 * 32;
-    uint4 cw[ROUNDS][W];  // codes of the stage at hand, and of the next as rounds pass
-    uint32_t par[ROUNDS];
+    struct Place {
+      int req, head, lo, hi, stage;
+      bool have;
+    };
+    uint4 cw[ROUNDS][W];  // codes of the step at hand, then of the next
+    uint32_t kpar[2], vpar[2];  // of this thread's tokens: the rows of keys are in the first two rounds
     bool live[ROUNDS];
-    int page[ROUNDS];     // of the next stage's rows
-    auto rows_page = [&](const PSegment& s, int stage, bool have) {
+    int page[ROUNDS];     // of the next step's rows
+    auto pages = [&](const Place& kp, const Place& vp) {
 #pragma unroll
       for (int j = 0; j < ROUNDS; ++j) {
-        const int t = j * N + me, key = stage * kStage + (t & (kStage - 1));
-        page[j] = have && t < 2 * kStage && key >= s.lo && key < s.hi
-                      ? __ldg(p.batch.table + (size_t)s.req * p.batch.ld_table + (key >> p.cache.page_shift))
+        const int t = j * N + me;
+        const Place& at = t < kStage ? kp : vp;
+        const int key = at.stage * kStage + (t & (kStage - 1));
+        page[j] = at.have && t < 2 * kStage && key >= at.lo && key < at.hi
+                      ? __ldg(p.batch.table + (size_t)at.req * p.batch.ld_table + (key >> p.cache.page_shift))
                       : -1;
       }
     };
-    auto load = [&](int j, const PSegment& s, int stage) {
-      live[j] = page[j] >= 0 && page[j] < p.cache.num_pages;
-      par[j] = 0;
-      if (live[j]) {
-        const int t = j * N + me, part = t >> 7;
-        const int P = p.cache.page, off = (stage * kStage + (t & (kStage - 1))) & (P - 1);
-        const uint8_t* blk = p.cache.blocks + ((uint32_t)page[j] * (uint32_t)p.cache.heads + s.head) *
-                                                  (uint64_t)p.cache.block_bytes;
-        const uint4* src = reinterpret_cast<const uint4*>(blk + (part * P + off) * (D / 2));
+    auto load = [&](const Place& kp, const Place& vp) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) cw[j][i] = __ldg(src + i);
-        par[j] = __ldg(reinterpret_cast<const uint32_t*>(blk + P * D) + part * P + off);
-      } else {
+      for (int j = 0; j < ROUNDS; ++j) {
+        live[j] = page[j] >= 0 && page[j] < p.cache.num_pages;
+        if (j < 2) kpar[j] = vpar[j] = 0;
+        if (live[j]) {
+          const int t = j * N + me, part = t >> 7;
+          const Place& at = t < kStage ? kp : vp;
+          const int P = p.cache.page, off = (at.stage * kStage + (t & (kStage - 1))) & (P - 1);
+          const uint8_t* blk = p.cache.blocks + ((uint32_t)page[j] * (uint32_t)p.cache.heads + at.head) *
+                                                    (uint64_t)p.cache.block_bytes;
+          const uint4* src = reinterpret_cast<const uint4*>(blk + (part * P + off) * (D / 2));
 #pragma unroll
-        for (int i = 0; i < W; ++i) cw[j][i] = make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < W; ++i) cw[j][i] = __ldg(src + i);
+          if (j < 2 && part == 0) {
+            kpar[j] = __ldg(reinterpret_cast<const uint32_t*>(blk + P * D) + off);
+            vpar[j] = __ldg(reinterpret_cast<const uint32_t*>(blk + P * D) + P + off);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < W; ++i) cw[j][i] = make_uint4(0, 0, 0, 0);
+        }
       }
     };
-    bool ok = true, more = walk.next(p, &sg);
-    int stage = more ? sg.s0 : 0;
-    auto advance = [&]() -> bool {  // to the next stage of the block's work
-      if (stage + 1 < sg.s1) {
-        ++stage;
-        return true;
+    auto place = [&](bool have, int stage) { return Place{sg.req, sg.head, sg.lo, sg.hi, stage, have}; };
+    bool ok = true;
+    Place kp = place(next_segment(), 0), vp = kp;
+    if (kp.have) kp.stage = sg.s0;
+    vp.have = false;
+    pages(kp, vp);
+    load(kp, vp);
+    uint32_t kit = 0, vit = 0;  // stages of keys, of values so far
+    while (kp.have || vp.have) {
+      Place nk = kp;  // the stage of keys after this one
+      if (kp.have) {
+        if (kp.stage + 1 < sg.s1) {
+          ++nk.stage;
+        } else {
+          const bool more = next_segment();
+          nk = place(more, more ? sg.s0 : 0);
+        }
       }
-      if (!walk.next(p, &sg)) return false;
-      stage = sg.s0;
-      return true;
-    };
-    if (more) {
-      rows_page(sg, stage, true);
-#pragma unroll
-      for (int j = 0; j < ROUNDS; ++j) load(j, sg, stage);
-    }
-    while (more) {
-      // (sg, stage) move on to the stage after the one whose codes are here
-      more = advance();
-      rows_page(sg, stage, more);
-      const int ks = it % KD, vs = it % VD, ts = it % TD;
-      ok = mbar_wait_long(&bar->t_empty[ts], ((it / TD) & 1) ^ 1, 0x311, 100) &&
-           mbar_wait_long(&bar->k_empty[ks], ((it / KD) & 1) ^ 1, 0x312, 100);
-      bool vok = false;
+      pages(nk, kp);
+      const int ks = kit % KD, kt = kit % TD, vs = vit % VD;
+      if (kp.have)
+        ok = mbar_wait_long(&bar->t_empty[kt], ((kit / TD) & 1) ^ 1, 0x311, 100) &&
+             mbar_wait_long(&bar->k_empty[ks], ((kit / KD) & 1) ^ 1, 0x312, 100);
+      if (vp.have) ok = ok && mbar_wait_long(&bar->v_empty[vs], ((vit / VD) & 1) ^ 1, 0x313, 100);
+      if (!ok) break;
 #pragma unroll
       for (int j = 0; j < ROUNDS; ++j) {
         const int t = j * N + me, tk = t & (kStage - 1);
-        if (!ok || (t & ~31) >= 2 * kStage) break;
         const bool val = t >= kStage;
-        if (val && !vok) {
-          ok = vok = mbar_wait_long(&bar->v_empty[vs], ((it / VD) & 1) ^ 1, 0x313, 100);
-          if (!ok) break;
-        }
-        // the softmax's constants of this token; no token: its logit is
-        // -infinity whatever the row
-        const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&par[j]));
-        const uint32_t tab = smem_u32(st + ts * C::TABLE) + (tk & 1) * 4;
-        const uint32_t t1 = tab + (tk >> 1) * 16, t2 = t1 + kStage * 8, t3 = tab + kStage * 16 + (tk >> 1) * 8;
+        if ((t & ~31) >= 2 * kStage || !(val ? vp.have : kp.have)) continue;
         const uint32_t dst = smem_u32((val ? sv + vs * C::TILE : sk + ks * C::TILE)) + (uint32_t)tk * 128u;
         const uint32_t sw = (uint32_t)(tk & 7);
         if (!val) {
-          sts_f32(t1, sb.x * (p.scale_log2 * 16777216.0f));
-          sts_f32(t1 + 8, sb.y * p.scale_log2);
+          // the softmax's constants of this token, its value's among them: the
+          // softmax of a stage begins before the stage's values are here.  No
+          // token: its logit is -infinity whatever the row
+          const float2 kb = __half22float2(*reinterpret_cast<const __half2*>(&kpar[j & 1]));
+          const float2 vb = __half22float2(*reinterpret_cast<const __half2*>(&vpar[j & 1]));
+          const float vsc = fmaxf(vb.x, 5.9604644775390625e-8f), rc = __fdividef(1.0f, vsc);
+          const uint32_t tab = smem_u32(st + kt * C::TABLE) + (tk & 1) * 4;
+          const uint32_t t1 = tab + (tk >> 1) * 16, t2 = t1 + kStage * 8, t3 = tab + kStage * 16 + (tk >> 1) * 8;
+          sts_f32(t1, kb.x * (p.scale_log2 * 16777216.0f));
+          sts_f32(t1 + 8, kb.y * p.scale_log2);
+          sts_f32(t2, live[j] ? lg2(vsc) : -INFINITY);
+          sts_f32(t2 + 8, live[j] ? rc : 0.f);
+          sts_f32(t3, live[j] ? fmaf(rc, vb.y, 8.0f) : 0.f);  // the value codes are centred: c - 8
 #pragma unroll
           for (int i = 0; i < W; ++i) {
             const uint32_t w4[4] = {cw[j][i].x, cw[j][i].y, cw[j][i].z, cw[j][i].w};
@@ -474,10 +505,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
             }
           }
         } else {
-          const float vsc = fmaxf(sb.x, 5.9604644775390625e-8f), rc = __fdividef(1.0f, vsc);
-          sts_f32(t2, live[j] ? lg2(vsc) : -INFINITY);
-          sts_f32(t2 + 8, live[j] ? rc : 0.f);
-          sts_f32(t3, live[j] ? fmaf(rc, sb.y, 8.0f) : 0.f);  // the value codes are centred: c - 8
 #pragma unroll
           for (int i = 0; i < W; ++i) {
             const uint32_t w4[4] = {cw[j][i].x, cw[j][i].y, cw[j][i].z, cw[j][i].w};
@@ -491,13 +518,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
             }
           }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(val ? &bar->v_full[vs] : &bar->k_full[ks]);
-        load(j, sg, stage);
       }
-      if (!ok) break;
-      ++it;
+      load(nk, kp);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+#pragma unroll
+        for (int j = 0; j < ROUNDS; ++j) {
+          const int t = j * N + me;
+          const bool val = t >= kStage;
+          if (t >= 2 * kStage || !(val ? vp.have : kp.have)) continue;
+          mbar_arrive(val ? &bar->v_full[vs] : &bar->k_full[ks]);
+          if (!val) mbar_arrive(&bar->t_full[kt]);
+        }
+      }
+      kit += kp.have;
+      vit += vp.have;
+      vp = kp;
+      kp = nk;
     }
   } else if (warp >= 8) {
     // ---------------- MMA issue (one warp, converged) ----------------
@@ -527,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
                  kIdescO<D>, kk ? 1u : accum);
         commit(smem_u32(&bar->o_done[0][0]) + 16 * tile + 8 * half);
       };
-      while (ok && walk.next(p, &sg)) {
+      while (ok && next_segment()) {
         const uint32_t tiles = uniform(sg.rows > kRows ? 2 : 1), T = uniform(sg.s1 - sg.s0);
         it = uniform(it);
         ok = wait(&bar->k_full[it % KD], (it / KD) & 1, 0x321);
@@ -554,11 +592,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
               if (!ok) break;
               tc_fence_after();
               issue_o(i, it % VD, half, s || half ? 1u : 0u);
+              if (half && i + 1 == tiles) commit(smem_u32(&bar->v_empty[0]) + 8 * (it % VD));
               if (next) issue_s(i, (it + 1) % KD, half);
             }
           }
           if (!ok) break;
-          commit(smem_u32(&bar->v_empty[0]) + 8 * (it % VD));
           if (next) commit(smem_u32(&bar->k_empty[0]) + 8 * ((it + 1) % KD));
         }
       }
@@ -573,14 +611,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
     uint32_t done = 0;  // halves of this tile so far: two give the barriers of a half their next phase
     // A wait that gave up ends waiting for good, but nothing else.
     bool ok = true;
-    while (walk.next(p, &sg)) {
+    while (next_segment()) {
       const KvRequest rq = sg.rq;
       const int rows = min(kRows, sg.rows - kRows * tile);  // of this tile; below 1: none
       const int base_pos = rq.len - rq.q_len;
       if (rows <= 0) {  // the tile is empty: only let the tables go on
         for (int s = sg.s0; s < sg.s1; ++s, ++it) {
-          ok = ok && mbar_wait_long(&bar->k_full[it % KD], (it / KD) & 1, 0x331) &&
-               mbar_wait_long(&bar->v_full[it % VD], (it / VD) & 1, 0x337);
+          ok = ok && mbar_wait_long(&bar->t_full[it % TD], (it / TD) & 1, 0x331);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar->t_empty[it % TD]);
         }
@@ -613,14 +650,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
         if (lane == 0) mbar_arrive(&bar->q_full[tile]);
       }
       float qs[4], m[4];
-      float2 l[4], beta[4];  // by even and odd columns
+      float l[4], beta[4];
       int pos[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // rows r + 8 k of this warp's 32
         qs[k] = __shfl_sync(0xffffffffu, qsum, r + 8 * k);
         pos[k] = base_pos + (sg.row0 + min(kRows * tile + 32 * quarter + r + 8 * k, sg.rows - 1)) / p.share;
         m[k] = kNone;
-        l[k] = beta[k] = make_float2(0.f, 0.f);
+        l[k] = beta[k] = 0.f;
       }
       // keys below all_hi and from all_lo are seen by every row of the tile
       const int all_hi = base_pos + (sg.row0 + kRows * tile) / p.share + 1;
@@ -628,8 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           p.window > 0 ? base_pos + (sg.row0 + kRows * tile + rows - 1) / p.share - p.window + 1 : 0;
 
       for (int s = sg.s0; s < sg.s1; ++s, ++it) {
-        ok = ok && mbar_wait_long(&bar->k_full[it % KD], (it / KD) & 1, 0x332) &&  // the table is written with the tiles
-             mbar_wait_long(&bar->v_full[it % VD], (it / VD) & 1, 0x336);
+        ok = ok && mbar_wait_long(&bar->t_full[it % TD], (it / TD) & 1, 0x332);
 #pragma unroll 1
         for (int half = 0; half < 2; ++half, ++done) {
           const int key0 = s * kStage + half * kHalf;
@@ -702,10 +738,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
               const float next = fmaxf(m[y], x - kHeadroom);
               w[y] = ex2(m[y] - next);
               m[y] = next;
-              l[y].x *= w[y];
-              l[y].y *= w[y];
-              beta[y].x *= w[y];
-              beta[y].y *= w[y];
+              l[y] *= w[y];
+              beta[y] *= w[y];
             }
             if (s > sg.s0 || half) {
               ok = ok && mbar_wait_long(&bar->o_done[tile][half ^ 1], ((done - 1) >> 1) & 1, 0x334);
@@ -725,7 +759,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
               }
             }
           }
-          // weights
+          // weights, and this half's sums by even and odd columns
+          float2 lt[4], bt[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) lt[y] = bt[y] = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t pw[2][8];
@@ -739,8 +776,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
                 const float2 e = make_float2(ex2(a.x), ex2(a.y));
                 const __half2 h2 = __floats2half2_rn(e.x, e.y);
                 pw[y >> 1][2 * k + (y & 1)] = *reinterpret_cast<const uint32_t*>(&h2);
-                l[y] = fma2(e, rc[c][k], l[y]);
-                beta[y] = fma2(e, rb, beta[y]);
+                lt[y] = fma2(e, rc[c][k], lt[y]);
+                bt[y] = fma2(e, rb, bt[y]);
               }
             }
             tmem_st_16x128(ts_addr + 16 * c, pw[0]);
@@ -749,6 +786,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            l[y] += lt[y].x + lt[y].y;
+            beta[y] += bt[y].x + bt[y].y;
+          }
           if (lane == 0) mbar_arrive(&bar->p_full[tile][half]);
         }
         if (lane == 0) mbar_arrive(&bar->t_empty[it % TD]);
@@ -757,69 +799,99 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       // ---- the item's end: sums of the quads, then a thread to a row ----
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        l[k].x += l[k].y;
-        beta[k].x += beta[k].y;
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
-          l[k].x += __shfl_xor_sync(0xffffffffu, l[k].x, o);
-          beta[k].x += __shfl_xor_sync(0xffffffffu, beta[k].x, o);
-        }
-      }
-      float lr = 0.f, br = 0.f, mr = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float a = __shfl_sync(0xffffffffu, l[k].x, (lane & 7) * 4);
-        const float b = __shfl_sync(0xffffffffu, beta[k].x, (lane & 7) * 4);
-        const float c = __shfl_sync(0xffffffffu, m[k], (lane & 7) * 4);
-        if ((lane >> 3) == k) {
-          lr = a;
-          br = b;
-          mr = c;
+          l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
+          beta[k] += __shfl_xor_sync(0xffffffffu, beta[k], o);
         }
       }
       ok = ok && mbar_wait_long(&bar->o_done[tile][1], ((done - 1) >> 1) & 1, 0x335);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const bool whole = sg.first && sg.last;
-      const int prow = kRows * tile + my;
-      float* part = whole ? nullptr
-                          : p.partials + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * PPartial<D>::FLOATS;
-      const float inv = whole ? (lr == 0.f ? 0.f : 1.0f / lr) : 1.0f;
-      const int t = grow / p.share, g = grow - t * p.share;
-      __half* const orow = p.out + (long long)(rq.q0 + t) * p.ldo + (long long)(sg.head * p.share + g) * D;
+      const int row0 = 32 * quarter + r;  // this thread's rows: row0 + 8 y
+      if (whole) {
+        float inv[4];
+        __half* orow[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          inv[y] = l[y] == 0.f ? 0.f : 1.0f / l[y];  // no key seen: zeros
+          const int gr = sg.row0 + kRows * tile + min(row0 + 8 * y, rows - 1), t = gr / p.share, g = gr - t * p.share;
+          orow[y] = p.out + (long long)(rq.q0 + t) * p.ldo + (long long)(sg.head * p.share + g) * D + 8 * qd;
+        }
 #pragma unroll 1
-      for (int b = 0; b < D / 32; ++b) {
-        uint32_t raw[32];
-        tmem_ld32(to_addr + 32 * b, raw);
-        if (my < rows) {
+        for (int b = 0; b < D / 32; ++b) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            // positions of channels 0 .. 7: 0 2 4 6 1 3 5 7; odd channels are 16 times too large
-            float x[8];
+          for (int h = 0; h < 2; ++h) {
+            float x[16];
+            tmem_ld_16x256(to_addr + 32 * b + ((16u * h) << 16), x);
+            tmem_wait_ld(x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int at = 8 * c + ((j & 3) << 1) + (j >> 2);
-              x[j] = fmaf(__uint_as_float(raw[at]), (j & 1) ? 1048576.0f : 16777216.0f, br) * inv;
-            }
-            if (whole) {
-              uint32_t h[4];
+            for (int e = 0; e < 2; ++e) {
+              const int y = 2 * h + e;
+              // Of 8 channels k = 0 .. 3 this thread holds qd' and qd' + 4 (qd' = 0 1 2 3:
+              // positions 0 1 | 2 3 | 4 5 | 6 7 are channels 0 4 | 1 5 | 2 6 | 3 7;
+              // odd channels are 16 times too large).  The quad transposes: each
+              // thread takes one whole group of 8, k = qd.
+              const float up = (qd & 1) ? 1048576.0f : 16777216.0f;
+              uint32_t mine[4];  // (channel qd, channel qd + 4) of group k
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const __half2 y = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
-                h[j] = *reinterpret_cast<const uint32_t*>(&y);
+              for (int k = 0; k < 4; ++k) {
+                const __half2 o2 = __floats2half2_rn(fmaf(x[4 * k + 2 * e], up, beta[y]) * inv[y],
+                                                     fmaf(x[4 * k + 2 * e + 1], up, beta[y]) * inv[y]);
+                mine[k] = *reinterpret_cast<const uint32_t*>(&o2);
               }
-              *reinterpret_cast<uint4*>(orow + 32 * b + 8 * c) = make_uint4(h[0], h[1], h[2], h[3]);
-            } else {
-              float4* dst = reinterpret_cast<float4*>(part + (size_t)prow * D + 32 * b + 8 * c);
-              dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-              dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+              uint32_t got[4];  // from thread i of the quad: its pair of group qd
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                // this round thread q gives the pair of group q ^ i to thread q ^ i
+                const int to = qd ^ i;
+                const uint32_t give = to == 0 ? mine[0] : to == 1 ? mine[1] : to == 2 ? mine[2] : mine[3];
+                got[i] = __shfl_xor_sync(0xffffffffu, give, i);  // thread qd ^ i's pair
+              }
+              uint32_t pr[4];  // by thread
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int at = qd ^ i;
+                pr[i] = at == 0 ? got[0] : at == 1 ? got[1] : at == 2 ? got[2] : got[3];
+              }
+              if (row0 + 8 * y < rows)
+                *reinterpret_cast<uint4*>(orow[y] + 32 * b) =
+                    make_uint4(prmt(pr[0], pr[1], 0x5410), prmt(pr[2], pr[3], 0x5410), prmt(pr[0], pr[1], 0x7632),
+                               prmt(pr[2], pr[3], 0x7632));
             }
           }
         }
-      }
-      if (!whole && my < rows) {
-        part[kItemRows * D + prow] = mr;
-        part[kItemRows * D + kItemRows + prow] = lr;
+      } else {
+        // a partial, its columns in TMEM's order
+        float* const part = p.partials + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * PPartial<D>::FLOATS;
+        const float up = (qd & 1) ? 1048576.0f : 16777216.0f;
+#pragma unroll 1
+        for (int b = 0; b < D / 32; ++b) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x[16];
+            tmem_ld_16x256(to_addr + 32 * b + ((16u * h) << 16), x);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int y = 2 * h + e;
+              if (row0 + 8 * y < rows) {
+                float* dst = part + (size_t)(kRows * tile + row0 + 8 * y) * D + 32 * b + 2 * qd;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  *reinterpret_cast<float2*>(dst + 8 * k) =
+                      make_float2(fmaf(x[4 * k + 2 * e], up, beta[y]), fmaf(x[4 * k + 2 * e + 1], up, beta[y]));
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (qd == 0 && row0 + 8 * y < rows) {
+            part[kItemRows * D + kRows * tile + row0 + 8 * y] = m[y];
+            part[kItemRows * D + kItemRows + kRows * tile + row0 + 8 * y] = l[y];
+          }
       }
       tc_fence_before();
       if (!whole && sg.first && tid == 0) {
@@ -837,7 +909,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the partials of the items that were cut (see the kernel for few rows).
+// Joins the partials of the items that were cut (see the kernel for few rows):
+// a thread to 8 channels of a row, which lie in the order 0 4 1 5 2 6 3 7.
 template <int D>
 __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillAttnParams p) {
   pdl_launch_dependents();
@@ -847,28 +920,33 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillAttnPara
   constexpr int F = PPartial<D>::FLOATS;
   const float* first = p.partials + ((size_t)blockIdx.x * 2 + 1) * F;
   const float* rest = p.partials + ((size_t)blockIdx.x + 1) * 2 * F;  // follower i at i * 2 F
-  for (int e = blockIdx.y * 256 + threadIdx.x; e < h.rows * (D / 4); e += gridDim.y * 256) {
-    const int row = e / (D / 4), ch = (e - row * (D / 4)) * 4;
+  for (int e = blockIdx.y * 256 + threadIdx.x; e < h.rows * (D / 8); e += gridDim.y * 256) {
+    const int row = e / (D / 8), ch = (e - row * (D / 8)) * 8;
     float m = first[kItemRows * D + row];
     for (int i = 0; i < h.followers; ++i) m = fmaxf(m, rest[(size_t)i * 2 * F + kItemRows * D + row]);
-    float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float l = 0.f, acc[8] = {};
 #pragma unroll 2
     for (int i = -1; i < h.followers; ++i) {
       const float* part = i < 0 ? first : rest + (size_t)i * 2 * F;
       const float w = ex2(part[kItemRows * D + row] - m);
-      const float4 v = *reinterpret_cast<const float4*>(part + (size_t)row * D + ch);
+      const float4* src = reinterpret_cast<const float4*>(part + (size_t)row * D + ch);
+      const float4 a = src[0], b = src[1];
       l = fmaf(w, part[kItemRows * D + kItemRows + row], l);
-      acc[0] = fmaf(w, v.x, acc[0]);
-      acc[1] = fmaf(w, v.y, acc[1]);
-      acc[2] = fmaf(w, v.z, acc[2]);
-      acc[3] = fmaf(w, v.w, acc[3]);
+      const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = fmaf(w, x[j], acc[j]);
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     const int gr = h.row0 + row, t = gr / p.share, g = gr - t * p.share;
-    const __half2 a = __floats2half2_rn(acc[0] * inv, acc[1] * inv);
-    const __half2 b = __floats2half2_rn(acc[2] * inv, acc[3] * inv);
-    *reinterpret_cast<uint2*>(p.out + (long long)(h.q0 + t) * p.ldo + (long long)(h.head * p.share + g) * D + ch) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // channels 2 j, 2 j + 1
+      const int c0 = 2 * j, c1 = c0 + 1;
+      const __half2 y = __floats2half2_rn(acc[((c0 & 3) << 1) + (c0 >> 2)] * inv, acc[((c1 & 3) << 1) + (c1 >> 2)] * inv);
+      o[j] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    *reinterpret_cast<uint4*>(p.out + (long long)(h.q0 + t) * p.ldo + (long long)(h.head * p.share + g) * D + ch) =
+        make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -895,7 +973,7 @@ tlq_status launch_one(const PrefillAttnParams& base, cudaStream_t stream) {
   lc.numAttrs = pdl_enabled() ? 1 : 0;
   tlq_status st = cuda_error(cudaLaunchKernelEx(&lc, kernel, p), "kv4 prompt attention: launch");
   if (st != TLQ_OK) return st;
-  lc.gridDim = dim3((unsigned)blocks, 8, 1);
+  lc.gridDim = dim3((unsigned)blocks, (unsigned)(kItemRows * D / 8 / 256), 1);
   lc.blockDim = dim3(256, 1, 1);
   lc.dynamicSmemBytes = 0;
   return cuda_error(cudaLaunchKernelEx(&lc, prefill_join_kernel<D>, p), "kv4 prompt attention join: launch");
