@@ -388,7 +388,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   const PSegment& sg = segments[warp];
   auto next_segment = [&]() -> bool {  // all lanes of a warp
     __syncwarp();
-    const int there = lane == 0 ? (int)walks[warp].next(p, &segments[warp]) : 0;
+    int there = 0;
+    if (lane == 0) {
+      PWalk w = walks[warp];
+      PSegment s;
+      there = w.next(p, &s);
+      walks[warp] = w;
+      if (there) segments[warp] = s;
+    }
     __syncwarp();
     return __shfl_sync(0xffffffffu, there, 0) != 0;
   };
@@ -841,24 +848,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
                                                      fmaf(x[4 * k + 2 * e + 1], up, beta[y]) * inv[y]);
                 mine[k] = *reinterpret_cast<const uint32_t*>(&o2);
               }
-              uint32_t got[4];  // from thread i of the quad: its pair of group qd
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                // this round thread q gives the pair of group q ^ i to thread q ^ i
-                const int to = qd ^ i;
-                const uint32_t give = to == 0 ? mine[0] : to == 1 ? mine[1] : to == 2 ? mine[2] : mine[3];
-                got[i] = __shfl_xor_sync(0xffffffffu, give, i);  // thread qd ^ i's pair
-              }
-              uint32_t pr[4];  // by thread
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int at = qd ^ i;
-                pr[i] = at == 0 ? got[0] : at == 1 ? got[1] : at == 2 ? got[2] : got[3];
+              // afterwards mine[i] is thread i's pair of group qd
+              {
+                const bool odd = qd & 1, high = qd & 2;
+                const uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? mine[0] : mine[1], 1);
+                const uint32_t c = __shfl_xor_sync(0xffffffffu, odd ? mine[2] : mine[3], 1);
+                mine[0] = odd ? a : mine[0];
+                mine[1] = odd ? mine[1] : a;
+                mine[2] = odd ? c : mine[2];
+                mine[3] = odd ? mine[3] : c;
+                const uint32_t d = __shfl_xor_sync(0xffffffffu, high ? mine[0] : mine[2], 2);
+                const uint32_t f = __shfl_xor_sync(0xffffffffu, high ? mine[1] : mine[3], 2);
+                mine[0] = high ? d : mine[0];
+                mine[1] = high ? f : mine[1];
+                mine[2] = high ? mine[2] : d;
+                mine[3] = high ? mine[3] : f;
               }
               if (row0 + 8 * y < rows)
                 *reinterpret_cast<uint4*>(orow[y] + 32 * b) =
-                    make_uint4(prmt(pr[0], pr[1], 0x5410), prmt(pr[2], pr[3], 0x5410), prmt(pr[0], pr[1], 0x7632),
-                               prmt(pr[2], pr[3], 0x7632));
+                    make_uint4(prmt(mine[0], mine[1], 0x5410), prmt(mine[2], mine[3], 0x5410),
+                               prmt(mine[0], mine[1], 0x7632), prmt(mine[2], mine[3], 0x7632));
             }
           }
         }
