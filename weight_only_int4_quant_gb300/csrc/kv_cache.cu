@@ -19,22 +19,6 @@ namespace {
 
 constexpr int kRowThreads = 256;
 
-// n / d for n < 2^31 by one multiplication (d >= 1): m = ceil(2^(31 + s) / d)
-// with 2^s >= d errs by less than 1 / d.
-struct FastDiv {
-  uint32_t d, m;
-  int s;
-};
-FastDiv fast_div(uint32_t d) {
-  FastDiv f{d, 0, 0};
-  while ((1ull << f.s) < d) ++f.s;
-  f.m = (uint32_t)(((1ull << (31 + f.s)) + d - 1) / d);
-  return f;
-}
-__device__ __forceinline__ uint32_t divide(uint32_t n, const FastDiv& f) {
-  return (uint32_t)(((uint64_t)n * f.m) >> (31 + f.s));
-}
-
 struct CodeRow {
   uint8_t* codes;
   uint32_t* par;  // (scale, minimum) pairs, one per group
@@ -140,7 +124,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
   // every lane of a warp takes the same number of turns (the shuffles need all)
   for (uint32_t r0 = blockIdx.x * RPB; r0 < rows; r0 += gridDim.x * RPB) {
     const uint32_t row = min(r0 + threadIdx.x / L, rows - 1);  // lanes past the end do the last row again
-    const uint32_t t = divide(row, heads);
+    const uint32_t t = (uint32_t)divide((int)row, heads);
     const int head = (int)(row - t * heads.d);
     const uint4* src = reinterpret_cast<const uint4*>(base + t * ld + head * D + sub * 16);
     const uint4 raw[2] = {__ldg(src), __ldg(src + 1)};
@@ -200,7 +184,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t row = min(r0 + u * RPB + threadIdx.x / L, rows - 1);
-      const uint32_t t = divide(row, heads);
+      const uint32_t t = (uint32_t)divide((int)row, heads);
       const long long slot = __ldg(slots + t);
       word[u] = make_uint2(0, 0);
       par[u] = 0;  // scale and minimum 0: zeros

@@ -63,21 +63,6 @@ struct DCfg {
   static constexpr int SMEM = RING + MERGE + STATS + DEPTH * 20 + 64;
 };
 
-// A partial of the workspace: O [R][D], then m [R], l [R].
-template <int D, int R>
-struct Partial {
-  static constexpr int FLOATS = R * (D + 2);
-};
-
-// What the joining kernel needs of an item that a block began but did not end.
-struct Header {
-  int followers;  // blocks after this one that hold a part of the item; 0: nothing to join
-  int q0;         // first query of the request
-  int row0;       // first (query, head) row of the item
-  int rows;
-  int head;       // key head
-};
-
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -117,8 +102,8 @@ struct DecodeParams {
   float scale_log2;  // softmax scale * log2(e)
   int window, share;  // share: query heads per key head
   int few_rows;       // requests of more rows are not this kernel's
-  float* partials;
-  Header* headers;
+  FastDiv by_share;
+  KvJoin join;
 };
 
 // Units of one request, the same for each of its items (key head, row block).
@@ -178,7 +163,7 @@ struct Walk {
       s->head = item / row_blocks;
       s->row0 = (item - s->head * row_blocks) * R;
       s->rows = min(R, rq.q_len * p.share - s->row0);
-      const int first_q = s->row0 / p.share, last_q = (s->row0 + s->rows - 1) / p.share;
+      const int first_q = divide(s->row0, p.by_share), last_q = divide(s->row0 + s->rows - 1, p.by_share);
       const int base = rq.len - rq.q_len;
       s->hi = max(0, base + last_q + 1);
       s->lo = p.window > 0 ? max(0, base + first_q - p.window + 1) : 0;
@@ -222,7 +207,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
     fence_mbar_init();
   }
   pdl_wait();
-  Header* const header = &p.headers[blockIdx.x];
+  KvJoinHeader* const header = &p.join.headers[blockIdx.x];
   if (tid == 0) header->followers = 0;
 
   auto count = [&](int i) -> long long {
@@ -327,7 +312,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
       const int row = 8 * nt + r;
       const bool on = row < rows;
       const int gr = row0 + (on ? row : 0);
-      const int t = gr / p.share, g = gr - t * p.share;
+      const int t = divide(gr, p.by_share), g = gr - t * p.share;
       const __half* src = p.q + (long long)(rq.q0 + t) * p.ldq + (long long)(head * p.share + g) * D;
       uint4 raw[H][2];
       float sum[H], big = 0.f;
@@ -490,7 +475,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
                     x = fmaf(sc[nt][1][2 * y + c] * f[nt][c], ksc[y][1], fmaf(kmi[y][1], qs[nt][c][1], x));
                   if (edge) {
                     const int key = tok0 + (i0 + i) * kTile + r + 8 * y;
-                    const int at = base_pos + (row0 + min(8 * nt + 2 * qd + c, rows - 1)) / p.share;  // the row's position
+                    const int at = base_pos + divide(row0 + min(8 * nt + 2 * qd + c, rows - 1), p.by_share);  // the row's position
                     const bool see = in[y] && key <= at && (p.window <= 0 || key > at - p.window);
                     x = see ? x : -INFINITY;
                   }
@@ -613,7 +598,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
     const bool whole = sg.first && sg.last;
     float* part = nullptr;
     if (!whole)
-      part = p.partials + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * Partial<D, R>::FLOATS;
+      part = p.join.parts + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * (R * (D + 2));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (nt > 0) named_barrier(1, 32 * W);
@@ -653,7 +638,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
         if (whole) {
           if (row < rows) {
             const float inv = ll == 0.f ? 0.f : 1.0f / ll;  // no key seen: zeros
-            const int gr = row0 + row, t = gr / p.share, g = gr - t * p.share;
+            const int gr = row0 + row, t = divide(gr, p.by_share), g = gr - t * p.share;
             const __half2 a = __floats2half2_rn(acc[0] * inv, acc[1] * inv);
             const __half2 b = __floats2half2_rn(acc[2] * inv, acc[3] * inv);
             *reinterpret_cast<uint2*>(p.out + (long long)(rq.q0 + t) * p.ldo +
@@ -675,50 +660,13 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
       long long b = ((last_u + 1) * n - 1) / U;
       while (U * b / n > last_u) --b;
       while (U * (b + 1) / n <= last_u) ++b;
-      *header = Header{(int)(b - blockIdx.x), rq.q0, row0, rows, head};
+      *header = KvJoinHeader{(int)(b - blockIdx.x), rq.q0, row0, rows, head};
     }
   }
 }
 
-// Joins the partials of the items that were cut: block x looks at what main
-// block x began, block y takes every gridDim.y-th set of 128 four-channel pieces.
-template <int D, int R>
-__global__ void __launch_bounds__(128) decode_join_kernel(const DecodeParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const Header h = p.headers[blockIdx.x];
-  if (h.followers <= 0) return;
-  const int e = blockIdx.y * 128 + threadIdx.x;
-  const int row = e / (D / 4), ch = (e - row * (D / 4)) * 4;
-  if (row >= h.rows) return;
-  constexpr int F = Partial<D, R>::FLOATS;
-  const float* first = p.partials + ((size_t)blockIdx.x * 2 + 1) * F;
-  const float* rest = p.partials + ((size_t)blockIdx.x + 1) * 2 * F;  // follower i at i * 2 F
-  float m = first[R * D + row];
-  for (int i = 0; i < h.followers; ++i) m = fmaxf(m, rest[(size_t)i * 2 * F + R * D + row]);
-  float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int i = -1; i < h.followers; ++i) {
-    const float* part = i < 0 ? first : rest + (size_t)i * 2 * F;
-    const float mi = part[R * D + row];
-    const float w = ex2(mi - m);
-    const float4 v = *reinterpret_cast<const float4*>(part + row * D + ch);
-    l = fmaf(w, part[R * D + R + row], l);
-    acc[0] = fmaf(w, v.x, acc[0]);
-    acc[1] = fmaf(w, v.y, acc[1]);
-    acc[2] = fmaf(w, v.z, acc[2]);
-    acc[3] = fmaf(w, v.w, acc[3]);
-  }
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  const int gr = h.row0 + row, t = gr / p.share, g = gr - t * p.share;
-  const __half2 a = __floats2half2_rn(acc[0] * inv, acc[1] * inv);
-  const __half2 b = __floats2half2_rn(acc[2] * inv, acc[3] * inv);
-  *reinterpret_cast<uint2*>(p.out + (long long)(h.q0 + t) * p.ldo + (long long)(h.head * p.share + g) * D + ch) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-
 template <int D, int NG, int NT>
-tlq_status launch_one(const DecodeParams& base, cudaStream_t stream) {
+tlq_status launch_one(const DecodeParams& base, void* ws, KvJoin* join, cudaStream_t stream) {
   using C = DCfg<D, NG, NT>;
   auto kernel = decode_attention_kernel<D, NG, NT>;
   static const cudaError_t attr =
@@ -726,9 +674,7 @@ tlq_status launch_one(const DecodeParams& base, cudaStream_t stream) {
   if (attr != cudaSuccess) return cuda_error(attr, "kv4 attention: shared memory");
   const int blocks = device_info().sms * C::CTAS;
   DecodeParams p = base;
-  p.headers = reinterpret_cast<Header*>(p.partials);
-  p.partials = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.partials) +
-                                        ((blocks * sizeof(Header) + 255) & ~size_t(255)));
+  p.join = *join = kv_join_at(ws, blocks, C::R);
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)blocks, 1, 1);
   lc.blockDim = dim3(C::THREADS, 1, 1);
@@ -739,17 +685,12 @@ tlq_status launch_one(const DecodeParams& base, cudaStream_t stream) {
   at.val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = &at;
   lc.numAttrs = pdl_enabled() ? 1 : 0;
-  tlq_status st = cuda_error(cudaLaunchKernelEx(&lc, kernel, p), "kv4 attention: launch");
-  if (st != TLQ_OK) return st;
-  lc.gridDim = dim3((unsigned)blocks, (unsigned)((C::R * D / 4 + 127) / 128), 1);
-  lc.blockDim = dim3(128, 1, 1);
-  lc.dynamicSmemBytes = 0;
-  return cuda_error(cudaLaunchKernelEx(&lc, decode_join_kernel<D, C::R>, p), "kv4 attention join: launch");
+  return cuda_error(cudaLaunchKernelEx(&lc, kernel, p), "kv4 attention: launch");
 }
 
 template <int D, int NG>
-tlq_status launch_rows(const DecodeParams& p, int rows, cudaStream_t stream) {
-  return rows <= 8 ? launch_one<D, NG, 1>(p, stream) : launch_one<D, NG, 2>(p, stream);
+tlq_status launch_rows(const DecodeParams& p, int rows, void* ws, KvJoin* join, cudaStream_t stream) {
+  return rows <= 8 ? launch_one<D, NG, 1>(p, ws, join, stream) : launch_one<D, NG, 2>(p, ws, join, stream);
 }
 
 }  // namespace
@@ -757,14 +698,11 @@ tlq_status launch_rows(const DecodeParams& p, int rows, cudaStream_t stream) {
 // The most that any form of the kernel takes at this head size, so that one
 // workspace serves steps of every shape.
 size_t kv4_decode_workspace(int head_dim) {
-  const size_t sms = (size_t)device_info().sms;
-  auto bytes = [&](size_t blocks, size_t R) {
-    return ((blocks * sizeof(Header) + 255) & ~size_t(255)) + blocks * 2 * R * (head_dim + 2) * sizeof(float);
-  };
-  return std::max(bytes(3 * sms, 8), bytes(2 * sms, 16));
+  const int sms = device_info().sms;
+  return std::max(kv_join_bytes(3 * sms, 8, head_dim), kv_join_bytes(2 * sms, 16, head_dim));
 }
 
-tlq_status launch_kv4_decode(const KvAttention& a, int few_rows, cudaStream_t stream) {
+tlq_status launch_kv4_decode(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream) {
   DecodeParams p{};
   p.cache = a.cache;
   p.batch = a.batch;
@@ -776,10 +714,11 @@ tlq_status launch_kv4_decode(const KvAttention& a, int few_rows, cudaStream_t st
   p.window = a.window;
   p.share = a.q_heads / a.cache.heads;
   p.few_rows = few_rows;
-  p.partials = static_cast<float*>(a.ws);
+  p.by_share = fast_div((uint32_t)p.share);
   const int rows = (int)std::min<long long>((long long)a.batch.max_q * p.share, few_rows);
-  if (a.head_dim == 64) return launch_rows<64, 1>(p, rows, stream);
-  return a.cache.group == 64 ? launch_rows<128, 2>(p, rows, stream) : launch_rows<128, 1>(p, rows, stream);
+  if (a.head_dim == 64) return launch_rows<64, 1>(p, rows, ws, join, stream);
+  return a.cache.group == 64 ? launch_rows<128, 2>(p, rows, ws, join, stream)
+                             : launch_rows<128, 1>(p, rows, ws, join, stream);
 }
 
 }  // namespace tlq

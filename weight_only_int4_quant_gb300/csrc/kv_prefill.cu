@@ -19,11 +19,12 @@
 //                   global memory to registers a stage ahead, then into the K
 //                   and V tiles; scales and minima into the softmax's tables
 //   warp 11         issues the MMAs
-// A stage is worked on in two halves of 64 tokens with an S each, so the tensor
-// cores form the next half's S and add the last half's P V while a softmax
-// works.  (With one S a stage, a tile's softmax and its MMAs took turns: 6300
-// clocks a stage, twice the tensor cores' time.)  Twelve warps, three to a
-// scheduler, leave the softmax 168 registers a thread; with thirteen it spilled.
+// The two tiles go their own ways through the stages, so that one tile's MMAs
+// run while the other's softmax works; the weights of a stage are handed over in
+// two halves, the first of which is multiplied during the softmax of the second.
+// (An S for each half, to be formed ahead, reads Q twice as often: shared memory,
+// 4600 of a stage's 5400 clocks busy, then bounds the stage.)  Twelve warps,
+// three to a scheduler, leave the softmax 168 registers a thread.
 // Both operands lie in shared memory as the cache has them, a token to a
 // 128-byte swizzled row: K-major for S, N-major (transposed by descriptor)
 // for P V, so no tile is transposed.  The order of channels inside a code
@@ -50,7 +51,8 @@ namespace {
 constexpr int kStage = 128;       // tokens of a stage
 constexpr int kRows = 128;        // rows of a tile
 constexpr int kItemRows = 256;    // rows of an item: two tiles
-constexpr int kHalf = 64;         // tokens of an S
+constexpr int kHalf = 64;         // tokens whose weights are handed over at once
+constexpr int kItemCost = 2;      // what beginning and ending an item costs, in stages
 constexpr int kCodeWarps = 3;     // warps that write the K and V tiles
 constexpr int kThreads = (8 + kCodeWarps + 1) * 32;
 constexpr float kHeadroom = 6.0f;   // a new reference puts the largest weight at 2^6
@@ -78,17 +80,8 @@ struct PrefillAttnParams {
   long long ldo;
   float scale_log2;
   int window, share, few_rows;
-  float* partials;
-  struct PHeader* headers;
-};
-
-struct PHeader {
-  int followers, q0, row0, rows, head;
-};
-
-template <int D>
-struct PPartial {
-  static constexpr int FLOATS = kItemRows * (D + 2);  // O [rows][D], m [rows], l [rows]
+  FastDiv by_share;
+  KvJoin join;
 };
 
 // Bounds of one row tile of a request.
@@ -98,7 +91,8 @@ struct TileShape {
 };
 __device__ __forceinline__ TileShape tile_shape(const PrefillAttnParams& p, const KvRequest& r, int rows, int qt) {
   TileShape t;
-  const int first_q = qt * kItemRows / p.share, last_q = (min(rows, (qt + 1) * kItemRows) - 1) / p.share;
+  const int first_q = divide(qt * kItemRows, p.by_share);
+  const int last_q = divide(min(rows, (qt + 1) * kItemRows) - 1, p.by_share);
   const int base = r.len - r.q_len;
   t.hi = max(0, base + last_q + 1);
   t.lo = p.window > 0 ? max(0, base + first_q - p.window + 1) : 0;
@@ -112,12 +106,15 @@ __device__ __forceinline__ int many_rows(const PrefillAttnParams& p, const KvReq
   return rows > p.few_rows ? rows : 0;
 }
 
+// A block's share of an item.  On the line of work an item is kItemCost units
+// and then one for each stage.
 struct PSegment {
   KvRequest rq;
   int req, head, row0, rows;
   int lo, hi;
-  int s0, s1;
-  bool first, last;
+  int s0, s1;         // stages of the share (absolute: token / kStage)
+  int tile_end[2];    // by tile: behind the last of them that one of its rows sees (s0: none)
+  bool first, last;   // holds the item's first, last stage
   long long item_end;
 };
 
@@ -133,15 +130,31 @@ struct PWalk {
     tiles = (rows + kItemRows - 1) / kItemRows;
     qt = head = 0;
   }
+  // To the row tile that u lies in; a warp together, 32 row tiles at a time.
   __device__ __forceinline__ void start(const PrefillAttnParams& p, int request, long long first) {
+    const int lane = threadIdx.x & 31;
     req = request;
     item_u = first;
     enter(p);
-    for (; qt + 1 < tiles; ++qt) {
-      const long long n = (long long)tile_shape(p, rq, rows, qt).n * p.cache.heads;
-      if (u < item_u + n) break;
-      item_u += n;
+    for (int q0 = 0; q0 < tiles; q0 += 32) {
+      const long long n =
+          q0 + lane < tiles ? (long long)(tile_shape(p, rq, rows, q0 + lane).n + kItemCost) * p.cache.heads : 0;
+      long long upto = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, n > 0 && u < item_u + upto);
+      if (hit) {
+        const int f = __ffs(hit) - 1;
+        qt = q0 + f;
+        item_u += __shfl_sync(0xffffffffu, upto - n, f);
+        return;
+      }
+      item_u += __shfl_sync(0xffffffffu, upto, 31);
     }
+    qt = tiles;
   }
   __device__ __forceinline__ bool next(const PrefillAttnParams& p, PSegment* s) {
     while (u < u_end) {
@@ -151,9 +164,11 @@ struct PWalk {
         continue;
       }
       const TileShape t = tile_shape(p, rq, rows, qt);
-      if (u >= item_u + t.n) {
-        const long long skip = min((long long)(p.cache.heads - head), (u - item_u) / t.n);
-        item_u += skip * t.n;
+      const int units = t.n + kItemCost;
+      if (u >= item_u + units) {
+        long long skip = 1;
+        if (u >= item_u + 2 * units) skip = min((long long)(p.cache.heads - head), (u - item_u) / units);
+        item_u += skip * units;
         head += (int)skip;
         if (head >= p.cache.heads) {
           head = 0;
@@ -161,7 +176,11 @@ struct PWalk {
         }
         continue;
       }
-      const int c0 = (int)(u - item_u), c1 = (int)min((long long)t.n, c0 + (u_end - u));
+      const int c0 = max(0, (int)(u - item_u) - kItemCost);
+      const int c1 = (int)min((long long)units, u_end - item_u) - kItemCost;
+      const bool begins = u <= item_u + kItemCost;
+      u = min(u_end, item_u + units);
+      if (c1 <= c0) continue;  // the share ends before the item's first stage
       s->rq = rq;
       s->req = req;
       s->head = head;
@@ -171,10 +190,15 @@ struct PWalk {
       s->hi = t.hi;
       s->s0 = t.s0 + c0;
       s->s1 = t.s0 + c1;
-      s->first = c0 == 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int last = min(s->rows, kRows * (i + 1)) - 1;  // the tile's last row
+        const int hi = last < kRows * i ? 0 : rq.len - rq.q_len + divide(s->row0 + last, p.by_share) + 1;
+        s->tile_end[i] = max(s->s0, min(s->s1, (max(hi, 0) + kStage - 1) / kStage));
+      }
+      s->first = begins;
       s->last = c1 == t.n;
-      s->item_end = item_u + t.n;
-      u += c1 - c0;
+      s->item_end = item_u + units;
       return true;
     }
     return false;
@@ -236,7 +260,7 @@ __device__ __forceinline__ uint64_t sw128_desc_n(uint32_t saddr, uint32_t block_
 
 // kind::f16, D = F32, A = B = F16, M = 128; bit 16: B is N-major.
 constexpr uint32_t kIdescS =
-    (1u << 4) | ((uint32_t)(kHalf >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+    (1u << 4) | ((uint32_t)(kStage >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 template <int D>
 constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 
@@ -306,10 +330,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // Barriers of a block.
 struct PBars {
   uint64_t q_full[2];              // by tile: Q written (4 warps)
-  uint64_t s_full[2][2];           // by tile and half: S complete
+  uint64_t s_full[2];              // by tile: S complete
   uint64_t p_full[2][2];           // by tile and half: the weights written (4 warps)
   uint64_t o_done[2][2];           // by tile and half: P V complete
-  uint64_t k_full[2], k_empty[2];  // written (4 warps), read
+  uint64_t k_full[2], k_empty[2];  // written (4 warps), read (2 tiles)
   uint64_t v_full[2], v_empty[2];
   uint64_t t_full[3], t_empty[3];  // table written (4 warps), read (8 warps)
   uint32_t tmem;
@@ -332,21 +356,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   // once an item and the softmax has no registers to spare
   __shared__ PWalk walks[kThreads / 32];
   __shared__ PSegment segments[kThreads / 32];
+  __shared__ long long request_units[kThreads];
 
   const int tid = threadIdx.x, warp = (int)uniform(tid >> 5), lane = tid & 31;
   pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->q_full[i], 4);
+      mbar_init(&bar->s_full[i], 1);
       for (int h = 0; h < 2; ++h) {
-        mbar_init(&bar->s_full[i][h], 1);
         mbar_init(&bar->p_full[i][h], 4);
         mbar_init(&bar->o_done[i][h], 1);
       }
       mbar_init(&bar->k_full[i], 4);
-      mbar_init(&bar->k_empty[i], 1);
+      mbar_init(&bar->k_empty[i], 2);
       mbar_init(&bar->v_full[i], 4);
-      mbar_init(&bar->v_empty[i], 1);
+      mbar_init(&bar->v_empty[i], 2);
     }
     for (int i = 0; i < TD; ++i) {
       mbar_init(&bar->t_full[i], 4);
@@ -360,15 +385,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   tc_fence_after();
   const uint32_t tmem = uniform(bar->tmem);
   pdl_wait();
-  PHeader* const header = &p.headers[blockIdx.x];
+  KvJoinHeader* const header = &p.join.headers[blockIdx.x];
   if (tid == 0) header->followers = 0;
 
-  auto count = [&](int i) -> long long {
-    const KvRequest r = kv_request(p.batch, p.cache.page, i);
+  // units of a request; a warp to a request where all fit the block at once
+  auto lane_units = [&](const KvRequest& r, int first, int step) {
     const int rows = many_rows(p, r);
     long long n = 0;
-    for (int qt = 0; qt * kItemRows < rows; ++qt) n += tile_shape(p, r, rows, qt).n;
+    for (int qt = first; qt * kItemRows < rows; qt += step) n += tile_shape(p, r, rows, qt).n + kItemCost;
     return n * p.cache.heads;
+  };
+  const bool small = p.batch.requests <= kThreads;
+  if (small) {
+    for (int i = warp; i < p.batch.requests; i += kThreads / 32) {
+      long long v = lane_units(kv_request(p.batch, p.cache.page, i), lane, 32);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) request_units[i] = v;
+    }
+    __syncthreads();
+  }
+  auto count = [&](int i) -> long long {
+    return small ? request_units[i] : lane_units(kv_request(p.batch, p.cache.page, i), 0, 1);
   };
   long long own, mine;
   search.count_all(p.batch.requests, count, &own, &mine);
@@ -376,14 +414,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   const long long n = min((long long)gridDim.x, U);
   const bool busy = (long long)blockIdx.x < n;
   if (busy) search.find(p.batch.requests, count, U * blockIdx.x / n, own, mine);
-  if (lane == 0) {
-    PWalk& walk = walks[warp];
-    walk.u = walk.u_end = 0;
+  {
+    PWalk w;
+    w.u = w.u_end = 0;
     if (busy && search.request >= 0) {
-      walk.u = U * blockIdx.x / n;
-      walk.u_end = U * (blockIdx.x + 1) / n;
-      walk.start(p, search.request, search.first);
+      w.u = U * blockIdx.x / n;
+      w.u_end = U * (blockIdx.x + 1) / n;
+      w.start(p, search.request, search.first);
     }
+    if (lane == 0) walks[warp] = w;
   }
   const PSegment& sg = segments[warp];
   auto next_segment = [&]() -> bool {  // all lanes of a warp
@@ -553,59 +592,81 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
         const bool there = mbar_wait_long(b, parity, where);
         return __all_sync(0xffffffffu, there);
       };
-      auto issue_s = [&](uint32_t tile, uint32_t slot, uint32_t half) {
+      // S of a tile and the stage in ring slot `slot` of the keys
+      auto issue_s = [&](uint32_t tile, uint32_t slot) {
         const uint64_t a0 = sw128_desc(smem_u32(sq) + tile * C::TILE);
-        const uint64_t b0 = sw128_desc(smem_u32(sk) + slot * C::TILE + half * (kHalf * 128));
+        const uint64_t b0 = sw128_desc(smem_u32(sk) + slot * C::TILE);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t o = ((kk >> 2) * C::BLOCK + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + kStage * tile + kHalf * half, a0 + o, b0 + o, kIdescS, kk != 0);
+          mma_ss(tmem + kStage * tile, a0 + o, b0 + o, kIdescS, kk != 0);
         }
-        commit(smem_u32(&bar->s_full[0][0]) + 16 * tile + 8 * half);
+        commit(smem_u32(&bar->s_full[0]) + 8 * tile);
+        commit(smem_u32(&bar->k_empty[0]) + 8 * slot);
       };
-      // MMAs of one thread run in order, so the S issued next may overwrite the weights this one reads
+      // MMAs of one thread run in order, so the S issued next may overwrite the weights these read
       auto issue_o = [&](uint32_t tile, uint32_t slot, uint32_t half, uint32_t accum) {
         const uint64_t b0 = sw128_desc_n(smem_u32(sv) + slot * C::TILE + half * (kHalf * 128), C::BLOCK);
 #pragma unroll
         for (int kk = 0; kk < kHalf / 16; ++kk)
-          mma_ts(tmem + 2 * kStage + D * tile, tmem + kStage * tile + kHalf * half + kk * 8, b0 + kk * (2048 >> 4),
+          mma_ts(tmem + 2 * kStage + D * tile, tmem + kStage * tile + (kHalf / 2) * half + kk * 8, b0 + kk * (2048 >> 4),
                  kIdescO<D>, kk ? 1u : accum);
         commit(smem_u32(&bar->o_done[0][0]) + 16 * tile + 8 * half);
+        if (half) commit(smem_u32(&bar->v_empty[0]) + 8 * slot);
       };
       while (ok && next_segment()) {
-        const uint32_t tiles = uniform(sg.rows > kRows ? 2 : 1), T = uniform(sg.s1 - sg.s0);
         it = uniform(it);
+        uint32_t left[2], at[2] = {it, it}, half[2] = {0, 0};  // by tile: stages left, the stage and half whose weights come next
         ok = wait(&bar->k_full[it % KD], (it / KD) & 1, 0x321);
-        for (uint32_t i = 0; i < tiles && ok; ++i) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          left[i] = uniform((uint32_t)(sg.tile_end[i] - sg.s0));
+          if (!ok || left[i] == 0) continue;
           ok = wait(&bar->q_full[i], q_seg[i] & 1, 0x322);
           ++q_seg[i];
-          if (!ok) break;
+          if (!ok) continue;
           tc_fence_after();
-          issue_s(i, it % KD, 0);
-          issue_s(i, it % KD, 1);
+          issue_s(i, it % KD);
         }
-        if (!ok) break;
-        commit(smem_u32(&bar->k_empty[0]) + 8 * (it % KD));
-        for (uint32_t s = 0; s < T && ok; ++s, ++it) {
-          const bool next = s + 1 < T;
-          ok = wait(&bar->v_full[it % VD], (it / VD) & 1, 0x324) &&
-               (!next || wait(&bar->k_full[(it + 1) % KD], ((it + 1) / KD) & 1, 0x323));
-#pragma unroll 1
-          for (uint32_t half = 0; half < 2; ++half) {
-#pragma unroll 1
-            for (uint32_t i = 0; i < tiles && ok; ++i) {
-              ok = wait(&bar->p_full[i][half], stages[i] & 1, 0x325);
-              stages[i] += half;
-              if (!ok) break;
-              tc_fence_after();
-              issue_o(i, it % VD, half, s || half ? 1u : 0u);
-              if (half && i + 1 == tiles) commit(smem_u32(&bar->v_empty[0]) + 8 * (it % VD));
-              if (next) issue_s(i, (it + 1) % KD, half);
+        // whichever tile's weights are there first
+        uint64_t since = 0;
+        while (ok && (left[0] | left[1])) {
+          bool idle = true;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (left[i] == 0 || !ok) continue;
+            const bool there = mbar_try_wait(&bar->p_full[i][half[i]], stages[i] & 1);
+            if (!__all_sync(0xffffffffu, there)) continue;
+            idle = false;
+            tc_fence_after();
+            const uint32_t a = at[i], h = half[i];
+            if (h == 0) ok = wait(&bar->v_full[a % VD], (a / VD) & 1, 0x324);
+            if (!ok) continue;
+            issue_o(i, a % VD, h, a != it || h ? 1u : 0u);
+            half[i] = h ^ 1;
+            if (h) {
+              ++stages[i];
+              ++at[i];
+              if (--left[i]) {
+                ok = wait(&bar->k_full[(a + 1) % KD], ((a + 1) / KD) & 1, 0x323);
+                if (ok) issue_s(i, (a + 1) % KD);
+              }
             }
           }
-          if (!ok) break;
-          if (next) commit(smem_u32(&bar->k_empty[0]) + 8 * ((it + 1) % KD));
+          if (!idle) {
+            since = 0;
+          } else if (since == 0) {
+            since = globaltimer_ns();
+          } else {
+            __nanosleep(20);
+            if (globaltimer_ns() - since > kWaitLimitNs) {
+              record_timeout(0x325);
+              ok = false;
+            }
+            ok = __all_sync(0xffffffffu, ok);
+          }
         }
+        it += uniform((uint32_t)(sg.s1 - sg.s0));
       }
     }
   } else {
@@ -615,28 +676,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
     const uint32_t ts_tile = lanes + kStage * tile;              // S of the two halves, and the weights over them
     const uint32_t to_addr = lanes + 2 * kStage + D * tile;      // O
-    uint32_t done = 0;  // halves of this tile so far: two give the barriers of a half their next phase
+    uint32_t done = 0;  // stages of this tile so far: the phase of its barriers
     // A wait that gave up ends waiting for good, but nothing else.
     bool ok = true;
     while (next_segment()) {
       const KvRequest rq = sg.rq;
       const int rows = min(kRows, sg.rows - kRows * tile);  // of this tile; below 1: none
       const int base_pos = rq.len - rq.q_len;
-      if (rows <= 0) {  // the tile is empty: only let the tables go on
-        for (int s = sg.s0; s < sg.s1; ++s, ++it) {
-          ok = ok && mbar_wait_long(&bar->t_full[it % TD], (it / TD) & 1, 0x331);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar->t_empty[it % TD]);
-        }
-        continue;
-      }
+      const int end = sg.tile_end[tile], s_end = sg.s1;
+      const bool none = end == sg.s0;  // no row of the tile sees a key of the share
       // Q: a thread to a row, in the codes' channel order
-      const int my = 32 * quarter + lane;
-      const int grow = sg.row0 + kRows * tile + my;
       float qsum = 0.f;
-      {
+      if (!none) {
+        const int my = 32 * quarter + lane;
+        const int grow = sg.row0 + kRows * tile + my;
         const bool on = my < rows;
-        const int t = grow / p.share, g = grow - t * p.share;
+        const int t = divide(grow, p.by_share), g = grow - t * p.share;
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(rq.q0 + (on ? t : 0)) * p.ldq +
                                                           (long long)(sg.head * p.share + (on ? g : 0)) * D);
         const uint32_t dst = smem_u32(sq + tile * C::TILE) + my * 128u;
@@ -662,26 +717,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // rows r + 8 k of this warp's 32
         qs[k] = __shfl_sync(0xffffffffu, qsum, r + 8 * k);
-        pos[k] = base_pos + (sg.row0 + min(kRows * tile + 32 * quarter + r + 8 * k, sg.rows - 1)) / p.share;
+        pos[k] = base_pos + divide(sg.row0 + min(kRows * tile + 32 * quarter + r + 8 * k, sg.rows - 1), p.by_share);
         m[k] = kNone;
         l[k] = beta[k] = 0.f;
       }
       // keys below all_hi and from all_lo are seen by every row of the tile
-      const int all_hi = base_pos + (sg.row0 + kRows * tile) / p.share + 1;
+      const int all_hi = base_pos + divide(sg.row0 + kRows * tile, p.by_share) + 1;
       const int all_lo =
-          p.window > 0 ? base_pos + (sg.row0 + kRows * tile + rows - 1) / p.share - p.window + 1 : 0;
+          p.window > 0 ? base_pos + divide(sg.row0 + max(0, kRows * tile + rows - 1), p.by_share) - p.window + 1 : 0;
 
-      for (int s = sg.s0; s < sg.s1; ++s, ++it) {
-        ok = ok && mbar_wait_long(&bar->t_full[it % TD], (it / TD) & 1, 0x332);
+      int s = sg.s0;
+      for (; s < end; ++s, ++it, ++done) {
+        ok = ok && mbar_wait_long(&bar->t_full[it % TD], (it / TD) & 1, 0x332) &&
+             mbar_wait_long(&bar->s_full[tile], done & 1, 0x333);
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half, ++done) {
+        for (int half = 0; half < 2; ++half) {
           const int key0 = s * kStage + half * kHalf;
-          ok = ok && mbar_wait_long(&bar->s_full[tile][half], (done >> 1) & 1, 0x333);
           ok = __all_sync(0xffffffffu, ok);
           tc_fence_after();
           const uint32_t tab = smem_u32(st + (it % TD) * C::TABLE) + half * (kHalf * 8) + qd * 16;
           const uint32_t tab3 = smem_u32(st + (it % TD) * C::TABLE) + kStage * 16 + half * (kHalf * 4) + qd * 8;
-          const uint32_t ts_addr = ts_tile + kHalf * half;
+          const uint32_t ts_addr = ts_tile + kHalf * half, tp_addr = ts_tile + (kHalf / 2) * half;  // S, weights over the first half
           // v[c][0]: columns 32 c .. of rows r, r + 8; v[c][1]: of rows r + 16, r + 24
           float v[2][2][16];
 #pragma unroll
@@ -749,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
               beta[y] *= w[y];
             }
             if (s > sg.s0 || half) {
-              ok = ok && mbar_wait_long(&bar->o_done[tile][half ^ 1], ((done - 1) >> 1) & 1, 0x334);
+              ok = ok && mbar_wait_long(&bar->o_done[tile][half ^ 1], (half ? done : done - 1) & 1, 0x334);
               ok = __all_sync(0xffffffffu, ok);
               tc_fence_after();
 #pragma unroll 1
@@ -787,8 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
                 bt[y] = fma2(e, rb, bt[y]);
               }
             }
-            tmem_st_16x128(ts_addr + 16 * c, pw[0]);
-            tmem_st_16x128(ts_addr + 16 * c + (16u << 16), pw[1]);
+            tmem_st_16x128(tp_addr + 16 * c, pw[0]);
+            tmem_st_16x128(tp_addr + 16 * c + (16u << 16), pw[1]);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -802,6 +858,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
         }
         if (lane == 0) mbar_arrive(&bar->t_empty[it % TD]);
       }
+      // stages that the tile does not see: let the rings go on
+      for (; s < s_end; ++s, ++it) {
+        ok = ok && mbar_wait_long(&bar->t_full[it % TD], (it / TD) & 1, 0x331) &&
+             mbar_wait_long(&bar->v_full[it % VD], (it / VD) & 1, 0x336);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar->t_empty[it % TD]);
+          if (quarter == 0) {
+            mbar_arrive(&bar->k_empty[it % KD]);
+            mbar_arrive(&bar->v_empty[it % VD]);
+          }
+        }
+      }
+      if (rows <= 0) continue;
 
       // ---- the item's end: sums of the quads, then a thread to a row ----
 #pragma unroll
@@ -812,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           beta[k] += __shfl_xor_sync(0xffffffffu, beta[k], o);
         }
       }
-      ok = ok && mbar_wait_long(&bar->o_done[tile][1], ((done - 1) >> 1) & 1, 0x335);
+      if (!none) ok = ok && mbar_wait_long(&bar->o_done[tile][1], (done - 1) & 1, 0x335);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const bool whole = sg.first && sg.last;
@@ -823,7 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           inv[y] = l[y] == 0.f ? 0.f : 1.0f / l[y];  // no key seen: zeros
-          const int gr = sg.row0 + kRows * tile + min(row0 + 8 * y, rows - 1), t = gr / p.share, g = gr - t * p.share;
+          const int gr = sg.row0 + kRows * tile + min(row0 + 8 * y, rows - 1);
+          const int t = divide(gr, p.by_share), g = gr - t * p.share;
           orow[y] = p.out + (long long)(rq.q0 + t) * p.ldo + (long long)(sg.head * p.share + g) * D + 8 * qd;
         }
 #pragma unroll 1
@@ -833,6 +904,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
             float x[16];
             tmem_ld_16x256(to_addr + 32 * b + ((16u * h) << 16), x);
             tmem_wait_ld(x);
+            if (none) {  // O was not formed
+#pragma unroll
+              for (int k = 0; k < 16; ++k) x[k] = 0.f;
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int y = 2 * h + e;
@@ -873,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
         }
       } else {
         // a partial, its columns in TMEM's order
-        float* const part = p.partials + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * PPartial<D>::FLOATS;
+        float* const part = p.join.parts + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * (kItemRows * (D + 2));
         const float up = (qd & 1) ? 1048576.0f : 16777216.0f;
 #pragma unroll 1
         for (int b = 0; b < D / 32; ++b) {
@@ -882,6 +957,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
             float x[16];
             tmem_ld_16x256(to_addr + 32 * b + ((16u * h) << 16), x);
             tmem_wait_ld(x);
+            if (none) {  // O was not formed
+#pragma unroll
+              for (int k = 0; k < 16; ++k) x[k] = 0.f;
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int y = 2 * h + e;
@@ -908,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
         long long b = ((last_u + 1) * n - 1) / U;
         while (U * b / n > last_u) --b;
         while (U * (b + 1) / n <= last_u) ++b;
-        *header = PHeader{(int)(b - blockIdx.x), rq.q0, sg.row0, sg.rows, sg.head};
+        *header = KvJoinHeader{(int)(b - blockIdx.x), rq.q0, sg.row0, sg.rows, sg.head};
       }
     }
   }
@@ -918,60 +997,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the partials of the items that were cut (see the kernel for few rows):
-// a thread to 8 channels of a row, which lie in the order 0 4 1 5 2 6 3 7.
 template <int D>
-__global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillAttnParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const PHeader h = p.headers[blockIdx.x];
-  if (h.followers <= 0) return;
-  constexpr int F = PPartial<D>::FLOATS;
-  const float* first = p.partials + ((size_t)blockIdx.x * 2 + 1) * F;
-  const float* rest = p.partials + ((size_t)blockIdx.x + 1) * 2 * F;  // follower i at i * 2 F
-  for (int e = blockIdx.y * 256 + threadIdx.x; e < h.rows * (D / 8); e += gridDim.y * 256) {
-    const int row = e / (D / 8), ch = (e - row * (D / 8)) * 8;
-    float m = first[kItemRows * D + row];
-    for (int i = 0; i < h.followers; ++i) m = fmaxf(m, rest[(size_t)i * 2 * F + kItemRows * D + row]);
-    float l = 0.f, acc[8] = {};
-#pragma unroll 2
-    for (int i = -1; i < h.followers; ++i) {
-      const float* part = i < 0 ? first : rest + (size_t)i * 2 * F;
-      const float w = ex2(part[kItemRows * D + row] - m);
-      const float4* src = reinterpret_cast<const float4*>(part + (size_t)row * D + ch);
-      const float4 a = src[0], b = src[1];
-      l = fmaf(w, part[kItemRows * D + kItemRows + row], l);
-      const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] = fmaf(w, x[j], acc[j]);
-    }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    const int gr = h.row0 + row, t = gr / p.share, g = gr - t * p.share;
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {  // channels 2 j, 2 j + 1
-      const int c0 = 2 * j, c1 = c0 + 1;
-      const __half2 y = __floats2half2_rn(acc[((c0 & 3) << 1) + (c0 >> 2)] * inv, acc[((c1 & 3) << 1) + (c1 >> 2)] * inv);
-      o[j] = *reinterpret_cast<const uint32_t*>(&y);
-    }
-    *reinterpret_cast<uint4*>(p.out + (long long)(h.q0 + t) * p.ldo + (long long)(h.head * p.share + g) * D + ch) =
-        make_uint4(o[0], o[1], o[2], o[3]);
-  }
-}
-
-template <int D>
-tlq_status launch_one(const PrefillAttnParams& base, cudaStream_t stream) {
+tlq_status launch_one(const PrefillAttnParams& p, cudaStream_t stream) {
   using C = PCfg<D>;
   auto kernel = prefill_attention_kernel<D>;
   static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (attr != cudaSuccess) return cuda_error(attr, "kv4 attention: shared memory");
-  const int blocks = device_info().sms;
-  PrefillAttnParams p = base;
-  p.headers = reinterpret_cast<PHeader*>(p.partials);
-  p.partials = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.partials) +
-                                        ((blocks * sizeof(PHeader) + 255) & ~size_t(255)));
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)blocks, 1, 1);
+  lc.gridDim = dim3((unsigned)p.join.blocks, 1, 1);
   lc.blockDim = dim3(kThreads, 1, 1);
   lc.dynamicSmemBytes = C::SMEM;
   lc.stream = stream;
@@ -980,22 +1013,14 @@ tlq_status launch_one(const PrefillAttnParams& base, cudaStream_t stream) {
   at.val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = &at;
   lc.numAttrs = pdl_enabled() ? 1 : 0;
-  tlq_status st = cuda_error(cudaLaunchKernelEx(&lc, kernel, p), "kv4 prompt attention: launch");
-  if (st != TLQ_OK) return st;
-  lc.gridDim = dim3((unsigned)blocks, (unsigned)(kItemRows * D / 8 / 256), 1);
-  lc.blockDim = dim3(256, 1, 1);
-  lc.dynamicSmemBytes = 0;
-  return cuda_error(cudaLaunchKernelEx(&lc, prefill_join_kernel<D>, p), "kv4 prompt attention join: launch");
+  return cuda_error(cudaLaunchKernelEx(&lc, kernel, p), "kv4 prompt attention: launch");
 }
 
 }  // namespace
 
-size_t kv4_prefill_workspace(int head_dim) {
-  const size_t blocks = (size_t)device_info().sms;
-  return ((blocks * sizeof(PHeader) + 255) & ~size_t(255)) + blocks * 2 * kItemRows * (head_dim + 2) * sizeof(float);
-}
+size_t kv4_prefill_workspace(int head_dim) { return kv_join_bytes(device_info().sms, kItemRows, head_dim); }
 
-tlq_status launch_kv4_prefill(const KvAttention& a, int few_rows, cudaStream_t stream) {
+tlq_status launch_kv4_prefill(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream) {
   PrefillAttnParams p{};
   p.cache = a.cache;
   p.batch = a.batch;
@@ -1006,8 +1031,9 @@ tlq_status launch_kv4_prefill(const KvAttention& a, int few_rows, cudaStream_t s
   p.scale_log2 = (float)((double)a.scale * M_LOG2E);
   p.window = a.window;
   p.share = a.q_heads / a.cache.heads;
+  p.by_share = fast_div((uint32_t)p.share);
   p.few_rows = few_rows;
-  p.partials = static_cast<float*>(a.ws);
+  p.join = *join = kv_join_at(ws, device_info().sms, kItemRows);
   return a.head_dim == 64 ? launch_one<64>(p, stream) : launch_one<128>(p, stream);
 }
 

@@ -7,6 +7,22 @@
 
 namespace tlq {
 
+// n / d for n < 2^31 by one multiplication (d >= 1): m = ceil(2^(31 + s) / d)
+// with 2^s >= d errs by less than 1 / d.
+struct FastDiv {
+  uint32_t d, m;
+  int s;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, 0};
+  while ((1ull << f.s) < d) ++f.s;
+  f.m = (uint32_t)(((1ull << (31 + f.s)) + d - 1) / d);
+  return f;
+}
+__device__ __forceinline__ int divide(int n, const FastDiv& f) {
+  return (int)(((uint64_t)(uint32_t)n * f.m) >> (31 + f.s));
+}
+
 // The cache: blocks is [pages][heads][block_bytes]; a block holds the key
 // codes [page][D/2], the value codes [page][D/2], the key parameters
 // [page][D/group][2] and the value parameters (FP16 scale, minimum).  Keys and
@@ -177,14 +193,43 @@ struct KvAttention {
   long long ldo;
   float scale;
   int window;
-  void* ws;
 };
+// What the joining kernel needs of an item that a block began but did not end.
+struct KvJoinHeader {
+  int followers;  // blocks after this one that hold a part of the item; 0: nothing to join
+  int q0;         // first query of the request
+  int row0;       // first (query, head) row of the item
+  int rows;
+  int head;       // key head
+};
+// The parts that one kernel leaves: two to a block, of the item it ends (0) and
+// of the one it begins (1).
+struct KvJoin {
+  KvJoinHeader* headers;  // [blocks]
+  float* parts;           // [blocks][2][O [rows][D], m [rows], l [rows]]
+  int blocks, rows;
+};
+inline size_t kv_join_bytes(int blocks, int rows, int head_dim) {
+  return ((blocks * sizeof(KvJoinHeader) + 255) & ~size_t(255)) +
+         (size_t)blocks * 2 * rows * (head_dim + 2) * sizeof(float);
+}
+inline KvJoin kv_join_at(void* ws, int blocks, int rows) {
+  KvJoin j;
+  j.headers = static_cast<KvJoinHeader*>(ws);
+  j.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ((blocks * sizeof(KvJoinHeader) + 255) & ~size_t(255)));
+  j.blocks = blocks;
+  j.rows = rows;
+  return j;
+}
+
+// Requests of up to few_rows (query, head) rows to a key head go through the
+// first kernel, the others through the second; each passes over what is not its
+// own.  *_workspace: bytes of the parts; the launches say where they lie.
 size_t kv4_decode_workspace(int head_dim);
 size_t kv4_prefill_workspace(int head_dim);
-// Requests of up to few_rows (query, head) rows to a key head go through the
-// first, the others through the second; each passes over what is not its own.
-tlq_status launch_kv4_decode(const KvAttention& a, int few_rows, cudaStream_t stream);
-tlq_status launch_kv4_prefill(const KvAttention& a, int few_rows, cudaStream_t stream);
+tlq_status launch_kv4_decode(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream);
+tlq_status launch_kv4_prefill(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream);
+tlq_status launch_kv4_join(const KvAttention& a, const KvJoin& few, const KvJoin& many, cudaStream_t stream);
 
 struct LoraArgs {
   const __half* x;

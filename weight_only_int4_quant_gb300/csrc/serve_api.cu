@@ -179,7 +179,7 @@ tlq_status tl_kv4_read(const tl_kv4_cache* cache, const int64_t* slots, int toke
 size_t tl_kv4_attention_workspace_size(int q_heads, int heads, int head_dim, int max_q) {
   clear_error();
   if (q_heads < 1 || heads < 1 || q_heads % heads || (head_dim != 64 && head_dim != 128) || max_q < 0) return 0;
-  return std::max(kv4_decode_workspace(head_dim), kv4_prefill_workspace(head_dim));
+  return kv4_decode_workspace(head_dim) + kv4_prefill_workspace(head_dim);
 }
 
 tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_t ldq, int q_heads, uint16_t* out,
@@ -230,14 +230,16 @@ tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_
   a.scale = scale;
   // a window that no context outgrows is none
   a.window = window >= std::min((long long)ld_table * cache->page_size, kMaxContext) ? 0 : window;
-  a.ws = workspace;
   // The tensor-core kernel takes one scale a row, so rows in two groups stay
   // with the other one whatever their number.
   const int few = cache->head_dim == cache->group ? kFewRows : 0x7fffffff;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const tlq_status first = launch_kv4_decode(a, few, s);
-  if (first != TLQ_OK || (long long)max_q * (q_heads / a.cache.heads) <= few) return first;
-  return launch_kv4_prefill(a, few, s);
+  KvJoin few_parts{}, many_parts{};
+  tlq_status ls = launch_kv4_decode(a, few, workspace, &few_parts, s);
+  if (ls == TLQ_OK && (long long)max_q * (q_heads / a.cache.heads) > few)
+    ls = launch_kv4_prefill(a, few, static_cast<uint8_t*>(workspace) + kv4_decode_workspace(cache->head_dim),
+                            &many_parts, s);
+  return ls == TLQ_OK ? launch_kv4_join(a, few_parts, many_parts, s) : ls;
 }
 
 tlq_status tl_lora_add(const uint16_t* x, int64_t ldx, const uint16_t* A, const uint16_t* B, const float* scales,
