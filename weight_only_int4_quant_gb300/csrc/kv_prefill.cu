@@ -307,16 +307,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-__device__ __forceinline__ float4 lds_f32x4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ float2 lds_f32x2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ void sts_f32(uint32_t a, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
@@ -343,8 +333,10 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const PrefillAttnParams p) {
   using C = PCfg<D>;
   constexpr int KD = C::KD, VD = C::VD, TD = C::TD;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // Declared with 16 bytes' alignment, since more is not kept behind the static
+  // arrays (and the compiler would take it as given); rounded up to 1024 by hand.
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // still a shared address to the compiler
   uint8_t* const sq = smem;                       // [2][TILE]
   uint8_t* const sk = sq + 2 * C::TILE;           // [KD][TILE]
   uint8_t* const sv = sk + KD * C::TILE;          // [VD][TILE]
@@ -630,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
         }
         // whichever tile's weights are there first
         uint64_t since = 0;
+        uint32_t tries = 0;  // without a result
         while (ok && (left[0] | left[1])) {
           bool idle = true;
 #pragma unroll
@@ -654,12 +647,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
             }
           }
           if (!idle) {
-            since = 0;
-          } else if (since == 0) {
-            since = globaltimer_ns();
-          } else {
-            __nanosleep(20);
-            if (globaltimer_ns() - since > kWaitLimitNs) {
+            tries = 0;
+          } else if ((++tries & 255u) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (tries == 256) since = now;
+            if (now - since > kWaitLimitNs) {
               record_timeout(0x325);
               ok = false;
             }
@@ -729,14 +721,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       int s = sg.s0;
       for (; s < end; ++s, ++it, ++done) {
         ok = ok && mbar_wait_long(&bar->t_full[it % TD], (it / TD) & 1, 0x332) &&
-             mbar_wait_long(&bar->s_full[tile], done & 1, 0x333);
+             mbar_wait(&bar->s_full[tile], done & 1, 0x333);
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           const int key0 = s * kStage + half * kHalf;
           ok = __all_sync(0xffffffffu, ok);
           tc_fence_after();
-          const uint32_t tab = smem_u32(st + (it % TD) * C::TABLE) + half * (kHalf * 8) + qd * 16;
-          const uint32_t tab3 = smem_u32(st + (it % TD) * C::TABLE) + kStage * 16 + half * (kHalf * 4) + qd * 8;
+          const uint8_t* tab = st + (it % TD) * C::TABLE + half * (kHalf * 8) + qd * 16;
+          const uint8_t* tab3 = st + (it % TD) * C::TABLE + kStage * 16 + half * (kHalf * 4) + qd * 8;
           const uint32_t ts_addr = ts_tile + kHalf * half, tp_addr = ts_tile + (kHalf / 2) * half;  // S, weights over the first half
           // v[c][0]: columns 32 c .. of rows r, r + 8; v[c][1]: of rows r + 16, r + 24
           float v[2][2][16];
@@ -753,8 +745,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
             tmem_wait_ld(v[c][1]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {  // column pair 32 c + 8 k + 2 qd
-              const float4 ab = lds_f32x4(tab + (16 * c + 4 * k) * 16);
-              const float4 lr = lds_f32x4(tab + (16 * c + 4 * k) * 16 + kStage * 8);
+              const float4 ab = *reinterpret_cast<const float4*>(tab + (16 * c + 4 * k) * 16);
+              const float4 lr = *reinterpret_cast<const float4*>(tab + (16 * c + 4 * k) * 16 + kStage * 8);
               rc[c][k] = make_float2(lr.z, lr.w);
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
@@ -831,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
             uint32_t pw[2][8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float2 rb = lds_f32x2(tab3 + (16 * c + 4 * k) * 8);
+              const float2 rb = *reinterpret_cast<const float2*>(tab3 + (16 * c + 4 * k) * 8);
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 const float* x = &v[c][y >> 1][4 * k + 2 * (y & 1)];
