@@ -5,7 +5,7 @@
 //   logit_ij = scale (s_j (q_i . c_j) + b_j sum(q_i)),  p' = p s'_j,
 //   o_i = (sum_j p'_ij c'_j + sum_j p_ij b'_j) / sum_j p_ij
 // The codes go to the matrix instructions exactly, as the FP16 subnormals
-// c * 2^-24 (a mask and at most one shift per pair); scales and minima are
+// c * 2^-24 (a mask, and a shift for most, per pair); scales and minima are
 // applied in FP32 in the softmax.  The only roundings to FP16 are those of the
 // weights p' and of the result.  Value codes enter as c - 8: a weight's rounding
 // then meets a factor of about the spread of the values (an uncentred code's
@@ -532,28 +532,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           sts_f32(t2, live[j] ? lg2(vsc) : -INFINITY);
           sts_f32(t2 + 8, live[j] ? rc : 0.f);
           sts_f32(t3, live[j] ? fmaf(rc, vb.y, 8.0f) : 0.f);  // the value codes are centred: c - 8
+        }
+        // c 2^-24 of a key, (c - 8) 2^-24 of a value, exact; one form of the code
+        // for both (the kernel's loops together outgrow the instruction cache)
+        const uint32_t eight = val ? 0x00080008u : 0u;
 #pragma unroll
-          for (int i = 0; i < W; ++i) {
-            const uint32_t w4[4] = {cw[j][i].x, cw[j][i].y, cw[j][i].z, cw[j][i].w};
+        for (int i = 0; i < W; ++i) {
+          const uint32_t w4[4] = {cw[j][i].x, cw[j][i].y, cw[j][i].z, cw[j][i].w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t w = w4[k], c = 4 * i + k;  // 8-channel piece c
-              sts128(dst + (c >> 3) * C::BLOCK + (((c & 7) ^ sw) << 4), w & 0x000F000Fu, (w >> 4) & 0x000F000Fu,
-                     (w >> 8) & 0x000F000Fu, (w >> 12) & 0x000F000Fu);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < W; ++i) {
-            const uint32_t w4[4] = {cw[j][i].x, cw[j][i].y, cw[j][i].z, cw[j][i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t w = w4[k], x = w >> 8, c = 4 * i + k;
-              // (c - 8) 2^-24, exact; odd channels enter 16 times too large, which the output takes back
-              sts128(dst + (c >> 3) * C::BLOCK + (((c & 7) ^ sw) << 4), hsub2u(w & 0x000F000Fu, 0x00080008u),
-                     hsub2u(w & 0x00F000F0u, 0x00800080u), hsub2u(x & 0x000F000Fu, 0x00080008u),
-                     hsub2u(x & 0x00F000F0u, 0x00800080u));
-            }
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t w = w4[k], c = 4 * i + k;  // 8-channel piece c
+            sts128(dst + (c >> 3) * C::BLOCK + (((c & 7) ^ sw) << 4), hsub2u(w & 0x000F000Fu, eight),
+                   hsub2u((w >> 4) & 0x000F000Fu, eight), hsub2u((w >> 8) & 0x000F000Fu, eight),
+                   hsub2u((w >> 12) & 0x000F000Fu, eight));
           }
         }
       }
@@ -879,6 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       tc_fence_after();
       const bool whole = sg.first && sg.last;
       const int row0 = 32 * quarter + r;  // this thread's rows: row0 + 8 y
+      const float up = 16777216.0f;       // codes were entered as c 2^-24
       if (whole) {
         float inv[4];
         __half* orow[4];
@@ -904,10 +896,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
             for (int e = 0; e < 2; ++e) {
               const int y = 2 * h + e;
               // Of 8 channels k = 0 .. 3 this thread holds qd' and qd' + 4 (qd' = 0 1 2 3:
-              // positions 0 1 | 2 3 | 4 5 | 6 7 are channels 0 4 | 1 5 | 2 6 | 3 7;
-              // odd channels are 16 times too large).  The quad transposes: each
-              // thread takes one whole group of 8, k = qd.
-              const float up = (qd & 1) ? 1048576.0f : 16777216.0f;
+              // positions 0 1 | 2 3 | 4 5 | 6 7 are channels 0 4 | 1 5 | 2 6 | 3 7).  The
+              // quad transposes: each thread takes one whole group of 8, k = qd.
               uint32_t mine[4];  // (channel qd, channel qd + 4) of group k
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -941,7 +931,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       } else {
         // a partial, its columns in TMEM's order
         float* const part = p.join.parts + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * (kItemRows * (D + 2));
-        const float up = (qd & 1) ? 1048576.0f : 16777216.0f;
 #pragma unroll 1
         for (int b = 0; b < D / 32; ++b) {
 #pragma unroll
