@@ -33,6 +33,7 @@
 // contiguous piece), and runs ahead over the ends of items.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "serve.cuh"
 
@@ -78,6 +79,22 @@ __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// D = A B
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -289,6 +306,8 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
     return;
   }
 
+  const int sw = qd & 1, other = sw ? -(D / 2) : D / 2;
+  const uint32_t sel_lo = sw ? 0x1054u : 0x5410u, sel_hi = sw ? 0x3276u : 0x7632u;
   // this warp's tiles inside a stage
   uint32_t kofs[kTiles], pofs[kTiles];
 #pragma unroll
@@ -396,48 +415,45 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
 
     for (int s = sg.s0; s < sg.s1; ++s, ++stage_i) {
       const int slot = stage_i % DEPTH;
-      ok = ok && mbar_wait_long(&full[slot], (stage_i / DEPTH) & 1, 0x301);
+      ok = ok && mbar_wait(&full[slot], (stage_i / DEPTH) & 1, 0x301);
       if (!ok) break;
       const int tok0 = s * kStage + warp * (kTiles * kTile);
       const uint32_t tiles = lds32(smem_u32(&there[slot])) >> (warp * kTiles);
       const uint32_t sb = smem_u32(smem) + slot * C::STAGE_BYTES;
-      if (tok0 < sg.hi && tok0 + kTiles * kTile > sg.lo && (tiles & ((1u << kTiles) - 1u))) {
-        // some row does not see some key of the tiles, or a page is missing
-        const bool edge = tok0 < sg.all_lo || tok0 + kTiles * kTile > sg.all_hi ||
-                          (~tiles & ((1u << kTiles) - 1u)) != 0;
+      // EDGE: some row does not see some key of the tiles, or a page is missing
+      auto work = [&](auto edge_form) __attribute__((always_inline)) {
+        constexpr bool EDGE = decltype(edge_form)::value;
         constexpr int JT = C::JOINT;
 #pragma unroll
         for (int i0 = 0; i0 < kTiles; i0 += JT) {
           float lw[JT][NT][2][2];  // [token half][column]: logits, in log2 units
           float vlg[JT][2][NG], vrc[JT][2][NG], vmi[JT][2][NG];
-          bool over = false;
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < JT; ++i) {
             // S^T = K Q^T on the codes, per group of channels
             float sc[NT][NG][4];
-  #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-  #pragma unroll
-              for (int g = 0; g < NG; ++g)
-  #pragma unroll
-                for (int k = 0; k < 4; ++k) sc[nt][g][k] = 0.f;
             const uint32_t kb = sb + kofs[i0 + i];
-  #pragma unroll
+#pragma unroll
             for (int h = 0; h < H; ++h) {
               const uint2 ka = lds64(kb + r * (D / 2) + 32 * h + 8 * qd);
               const uint2 kc = lds64(kb + (r + 8) * (D / 2) + 32 * h + 8 * qd);
-  #pragma unroll
+#pragma unroll
               for (int j = 0; j < 2; ++j) {
                 const uint32_t wa = j ? ka.y : ka.x, wc = j ? kc.y : kc.x;
-  #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const uint32_t xa = e ? wa >> 8 : wa, xc = e ? wc >> 8 : wc;
                   const uint32_t a0 = xa & 0x000F000Fu, a1 = xc & 0x000F000Fu;
                   const uint32_t a2 = xa & 0x00F000F0u, a3 = xc & 0x00F000F0u;
                   const int ks = 4 * h + 2 * j + e;
-  #pragma unroll
-                  for (int nt = 0; nt < NT; ++nt)
-                    mma_16816(sc[nt][NG == 1 ? 0 : h], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    float(&d)[4] = sc[nt][NG == 1 ? 0 : h];
+                    if (NG == 1 ? ks == 0 : ks == 4 * h)
+                      mma_16816_first(d, a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+                    else
+                      mma_16816(d, a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+                  }
                 }
               }
             }
@@ -445,55 +461,70 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
             const uint32_t kp = sb + pofs[i0 + i], vp = kp + chunk * (NG * 4);
             float ksc[2][NG], kmi[2][NG];
             bool in[2];
-  #pragma unroll
+#pragma unroll
             for (int y = 0; y < 2; ++y) {
               const int tk = r + 8 * y, key = tok0 + (i0 + i) * kTile + tk;
-              in[y] = !edge || (key >= sg.lo && key < sg.hi && (tiles >> (i0 + i) & 1u));  // else no token of ours lies there
-  #pragma unroll
+              in[y] = !EDGE || (key >= sg.lo && key < sg.hi && (tiles >> (i0 + i) & 1u));  // else no token of ours lies there
+#pragma unroll
               for (int g = 0; g < NG; ++g) {
                 uint32_t a = lds32(kp + (tk * NG + g) * 4), b = lds32(vp + (tk * NG + g) * 4);
-                a = in[y] ? a : 0x00003C00u;  // scale 1, minimum 0
-                b = in[y] ? b : 0x00003C00u;
+                if (!in[y]) a = b = 0x00003C00u;  // scale 1, minimum 0
                 const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
                 const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
                 ksc[y][g] = fa.x;
                 kmi[y][g] = fa.y;
                 const float vs = fmaxf(fb.x, 5.9604644775390625e-8f);
                 vlg[i][y][g] = lg2(vs);
-                vrc[i][y][g] = __fdividef(1.0f, vs);
+                vrc[i][y][g] = reciprocal(vs);
                 vmi[i][y][g] = fb.y;
               }
             }
-  #pragma unroll
+#pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-  #pragma unroll
+#pragma unroll
               for (int y = 0; y < 2; ++y)
-  #pragma unroll
+#pragma unroll
                 for (int c = 0; c < 2; ++c) {
                   float x = fmaf(sc[nt][0][2 * y + c] * f[nt][c], ksc[y][0], kmi[y][0] * qs[nt][c][0]);
                   if constexpr (NG == 2)
                     x = fmaf(sc[nt][1][2 * y + c] * f[nt][c], ksc[y][1], fmaf(kmi[y][1], qs[nt][c][1], x));
-                  if (edge) {
+                  if constexpr (EDGE) {
                     const int key = tok0 + (i0 + i) * kTile + r + 8 * y;
                     const int at = base_pos + divide(row0 + min(8 * nt + 2 * qd + c, rows - 1), p.by_share);  // the row's position
                     const bool see = in[y] && key <= at && (p.window <= 0 || key > at - p.window);
                     x = see ? x : -INFINITY;
                   }
                   lw[i][nt][y][c] = x;
-                  float a = x + vlg[i][y][0];
-                  if constexpr (NG == 2) a = x + fmaxf(vlg[i][y][0], vlg[i][y][1]);
-                  over |= a > m[nt][c] + kTrigger;
                 }
           }
-          if (__any_sync(0xffffffffu, over)) {
-  #pragma unroll
+          // exponents of the weights p s', under the rows' references
+          float ew[JT][NT][2][NG][2];
+          auto exponents = [&]() __attribute__((always_inline)) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < JT; ++i)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                  for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                      ew[i][nt][y][g][c] = lw[i][nt][y][c] + (vlg[i][y][g] - m[nt][c]);
+                      top = fmaxf(top, ew[i][nt][y][g][c]);
+                    }
+            return top;
+          };
+          if (__any_sync(0xffffffffu, exponents() > kTrigger)) {
+#pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-  #pragma unroll
+#pragma unroll
               for (int c = 0; c < 2; ++c) {
                 float x = -INFINITY;
-  #pragma unroll
+#pragma unroll
                 for (int i = 0; i < JT; ++i)
-  #pragma unroll
+#pragma unroll
                   for (int y = 0; y < 2; ++y) {
                     float lg = vlg[i][y][0];
                     if constexpr (NG == 2) lg = fmaxf(lg, vlg[i][y][1]);
@@ -507,36 +538,36 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
                   const float w = ex2(m[nt][c] - next);  // 0 for the first reference
                   m[nt][c] = next;
                   l[nt][c] *= w;
-  #pragma unroll
+#pragma unroll
                   for (int g = 0; g < NG; ++g) beta[nt][c][g] *= w;
-  #pragma unroll
+#pragma unroll
                   for (int j = 0; j < 4 * H; ++j) {
                     o[nt][j][c] *= w;
                     o[nt][j][2 + c] *= w;
                   }
                 }
               }
+            exponents();
           }
 
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < JT; ++i) {
             // weights p s' as FP16, their sums, and P^T fragments
             uint32_t pf[NT][NG][2];
-  #pragma unroll
+#pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-  #pragma unroll
+#pragma unroll
               for (int y = 0; y < 2; ++y)
-  #pragma unroll
+#pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                  const __half2 h2 = __floats2half2_rn(ex2(lw[i][nt][y][0] + (vlg[i][y][g] - m[nt][0])),
-                                                       ex2(lw[i][nt][y][1] + (vlg[i][y][g] - m[nt][1])));
+                  const __half2 h2 = __floats2half2_rn(ex2(ew[i][nt][y][g][0]), ex2(ew[i][nt][y][g][1]));
                   const float2 back = __half22float2(h2);
                   const float w[2] = {back.x * vrc[i][y][g], back.y * vrc[i][y][g]};
-  #pragma unroll
+#pragma unroll
                   for (int c = 0; c < 2; ++c) {
                     if (g == 0) l[nt][c] += w[c];
                     // a minimum that this row does not see is left out, whatever it holds
-                    const float mi = edge && w[c] == 0.f ? 0.f : vmi[i][y][g];
+                    const float mi = EDGE && w[c] == 0.f ? 0.f : vmi[i][y][g];
                     beta[nt][c][g] = fmaf(w[c], mi, beta[nt][c][g]);
                   }
                   pf[nt][g][y] = movmatrix(*reinterpret_cast<const uint32_t*>(&h2));
@@ -545,24 +576,21 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
             // O^T += V^T P^T: word 8 h + r of tokens 2 qd, 2 qd + 1, + 8, + 9.
             // Odd lanes of a quad read their two tokens in the other order
             // (banks), the byte selectors put them back.
-            const uint32_t vb = sb + kofs[i0 + i] + chunk * (D / 2);
-            const int sw = qd & 1;
-            const uint32_t sel_lo = sw ? 0x1054u : 0x5410u, sel_hi = sw ? 0x3276u : 0x7632u;
-  #pragma unroll
+            const uint32_t vb = sb + kofs[i0 + i] + chunk * (D / 2) + 4 * r + (2 * qd + sw) * (D / 2);
+#pragma unroll
             for (int h = 0; h < H; ++h) {
-              const uint32_t at = vb + 32 * h + 4 * r + (2 * qd) * (D / 2);
-              const uint32_t t0 = lds32(at + sw * (D / 2)), t1 = lds32(at + (sw ^ 1) * (D / 2));
-              const uint32_t t8 = lds32(at + (8 + sw) * (D / 2)), t9 = lds32(at + (8 + (sw ^ 1)) * (D / 2));
+              const uint32_t t0 = lds32(vb + 32 * h), t1 = lds32(vb + 32 * h + other);
+              const uint32_t t8 = lds32(vb + 32 * h + 8 * (D / 2)), t9 = lds32(vb + 32 * h + 8 * (D / 2) + other);
               const uint32_t wl[2] = {prmt(t0, t1, sel_lo), prmt(t0, t1, sel_hi)};
               const uint32_t wh[2] = {prmt(t8, t9, sel_lo), prmt(t8, t9, sel_hi)};
-  #pragma unroll
+#pragma unroll
               for (int j = 0; j < 2; ++j)
-  #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const uint32_t xa = e ? wl[j] >> 8 : wl[j], xc = e ? wh[j] >> 8 : wh[j];
                   const uint32_t a0 = xa & 0x000F000Fu, a1 = xa & 0x00F000F0u;  // channels 4 j + 2 e, + 1 of the word
                   const uint32_t a2 = xc & 0x000F000Fu, a3 = xc & 0x00F000F0u;
-  #pragma unroll
+#pragma unroll
                   for (int nt = 0; nt < NT; ++nt)
                     mma_16816(o[nt][4 * h + 2 * j + e], a0, a1, a2, a3, pf[nt][NG == 1 ? 0 : h][0],
                               pf[nt][NG == 1 ? 0 : h][1]);
@@ -570,7 +598,12 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
             }
           }
         }
-      }
+      };
+      const uint32_t both = (1u << kTiles) - 1u;
+      if (tok0 >= sg.all_lo && tok0 + kTiles * kTile <= sg.all_hi && (tiles & both) == both)
+        work(std::false_type{});
+      else if (tok0 < sg.hi && tok0 + kTiles * kTile > sg.lo && (tiles & both))
+        work(std::true_type{});
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[slot]);
     }
