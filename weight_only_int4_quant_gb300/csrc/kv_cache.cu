@@ -39,24 +39,6 @@ __device__ __forceinline__ bool in_cache(const KvCache& c, long long slot) {
   return slot >= 0 && slot < c.num_pages << c.page_shift;
 }
 
-// Two FP32 operations in one instruction, each rounded as by itself.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
-      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n"
-      " mov.b64 {%0, %1}, w;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
 // The word of eight codes rint((x - b) / s), and whether all of them are
 // certain.  inv is 1 / s to one unit in the last place and the product is
 // rounded once, to a whole number n, by adding 2^23; so n - 1/2 <= t <= n + 1/2

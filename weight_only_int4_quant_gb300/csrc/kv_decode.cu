@@ -322,91 +322,100 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
     const KvRequest rq = sg.rq;
     const int head = sg.head, row0 = sg.row0, rows = sg.rows, base_pos = rq.len - rq.q_len;
     // Query fragments: row n = 8 nt + r, channels 64 h + 16 qd .. + 15, scaled
-    // by a power of two so that the row's largest value lies in [2^14, 2^15)
-    // (an exact product; q / 16 for the odd nibbles then stays normal).
+    // by a power of two so that the item's largest value lies in [2^14, 2^15)
+    // (exact, and q / 16 for the odd nibbles stays normal, down to 2^-24 of it).
     uint32_t qf[NT][4 * H][2];
-    float f[NT][2], qs[NT][2][NG];  // of this thread's columns (rows 2 qd, 2 qd + 1)
+    float2 qs[NT][NG];  // scaled sums of this thread's columns (rows 2 qd, 2 qd + 1)
+    float f;            // codes' products to logits
+    {
+      uint4 raw[NT][H][2];
+      float sum[NT][H], big = 0.f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = 8 * nt + r;
-      const bool on = row < rows;
-      const int gr = row0 + (on ? row : 0);
-      const int t = divide(gr, p.by_share), g = gr - t * p.share;
-      const __half* src = p.q + (long long)(rq.q0 + t) * p.ldq + (long long)(head * p.share + g) * D;
-      uint4 raw[H][2];
-      float sum[H], big = 0.f;
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = 8 * nt + r;
+        const bool on = row < rows;
+        const int gr = row0 + (on ? row : 0);
+        const int t = divide(gr, p.by_share), g = gr - t * p.share;
+        const __half* src = p.q + (long long)(rq.q0 + t) * p.ldq + (long long)(head * p.share + g) * D;
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        sum[h] = 0.f;
+        for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          raw[h][j] = on ? *reinterpret_cast<const uint4*>(src + 64 * h + 16 * qd + 8 * j) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {raw[h][j].x, raw[h][j].y, raw[h][j].z, raw[h][j].w};
+          for (int j = 0; j < 2; ++j)
+            raw[nt][h][j] =
+                on ? *reinterpret_cast<const uint4*>(src + 64 * h + 16 * qd + 8 * j) : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-            sum[h] += v.x + v.y;
-            big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          sum[nt][h] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t w[4] = {raw[nt][h][j].x, raw[nt][h][j].y, raw[nt][h][j].z, raw[nt][h][j].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+              sum[nt][h] += v.x + v.y;
+              big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
+            }
           }
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) sum[nt][h] += __shfl_xor_sync(0xffffffffu, sum[nt][h], o);
         }
-      }
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-#pragma unroll
-        for (int h = 0; h < H; ++h) sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], o);
-      }
-      int e = 0;  // 2^e * big in [2^14, 2^15); 0 for zero, infinite and NaN rows
+      for (int o = 1; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      int e = 0;  // 2^e * big in [2^14, 2^15); 0 where all are zero or one is infinite
       if (big > 0.f && big < 65536.f) e = 14 + 127 - (int)(__float_as_uint(big) >> 23);
       const float up = __uint_as_float((uint32_t)(127 + e) << 23);
       const float up16 = __uint_as_float((uint32_t)(127 + e - 4) << 23);
+      f = p.scale_log2 * __uint_as_float((uint32_t)(127 + 24 - e) << 23);
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t w[4] = {raw[h][j].x, raw[h][j].y, raw[h][j].z, raw[h][j].w};
-          // pairs (ch 0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16 of the code word
-          float2 v[4];
+        for (int h = 0; h < H; ++h) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-          const __half2 a0 = __floats2half2_rn(v[0].x * up, v[2].x * up);
-          const __half2 a1 = __floats2half2_rn(v[0].y * up16, v[2].y * up16);
-          const __half2 a2 = __floats2half2_rn(v[1].x * up, v[3].x * up);
-          const __half2 a3 = __floats2half2_rn(v[1].y * up16, v[3].y * up16);
-          qf[nt][4 * h + 2 * j][0] = *reinterpret_cast<const uint32_t*>(&a0);
-          qf[nt][4 * h + 2 * j][1] = *reinterpret_cast<const uint32_t*>(&a1);
-          qf[nt][4 * h + 2 * j + 1][0] = *reinterpret_cast<const uint32_t*>(&a2);
-          qf[nt][4 * h + 2 * j + 1][1] = *reinterpret_cast<const uint32_t*>(&a3);
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t w[4] = {raw[nt][h][j].x, raw[nt][h][j].y, raw[nt][h][j].z, raw[nt][h][j].w};
+            // pairs (ch 0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16 of the code word
+            float2 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+            const __half2 a0 = __floats2half2_rn(v[0].x * up, v[2].x * up);
+            const __half2 a1 = __floats2half2_rn(v[0].y * up16, v[2].y * up16);
+            const __half2 a2 = __floats2half2_rn(v[1].x * up, v[3].x * up);
+            const __half2 a3 = __floats2half2_rn(v[1].y * up16, v[3].y * up16);
+            qf[nt][4 * h + 2 * j][0] = *reinterpret_cast<const uint32_t*>(&a0);
+            qf[nt][4 * h + 2 * j][1] = *reinterpret_cast<const uint32_t*>(&a1);
+            qf[nt][4 * h + 2 * j + 1][0] = *reinterpret_cast<const uint32_t*>(&a2);
+            qf[nt][4 * h + 2 * j + 1][1] = *reinterpret_cast<const uint32_t*>(&a3);
+          }
         }
-      }
-      const float down = p.scale_log2 * __uint_as_float((uint32_t)(127 + 24 - e) << 23);
+        float s[2][2];  // [column][half]
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int src_lane = (2 * qd + c) * 4;
-        f[nt][c] = __shfl_sync(0xffffffffu, down, src_lane);
-        float s0 = __shfl_sync(0xffffffffu, sum[0], src_lane);
-        if constexpr (H == 2) {
-          const float s1 = __shfl_sync(0xffffffffu, sum[1], src_lane);
-          if constexpr (NG == 1)
-            s0 += s1;
-          else
-            qs[nt][c][1] = s1 * p.scale_log2;
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            s[c][h] = __shfl_sync(0xffffffffu, sum[nt][h], (2 * qd + c) * 4) * p.scale_log2;
+        if constexpr (H == 1) {
+          qs[nt][0] = make_float2(s[0][0], s[1][0]);
+        } else if constexpr (NG == 1) {
+          qs[nt][0] = make_float2(s[0][0] + s[0][1], s[1][0] + s[1][1]);
+        } else {
+          qs[nt][0] = make_float2(s[0][0], s[1][0]);
+          qs[nt][NG - 1] = make_float2(s[0][1], s[1][1]);
         }
-        qs[nt][c][0] = s0 * p.scale_log2;
       }
     }
 
     float o[NT][4 * H][4];
-    float m[NT][2], l[NT][2], beta[NT][2][NG];
+    float m[NT][2];
+    float2 l[NT], beta[NT][NG];  // by column
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = kNone;
+      l[nt] = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        m[nt][c] = kNone;
-        l[nt][c] = 0.f;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) beta[nt][c][g] = 0.f;
-      }
+      for (int g = 0; g < NG; ++g) beta[nt][g] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < 4 * H; ++j)
 #pragma unroll
@@ -426,7 +435,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
         constexpr int JT = C::JOINT;
 #pragma unroll
         for (int i0 = 0; i0 < kTiles; i0 += JT) {
-          float lw[JT][NT][2][2];  // [token half][column]: logits, in log2 units
+          float2 lw[JT][NT][2];  // [token half]: logits of the two columns, in log2 units
           float vlg[JT][2][NG], vrc[JT][2][NG], vmi[JT][2][NG];
 #pragma unroll
           for (int i = 0; i < JT; ++i) {
@@ -471,7 +480,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
                 if (!in[y]) a = b = 0x00003C00u;  // scale 1, minimum 0
                 const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
                 const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
-                ksc[y][g] = fa.x;
+                ksc[y][g] = fa.x * f;
                 kmi[y][g] = fa.y;
                 const float vs = fmaxf(fb.x, 5.9604644775390625e-8f);
                 vlg[i][y][g] = lg2(vs);
@@ -483,22 +492,27 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int y = 0; y < 2; ++y)
+              {
+                float2 x = mul2(make_float2(kmi[y][0], kmi[y][0]), qs[nt][0]);
+                x = fma2(make_float2(sc[nt][0][2 * y], sc[nt][0][2 * y + 1]), make_float2(ksc[y][0], ksc[y][0]), x);
+                if constexpr (NG == 2) {
+                  x = fma2(make_float2(kmi[y][1], kmi[y][1]), qs[nt][1], x);
+                  x = fma2(make_float2(sc[nt][1][2 * y], sc[nt][1][2 * y + 1]), make_float2(ksc[y][1], ksc[y][1]), x);
+                }
+                if constexpr (EDGE) {
+                  const int key = tok0 + (i0 + i) * kTile + r + 8 * y;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  float x = fmaf(sc[nt][0][2 * y + c] * f[nt][c], ksc[y][0], kmi[y][0] * qs[nt][c][0]);
-                  if constexpr (NG == 2)
-                    x = fmaf(sc[nt][1][2 * y + c] * f[nt][c], ksc[y][1], fmaf(kmi[y][1], qs[nt][c][1], x));
-                  if constexpr (EDGE) {
-                    const int key = tok0 + (i0 + i) * kTile + r + 8 * y;
+                  for (int c = 0; c < 2; ++c) {
                     const int at = base_pos + divide(row0 + min(8 * nt + 2 * qd + c, rows - 1), p.by_share);  // the row's position
                     const bool see = in[y] && key <= at && (p.window <= 0 || key > at - p.window);
-                    x = see ? x : -INFINITY;
+                    if (!see) (c ? x.y : x.x) = -INFINITY;
                   }
-                  lw[i][nt][y][c] = x;
                 }
+                lw[i][nt][y] = x;
+              }
           }
           // exponents of the weights p s', under the rows' references
-          float ew[JT][NT][2][NG][2];
+          float2 ew[JT][NT][2][NG];
           auto exponents = [&]() __attribute__((always_inline)) {
             float top = -INFINITY;
 #pragma unroll
@@ -508,12 +522,11 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
 #pragma unroll
-                  for (int g = 0; g < NG; ++g)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                      ew[i][nt][y][g][c] = lw[i][nt][y][c] + (vlg[i][y][g] - m[nt][c]);
-                      top = fmaxf(top, ew[i][nt][y][g][c]);
-                    }
+                  for (int g = 0; g < NG; ++g) {
+                    const float2 less = add2(make_float2(vlg[i][y][g], vlg[i][y][g]), make_float2(-m[nt][0], -m[nt][1]));
+                    ew[i][nt][y][g] = add2(lw[i][nt][y], less);
+                    top = fmaxf(top, fmaxf(ew[i][nt][y][g].x, ew[i][nt][y][g].y));
+                  }
             return top;
           };
           if (__any_sync(0xffffffffu, exponents() > kTrigger)) {
@@ -528,7 +541,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
                   for (int y = 0; y < 2; ++y) {
                     float lg = vlg[i][y][0];
                     if constexpr (NG == 2) lg = fmaxf(lg, vlg[i][y][1]);
-                    x = fmaxf(x, lw[i][nt][y][c] + lg);
+                    x = fmaxf(x, (c ? lw[i][nt][y].y : lw[i][nt][y].x) + lg);
                   }
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
@@ -537,9 +550,9 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
                 if (next > m[nt][c]) {
                   const float w = ex2(m[nt][c] - next);  // 0 for the first reference
                   m[nt][c] = next;
-                  l[nt][c] *= w;
+                  (c ? l[nt].y : l[nt].x) *= w;
 #pragma unroll
-                  for (int g = 0; g < NG; ++g) beta[nt][c][g] *= w;
+                  for (int g = 0; g < NG; ++g) (c ? beta[nt][g].y : beta[nt][g].x) *= w;
 #pragma unroll
                   for (int j = 0; j < 4 * H; ++j) {
                     o[nt][j][c] *= w;
@@ -560,15 +573,14 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
               for (int y = 0; y < 2; ++y)
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                  const __half2 h2 = __floats2half2_rn(ex2(ew[i][nt][y][g][0]), ex2(ew[i][nt][y][g][1]));
-                  const float2 back = __half22float2(h2);
-                  const float w[2] = {back.x * vrc[i][y][g], back.y * vrc[i][y][g]};
-#pragma unroll
-                  for (int c = 0; c < 2; ++c) {
-                    if (g == 0) l[nt][c] += w[c];
-                    // a minimum that this row does not see is left out, whatever it holds
-                    const float mi = EDGE && w[c] == 0.f ? 0.f : vmi[i][y][g];
-                    beta[nt][c][g] = fmaf(w[c], mi, beta[nt][c][g]);
+                  const __half2 h2 = __floats2half2_rn(ex2(ew[i][nt][y][g].x), ex2(ew[i][nt][y][g].y));
+                  const float2 w = mul2(__half22float2(h2), make_float2(vrc[i][y][g], vrc[i][y][g]));
+                  if (g == 0) l[nt] = add2(l[nt], w);
+                  if constexpr (EDGE) {  // a minimum that a row does not see is left out, whatever it holds
+                    if (w.x != 0.f) beta[nt][g].x = fmaf(w.x, vmi[i][y][g], beta[nt][g].x);
+                    if (w.y != 0.f) beta[nt][g].y = fmaf(w.y, vmi[i][y][g], beta[nt][g].y);
+                  } else {
+                    beta[nt][g] = fma2(w, make_float2(vmi[i][y][g], vmi[i][y][g]), beta[nt][g]);
                   }
                   pf[nt][g][y] = movmatrix(*reinterpret_cast<const uint32_t*>(&h2));
                 }
@@ -614,18 +626,21 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
+        float lc = c ? l[nt].y : l[nt].x, bc[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) bc[g] = c ? beta[nt][g].y : beta[nt][g].x;
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
-          l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+          lc += __shfl_xor_sync(0xffffffffu, lc, x);
 #pragma unroll
-          for (int g = 0; g < NG; ++g) beta[nt][c][g] += __shfl_xor_sync(0xffffffffu, beta[nt][c][g], x);
+          for (int g = 0; g < NG; ++g) bc[g] += __shfl_xor_sync(0xffffffffu, bc[g], x);
         }
         if (r == 0) {
           float* st = stats + (warp * R + 8 * nt + 2 * qd + c) * (2 + NG);
           st[0] = m[nt][c];
-          st[1] = l[nt][c];
+          st[1] = lc;
 #pragma unroll
-          for (int g = 0; g < NG; ++g) st[2 + g] = beta[nt][c][g];
+          for (int g = 0; g < NG; ++g) st[2 + g] = bc[g];
         }
       }
     const bool whole = sg.first && sg.last;
