@@ -93,6 +93,7 @@ class _KV4Cache(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_f16 = _f32 = _i32 = _i64 = _u8 = None  # torch's types, once the library is loaded
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -109,7 +110,10 @@ def load():
         if _lib is not None:
             return _lib
         try:  # share the process's CUDA runtime with torch
-            import torch  # noqa: F401
+            import torch
+
+            global _f16, _f32, _i32, _i64, _u8
+            _f16, _f32, _i32, _i64, _u8 = torch.float16, torch.float32, torch.int32, torch.int64, torch.uint8
         except ImportError:
             pass
         if not os.path.exists(_LIB_PATH):
@@ -176,7 +180,7 @@ def _stream(stream):
 
     if stream is None:
         # the raw handle: torch.cuda.current_stream() builds a Stream object, 3 us of every call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -497,15 +501,15 @@ def tl_selftest_wait_timeout(limit_us: int, stream=None) -> None:
 # multi-request serving: paged 4-bit cache, attention, tables, adapters
 # ---------------------------------------------------------------------------
 
-# These calls are made per step, several to a step, so their checks take the
-# short way through for arguments that are as they should be (a serving step's
-# kernels run for a few microseconds); what is not goes on to the full checks
-# and their messages.
+# These calls are made per step, several to a step, and their kernels run for a
+# few microseconds, so their checks take the short way through for arguments
+# that are as they should be; what is not goes on to the full checks and their
+# messages.
 
 def _ptr(t, dtype, name):
     """Data pointer of a contiguous CUDA tensor of one dtype."""
     try:
-        if t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
@@ -534,21 +538,44 @@ def _rows(t, dtype, name, dims):
     return t.data_ptr(), (stride[0] if shape[0] > 1 else max(inner, 8))
 
 
-def _ints(t, dtype, name, n=None):
-    p = _ptr(t, dtype, name)
-    if n is not None and t.numel() != n:
+def _rows2(t, dtype, name, n):
+    """_rows of a [tokens, n] tensor: (pointer, stride, tokens)."""
+    if t.dtype is dtype and t.is_cuda and t.dim() == 2:
+        tokens, cols = t.shape
+        ld, one = t.stride()
+        if cols == n and one == 1 and tokens > 1:
+            return t.data_ptr(), ld, tokens
+    p, ld = _rows(t, dtype, name, (n,))
+    return p, ld, t.shape[0]
+
+
+def _rows3(t, dtype, name, a, b):
+    """_rows of a [tokens, a, b] tensor: (pointer, stride, tokens)."""
+    if t.dtype is dtype and t.is_cuda and t.dim() == 3:
+        tokens, x, y = t.shape
+        ld, mid, one = t.stride()
+        if x == a and y == b and one == 1 and mid == b and tokens > 1:
+            return t.data_ptr(), ld, tokens
+    p, ld = _rows(t, dtype, name, (a, b))
+    return p, ld, t.shape[0]
+
+
+def _ints(t, dtype, name, n):
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() == n:
+        return t.data_ptr()
+    p = _dev(t, (dtype,), name)
+    if t.numel() != n:
         raise ValueError("%s has %d elements, expected %d" % (name, t.numel(), n))
     return p
 
 
 def _table(table, requests):
-    import torch
-
-    p = _ptr(table, torch.int32, "table")
-    shape = table.shape
-    if len(shape) != 2 or shape[0] != requests:
-        raise ValueError("table has shape %s, expected [%d, pages]" % (tuple(shape), requests))
-    return p, shape[1]
+    p = _ptr(table, _i32, "table")
+    if table.dim() == 2:
+        rows, width = table.shape
+        if rows == requests:
+            return p, width
+    raise ValueError("table has shape %s, expected [%d, pages]" % (tuple(table.shape), requests))
 
 
 def tl_kv4_block_bytes(page_size: int, head_dim: int, group: int) -> int:
@@ -562,20 +589,18 @@ def tl_kv4_block_bytes(page_size: int, head_dim: int, group: int) -> int:
 def tl_kv_plan(cached, added, table, free_pages, q_start, seq_lens, token_req, token_pos, slots, counts,
                page_size: int, num_pages: int, free_head=None, stream=None) -> None:
     """Block tables, slots and positions of a step's tokens (see include/tlq.h);
-    table and the arrays from q_start to counts are written."""
-    import torch
-
-    i32 = torch.int32
-    n = cached.numel()
-    room = slots.numel()
+table and the arrays from q_start to counts are written."""
+    lib = _lib or load()
+    n, room = cached.numel(), slots.numel()
     tp, width = _table(table, n)
-    _raise_if(load().tl_kv_plan(_ints(cached, i32, "cached"), _ints(added, i32, "added", n), n, tp, width,
-                                _ints(free_pages, i32, "free_pages"), free_pages.numel(),
-                                _ints(free_head, i32, "free_head", 1) if free_head is not None else None, page_size,
-                                num_pages, _ints(q_start, i32, "q_start", n + 1), _ints(seq_lens, i32, "seq_lens", n),
-                                _ints(token_req, i32, "token_req", room), _ints(token_pos, i32, "token_pos", room),
-                                _ints(slots, torch.int64, "slots"), room, _ints(counts, i32, "counts", 4),
-                                _stream(stream)))
+    st = lib.tl_kv_plan(_ptr(cached, _i32, "cached"), _ints(added, _i32, "added", n), n, tp, width,
+                        _ptr(free_pages, _i32, "free_pages"), free_pages.numel(),
+                        None if free_head is None else _ints(free_head, _i32, "free_head", 1), page_size, num_pages,
+                        _ints(q_start, _i32, "q_start", n + 1), _ints(seq_lens, _i32, "seq_lens", n),
+                        _ints(token_req, _i32, "token_req", room), _ints(token_pos, _i32, "token_pos", room),
+                        _ptr(slots, _i64, "slots"), room, _ints(counts, _i32, "counts", 4), _stream(stream))
+    if st:
+        _raise_if(st)
 
 
 class KV4Cache:
@@ -612,29 +637,26 @@ class KV4Cache:
 
 def tl_kv4_append(cache: KV4Cache, k, v, slots, stream=None) -> None:
     """Quantize k, v [tokens, heads, head_dim] into the cache's slots."""
-    import torch
-
-    dims = cache._dims
-    kp, ldk = _rows(k, torch.float16, "k", dims)
-    vp, ldv = _rows(v, torch.float16, "v", dims)
+    kp, ldk, nk = _rows3(k, _f16, "k", cache.heads, cache.head_dim)
+    vp, ldv, nv = _rows3(v, _f16, "v", cache.heads, cache.head_dim)
     n = slots.numel()
-    if k.shape[0] != n or v.shape[0] != n:
-        raise ValueError("k and v have %d and %d tokens, slots %d" % (k.shape[0], v.shape[0], n))
-    _raise_if(load().tl_kv4_append(cache._ref, kp, ldk, vp, ldv, _ints(slots, torch.int64, "slots"), n,
-                                   _stream(stream)))
+    if nk != n or nv != n:
+        raise ValueError("k and v have %d and %d tokens, slots %d" % (nk, nv, n))
+    st = _lib.tl_kv4_append(cache._ref, kp, ldk, vp, ldv, _ptr(slots, _i64, "slots"), n, _stream(stream))
+    if st:
+        _raise_if(st)
 
 
 def tl_kv4_read(cache: KV4Cache, slots, k, v, stream=None) -> None:
     """The FP16 values of cached tokens into k, v [tokens, heads, head_dim]."""
-    import torch
-
     n = slots.numel()
     shape = (n,) + cache._dims
-    for t, name in ((k, "k"), (v, "v")):
-        if t.shape != shape:
-            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
-    _raise_if(load().tl_kv4_read(cache._ref, _ptr(slots, torch.int64, "slots"), n, _ptr(k, torch.float16, "k"),
-                                 _ptr(v, torch.float16, "v"), _stream(stream)))
+    if k.shape != shape or v.shape != shape:
+        raise ValueError("k and v have shapes %s and %s, expected %s" % (tuple(k.shape), tuple(v.shape), shape))
+    st = _lib.tl_kv4_read(cache._ref, _ptr(slots, _i64, "slots"), n, _ptr(k, _f16, "k"), _ptr(v, _f16, "v"),
+                          _stream(stream))
+    if st:
+        _raise_if(st)
 
 
 def tl_kv4_attention_workspace_size(q_heads: int, heads: int, head_dim: int, max_q: int) -> int:
@@ -646,46 +668,43 @@ def tl_kv4_attention(cache: KV4Cache, q, out, q_start, seq_lens, table, max_q: i
                      workspace=None, stream=None) -> None:
     """Causal attention of q [tokens, q_heads, head_dim] over the cache into
     out; workspace: cache.attention_workspace(q_heads, max_q)."""
-    import torch
-
     if q.dim() != 3:
         raise ValueError("q has shape %s, expected [tokens, q_heads, %d]" % (tuple(q.shape), cache.head_dim))
-    qp, ldq = _rows(q, torch.float16, "q", (q.shape[1], cache.head_dim))
-    op, ldo = _rows(out, torch.float16, "out", (q.shape[1], cache.head_dim))
-    if out.shape[0] != q.shape[0]:
-        raise ValueError("out has %d tokens, q %d" % (out.shape[0], q.shape[0]))
+    heads = q.shape[1]
+    qp, ldq, tokens = _rows3(q, _f16, "q", heads, cache.head_dim)
+    op, ldo, no = _rows3(out, _f16, "out", heads, cache.head_dim)
+    if no != tokens:
+        raise ValueError("out has %d tokens, q %d" % (no, tokens))
     n = seq_lens.numel()
     tp, width = _table(table, n)
-    ws = _ptr(workspace, torch.uint8, "workspace") if workspace is not None else None
-    nb = workspace.numel() if workspace is not None else 0
-    _raise_if(load().tl_kv4_attention(cache._ref, qp, ldq, q.shape[1], op, ldo,
-                                      _ints(q_start, torch.int32, "q_start", n + 1),
-                                      _ints(seq_lens, torch.int32, "seq_lens"), tp, width, n, q.shape[0], max_q,
-                                      scale, window, ws, nb, _stream(stream)))
+    ws, nb = (None, 0) if workspace is None else (_ptr(workspace, _u8, "workspace"), workspace.numel())
+    st = _lib.tl_kv4_attention(cache._ref, qp, ldq, heads, op, ldo, _ints(q_start, _i32, "q_start", n + 1),
+                               _ptr(seq_lens, _i32, "seq_lens"), tp, width, n, tokens, max_q, scale, window, ws, nb,
+                               _stream(stream))
+    if st:
+        _raise_if(st)
 
 
 def tl_lora_add(x, A, B, scales, q_start, adapters, max_q: int, y, out, stream=None) -> None:
     """out = y + scale * B[a] (A[a] x) per token, a the adapter of the token's
     request; A [adapters, rank, K], B [adapters, N, rank], out may be y."""
-    import torch
-
-    f16 = torch.float16
+    lib = _lib or load()
     if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
         raise ValueError("A %s and B %s: expected [adapters, rank, K] and [adapters, N, rank]"
                          % (tuple(A.shape), tuple(B.shape)))
     num, rank, K = A.shape
     N = B.shape[1]
-    xp, ldx = _rows(x, f16, "x", (K,))
-    yp, ldy = _rows(y, f16, "y", (N,))
-    op, ldo = _rows(out, f16, "out", (N,))
-    if y.shape[0] != x.shape[0] or out.shape[0] != x.shape[0]:
-        raise ValueError("x, y and out have %d, %d and %d tokens" % (x.shape[0], y.shape[0], out.shape[0]))
+    xp, ldx, tokens = _rows2(x, _f16, "x", K)
+    yp, ldy, ny = _rows2(y, _f16, "y", N)
+    op, ldo, no = (yp, ldy, ny) if out is y else _rows2(out, _f16, "out", N)
+    if ny != tokens or no != tokens:
+        raise ValueError("x, y and out have %d, %d and %d tokens" % (tokens, ny, no))
     n = adapters.numel()
-    _raise_if(load().tl_lora_add(xp, ldx, _ptr(A, f16, "A"), _ptr(B, f16, "B"),
-                                 _ints(scales, torch.float32, "scales", num),
-                                 _ints(q_start, torch.int32, "q_start", n + 1),
-                                 _ints(adapters, torch.int32, "adapters"), n, x.shape[0], max_q, K, N, rank, num, yp,
-                                 ldy, op, ldo, _stream(stream)))
+    st = lib.tl_lora_add(xp, ldx, _ptr(A, _f16, "A"), _ptr(B, _f16, "B"), _ints(scales, _f32, "scales", num),
+                         _ints(q_start, _i32, "q_start", n + 1), _ptr(adapters, _i32, "adapters"), n, tokens, max_q, K,
+                         N, rank, num, yp, ldy, op, ldo, _stream(stream))
+    if st:
+        _raise_if(st)
 
 
 # ---------------------------------------------------------------------------
