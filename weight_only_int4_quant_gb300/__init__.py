@@ -8,9 +8,11 @@ raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
+from .build import BINDING as _BINDING_PATH
 from .build import LIB as _LIB_PATH
 from .build import build as _build
 
@@ -94,6 +96,7 @@ class _KV4Cache(ctypes.Structure):
 _lock = threading.Lock()
 _lib = None
 _f16 = _f32 = _i32 = _i64 = _u8 = None  # torch's types, once the library is loaded
+_short = None  # the C API module of the serving calls
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -116,7 +119,7 @@ def load():
             _f16, _f32, _i32, _i64, _u8 = torch.float16, torch.float32, torch.int32, torch.int64, torch.uint8
         except ImportError:
             pass
-        if not os.path.exists(_LIB_PATH):
+        if not os.path.exists(_LIB_PATH) or not os.path.exists(_BINDING_PATH):
             raise RuntimeError("libtlq.so is not built (%s); call weight_only_int4_quant_gb300.build()"
                                % _LIB_PATH)
         lib = ctypes.CDLL(_LIB_PATH)
@@ -166,8 +169,25 @@ def load():
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = res
+        _load_binding(lib)
         _lib = lib
         return lib
+
+
+def _load_binding(lib):
+    """The C API module that makes the serving calls (csrc/binding.c)."""
+    global _short
+    if _f16 is None:  # no torch: nothing to call it with
+        return
+    import torch
+
+    spec = importlib.util.spec_from_file_location("_tlq_binding", _BINDING_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(_f16, _f32, _i32, _i64, _u8, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
+                *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                  for f in ("tl_kv_plan", "tl_kv4_append", "tl_kv4_read", "tl_kv4_attention", "tl_lora_add")))
+    _short = module
 
 
 def _raise_if(st: int):
@@ -502,9 +522,9 @@ def tl_selftest_wait_timeout(limit_us: int, stream=None) -> None:
 # ---------------------------------------------------------------------------
 
 # These calls are made per step, several to a step, and their kernels run for a
-# few microseconds, so their checks take the short way through for arguments
-# that are as they should be; what is not goes on to the full checks and their
-# messages.
+# few microseconds, so what is as it should be goes through the C API module
+# (_short); what is not comes back with -1 and goes on through the checks here,
+# with their messages.
 
 def _ptr(t, dtype, name):
     """Data pointer of a contiguous CUDA tensor of one dtype."""
@@ -591,6 +611,12 @@ def tl_kv_plan(cached, added, table, free_pages, q_start, seq_lens, token_req, t
     """Block tables, slots and positions of a step's tokens (see include/tlq.h);
 table and the arrays from q_start to counts are written."""
     lib = _lib or load()
+    st = _short.plan(cached, added, table, free_pages, q_start, seq_lens, token_req, token_pos, slots, counts, page_size,
+                     num_pages, free_head, stream)
+    if st == 0:
+        return
+    if st > 0:
+        _raise_if(st)
     n, room = cached.numel(), slots.numel()
     tp, width = _table(table, n)
     st = lib.tl_kv_plan(_ptr(cached, _i32, "cached"), _ints(added, _i32, "added", n), n, tp, width,
@@ -624,6 +650,7 @@ class KV4Cache:
         self.page_size, self.group = page_size, group
         self._c = _KV4Cache(_dev(blocks, (torch.uint8,), "blocks"), num_pages, heads, head_dim, page_size, group)
         self._ref = ctypes.byref(self._c)
+        self._address = ctypes.addressof(self._c)
         self._dims = (heads, head_dim)
 
     def attention_workspace(self, q_heads: int, max_q: int):
@@ -637,6 +664,11 @@ class KV4Cache:
 
 def tl_kv4_append(cache: KV4Cache, k, v, slots, stream=None) -> None:
     """Quantize k, v [tokens, heads, head_dim] into the cache's slots."""
+    st = _short.append(cache._address, cache.heads, cache.head_dim, k, v, slots, stream)
+    if st == 0:
+        return
+    if st > 0:
+        _raise_if(st)
     kp, ldk, nk = _rows3(k, _f16, "k", cache.heads, cache.head_dim)
     vp, ldv, nv = _rows3(v, _f16, "v", cache.heads, cache.head_dim)
     n = slots.numel()
@@ -649,6 +681,11 @@ def tl_kv4_append(cache: KV4Cache, k, v, slots, stream=None) -> None:
 
 def tl_kv4_read(cache: KV4Cache, slots, k, v, stream=None) -> None:
     """The FP16 values of cached tokens into k, v [tokens, heads, head_dim]."""
+    st = _short.read(cache._address, cache.heads, cache.head_dim, slots, k, v, stream)
+    if st == 0:
+        return
+    if st > 0:
+        _raise_if(st)
     n = slots.numel()
     shape = (n,) + cache._dims
     if k.shape != shape or v.shape != shape:
@@ -668,6 +705,12 @@ def tl_kv4_attention(cache: KV4Cache, q, out, q_start, seq_lens, table, max_q: i
                      workspace=None, stream=None) -> None:
     """Causal attention of q [tokens, q_heads, head_dim] over the cache into
     out; workspace: cache.attention_workspace(q_heads, max_q)."""
+    st = _short.attention(cache._address, cache.head_dim, q, out, q_start, seq_lens, table, max_q, scale, window,
+                          workspace, stream)
+    if st == 0:
+        return
+    if st > 0:
+        _raise_if(st)
     if q.dim() != 3:
         raise ValueError("q has shape %s, expected [tokens, q_heads, %d]" % (tuple(q.shape), cache.head_dim))
     heads = q.shape[1]
@@ -689,6 +732,11 @@ def tl_lora_add(x, A, B, scales, q_start, adapters, max_q: int, y, out, stream=N
     """out = y + scale * B[a] (A[a] x) per token, a the adapter of the token's
     request; A [adapters, rank, K], B [adapters, N, rank], out may be y."""
     lib = _lib or load()
+    st = _short.lora(x, A, B, scales, q_start, adapters, max_q, y, out, stream)
+    if st == 0:
+        return
+    if st > 0:
+        _raise_if(st)
     if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
         raise ValueError("A %s and B %s: expected [adapters, rank, K] and [adapters, N, rank]"
                          % (tuple(A.shape), tuple(B.shape)))
