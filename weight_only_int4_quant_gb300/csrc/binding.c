@@ -83,14 +83,14 @@ static int flat(PyObject* t, PyObject* type, long long n, void** p, long long* n
 }
 
 /* Rows [tokens, a] (dims = 2) or [tokens, a, b] (dims = 3), contiguous but for
- * the token stride, more than one of them. */
+ * the token stride; at least one (whose stride says nothing). */
 static int rows(PyObject* t, int dims, long long a, long long b, void** p, int64_t* ld, long long* tokens) {
   long long size[3], step[3];
   if (!attr_is(t, s_dtype, t_f16) || !attr_is(t, s_is_cuda, Py_True) || !extents(t, 0, dims, size) ||
       !extents(t, 1, dims, step))
     return 0;
-  if (size[0] < 2 || size[1] != a || (dims == 3 && (size[2] != b || step[1] != b)) || step[dims - 1] != 1) return 0;
-  *ld = step[0];
+  if (size[0] < 1 || size[1] != a || (dims == 3 && (size[2] != b || step[1] != b)) || step[dims - 1] != 1) return 0;
+  *ld = size[0] > 1 ? step[0] : (dims == 3 ? a * b : a);
   *tokens = size[0];
   return pointer(t, p);
 }
