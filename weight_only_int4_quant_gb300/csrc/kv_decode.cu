@@ -20,8 +20,11 @@
 // The running reference m of the softmax is kept per row in log2 units of
 // p * s' (not p), so that the FP16 weights p s' use FP16's whole range
 // whatever the scales: they lie below 2^14 and the largest is at least 2^6.
-// m moves only when a weight would pass that.  Sums of p and of p b' use the
-// rounded weights too, so the result is an exact weighted mean under them.
+// m moves only when a weight would pass that.  Value codes are centred:
+// 8 sum(p s') is kept beside O, by the same kind of instruction so that both
+// round alike, and taken off every other stage; minima are b' + 8 s'.  (Uncentred sums over 100000 tokens cancel to 1 / 400 of themselves
+// and lose as much of FP32.)  Sums of p and of p b' use the rounded weights too,
+// so the result is an exact weighted mean under them.
 //
 // Work: a unit is a stage of 128 tokens, 32 to each of a block's four warps.
 // All units of the batch (requests x key heads x row blocks x stages) lie on
@@ -45,6 +48,7 @@ constexpr int kTile = 16;    // tokens of a matrix instruction
 constexpr int kTiles = 2;    // tiles of a warp in a stage
 constexpr float kHeadroom = 6.0f;   // a new reference puts the largest weight at 2^6
 constexpr float kTrigger = 14.0f;   // weights stay at or below 2^14
+constexpr uint32_t kEight = 0x00080008u, kEight16 = 0x00800080u;  // two codes of 8, of 8 * 16
 constexpr float kNone = -1e30f;     // the reference of a row that has seen no key (finite: differences stay numbers)
 
 template <int D, int NG, int NT>
@@ -410,19 +414,38 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
     float o[NT][4 * H][4];
     float m[NT][2];
     float2 l[NT], beta[NT][NG];  // by column
+    float eight[NT][NG][4];      // 8 sum(p s') since it was last taken off O, in the layout of O's registers
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = kNone;
       l[nt] = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int g = 0; g < NG; ++g) beta[nt][g] = make_float2(0.f, 0.f);
+      for (int g = 0; g < NG; ++g) {
+        beta[nt][g] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) eight[nt][g][k] = 0.f;
+      }
 #pragma unroll
       for (int j = 0; j < 4 * H; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[nt][j][k] = 0.f;
     }
 
+    auto centre = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int j = 0; j < 4 * H; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[nt][j][k] -= eight[nt][NG == 1 ? 0 : j / 4][k];
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) eight[nt][g][k] = 0.f;
+      }
+    };
     for (int s = sg.s0; s < sg.s1; ++s, ++stage_i) {
+      if ((s & 1) == 0) centre();
       const int slot = stage_i % DEPTH;
       ok = ok && mbar_wait(&full[slot], (stage_i / DEPTH) & 1, 0x301);
       if (!ok) break;
@@ -485,7 +508,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
                 const float vs = fmaxf(fb.x, 5.9604644775390625e-8f);
                 vlg[i][y][g] = lg2(vs);
                 vrc[i][y][g] = reciprocal(vs);
-                vmi[i][y][g] = fb.y;
+                vmi[i][y][g] = fmaf(8.0f, fb.x, fb.y);  // of the centred codes
               }
             }
 #pragma unroll
@@ -554,6 +577,11 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
 #pragma unroll
                   for (int g = 0; g < NG; ++g) (c ? beta[nt][g].y : beta[nt][g].x) *= w;
 #pragma unroll
+                  for (int g = 0; g < NG; ++g) {
+                    eight[nt][g][c] *= w;
+                    eight[nt][g][2 + c] *= w;
+                  }
+#pragma unroll
                   for (int j = 0; j < 4 * H; ++j) {
                     o[nt][j][c] *= w;
                     o[nt][j][2 + c] *= w;
@@ -573,7 +601,8 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
               for (int y = 0; y < 2; ++y)
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                  const __half2 h2 = __floats2half2_rn(ex2(ew[i][nt][y][g].x), ex2(ew[i][nt][y][g].y));
+                  const float2 e = make_float2(ex2(ew[i][nt][y][g].x), ex2(ew[i][nt][y][g].y));
+                  const __half2 h2 = __floats2half2_rn(e.x, e.y);
                   const float2 w = mul2(__half22float2(h2), make_float2(vrc[i][y][g], vrc[i][y][g]));
                   if (g == 0) l[nt] = add2(l[nt], w);
                   if constexpr (EDGE) {  // a minimum that a row does not see is left out, whatever it holds
@@ -584,6 +613,12 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
                   }
                   pf[nt][g][y] = movmatrix(*reinterpret_cast<const uint32_t*>(&h2));
                 }
+
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int g = 0; g < NG; ++g)
+                mma_16816(eight[nt][g], kEight, kEight16, kEight, kEight16, pf[nt][g][0], pf[nt][g][1]);
 
             // O^T += V^T P^T: word 8 h + r of tokens 2 qd, 2 qd + 1, + 8, + 9.
             // Odd lanes of a quad read their two tokens in the other order
@@ -621,6 +656,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
     }
 
     // ---------------- join the warps ----------------
+    centre();
     named_barrier(1, 32 * W);  // the merge buffer and statistics of the last item have been read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
