@@ -3,32 +3,37 @@
 // put together, in the order of the blocks, so that the result is the same
 // every time:  o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i,  m = max m_i.
 //
-// Block x looks at what main block x began and did not end; block y takes every
-// gridDim.y-th set of threads, a thread to 8 channels of a row.  Latency bounds
-// it (a part is a few hundred kilobytes in L2), so the parts of both kernels of
-// a mixed batch are joined by one launch.
+// A set of blocks (one for the few rows of the one kernel, kManyBlocks for the
+// 256 of the other) looks at what one main block began and did not end, a
+// thread to 8 channels of a row.  Latency bounds it (a part is a few hundred
+// kilobytes in L2): the parts of both kernels of a mixed batch are joined by
+// one launch, and all of its blocks are resident at once.  (A block to each 128
+// pieces of a part, 32 to a main block, took 21 us to come and go where nothing
+// was to be joined.)
 #include "serve.cuh"
 
 namespace tlq {
 namespace {
 
 constexpr int kJoinThreads = 128;
+constexpr int kManyBlocks = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const KvJoin few, const KvJoin many, __half* out,
                                                            long long ldo, int share) {
   pdl_launch_dependents();
-  pdl_wait();
   const bool first_kind = (int)blockIdx.x < few.blocks;
   const KvJoin& j = first_kind ? few : many;
-  const int block = first_kind ? blockIdx.x : blockIdx.x - few.blocks;
+  const int at = first_kind ? blockIdx.x : blockIdx.x - few.blocks;
+  const int each = first_kind ? 1 : kManyBlocks, block = at / each;
+  pdl_wait();
   const KvJoinHeader h = j.headers[block];
   if (h.followers <= 0) return;
   const int R = j.rows;
   const size_t F = (size_t)R * (D + 2);  // a part: O [R][D], m [R], l [R]
   const float* first = j.parts + ((size_t)block * 2 + 1) * F;
   const float* rest = j.parts + ((size_t)block + 1) * 2 * F;  // follower i at i * 2 F
-  for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < h.rows * (D / 8); e += gridDim.y * kJoinThreads) {
+  for (int e = (at - block * each) * kJoinThreads + threadIdx.x; e < h.rows * (D / 8); e += each * kJoinThreads) {
     const int row = e / (D / 8), ch = (e - row * (D / 8)) * 8;
     float m = first[R * D + row];
     for (int i = 0; i < h.followers; ++i) m = fmaxf(m, rest[(size_t)i * 2 * F + R * D + row]);
@@ -62,10 +67,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const KvJoin few, co
 }  // namespace
 
 tlq_status launch_kv4_join(const KvAttention& a, const KvJoin& few, const KvJoin& many, cudaStream_t stream) {
-  const int rows = many.blocks > 0 ? many.rows : few.rows;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)(few.blocks + many.blocks),
-                    (unsigned)((rows * a.head_dim / 8 + kJoinThreads - 1) / kJoinThreads), 1);
+  lc.gridDim = dim3((unsigned)(few.blocks + many.blocks * kManyBlocks), 1, 1);
   lc.blockDim = dim3(kJoinThreads, 1, 1);
   lc.stream = stream;
   cudaLaunchAttribute at;

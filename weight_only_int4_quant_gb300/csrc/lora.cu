@@ -292,20 +292,21 @@ tlq_status launch_form(const LoraArgs& a, cudaStream_t stream) {
   return cuda_error(cudaLaunchKernelEx(&lc, lora_kernel<MT, KR>, a), "lora: launch");
 }
 
-template <int MT>
-tlq_status launch_tiles(const LoraArgs& a, cudaStream_t stream) {
-  if (a.rank <= 16) return launch_form<MT, 1>(a, stream);
-  if (a.rank <= 32) return launch_form<MT, 2>(a, stream);
-  return launch_form<MT, 4>(a, stream);
-}
-
 }  // namespace
 
 tlq_status launch_lora(const LoraArgs& a, cudaStream_t stream) {
-  // 64-token tiles read A and B a quarter as often; 16-token tiles spread short
-  // steps over more blocks.
-  if (a.max_q <= 16 || tile_bound(a, 1) * kRanks <= 2 * device_info().sms) return launch_tiles<1>(a, stream);
-  return launch_tiles<4>(a, stream);
+  // 64-token tiles read A and B a quarter as often; 16-token tiles make more
+  // blocks, which matters until every SM has its share.  Measured (K = 2048,
+  // N = 6144; 16- against 64-token tiles): rank 16, 660 tokens of 4 requests 12.2
+  // against 15.1 us, 1377 of 8 26.4 against 19.7, 4460 of 4 54.4 against 37.4;
+  // 653 of 48 15.1 against 19.3.  At ranks above 32 A x and the registers that
+  // hold it leave 64-token tiles one block to an SM: 20.1 against 39.4 us for the
+  // 660 tokens, 75.1 against 72.5 for the 4460, and 90 against 111 with K = 8192.
+  const bool tall = a.rank <= 32 && a.tokens > 1024 && a.tokens / 16 > a.requests;
+  if (tall) return a.rank <= 16 ? launch_form<4, 1>(a, stream) : launch_form<4, 2>(a, stream);
+  if (a.rank <= 16) return launch_form<1, 1>(a, stream);
+  if (a.rank <= 32) return launch_form<1, 2>(a, stream);
+  return launch_form<1, 4>(a, stream);
 }
 
 }  // namespace tlq

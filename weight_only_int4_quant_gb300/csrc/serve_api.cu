@@ -57,7 +57,7 @@ tlq_status check_cache(const tl_kv4_cache* c, KvCache* out, const char* who) {
 
 // Up to this many (query, head) rows to a key head a request's attention runs
 // on the kernel for few rows.
-constexpr int kFewRows = 32;
+constexpr int kFewRows = 64;
 
 size_t cache_bytes(const KvCache& c) { return (size_t)c.num_pages * c.heads * c.block_bytes; }
 
