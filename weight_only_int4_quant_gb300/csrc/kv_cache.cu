@@ -7,9 +7,14 @@
 // The smallest FP16 number as the least scale keeps constant rows exact
 // (c = 0) and every scale's logarithm finite for the attention kernels.
 //
-// DRAM traffic bounds both kernels: 32 bytes of activations against 8 bytes of
-// codes per thread, one pass, a row's lanes side by side so that loads and
-// stores cover whole sectors.
+// DRAM traffic is the floor of both kernels (2.5 bytes a value and a group's
+// parameters, one pass): 16 channels a lane, a row's lanes side by side, the
+// next row asked for before the current one's arithmetic, stores of whole
+// sectors.  Writing is bound by issue (a rounding, a check of it and a shift per
+// code), reading by outstanding loads.  16001 tokens x 16 heads of 128, keys and
+// values, groups of 64 (168 MB each way): append 42.5 us (4.0 TB/s; 46 without
+// the row ahead), read 32.8 us (5.1 TB/s; 35.8 with 4 and 35.3 with 8 blocks to
+// an SM for 6).  Few tokens are bound by latency: 16 tokens take 2.1 us each way.
 #include <algorithm>
 
 #include "serve.cuh"
@@ -18,6 +23,7 @@ namespace tlq {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kAppendBlocks = 4, kReadBlocks = 6;  // resident to an SM (registers)
 
 struct CodeRow {
   uint8_t* codes;
@@ -93,7 +99,7 @@ __device__ __forceinline__ float reciprocal(float x) {
 // lane, GL lanes to a group; a token's heads follow one another, keys and
 // values are the grid's y.
 template <int D, int GL>
-__global__ void __launch_bounds__(kRowThreads, 4)
+__global__ void __launch_bounds__(kRowThreads, kAppendBlocks)
     append_kernel(const KvCache c, const __half* __restrict__ k, long long ldk, const __half* __restrict__ v,
                   long long ldv, const long long* __restrict__ slots, uint32_t rows, FastDiv heads) {
   constexpr int L = D / 16, RPB = kRowThreads / L;
@@ -103,14 +109,24 @@ __global__ void __launch_bounds__(kRowThreads, 4)
   const __half* const base = part ? v : k;
   const long long ld = part ? ldv : ldk;
   const int sub = threadIdx.x % L;
-  // every lane of a warp takes the same number of turns (the shuffles need all)
-  for (uint32_t r0 = blockIdx.x * RPB; r0 < rows; r0 += gridDim.x * RPB) {
-    const uint32_t row = min(r0 + threadIdx.x / L, rows - 1);  // lanes past the end do the last row again
+  // Every lane of a warp takes the same number of turns (the shuffles need all);
+  // lanes past the end do the last row again.  A row is asked for a turn ahead.
+  uint4 raw[2];
+  long long slot;
+  auto fetch = [&](uint32_t r0) {
+    const uint32_t row = min(r0 + threadIdx.x / L, rows - 1);
     const uint32_t t = (uint32_t)divide((int)row, heads);
-    const int head = (int)(row - t * heads.d);
-    const uint4* src = reinterpret_cast<const uint4*>(base + t * ld + head * D + sub * 16);
-    const uint4 raw[2] = {__ldg(src), __ldg(src + 1)};
-    const long long slot = __ldg(slots + t);
+    const uint4* src = reinterpret_cast<const uint4*>(base + t * ld + (int)(row - t * heads.d) * D + sub * 16);
+    raw[0] = __ldg(src);
+    raw[1] = __ldg(src + 1);
+    slot = __ldg(slots + t);
+  };
+  uint32_t r0 = blockIdx.x * RPB;
+  if (r0 < rows) fetch(r0);
+  for (; r0 < rows; r0 += gridDim.x * RPB) {
+    const uint32_t row = min(r0 + threadIdx.x / L, rows - 1);
+    const int head = (int)(row - (uint32_t)divide((int)row, heads) * heads.d);
+    const long long here = slot;
     float2 x[8];
     __half2 lo2, hi2;
 #pragma unroll
@@ -122,6 +138,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
       lo2 = i ? __hmin2(lo2, h) : h;
       hi2 = i ? __hmax2(hi2, h) : h;
     }
+    if (rows - r0 > gridDim.x * RPB) fetch(r0 + gridDim.x * RPB);
 #pragma unroll
     for (int o = 1; o < GL; o <<= 1) {
       lo2 = __hmin2(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
@@ -141,8 +158,8 @@ __global__ void __launch_bounds__(kRowThreads, 4)
       word[1] = code_word_by_division(make_float4(x[4].x, x[4].y, x[5].x, x[5].y),
                                       make_float4(x[6].x, x[6].y, x[7].x, x[7].y), s, b);
     }
-    if (in_cache(c, slot)) {
-      const CodeRow out = code_row<D>(c, slot, head, part);
+    if (in_cache(c, here)) {
+      const CodeRow out = code_row<D>(c, here, head, part);
       reinterpret_cast<uint2*>(out.codes)[sub] = make_uint2(word[0], word[1]);
       if (sub % GL == 0)
         out.par[sub / GL] = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(bh) << 16);
@@ -151,7 +168,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 }
 
 template <int D, int GL>
-__global__ void __launch_bounds__(kRowThreads, 4)
+__global__ void __launch_bounds__(kRowThreads, kReadBlocks)
     read_kernel(const KvCache c, const long long* __restrict__ slots, uint32_t rows, FastDiv heads,
                 __half* __restrict__ k, __half* __restrict__ v) {
   constexpr int L = D / 16, U = 2, RPB = kRowThreads / L;  // U rows of a thread under way at a time
@@ -179,7 +196,6 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t row = r0 + u * RPB + threadIdx.x / L;
-      if (row >= rows) continue;
       const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&par[u]));
       const float2 s2 = make_float2(sb.x, sb.x);
       // 2^23 + code, from the bits; the constant goes out again exactly: the
@@ -195,18 +211,29 @@ __global__ void __launch_bounds__(kRowThreads, 4)
         const __half2 p = __floats2half2_rn(f.x, f.y);
         h[i] = *reinterpret_cast<const uint32_t*>(&p);
       }
-      uint4* dst = reinterpret_cast<uint4*>(base + (long long)row * D + sub * 16);
-      dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
-      dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+      // Two neighbours' 64 bytes go out as two stores of whole 32-byte sectors:
+      // first the even lane's, a half from each lane, then the odd one's.
+      const bool odd = sub & 1;
+      uint32_t got[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) got[i] = __shfl_xor_sync(0xffffffffu, odd ? h[i] : h[i + 4], 1);
+      if (row < rows) {
+        uint4* dst = reinterpret_cast<uint4*>(base + (long long)row * D + (sub & ~1) * 16 + (odd ? 8 : 0));
+        dst[0] = odd ? make_uint4(got[0], got[1], got[2], got[3]) : make_uint4(h[0], h[1], h[2], h[3]);
+        dst[2] = odd ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(got[0], got[1], got[2], got[3]);
+      }
     }
   }
 }
 
 template <class K, class... Args>
-tlq_status launch_rows(K kernel, long long rows, int lanes, const char* what, cudaStream_t stream, Args... args) {
-  if (rows > 0x7fffffffll) return set_error(TLQ_EUNSUPPORTED, "%s: %lld rows (tokens x heads, at most 2^31 - 1)", what, rows);
+tlq_status launch_rows(K kernel, int resident, long long rows, int lanes, const char* what, cudaStream_t stream,
+                       Args... args) {
+  if (rows > 0x7fffffffll)
+    return set_error(TLQ_EUNSUPPORTED, "%s: %lld rows (tokens x heads, at most 2^31 - 1)", what, rows);
   const long long per = kRowThreads / lanes;  // a block's first turn, one row a thread group, while blocks are few
-  const long long blocks = std::min<long long>((rows + per - 1) / per, (long long)device_info().sms * 2);  // with keys and values a full wave
+  // at most one wave of `resident` blocks to an SM, keys and values together
+  const long long blocks = std::min<long long>((rows + per - 1) / per, (long long)device_info().sms * resident / 2);
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)std::max<long long>(blocks, 1), 2, 1);
   lc.blockDim = dim3(kRowThreads, 1, 1);
@@ -226,9 +253,9 @@ tlq_status launch_kv4_append(const KvCache& c, int head_dim, const __half* k, lo
   const long long rows = (long long)tokens * c.heads;
   const FastDiv heads = fast_div((uint32_t)c.heads);
   if (head_dim == 128)
-    return launch_rows(c.group == 64 ? append_kernel<128, 4> : append_kernel<128, 8>, rows, 8, "kv4 append: launch", stream, c, k, ldk, v, ldv, slots,
-                       (uint32_t)rows, heads);
-  return launch_rows(append_kernel<64, 4>, rows, 4, "kv4 append: launch", stream, c, k, ldk, v, ldv, slots,
+    return launch_rows(c.group == 64 ? append_kernel<128, 4> : append_kernel<128, 8>, kAppendBlocks, rows, 8,
+                       "kv4 append: launch", stream, c, k, ldk, v, ldv, slots, (uint32_t)rows, heads);
+  return launch_rows(append_kernel<64, 4>, kAppendBlocks, rows, 4, "kv4 append: launch", stream, c, k, ldk, v, ldv, slots,
                      (uint32_t)rows, heads);
 }
 
@@ -237,8 +264,10 @@ tlq_status launch_kv4_read(const KvCache& c, int head_dim, const long long* slot
   const long long rows = (long long)tokens * c.heads;
   const FastDiv heads = fast_div((uint32_t)c.heads);
   if (head_dim == 128)
-    return launch_rows(c.group == 64 ? read_kernel<128, 4> : read_kernel<128, 8>, rows, 8, "kv4 read: launch", stream, c, slots, (uint32_t)rows, heads, k, v);
-  return launch_rows(read_kernel<64, 4>, rows, 4, "kv4 read: launch", stream, c, slots, (uint32_t)rows, heads, k, v);
+    return launch_rows(c.group == 64 ? read_kernel<128, 4> : read_kernel<128, 8>, kReadBlocks, rows, 8,
+                       "kv4 read: launch", stream, c, slots, (uint32_t)rows, heads, k, v);
+  return launch_rows(read_kernel<64, 4>, kReadBlocks, rows, 4, "kv4 read: launch", stream, c, slots, (uint32_t)rows,
+                     heads, k, v);
 }
 
 }  // namespace tlq

@@ -7,9 +7,10 @@
 // 256 of the other) looks at what one main block began and did not end, a
 // thread to 8 channels of a row.  Latency bounds it (a part is a few hundred
 // kilobytes in L2): the parts of both kernels of a mixed batch are joined by
-// one launch, and all of its blocks are resident at once.  (A block to each 128
-// pieces of a part, 32 to a main block, took 21 us to come and go where nothing
-// was to be joined.)
+// one launch.  8 blocks to a main block take a prompt of 2048 tokens, 16 heads, in
+// 70 us, 4 in 77; a grid of 608 x 32 blocks, most with nothing to join, took 75.
+// 96 registers keep the loads of four parts under way: at 64 the 14 parts
+// an item of four long contexts took 9 us longer.
 #include "serve.cuh"
 
 namespace tlq {
