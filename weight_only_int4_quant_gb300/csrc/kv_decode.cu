@@ -24,8 +24,11 @@
 // 8 sum(p s') is kept beside O, by the same kind of instruction so that both
 // round alike, and taken off every other stage; minima are b' + 8 s'.  (On
 // 131072 tokens uncentred sums are 400 times the result: an error of 4.9e-4
-// against 3.1e-4, for 69 against 77 us.)  Sums of p and of p b' use the rounded
-// weights too, so the result is an exact weighted mean under them.
+// against 2.9e-4, for 69 against 78 us.)  Sums of p and of p b' use the rounded
+// weights too, so the result is an exact weighted mean under them.  Value codes
+// are entered as 4 c and 64 c: the instruction aligns a subnormal factor as if
+// its leading bit were there, and what it cuts off a product of c alone adds up
+// to 2e-6 of the values' spread in every even channel, the same for any length.
 //
 // Work: a unit is a stage of 128 tokens, 32 to each of a block's four warps.
 // All units of the batch (requests x key heads x row blocks x stages) lie on
@@ -38,8 +41,8 @@
 //
 // Long batches are bound by issue: some 270 instructions per 16 tokens and warp,
 // on 55 % of the clocks, the ALU pipe 54 % busy, DRAM 54 %.  64 requests on up to
-// 8192 tokens, 32 / 8 heads of 128: 79 us, 4.1 TB/s; four on up to 131072 with
-// two groups: 77 us, 3.75 TB/s.  Short ones by latency: 500 tokens, 16 heads: 9 us
+// 8192 tokens, 32 / 8 heads of 128: 80 us, 4.0 TB/s; four on up to 131072 with
+// two groups: 78 us, 3.7 TB/s.  Short ones by latency: 500 tokens, 16 heads: 9 us
 // with the join, half of it the start of the two launches.
 #include <algorithm>
 #include <cmath>
@@ -55,7 +58,7 @@ constexpr int kTile = 16;    // tokens of a matrix instruction
 constexpr int kTiles = 2;    // tiles of a warp in a stage
 constexpr float kHeadroom = 6.0f;   // a new reference puts the largest weight at 2^6
 constexpr float kTrigger = 14.0f;   // weights stay at or below 2^14
-constexpr uint32_t kEight = 0x00080008u, kEight16 = 0x00800080u;  // two codes of 8, of 8 * 16
+constexpr uint32_t kEight = 0x00200020u, kEight16 = 0x02000200u;  // two codes of 8 * 4, of 8 * 64
 constexpr float kNone = -1e30f;     // the reference of a row that has seen no key (finite: differences stay numbers)
 
 template <int D, int NG, int NT>
@@ -641,9 +644,9 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
               for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const uint32_t xa = e ? wl[j] >> 8 : wl[j], xc = e ? wh[j] >> 8 : wh[j];
-                  const uint32_t a0 = xa & 0x000F000Fu, a1 = xa & 0x00F000F0u;  // channels 4 j + 2 e, + 1 of the word
-                  const uint32_t a2 = xc & 0x000F000Fu, a3 = xc & 0x00F000F0u;
+                  const uint32_t xa = e ? wl[j] >> 6 : wl[j] << 2, xc = e ? wh[j] >> 6 : wh[j] << 2;
+                  const uint32_t a0 = xa & 0x003C003Cu, a1 = xa & 0x03C003C0u;  // channels 4 j + 2 e, + 1 of the word
+                  const uint32_t a2 = xc & 0x003C003Cu, a3 = xc & 0x03C003C0u;
 #pragma unroll
                   for (int nt = 0; nt < NT; ++nt)
                     mma_16816(o[nt][4 * h + 2 * j + e], a0, a1, a2, a3, pf[nt][NG == 1 ? 0 : h][0],
@@ -700,10 +703,10 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
         for (int h = 0; h < H; ++h)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float k24 = 16777216.0f, k20 = 1048576.0f;
+            const float k22 = 4194304.0f, k18 = 262144.0f;
             *reinterpret_cast<float4*>(dst + 64 * h + 4 * j) =
-                make_float4(o[nt][4 * h + 2 * j][c] * k24, o[nt][4 * h + 2 * j][2 + c] * k20,
-                            o[nt][4 * h + 2 * j + 1][c] * k24, o[nt][4 * h + 2 * j + 1][2 + c] * k20);
+                make_float4(o[nt][4 * h + 2 * j][c] * k22, o[nt][4 * h + 2 * j][2 + c] * k18,
+                            o[nt][4 * h + 2 * j + 1][c] * k22, o[nt][4 * h + 2 * j + 1][2 + c] * k18);
           }
       }
       named_barrier(1, 32 * W);
