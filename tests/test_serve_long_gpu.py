@@ -123,7 +123,8 @@ def test_many_requests_with_prompts(lib, count):
     compare(lib, [a + (i * 53) % 300 for i, a in enumerate(adds)], adds, 4, 2, 128, 128, 16)
 
 
-@pytest.mark.parametrize("heads,max_q", [((8, 8), 32), ((8, 8), 33), ((8, 1), 4), ((8, 1), 5), ((33, 1), 1)])
+@pytest.mark.parametrize("heads,max_q", [((8, 8), 32), ((8, 8), 33), ((8, 1), 4), ((8, 1), 5), ((33, 1), 1),
+                                         ((8, 8), 64), ((8, 8), 65), ((8, 1), 8), ((8, 1), 9), ((65, 1), 1)])
 def test_either_side_of_the_row_rule(lib, heads, max_q):
     compare(lib, [900, 1800], [max_q, 1], *heads, 128, 128, 16)
 
