@@ -1,0 +1,148 @@
+"""Corners of the serving attention: value scales that differ, lengths that do
+not fit, and tokens that are not finite, against definitions in 64 bits.
+
+Tolerances (U = 2^-11, half a step of FP16 relative to the value).  Keys and
+value codes enter the products exactly; what is rounded is each weight p s'
+once (the second product), the output once, and the logits in FP32.
+
+* A weight's rounding moves o by at most U p_t |c_t - 8| s'_t with
+  8 s' <= (8 / 15) (max - min) <= (16 / 15) V, V the largest value of the
+  channel's group: 2 U V with what FP16 leaves out of the smallest weights
+  (below 2^-31 of the largest: n 2^-28 V / 7.5 for n tokens, n <= 2^17).
+* The output: U |o|, or half of FP16's smallest step, 2^-25.
+* A logit is a sum of at most 128 products and two more terms, each rounded or
+  cut to 2^-20 of the largest: dS = scale 2^-17 sum |q| (|b| + 15 s), and a
+  weighted mean moves by at most 2 dS V.
+* For independent tokens these add up as squares: the norm of the difference
+  is held to 3 U of the norm, U for each of the three (and FP16's smallest half
+  steps, 2^-25 each).
+"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -11
+FORMS = [(128, 128), (128, 64), (64, 64)]
+
+
+def value_gains(kind, t, h, d, gen):
+    """Factors of the value rows [t, h, d]."""
+    rand = lambda *s: torch.rand(*s, device="cuda", generator=gen)  # noqa: E731
+    if kind == "zero rows":
+        return (rand(t, h, 1) < 0.5).float()
+    if kind == "zero half":
+        return (torch.arange(d, device="cuda") >= 64).float().expand(t, h, d)
+    if kind == "wide rows":  # scales over a factor of 2^22
+        return 2.0 ** (22 * rand(t, h, 1) - 14)
+    if kind == "wide halves":  # the scales of the two groups 2^21 apart
+        return torch.where(torch.arange(d, device="cuda") >= 64, 2.0 ** 13, 2.0 ** -8).expand(t, h, d)
+    return torch.ones(t, h, d, device="cuda")
+
+
+class Batch:
+    """A filled cache and queries whose logits have the given spread."""
+
+    def __init__(self, lib, lens, adds, hq, hkv, d, group, page=16, spread=1.0, kind="", seed=1, width=None):
+        gen = torch.Generator("cuda").manual_seed(seed)
+        self.lib, self.lens, self.adds, self.hq = lib, lens, adds, hq
+        need = [-(-n // page) for n in lens]
+        self.cache = lib.KV4Cache(sum(need) + 2, hkv, d, page, group)
+        self.cache.blocks.fill_(0xFF)  # NaN scales and minima wherever no token is
+        order = torch.randperm(sum(need) + 2, device="cuda", generator=gen).int()
+        self.table = torch.full((len(lens), width or max(need + [1])), -1, dtype=torch.int32, device="cuda")
+        at, self.slots = 0, []
+        for i, n in enumerate(lens):
+            self.table[i, :need[i]] = order[at:at + need[i]]
+            at += need[i]
+            pos = torch.arange(n, device="cuda")
+            self.slots.append(self.table[i].long()[pos // page] * page + pos % page)
+            for a in range(0, n, 1 << 15):
+                part = self.slots[i][a:a + (1 << 15)]
+                k = torch.randn(len(part), hkv, d, device="cuda", generator=gen)
+                v = torch.randn(len(part), hkv, d, device="cuda", generator=gen)
+                v = v * value_gains(kind, len(part), hkv, d, gen)
+                lib.tl_kv4_append(self.cache, k.half(), v.half(), part.contiguous())
+        self.start = torch.zeros(len(lens) + 1, dtype=torch.int32, device="cuda")
+        self.start[1:] = torch.tensor(adds, device="cuda").cumsum(0)
+        self.q = (torch.randn(sum(adds), hq, d, device="cuda", generator=gen) * spread).half()
+        self.seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+    def tokens(self, i):
+        """Keys and values (64 bits, [heads, n, d]) of a request's tokens and the keys' size |b| + 15 s."""
+        c, n = self.cache, self.lens[i]
+        d, p, g, h = c.head_dim, c.page_size, c.group, c.heads
+        blk = c.blocks[self.table[i, :-(-n // p)].long()]
+        half, par, got = p * d // 2, 4 * p * d // g, []
+        for part in (0, 1):
+            code = blk[:, :, part * half:(part + 1) * half].reshape(-1, h, p, d // 2)
+            code = torch.stack((code & 15, code >> 4), -1).reshape(-1, h, p, d // g, g).double()
+            at = 2 * half + part * par
+            sb = blk[:, :, at:at + par].contiguous().view(torch.float16).reshape(-1, h, p, d // g, 2).double()
+            s, b = sb[..., :1], sb[..., 1:]
+            for x in (code * s + b, (b.abs() + 15 * s).expand_as(code)):
+                got.append(x.permute(1, 0, 2, 3, 4).reshape(h, -1, d)[:, :n])
+        return got[0], got[2], got[1]
+
+    def run(self, max_q=None, window=0, seq=None, out=None, **kw):
+        lib, scale = self.lib, self.cache.head_dim ** -0.5
+        max_q = max(self.adds) if max_q is None else max_q
+        out = torch.full_like(self.q, 7.0) if out is None else out
+        lib.tl_kv4_attention(self.cache, self.q, out, self.start, self.seq if seq is None else seq, self.table, max_q,
+                             scale, window, workspace=self.cache.attention_workspace(self.hq, max_q), **kw)
+        torch.cuda.synchronize()
+        lib.tl_check_status()
+        return out
+
+    def check(self, out, window=0, seq=None, max_q=None, norm=True):
+        """out against the definition: query t of request i lies at position seq[i] - adds[i] + t and sees those of
+        the request's tokens at its position or before it."""
+        c, at = self.cache, 0
+        d, hkv, share = c.head_dim, c.heads, self.hq // c.heads
+        scale = d ** -0.5
+        seq = (self.seq if seq is None else seq).tolist()
+        for i, (n, a) in enumerate(zip(self.lens, self.adds)):
+            m = a if max_q is None else min(a, max_q)
+            if m > 0 and n > 0:
+                k, v, size = self.tokens(i)
+                q = self.q[at:at + m].double().reshape(m, hkv, share, d).permute(1, 2, 0, 3)
+                s = scale * (q @ k[:, None].transpose(-1, -2))
+                mag = scale * (q.abs() @ size[:, None].transpose(-1, -2))
+                pos = torch.arange(seq[i] - a, seq[i] - a + m, device="cuda")[:, None]
+                key = torch.arange(n, device="cuda")
+                hide = (key > pos) | ((key <= pos - window) if window else torch.zeros_like(key, dtype=torch.bool))
+                s.masked_fill_(hide, float("-inf"))
+                ds = 2.0 ** -17 * mag.masked_fill_(hide, 0).amax(-1, keepdim=True)
+                w = torch.exp(s - s.amax(-1, keepdim=True).clamp_min(-1e300))
+                want = w @ v[:, None] / w.sum(-1, keepdim=True).clamp_min(1e-300)
+                vmax = v.abs().unflatten(-1, (-1, c.group)).amax((1, 3), keepdim=True).expand(hkv, 1, d // c.group, c.group)
+                vmax = vmax.reshape(hkv, 1, 1, d)
+                bound = U * want.abs() + 2.0 ** -25 + 2 * U * vmax + 2 * ds * vmax
+                got = out[at:at + m].double().reshape(m, hkv, share, d).permute(1, 2, 0, 3)
+                assert torch.isfinite(got).all(), i
+                off = (got - want).abs() - bound
+                assert (off <= 0).all(), (i, n, a, off.max().item())
+                if norm:  # group by group
+                    diff, ref = (x.unflatten(-1, (-1, c.group)).square().sum((0, 1, 2, 4)).sqrt()
+                                 for x in (got - want, want))
+                    floor = 2.0 ** -25 * (want.numel() * c.group / d) ** 0.5
+                    assert (diff <= 3 * U * ref + floor).all(), (i, (diff / ref).tolist())
+            elif m > 0:
+                assert not out[at:at + m].any()
+            if m < a:
+                assert (out[at + m:at + a] == 7).all()
+            at += a
+
+
+@pytest.mark.parametrize("d,group", FORMS)
+@pytest.mark.parametrize("kind", ["", "zero rows", "wide rows", "zero half"])
+@pytest.mark.parametrize("n,adds", [(300, 1), (300, 40), (8000, 1), (8000, 40), (131072, 1)])
+@pytest.mark.parametrize("spread", [1.0, 3.0])
+def test_value_scales_that_differ(lib, d, group, kind, n, adds, spread):
+    """A token's share of the softmax does not depend on the scale of its value: zero and constant rows (scale
+    2^-24) beside ordinary ones, scales over a factor of 2^22, a half of the channels at zero."""
+    if kind == "zero half" and d == 64:
+        kind = "zero rows"
+    b = Batch(lib, [n, n // 2 + 3], [adds, adds], 4, 2, d, group, 16, spread, kind, seed=n + adds)
+    b.check(b.run())

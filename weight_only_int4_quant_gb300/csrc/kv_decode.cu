@@ -18,14 +18,17 @@
 // or dequantized through shared memory.
 //
 // The running reference m of the softmax is kept per row in log2 units of
-// p * s' (not p), so that the FP16 weights p s' use FP16's whole range
-// whatever the scales: they lie below 2^14 and the largest is at least 2^6.
+// p * s' (not p), so that no FP16 weight p s' overflows and the largest keep
+// all of their bits: they lie below 2^14 and the largest is at least 2^6.
 // m moves only when a weight would pass that.  Value codes are centred:
 // 8 sum(p s') is kept beside O, by the same kind of instruction so that both
 // round alike, and taken off every other stage; minima are b' + 8 s'.  (On
 // 131072 tokens uncentred sums are 400 times the result: an error of 4.9e-4
-// against 2.9e-4, for 69 against 78 us.)  Sums of p and of p b' use the rounded
-// weights too, so the result is an exact weighted mean under them.  Value codes
+// against 2.9e-4, for 69 against 78 us.)  Sums of p and of p b' are FP32, of the
+// weights before their rounding to FP16: where scales differ, the weights of
+// the tokens with small ones end in FP16's last bits or below them, while their
+// p may be most of the softmax (a zero or constant value row has scale 2^-24).
+// Only the share of codes that s' makes small is rounded with them.  Value codes
 // are entered as 4 c and 64 c: the instruction aligns a subnormal factor as if
 // its leading bit were there, and what it cuts off a product of c alone adds up
 // to 2e-6 of the values' spread in every even channel, the same for any length.
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
                 for (int g = 0; g < NG; ++g) {
                   const float2 e = make_float2(ex2(ew[i][nt][y][g].x), ex2(ew[i][nt][y][g].y));
                   const __half2 h2 = __floats2half2_rn(e.x, e.y);
-                  const float2 w = mul2(__half22float2(h2), make_float2(vrc[i][y][g], vrc[i][y][g]));
+                  const float2 w = mul2(e, make_float2(vrc[i][y][g], vrc[i][y][g]));  // p, before any rounding to FP16
                   if (g == 0) l[nt] = add2(l[nt], w);
                   if constexpr (EDGE) {  // a minimum that a row does not see is left out, whatever it holds
                     if (w.x != 0.f) beta[nt][g].x = fmaf(w.x, vmi[i][y][g], beta[nt][g].x);
