@@ -146,3 +146,12 @@ def test_value_scales_that_differ(lib, d, group, kind, n, adds, spread):
         kind = "zero rows"
     b = Batch(lib, [n, n // 2 + 3], [adds, adds], 4, 2, d, group, 16, spread, kind, seed=n + adds)
     b.check(b.run())
+
+
+@pytest.mark.parametrize("n,adds", [(300, 1), (300, 40), (8000, 1), (8000, 40), (131072, 1)])
+@pytest.mark.parametrize("spread", [1.0, 3.0])
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (12, 1)])
+def test_groups_of_different_scales(lib, n, adds, spread, hq, hkv):
+    """Two groups of a row whose scales are 2^21 apart: each is as exact as by itself."""
+    b = Batch(lib, [n, n // 2 + 3], [adds, adds], hq, hkv, 128, 64, 16, spread, "wide halves", seed=n + adds)
+    b.check(b.run())

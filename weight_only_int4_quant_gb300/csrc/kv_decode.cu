@@ -17,10 +17,13 @@
 // interleaved by PRMT, P^T comes from S^T by movmatrix: no tile is transposed
 // or dequantized through shared memory.
 //
-// The running reference m of the softmax is kept per row in log2 units of
-// p * s' (not p), so that no FP16 weight p s' overflows and the largest keep
-// all of their bits: they lie below 2^14 and the largest is at least 2^6.
-// m moves only when a weight would pass that.  Value codes are centred:
+// The running reference m of the softmax is kept per row and group in log2
+// units of p * s' (not p), so that no FP16 weight p s' overflows and the
+// largest keep all of their bits: they lie below 2^14 and the largest is at
+// least 2^6.  m moves only when a weight would pass that.  (One reference for
+// both groups of a row takes 76 us for 80 where the scales are alike, four
+// contexts of up to 131072 tokens, and loses the weights of the group whose
+// scales are the smaller.)  Value codes are centred:
 // 8 sum(p s') is kept beside O, by the same kind of instruction so that both
 // round alike, and taken off every other stage; minima are b' + 8 s'.  (On
 // 131072 tokens uncentred sums are 400 times the result: an error of 4.9e-4
@@ -425,15 +428,15 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
     }
 
     float o[NT][4 * H][4];
-    float m[NT][2];
-    float2 l[NT], beta[NT][NG];  // by column
+    float2 m[NT][NG];            // by column, as are the sums: l under the first group's reference
+    float2 l[NT], beta[NT][NG];
     float eight[NT][NG][4];      // 8 sum(p s') since it was last taken off O, in the layout of O's registers
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = kNone;
       l[nt] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
+        m[nt][g] = make_float2(kNone, kNone);
         beta[nt][g] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < 4; ++k) eight[nt][g][k] = 0.f;
@@ -559,7 +562,8 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
                 for (int y = 0; y < 2; ++y)
 #pragma unroll
                   for (int g = 0; g < NG; ++g) {
-                    const float2 less = add2(make_float2(vlg[i][y][g], vlg[i][y][g]), make_float2(-m[nt][0], -m[nt][1]));
+                    const float2 less =
+                        add2(make_float2(vlg[i][y][g], vlg[i][y][g]), make_float2(-m[nt][g].x, -m[nt][g].y));
                     ew[i][nt][y][g] = add2(lw[i][nt][y], less);
                     top = fmaxf(top, fmaxf(ew[i][nt][y][g].x, ew[i][nt][y][g].y));
                   }
@@ -569,38 +573,34 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                float x = -INFINITY;
+              for (int g = 0; g < NG; ++g)
 #pragma unroll
-                for (int i = 0; i < JT; ++i)
+                for (int c = 0; c < 2; ++c) {
+                  float x = -INFINITY;
 #pragma unroll
-                  for (int y = 0; y < 2; ++y) {
-                    float lg = vlg[i][y][0];
-                    if constexpr (NG == 2) lg = fmaxf(lg, vlg[i][y][1]);
-                    x = fmaxf(x, (c ? lw[i][nt][y].y : lw[i][nt][y].x) + lg);
-                  }
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                const float next = fmaxf(m[nt][c], x - kHeadroom);
-                if (next > m[nt][c]) {
-                  const float w = ex2(m[nt][c] - next);  // 0 for the first reference
-                  m[nt][c] = next;
-                  (c ? l[nt].y : l[nt].x) *= w;
+                  for (int i = 0; i < JT; ++i)
 #pragma unroll
-                  for (int g = 0; g < NG; ++g) (c ? beta[nt][g].y : beta[nt][g].x) *= w;
-#pragma unroll
-                  for (int g = 0; g < NG; ++g) {
+                    for (int y = 0; y < 2; ++y)
+                      x = fmaxf(x, (c ? lw[i][nt][y].y : lw[i][nt][y].x) + vlg[i][y][g]);
+                  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                  float& ref = c ? m[nt][g].y : m[nt][g].x;
+                  const float next = fmaxf(ref, x - kHeadroom);
+                  if (next > ref) {
+                    const float w = ex2(ref - next);  // 0 for the first reference
+                    ref = next;
+                    if (g == 0) (c ? l[nt].y : l[nt].x) *= w;
+                    (c ? beta[nt][g].y : beta[nt][g].x) *= w;
                     eight[nt][g][c] *= w;
                     eight[nt][g][2 + c] *= w;
-                  }
 #pragma unroll
-                  for (int j = 0; j < 4 * H; ++j) {
-                    o[nt][j][c] *= w;
-                    o[nt][j][2 + c] *= w;
+                    for (int j = 4 * H / NG * g; j < 4 * H / NG * (g + 1); ++j) {
+                      o[nt][j][c] *= w;
+                      o[nt][j][2 + c] *= w;
+                    }
                   }
                 }
-              }
             exponents();
           }
 
@@ -670,6 +670,22 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
 
     // ---------------- join the warps ----------------
     centre();
+    // The second group's sums go over to the first one's reference.  The two lie
+    // within 60 of each other (scales 2^-24 .. 2^13 and the play of the references).
+    if constexpr (NG == 2) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float w = ex2(c ? m[nt][1].y - m[nt][0].y : m[nt][1].x - m[nt][0].x);
+          (c ? beta[nt][1].y : beta[nt][1].x) *= w;
+#pragma unroll
+          for (int j = 2 * H; j < 4 * H; ++j) {
+            o[nt][j][c] *= w;
+            o[nt][j][2 + c] *= w;
+          }
+        }
+    }
     named_barrier(1, 32 * W);  // the merge buffer and statistics of the last item have been read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -686,7 +702,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
         }
         if (r == 0) {
           float* st = stats + (warp * R + 8 * nt + 2 * qd + c) * (2 + NG);
-          st[0] = m[nt][c];
+          st[0] = c ? m[nt][0].y : m[nt][0].x;
           st[1] = lc;
 #pragma unroll
           for (int g = 0; g < NG; ++g) st[2 + g] = bc[g];
