@@ -687,12 +687,14 @@ tlq_status tl_kv4_read(const tl_kv4_cache* cache, const int64_t* slots, int toke
  *             what tl_kv_plan writes).  seq_lens counts the step's own tokens,
  *             which tl_kv4_append has put into the cache.  Entries that no
  *             visible token lies in are not read as pages; a page id outside
- *             the cache counts as holding no tokens
+ *             the cache counts as holding no tokens, and so do those behind
+ *             the table's row (positions are still those of seq_lens).
  *             A request's context is at most 2^30 tokens
  *   tokens    rows of q; queries outside [0, tokens) count as none, rows of
  *             no request are not written
- *   max_q     the most queries that a request has (an upper bound will do;
- *             a request's further queries are left out)
+ *   max_q     the most queries that a request has (an upper bound will do; of
+ *             a request with more, the last ones are left out and their rows
+ *             are not written)
  *   workspace device, 16-byte aligned, of tl_kv4_attention_workspace_size
  *             bytes or more; undefined afterwards, no contents needed before.
  *             Calls whose executions overlap need separate workspaces

@@ -155,3 +155,24 @@ def test_groups_of_different_scales(lib, n, adds, spread, hq, hkv):
     """Two groups of a row whose scales are 2^21 apart: each is as exact as by itself."""
     b = Batch(lib, [n, n // 2 + 3], [adds, adds], hq, hkv, 128, 64, 16, spread, "wide halves", seed=n + adds)
     b.check(b.run())
+
+
+@pytest.mark.parametrize("d,group", FORMS)
+@pytest.mark.parametrize("window", [0, 1, 40, 300])
+@pytest.mark.parametrize("adds,max_q", [([5, 2, 9], 3), ([5, 2, 9], 1), ([170, 40, 300], 100), ([170, 3, 300], 20)])
+def test_max_q_below_a_requests_queries(lib, d, group, window, adds, max_q):
+    """The queries that are left out are the last ones; the others keep their positions."""
+    b = Batch(lib, [400, 90, 310], adds, 4, 2, d, group, 16, 1.0, seed=window + max_q)
+    b.check(b.run(max_q, window), window, max_q=max_q, norm=False)
+
+
+@pytest.mark.parametrize("d,group", FORMS)
+@pytest.mark.parametrize("window", [0, 1, 30, 200, 320, 2000])
+@pytest.mark.parametrize("adds", [[3, 1, 4], [130, 1, 290]])
+def test_lengths_beyond_the_table(lib, d, group, window, adds):
+    """Tokens behind the table's row are not in the cache (a step whose pages did not suffice counts them);
+    positions are those of the full length."""
+    b = Batch(lib, [320, 50, 320], adds, 4, 2, d, group, 16, 1.0, seed=window + adds[0])
+    for more in (1, 17, 250):
+        seq = b.seq + torch.tensor([more, 0, more + 3], dtype=torch.int32, device="cuda")
+        b.check(b.run(window=window, seq=seq), window, seq, norm=False)

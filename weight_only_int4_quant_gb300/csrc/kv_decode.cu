@@ -201,11 +201,10 @@ struct Walk {
       s->row0 = (item - s->head * row_blocks) * R;
       s->rows = min(R, rq.q_len * p.share - s->row0);
       const int first_q = divide(s->row0, p.by_share), last_q = divide(s->row0 + s->rows - 1, p.by_share);
-      const int base = rq.len - rq.q_len;
-      s->hi = max(0, base + last_q + 1);
-      s->lo = p.window > 0 ? max(0, base + first_q - p.window + 1) : 0;
-      s->all_hi = base + first_q + 1;
-      s->all_lo = p.window > 0 ? base + last_q - p.window + 1 : 0;
+      s->hi = max(0, min(rq.len, rq.base + last_q + 1));
+      s->lo = p.window > 0 ? max(0, rq.base + first_q - p.window + 1) : 0;
+      s->all_hi = min(s->hi, rq.base + first_q + 1);
+      s->all_lo = p.window > 0 ? rq.base + last_q - p.window + 1 : 0;
       const int stage = s->lo / kStage;
       s->s0 = stage + c0;
       s->s1 = min(stage + c1, (s->hi + kStage - 1) / kStage);
@@ -340,7 +339,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
   bool ok = true;
   while (walk.next(p, &sg)) {
     const KvRequest rq = sg.rq;
-    const int head = sg.head, row0 = sg.row0, rows = sg.rows, base_pos = rq.len - rq.q_len;
+    const int head = sg.head, row0 = sg.row0, rows = sg.rows, base_pos = rq.base;
     // Query fragments: row n = 8 nt + r, channels 64 h + 16 qd .. + 15, scaled
     // by a power of two so that the item's largest value lies in [2^14, 2^15)
     // (exact, and q / 16 for the odd nibbles stays normal, down to 2^-24 of it).

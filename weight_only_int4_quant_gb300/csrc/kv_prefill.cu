@@ -99,9 +99,8 @@ __device__ __forceinline__ TileShape tile_shape(const PrefillAttnParams& p, cons
   TileShape t;
   const int first_q = divide(qt * kItemRows, p.by_share);
   const int last_q = divide(min(rows, (qt + 1) * kItemRows) - 1, p.by_share);
-  const int base = r.len - r.q_len;
-  t.hi = max(0, base + last_q + 1);
-  t.lo = p.window > 0 ? max(0, base + first_q - p.window + 1) : 0;
+  t.hi = max(0, min(r.len, r.base + last_q + 1));
+  t.lo = p.window > 0 ? max(0, r.base + first_q - p.window + 1) : 0;
   t.s0 = t.lo / kStage;
   t.n = max(1, (t.hi + kStage - 1) / kStage - t.s0);
   return t;
@@ -199,8 +198,8 @@ struct PWalk {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int last = min(s->rows, kRows * (i + 1)) - 1;  // the tile's last row
-        const int hi = last < kRows * i ? 0 : rq.len - rq.q_len + divide(s->row0 + last, p.by_share) + 1;
-        s->tile_end[i] = max(s->s0, min(s->s1, (max(hi, 0) + kStage - 1) / kStage));
+        const int hi = last < kRows * i ? 0 : rq.base + divide(s->row0 + last, p.by_share) + 1;
+        s->tile_end[i] = max(s->s0, min(s->s1, (max(min(hi, t.hi), 0) + kStage - 1) / kStage));
       }
       s->first = begins;
       s->last = c1 == t.n;
@@ -654,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
     while (next_segment()) {
       const KvRequest rq = sg.rq;
       const int rows = min(kRows, sg.rows - kRows * tile);  // of this tile; below 1: none
-      const int base_pos = rq.len - rq.q_len;
+      const int base_pos = rq.base;
       const int end = sg.tile_end[tile], s_end = sg.s1;
       const bool none = end == sg.s0;  // no row of the tile sees a key of the share
       // Q: a thread to a row, in the codes' channel order

@@ -80,18 +80,23 @@ struct KvBatch {
 constexpr long long kMaxContext = 1ll << 30;
 
 struct KvRequest {
-  int q0, q_len, len;
+  int q0, q_len;  // first query's row; queries that are worked on
+  int base;       // the first query's position (negative: before the first token)
+  int len;        // tokens that the table's row has room for
 };
 
-// Lengths as the kernels use them: queries outside [0, tokens) and lengths
-// beyond the table's row count as none.
+// Lengths as the kernels use them: queries outside [0, tokens) and tokens
+// behind the table's row count as none.  Positions come from the request's own
+// lengths, whatever is left out of its queries or tokens.
 __device__ __forceinline__ KvRequest kv_request(const KvBatch& b, int page, int i) {
   KvRequest r;
   r.q0 = b.q_start[i];
   const int q1 = b.q_start[i + 1];
-  r.q_len = (r.q0 >= 0 && q1 >= r.q0 && q1 <= b.tokens) ? min(q1 - r.q0, b.max_q) : 0;
-  const long long room = (long long)b.ld_table * page;
-  r.len = (int)max(0ll, min((long long)b.seq_lens[i], min(room, kMaxContext)));
+  const int queries = (r.q0 >= 0 && q1 >= r.q0 && q1 <= b.tokens) ? q1 - r.q0 : 0;
+  const int tokens = min(max(b.seq_lens[i], 0), (int)kMaxContext);
+  r.q_len = min(queries, b.max_q);
+  r.base = max(tokens - queries, -(int)kMaxContext);
+  r.len = (int)min((long long)tokens, (long long)b.ld_table * page);
   return r;
 }
 

@@ -231,8 +231,7 @@ tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_
   a.out = reinterpret_cast<__half*>(out);
   a.ldo = ldo;
   a.scale = scale;
-  // a window that no context outgrows is none
-  a.window = window >= std::min((long long)ld_table * cache->page_size, kMaxContext) ? 0 : window;
+  a.window = window >= kMaxContext ? 0 : window;  // a window that no context outgrows is none
   // The tensor-core kernel takes one scale a row, so rows in two groups stay
   // with the other one whatever their number (a prompt of 2048 tokens, 16 heads:
   // 249 us, where rows in one group take 69).
