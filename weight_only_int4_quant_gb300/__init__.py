@@ -7,6 +7,7 @@ raises instead of falling back to anything else.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.util
 import os
@@ -204,6 +205,33 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+_here = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Context in which torch allocates for work on ``stream``.  Memory of
+    another stream may still be in use there when the work begins, and may be
+    handed out there again before the work has ended."""
+    if stream is None:
+        return _here
+    import torch
+
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _result(stream, *tensors):
+    """Tensors allocated under _on(stream), for the caller: their memory goes
+    back only when the caller's stream is done with them too."""
+    if stream is not None:
+        import torch
+
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream())
+    return tensors[0] if len(tensors) == 1 else tensors
 
 
 def _dev(t, dtype, name):
@@ -405,9 +433,10 @@ def dequant_fp16(W, scales, zeros, bits: int, group: int, stream=None):
     """The FP16 body [N, K] of a packed weight (one rounding per weight)."""
     import torch
 
-    out = torch.empty((W.shape[0], W.shape[1] * (32 // bits)), dtype=torch.float16, device=W.device)
-    tl_dequant_fp16(W, scales, zeros, out, bits, group, stream)
-    return out
+    with _on(stream):
+        out = torch.empty((W.shape[0], W.shape[1] * (32 // bits)), dtype=torch.float16, device=W.device)
+        tl_dequant_fp16(W, scales, zeros, out, bits, group, stream)
+    return _result(stream, out)
 
 
 def tl_interleave_rows(a, b, out, stream=None) -> None:
@@ -756,7 +785,7 @@ def tl_lora_add(x, A, B, scales, q_start, adapters, max_q: int, y, out, stream=N
 
 
 # ---------------------------------------------------------------------------
-# conveniences that allocate their outputs with torch
+# conveniences that allocate their outputs with torch (on the stream they run on)
 # ---------------------------------------------------------------------------
 
 def quant_gemm(A, W, scales, zeros, bits: int, group: int, stream=None):
@@ -764,37 +793,41 @@ def quant_gemm(A, W, scales, zeros, bits: int, group: int, stream=None):
     (allocated here by torch)."""
     import torch
 
-    C = torch.empty((A.shape[0], W.shape[0]), dtype=torch.float16, device=A.device)
-    K = A.shape[1]
-    ws = gemm_workspace(A.shape[0], W.shape[0], K, bits, group, A.device)
-    tl_quant_gemm_ws(A, W, scales, zeros, C, bits, group, ws, stream)
-    return C
+    with _on(stream):
+        C = torch.empty((A.shape[0], W.shape[0]), dtype=torch.float16, device=A.device)
+        K = A.shape[1]
+        ws = gemm_workspace(A.shape[0], W.shape[0], K, bits, group, A.device)
+        tl_quant_gemm_ws(A, W, scales, zeros, C, bits, group, ws, stream)
+    return _result(stream, C)
 
 
 def pack_weights(codes, bits: int, stream=None):
     import torch
 
     N, K = codes.shape
-    W = torch.empty((N, K * bits // 32), dtype=torch.int32, device=codes.device)
-    tl_pack_weights(codes, W, bits, stream)
-    return W
+    with _on(stream):
+        W = torch.empty((N, K * bits // 32), dtype=torch.int32, device=codes.device)
+        tl_pack_weights(codes, W, bits, stream)
+    return _result(stream, W)
 
 
 def quant_gemm_swiglu(A, Wgu, scales, zeros, bits: int, group: int, stream=None):
     import torch
 
-    C = torch.empty((A.shape[0], Wgu.shape[0] // 2), dtype=torch.float16, device=A.device)
-    ws = gemm_workspace(A.shape[0], Wgu.shape[0], A.shape[1], bits, group, A.device)
-    tl_quant_gemm_swiglu(A, Wgu, scales, zeros, C, bits, group, stream, ws)
-    return C
+    with _on(stream):
+        C = torch.empty((A.shape[0], Wgu.shape[0] // 2), dtype=torch.float16, device=A.device)
+        ws = gemm_workspace(A.shape[0], Wgu.shape[0], A.shape[1], bits, group, A.device)
+        tl_quant_gemm_swiglu(A, Wgu, scales, zeros, C, bits, group, stream, ws)
+    return _result(stream, C)
 
 
 def interleave_rows(a, b, stream=None):
     import torch
 
-    out = torch.empty((2 * a.shape[0],) + tuple(a.shape[1:]), dtype=a.dtype, device=a.device)
-    tl_interleave_rows(a, b, out, stream)
-    return out
+    with _on(stream):
+        out = torch.empty((2 * a.shape[0],) + tuple(a.shape[1:]), dtype=a.dtype, device=a.device)
+        tl_interleave_rows(a, b, out, stream)
+    return _result(stream, out)
 
 
 def requant_int4_to_int2(W4, s4, z4, group: int, in_place_scales: bool = False, stream=None):
@@ -802,10 +835,11 @@ def requant_int4_to_int2(W4, s4, z4, group: int, in_place_scales: bool = False, 
     in_place_scales the INT2 scales/zeros overwrite s4/z4."""
     import torch
 
-    W2 = torch.empty((W4.shape[0], W4.shape[1] // 2), dtype=torch.int32, device=W4.device)
-    s2, z2 = (s4, z4) if in_place_scales else (torch.empty_like(s4), torch.empty_like(z4))
-    tl_requant_int4_to_int2(W4, s4, z4, W2, s2, z2, group, stream)
-    return W2, s2, z2
+    with _on(stream):
+        W2 = torch.empty((W4.shape[0], W4.shape[1] // 2), dtype=torch.int32, device=W4.device)
+        s2, z2 = (s4, z4) if in_place_scales else (torch.empty_like(s4), torch.empty_like(z4))
+        tl_requant_int4_to_int2(W4, s4, z4, W2, s2, z2, group, stream)
+    return _result(stream, W2, s2, z2)
 
 
 def kv4_attention(cache: KV4Cache, q, q_start, seq_lens, table, max_q: int, scale=None, window: int = 0, stream=None):
@@ -813,28 +847,31 @@ def kv4_attention(cache: KV4Cache, q, q_start, seq_lens, table, max_q: int, scal
     head_dim ** -0.5."""
     import torch
 
-    out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
-    tl_kv4_attention(cache, q, out, q_start, seq_lens, table, max_q,
-                     cache.head_dim ** -0.5 if scale is None else scale, window,
-                     cache.attention_workspace(q.shape[1], max_q), stream)
-    return out
+    with _on(stream):
+        out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+        tl_kv4_attention(cache, q, out, q_start, seq_lens, table, max_q,
+                         cache.head_dim ** -0.5 if scale is None else scale, window,
+                         cache.attention_workspace(q.shape[1], max_q), stream)
+    return _result(stream, out)
 
 
 def lora_add(x, A, B, scales, q_start, adapters, max_q: int, y, stream=None):
     """y + the requests' adapters applied to x."""
     import torch
 
-    out = torch.empty(y.shape, dtype=torch.float16, device=y.device)
-    tl_lora_add(x, A, B, scales, q_start, adapters, max_q, y, out, stream)
-    return out
+    with _on(stream):
+        out = torch.empty(y.shape, dtype=torch.float16, device=y.device)
+        tl_lora_add(x, A, B, scales, q_start, adapters, max_q, y, out, stream)
+    return _result(stream, out)
 
 
 def unpack_weights(W, K: int, bits: int, stream=None):
     import torch
 
-    codes = torch.empty((W.shape[0], K), dtype=torch.uint8, device=W.device)
-    tl_unpack_weights(W, codes, bits, stream)
-    return codes
+    with _on(stream):
+        codes = torch.empty((W.shape[0], K), dtype=torch.uint8, device=W.device)
+        tl_unpack_weights(W, codes, bits, stream)
+    return _result(stream, codes)
 
 
 def _block_workspace(shapes, bits, group, max_rows, device):
@@ -926,7 +963,8 @@ class _BlockBase:
             for i, name in enumerate(self.NAMES):
                 W4, s4, z4 = self.proj[name]
                 N, K = self.dims[name]
-                W2 = torch.empty((N, K // 16), dtype=torch.int32, device=W4.device)
+                with _on(stream):
+                    W2 = _result(stream, torch.empty((N, K // 16), dtype=torch.int32, device=W4.device))
                 new[name] = (W2, s4, z4)
                 dst[i] = _QProj(W2.data_ptr(), s4.data_ptr(), z4.data_ptr(), N, K, 0)
         _raise_if(fn(ctypes.byref(self._c), dst, _stream(stream)))
