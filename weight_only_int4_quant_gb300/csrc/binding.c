@@ -125,6 +125,18 @@ static PyObject* answer(int status) {
   return PyLong_FromLong(status);
 }
 
+/* The library's answer, with the interpreter's lock released over the call: a
+ * first launch loads modules, a full queue waits for the GPU, and a callback on
+ * the stream may need the interpreter.  The arguments are C values by then. */
+#define CALL(f, ...)          \
+  do {                        \
+    tlq_status st;            \
+    Py_BEGIN_ALLOW_THREADS    \
+    st = f(__VA_ARGS__);      \
+    Py_END_ALLOW_THREADS      \
+    return (int)st;           \
+  } while (0)
+
 /* The cache's descriptor, by its address. */
 static int cache_of(PyObject* o, const tl_kv4_cache** c) {
   *c = (const tl_kv4_cache*)PyLong_AsVoidPtr(o);
@@ -145,8 +157,8 @@ static int plan(PyObject* const* a, Py_ssize_t n) {
       (a[12] != Py_None && !flat(a[12], t_i32, 1, &head, NULL)) || !stream_of(a[13], &s) || requests > 0x7fffffffll ||
       room > 0x7fffffffll || num_free > 0x7fffffffll || size[1] > 0x7fffffffll)
     return FALLBACK;
-  return f_plan(cached, added, (int)requests, table, (int)size[1], free_pages, (int)num_free, head, (int)page, pages,
-                q_start, lens, req, pos, slots, (int)room, counts, s);
+  CALL(f_plan, cached, added, (int)requests, table, (int)size[1], free_pages, (int)num_free, head, (int)page, pages,
+       q_start, lens, req, pos, slots, (int)room, counts, s);
 }
 
 static int append(PyObject* const* a, Py_ssize_t n) {
@@ -159,7 +171,7 @@ static int append(PyObject* const* a, Py_ssize_t n) {
       !rows(a[3], 3, heads, dim, &k, &ldk, &tokens) || !rows(a[4], 3, heads, dim, &v, &ldv, &nv) || nv != tokens ||
       !flat(a[5], t_i64, tokens, &slots, NULL) || !stream_of(a[6], &s) || tokens > 0x7fffffffll)
     return FALLBACK;
-  return f_append(c, k, ldk, v, ldv, slots, (int)tokens, s);
+  CALL(f_append, c, k, ldk, v, ldv, slots, (int)tokens, s);
 }
 
 static int read_back(PyObject* const* a, Py_ssize_t n) {
@@ -173,7 +185,7 @@ static int read_back(PyObject* const* a, Py_ssize_t n) {
       ldk != heads * dim || ldv != heads * dim || !flat(a[3], t_i64, tokens, &slots, NULL) || !stream_of(a[6], &s) ||
       tokens > 0x7fffffffll)
     return FALLBACK;
-  return f_read(c, slots, (int)tokens, k, v, s);
+  CALL(f_read, c, slots, (int)tokens, k, v, s);
 }
 
 static int attention(PyObject* const* a, Py_ssize_t n) {
@@ -190,8 +202,9 @@ static int attention(PyObject* const* a, Py_ssize_t n) {
       !flat(a[10], t_u8, -1, &ws, &bytes) || !stream_of(a[11], &s) || tokens > 0x7fffffffll ||
       requests > 0x7fffffffll || size[1] > 0x7fffffffll || qs[1] > 0x7fffffffll)
     return FALLBACK;
-  return f_attention(c, q, ldq, (int)qs[1], out, ldo, q_start, lens, table, (int)size[1], (int)requests, (int)tokens,
-                     (int)max_q, (float)PyFloat_AS_DOUBLE(a[8]), (int)window, ws, (size_t)bytes, s);
+  const float scale = (float)PyFloat_AS_DOUBLE(a[8]);
+  CALL(f_attention, c, q, ldq, (int)qs[1], out, ldo, q_start, lens, table, (int)size[1], (int)requests, (int)tokens,
+       (int)max_q, scale, (int)window, ws, (size_t)bytes, s);
 }
 
 static int lora(PyObject* const* a, Py_ssize_t n) {
@@ -207,8 +220,8 @@ static int lora(PyObject* const* a, Py_ssize_t n) {
       tokens > 0x7fffffffll || requests > 0x7fffffffll || sa[0] > 0x7fffffffll || sa[2] > 0x7fffffffll ||
       sb[1] > 0x7fffffffll)
     return FALLBACK;
-  return f_lora(x, ldx, A, B, scales, q_start, adapters, (int)requests, (int)tokens, (int)max_q, (int)sa[2], (int)sb[1],
-                (int)sa[1], (int)sa[0], y, ldy, out, ldo, s);
+  CALL(f_lora, x, ldx, A, B, scales, q_start, adapters, (int)requests, (int)tokens, (int)max_q, (int)sa[2], (int)sb[1],
+       (int)sa[1], (int)sa[0], y, ldy, out, ldo, s);
 }
 
 #define METHOD(name)                                                              \
