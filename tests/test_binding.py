@@ -4,10 +4,15 @@ import ctypes
 import importlib.util
 import os
 import shutil
+import subprocess
+import sys
+import sysconfig
 import threading
 import time
 
 import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 F16, F32, I32, I64, U8 = (object() for _ in range(5))
 
@@ -100,3 +105,64 @@ def test_other_threads_run_during_a_call(module, name):
         thread.join()
     assert end - begin >= 0.9e-6 * MICROSECONDS  # the call was made
     assert sum(begin + 0.05 < t < end - 0.05 for t in ticks) > 10
+
+
+def run_python(code):
+    return subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+
+
+@pytest.mark.parametrize("missing", ["module", "torch", "both"])
+def test_the_library_loads_without_it(module, missing):
+    code = "import sys\n" + ("sys.modules['torch'] = None\n" if missing != "module" else "")
+    code += "import weight_only_int4_quant_gb300 as tlq\n"
+    code += "tlq._BINDING_PATH = '/nowhere.so'\n" if missing != "torch" else ""
+    r = run_python(code + "tlq.load(); print(tlq.tl_version(), tlq.tl_kv4_block_bytes(16, 128, 128))")
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.split()[-1] == str(16 * (128 + 8))
+
+
+def test_the_library_builds_without_a_c_compiler(module, tmp_path, monkeypatch):
+    import weight_only_int4_quant_gb300 as tlq
+
+    b = sys.modules["weight_only_int4_quant_gb300.build"]
+    there = tmp_path / os.path.basename(b.BINDING)
+    monkeypatch.setattr(b, "BINDING", str(there))
+    for cc in ("no-such-compiler", "false"):
+        there.write_bytes(b"of an older source")
+        os.utime(there, (1, 1))
+        monkeypatch.setenv("CC", cc)
+        with pytest.warns(UserWarning, match="C API module"):
+            assert tlq.build() == b.LIB
+        assert not there.exists()  # an older one does not stay
+
+
+def test_each_interpreter_has_its_own(module):
+    import weight_only_int4_quant_gb300 as tlq
+
+    assert tlq._BINDING_PATH.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+@pytest.mark.gpu
+def test_the_long_way_gives_the_same(lib, monkeypatch):
+    import test_serve_gpu as serve
+
+    torch = serve.torch
+    assert lib._short is not lib._LongWay  # built and in use
+    short = []
+    for way in (lib._short, lib._LongWay):
+        monkeypatch.setattr(lib, "_short", way)
+        c = serve.Case(lib, [50, 300, 7], [2, 1, 1], 8, 2, 128, 128, 16, seed=3)
+        ko, vo = (torch.empty(300, 2, 128, dtype=torch.float16, device="cuda") for _ in "kv")
+        slots = c.table[1].long()[torch.arange(300, device="cuda") // 16] * 16 + torch.arange(300, device="cuda") % 16
+        lib.tl_kv4_read(c.cache, slots, ko, vo)
+        g = torch.Generator("cuda").manual_seed(1)
+        r = lambda *s: torch.randn(*s, device="cuda", generator=g).half()  # noqa: E731
+        low = lib.lora_add(r(4, 64), r(2, 8, 64), r(2, 32, 8), torch.ones(2, device="cuda"), c.start,
+                           torch.tensor([0, 1, -1], dtype=torch.int32, device="cuda"), 2, r(4, 32))
+        i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+        plan = [i32(4), i32(3), i32(5), i32(5), torch.zeros(5, dtype=torch.int64, device="cuda"), i32(4)]
+        lib.tl_kv_plan(i32(3), torch.tensor([2, 1, 1], dtype=torch.int32, device="cuda"), c.table.clone(),
+                       torch.arange(9, dtype=torch.int32, device="cuda"), *plan, page_size=16, num_pages=40)
+        short.append([c.run(lib, 0.1), ko, vo, low, *plan])
+    for a, b in zip(*short):
+        assert torch.equal(a, b)

@@ -97,7 +97,20 @@ class _KV4Cache(ctypes.Structure):
 _lock = threading.Lock()
 _lib = None
 _f16 = _f32 = _i32 = _i64 = _u8 = None  # torch's types, once the library is loaded
-_short = None  # the C API module of the serving calls
+
+
+class _LongWay:
+    """In the place of the C API module where there is none: every serving call
+    takes the way through ctypes."""
+
+    @staticmethod
+    def plan(*args):
+        return -1
+
+    append = read = attention = lora = plan
+
+
+_short = _LongWay  # the C API module of the serving calls, once loaded
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -120,7 +133,7 @@ def load():
             _f16, _f32, _i32, _i64, _u8 = torch.float16, torch.float32, torch.int32, torch.int64, torch.uint8
         except ImportError:
             pass
-        if not os.path.exists(_LIB_PATH) or not os.path.exists(_BINDING_PATH):
+        if not os.path.exists(_LIB_PATH):
             raise RuntimeError("libtlq.so is not built (%s); call weight_only_int4_quant_gb300.build()"
                                % _LIB_PATH)
         lib = ctypes.CDLL(_LIB_PATH)
@@ -176,12 +189,15 @@ def load():
 
 
 def _load_binding(lib):
-    """The C API module that makes the serving calls (csrc/binding.c)."""
+    """The C API module that shortens the serving calls (csrc/binding.c), where
+    it has been built and torch has CUDA."""
     global _short
-    if _f16 is None:  # no torch: nothing to call it with
+    if _f16 is None or not os.path.exists(_BINDING_PATH):
         return
     import torch
 
+    if not hasattr(torch._C, "_cuda_getCurrentRawStream"):
+        return
     spec = importlib.util.spec_from_file_location("_tlq_binding", _BINDING_PATH)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)

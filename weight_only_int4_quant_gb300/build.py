@@ -1,6 +1,7 @@
 """Build libtlq.so (sm_103a) in-tree with nvcc: one object per .cu, compiled in
 parallel, then one shared-library link; beside it, with the C compiler, the
-Python module that makes the serving calls.  No cmake, no torch extension."""
+Python module that shortens the serving calls (the library does without it
+where it cannot be built).  No cmake, no torch extension."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -8,13 +9,15 @@ import glob
 import os
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libtlq.so")
-BINDING = os.path.join(BUILD, "_tlq_binding.so")
+# one file for each interpreter that uses the tree
+BINDING = os.path.join(BUILD, "_tlq_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-rdc=true", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -31,33 +34,51 @@ def _sources():
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(CSRC, "binding.c")] + \
+    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
         sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [os.path.abspath(__file__)]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _fresh(path, deps) -> bool:
+    if not os.path.exists(path):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(d) <= t for d in deps)
 
 
-def _build_binding() -> None:
-    """_tlq_binding.so: the C API module of the serving calls (host code only)."""
+def up_to_date() -> bool:
+    return _fresh(LIB, _deps())
+
+
+def build_binding(force: bool = False) -> bool:
+    """BINDING: the C API module of the serving calls (host code only).  Without
+    a C compiler or Python's headers there is none, and those calls go through
+    ctypes."""
+    src = os.path.join(CSRC, "binding.c")
+    if not force and _fresh(BINDING, [src, os.path.join(INCLUDE, "tlq.h"), os.path.abspath(__file__)]):
+        return True
     tmp = BINDING + ".tmp%d" % os.getpid()
     cmd = [os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-Wall", "-shared", "-fPIC",
-           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.c"), "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("the C compiler failed for binding.c:\n%s\n%s" % (" ".join(cmd), r.stderr))
+           "-I" + sysconfig.get_paths()["include"], src, "-o", tmp]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = r.stderr or "exit status %d" % r.returncode if r.returncode else ""
+    except OSError as e:
+        why = str(e)
+    if why:
+        if os.path.exists(BINDING):  # of an older source
+            os.remove(BINDING)
+        warnings.warn("no C API module, the serving calls will take longer: %s\n%s" % (" ".join(cmd), why))
+        return False
     os.replace(tmp, BINDING)
+    return True
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile every kernel source for sm_103a and link libtlq.so; return its path."""
+    os.makedirs(BUILD, exist_ok=True)
+    build_binding(force)
     if not force and up_to_date():
         return LIB
-    os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     srcs = _sources()
 
@@ -86,7 +107,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
     os.replace(tmp, LIB)
-    _build_binding()
     return LIB
 
 
