@@ -587,8 +587,9 @@ tlq_status tl_probe_read_bandwidth(const void* buf, size_t bytes, int reps, uint
  *   key parameters   [page_size][head_dim/group] pairs of FP16 (scale, minimum)
  *   value parameters [page_size][head_dim/group] pairs of FP16 (scale, minimum)
  * Code rows pack channels as tl_pack_weights packs a weight row (least
- * significant first); a channel stands for code * scale + minimum.  A token's
- * slot is page * page_size + offset.
+ * significant first); a channel stands for code * scale + minimum, scales are
+ * at least 2^-24, and neither is infinite.  A token's slot is page * page_size
+ * + offset.
  * ---------------------------------------------------------------------------
  */
 typedef struct {
@@ -649,7 +650,9 @@ tlq_status tl_kv_plan(const int32_t* cached, const int32_t* added, int requests,
  *     code = clamp(rint((x - minimum) / scale), 0, 15)
  *   k, v   FP16 [tokens][heads][head_dim] with token strides ldk, ldv (in
  *          elements, multiples of 8; the columns of a fused qkv projection's
- *          rows are taken as they lie); 16-byte aligned; finite
+ *          rows are taken as they lie); 16-byte aligned; a group with a value
+ *          that is not finite has NaN for scale and minimum and stands for
+ *          NaN throughout
  *   slots  int64 [tokens]; slots outside the cache (-1) are passed over; a
  *          call's slots are distinct
  *   Bit-exact; deterministic.  Returns TLQ_OK, TLQ_EINVAL, TLQ_EUNSUPPORTED

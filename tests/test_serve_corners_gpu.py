@@ -176,3 +176,40 @@ def test_lengths_beyond_the_table(lib, d, group, window, adds):
     for more in (1, 17, 250):
         seq = b.seq + torch.tensor([more, 0, more + 3], dtype=torch.int32, device="cuda")
         b.check(b.run(window=window, seq=seq), window, seq, norm=False)
+
+
+@pytest.mark.parametrize("d,group", FORMS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", ["first", "last", "one each", "all", "with its opposite"])
+def test_values_that_are_not_finite_show(lib, d, group, bad, where):
+    """A group with one such value reads back as NaN; the groups beside it as they were."""
+    gen = torch.Generator("cuda").manual_seed(5)
+    t, h = 37, 3
+    x = torch.randn(t, h, d, device="cuda", generator=gen).half()
+    cache = lib.KV4Cache(3, h, d, 16, group)
+    slots = torch.randperm(48, device="cuda", generator=gen)[:t].contiguous()
+
+    def through(k):
+        ko, vo = torch.empty_like(k), torch.empty_like(k)
+        lib.tl_kv4_append(cache, k, x, slots)
+        lib.tl_kv4_read(cache, slots, ko, vo)
+        return ko, vo
+
+    good, v = through(x)
+    y = x.clone()
+    rows = torch.arange(0, t, 2, device="cuda")
+    at = {"first": [0], "last": [d - 1], "one each": list(range(5, d, group)), "all": list(range(group)),
+          "with its opposite": [3, group - 2]}[where]
+    for i, c in enumerate(at):
+        y[rows, 1, c] = -bad if where == "with its opposite" and i else bad
+    got, v2 = through(y)
+    hit = torch.zeros(t, h, d // group, dtype=torch.bool, device="cuda")
+    hit[rows[:, None], 1, torch.tensor(sorted({c // group for c in at}), device="cuda")] = True
+    hit = hit.repeat_interleave(group, -1)
+    assert got[hit].isnan().all()
+    assert torch.equal(got[~hit], good[~hit]) and torch.equal(v, v2)
+    at = 16 * d + (slots % 16) * (4 * d // group)  # the keys' scales and minima
+    at = (at[:, None, None] + torch.arange(4 * d // group, device="cuda")).expand(t, h, -1)
+    par = cache.blocks[slots // 16].gather(2, at)
+    par = par.contiguous().view(torch.float16).reshape(t, h, -1, 2)
+    assert torch.equal(par.isnan(), hit.unflatten(-1, (-1, group))[..., :2])

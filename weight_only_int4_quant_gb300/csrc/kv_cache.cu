@@ -5,7 +5,9 @@
 //   c = clamp(rint((x - b) / s), 0, 15)
 // (binary32, rounded to nearest even at every step) and stands for c * s + b.
 // The smallest FP16 number as the least scale keeps constant rows exact
-// (c = 0) and every scale's logarithm finite for the attention kernels.
+// (c = 0) and every scale's logarithm finite for the attention kernels.  Where
+// an x is not finite, s is not either: s and b are stored as NaN and the whole
+// group stands for NaN (no infinity reaches the attention kernels' sums).
 //
 // DRAM traffic is the floor of both kernels (2.5 bytes a value and a group's
 // parameters, one pass): 16 channels a lane, a row's lanes side by side, the
@@ -51,7 +53,7 @@ __device__ __forceinline__ bool in_cache(const KvCache& c, long long slot) {
 // for a t within 15 * 2^-23 < 2^-19 of the true quotient.  n is the rounding of
 // the IEEE quotient unless the remainder (x - b) - n s comes within 2^-18 s of
 // half a step; such words, and rows whose top passes the last level (scales
-// near 2^-24), are redone with divisions.  x >= b always: b is one of the row's
+// near 2^-24), or with a NaN or an infinity, are redone with divisions.  x >= b always: b is one of the row's
 // own values.  The whole numbers' bits are 0x4B000000 + n: shifted together
 // they leave a known constant on top of the codes.
 __device__ __forceinline__ bool code_word(const float2 (&x)[4], float s, float b, float inv, uint32_t* word) {
@@ -135,19 +137,19 @@ __global__ void __launch_bounds__(kRowThreads, kAppendBlocks)
       const uint32_t w = (i & 2) ? ((i & 1) ? q.w : q.z) : ((i & 1) ? q.y : q.x);
       const __half2 h = *reinterpret_cast<const __half2*>(&w);
       x[i] = __half22float2(h);
-      lo2 = i ? __hmin2(lo2, h) : h;
-      hi2 = i ? __hmax2(hi2, h) : h;
+      lo2 = i ? __hmin2_nan(lo2, h) : h;
+      hi2 = i ? __hmax2_nan(hi2, h) : h;
     }
     if (rows - r0 > gridDim.x * RPB) fetch(r0 + gridDim.x * RPB);
 #pragma unroll
     for (int o = 1; o < GL; o <<= 1) {
-      lo2 = __hmin2(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
-      hi2 = __hmax2(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+      lo2 = __hmin2_nan(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
+      hi2 = __hmax2_nan(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
     }
-    const __half bh = __hmin(__low2half(lo2), __high2half(lo2)), th = __hmax(__low2half(hi2), __high2half(hi2));
+    const __half bh = __hmin_nan(__low2half(lo2), __high2half(lo2)), th = __hmax_nan(__low2half(hi2), __high2half(hi2));
     const __half tiny = __ushort_as_half((unsigned short)1);
     const float b = __half2float(bh), top = __half2float(th);
-    const __half sh = __hmax(__float2half_rn(fifteenth(top - b)), tiny);
+    const __half sh = __hmax_nan(__float2half_rn(fifteenth(top - b)), tiny);
     const float s = __half2float(sh), inv = reciprocal(s);
     uint32_t word[2];
     const float2 x0[4] = {x[0], x[1], x[2], x[3]}, x1[4] = {x[4], x[5], x[6], x[7]};
@@ -162,7 +164,8 @@ __global__ void __launch_bounds__(kRowThreads, kAppendBlocks)
       const CodeRow out = code_row<D>(c, here, head, part);
       reinterpret_cast<uint2*>(out.codes)[sub] = make_uint2(word[0], word[1]);
       if (sub % GL == 0)
-        out.par[sub / GL] = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(bh) << 16);
+        out.par[sub / GL] =
+            s < INFINITY ? (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(bh) << 16) : 0x7FFF7FFFu;
     }
   }
 }
