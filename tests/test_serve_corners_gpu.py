@@ -213,3 +213,43 @@ def test_values_that_are_not_finite_show(lib, d, group, bad, where):
     par = cache.blocks[slots // 16].gather(2, at)
     par = par.contiguous().view(torch.float16).reshape(t, h, -1, 2)
     assert torch.equal(par.isnan(), hit.unflatten(-1, (-1, group))[..., :2])
+
+
+def with_bad_token(lib, b, i, at, what, part):
+    """Token `at` of request i gets a NaN for scale, minimum or both, or a row with an infinity is written there."""
+    c = b.cache
+    slot = int(b.slots[i][at])
+    d, p, g = c.head_dim, c.page_size, c.group
+    if what == "written":
+        rows = [torch.ones(1, c.heads, d, dtype=torch.float16, device="cuda") for _ in "kv"]
+        rows[part][..., 1::64] = float("-inf")
+        lib.tl_kv4_append(c, *rows, b.slots[i][at:at + 1])
+        return
+    blk = c.blocks[slot // p]
+    width = 4 * d // g
+    off = p * d + part * p * width + (slot % p) * width
+    par = blk[:, off:off + width].contiguous().view(torch.float16).reshape(c.heads, -1, 2)
+    if what != "minimum":
+        par[..., 0] = float("nan")
+    if what != "scale":
+        par[..., 1] = float("nan")
+    blk[:, off:off + width] = par.reshape(c.heads, -1).view(torch.uint8)
+
+
+@pytest.mark.parametrize("d,group", FORMS)
+@pytest.mark.parametrize("what", ["scale", "minimum", "both", "written"])
+@pytest.mark.parametrize("part", [0, 1])
+@pytest.mark.parametrize("adds,window", [(4, 0), (4, 20), (200, 0), (200, 70)])
+def test_tokens_that_are_not_finite(lib, d, group, what, part, adds, window):
+    """Rows that do not see such a token are what they were; rows that see it show it."""
+    n = 330
+    b = Batch(lib, [n, 100], [adds, 1], 4, 2, d, group, 16, 1.0, seed=adds + window)
+    good = b.run(window=window)
+    at = n - adds + (1 if adds < 10 else adds // 2)
+    with_bad_token(lib, b, 0, at, what, part)
+    got = b.run(window=window)
+    pos = torch.arange(n - adds, n, device="cuda")
+    sees = (pos >= at) & ((pos < at + window) if window else True)
+    keep = torch.cat((~sees, torch.ones(1, dtype=torch.bool, device="cuda")))
+    assert torch.equal(got[keep], good[keep])
+    assert not torch.isfinite(got[:adds][sees].float()).any()

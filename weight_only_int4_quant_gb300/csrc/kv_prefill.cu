@@ -509,17 +509,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
         if (!val) {
           // the softmax's constants of this token, its value's among them: the
           // softmax of a stage begins before the stage's values are here.  No
-          // token: its logit is -infinity whatever the row
+          // token: its logit is -infinity whatever the row.  A NaN among the
+          // value's makes the logit NaN instead of the sums, which rows that
+          // do not see the token share with those that do (0 times NaN)
           const float2 kb = __half22float2(*reinterpret_cast<const __half2*>(&kpar[j & 1]));
           const float2 vb = __half22float2(*reinterpret_cast<const __half2*>(&vpar[j & 1]));
           const float vsc = fmaxf(vb.x, 5.9604644775390625e-8f), rc = __fdividef(1.0f, vsc);
+          const bool fine = live[j] && !isnan(vb.x + vb.y);
           const uint32_t tab = smem_u32(st + kt * C::TABLE) + (tk & 1) * 4;
           const uint32_t t1 = tab + (tk >> 1) * 16, t2 = t1 + kStage * 8, t3 = tab + kStage * 16 + (tk >> 1) * 8;
           sts_f32(t1, kb.x * (p.scale_log2 * 16777216.0f));
           sts_f32(t1 + 8, kb.y * p.scale_log2);
-          sts_f32(t2, live[j] ? lg2(vsc) : -INFINITY);
-          sts_f32(t2 + 8, live[j] ? rc : 0.f);
-          sts_f32(t3, live[j] ? fmaf(rc, vb.y, 8.0f) : 0.f);  // the value codes are centred: c - 8
+          sts_f32(t2, !live[j] ? -INFINITY : fine ? lg2(vsc) : NAN);
+          sts_f32(t2 + 8, fine ? rc : 0.f);
+          sts_f32(t3, fine ? fmaf(rc, vb.y, 8.0f) : 0.f);  // the value codes are centred: c - 8
         }
         // c 2^-24 of a key, (c - 8) 2^-24 of a value, exact; one form of the code
         // for both (the kernel's loops together outgrow the instruction cache)
