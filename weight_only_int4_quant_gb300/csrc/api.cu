@@ -48,17 +48,20 @@ bool pdl_enabled() {
 }
 
 const DeviceInfo& device_info() {
-  static DeviceInfo info = [] {
-    DeviceInfo d{148, 128 << 20, 227 * 1024};
-    int dev = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess) {
-      cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-      cudaDeviceGetAttribute(&d.l2_bytes, cudaDevAttrL2CacheSize, dev);
-      cudaDeviceGetAttribute(&d.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-    }
-    return d;
-  }();
-  return info;
+  constexpr int kDevices = 64;
+  static const DeviceInfo none{148, 128 << 20, 227 * 1024};  // without a device
+  static DeviceInfo info[kDevices];
+  static std::once_flag once[kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return none;
+  std::call_once(once[dev], [dev] {
+    DeviceInfo d = none;
+    cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaDeviceGetAttribute(&d.l2_bytes, cudaDevAttrL2CacheSize, dev);
+    cudaDeviceGetAttribute(&d.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    info[dev] = d;
+  });
+  return info[dev];
 }
 
 tlq_status encode_tiled_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,

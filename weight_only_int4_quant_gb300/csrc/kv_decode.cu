@@ -781,8 +781,7 @@ template <int D, int NG, int NT>
 tlq_status launch_one(const DecodeParams& base, void* ws, KvJoin* join, cudaStream_t stream) {
   using C = DCfg<D, NG, NT>;
   auto kernel = decode_attention_kernel<D, NG, NT>;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  const cudaError_t attr = opt_in_smem<decode_attention_kernel<D, NG, NT>>(C::SMEM);
   if (attr != cudaSuccess) return cuda_error(attr, "kv4 attention: shared memory");
   const int blocks = device_info().sms * C::CTAS;
   DecodeParams p = base;

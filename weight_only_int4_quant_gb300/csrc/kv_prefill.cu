@@ -973,7 +973,7 @@ template <int D>
 tlq_status launch_one(const PrefillAttnParams& p, cudaStream_t stream) {
   using C = PCfg<D>;
   auto kernel = prefill_attention_kernel<D>;
-  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  const cudaError_t attr = opt_in_smem<prefill_attention_kernel<D>>(C::SMEM);
   if (attr != cudaSuccess) return cuda_error(attr, "kv4 attention: shared memory");
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)p.join.blocks, 1, 1);

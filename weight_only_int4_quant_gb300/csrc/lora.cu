@@ -279,8 +279,7 @@ template <int MT, int KR>
 tlq_status launch_form(const LoraArgs& a, cudaStream_t stream) {
   const long long tiles = tile_bound(a, MT);
   if (tiles * kRanks > 0x7fffffffll) return set_error(TLQ_EUNSUPPORTED, "lora: %lld token tiles", tiles);
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(lora_kernel<MT, KR>, cudaFuncAttributeMaxDynamicSharedMemorySize, LCfg<MT, KR>::SMEM);
+  const cudaError_t attr = opt_in_smem<lora_kernel<MT, KR>>(LCfg<MT, KR>::SMEM);
   if (attr != cudaSuccess) return cuda_error(attr, "lora: shared memory");
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(tiles * kRanks), 1, 1);

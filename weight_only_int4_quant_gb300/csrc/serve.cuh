@@ -3,6 +3,8 @@
 // position in the batch's work into a request.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace tlq {
@@ -186,6 +188,22 @@ __device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, u
       return false;
     }
   }
+}
+
+// Opts a kernel in to `bytes` of dynamic shared memory on the current device:
+// the attribute is the device's, so it is set once on each, and again after a
+// failure.
+template <auto kKernel>
+cudaError_t opt_in_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};  // a bit for each of the first 64 devices
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t set = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (set == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return set;
 }
 
 // Launchers (arguments validated by the entry points).
