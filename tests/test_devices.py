@@ -33,6 +33,7 @@ int cudaFuncSetAttribute(const void* f, int a, int v) {
   return 0;
 }
 int cudaLaunchKernelExC(const struct config* c, const void* f, void** args) {
+  if (c->grid.x > 0x7fffffffu || c->grid.y > 65535 || c->grid.z > 65535) return 9;
   if (c->smem > 49152) {
     int ok = 0;
     for (int i = 0; i < kernels; ++i) ok |= opted[i].f == f && opted[i].dev == device && opted[i].bytes >= (int)c->smem;
@@ -78,13 +79,36 @@ print("done")
 """
 
 
-def test_shared_memory_and_sizes_by_device(tmp_path):
+def run_child(code, tmp_path):
     import weight_only_int4_quant_gb300 as tlq
 
     tlq.build()
     (tmp_path / "fake.c").write_text(FAKE)
     so = str(tmp_path / "fake.so")
     subprocess.run(["gcc", "-O1", "-shared", "-fPIC", str(tmp_path / "fake.c"), "-o", so], check=True)
-    r = subprocess.run([sys.executable, "-c", CHILD], capture_output=True, text=True, cwd=ROOT,
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT,
                        env=dict(os.environ, LD_PRELOAD=so))
     assert r.returncode == 0 and "done" in r.stdout, r.stderr
+
+
+def test_shared_memory_and_sizes_by_device(tmp_path):
+    run_child(CHILD, tmp_path)
+
+
+MANY = """
+import ctypes, sys
+sys.modules["torch"] = None
+import weight_only_int4_quant_gb300 as tlq
+lib, fake, G = tlq.load(), ctypes.CDLL(None), 1 << 36
+
+for n in (0, 1, 255, 257, 65535 * 256, 65535 * 256 + 1, 1 << 25, (1 << 31) - 1):
+    for room in (0, 5, 1 << 30):
+        st = lib.tl_kv_plan(G, 2 * G, n, 3 * G, 1, 4 * G, 32, None, 16, 100, 5 * G, 6 * G, 7 * G, 8 * G, 9 * G, room,
+                            10 * G, None)
+        assert st == tlq.TLQ_OK and fake.fake_launches() == 1, (n, room, st, tlq.tl_last_error())
+print("done")
+"""
+
+
+def test_plan_of_any_number_of_requests(tmp_path):
+    run_child(MANY, tmp_path)

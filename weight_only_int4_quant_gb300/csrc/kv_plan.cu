@@ -8,8 +8,9 @@
 // Whole-number work of a few hundred kilobytes at most: latency bounds it, so
 // it is one launch in which no block waits for another.  Every block sums the
 // lengths of the requests before its 256 by itself (8 bytes each, from L2)
-// instead of passing sums between blocks; the blocks of one set of 256
-// requests share that set's tokens and table rows.  1000 requests with 55000 new
+// instead of passing sums between blocks (so its work grows with the square of
+// the requests: right for thousands, seconds for tens of millions); the blocks
+// of one set of 256 requests share that set's tokens and table rows.  1000 requests with 55000 new
 // tokens: 5.6 us; 16 requests: 2.7 us, most of it the launch.
 #include <algorithm>
 
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const KvPlanArgs a, 
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x;
-  const int c0 = (int)blockIdx.y * kPlanThreads;
+  const int c0 = (int)blockIdx.x * kPlanThreads;
 
   // tokens, new pages and wanted pages of the requests before this set
   longlong2 before{0, 0}, wanted{0, 0}, sum;
@@ -104,9 +105,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const KvPlanArgs a, 
   longlong2 wsum;
   scan2(longlong2{s.wanted, 0}, warp_sum, &wsum);  // its barriers also publish the arrays above
 
-  const bool last = blockIdx.y + 1 == gridDim.y;
+  const bool last = blockIdx.x + 1 == gridDim.x;
   const long long total = before.x + sum.x;
-  if (blockIdx.x == 0) {
+  if (blockIdx.y == 0) {
     if (c0 + tid < a.requests) {
       a.q_start[c0 + tid] = (int)min(t0, 0x7fffffffll);
       a.seq_lens[c0 + tid] = (int)min((long long)s.cached + s.added, 0x7fffffffll);
@@ -126,8 +127,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const KvPlanArgs a, 
 
   // table rows: a warp to a request
   const int lane = tid & 31;
-  for (int i = (int)blockIdx.x * (kPlanThreads / 32) + (tid >> 5); i < kPlanThreads && c0 + i < a.requests;
-       i += (int)gridDim.x * (kPlanThreads / 32)) {
+  for (int i = (int)blockIdx.y * (kPlanThreads / 32) + (tid >> 5); i < kPlanThreads && c0 + i < a.requests;
+       i += (int)gridDim.y * (kPlanThreads / 32)) {
     int* row = a.table + (size_t)(c0 + i) * a.ld_table + held_s[i];
     const long long p0 = pages[i];
     for (int j = lane; j < need_s[i]; j += 32) row[j] = free_page(p0 + j);
@@ -137,8 +138,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const KvPlanArgs a, 
   // from the table, whose rows other blocks are writing
   const long long end = min(tok[kPlanThreads], (long long)a.capacity);
   const int P = 1 << page_shift;
-  for (long long t = tok[0] + (long long)blockIdx.x * kPlanThreads + tid; t < end;
-       t += (long long)gridDim.x * kPlanThreads) {
+  for (long long t = tok[0] + (long long)blockIdx.y * kPlanThreads + tid; t < end;
+       t += (long long)gridDim.y * kPlanThreads) {
     int lo = 0, hi = kPlanThreads;  // the last request with tok[i] <= t (requests without tokens are passed over)
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -159,8 +160,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const KvPlanArgs a, 
     a.slots[t] = page >= 0 && page < a.num_pages ? (long long)page * P + (pos & (P - 1)) : -1;
   }
   if (last) {
-    for (long long t = total + (long long)blockIdx.x * kPlanThreads + tid; t < a.capacity;
-         t += (long long)gridDim.x * kPlanThreads) {
+    for (long long t = total + (long long)blockIdx.y * kPlanThreads + tid; t < a.capacity;
+         t += (long long)gridDim.y * kPlanThreads) {
       a.token_req[t] = -1;
       a.token_pos[t] = -1;
       a.slots[t] = -1;
@@ -173,12 +174,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const KvPlanArgs a, 
 tlq_status launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
   int shift = 0;
   while ((1 << shift) < a.page) ++shift;
-  const int sets = a.requests > 0 ? (a.requests + kPlanThreads - 1) / kPlanThreads : 1;
-  // enough blocks for one token or one table row per thread or warp, at most a wave
-  long long x = ((long long)a.capacity + kPlanThreads - 1) / kPlanThreads / sets + 1;
-  x = std::min<long long>(x, std::max(1, 2 * device_info().sms / sets));
+  const int sets = a.requests > 0 ? (a.requests - 1) / kPlanThreads + 1 : 1;
+  // enough blocks for one token or one table row per thread or warp, at most a wave;
+  // sets go along x, which has no limit that requests could reach
+  long long y = ((long long)a.capacity + kPlanThreads - 1) / kPlanThreads / sets + 1;
+  y = std::min<long long>(y, std::max(1, 2 * device_info().sms / sets));
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)x, (unsigned)sets, 1);
+  lc.gridDim = dim3((unsigned)sets, (unsigned)y, 1);
   lc.blockDim = dim3(kPlanThreads, 1, 1);
   lc.stream = stream;
   cudaLaunchAttribute at;
