@@ -158,3 +158,23 @@ def test_lora_refusals(tlq, bad, word):
 
 def test_lora_unsupported_rank(tlq):
     assert lora(tlq, rank=72) == tlq.TLQ_EUNSUPPORTED
+
+
+@pytest.mark.parametrize("at", [3, 4, 5])
+@pytest.mark.parametrize("name,size", [("out", 6 * 1024 * 2), ("ws", None)])
+def test_attention_refuses_outputs_over_the_batch(tlq, at, name, size):
+    """q_start, seq_lens and table lie at 3, 4 and 5 M; the buffer's first and its last bytes over their first."""
+    size = size or tlq.tl_kv4_attention_workspace_size(8, 4, 128, 3)
+    for address in (at * M, at * M - size + 16):
+        if name == "ws" and address < 0:
+            continue
+        assert attention(tlq, cache(tlq), **{name: address}) == tlq.TLQ_EINVAL
+        assert "overlaps" in tlq.tl_last_error()
+
+
+@pytest.mark.parametrize("at", [4, 5, 6])
+def test_lora_refuses_outputs_over_the_batch(tlq, at):
+    """scales, q_start and adapters lie at 4, 5 and 6 M."""
+    for address in (at * M, at * M - 10 * 512 * 2 + 16):
+        assert lora(tlq, out=address) == tlq.TLQ_EINVAL
+        assert "overlaps" in tlq.tl_last_error()

@@ -223,6 +223,14 @@ tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_
   if (overlap(out, ob, q, qb) || overlap(out, ob, a.cache.blocks, cb) || overlap(workspace, need, q, qb) ||
       overlap(workspace, need, out, ob) || overlap(workspace, need, a.cache.blocks, cb))
     return set_error(TLQ_EINVAL, "%s: out or the workspace overlaps another buffer", who);
+  const struct {
+    const void* p;
+    size_t n;
+  } lengths[3] = {{q_start, 4 * ((size_t)requests + 1)}, {seq_lens, 4 * (size_t)requests},
+                  {table, 4 * (size_t)requests * ld_table}};
+  for (const auto& l : lengths)
+    if (overlap(out, ob, l.p, l.n) || overlap(workspace, need, l.p, l.n))
+      return set_error(TLQ_EINVAL, "%s: out or the workspace overlaps the batch's arrays", who);
   a.batch = KvBatch{q_start, seq_lens, table, ld_table, requests, tokens, max_q};
   a.head_dim = cache->head_dim;
   a.q_heads = q_heads;
@@ -271,6 +279,8 @@ tlq_status tl_lora_add(const uint16_t* x, int64_t ldx, const uint16_t* A, const 
   const size_t xb = span(tokens, ldx, K, 2), yb = span(tokens, ldy, N, 2), ob = span(tokens, ldo, N, 2);
   const size_t ab = 2 * (size_t)num_adapters * rank * K, bb = 2 * (size_t)num_adapters * rank * N;
   if (overlap(out, ob, x, xb) || overlap(out, ob, A, ab) || overlap(out, ob, B, bb) ||
+      overlap(out, ob, scales, 4 * (size_t)num_adapters) || overlap(out, ob, q_start, 4 * ((size_t)requests + 1)) ||
+      overlap(out, ob, adapters, 4 * (size_t)requests) ||
       (overlap(out, ob, y, yb) && !(out == y && (ldo == ldy || tokens == 1))))
     return set_error(TLQ_EINVAL, "%s: out overlaps an input (out may be exactly y)", who);
   LoraArgs a{};
