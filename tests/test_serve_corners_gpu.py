@@ -253,3 +253,23 @@ def test_tokens_that_are_not_finite(lib, d, group, what, part, adds, window):
     keep = torch.cat((~sees, torch.ones(1, dtype=torch.bool, device="cuda")))
     assert torch.equal(got[keep], good[keep])
     assert not torch.isfinite(got[:adds][sees].float()).any()
+
+
+@pytest.mark.parametrize("d,group", [(128, 128), (64, 64)])
+@pytest.mark.parametrize("adds", [[200, 260, 130], [40, 299, 33]])
+@pytest.mark.parametrize("window", [0, 90])
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 2 ** 31 - 1, 60])
+def test_pages_outside_the_cache_under_prompts(lib, d, group, adds, window, bad):
+    """Such a page holds no tokens and nothing is read through it, in the tensor-core kernel too."""
+    from test_serve_gpu import Case, check
+
+    hq, hkv = 8, 2
+    assert group == d and min(adds) * hq // hkv > 64  # every request has more rows than the few-rows kernel takes
+    c = Case(lib, [300, 299, 140], adds, hq, hkv, d, group, 16, seed=7)
+    assert c.cache.num_pages <= 60
+    drop = [(0, 0), (0, 7), (0, 18), (1, 3)] + [(2, j) for j in range(9)]
+    for i, j in drop:
+        c.table[i, j] = bad
+    ref = c.reference(0.1, window, drop=set(drop))
+    check(c.run(lib, 0.1, window), *ref)
+    assert not ref[0][c.start_host[2]:].any()  # the third request has no page left
