@@ -21,7 +21,7 @@
 // units of p * s' (not p), so that no FP16 weight p s' overflows and the
 // largest keep all of their bits: they lie below 2^14 and the largest is at
 // least 2^6.  m moves only when a weight would pass that.  (One reference for
-// both groups of a row takes 76 us for 80 where the scales are alike, four
+// both groups of a row takes 76 us for 79 where the scales are alike, four
 // contexts of up to 131072 tokens, and loses the weights of the group whose
 // scales are the smaller.)  Value codes are centred:
 // 8 sum(p s') is kept beside O, by the same kind of instruction so that both
@@ -45,10 +45,10 @@
 // through a ring of bulk copies, one per page (a page and head is one
 // contiguous piece), and runs ahead over the ends of items.
 //
-// Long batches are bound by issue: some 270 instructions per 16 tokens and warp,
-// on 55 % of the clocks, the ALU pipe 54 % busy, DRAM 54 %.  64 requests on up to
-// 8192 tokens, 32 / 8 heads of 128: 80 us, 4.0 TB/s; four on up to 131072 with
-// two groups: 78 us, 3.7 TB/s.  Short ones by latency: 500 tokens, 16 heads: 9 us
+// Long batches are bound by issue: 290 instructions per 16 tokens and key head,
+// all warps' beside the tiles included, on 55 % of the clocks, the ALU pipe 54 %
+// busy, DRAM 55 %.  64 requests on up to 8192 tokens, 32 / 8 heads of 128: 80 us,
+// 4.0 TB/s; four on up to 131072 with two groups: 79 us, 3.7 TB/s.  Short ones by latency: 500 tokens, 16 heads: 9 us
 // with the join, half of it the start of the two launches.
 #include <algorithm>
 #include <cmath>

@@ -41,8 +41,8 @@
 // span, and partial items are joined by a second kernel in a fixed order.
 //
 // Long spans are bound by the softmax of a stage (5400 clocks, its MMAs 2000 of
-// them): chunks on up to 16384 tokens, 32 / 8 heads of 128, take 866 us, 756
-// TFLOP/s.  A prompt of 2048 tokens, 16 heads, takes 69 us, 250 TFLOP/s: about
+// them): chunks on up to 16384 tokens, 32 / 8 heads of 128, take 870 us, 753
+// TFLOP/s.  A prompt of 2048 tokens, 16 heads, takes 68 us, 254 TFLOP/s: about
 // 9 us pass before a block's first stage (search, page, codes: dependent loads
 // and cold instructions) and 6 us at a change of item.
 #include <algorithm>

@@ -59,7 +59,9 @@ tlq_status check_cache(const tl_kv4_cache* c, KvCache* out, const char* who) {
 // on the kernel for few rows.  Its time grows with every 16 rows, the other
 // kernel's tiles are 256 rows high.  Few / many, 8 key heads of 128: 16 requests on
 // 8000 tokens, 32 rows 96 / 189 us, 64 rows 179 / 188, 96 rows 261 / 185; on 2000
-// tokens, 64 rows 60 / 80, 96 rows 84 / 81; one request on 1000, 128 rows 16 / 36.
+// tokens, 64 rows 60 / 80, 96 rows 84 / 81.  That is the crossing of batches that
+// fill the GPU; the rule knows rows alone, and a single short request above it
+// would do better here (one on 1000 tokens, 128 rows: 16 / 36).
 constexpr int kFewRows = 64;
 
 size_t cache_bytes(const KvCache& c) { return (size_t)c.num_pages * c.heads * c.block_bytes; }
@@ -242,7 +244,7 @@ tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_
   a.window = window >= kMaxContext ? 0 : window;  // a window that no context outgrows is none
   // The tensor-core kernel takes one scale a row, so rows in two groups stay
   // with the other one whatever their number (a prompt of 2048 tokens, 16 heads:
-  // 249 us, where rows in one group take 69).
+  // 246 us, where rows in one group take 68).
   const int few = cache->head_dim == cache->group ? kFewRows : 0x7fffffff;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   KvJoin few_parts{}, many_parts{};
