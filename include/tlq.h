@@ -619,7 +619,8 @@ size_t tl_kv4_block_bytes(int page_size, int head_dim, int group);
  *   cached, added  int32 [requests]
  *   table          int32 [requests][ld_table], read for pages held, written
  *                  for new ones (other entries are left as they are)
- *   free_pages     int32 [num_free] page ids; free_head: device int32 or NULL (0)
+ *   free_pages     int32 [num_free] page ids; free_head: device int32 or NULL
+ *                  (0; negative counts as 0)
  *   num_pages      pages of the cache; a page id outside it gives slot -1
  *   q_start        out int32 [requests + 1], exclusive sums of added
  *   seq_lens       out int32 [requests], cached + added

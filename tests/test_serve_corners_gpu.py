@@ -273,3 +273,28 @@ def test_pages_outside_the_cache_under_prompts(lib, d, group, adds, window, bad)
     ref = c.reference(0.1, window, drop=set(drop))
     check(c.run(lib, 0.1, window), *ref)
     assert not ref[0][c.start_host[2]:].any()  # the third request has no page left
+
+
+@pytest.mark.parametrize("head", [-1, -2, -2 ** 31, 0, 2, 9, 10, 2 ** 31 - 1])
+def test_free_list_heads(lib, head):
+    """Whatever the head, the pages that a step hands out are those its counts say, and the next step's are others."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    free = torch.arange(100, 110, **i32)
+    cached, added = torch.zeros(3, **i32), torch.tensor([17, 1, 30], **i32)  # 2, 1 and 2 pages
+    first = torch.tensor([head], **i32)
+    given = []
+    for _ in range(2):
+        table = torch.full((3, 2), -1, **i32)
+        start, lens, counts = torch.empty(4, **i32), torch.empty(3, **i32), torch.empty(4, **i32)
+        req, pos = torch.empty(48, **i32), torch.empty(48, **i32)
+        slots = torch.empty(48, dtype=torch.int64, device="cuda")
+        lib.tl_kv_plan(cached, added, table, free, start, lens, req, pos, slots, counts, page_size=16, num_pages=200,
+                       free_head=first)
+        pages = [p for p in table.flatten().tolist() if p >= 0]
+        at = max(first.item(), 0)
+        taken = min(5, max(0, 10 - at))
+        assert pages == list(range(100 + at, 100 + at + taken))
+        assert counts.tolist() == [48, taken, at + taken, 5 - taken]
+        given += pages
+        first = counts[2:3].clone()
+    assert len(set(given)) == len(given)

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const KvPlanArgs a, 
 
   const PlanShape s = plan_shape(a, c0 + tid);
   const longlong2 upto = scan2(longlong2{s.added, s.need}, warp_sum, &sum);
-  const long long head = a.free_head ? (long long)*a.free_head : 0;
+  const long long head = a.free_head ? (long long)max(*a.free_head, 0) : 0;
   const long long t0 = before.x + upto.x - s.added;
   tok[tid] = t0;
   pages[tid] = head + before.y + upto.y - s.need;
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const KvPlanArgs a, 
     }
     if (last && tid == 0) {
       a.q_start[a.requests] = (int)min(total, 0x7fffffffll);
-      const long long avail = max(0ll, head >= 0 ? (long long)a.num_free - head : 0ll);
+      const long long avail = max(0ll, (long long)a.num_free - head);
       const long long taken = min(before.y + sum.y, avail);
       a.counts[0] = (int)min(total, 0x7fffffffll);
       a.counts[1] = (int)taken;
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const KvPlanArgs a, 
     }
   }
 
-  auto free_page = [&](long long at) { return at >= 0 && at < a.num_free ? a.free_pages[at] : -1; };
+  auto free_page = [&](long long at) { return at < a.num_free ? a.free_pages[at] : -1; };
 
   // table rows: a warp to a request
   const int lane = tid & 31;
