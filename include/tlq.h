@@ -680,7 +680,8 @@ tlq_status tl_kv4_read(const tl_kv4_cache* cache, const int64_t* slots, int toke
  *   head i reads key head i / (q_heads / heads).
  *     out = softmax(scale * q . k) v
  *   Sums and softmax statistics are FP32; weights are rounded to FP16 for the
- *   second product.  A query that sees no key (seq_lens[b] smaller than the
+ *   second product.  A NaN in the cache shows in the queries that see its token
+ *   and in no others.  A query that sees no key (seq_lens[b] smaller than the
  *   request's queries, or none of its pages in the cache) gives zeros.
  *
  *   q, out    FP16 [tokens][q_heads][head_dim], token strides ldq, ldo
