@@ -717,6 +717,114 @@ tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_
 size_t tl_kv4_attention_workspace_size(int q_heads, int heads, int head_dim, int max_q);
 
 /*
+ * Rotary positions.  Pair i (0 .. rot_dim/2 - 1) of a head's first rot_dim
+ * channels, (a, b), turns by the angle of its position:
+ *   (a, b) -> (a cos - b sin, b cos + a sin),  (cos, sin) = table[position][i]
+ * Other channels are left.  With several axes (time, height and width of
+ * images and video) the first sections[0] pairs go by a token's position on
+ * the first axis, the next sections[1] by that on the second, and so on.
+ */
+typedef struct {
+  const float* table;    /* device, FP32 [num_positions][rot_dim/2][2], 16-byte aligned: cos and sin */
+  int64_t num_positions; /* 1 .. 2^30 */
+  int rot_dim;           /* a multiple of 16, up to the head size */
+  int interleaved;       /* pairs: 0 channels (i, i + rot_dim/2), else (2i, 2i + 1) */
+  int axes;              /* 1 .. 3 */
+  int sections[3];       /* pairs of each axis; they add up to rot_dim/2 */
+} tl_rope;
+
+/*
+ * tl_rope_table -- table[p][i] = (cos, sin)(p * inv_freq[i]) * scale, in 64 bits
+ * and rounded once to FP32 (angles of far positions keep their digits).
+ *   inv_freq  device FP64 [rot_dim/2];  table  device, 4 * num_positions *
+ *             rot_dim bytes, 16-byte aligned;  scale  1 for plain rotations
+ * Returns TLQ_OK, TLQ_EINVAL or TLQ_ECUDA.
+ */
+tlq_status tl_rope_table(const double* inv_freq, int64_t num_positions, int rot_dim, double scale, float* table,
+                         void* stream);
+
+/*
+ * tl_qk_norm_rope -- the query and key heads of `tokens` tokens normed and
+ * rotated, one pass.
+ *
+ *   Per head x of head_dim channels (FP32, rounded after every operation):
+ *     y = (x * r) * weight,  r = 1 / sqrt(sum(x^2) / head_dim + eps)
+ *   (weight NULL: y = x), then the rotation, its products rounded and then
+ *   their sum, and one rounding to FP16.  The squares are added up as a tree:
+ *   each 8 channels by halves (j and j + 4, then j and j + 2, then the two),
+ *   then these sums by halves.  So results are defined to the bit.
+ *
+ *   q, q_out   FP16 [tokens][q_heads][head_dim], token strides ldq, ldqo (in
+ *              elements, multiples of 8); k, k_out likewise.  Either heads may
+ *              be 0 (its pointers are not looked at).  An output may be exactly
+ *              its input, else it shares no byte with an input or the other
+ *              output (columns of the same fused rows do not)
+ *   weights    FP16 [head_dim] or NULL; all pointers 16-byte aligned
+ *   head_dim   64, 128 or 256;  eps  finite, not negative
+ *   rope       NULL: no rotation;  positions  int32 [axes][tokens]
+ *   A token with a negative position on an axis (tl_kv_plan's entries behind
+ *   the last token) is passed over: its rows are not written.  A position at
+ *   or past num_positions gives NaN in the rotated channels.
+ *   Bit-exact; deterministic.  Returns TLQ_OK, TLQ_EINVAL, TLQ_EUNSUPPORTED (a
+ *   head_dim that is not taken, 2^31 rows or more) or TLQ_ECUDA.
+ */
+tlq_status tl_qk_norm_rope(const tl_rope* rope, const int32_t* positions, const uint16_t* q, int64_t ldq, int q_heads,
+                           const uint16_t* q_weight, uint16_t* q_out, int64_t ldqo, const uint16_t* k, int64_t ldk,
+                           int k_heads, const uint16_t* k_weight, uint16_t* k_out, int64_t ldko, int head_dim,
+                           float eps, int tokens, void* stream);
+
+/*
+ * tl_kv4_append_rope -- what tl_qk_norm_rope does with keys, on their way into
+ * the cache: the bits are those of tl_qk_norm_rope followed by tl_kv4_append,
+ * in one launch and without the keys' way through memory.  The queries of the
+ * same tokens are normed and rotated beside them (q_heads 0: none).
+ *   k, v, slots  as in tl_kv4_append;  the rest as in tl_qk_norm_rope.  A token
+ *   with a negative position is passed over altogether, one whose slot is
+ *   outside the cache brings its queries only; a position at or past
+ *   num_positions gives a key that stands for NaN.
+ *   Bit-exact; deterministic.  Returns as tl_kv4_append.
+ */
+tlq_status tl_kv4_append_rope(const tl_kv4_cache* cache, const tl_rope* rope, const int32_t* positions,
+                              const uint16_t* k, int64_t ldk, const uint16_t* k_weight, const uint16_t* v, int64_t ldv,
+                              const int64_t* slots, const uint16_t* q, int64_t ldq, int q_heads,
+                              const uint16_t* q_weight, uint16_t* q_out, int64_t ldqo, float eps, int tokens,
+                              void* stream);
+
+/*
+ * tl_sample -- one token a row of logits, from a given uniform number.
+ *
+ *   With w_i = exp((x_i - max x) / T) and the row's values in the order of x
+ *   falling, equal ones by index rising, a token is kept if it is
+ *     among the first top_k, and
+ *     in the shortest run from the first on whose weights reach top_p times
+ *     those of the first top_k, and
+ *     of weight min_p or more;
+ *   the first is always kept.  The row's token is the first kept one, by index,
+ *   at which the running sum of the kept weights passes uniform times their
+ *   sum; its log-probability is ln(w / that sum).  Weights below 2^-40 count as
+ *   none.  They are held as whole numbers, 2^43 for the largest and each within
+ *   about 2^-40 of it, so sums are exact whatever their order.
+ *
+ *   logits       FP16 (fp16 = 1) or FP32 (0) [rows][vocab], row stride ld
+ *                (elements); -infinity: a token that is not to be drawn.  A row
+ *                with a NaN or +infinity, or with nothing else than -infinity,
+ *                gives token -1 and log-probability NaN
+ *   vocab        1 .. 2^20
+ *   uniform      FP32 [rows], taken into [0, 1 - 2^-24]
+ *   temperature  FP32 [rows] or NULL (1); not above 0 (or NaN): the row's
+ *                greatest logit, the first of equal ones, log-probability 0
+ *   top_k        int32 [rows] or NULL; below 1: all
+ *   top_p, min_p FP32 [rows] or NULL; top_p of 1 or more and min_p of 0 or less
+ *                (or NaN) leave every token, min_p above 1 counts as 1
+ *   tokens       out int32 [rows];  logprobs  out FP32 [rows] or NULL
+ *   Outputs overlap no input and not each other.  Deterministic.  Returns
+ *   TLQ_OK, TLQ_EINVAL, TLQ_EUNSUPPORTED (a longer row) or TLQ_ECUDA.
+ */
+tlq_status tl_sample(const void* logits, int fp16, int64_t ld, int rows, int vocab, const float* uniform,
+                     const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                     int32_t* tokens, float* logprobs, void* stream);
+
+/*
  * tl_lora_add -- low-rank adapters of many requests beside a shared projection:
  *
  *   out[t] = fp16( y[t] + scales[a] * B[a] (A[a] x[t]) ),  a = adapters[b] of

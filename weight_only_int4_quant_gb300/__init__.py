@@ -31,6 +31,8 @@ __all__ = [
     "tl_loop_block_l2_plan", "tl_prefill_plan",
     "tl_kv4_block_bytes", "tl_kv_plan", "tl_kv4_append", "tl_kv4_read", "tl_kv4_attention",
     "tl_kv4_attention_workspace_size", "tl_lora_add", "KV4Cache", "kv4_attention", "lora_add",
+    "tl_rope_table", "tl_qk_norm_rope", "tl_kv4_append_rope", "tl_sample", "Rope", "rope_table", "qk_norm_rope",
+    "sample",
 ]
 
 # every symbol include/tlq.h declares
@@ -43,7 +45,8 @@ EXPORTED = (
     "tl_quant_gemm_batched_host", "tl_quant_gemm_ws", "tl_quant_gemm_workspace_size", "tl_quant_gemm_swiglu_ws",
     "tl_loop_block_to_int2", "tl_swiglu_block_to_int2", "tl_probe_read_bandwidth", "tl_loop_block_l2_plan",
     "tl_prefill_plan", "tl_kv4_block_bytes", "tl_kv_plan", "tl_kv4_append", "tl_kv4_read", "tl_kv4_attention",
-    "tl_kv4_attention_workspace_size", "tl_lora_add",
+    "tl_kv4_attention_workspace_size", "tl_lora_add", "tl_rope_table", "tl_qk_norm_rope", "tl_kv4_append_rope",
+    "tl_sample",
 )
 
 TLQ_OK, TLQ_EINVAL, TLQ_EUNSUPPORTED, TLQ_ECUDA, TLQ_ETIMEOUT = 0, 1, 2, 3, 4
@@ -94,9 +97,14 @@ class _KV4Cache(ctypes.Structure):
                 ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int), ("group", ctypes.c_int)]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("num_positions", ctypes.c_int64), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("axes", ctypes.c_int), ("sections", ctypes.c_int * 3)]
+
+
 _lock = threading.Lock()
 _lib = None
-_f16 = _f32 = _i32 = _i64 = _u8 = None  # torch's types, once the library is loaded
+_f16 = _f32 = _f64 = _i32 = _i64 = _u8 = None  # torch's types, once the library is loaded
 
 
 class _LongWay:
@@ -107,7 +115,7 @@ class _LongWay:
     def plan(*args):
         return -1
 
-    append = read = attention = lora = plan
+    append = read = attention = lora = norm_rope = append_rope = sample = plan
 
 
 _short = _LongWay  # the C API module of the serving calls, once loaded
@@ -129,8 +137,9 @@ def load():
         try:  # share the process's CUDA runtime with torch
             import torch
 
-            global _f16, _f32, _i32, _i64, _u8
+            global _f16, _f32, _f64, _i32, _i64, _u8
             _f16, _f32, _i32, _i64, _u8 = torch.float16, torch.float32, torch.int32, torch.int64, torch.uint8
+            _f64 = torch.float64
         except ImportError:
             pass
         if not os.path.exists(_LIB_PATH):
@@ -139,7 +148,7 @@ def load():
         lib = ctypes.CDLL(_LIB_PATH)
         P, I, U = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint
         L, Z, F = ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
-        KV = ctypes.POINTER(_KV4Cache)
+        KV, R, D = ctypes.POINTER(_KV4Cache), ctypes.POINTER(_Rope), ctypes.c_double
         sigs = {
             "tl_last_error": ([], ctypes.c_char_p),
             "tl_version": ([], ctypes.c_char_p),
@@ -178,6 +187,10 @@ def load():
             "tl_kv4_attention": ([KV, P, L, I, P, L, P, P, P, I, I, I, I, F, I, P, Z, P], I),
             "tl_kv4_attention_workspace_size": ([I, I, I, I], Z),
             "tl_lora_add": ([P, L, P, P, P, P, P, I, I, I, I, I, I, I, P, L, P, L, P], I),
+            "tl_rope_table": ([P, L, I, D, P, P], I),
+            "tl_qk_norm_rope": ([R, P, P, L, I, P, P, L, P, L, I, P, P, L, I, F, I, P], I),
+            "tl_kv4_append_rope": ([KV, R, P, P, L, P, P, L, P, P, L, I, P, P, L, F, I, P], I),
+            "tl_sample": ([P, I, L, I, I, P, P, P, P, P, P, P, P], I),
         }
         for name, (args, res) in sigs.items():
             f = getattr(lib, name)
@@ -204,6 +217,8 @@ def _load_binding(lib):
     module.bind(_f16, _f32, _i32, _i64, _u8, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
                 *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                   for f in ("tl_kv_plan", "tl_kv4_append", "tl_kv4_read", "tl_kv4_attention", "tl_lora_add")))
+    module.bind_step(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                       for f in ("tl_qk_norm_rope", "tl_kv4_append_rope", "tl_sample")))
     _short = module
 
 
@@ -801,6 +816,152 @@ def tl_lora_add(x, A, B, scales, q_start, adapters, max_q: int, y, out, stream=N
 
 
 # ---------------------------------------------------------------------------
+# between the projections and the cache, and behind the last projection
+# ---------------------------------------------------------------------------
+
+def tl_rope_table(inv_freq, table, scale: float = 1.0, stream=None) -> None:
+    """cos and sin of position * inv_freq (FP64 [rot_dim / 2]), times scale, into
+    table (FP32 [positions, rot_dim / 2, 2])."""
+    half = inv_freq.numel()
+    if table.dim() != 3 or tuple(table.shape[1:]) != (half, 2):
+        raise ValueError("table has shape %s, expected [positions, %d, 2]" % (tuple(table.shape), half))
+    _raise_if(load().tl_rope_table(_dev(inv_freq, (_f64,), "inv_freq"), table.shape[0], 2 * half, scale,
+                                   _dev(table, (_f32,), "table"), _stream(stream)))
+
+
+class Rope:
+    """Rotary positions: the table of cosines and sines (FP32 CUDA tensor
+    [positions, rot_dim / 2, 2], see tl_rope_table), how channels pair up
+    (interleaved: neighbours, else the halves of the rotated channels) and the
+    pairs of each position axis (sections; one axis when not given)."""
+
+    def __init__(self, table, interleaved: bool = False, sections=None):
+        load()
+        if table.dim() != 3 or table.shape[2] != 2:
+            raise ValueError("table has shape %s, expected [positions, rot_dim / 2, 2]" % (tuple(table.shape),))
+        sections = [table.shape[1]] if sections is None else [int(n) for n in sections]
+        if not 1 <= len(sections) <= 3 or min(sections) < 0 or sum(sections) != table.shape[1]:
+            raise ValueError("sections %s: one to three, not negative, of %d pairs in all" % (sections, table.shape[1]))
+        self.table, self.rot_dim, self.axes, self.sections = table, 2 * table.shape[1], len(sections), tuple(sections)
+        self.interleaved = bool(interleaved)
+        self._c = _Rope(_dev(table, (_f32,), "table"), table.shape[0], self.rot_dim, int(self.interleaved), self.axes,
+                        (ctypes.c_int * 3)(*sections))
+        self._ref = ctypes.byref(self._c)
+        self._address = ctypes.addressof(self._c)
+
+
+def _positions(rope, positions, tokens):
+    if rope is None:
+        return None
+    if positions is None:
+        raise ValueError("positions are needed beside a rope")
+    if rope.axes > 1 and tuple(positions.shape) != (rope.axes, tokens):
+        raise ValueError("positions have shape %s, expected [%d, %d]" % (tuple(positions.shape), rope.axes, tokens))
+    return _ints(positions, _i32, "positions", rope.axes * tokens)
+
+
+def _head_rows(x, out, weight, head_dim, name):
+    """Pointers and strides of one kind of heads: (x, ld, heads, weight, out, ld of out, tokens)."""
+    if x is None:
+        return None, 0, 0, None, None, 0, None
+    if x.dim() != 3:
+        raise ValueError("%s has shape %s, expected [tokens, heads, %d]" % (name, tuple(x.shape), head_dim))
+    heads = x.shape[1]
+    xp, ld, tokens = _rows3(x, _f16, name, heads, head_dim)
+    op = ldo = None
+    if out is not None:
+        op, ldo, n = _rows3(out, _f16, name + "_out", heads, head_dim)
+        if n != tokens:
+            raise ValueError("%s_out has %d tokens, %s %d" % (name, n, name, tokens))
+    wp = None if weight is None else _ints(weight, _f16, name + "_weight", head_dim)
+    return xp, ld, heads, wp, op, ldo or 0, tokens
+
+
+def tl_qk_norm_rope(rope, q, k, positions, q_out, k_out, q_weight=None, k_weight=None, eps: float = 1e-6,
+                    stream=None) -> None:
+    """Norm (where a weight is given) and rotate (where a rope is) the heads of q
+    and k [tokens, heads, head_dim] into q_out and k_out, which may be q and k
+    themselves; either may be None.  positions: int32 [tokens] or [axes, tokens]."""
+    lib = _lib or load()
+    st = _short.norm_rope(None if rope is None else rope._address, 0 if rope is None else rope.axes, q, k, positions,
+                          q_out, k_out, q_weight, k_weight, eps, stream)
+    if st == 0:
+        return
+    if st > 0:
+        _raise_if(st)
+    if q is None and k is None:
+        raise ValueError("q and k are both None")
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is not None and out is None:
+            raise ValueError("%s_out is None" % name)
+    some = q if q is not None else k
+    d = some.shape[-1]
+    qp, ldq, hq, qw, qo, ldqo, nq = _head_rows(q, q_out, q_weight, d, "q")
+    kp, ldk, hk, kw, ko, ldko, nk = _head_rows(k, k_out, k_weight, d, "k")
+    tokens = nk if nq is None else nq
+    if nk not in (None, tokens):
+        raise ValueError("q and k have %d and %d tokens" % (nq, nk))
+    st = lib.tl_qk_norm_rope(None if rope is None else rope._ref, _positions(rope, positions, tokens), qp, ldq, hq, qw,
+                             qo, ldqo, kp, ldk, hk, kw, ko, ldko, d, eps, tokens, _stream(stream))
+    if st:
+        _raise_if(st)
+
+
+def tl_kv4_append_rope(cache: KV4Cache, rope, k, v, positions, slots, k_weight=None, q=None, q_out=None,
+                       q_weight=None, eps: float = 1e-6, stream=None) -> None:
+    """Norm and rotate keys on their way into the cache's slots, with the values;
+    q (if given) normed and rotated into q_out, which may be q."""
+    st = _short.append_rope(cache._address, cache.heads, cache.head_dim, None if rope is None else rope._address,
+                            0 if rope is None else rope.axes, k, v, positions, slots, k_weight, q, q_out, q_weight, eps,
+                            stream)
+    if st == 0:
+        return
+    if st > 0:
+        _raise_if(st)
+    kp, ldk, nk = _rows3(k, _f16, "k", cache.heads, cache.head_dim)
+    vp, ldv, nv = _rows3(v, _f16, "v", cache.heads, cache.head_dim)
+    n = slots.numel()
+    if q is not None and q_out is None:
+        raise ValueError("q_out is None")
+    qp, ldq, hq, qw, qo, ldqo, nq = _head_rows(q, q_out, q_weight, cache.head_dim, "q")
+    if nk != n or nv != n or nq not in (None, n):
+        raise ValueError("k, v and q have %d, %d and %s tokens, slots %d" % (nk, nv, nq, n))
+    kw = None if k_weight is None else _ints(k_weight, _f16, "k_weight", cache.head_dim)
+    st = _lib.tl_kv4_append_rope(cache._ref, None if rope is None else rope._ref, _positions(rope, positions, n), kp, ldk,
+                                 kw, vp, ldv, _ptr(slots, _i64, "slots"), qp, ldq, hq, qw, qo, ldqo, eps, n,
+                                 _stream(stream))
+    if st:
+        _raise_if(st)
+
+
+def tl_sample(logits, uniform, tokens, temperature=None, top_k=None, top_p=None, min_p=None, logprobs=None,
+              stream=None) -> None:
+    """A token of each row of logits [rows, vocab] (FP16 or FP32) into tokens
+    (int32 [rows]), from one uniform number a row; temperature, top_k (int32),
+    top_p and min_p are arrays of one value a row, or None."""
+    lib = _lib or load()
+    st = _short.sample(logits, uniform, tokens, temperature, top_k, top_p, min_p, logprobs, stream)
+    if st == 0:
+        return
+    if st > 0:
+        _raise_if(st)
+    if logits.dim() != 2:
+        raise ValueError("logits have shape %s, expected [rows, vocab]" % (tuple(logits.shape),))
+    rows, vocab = logits.shape
+    if logits.dtype not in (_f16, _f32):
+        raise ValueError("logits have dtype %s, expected float16 or float32" % logits.dtype)
+    lp, ld = _rows(logits, logits.dtype, "logits", (vocab,))
+    optional = [None if t is None else _ints(t, kind, name, rows)
+                for t, kind, name in ((temperature, _f32, "temperature"), (top_k, _i32, "top_k"),
+                                      (top_p, _f32, "top_p"), (min_p, _f32, "min_p"))]
+    st = lib.tl_sample(lp, int(logits.dtype is _f16), ld, rows, vocab, _ints(uniform, _f32, "uniform", rows), *optional,
+                       _ints(tokens, _i32, "tokens", rows),
+                       None if logprobs is None else _ints(logprobs, _f32, "logprobs", rows), _stream(stream))
+    if st:
+        _raise_if(st)
+
+
+# ---------------------------------------------------------------------------
 # conveniences that allocate their outputs with torch (on the stream they run on)
 # ---------------------------------------------------------------------------
 
@@ -879,6 +1040,38 @@ def lora_add(x, A, B, scales, q_start, adapters, max_q: int, y, stream=None):
         out = torch.empty(y.shape, dtype=torch.float16, device=y.device)
         tl_lora_add(x, A, B, scales, q_start, adapters, max_q, y, out, stream)
     return _result(stream, out)
+
+
+def rope_table(num_positions: int, inv_freq, scale: float = 1.0, stream=None):
+    """The table of a Rope: cos and sin of position * inv_freq (FP64 CUDA tensor)."""
+    import torch
+
+    with _on(stream):
+        table = torch.empty((num_positions, inv_freq.numel(), 2), dtype=torch.float32, device=inv_freq.device)
+        tl_rope_table(inv_freq, table, scale, stream)
+    return _result(stream, table)
+
+
+def qk_norm_rope(rope, q, k, positions, q_weight=None, k_weight=None, eps: float = 1e-6, stream=None):
+    """(q, k) normed and rotated, compact.  Tokens that are passed over hold zeros."""
+    import torch
+
+    with _on(stream):
+        q_out = torch.zeros(q.shape, dtype=torch.float16, device=q.device)
+        k_out = torch.zeros(k.shape, dtype=torch.float16, device=k.device)
+        tl_qk_norm_rope(rope, q, k, positions, q_out, k_out, q_weight, k_weight, eps, stream)
+    return _result(stream, q_out, k_out)
+
+
+def sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """(tokens, log-probabilities) of the rows of logits."""
+    import torch
+
+    with _on(stream):
+        tokens = torch.empty((logits.shape[0],), dtype=torch.int32, device=logits.device)
+        logprobs = torch.empty((logits.shape[0],), dtype=torch.float32, device=logits.device)
+        tl_sample(logits, uniform, tokens, temperature, top_k, top_p, min_p, logprobs, stream)
+    return _result(stream, tokens, logprobs)
 
 
 def unpack_weights(W, K: int, bits: int, stream=None):

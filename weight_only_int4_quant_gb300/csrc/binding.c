@@ -12,6 +12,7 @@
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <string.h>
 
 #include "../../include/tlq.h"
 
@@ -31,6 +32,15 @@ static tlq_status (*f_attention)(const tl_kv4_cache*, const uint16_t*, int64_t, 
 static tlq_status (*f_lora)(const uint16_t*, int64_t, const uint16_t*, const uint16_t*, const float*, const int32_t*,
                             const int32_t*, int, int, int, int, int, int, int, const uint16_t*, int64_t, uint16_t*,
                             int64_t, void*);
+
+static tlq_status (*f_norm_rope)(const tl_rope*, const int32_t*, const uint16_t*, int64_t, int, const uint16_t*, uint16_t*,
+                                 int64_t, const uint16_t*, int64_t, int, const uint16_t*, uint16_t*, int64_t, int, float,
+                                 int, void*);
+static tlq_status (*f_append_rope)(const tl_kv4_cache*, const tl_rope*, const int32_t*, const uint16_t*, int64_t,
+                                   const uint16_t*, const uint16_t*, int64_t, const int64_t*, const uint16_t*, int64_t,
+                                   int, const uint16_t*, uint16_t*, int64_t, float, int, void*);
+static tlq_status (*f_sample)(const void*, int, int64_t, int, int, const float*, const float*, const int32_t*, const float*,
+                              const float*, int32_t*, float*, void*);
 
 /* 1 if attribute `name` of o is `want` (an object compared by identity). */
 static int attr_is(PyObject* o, PyObject* name, PyObject* want) {
@@ -224,6 +234,98 @@ static int lora(PyObject* const* a, Py_ssize_t n) {
        (int)sa[1], (int)sa[0], y, ldy, out, ldo, s);
 }
 
+/* As flat(), with None for NULL. */
+static int flat_or_none(PyObject* t, PyObject* type, long long n, void** p) {
+  *p = NULL;
+  return t == Py_None || flat(t, type, n, p, NULL);
+}
+
+/* Heads [tokens, heads, dim] (None: none) with their output (out NULL: they have
+ * none) and weight; *tokens is checked, or filled in where it is negative. */
+typedef struct {
+  void *x, *out, *weight;
+  int64_t ld, ldo;
+  long long heads;
+} head_rows;
+static int heads_of(PyObject* x, PyObject* out, PyObject* weight, long long dim, long long* tokens, head_rows* r) {
+  long long size[3], n;
+  memset(r, 0, sizeof *r);
+  if (x == Py_None) return 1;
+  if (!extents(x, 0, 3, size) || !rows(x, 3, size[1], dim, &r->x, &r->ld, &n) || (*tokens >= 0 && n != *tokens) ||
+      size[1] > 0x7fffffffll || !flat_or_none(weight, t_f16, dim, &r->weight))
+    return 0;
+  *tokens = n;
+  r->heads = size[1];
+  if (!out) return 1;
+  return rows(out, 3, size[1], dim, &r->out, &r->ldo, &n) && n == *tokens;
+}
+
+/* The rope's descriptor by its address, and its positions [axes, tokens] (of one
+ * axis: that many of any shape); None: neither. */
+static int rope_of(PyObject* address, PyObject* axes, PyObject* positions, long long tokens, const tl_rope** r, void** p) {
+  long long n, size[2];
+  *r = NULL;
+  *p = NULL;
+  if (address == Py_None) return 1;
+  *r = (const tl_rope*)PyLong_AsVoidPtr(address);
+  return *r && !PyErr_Occurred() && as_int(axes, &n) && flat(positions, t_i32, n * tokens, p, NULL) &&
+         (n == 1 || (extents(positions, 0, 2, size) && size[0] == n));
+}
+
+static int norm_rope(PyObject* const* a, Py_ssize_t n) {
+  /* rope address, axes, q, k, positions, q_out, k_out, q_weight, k_weight, eps, stream */
+  const tl_rope* rope;
+  void *positions, *s;
+  long long size[3], tokens = -1;
+  head_rows q, k;
+  if (n != 11 || (a[2] == Py_None && a[3] == Py_None) || !extents(a[2] != Py_None ? a[2] : a[3], 0, 3, size) ||
+      !heads_of(a[2], a[5], a[7], size[2], &tokens, &q) || !heads_of(a[3], a[6], a[8], size[2], &tokens, &k) ||
+      !rope_of(a[0], a[1], a[4], tokens, &rope, &positions) || !PyFloat_CheckExact(a[9]) || !stream_of(a[10], &s) ||
+      tokens > 0x7fffffffll || size[2] > 0x7fffffffll)
+    return FALLBACK;
+  const float eps = (float)PyFloat_AS_DOUBLE(a[9]);
+  CALL(f_norm_rope, rope, positions, q.x, q.ld, (int)q.heads, q.weight, q.out, q.ldo, k.x, k.ld, (int)k.heads, k.weight,
+       k.out, k.ldo, (int)size[2], eps, (int)tokens, s);
+}
+
+static int append_rope(PyObject* const* a, Py_ssize_t n) {
+  /* cache address, heads, head_dim, rope address, axes, k, v, positions, slots, k_weight, q, q_out, q_weight, eps,
+   * stream */
+  const tl_kv4_cache* c;
+  const tl_rope* rope;
+  void *positions, *slots, *s;
+  long long heads, dim, tokens = -1;
+  head_rows q, k, v;
+  if (n != 15 || !cache_of(a[0], &c) || !as_int(a[1], &heads) || !as_int(a[2], &dim) ||
+      !heads_of(a[5], NULL, a[9], dim, &tokens, &k) || k.heads != heads ||
+      !heads_of(a[6], NULL, Py_None, dim, &tokens, &v) || v.heads != heads ||
+      !heads_of(a[10], a[11], a[12], dim, &tokens, &q) || !flat(a[8], t_i64, tokens, &slots, NULL) ||
+      !rope_of(a[3], a[4], a[7], tokens, &rope, &positions) || !PyFloat_CheckExact(a[13]) || !stream_of(a[14], &s) ||
+      tokens > 0x7fffffffll)
+    return FALLBACK;
+  const float eps = (float)PyFloat_AS_DOUBLE(a[13]);
+  CALL(f_append_rope, c, rope, positions, k.x, k.ld, k.weight, v.x, v.ld, slots, q.x, q.ld, (int)q.heads, q.weight, q.out,
+       q.ldo, eps, (int)tokens, s);
+}
+
+static int sample(PyObject* const* a, Py_ssize_t n) {
+  /* logits, uniform, tokens, temperature, top_k, top_p, min_p, logprobs, stream */
+  void *x, *uniform, *tokens, *temperature, *top_k, *top_p, *min_p, *logprobs, *s;
+  long long size[2], step[2];
+  if (n != 9 || !extents(a[0], 0, 2, size) || !extents(a[0], 1, 2, step) || size[0] < 1 || step[1] != 1 ||
+      !attr_is(a[0], s_is_cuda, Py_True))
+    return FALLBACK;
+  const int half = attr_is(a[0], s_dtype, t_f16);
+  if ((!half && !attr_is(a[0], s_dtype, t_f32)) || !pointer(a[0], &x) || !flat(a[1], t_f32, size[0], &uniform, NULL) ||
+      !flat(a[2], t_i32, size[0], &tokens, NULL) || !flat_or_none(a[3], t_f32, size[0], &temperature) ||
+      !flat_or_none(a[4], t_i32, size[0], &top_k) || !flat_or_none(a[5], t_f32, size[0], &top_p) ||
+      !flat_or_none(a[6], t_f32, size[0], &min_p) || !flat_or_none(a[7], t_f32, size[0], &logprobs) ||
+      !stream_of(a[8], &s) || size[0] > 0x7fffffffll || size[1] > 0x7fffffffll)
+    return FALLBACK;
+  CALL(f_sample, x, half, size[0] > 1 ? step[0] : size[1], (int)size[0], (int)size[1], uniform, temperature, top_k, top_p,
+       min_p, tokens, logprobs, s);
+}
+
 #define METHOD(name)                                                              \
   static PyObject* py_##name(PyObject* self, PyObject* const* a, Py_ssize_t n) { \
     (void)self;                                                                   \
@@ -234,6 +336,9 @@ METHOD(append)
 METHOD(read_back)
 METHOD(attention)
 METHOD(lora)
+METHOD(norm_rope)
+METHOD(append_rope)
+METHOD(sample)
 
 /* bind(float16, float32, int32, int64, uint8, get_device, get_stream, and the
  * addresses of the five entry points in the order above) */
@@ -266,6 +371,25 @@ static PyObject* bind(PyObject* self, PyObject* args) {
   Py_RETURN_NONE;
 }
 
+/* bind_step(addresses of tl_qk_norm_rope, tl_kv4_append_rope, tl_sample) */
+static PyObject* bind_step(PyObject* self, PyObject* args) {
+  PyObject* f[3];
+  void* p[3];
+  (void)self;
+  if (!PyArg_ParseTuple(args, "OOO", &f[0], &f[1], &f[2])) return NULL;
+  for (int i = 0; i < 3; ++i) {
+    p[i] = PyLong_AsVoidPtr(f[i]);
+    if (!p[i] || PyErr_Occurred()) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null entry point");
+      return NULL;
+    }
+  }
+  *(void**)&f_norm_rope = p[0];
+  *(void**)&f_append_rope = p[1];
+  *(void**)&f_sample = p[2];
+  Py_RETURN_NONE;
+}
+
 static PyMethodDef methods[] = {
     {"bind", bind, METH_VARARGS, "Torch's types and the library's entry points; once."},
     {"plan", (PyCFunction)(void (*)(void))py_plan, METH_FASTCALL, "tl_kv_plan"},
@@ -273,6 +397,10 @@ static PyMethodDef methods[] = {
     {"read", (PyCFunction)(void (*)(void))py_read_back, METH_FASTCALL, "tl_kv4_read"},
     {"attention", (PyCFunction)(void (*)(void))py_attention, METH_FASTCALL, "tl_kv4_attention"},
     {"lora", (PyCFunction)(void (*)(void))py_lora, METH_FASTCALL, "tl_lora_add"},
+    {"bind_step", bind_step, METH_VARARGS, "The entry points of a step's other calls; once, after bind."},
+    {"norm_rope", (PyCFunction)(void (*)(void))py_norm_rope, METH_FASTCALL, "tl_qk_norm_rope"},
+    {"append_rope", (PyCFunction)(void (*)(void))py_append_rope, METH_FASTCALL, "tl_kv4_append_rope"},
+    {"sample", (PyCFunction)(void (*)(void))py_sample, METH_FASTCALL, "tl_sample"},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tlq_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};

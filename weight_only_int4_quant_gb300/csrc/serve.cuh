@@ -232,6 +232,51 @@ tlq_status launch_kv4_append(const KvCache& c, int head_dim, const __half* k, lo
 tlq_status launch_kv4_read(const KvCache& c, int head_dim, const long long* slots, int tokens, __half* k, __half* v,
                            cudaStream_t stream);
 
+// cos and sin of each position and pair, and which axis a pair's position is taken from.
+struct RopeTable {
+  const float2* table;  // [positions][rot / 2]
+  int positions;
+  int rot;         // channels that are rotated; 0: none
+  bool neighbours;  // pairs (2 i, 2 i + 1); else (i, i + rot / 2)
+  int axes, end0, end1;  // pairs below end0 go by the first axis, below end1 by the second
+};
+struct RopeRows {
+  const __half* x;
+  long long ld;
+  __half* out;  // NULL: into the cache
+  long long ldo;
+  const __half* weight;  // NULL: no norm
+  int heads;
+};
+struct RopeArgs {
+  const char* who;
+  RopeTable rope;
+  const int* positions;  // [axes][tokens]
+  RopeRows q, k, v;
+  int tokens, head_dim;
+  float eps;
+  KvCache cache;
+  const long long* slots;
+};
+tlq_status launch_rope(const RopeArgs& a, cudaStream_t stream);
+tlq_status launch_rope_table(const double* freq, float* table, long long positions, int half, double scale,
+                             cudaStream_t stream);
+
+// The longest row of logits (whole-number weights of 2^43 add up in 64 bits).
+constexpr int kMaxVocab = 1 << 20;
+struct SampleArgs {
+  const void* logits;
+  bool half;  // FP16, else FP32
+  long long ld;
+  int rows, vocab;
+  const float *uniform, *temperature;
+  const int* top_k;
+  const float *top_p, *min_p;
+  int* tokens;
+  float* logprobs;
+};
+tlq_status launch_sample(const SampleArgs& a, cudaStream_t stream);
+
 struct KvAttention {
   KvCache cache;
   KvBatch batch;

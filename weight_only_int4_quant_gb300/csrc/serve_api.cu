@@ -66,6 +66,95 @@ constexpr int kFewRows = 64;
 
 size_t cache_bytes(const KvCache& c) { return (size_t)c.num_pages * c.heads * c.block_bytes; }
 
+// Rows that may lie in others' gaps (columns of a fused projection's rows).
+struct RowSet {
+  const void* p;
+  size_t step, bytes;  // from row to row, of a row
+};
+
+// Two sets of `rows` rows share bytes.
+bool meet(const RowSet& a, const RowSet& b, long long rows) {
+  if (!a.bytes || !b.bytes || rows < 1) return false;
+  if (!overlap(a.p, (rows - 1) * a.step + a.bytes, b.p, (rows - 1) * b.step + b.bytes)) return false;
+  if (rows == 1 || a.step != b.step) return true;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  const size_t d = y >= x ? (y - x) % a.step : (a.step - (x - y) % a.step) % a.step;  // b's rows behind a's
+  return d < a.bytes || a.step - d < b.bytes;
+}
+
+long long row_values(const RopeRows& r, const RopeArgs& a) { return (long long)r.heads * a.head_dim; }
+RowSet rows_in(const RopeRows& r, const RopeArgs& a) {
+  return RowSet{r.x, 2 * (size_t)r.ld, 2 * (size_t)row_values(r, a)};
+}
+RowSet rows_out(const RopeRows& r, const RopeArgs& a) {
+  return RowSet{r.out, 2 * (size_t)r.ldo, 2 * (size_t)row_values(r, a)};
+}
+size_t table_bytes(const RopeTable& t) { return 4 * (size_t)t.positions * t.rot; }
+size_t positions_bytes(const RopeArgs& a) { return a.rope.rot ? 4 * (size_t)a.rope.axes * a.tokens : 0; }
+
+// r's output overlaps an input other than its own rows, or those but not exactly.
+bool output_meets(const RopeRows& r, const RopeArgs& a) {
+  if (!r.heads) return false;
+  const RowSet out = rows_out(r, a);
+  for (const RopeRows* x : {&a.q, &a.k, &a.v}) {
+    if (x->heads && !(x == &r && r.out == r.x && (r.ld == r.ldo || a.tokens == 1)) && meet(out, rows_in(*x, a), a.tokens))
+      return true;
+    if (x->weight && overlap(r.out, span(a.tokens, r.ldo, row_values(r, a), 2), x->weight, 2 * (size_t)a.head_dim))
+      return true;
+  }
+  const size_t n = span(a.tokens, r.ldo, row_values(r, a), 2);
+  return overlap(r.out, n, a.positions, positions_bytes(a)) || overlap(r.out, n, a.rope.table, table_bytes(a.rope)) ||
+         overlap(r.out, n, a.slots, a.slots ? 8 * (size_t)a.tokens : 0);
+}
+
+tlq_status check_rope(const char* who, const tl_rope* rope, const int32_t* positions, int head_dim, float eps, int tokens,
+                      RopeArgs* a) {
+  if (tokens < 0) return set_error(TLQ_EINVAL, "%s: tokens=%d", who, tokens);
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return set_error(TLQ_EINVAL, "%s: eps=%g (finite, not negative)", who, eps);
+  a->who = who;
+  a->tokens = tokens;
+  a->head_dim = head_dim;
+  a->eps = eps;
+  if (!rope) return TLQ_OK;
+  const int rot = rope->rot_dim;
+  if (rot < 16 || rot > head_dim || rot % 16)
+    return set_error(TLQ_EINVAL, "%s: rot_dim=%d (a multiple of 16, up to head_dim=%d)", who, rot, head_dim);
+  if (rope->num_positions < 1 || rope->num_positions > kMaxContext)
+    return set_error(TLQ_EINVAL, "%s: num_positions=%lld (1..2^30)", who, (long long)rope->num_positions);
+  if (rope->axes < 1 || rope->axes > 3) return set_error(TLQ_EINVAL, "%s: axes=%d (1..3)", who, rope->axes);
+  long long pairs = 0;
+  for (int i = 0; i < rope->axes; ++i) {
+    if (rope->sections[i] < 0) return set_error(TLQ_EINVAL, "%s: sections[%d]=%d", who, i, rope->sections[i]);
+    pairs += rope->sections[i];
+  }
+  if (pairs != rot / 2)
+    return set_error(TLQ_EINVAL, "%s: the sections hold %lld pairs, rot_dim=%d has %d", who, pairs, rot, rot / 2);
+  if (tokens > 0 && (!rope->table || !positions)) return set_error(TLQ_EINVAL, "%s: null pointer", who);
+  if (!aligned(rope->table, 16) || !aligned(positions, 4))
+    return set_error(TLQ_EINVAL, "%s: the table must be 16-byte aligned, positions 4-byte", who);
+  a->rope = RopeTable{reinterpret_cast<const float2*>(rope->table), (int)rope->num_positions, rot,
+                      rope->interleaved != 0, rope->axes, rope->sections[0],
+                      rope->axes > 1 ? rope->sections[0] + rope->sections[1] : rot / 2};
+  a->positions = positions;
+  return TLQ_OK;
+}
+
+tlq_status check_heads(const char* who, const char* name, const uint16_t* x, int64_t ld, int heads,
+                       const uint16_t* weight, uint16_t* out, int64_t ldo, bool has_out, const RopeArgs& a, RopeRows* r) {
+  if (heads < 0 || heads > 4096) return set_error(TLQ_EINVAL, "%s: %s_heads=%d (0..4096)", who, name, heads);
+  if (heads == 0 || a.tokens == 0) return TLQ_OK;
+  const long long row = (long long)heads * a.head_dim;
+  if (!x || (has_out && !out)) return set_error(TLQ_EINVAL, "%s: null pointer", who);
+  if (a.tokens > 1 && (ld < row || ld % 8 || (has_out && (ldo < row || ldo % 8))))
+    return set_error(TLQ_EINVAL, "%s: ld%s=%lld ld%s_out=%lld (at least heads*head_dim = %lld, multiples of 8)", who, name,
+                     (long long)ld, name, (long long)ldo, row);
+  if (!aligned(x, 16) || !aligned(out, 16) || !aligned(weight, 16))
+    return set_error(TLQ_EINVAL, "%s: %s, its output and its weight must be 16-byte aligned", who, name);
+  *r = RopeRows{reinterpret_cast<const __half*>(x), ld, reinterpret_cast<__half*>(out), ldo,
+                reinterpret_cast<const __half*>(weight), heads};
+  return TLQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -253,6 +342,114 @@ tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_
     ls = launch_kv4_prefill(a, few, static_cast<uint8_t*>(workspace) + kv4_decode_workspace(cache->head_dim),
                             &many_parts, s);
   return ls == TLQ_OK ? launch_kv4_join(a, few_parts, many_parts, s) : ls;
+}
+
+tlq_status tl_rope_table(const double* inv_freq, int64_t num_positions, int rot_dim, double scale, float* table,
+                         void* stream) {
+  clear_error();
+  const char* who = "tl_rope_table";
+  if (rot_dim < 16 || rot_dim > 256 || rot_dim % 16)
+    return set_error(TLQ_EINVAL, "%s: rot_dim=%d (a multiple of 16, 16..256)", who, rot_dim);
+  if (num_positions < 1 || num_positions > kMaxContext)
+    return set_error(TLQ_EINVAL, "%s: num_positions=%lld (1..2^30)", who, (long long)num_positions);
+  if (!std::isfinite(scale)) return set_error(TLQ_EINVAL, "%s: scale is not finite", who);
+  if (!inv_freq || !table) return set_error(TLQ_EINVAL, "%s: null pointer", who);
+  if (!aligned(table, 16) || !aligned(inv_freq, 8))
+    return set_error(TLQ_EINVAL, "%s: table must be 16-byte aligned, inv_freq 8-byte", who);
+  if (overlap(table, 4 * (size_t)num_positions * rot_dim, inv_freq, 4 * (size_t)rot_dim))
+    return set_error(TLQ_EINVAL, "%s: table overlaps inv_freq", who);
+  return launch_rope_table(inv_freq, table, num_positions, rot_dim / 2, scale, static_cast<cudaStream_t>(stream));
+}
+
+tlq_status tl_qk_norm_rope(const tl_rope* rope, const int32_t* positions, const uint16_t* q, int64_t ldq, int q_heads,
+                           const uint16_t* q_weight, uint16_t* q_out, int64_t ldqo, const uint16_t* k, int64_t ldk,
+                           int k_heads, const uint16_t* k_weight, uint16_t* k_out, int64_t ldko, int head_dim,
+                           float eps, int tokens, void* stream) {
+  clear_error();
+  const char* who = "tl_qk_norm_rope";
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return set_error(head_dim > 0 ? TLQ_EUNSUPPORTED : TLQ_EINVAL, "%s: head_dim=%d (64, 128 or 256)", who, head_dim);
+  RopeArgs a{};
+  tlq_status st = check_rope(who, rope, positions, head_dim, eps, tokens, &a);
+  if (st == TLQ_OK) st = check_heads(who, "q", q, ldq, q_heads, q_weight, q_out, ldqo, true, a, &a.q);
+  if (st == TLQ_OK) st = check_heads(who, "k", k, ldk, k_heads, k_weight, k_out, ldko, true, a, &a.k);
+  if (st != TLQ_OK || tokens == 0 || q_heads + k_heads == 0) return st;
+  if (output_meets(a.q, a) || output_meets(a.k, a) || meet(rows_out(a.q, a), rows_out(a.k, a), tokens))
+    return set_error(TLQ_EINVAL, "%s: an output overlaps an input or the other output (it may be exactly its input)", who);
+  return launch_rope(a, static_cast<cudaStream_t>(stream));
+}
+
+tlq_status tl_kv4_append_rope(const tl_kv4_cache* cache, const tl_rope* rope, const int32_t* positions,
+                              const uint16_t* k, int64_t ldk, const uint16_t* k_weight, const uint16_t* v, int64_t ldv,
+                              const int64_t* slots, const uint16_t* q, int64_t ldq, int q_heads,
+                              const uint16_t* q_weight, uint16_t* q_out, int64_t ldqo, float eps, int tokens,
+                              void* stream) {
+  clear_error();
+  const char* who = "tl_kv4_append_rope";
+  RopeArgs a{};
+  tlq_status st = check_cache(cache, &a.cache, who);
+  if (st == TLQ_OK) st = check_rope(who, rope, positions, cache->head_dim, eps, tokens, &a);
+  if (st == TLQ_OK) st = check_heads(who, "q", q, ldq, q_heads, q_weight, q_out, ldqo, true, a, &a.q);
+  if (st == TLQ_OK) st = check_heads(who, "k", k, ldk, a.cache.heads, k_weight, nullptr, 0, false, a, &a.k);
+  if (st == TLQ_OK) st = check_heads(who, "v", v, ldv, a.cache.heads, nullptr, nullptr, 0, false, a, &a.v);
+  if (st != TLQ_OK || tokens == 0) return st;
+  if (!slots) return set_error(TLQ_EINVAL, "%s: null pointer", who);
+  if (!aligned(slots, 8)) return set_error(TLQ_EINVAL, "%s: slots must be 8-byte aligned", who);
+  a.slots = reinterpret_cast<const long long*>(slots);
+  if (output_meets(a.q, a)) return set_error(TLQ_EINVAL, "%s: q_out overlaps an input (it may be exactly q)", who);
+  const size_t cb = cache_bytes(a.cache);
+  bool in_cache = overlap(a.cache.blocks, cb, slots, 8 * (size_t)tokens);
+  for (const RopeRows* r : {&a.q, &a.k, &a.v}) {
+    in_cache |= overlap(a.cache.blocks, cb, r->x, span(r->heads ? tokens : 0, r->ld, row_values(*r, a), 2));
+    in_cache |= overlap(a.cache.blocks, cb, r->weight, r->weight ? 2 * (size_t)a.head_dim : 0);
+  }
+  in_cache |= overlap(a.cache.blocks, cb, a.q.out, span(a.q.heads ? tokens : 0, a.q.ldo, row_values(a.q, a), 2));
+  in_cache |= overlap(a.cache.blocks, cb, a.positions, positions_bytes(a)) ||
+              overlap(a.cache.blocks, cb, a.rope.table, table_bytes(a.rope));
+  if (in_cache) return set_error(TLQ_EINVAL, "%s: the cache overlaps another buffer", who);
+  return launch_rope(a, static_cast<cudaStream_t>(stream));
+}
+
+tlq_status tl_sample(const void* logits, int fp16, int64_t ld, int rows, int vocab, const float* uniform,
+                     const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                     int32_t* tokens, float* logprobs, void* stream) {
+  clear_error();
+  const char* who = "tl_sample";
+  if (rows < 0) return set_error(TLQ_EINVAL, "%s: rows=%d", who, rows);
+  if (vocab < 1) return set_error(TLQ_EINVAL, "%s: vocab=%d (must be >= 1)", who, vocab);
+  if (vocab > kMaxVocab) return set_error(TLQ_EUNSUPPORTED, "%s: vocab=%d (at most %d)", who, vocab, kMaxVocab);
+  if (rows > 0x0fffffff) return set_error(TLQ_EUNSUPPORTED, "%s: rows=%d (at most 2^28 - 1)", who, rows);
+  if (fp16 != 0 && fp16 != 1) return set_error(TLQ_EINVAL, "%s: fp16=%d (1: FP16, 0: FP32)", who, fp16);
+  if (rows == 0) return TLQ_OK;
+  if (!logits || !uniform || !tokens) return set_error(TLQ_EINVAL, "%s: null pointer", who);
+  if (rows > 1 && ld < vocab) return set_error(TLQ_EINVAL, "%s: ld=%lld (at least vocab = %d)", who, (long long)ld, vocab);
+  const size_t size = fp16 ? 2 : 4, n = 4 * (size_t)rows;
+  if (!aligned(logits, size) || !aligned(uniform, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) ||
+      !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(tokens, 4) || !aligned(logprobs, 4))
+    return set_error(TLQ_EINVAL, "%s: arrays must be aligned to their elements", who);
+  const void* const in[5] = {uniform, temperature, top_k, top_p, min_p};
+  const void* const res[2] = {tokens, logprobs};
+  for (const void* o : res) {
+    if (!o) continue;
+    bool meets = overlap(o, n, logits, span(rows, ld, vocab, size));
+    for (const void* i : in) meets |= i && overlap(o, n, i, n);
+    if (meets) return set_error(TLQ_EINVAL, "%s: an output overlaps an input", who);
+  }
+  if (logprobs && overlap(tokens, n, logprobs, n)) return set_error(TLQ_EINVAL, "%s: the outputs overlap", who);
+  SampleArgs a{};
+  a.logits = logits;
+  a.half = fp16 != 0;
+  a.ld = ld;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.uniform = uniform;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.tokens = tokens;
+  a.logprobs = logprobs;
+  return launch_sample(a, static_cast<cudaStream_t>(stream));
 }
 
 tlq_status tl_lora_add(const uint16_t* x, int64_t ldx, const uint16_t* A, const uint16_t* B, const float* scales,
