@@ -717,6 +717,37 @@ tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_
 size_t tl_kv4_attention_workspace_size(int q_heads, int heads, int head_dim, int max_q);
 
 /*
+ * tl_kv4_attention_prefix -- attention of requests that share a prefix, whose
+ * pages are read once for all of them.
+ *
+ *   A query sees the whole prefix, and of its request's own tokens those that
+ *   tl_kv4_attention would show it: the request's own tokens are positions
+ *   0 .. seq_lens[b] - 1 of its table row, the prefix lies before them.
+ *     out = softmax(scale * q . k) v  over both together
+ *   prefix_len    device int32: tokens of the prefix (may end inside a page:
+ *                 own tokens begin with a page of their own; below 1: none)
+ *   prefix_table  int32 [prefix_pages] page ids of the prefix; a page id
+ *                 outside the cache counts as holding no tokens, and so do
+ *                 those behind the table
+ *   The other arguments, what is not written, and what a NaN does are as in
+ *   tl_kv4_attention (without a window).  A batch whose queries are few (64
+ *   rows of one key head, or any number where rows hold two groups) reads the
+ *   prefix once for each 16 rows, from L2.
+ *   workspace     of tl_kv4_attention_prefix_workspace_size bytes or more
+ *   Lengths are read on the GPU only, the prefix's too.  Deterministic.
+ *   Returns as tl_kv4_attention.
+ */
+tlq_status tl_kv4_attention_prefix(const tl_kv4_cache* cache, const uint16_t* q, int64_t ldq, int q_heads,
+                                   uint16_t* out, int64_t ldo, const int32_t* q_start, const int32_t* seq_lens,
+                                   const int32_t* table, int ld_table, const int32_t* prefix_len,
+                                   const int32_t* prefix_table, int prefix_pages, int requests, int tokens, int max_q,
+                                   float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that tl_kv4_attention_prefix takes for up to that many
+ * tokens; 0 for arguments it would not take. */
+size_t tl_kv4_attention_prefix_workspace_size(int q_heads, int heads, int head_dim, int tokens, int max_q);
+
+/*
  * Rotary positions.  Pair i (0 .. rot_dim/2 - 1) of a head's first rot_dim
  * channels, (a, b), turns by the angle of its position:
  *   (a, b) -> (a cos - b sin, b cos + a sin),  (cos, sin) = table[position][i]

@@ -32,7 +32,7 @@ __all__ = [
     "tl_kv4_block_bytes", "tl_kv_plan", "tl_kv4_append", "tl_kv4_read", "tl_kv4_attention",
     "tl_kv4_attention_workspace_size", "tl_lora_add", "KV4Cache", "kv4_attention", "lora_add",
     "tl_rope_table", "tl_qk_norm_rope", "tl_kv4_append_rope", "tl_sample", "Rope", "rope_table", "qk_norm_rope",
-    "sample",
+    "sample", "tl_kv4_attention_prefix", "tl_kv4_attention_prefix_workspace_size", "kv4_attention_prefix",
 ]
 
 # every symbol include/tlq.h declares
@@ -46,7 +46,7 @@ EXPORTED = (
     "tl_loop_block_to_int2", "tl_swiglu_block_to_int2", "tl_probe_read_bandwidth", "tl_loop_block_l2_plan",
     "tl_prefill_plan", "tl_kv4_block_bytes", "tl_kv_plan", "tl_kv4_append", "tl_kv4_read", "tl_kv4_attention",
     "tl_kv4_attention_workspace_size", "tl_lora_add", "tl_rope_table", "tl_qk_norm_rope", "tl_kv4_append_rope",
-    "tl_sample",
+    "tl_sample", "tl_kv4_attention_prefix", "tl_kv4_attention_prefix_workspace_size",
 )
 
 TLQ_OK, TLQ_EINVAL, TLQ_EUNSUPPORTED, TLQ_ECUDA, TLQ_ETIMEOUT = 0, 1, 2, 3, 4
@@ -115,7 +115,7 @@ class _LongWay:
     def plan(*args):
         return -1
 
-    append = read = attention = lora = norm_rope = append_rope = sample = plan
+    append = read = attention = attention_prefix = lora = norm_rope = append_rope = sample = plan
 
 
 _short = _LongWay  # the C API module of the serving calls, once loaded
@@ -187,6 +187,8 @@ def load():
             "tl_kv4_attention": ([KV, P, L, I, P, L, P, P, P, I, I, I, I, F, I, P, Z, P], I),
             "tl_kv4_attention_workspace_size": ([I, I, I, I], Z),
             "tl_lora_add": ([P, L, P, P, P, P, P, I, I, I, I, I, I, I, P, L, P, L, P], I),
+            "tl_kv4_attention_prefix": ([KV, P, L, I, P, L, P, P, P, I, P, P, I, I, I, I, F, P, Z, P], I),
+            "tl_kv4_attention_prefix_workspace_size": ([I, I, I, I, I], Z),
             "tl_rope_table": ([P, L, I, D, P, P], I),
             "tl_qk_norm_rope": ([R, P, P, L, I, P, P, L, P, L, I, P, P, L, I, F, I, P], I),
             "tl_kv4_append_rope": ([KV, R, P, P, L, P, P, L, P, P, L, I, P, P, L, F, I, P], I),
@@ -218,7 +220,7 @@ def _load_binding(lib):
                 *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                   for f in ("tl_kv_plan", "tl_kv4_append", "tl_kv4_read", "tl_kv4_attention", "tl_lora_add")))
     module.bind_step(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
-                       for f in ("tl_qk_norm_rope", "tl_kv4_append_rope", "tl_sample")))
+                       for f in ("tl_qk_norm_rope", "tl_kv4_append_rope", "tl_sample", "tl_kv4_attention_prefix")))
     _short = module
 
 
@@ -721,6 +723,14 @@ class KV4Cache:
         n = tl_kv4_attention_workspace_size(q_heads, self.heads, self.head_dim, max_q)
         return torch.empty(n, dtype=torch.uint8, device=self.blocks.device)
 
+    def prefix_workspace(self, q_heads: int, tokens: int, max_q: int):
+        """A workspace tensor for tl_kv4_attention_prefix of up to that many tokens
+        a step (allocated by torch; keep it for all steps)."""
+        import torch
+
+        n = tl_kv4_attention_prefix_workspace_size(q_heads, self.heads, self.head_dim, tokens, max_q)
+        return torch.empty(n, dtype=torch.uint8, device=self.blocks.device)
+
 
 def tl_kv4_append(cache: KV4Cache, k, v, slots, stream=None) -> None:
     """Quantize k, v [tokens, heads, head_dim] into the cache's slots."""
@@ -784,6 +794,40 @@ def tl_kv4_attention(cache: KV4Cache, q, out, q_start, seq_lens, table, max_q: i
     st = _lib.tl_kv4_attention(cache._ref, qp, ldq, heads, op, ldo, _ints(q_start, _i32, "q_start", n + 1),
                                _ptr(seq_lens, _i32, "seq_lens"), tp, width, n, tokens, max_q, scale, window, ws, nb,
                                _stream(stream))
+    if st:
+        _raise_if(st)
+
+
+def tl_kv4_attention_prefix_workspace_size(q_heads: int, heads: int, head_dim: int, tokens: int, max_q: int) -> int:
+    """Bytes of workspace tl_kv4_attention_prefix takes."""
+    return int(load().tl_kv4_attention_prefix_workspace_size(q_heads, heads, head_dim, tokens, max_q))
+
+
+def tl_kv4_attention_prefix(cache: KV4Cache, q, out, q_start, seq_lens, table, prefix_len, prefix_table, max_q: int,
+                            scale: float, workspace=None, stream=None) -> None:
+    """Attention of requests behind a shared prefix (prefix_len: int32 [1],
+    prefix_table: int32 [pages]); seq_lens and table are of their own tokens.
+    workspace: cache.prefix_workspace(q_heads, tokens, max_q)."""
+    st = _short.attention_prefix(cache._address, cache.head_dim, q, out, q_start, seq_lens, table, prefix_len,
+                                 prefix_table, max_q, scale, workspace, stream)
+    if st == 0:
+        return
+    if st > 0:
+        _raise_if(st)
+    if q.dim() != 3:
+        raise ValueError("q has shape %s, expected [tokens, q_heads, %d]" % (tuple(q.shape), cache.head_dim))
+    heads = q.shape[1]
+    qp, ldq, tokens = _rows3(q, _f16, "q", heads, cache.head_dim)
+    op, ldo, no = _rows3(out, _f16, "out", heads, cache.head_dim)
+    if no != tokens:
+        raise ValueError("out has %d tokens, q %d" % (no, tokens))
+    n = seq_lens.numel()
+    tp, width = _table(table, n)
+    ws, nb = (None, 0) if workspace is None else (_ptr(workspace, _u8, "workspace"), workspace.numel())
+    st = _lib.tl_kv4_attention_prefix(cache._ref, qp, ldq, heads, op, ldo, _ints(q_start, _i32, "q_start", n + 1),
+                                      _ptr(seq_lens, _i32, "seq_lens"), tp, width, _ints(prefix_len, _i32, "prefix_len", 1),
+                                      _ptr(prefix_table, _i32, "prefix_table"), prefix_table.numel(), n, tokens, max_q,
+                                      scale, ws, nb, _stream(stream))
     if st:
         _raise_if(st)
 
@@ -1029,6 +1073,19 @@ def kv4_attention(cache: KV4Cache, q, q_start, seq_lens, table, max_q: int, scal
         tl_kv4_attention(cache, q, out, q_start, seq_lens, table, max_q,
                          cache.head_dim ** -0.5 if scale is None else scale, window,
                          cache.attention_workspace(q.shape[1], max_q), stream)
+    return _result(stream, out)
+
+
+def kv4_attention_prefix(cache: KV4Cache, q, q_start, seq_lens, table, prefix_len, prefix_table, max_q: int, scale=None,
+                         stream=None):
+    """Attention output [tokens, q_heads, head_dim] behind a shared prefix."""
+    import torch
+
+    with _on(stream):
+        out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+        tl_kv4_attention_prefix(cache, q, out, q_start, seq_lens, table, prefix_len, prefix_table, max_q,
+                                cache.head_dim ** -0.5 if scale is None else scale,
+                                cache.prefix_workspace(q.shape[1], q.shape[0], max_q), stream)
     return _result(stream, out)
 
 

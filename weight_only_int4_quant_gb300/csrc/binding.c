@@ -42,6 +42,10 @@ static tlq_status (*f_append_rope)(const tl_kv4_cache*, const tl_rope*, const in
 static tlq_status (*f_sample)(const void*, int, int64_t, int, int, const float*, const float*, const int32_t*, const float*,
                               const float*, int32_t*, float*, void*);
 
+static tlq_status (*f_attention_prefix)(const tl_kv4_cache*, const uint16_t*, int64_t, int, uint16_t*, int64_t,
+                                        const int32_t*, const int32_t*, const int32_t*, int, const int32_t*,
+                                        const int32_t*, int, int, int, int, float, void*, size_t, void*);
+
 /* 1 if attribute `name` of o is `want` (an object compared by identity). */
 static int attr_is(PyObject* o, PyObject* name, PyObject* want) {
   PyObject* v = PyObject_GetAttr(o, name);
@@ -308,6 +312,27 @@ static int append_rope(PyObject* const* a, Py_ssize_t n) {
        q.ldo, eps, (int)tokens, s);
 }
 
+static int attention_prefix(PyObject* const* a, Py_ssize_t n) {
+  /* cache address, head_dim, q, out, q_start, seq_lens, table, prefix_len, prefix_table, max_q, scale, workspace,
+   * stream */
+  const tl_kv4_cache* c;
+  void *q, *out, *q_start, *lens, *table, *prefix_len, *prefix_table, *ws, *s;
+  int64_t ldq, ldo;
+  long long dim, tokens, no, requests, max_q, pages, bytes, qs[3], size[2];
+  if (n != 13 || !cache_of(a[0], &c) || !as_int(a[1], &dim) || !extents(a[2], 0, 3, qs) ||
+      !rows(a[2], 3, qs[1], dim, &q, &ldq, &tokens) || !rows(a[3], 3, qs[1], dim, &out, &ldo, &no) || no != tokens ||
+      !flat(a[5], t_i32, -1, &lens, &requests) || !flat(a[4], t_i32, requests + 1, &q_start, NULL) ||
+      !flat(a[6], t_i32, -1, &table, NULL) || !extents(a[6], 0, 2, size) || size[0] != requests ||
+      !flat(a[7], t_i32, 1, &prefix_len, NULL) || !flat(a[8], t_i32, -1, &prefix_table, &pages) ||
+      !as_int(a[9], &max_q) || !PyFloat_CheckExact(a[10]) || !flat(a[11], t_u8, -1, &ws, &bytes) ||
+      !stream_of(a[12], &s) || tokens > 0x7fffffffll || requests > 0x7fffffffll || size[1] > 0x7fffffffll ||
+      pages > 0x7fffffffll || qs[1] > 0x7fffffffll)
+    return FALLBACK;
+  const float scale = (float)PyFloat_AS_DOUBLE(a[10]);
+  CALL(f_attention_prefix, c, q, ldq, (int)qs[1], out, ldo, q_start, lens, table, (int)size[1], prefix_len, prefix_table,
+       (int)pages, (int)requests, (int)tokens, (int)max_q, scale, ws, (size_t)bytes, s);
+}
+
 static int sample(PyObject* const* a, Py_ssize_t n) {
   /* logits, uniform, tokens, temperature, top_k, top_p, min_p, logprobs, stream */
   void *x, *uniform, *tokens, *temperature, *top_k, *top_p, *min_p, *logprobs, *s;
@@ -339,6 +364,7 @@ METHOD(lora)
 METHOD(norm_rope)
 METHOD(append_rope)
 METHOD(sample)
+METHOD(attention_prefix)
 
 /* bind(float16, float32, int32, int64, uint8, get_device, get_stream, and the
  * addresses of the five entry points in the order above) */
@@ -371,13 +397,13 @@ static PyObject* bind(PyObject* self, PyObject* args) {
   Py_RETURN_NONE;
 }
 
-/* bind_step(addresses of tl_qk_norm_rope, tl_kv4_append_rope, tl_sample) */
+/* bind_step(addresses of tl_qk_norm_rope, tl_kv4_append_rope, tl_sample, tl_kv4_attention_prefix) */
 static PyObject* bind_step(PyObject* self, PyObject* args) {
-  PyObject* f[3];
-  void* p[3];
+  PyObject* f[4];
+  void* p[4];
   (void)self;
-  if (!PyArg_ParseTuple(args, "OOO", &f[0], &f[1], &f[2])) return NULL;
-  for (int i = 0; i < 3; ++i) {
+  if (!PyArg_ParseTuple(args, "OOOO", &f[0], &f[1], &f[2], &f[3])) return NULL;
+  for (int i = 0; i < 4; ++i) {
     p[i] = PyLong_AsVoidPtr(f[i]);
     if (!p[i] || PyErr_Occurred()) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null entry point");
@@ -387,6 +413,7 @@ static PyObject* bind_step(PyObject* self, PyObject* args) {
   *(void**)&f_norm_rope = p[0];
   *(void**)&f_append_rope = p[1];
   *(void**)&f_sample = p[2];
+  *(void**)&f_attention_prefix = p[3];
   Py_RETURN_NONE;
 }
 
@@ -401,6 +428,7 @@ static PyMethodDef methods[] = {
     {"norm_rope", (PyCFunction)(void (*)(void))py_norm_rope, METH_FASTCALL, "tl_qk_norm_rope"},
     {"append_rope", (PyCFunction)(void (*)(void))py_append_rope, METH_FASTCALL, "tl_kv4_append_rope"},
     {"sample", (PyCFunction)(void (*)(void))py_sample, METH_FASTCALL, "tl_sample"},
+    {"attention_prefix", (PyCFunction)(void (*)(void))py_attention_prefix, METH_FASTCALL, "tl_kv4_attention_prefix"},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tlq_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -56,8 +56,14 @@
 
 #include "serve.cuh"
 
+#ifndef TLQ_KV_SHARED_UNIT
+#define TLQ_KV_SHARED_UNIT 0  // 1: the forms for a batch with a shared prefix, built by themselves
+#endif
+
 namespace tlq {
 namespace {
+
+constexpr bool kShared = TLQ_KV_SHARED_UNIT;
 
 constexpr int kStage = 128;  // tokens of a stage
 constexpr int kTile = 16;    // tokens of a matrix instruction
@@ -141,6 +147,8 @@ struct DecodeParams {
   int few_rows;       // requests of more rows are not this kernel's
   FastDiv by_share;
   KvJoin join;
+  KvShared shared;
+  int q_heads;
 };
 
 // Units of one request, the same for each of its items (key head, row block).
@@ -182,8 +190,8 @@ struct Walk {
   int req;
 
   __device__ __forceinline__ bool next(const DecodeParams& p, Segment* s) {
-    while (u < u_end && req < p.batch.requests) {
-      const KvRequest rq = kv_request(p.batch, p.cache.page, req);
+    while (u < u_end && req < kv_requests<kShared>(p.batch)) {
+      const KvRequest rq = kv_request_or_prefix<kShared>(p.batch, p.cache.page, req);
       const ItemShape shape = item_shape<R>(p, rq);
       const long long units = (long long)shape.items * shape.units;
       if (u >= req_u + units) {  // on to the next request (one without queries is passed over)
@@ -247,18 +255,18 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
   if (tid == 0) header->followers = 0;
 
   auto count = [&](int i) -> long long {
-    const ItemShape s = item_shape<R>(p, kv_request(p.batch, p.cache.page, i));
+    const ItemShape s = item_shape<R>(p, kv_request_or_prefix<kShared>(p.batch, p.cache.page, i));
     return (long long)s.items * s.units;
   };
   long long own, mine;
-  search.count_all(p.batch.requests, count, &own, &mine);  // its barriers publish the mbarriers too
+  search.count_all(kv_requests<kShared>(p.batch), count, &own, &mine);  // its barriers publish the mbarriers too
   const long long U = search.total;
   const long long n = min((long long)gridDim.x, U);
   if ((long long)blockIdx.x >= n) return;
   Walk<R> walk;
   walk.u = U * blockIdx.x / n;
   walk.u_end = U * (blockIdx.x + 1) / n;
-  search.find(p.batch.requests, count, walk.u, own, mine);
+  search.find(kv_requests<kShared>(p.batch), count, walk.u, own, mine);
   walk.req = search.request;
   walk.req_u = search.first;
   if (walk.req < 0) return;  // not reached: u < U
@@ -274,7 +282,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
     const int chunks = kStage >> chunk_shift;
     bool ok = true;
     while (ok && walk.next(p, &sg)) {
-      const int* row = p.batch.table + (size_t)sg.req * p.batch.ld_table;
+      const int* row = kv_table_row<kShared>(p.batch, sg.req);
       const int pages = (sg.hi + p.cache.page - 1) >> p.cache.page_shift;  // pages that hold a visible key
       auto page_of = [&](int s) {  // lane i: the page of chunk i of stage s
         const int at = (int)(((long long)s * kStage + lane * chunk) >> p.cache.page_shift);
@@ -747,7 +755,15 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
           acc[2] = fmaf(wm, v.z + bt, acc[2]);
           acc[3] = fmaf(wm, v.w + bt, acc[3]);
         }
-        if (whole) {
+        if (kShared && whole) {
+          if (row < rows) {
+            const KvRowSums& to = sg.req < p.batch.requests ? p.shared.own : p.shared.prefix;
+            const int gr = row0 + row, t = divide(gr, p.by_share), g = gr - t * p.share;
+            const size_t at = (size_t)(rq.q0 + t) * p.q_heads + head * p.share + g;
+            *reinterpret_cast<float4*>(to.o + at * D + ch) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (ch == 0) to.ml[at] = make_float2(mm, ll);
+          }
+        } else if (whole) {
           if (row < rows) {
             const float inv = ll == 0.f ? 0.f : 1.0f / ll;  // no key seen: zeros
             const int gr = row0 + row, t = divide(gr, p.by_share), g = gr - t * p.share;
@@ -772,7 +788,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
       long long b = ((last_u + 1) * n - 1) / U;
       while (U * b / n > last_u) --b;
       while (U * (b + 1) / n <= last_u) ++b;
-      *header = KvJoinHeader{(int)(b - blockIdx.x), rq.q0, row0, rows, head};
+      *header = KvJoinHeader{(int)(b - blockIdx.x), rq.q0, row0, rows, head, sg.req >= p.batch.requests};
     }
   }
 }
@@ -806,14 +822,21 @@ tlq_status launch_rows(const DecodeParams& p, int rows, void* ws, KvJoin* join, 
 
 }  // namespace
 
+#if !TLQ_KV_SHARED_UNIT
 // The most that any form of the kernel takes at this head size, so that one
 // workspace serves steps of every shape.
 size_t kv4_decode_workspace(int head_dim) {
   const int sms = device_info().sms;
   return std::max(kv_join_bytes(3 * sms, 8, head_dim), kv_join_bytes(2 * sms, 16, head_dim));
 }
+#endif
 
-tlq_status launch_kv4_decode(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream) {
+#if TLQ_KV_SHARED_UNIT
+tlq_status launch_kv4_decode_shared(
+#else
+tlq_status launch_kv4_decode(
+#endif
+    const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream) {
   DecodeParams p{};
   p.cache = a.cache;
   p.batch = a.batch;
@@ -826,7 +849,12 @@ tlq_status launch_kv4_decode(const KvAttention& a, int few_rows, void* ws, KvJoi
   p.share = a.q_heads / a.cache.heads;
   p.few_rows = few_rows;
   p.by_share = fast_div((uint32_t)p.share);
-  const int rows = (int)std::min<long long>((long long)a.batch.max_q * p.share, few_rows);
+  p.shared = a.shared;
+  p.q_heads = a.q_heads;
+  long long most = (long long)a.batch.max_q * p.share;
+  if (kShared && (long long)a.batch.tokens * p.share <= few_rows)
+    most = std::max<long long>(most, (long long)a.batch.tokens * p.share);
+  const int rows = (int)std::min<long long>(most, few_rows);
   if (a.head_dim == 64) return launch_rows<64, 1>(p, rows, ws, join, stream);
   return a.cache.group == 64 ? launch_rows<128, 2>(p, rows, ws, join, stream)
                              : launch_rows<128, 1>(p, rows, ws, join, stream);

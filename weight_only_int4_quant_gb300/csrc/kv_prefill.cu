@@ -51,8 +51,14 @@
 #include "serve.cuh"
 #include "tc_common.cuh"
 
+#ifndef TLQ_KV_SHARED_UNIT
+#define TLQ_KV_SHARED_UNIT 0  // 1: the forms for a batch with a shared prefix, built by themselves
+#endif
+
 namespace tlq {
 namespace {
+
+constexpr bool kShared = TLQ_KV_SHARED_UNIT;
 
 constexpr int kStage = 128;       // tokens of a stage
 constexpr int kRows = 128;        // rows of a tile
@@ -88,6 +94,8 @@ struct PrefillAttnParams {
   int window, share, few_rows;
   FastDiv by_share;
   KvJoin join;
+  KvShared shared;
+  int q_heads;
 };
 
 // Bounds of one row tile of a request.
@@ -130,7 +138,7 @@ struct PWalk {
   KvRequest rq;
 
   __device__ __forceinline__ void enter(const PrefillAttnParams& p) {
-    rq = kv_request(p.batch, p.cache.page, req);
+    rq = kv_request_or_prefix<kShared>(p.batch, p.cache.page, req);
     rows = many_rows(p, rq);
     tiles = (rows + kItemRows - 1) / kItemRows;
     qt = head = 0;
@@ -164,7 +172,7 @@ struct PWalk {
   __device__ __forceinline__ bool next(const PrefillAttnParams& p, PSegment* s) {
     while (u < u_end) {
       if (qt >= tiles) {
-        if (++req >= p.batch.requests) return false;
+        if (++req >= kv_requests<kShared>(p.batch)) return false;
         enter(p);
         continue;
       }
@@ -375,10 +383,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
     for (int qt = first; qt * kItemRows < rows; qt += step) n += tile_shape(p, r, rows, qt).n + kItemCost;
     return n * p.cache.heads;
   };
-  const bool small = p.batch.requests <= kThreads;
+  const int requests = kv_requests<kShared>(p.batch);
+  const bool small = requests <= kThreads;
   if (small) {
-    for (int i = warp; i < p.batch.requests; i += kThreads / 32) {
-      long long v = lane_units(kv_request(p.batch, p.cache.page, i), lane, 32);
+    for (int i = warp; i < requests; i += kThreads / 32) {
+      long long v = lane_units(kv_request_or_prefix<kShared>(p.batch, p.cache.page, i), lane, 32);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if (lane == 0) request_units[i] = v;
@@ -386,14 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
     __syncthreads();
   }
   auto count = [&](int i) -> long long {
-    return small ? request_units[i] : lane_units(kv_request(p.batch, p.cache.page, i), 0, 1);
+    return small ? request_units[i] : lane_units(kv_request_or_prefix<kShared>(p.batch, p.cache.page, i), 0, 1);
   };
   long long own, mine;
-  search.count_all(p.batch.requests, count, &own, &mine);
+  search.count_all(requests, count, &own, &mine);
   const long long U = search.total;
   const long long n = min((long long)gridDim.x, U);
   const bool busy = (long long)blockIdx.x < n;
-  if (busy) search.find(p.batch.requests, count, U * blockIdx.x / n, own, mine);
+  if (busy) search.find(requests, count, U * blockIdx.x / n, own, mine);
   {
     PWalk w;
     w.u = w.u_end = 0;
@@ -446,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
         const Place& at = t < kStage ? kp : vp;
         const int key = at.stage * kStage + (t & (kStage - 1));
         page[j] = at.have && t < 2 * kStage && key >= at.lo && key < at.hi
-                      ? __ldg(p.batch.table + (size_t)at.req * p.batch.ld_table + (key >> p.cache.page_shift))
+                      ? __ldg(kv_table_row<kShared>(p.batch, at.req) + (key >> p.cache.page_shift))
                       : -1;
       }
     };
@@ -862,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       const bool whole = sg.first && sg.last;
       const int row0 = 32 * quarter + r;  // this thread's rows: row0 + 8 y
       const float up = 16777216.0f;       // codes were entered as c 2^-24
-      if (whole) {
+      if (!kShared && whole) {
         float inv[4];
         __half* orow[4];
 #pragma unroll
@@ -920,8 +929,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           }
         }
       } else {
-        // a partial, its columns in TMEM's order
-        float* const part = p.join.parts + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * (kItemRows * (D + 2));
+        // a partial (or a whole row's sums), its columns in TMEM's order
+        float *po[4], *pm[4];
+        int lstep = kItemRows;  // from m to l
+        if (kShared && whole) {
+          const KvRowSums& to = sg.req < p.batch.requests ? p.shared.own : p.shared.prefix;
+          lstep = 1;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int gr = sg.row0 + kRows * tile + min(row0 + 8 * y, rows - 1);
+            const int t = divide(gr, p.by_share), g = gr - t * p.share;
+            const size_t at = (size_t)(rq.q0 + t) * p.q_heads + sg.head * p.share + g;
+            po[y] = to.o + at * D + 2 * qd;
+            pm[y] = reinterpret_cast<float*>(to.ml + at);
+          }
+        } else {
+          float* const part = p.join.parts + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * (kItemRows * (D + 2));
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            po[y] = part + (size_t)(kRows * tile + row0 + 8 * y) * D + 2 * qd;
+            pm[y] = part + kItemRows * D + kRows * tile + row0 + 8 * y;
+          }
+        }
 #pragma unroll 1
         for (int b = 0; b < D / 32; ++b) {
 #pragma unroll
@@ -937,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
             for (int e = 0; e < 2; ++e) {
               const int y = 2 * h + e;
               if (row0 + 8 * y < rows) {
-                float* dst = part + (size_t)(kRows * tile + row0 + 8 * y) * D + 32 * b + 2 * qd;
+                float* dst = po[y] + 32 * b;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                   *reinterpret_cast<float2*>(dst + 8 * k) =
@@ -949,8 +978,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
 #pragma unroll
         for (int y = 0; y < 4; ++y)
           if (qd == 0 && row0 + 8 * y < rows) {
-            part[kItemRows * D + kRows * tile + row0 + 8 * y] = m[y];
-            part[kItemRows * D + kItemRows + kRows * tile + row0 + 8 * y] = l[y];
+            pm[y][0] = m[y];
+            pm[y][lstep] = l[y];
           }
       }
       tc_fence_before();
@@ -959,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
         long long b = ((last_u + 1) * n - 1) / U;
         while (U * b / n > last_u) --b;
         while (U * (b + 1) / n <= last_u) ++b;
-        *header = KvJoinHeader{(int)(b - blockIdx.x), rq.q0, sg.row0, sg.rows, sg.head};
+        *header = KvJoinHeader{(int)(b - blockIdx.x), rq.q0, sg.row0, sg.rows, sg.head, sg.req >= p.batch.requests};
       }
     }
   }
@@ -990,9 +1019,16 @@ tlq_status launch_one(const PrefillAttnParams& p, cudaStream_t stream) {
 
 }  // namespace
 
+#if !TLQ_KV_SHARED_UNIT
 size_t kv4_prefill_workspace(int head_dim) { return kv_join_bytes(device_info().sms, kItemRows, head_dim); }
+#endif
 
-tlq_status launch_kv4_prefill(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream) {
+#if TLQ_KV_SHARED_UNIT
+tlq_status launch_kv4_prefill_shared(
+#else
+tlq_status launch_kv4_prefill(
+#endif
+    const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream) {
   PrefillAttnParams p{};
   p.cache = a.cache;
   p.batch = a.batch;
@@ -1005,6 +1041,8 @@ tlq_status launch_kv4_prefill(const KvAttention& a, int few_rows, void* ws, KvJo
   p.share = a.q_heads / a.cache.heads;
   p.by_share = fast_div((uint32_t)p.share);
   p.few_rows = few_rows;
+  p.shared = a.shared;
+  p.q_heads = a.q_heads;
   p.join = *join = kv_join_at(ws, device_info().sms, kItemRows);
   return a.head_dim == 64 ? launch_one<64>(p, stream) : launch_one<128>(p, stream);
 }

@@ -1,0 +1,4 @@
+// The kernel of kv_prefill.cu for a batch that shares a prefix: the same source,
+// compiled as a translation unit of its own so that the two build in parallel.
+#define TLQ_KV_SHARED_UNIT 1
+#include "kv_prefill.cu"

@@ -76,6 +76,10 @@ struct KvBatch {
   const int* table;
   int ld_table;
   int requests, tokens, max_q;
+  // tokens that all requests share, before their own (NULL: none)
+  const int* prefix_len;
+  const int* prefix_table;
+  int prefix_pages;
 };
 
 // The longest context (positions and windows stay far from 32-bit limits).
@@ -100,6 +104,27 @@ __device__ __forceinline__ KvRequest kv_request(const KvBatch& b, int page, int 
   r.base = max(tokens - queries, -(int)kMaxContext);
   r.len = (int)min((long long)tokens, (long long)b.ld_table * page);
   return r;
+}
+
+// The same with the prefix that a batch shares as one request more, behind the
+// others: its queries are all of the batch's and see all of it.
+template <bool SHARED>
+__device__ __forceinline__ int kv_requests(const KvBatch& b) {
+  return b.requests + (SHARED ? 1 : 0);
+}
+template <bool SHARED>
+__device__ __forceinline__ KvRequest kv_request_or_prefix(const KvBatch& b, int page, int i) {
+  if (!SHARED || i < b.requests) return kv_request(b, page, i);
+  KvRequest r;
+  r.q0 = 0;
+  r.q_len = b.tokens;
+  r.base = min(max(__ldg(b.prefix_len), 0), (int)kMaxContext);
+  r.len = (int)min((long long)r.base, (long long)b.prefix_pages * page);
+  return r;
+}
+template <bool SHARED>
+__device__ __forceinline__ const int* kv_table_row(const KvBatch& b, int i) {
+  return !SHARED || i < b.requests ? b.table + (size_t)i * b.ld_table : b.prefix_table;
 }
 
 // Where unit `u` of the batch's work lies: requests have count(i) units each,
@@ -277,6 +302,17 @@ struct SampleArgs {
 };
 tlq_status launch_sample(const SampleArgs& a, cudaStream_t stream);
 
+// Where the softmax's sums of each row go that is joined with others of the
+// same row afterwards: [tokens][q_heads] rows of O [D], and of m and l.
+struct KvRowSums {
+  float* o;
+  float2* ml;
+};
+struct KvShared {
+  KvRowSums own, prefix;
+};
+inline size_t kv_row_sums_bytes(long long rows, int head_dim) { return (size_t)rows * (head_dim + 2) * sizeof(float); }
+
 struct KvAttention {
   KvCache cache;
   KvBatch batch;
@@ -287,6 +323,7 @@ struct KvAttention {
   long long ldo;
   float scale;
   int window;
+  KvShared shared;  // of a batch with a prefix
 };
 // What the joining kernel needs of an item that a block began but did not end.
 struct KvJoinHeader {
@@ -295,6 +332,7 @@ struct KvJoinHeader {
   int row0;       // first (query, head) row of the item
   int rows;
   int head;       // key head
+  int prefix;     // the item is of the shared prefix
 };
 // The parts that one kernel leaves: two to a block, of the item it ends (0) and
 // of the one it begins (1).
@@ -324,6 +362,12 @@ size_t kv4_prefill_workspace(int head_dim);
 tlq_status launch_kv4_decode(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream);
 tlq_status launch_kv4_prefill(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream);
 tlq_status launch_kv4_join(const KvAttention& a, const KvJoin& few, const KvJoin& many, cudaStream_t stream);
+// The same three for a batch with a prefix: sums of rows go to a.shared, and
+// _merge puts the prefix's and a request's own together.
+tlq_status launch_kv4_decode_shared(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream);
+tlq_status launch_kv4_prefill_shared(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream);
+tlq_status launch_kv4_join_shared(const KvAttention& a, const KvJoin& few, const KvJoin& many, cudaStream_t stream);
+tlq_status launch_kv4_merge(const KvAttention& a, int few_rows, cudaStream_t stream);
 
 struct LoraArgs {
   const __half* x;

@@ -66,6 +66,103 @@ constexpr int kFewRows = 64;
 
 size_t cache_bytes(const KvCache& c) { return (size_t)c.num_pages * c.heads * c.block_bytes; }
 
+// The checks that both attention calls share; *a is filled in where there is
+// something to do (requests, tokens and max_q above 0).
+struct AttentionCall {
+  const char* who;
+  const tl_kv4_cache* cache;
+  const uint16_t* q;
+  int64_t ldq;
+  int q_heads;
+  uint16_t* out;
+  int64_t ldo;
+  const int32_t *q_start, *seq_lens, *table;
+  int ld_table, requests, tokens, max_q;
+  float scale;
+  int window;
+  bool shared;  // of a batch with a prefix:
+  const int32_t *prefix_len, *prefix_table;
+  int prefix_pages;
+  void* workspace;
+  size_t workspace_bytes;
+};
+
+// bytes of workspace: the kernels' parts, and behind them the sums of all rows of a batch with a prefix
+size_t attention_workspace(int head_dim) { return kv4_decode_workspace(head_dim) + kv4_prefill_workspace(head_dim); }
+size_t prefix_workspace(int q_heads, int head_dim, long long tokens) {
+  const size_t sums = (kv_row_sums_bytes(tokens * q_heads, head_dim) + 255) & ~size_t(255);
+  return ((attention_workspace(head_dim) + 255) & ~size_t(255)) + 2 * sums;
+}
+
+tlq_status check_attention(const AttentionCall& c, KvAttention* a, bool* empty) {
+  const char* who = c.who;
+  *empty = true;
+  const tlq_status st = check_cache(c.cache, &a->cache, who);
+  if (st != TLQ_OK) return st;
+  if (c.q_heads < 1 || c.q_heads % a->cache.heads)
+    return set_error(TLQ_EINVAL, "%s: q_heads=%d is not a positive multiple of the cache's heads=%d", who, c.q_heads,
+                     a->cache.heads);
+  if (c.requests < 0 || c.tokens < 0 || c.max_q < 0)
+    return set_error(TLQ_EINVAL, "%s: requests=%d tokens=%d max_q=%d", who, c.requests, c.tokens, c.max_q);
+  if (c.window < 0) return set_error(TLQ_EINVAL, "%s: window=%d (0: none)", who, c.window);
+  if (c.shared && c.prefix_pages < 0) return set_error(TLQ_EINVAL, "%s: prefix_pages=%d", who, c.prefix_pages);
+  if (!std::isfinite(c.scale)) return set_error(TLQ_EINVAL, "%s: scale is not finite", who);
+  if (c.requests == 0 || c.tokens == 0 || c.max_q == 0) return TLQ_OK;
+  if (!c.q || !c.out || !c.q_start || !c.seq_lens || !c.table ||
+      (c.shared && (!c.prefix_len || (c.prefix_pages > 0 && !c.prefix_table))))
+    return set_error(TLQ_EINVAL, "%s: null pointer", who);
+  if (c.ld_table < 1) return set_error(TLQ_EINVAL, "%s: ld_table=%d (must be >= 1)", who, c.ld_table);
+  const int head_dim = c.cache->head_dim;
+  const long long row = (long long)c.q_heads * head_dim;
+  if (c.tokens > 1 && (c.ldq < row || c.ldo < row || c.ldq % 8 || c.ldo % 8))
+    return set_error(TLQ_EINVAL, "%s: ldq=%lld ldo=%lld (at least q_heads*head_dim = %lld, multiples of 8)", who,
+                     (long long)c.ldq, (long long)c.ldo, row);
+  if (!aligned(c.q, 16) || !aligned(c.out, 16) || !aligned(c.workspace, 16) || !aligned(c.q_start, 4) ||
+      !aligned(c.seq_lens, 4) || !aligned(c.table, 4) || !aligned(c.prefix_len, 4) || !aligned(c.prefix_table, 4))
+    return set_error(TLQ_EINVAL, "%s: q, out and the workspace must be 16-byte aligned", who);
+  const int max_q = std::min(c.max_q, c.tokens), share = c.q_heads / a->cache.heads;
+  if ((long long)max_q * share > 0x3fffffff)
+    return set_error(TLQ_EUNSUPPORTED, "%s: max_q=%d x %d query heads to a key head (at most 2^30 rows)", who, max_q,
+                     share);
+  if (c.shared && ((long long)c.tokens * share > 0x3fffffff || c.requests == 0x7fffffff))
+    return set_error(TLQ_EUNSUPPORTED, "%s: tokens=%d x %d query heads to a key head, requests=%d (at most 2^30 rows)",
+                     who, c.tokens, share, c.requests);
+  const size_t need = c.shared ? prefix_workspace(c.q_heads, head_dim, c.tokens) : attention_workspace(head_dim);
+  if (!c.workspace || c.workspace_bytes < need)
+    return set_error(TLQ_EINVAL, "%s: workspace of %zu bytes (%zu needed)", who,
+                     c.workspace ? c.workspace_bytes : size_t(0), need);
+  const size_t qb = span(c.tokens, c.ldq, row, 2), ob = span(c.tokens, c.ldo, row, 2), cb = cache_bytes(a->cache);
+  if (overlap(c.out, ob, c.q, qb) || overlap(c.out, ob, a->cache.blocks, cb) || overlap(c.workspace, need, c.q, qb) ||
+      overlap(c.workspace, need, c.out, ob) || overlap(c.workspace, need, a->cache.blocks, cb))
+    return set_error(TLQ_EINVAL, "%s: out or the workspace overlaps another buffer", who);
+  const struct {
+    const void* p;
+    size_t n;
+  } lengths[5] = {{c.q_start, 4 * ((size_t)c.requests + 1)}, {c.seq_lens, 4 * (size_t)c.requests},
+                  {c.table, 4 * (size_t)c.requests * c.ld_table}, {c.prefix_len, c.shared ? size_t(4) : 0},
+                  {c.prefix_table, c.shared ? 4 * (size_t)c.prefix_pages : 0}};
+  for (const auto& l : lengths)
+    if (overlap(c.out, ob, l.p, l.n) || overlap(c.workspace, need, l.p, l.n))
+      return set_error(TLQ_EINVAL, "%s: out or the workspace overlaps the batch's arrays", who);
+  a->batch = KvBatch{c.q_start, c.seq_lens, c.table, c.ld_table, c.requests, c.tokens, max_q,
+                     c.prefix_len, c.prefix_table, c.prefix_pages};
+  a->head_dim = head_dim;
+  a->q_heads = c.q_heads;
+  a->q = reinterpret_cast<const __half*>(c.q);
+  a->ldq = c.ldq;
+  a->out = reinterpret_cast<__half*>(c.out);
+  a->ldo = c.ldo;
+  a->scale = c.scale;
+  a->window = c.window >= kMaxContext ? 0 : c.window;  // a window that no context outgrows is none
+  *empty = false;
+  return TLQ_OK;
+}
+
+// The tensor-core kernel takes one scale a row, so rows in two groups stay
+// with the other one whatever their number (a prompt of 2048 tokens, 16 heads:
+// 246 us, where rows in one group take 68).
+int few_rows_of(const tl_kv4_cache& c) { return c.head_dim == c.group ? kFewRows : 0x7fffffff; }
+
 // Rows that may lie in others' gaps (columns of a fused projection's rows).
 struct RowSet {
   const void* p;
@@ -273,7 +370,7 @@ tlq_status tl_kv4_read(const tl_kv4_cache* cache, const int64_t* slots, int toke
 size_t tl_kv4_attention_workspace_size(int q_heads, int heads, int head_dim, int max_q) {
   clear_error();
   if (q_heads < 1 || heads < 1 || q_heads % heads || (head_dim != 64 && head_dim != 128) || max_q < 0) return 0;
-  return kv4_decode_workspace(head_dim) + kv4_prefill_workspace(head_dim);
+  return attention_workspace(head_dim);
 }
 
 tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_t ldq, int q_heads, uint16_t* out,
@@ -281,67 +378,61 @@ tlq_status tl_kv4_attention(const tl_kv4_cache* cache, const uint16_t* q, int64_
                             int ld_table, int requests, int tokens, int max_q, float scale, int window,
                             void* workspace, size_t workspace_bytes, void* stream) {
   clear_error();
-  const char* who = "tl_kv4_attention";
   KvAttention a{};
-  const tlq_status st = check_cache(cache, &a.cache, who);
-  if (st != TLQ_OK) return st;
-  if (q_heads < 1 || q_heads % a.cache.heads)
-    return set_error(TLQ_EINVAL, "%s: q_heads=%d is not a positive multiple of the cache's heads=%d", who, q_heads,
-                     a.cache.heads);
-  if (requests < 0 || tokens < 0 || max_q < 0)
-    return set_error(TLQ_EINVAL, "%s: requests=%d tokens=%d max_q=%d", who, requests, tokens, max_q);
-  if (window < 0) return set_error(TLQ_EINVAL, "%s: window=%d (0: none)", who, window);
-  if (!std::isfinite(scale)) return set_error(TLQ_EINVAL, "%s: scale is not finite", who);
-  if (requests == 0 || tokens == 0 || max_q == 0) return TLQ_OK;
-  if (!q || !out || !q_start || !seq_lens || !table) return set_error(TLQ_EINVAL, "%s: null pointer", who);
-  if (ld_table < 1) return set_error(TLQ_EINVAL, "%s: ld_table=%d (must be >= 1)", who, ld_table);
-  const long long row = (long long)q_heads * cache->head_dim;
-  if (tokens > 1 && (ldq < row || ldo < row || ldq % 8 || ldo % 8))
-    return set_error(TLQ_EINVAL, "%s: ldq=%lld ldo=%lld (at least q_heads*head_dim = %lld, multiples of 8)", who,
-                     (long long)ldq, (long long)ldo, row);
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(q_start, 4) ||
-      !aligned(seq_lens, 4) || !aligned(table, 4))
-    return set_error(TLQ_EINVAL, "%s: q, out and the workspace must be 16-byte aligned", who);
-  max_q = std::min(max_q, tokens);
-  if ((long long)max_q * (q_heads / a.cache.heads) > 0x3fffffff)
-    return set_error(TLQ_EUNSUPPORTED, "%s: max_q=%d x %d query heads to a key head (at most 2^30 rows)", who, max_q,
-                     q_heads / a.cache.heads);
-  const size_t need = tl_kv4_attention_workspace_size(q_heads, a.cache.heads, cache->head_dim, max_q);
-  if (!workspace || workspace_bytes < need)
-    return set_error(TLQ_EINVAL, "%s: workspace of %zu bytes (%zu needed)", who, workspace ? workspace_bytes : size_t(0),
-                     need);
-  const size_t qb = span(tokens, ldq, row, 2), ob = span(tokens, ldo, row, 2), cb = cache_bytes(a.cache);
-  if (overlap(out, ob, q, qb) || overlap(out, ob, a.cache.blocks, cb) || overlap(workspace, need, q, qb) ||
-      overlap(workspace, need, out, ob) || overlap(workspace, need, a.cache.blocks, cb))
-    return set_error(TLQ_EINVAL, "%s: out or the workspace overlaps another buffer", who);
-  const struct {
-    const void* p;
-    size_t n;
-  } lengths[3] = {{q_start, 4 * ((size_t)requests + 1)}, {seq_lens, 4 * (size_t)requests},
-                  {table, 4 * (size_t)requests * ld_table}};
-  for (const auto& l : lengths)
-    if (overlap(out, ob, l.p, l.n) || overlap(workspace, need, l.p, l.n))
-      return set_error(TLQ_EINVAL, "%s: out or the workspace overlaps the batch's arrays", who);
-  a.batch = KvBatch{q_start, seq_lens, table, ld_table, requests, tokens, max_q};
-  a.head_dim = cache->head_dim;
-  a.q_heads = q_heads;
-  a.q = reinterpret_cast<const __half*>(q);
-  a.ldq = ldq;
-  a.out = reinterpret_cast<__half*>(out);
-  a.ldo = ldo;
-  a.scale = scale;
-  a.window = window >= kMaxContext ? 0 : window;  // a window that no context outgrows is none
-  // The tensor-core kernel takes one scale a row, so rows in two groups stay
-  // with the other one whatever their number (a prompt of 2048 tokens, 16 heads:
-  // 246 us, where rows in one group take 68).
-  const int few = cache->head_dim == cache->group ? kFewRows : 0x7fffffff;
+  bool empty;
+  const tlq_status st = check_attention(
+      AttentionCall{"tl_kv4_attention", cache, q, ldq, q_heads, out, ldo, q_start, seq_lens, table, ld_table, requests,
+                    tokens, max_q, scale, window, false, nullptr, nullptr, 0, workspace, workspace_bytes},
+      &a, &empty);
+  if (st != TLQ_OK || empty) return st;
+  const int few = few_rows_of(*cache);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   KvJoin few_parts{}, many_parts{};
   tlq_status ls = launch_kv4_decode(a, few, workspace, &few_parts, s);
-  if (ls == TLQ_OK && (long long)max_q * (q_heads / a.cache.heads) > few)
+  if (ls == TLQ_OK && (long long)a.batch.max_q * (q_heads / a.cache.heads) > few)
     ls = launch_kv4_prefill(a, few, static_cast<uint8_t*>(workspace) + kv4_decode_workspace(cache->head_dim),
                             &many_parts, s);
   return ls == TLQ_OK ? launch_kv4_join(a, few_parts, many_parts, s) : ls;
+}
+
+size_t tl_kv4_attention_prefix_workspace_size(int q_heads, int heads, int head_dim, int tokens, int max_q) {
+  clear_error();
+  if (q_heads < 1 || heads < 1 || q_heads % heads || (head_dim != 64 && head_dim != 128) || tokens < 0 || max_q < 0)
+    return 0;
+  return prefix_workspace(q_heads, head_dim, tokens);
+}
+
+tlq_status tl_kv4_attention_prefix(const tl_kv4_cache* cache, const uint16_t* q, int64_t ldq, int q_heads,
+                                   uint16_t* out, int64_t ldo, const int32_t* q_start, const int32_t* seq_lens,
+                                   const int32_t* table, int ld_table, const int32_t* prefix_len,
+                                   const int32_t* prefix_table, int prefix_pages, int requests, int tokens, int max_q,
+                                   float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  KvAttention a{};
+  bool empty;
+  const tlq_status st = check_attention(
+      AttentionCall{"tl_kv4_attention_prefix", cache, q, ldq, q_heads, out, ldo, q_start, seq_lens, table, ld_table,
+                    requests, tokens, max_q, scale, 0, true, prefix_len, prefix_table, prefix_pages, workspace,
+                    workspace_bytes},
+      &a, &empty);
+  if (st != TLQ_OK || empty) return st;
+  const int few = few_rows_of(*cache), d = cache->head_dim;
+  const long long rows = (long long)tokens * q_heads;
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  uint8_t* sums = at + ((attention_workspace(d) + 255) & ~size_t(255));
+  const size_t each = (kv_row_sums_bytes(rows, d) + 255) & ~size_t(255);
+  for (KvRowSums* r : {&a.shared.own, &a.shared.prefix}) {
+    r->o = reinterpret_cast<float*>(sums);
+    r->ml = reinterpret_cast<float2*>(r->o + rows * d);
+    sums += each;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  KvJoin few_parts{}, many_parts{};
+  tlq_status ls = launch_kv4_decode_shared(a, few, at, &few_parts, s);
+  if (ls == TLQ_OK && (long long)tokens * (q_heads / a.cache.heads) > few)
+    ls = launch_kv4_prefill_shared(a, few, at + kv4_decode_workspace(d), &many_parts, s);
+  if (ls == TLQ_OK) ls = launch_kv4_join_shared(a, few_parts, many_parts, s);
+  return ls == TLQ_OK ? launch_kv4_merge(a, few, s) : ls;
 }
 
 tlq_status tl_rope_table(const double* inv_freq, int64_t num_positions, int rot_dim, double scale, float* table,
