@@ -15,11 +15,14 @@
 // operations a clock and SM).
 //
 // A cluster of blocks takes a row, a block a piece of it that lies in shared
-// memory from its first reading on (the row is read from DRAM once).  Cuts are
-// found by histograms: first over (max - x) / T in 2048 equal bins, then over
-// the values inside the one bin that holds the cut, until it is a single value;
-// counts and weights (three limbs of 15 bits each, so that 32-bit atomics do)
-// are added up over the cluster through distributed shared memory.
+// memory from its first reading on (the row is read from DRAM once).  A cut is
+// found by a histogram of (max - x) / T in 2048 equal bins (counts, and weights
+// in three limbs of 15 bits so that 32-bit atomics do).  The blocks tell each
+// other the sums of 32 bins each, every block finds the bin that holds the cut,
+// reads it from all of them, and ranks the bin's values, which each block sends
+// to all.  A bin of more than kList values (flat or equal logits) is divided by
+// further histograms over its values.  Three exchanges in the cluster, four with
+// a cut by count, are the whole latency beside the work.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -112,30 +115,37 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-struct Bin {
-  uint32_t count, limb[3];
-};
+constexpr int kGroups = 64, kGroupBins = kBins / kGroups;
+constexpr int kList = 512;  // candidates for a cut that are ranked one by one
+static_assert(kGroupBins == 32, "a lane to a bin");
 
-// What the blocks of a cluster tell each other.
+// The state of a block; other blocks of its cluster write what is marked.
 struct Shared {
-  uint32_t hist[4][kBins];  // counts, limbs
+  uint32_t hist[4][kBins];               // counts, limbs (read by others)
   uint64_t powers[256];
+  uint64_t list[2][kList];               // candidates, of the cut by count and by mass (written by others)
+  uint64_t list_mass[kList];             // their weights
+  uint64_t group_mass[8][kGroups];       // by block (written by others)
+  uint32_t group_count[8][kGroups];      // likewise
+  uint64_t mass[8];                      // likewise
+  uint32_t count[8], low[8], high[8];    // likewise
+  float top[8];                          // likewise
+  int top_at[8], bad[8];                 // likewise
   uint64_t warp_mass[kWarps];
   uint32_t warp_count[kWarps];
-  // of each block, written by all blocks into all
-  float top[16];
-  int top_at[16];
-  uint32_t low[16], high[16];
-  uint64_t mass[16];
-  uint32_t count[16];
-  int bad[16];
-  // the answer of a search, written by the block that has it into all
-  int found_bin, found_index;
-  uint64_t above_mass;
-  uint32_t above_count;
-  uint64_t bin_mass;
-  uint32_t bin_count;
+  float warp_top[kWarps];
+  int warp_at[kWarps], warp_bad[kWarps];
+  // what a search has found
+  int bin;
+  uint32_t before_count, bin_count, offset, pushed;
+  uint64_t before_mass, bin_mass, want_mass;
+  uint64_t cut, cut_mass;
+  int found_index;                       // written by others
 };
+
+__device__ __forceinline__ float value_of_key(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
 
 struct Row {
   float top;
@@ -159,92 +169,149 @@ __device__ __forceinline__ float value_of<__half>(__half v) {
   return __half2float(v);
 }
 
-// Sums over the block; every thread gets them.  Two barriers.
-__device__ __forceinline__ void block_sum(Shared& s, uint64_t& mass, uint32_t& count) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mass += __shfl_xor_sync(0xffffffffu, mass, o);
-    count += __shfl_xor_sync(0xffffffffu, count, o);
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) {
-    s.warp_mass[threadIdx.x >> 5] = mass;
-    s.warp_count[threadIdx.x >> 5] = count;
-  }
-  __syncthreads();
-  mass = 0;
-  count = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    mass += s.warp_mass[w];
-    count += s.warp_count[w];
-  }
-}
-
-// Exclusive sums over the block's threads, and the total.
-__device__ __forceinline__ void block_scan(Shared& s, uint64_t& mass, uint32_t& count) {
+// Exclusive sums over the block's threads.
+__device__ __forceinline__ uint64_t block_scan(Shared& s, uint64_t mass) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint64_t m0 = mass;
-  const uint32_t c0 = count;
+  const uint64_t own = mass;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint64_t m = __shfl_up_sync(0xffffffffu, mass, o);
-    const uint32_t c = __shfl_up_sync(0xffffffffu, count, o);
+    if (lane >= o) mass += m;
+  }
+  __syncthreads();
+  if (lane == 31) s.warp_mass[warp] = mass;
+  __syncthreads();
+  mass -= own;
+  for (int w = 0; w < warp; ++w) mass += s.warp_mass[w];
+  return mass;
+}
+
+// The bin in which the running count reaches want_count or, with want_mass, the
+// running mass reaches that: by one warp, from the blocks' sums of 32 bins each
+// and then those bins themselves.  s.bin is -1 where all bins stay below.
+__device__ __forceinline__ void find_bin(Shared& s, cg::cluster_group& cluster, int C, int rank, bool with_mass,
+                                         bool counting, uint32_t want_count, uint64_t want_mass) {
+  const int lane = threadIdx.x & 31;
+  uint64_t m[2] = {0, 0};
+  uint32_t c[2] = {0, 0};
+  for (int o = 0; o < C; ++o)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      c[j] += s.group_count[o][2 * lane + j];
+      if (with_mass) m[j] += s.group_mass[o][2 * lane + j];
+    }
+  uint64_t pm = m[0] + m[1];
+  uint32_t pc = c[0] + c[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t x = __shfl_up_sync(0xffffffffu, pm, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, pc, o);
     if (lane >= o) {
-      mass += m;
-      count += c;
+      pm += x;
+      pc += y;
     }
   }
-  __syncthreads();
-  if (lane == 31) {
-    s.warp_mass[warp] = mass;
-    s.warp_count[warp] = count;
+  uint64_t base_m = s.before_mass;
+  uint32_t base_c = s.before_count;
+  const uint32_t hit = __ballot_sync(0xffffffffu, counting ? base_c + pc >= want_count : base_m + pm >= want_mass);
+  if (!hit) {
+    if (lane == 0) s.bin = -1;
+    return;
   }
-  __syncthreads();
-  mass -= m0;
-  count -= c0;
-  for (int w = 0; w < warp; ++w) {
-    mass += s.warp_mass[w];
-    count += s.warp_count[w];
+  const int from = __ffs(hit) - 1;
+  base_m += __shfl_sync(0xffffffffu, pm - m[0] - m[1], from);
+  base_c += __shfl_sync(0xffffffffu, pc - c[0] - c[1], from);
+  const uint64_t m0 = __shfl_sync(0xffffffffu, m[0], from);
+  const uint32_t c0 = __shfl_sync(0xffffffffu, c[0], from);
+  const bool second = counting ? base_c + c0 < want_count : base_m + m0 < want_mass;
+  if (second) {
+    base_m += m0;
+    base_c += c0;
+  }
+  const int bin = (2 * from + (second ? 1 : 0)) * kGroupBins + lane;
+  uint64_t bm = 0;
+  uint32_t bc = 0, offset = 0;
+  for (int o = 0; o < C; ++o) {
+    const Shared& of = *cluster.map_shared_rank(&s, o);
+    const uint32_t n = of.hist[0][bin];
+    if (o < rank) offset += n;
+    bc += n;
+    if (with_mass) bm += of.hist[1][bin] + ((uint64_t)of.hist[2][bin] << 15) + ((uint64_t)of.hist[3][bin] << 30);
+  }
+  pm = bm;
+  pc = bc;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t x = __shfl_up_sync(0xffffffffu, pm, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, pc, o);
+    if (lane >= o) {
+      pm += x;
+      pc += y;
+    }
+  }
+  const uint32_t there = __ballot_sync(0xffffffffu, counting ? base_c + pc >= want_count : base_m + pm >= want_mass);
+  if (lane == __ffs(there) - 1) {
+    s.bin = bin;
+    s.before_mass = base_m + pm - bm;
+    s.before_count = base_c + pc - bc;
+    s.bin_mass = bm;
+    s.bin_count = bc;
+    s.offset = offset;
+    s.pushed = 0;
   }
 }
 
 template <class T, bool STAGED>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Shared& s = *reinterpret_cast<Shared*>(smem_raw);
-  T* const stage = reinterpret_cast<T*>(smem_raw + ((sizeof(Shared) + 15) & ~size_t(15)));
+  constexpr int kVec = 16 / (int)sizeof(T);
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long row = blockIdx.x / C;
   pdl_launch_dependents();
   for (int i = tid; i < 256; i += kThreads) s.powers[i] = kPowers.v[i];
+  for (int i = tid; i < 4 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
   pdl_wait();
 
   const T* const base = static_cast<const T*>(p.logits) + row * p.ld;
   const int i0 = min(p.vocab, rank * p.piece), n = min(p.vocab, i0 + p.piece) - i0;
   const T* const mine = base + i0;
+  // in shared memory the piece lies as it does to 16 bytes in global memory
+  const int lead = (int)((reinterpret_cast<uintptr_t>(mine) & 15) / sizeof(T));
+  T* const stage = reinterpret_cast<T*>(smem_raw + ((sizeof(Shared) + 15) & ~size_t(15))) + lead;
   auto at = [&](int i) -> float { return value_of<T>(STAGED ? stage[i] : mine[i]); };
 
   // ---- the piece into shared memory, its greatest value (lowest index first) ----
   float top = -INFINITY;
   int top_at = 0x7fffffff, bad = 0;
-  auto look = [&](float x, int i) {
+  auto look = [&](T v, int i) {
+    const float x = value_of<T>(v);
     bad |= !(x < INFINITY);
-    if (x > top) {
+    if (x > top) {  // a thread's indexes rise
       top = x;
-      top_at = i;
+      top_at = i0 + i;
     }
   };
-  if (STAGED) {
-    for (int i = tid; i < n; i += kThreads) {
-      const T v = mine[i];
-      stage[i] = v;
-      look(value_of<T>(v), i0 + i);
-    }
-  } else {
-    for (int i = tid; i < n; i += kThreads) look(value_of<T>(mine[i]), i0 + i);
+  const int head = min(n, lead ? kVec - lead : 0), vectors = (n - head) / kVec;
+  if (tid < head) {
+    const T v = mine[tid];
+    if (STAGED) stage[tid] = v;
+    look(v, tid);
+  }
+#pragma unroll 4
+  for (int i = tid; i < vectors; i += kThreads) {
+    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(mine + head) + i);
+    if (STAGED) *reinterpret_cast<uint4*>(stage + head + i * kVec) = raw;
+    const T* v = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) look(v[j], head + i * kVec + j);
+  }
+  for (int i = head + vectors * kVec + tid; i < n; i += kThreads) {
+    const T v = mine[i];
+    if (STAGED) stage[i] = v;
+    look(v, i);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -256,28 +323,24 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     }
     bad |= __shfl_xor_sync(0xffffffffu, bad, o);
   }
-  __shared__ float warp_top[kWarps];
-  __shared__ int warp_at[kWarps], warp_bad[kWarps];
   if (lane == 0) {
-    warp_top[warp] = top;
-    warp_at[warp] = top_at;
-    warp_bad[warp] = bad;
+    s.warp_top[warp] = top;
+    s.warp_at[warp] = top_at;
+    s.warp_bad[warp] = bad;
   }
   __syncthreads();
   if (tid < C) {
-    float x = warp_top[0];
-    int j = warp_at[0], b = warp_bad[0];
-    for (int w = 1; w < kWarps; ++w) {
-      if (warp_top[w] > x || (warp_top[w] == x && warp_at[w] < j)) {
-        x = warp_top[w];
-        j = warp_at[w];
+    for (int w = 0; w < kWarps; ++w) {
+      if (s.warp_top[w] > top || (s.warp_top[w] == top && s.warp_at[w] < top_at)) {
+        top = s.warp_top[w];
+        top_at = s.warp_at[w];
       }
-      b |= warp_bad[w];
+      bad |= s.warp_bad[w];
     }
     Shared& to = *cluster.map_shared_rank(&s, tid);
-    to.top[rank] = x;
-    to.top_at[rank] = j;
-    to.bad[rank] = b;
+    to.top[rank] = top;
+    to.top_at[rank] = top_at;
+    to.bad[rank] = bad;
   }
   cluster.sync();
   top = s.top[0];
@@ -290,15 +353,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     }
     bad |= s.bad[c];
   }
-  const bool first_thread = rank == 0 && tid == 0;
   const float t = p.temperature ? __ldg(p.temperature + row) : 1.0f;
   const bool none = bad || !(top > -INFINITY), greedy = !(t > 0.f);
-  if (none || greedy) {  // the same for the whole cluster
-    if (first_thread) {
+  if (none || greedy) {  // the same for the whole cluster; nothing of a block is looked at by another any more
+    if (rank == 0 && tid == 0) {
       p.tokens[row] = none ? -1 : top_at;
       if (p.logprobs) p.logprobs[row] = none ? NAN : 0.f;
     }
-    cluster.sync();  // no block ends while another may write to it
     return;
   }
 
@@ -308,32 +369,37 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   r.scale = fminf(r.e.hi, 1e30f) * ((float)kBins / kOctaves);
   const int k = p.top_k ? __ldg(p.top_k + row) : 0;
   const float tp = p.top_p ? __ldg(p.top_p + row) : 1.0f;
-  const float mp = p.min_p ? __ldg(p.min_p + row) : 0.f;
   const bool by_count = k > 0 && k < p.vocab, by_mass = tp < 1.0f;
 
-  uint32_t cut_key = 0;       // kept: keys above it, and
-  int cut_at = 0x7fffffff;    // those equal to it up to this index
-  if (by_count || by_mass) {
-    // Finds, in the falling order, the first value at which the count reaches
-    // want_count (mass 0) or the mass want_mass: its key, and how many of that
-    // value are needed.
-    uint64_t limit_mass = 0;  // of the values that the count leaves
-    uint32_t ties = 0xffffffffu;  // all of them
-    for (int pass = by_count ? 0 : 1; pass < (by_mass ? 2 : 1); ++pass) {
-      const bool counting = pass == 0;
-      uint64_t before_mass = 0, want_mass = 0;
-      uint32_t before_count = 0, key_low = 0, key_high = 0xffffffffu, shift = 0;
-      int bin = -1;  // of the first level; -1: not known yet
-      for (int level = 0; level < 8; ++level) {
-        for (int i = tid; i < 4 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
-        __syncthreads();
+  // kept: (key, index) pairs, as one number that falls in the order's direction, from this one on
+  uint64_t cut = 0;
+  auto pair_of = [&](uint32_t key, int i) -> uint64_t { return ((uint64_t)key << 32) | (0xffffffffu - (uint32_t)(i0 + i)); };
+
+  bool fresh = false;  // the histogram is that of all values
+  uint64_t limit_mass = 0;
+#pragma unroll 1
+  for (int pass = by_count ? 0 : 1; pass < (by_mass ? 2 : 1); ++pass) {
+    const bool counting = pass == 0;
+    uint32_t key_low = 0, key_high = 0xffffffffu, shift = 0;
+    int bin = -1;  // of all values' histogram, once it is known
+    if (tid == 0) {
+      s.before_mass = 0;
+      s.before_count = 0;
+    }
+#pragma unroll 1
+    for (bool first_level = true;; first_level = false) {
+      if (!(first_level && fresh)) {
+        if (!first_level || (pass > 0 && by_count)) {  // zero from the start on otherwise
+          for (int i = tid; i < 4 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
+          __syncthreads();
+        }
+#pragma unroll 2
         for (int i = tid; i < n; i += kThreads) {
           const float x = at(i);
-          const int b1 = first_bin(r, x);
-          int b = b1;
-          if (level > 0) {
+          int b = first_bin(r, x);
+          if (!first_level) {
             const uint32_t key = key_of(x);
-            b = b1 == bin && key >= key_low && key <= key_high ? (int)((key_high - key) >> shift) : kBins;
+            b = b == bin && key >= key_low && key <= key_high ? (int)((key_high - key) >> shift) : kBins;
           }
           if (b < kBins) {
             atomicAdd(&s.hist[0][b], 1u);
@@ -345,187 +411,193 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
             }
           }
         }
-        cluster.sync();
-        // a block's share of the bins, added up over the cluster: bins [rank * share, + share)
-        const int share = (kBins + C - 1) / C, each = (share + kThreads - 1) / kThreads;
-        uint64_t m = 0, my_mass[4];
-        uint32_t c = 0, my_count[4];
-        for (int j = 0; j < each; ++j) {
-          const int i = tid * each + j, b = rank * share + i;
-          my_mass[j] = 0;
-          my_count[j] = 0;
-          if (i < share && b < kBins)
-            for (int o = 0; o < C; ++o) {
-              const Shared& from = *cluster.map_shared_rank(&s, o);
-              my_count[j] += from.hist[0][b];
-              if (by_mass)
-                my_mass[j] += from.hist[1][b] + ((uint64_t)from.hist[2][b] << 15) + ((uint64_t)from.hist[3][b] << 30);
-            }
-          m += my_mass[j];
-          c += my_count[j];
-        }
-        uint64_t all_m = m, pre_m = m;
-        uint32_t all_c = c, pre_c = c;
-        block_sum(s, all_m, all_c);
-        block_scan(s, pre_m, pre_c);
-        if (tid < C) {
-          Shared& to = *cluster.map_shared_rank(&s, tid);
-          to.mass[rank] = all_m;
-          to.count[rank] = all_c;
-          to.found_bin = -1;
-        }
-        cluster.sync();
-        uint64_t total_m = 0, base_m = before_mass;
-        uint32_t base_c = before_count;
-        for (int o = 0; o < C; ++o) {
-          if (o < rank) {
-            base_m += s.mass[o];
-            base_c += s.count[o];
+        __syncthreads();
+        // sums of 32 bins, to every block
+#pragma unroll
+        for (int g = warp; g < kGroups; g += kWarps) {
+          const int b = g * kGroupBins + lane;
+          const uint32_t c = __reduce_add_sync(0xffffffffu, s.hist[0][b]);
+          uint64_t m = 0;
+          if (by_mass) {
+            m = s.hist[1][b] + ((uint64_t)s.hist[2][b] << 15) + ((uint64_t)s.hist[3][b] << 30);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
           }
-          total_m += s.mass[o];
-        }
-        if (level == 0 && !counting) {
-          // the shortest run that reaches p of the mass: ceil(p * mass), of at least one value
-          const uint64_t whole_m = by_count && limit_mass ? limit_mass : total_m;
-          const float q = fmaxf(tp, 0.f);
-          const uint64_t frac = (uint64_t)((double)q * 18446744073709551616.0);
-          want_mass = max(1ull, (unsigned long long)(__umul64hi(frac, whole_m) + (frac * whole_m != 0)));
-        }
-        base_m += pre_m;
-        base_c += pre_c;
-        for (int j = 0; j < each; ++j) {
-          const bool here = counting ? base_c < (uint32_t)k && base_c + my_count[j] >= (uint32_t)k
-                                     : base_m < want_mass && base_m + my_mass[j] >= want_mass;
-          if (here)
-            for (int o = 0; o < C; ++o) {
-              Shared& to = *cluster.map_shared_rank(&s, o);
-              to.found_bin = rank * share + tid * each + j;
-              to.above_mass = base_m;
-              to.above_count = base_c;
-              to.bin_mass = my_mass[j];
-              to.bin_count = my_count[j];
-            }
-          base_m += my_mass[j];
-          base_c += my_count[j];
+          if (lane < C) {
+            Shared& to = *cluster.map_shared_rank(&s, lane);
+            to.group_count[rank][g] = c;
+            if (by_mass) to.group_mass[rank][g] = m;
+          }
         }
         cluster.sync();
-        const int found = s.found_bin;
-        if (found < 0) break;  // fewer values with weight than that: nothing is cut
-        before_mass = s.above_mass;
-        before_count = s.above_count;
-        const uint32_t in_bin = s.bin_count;
-        const uint64_t mass_in_bin = s.bin_mass;
-        if (level == 0) {
-          bin = found;
-        } else {
-          key_high -= (uint32_t)found << shift;
-          key_low = shift ? max(key_low, key_high - ((1u << shift) - 1u)) : key_high;
+        fresh = first_level;
+      }
+      if (warp == 0) {
+        __syncwarp();
+        if (first_level && !counting) {
+          // the shortest run that reaches p of the mass: ceil(p * mass), of at least one value
+          uint64_t all = 0;
+          for (int o = 0; o < C; ++o) all += s.group_mass[o][lane] + s.group_mass[o][lane + 32];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+          if (limit_mass) all = limit_mass;
+          const uint64_t frac = (uint64_t)((double)fmaxf(tp, 0.f) * 18446744073709551616.0);
+          const uint64_t want = __umul64hi(frac, all) + (frac * all != 0);
+          if (lane == 0) s.want_mass = want ? want : 1;
+          __syncwarp();
         }
-        // the least and greatest key in there
-        uint32_t low = 0xffffffffu, high = 0;
+        find_bin(s, cluster, C, rank, by_mass, counting, (uint32_t)k, s.want_mass);
+      }
+      __syncthreads();
+      const int found = s.bin;
+      if (found < 0) break;  // fewer values with weight than that: nothing is cut
+      const uint32_t in_bin = s.bin_count;
+      if (first_level) {
+        bin = found;
+      } else {
+        key_high -= (uint32_t)found << shift;
+        key_low = shift ? max(key_low, key_high - ((1u << shift) - 1u)) : key_high;
+      }
+      auto inside = [&](float x, uint32_t key) {
+        return first_bin(r, x) == bin && key >= key_low && key <= key_high;
+      };
+      if (in_bin <= (uint32_t)kList) {
+        // every block gets all candidates and ranks them
         for (int i = tid; i < n; i += kThreads) {
           const float x = at(i);
           const uint32_t key = key_of(x);
-          if (first_bin(r, x) == bin && key >= key_low && key <= key_high) {
-            low = min(low, key);
-            high = max(high, key);
+          if (inside(x, key)) {
+            const uint32_t spot = s.offset + atomicAdd(&s.pushed, 1u);
+            for (int o = 0; o < C; ++o) cluster.map_shared_rank(&s, o)->list[pass][spot] = pair_of(key, i);
           }
-        }
-        low = __reduce_min_sync(0xffffffffu, low);
-        high = __reduce_max_sync(0xffffffffu, high);
-        __syncthreads();
-        if (lane == 0) {
-          s.warp_count[warp] = low;
-          s.warp_mass[warp] = high;
-        }
-        __syncthreads();
-        if (tid < C) {
-          for (int w = 0; w < kWarps; ++w) {
-            low = min(low, s.warp_count[w]);
-            high = max(high, (uint32_t)s.warp_mass[w]);
-          }
-          Shared& to = *cluster.map_shared_rank(&s, tid);
-          to.low[rank] = low;
-          to.high[rank] = high;
         }
         cluster.sync();
-        key_low = 0xffffffffu;
-        key_high = 0;
-        for (int o = 0; o < C; ++o) {
-          key_low = min(key_low, s.low[o]);
-          key_high = max(key_high, s.high[o]);
+        const uint64_t* const list = s.list[pass];
+        const uint64_t me = tid < (int)in_bin ? list[tid] : 0;
+        uint64_t w = 0;
+        if (tid < (int)in_bin) {
+          w = weight_of(value_of_key((uint32_t)(me >> 32)), r.top, r.e, s.powers);
+          s.list_mass[tid] = w;
         }
-        if (key_low == key_high) {  // one value, in_bin times
-          ties = counting ? (uint32_t)k - before_count
-                          : (uint32_t)((want_mass - before_mass + mass_in_bin / in_bin - 1) / (mass_in_bin / in_bin));
-          if (counting) limit_mass = before_mass + (mass_in_bin / in_bin) * ties;
-          if (ties >= in_bin) ties = 0xffffffffu;
-          cut_key = key_low;
-          break;
-        }
-        shift = 0;
-        while (((key_high - key_low) >> shift) >= (uint32_t)kBins) ++shift;
-      }
-    }
-    if (ties != 0xffffffffu) {
-      // the index of the last of the ties: warps hold pieces of 32 * steps values in order
-      const int seg = (n + kWarps - 1) / kWarps;
-      uint32_t c = 0;
-      for (int i = warp * seg + lane; i < min(n, (warp + 1) * seg); i += 32) c += key_of(at(i)) == cut_key;
-      c = __reduce_add_sync(0xffffffffu, c);
-      __syncthreads();
-      if (lane == 0) s.warp_count[warp] = c;
-      __syncthreads();
-      uint32_t all = 0, before = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += s.warp_count[w];
-        all += s.warp_count[w];
-      }
-      if (tid < C) cluster.map_shared_rank(&s, tid)->count[rank] = all;
-      cluster.sync();
-      for (int o = 0; o < rank; ++o) before += s.count[o];
-      if (before < ties && before + c >= ties) {  // this warp
-        uint32_t left = ties - before;
-        for (int i = warp * seg; i < min(n, (warp + 1) * seg); i += 32) {
-          const bool hit = i + lane < min(n, (warp + 1) * seg) && key_of(at(i + lane)) == cut_key;
-          const uint32_t hits = __ballot_sync(0xffffffffu, hit);
-          if ((uint32_t)__popc(hits) >= left) {
-            const int spot = __fns(hits, 0, (int)left);
-            if (lane < C) cluster.map_shared_rank(&s, lane)->found_index = i0 + i + spot;
-            break;
+        __syncthreads();
+        if (tid < (int)in_bin) {
+          uint64_t m = s.before_mass;
+          uint32_t c = s.before_count;
+          for (uint32_t j = 0; j < in_bin; ++j)
+            if (list[j] > me) {
+              m += s.list_mass[j];
+              ++c;
+            }
+          if (counting ? c + 1 == (uint32_t)k : m < s.want_mass && m + w >= s.want_mass) {
+            s.cut = me;
+            s.cut_mass = m + w;
           }
-          left -= __popc(hits);
+        }
+        __syncthreads();
+        cut = s.cut;
+        limit_mass = s.cut_mass;
+        break;
+      }
+      // the least and greatest key in there
+      uint32_t low = 0xffffffffu, high = 0;
+      for (int i = tid; i < n; i += kThreads) {
+        const float x = at(i);
+        const uint32_t key = key_of(x);
+        if (inside(x, key)) {
+          low = min(low, key);
+          high = max(high, key);
         }
       }
+      low = __reduce_min_sync(0xffffffffu, low);
+      high = __reduce_max_sync(0xffffffffu, high);
+      if (lane == 0) {
+        s.warp_count[warp] = low;
+        s.warp_mass[warp] = high;
+      }
+      __syncthreads();
+      if (tid < C) {
+        for (int w = 0; w < kWarps; ++w) {
+          low = min(low, s.warp_count[w]);
+          high = max(high, (uint32_t)s.warp_mass[w]);
+        }
+        Shared& to = *cluster.map_shared_rank(&s, tid);
+        to.low[rank] = low;
+        to.high[rank] = high;
+      }
       cluster.sync();
-      cut_at = s.found_index;
+      key_low = 0xffffffffu;
+      key_high = 0;
+      for (int o = 0; o < C; ++o) {
+        key_low = min(key_low, s.low[o]);
+        key_high = max(key_high, s.high[o]);
+      }
+      if (key_low == key_high) {
+        // one value, in_bin times: the index of the last that is needed
+        const uint64_t each = s.bin_mass / in_bin;
+        const uint32_t ties = counting ? (uint32_t)k - s.before_count
+                                       : (uint32_t)((s.want_mass - s.before_mass + each - 1) / each);
+        const int seg = (n + kWarps - 1) / kWarps, end = min(n, (warp + 1) * seg);
+        uint32_t c = 0;
+        for (int i = warp * seg + lane; i < end; i += 32) c += key_of(at(i)) == key_low;
+        c = __reduce_add_sync(0xffffffffu, c);
+        __syncthreads();
+        if (lane == 0) s.warp_count[warp] = c;
+        __syncthreads();
+        uint32_t all = 0, before = 0;
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) before += s.warp_count[w];
+          all += s.warp_count[w];
+        }
+        if (tid < C) cluster.map_shared_rank(&s, tid)->count[rank] = all;
+        cluster.sync();
+        for (int o = 0; o < rank; ++o) before += s.count[o];
+        if (before < ties && before + c >= ties) {  // this warp
+          uint32_t left = ties - before;
+          for (int i = warp * seg; i < end; i += 32) {
+            const bool hit = i + lane < end && key_of(at(i + lane)) == key_low;
+            const uint32_t hits = __ballot_sync(0xffffffffu, hit);
+            if ((uint32_t)__popc(hits) >= left) {
+              const int spot = __fns(hits, 0, (int)left);
+              if (lane < C) cluster.map_shared_rank(&s, lane)->found_index = i0 + i + spot;
+              break;
+            }
+            left -= __popc(hits);
+          }
+        }
+        cluster.sync();
+        cut = ((uint64_t)key_low << 32) | (0xffffffffu - (uint32_t)s.found_index);
+        limit_mass = s.before_mass + each * ties;
+        break;
+      }
+      shift = 0;
+      while (((key_high - key_low) >> shift) >= (uint32_t)kBins) ++shift;
     }
+    __syncthreads();
   }
 
   // ---- the mass of what is kept, by warps' segments in order ----
-  const uint64_t least = (uint64_t)ceil(fmin((double)fmaxf(mp, 0.f), 1.0) * 8796093022208.0);
-  const bool cut = by_count || by_mass;
+  const float mp = p.min_p ? __ldg(p.min_p + row) : 0.f;
+  const uint64_t least = mp > 0.f ? (uint64_t)ceil(fmin((double)mp, 1.0) * 8796093022208.0) : 0;
+  const uint32_t cut_key = (uint32_t)(cut >> 32);
   auto kept_weight = [&](int i) -> uint64_t {
     const float x = at(i);
-    if (cut) {
-      const uint32_t key = key_of(x);
-      if (key < cut_key || (key == cut_key && i0 + i > cut_at)) return 0;
-    }
+    const uint32_t key = key_of(x);
+    if (key < cut_key || (key == cut_key && pair_of(key, i) < cut)) return 0;
     const uint64_t w = weight_of(x, r.top, r.e, s.powers);
     return w >= least ? w : 0;
   };
   const int seg = (n + kWarps - 1) / kWarps;
   uint64_t m = 0;
+#pragma unroll 2
   for (int i = warp * seg + lane; i < min(n, (warp + 1) * seg); i += 32) m += kept_weight(i);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-  __syncthreads();
   if (lane == 0) s.warp_mass[warp] = m;
   __syncthreads();
   uint64_t all = 0;
   for (int w = 0; w < kWarps; ++w) all += s.warp_mass[w];
   if (tid < C) cluster.map_shared_rank(&s, tid)->mass[rank] = all;
-  cluster.sync();
+  cluster.sync();  // from here on a block looks at its own memory only
   uint64_t total = 0, before = 0;
   for (int o = 0; o < C; ++o) {
     if (o < rank) before += s.mass[o];
@@ -539,14 +611,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     // the segment's values in order, a run of them to a thread
     const int begin = w * seg, end = min(n, begin + seg), each = (seg + kThreads - 1) / kThreads;
     uint64_t run = 0;
-    uint32_t unused = 0;
     for (int j = 0; j < each; ++j) {
       const int i = begin + tid * each + j;
       if (i < end) run += kept_weight(i);
     }
-    uint64_t upto = run;
-    block_scan(s, upto, unused);
-    upto += before;
+    uint64_t upto = before + block_scan(s, run);
     if (upto <= target && target < upto + run)
       for (int j = 0; j < each; ++j) {
         const int i = begin + tid * each + j;
@@ -564,7 +633,6 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         upto += wi;
       }
   }
-  cluster.sync();  // no block ends while another may write to it
 }
 
 template <class T, bool STAGED>
@@ -592,7 +660,7 @@ tlq_status launch_as(SampleParams p, int rows, cudaStream_t stream) {
   int blocks = 1;
   while (blocks < 8 && p.vocab > 4096 * blocks) blocks *= 2;
   p.piece = (p.vocab + blocks - 1) / blocks;
-  const size_t fixed = (sizeof(Shared) + 15) & ~size_t(15), staged = fixed + (size_t)p.piece * sizeof(T);
+  const size_t fixed = (sizeof(Shared) + 15) & ~size_t(15), staged = fixed + (size_t)p.piece * sizeof(T) + 16;
   return staged <= (size_t)kMaxSmem ? launch_one<T, true>(p, rows, blocks, staged, stream)
                                     : launch_one<T, false>(p, rows, blocks, fixed, stream);
 }
