@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
   }
   pdl_wait();
   KvJoinHeader* const header = &p.join.headers[blockIdx.x];
-  if (tid == 0) header->followers = 0;
+  if (!kShared && tid == 0) header->followers = 0;
 
   auto count = [&](int i) -> long long {
     const ItemShape s = item_shape<R>(p, kv_request_or_prefix<kShared>(p.batch, p.cache.page, i));
@@ -716,6 +716,20 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
         }
       }
     const bool whole = sg.first && sg.last;
+    // the block that holds the item's last unit
+    int end_block = 0;
+    if (!whole && sg.first && (kShared || tid == 0)) {
+      const long long last_u = sg.item_end - 1;
+      long long b = ((last_u + 1) * n - 1) / U;
+      while (U * b / n > last_u) --b;
+      while (U * (b + 1) / n <= last_u) ++b;
+      end_block = (int)b;
+    }
+    const KvRowSums& sums = sg.req < p.batch.requests ? p.shared.own : p.shared.prefix;
+    auto sums_row = [&](int row) -> size_t {
+      const int gr = row0 + row, t = divide(gr, p.by_share), g = gr - t * p.share;
+      return (size_t)(rq.q0 + t) * p.q_heads + head * p.share + g;
+    };
     float* part = nullptr;
     if (!whole)
       part = p.join.parts + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * (R * (D + 2));
@@ -757,11 +771,9 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
         }
         if (kShared && whole) {
           if (row < rows) {
-            const KvRowSums& to = sg.req < p.batch.requests ? p.shared.own : p.shared.prefix;
-            const int gr = row0 + row, t = divide(gr, p.by_share), g = gr - t * p.share;
-            const size_t at = (size_t)(rq.q0 + t) * p.q_heads + head * p.share + g;
-            *reinterpret_cast<float4*>(to.o + at * D + ch) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            if (ch == 0) to.ml[at] = make_float2(mm, ll);
+            const size_t at = sums_row(row);
+            *reinterpret_cast<float4*>(sums.o + at * D + ch) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (ch == 0) sums.ml[at] = make_float2(mm, ll);
           }
         } else if (whole) {
           if (row < rows) {
@@ -778,18 +790,13 @@ __global__ void __launch_bounds__(DCfg<D, NG, NT>::THREADS, DCfg<D, NG, NT>::CTA
           if (ch == 0) {
             part[R * D + row] = mm;
             part[R * D + R + row] = ll;
+            if (kShared && sg.first && row < rows) sums.ml[sums_row(row)] = kv_row_in_parts(blockIdx.x, end_block - blockIdx.x);
           }
         }
       }
     }
-    if (!whole && sg.first && tid == 0) {
-      // the block that holds the item's last unit
-      const long long last_u = sg.item_end - 1;
-      long long b = ((last_u + 1) * n - 1) / U;
-      while (U * b / n > last_u) --b;
-      while (U * (b + 1) / n <= last_u) ++b;
-      *header = KvJoinHeader{(int)(b - blockIdx.x), rq.q0, row0, rows, head, sg.req >= p.batch.requests};
-    }
+    if (!kShared && !whole && sg.first && tid == 0)
+      *header = KvJoinHeader{(int)(end_block - blockIdx.x), rq.q0, row0, rows, head};
   }
 }
 

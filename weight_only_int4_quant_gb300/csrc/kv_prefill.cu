@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   const uint32_t tmem = uniform(bar->tmem);
   pdl_wait();
   KvJoinHeader* const header = &p.join.headers[blockIdx.x];
-  if (tid == 0) header->followers = 0;
+  if (!kShared && tid == 0) header->followers = 0;
 
   // units of a request; a warp to a request where all fit the block at once
   auto lane_units = [&](const KvRequest& r, int first, int step) {
@@ -869,6 +869,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const bool whole = sg.first && sg.last;
+      auto end_block = [&]() -> int {  // the block that holds the item's last unit
+        const long long last_u = sg.item_end - 1;
+        long long b = ((last_u + 1) * n - 1) / U;
+        while (U * b / n > last_u) --b;
+        while (U * (b + 1) / n <= last_u) ++b;
+        return (int)b;
+      };
       const int row0 = 32 * quarter + r;  // this thread's rows: row0 + 8 y
       const float up = 16777216.0f;       // codes were entered as c 2^-24
       if (!kShared && whole) {
@@ -932,23 +939,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
         // a partial (or a whole row's sums), its columns in TMEM's order
         float *po[4], *pm[4];
         int lstep = kItemRows;  // from m to l
-        if (kShared && whole) {
-          const KvRowSums& to = sg.req < p.batch.requests ? p.shared.own : p.shared.prefix;
-          lstep = 1;
+        float* const part = p.join.parts + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * (kItemRows * (D + 2));
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          po[y] = part + (size_t)(kRows * tile + row0 + 8 * y) * D + 2 * qd;
+          pm[y] = part + kItemRows * D + kRows * tile + row0 + 8 * y;
+        }
+        if (kShared && sg.first) {
+          const KvRowSums& sums = sg.req < p.batch.requests ? p.shared.own : p.shared.prefix;
+          const int followers = whole ? 0 : end_block() - (int)blockIdx.x;
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int gr = sg.row0 + kRows * tile + min(row0 + 8 * y, rows - 1);
             const int t = divide(gr, p.by_share), g = gr - t * p.share;
             const size_t at = (size_t)(rq.q0 + t) * p.q_heads + sg.head * p.share + g;
-            po[y] = to.o + at * D + 2 * qd;
-            pm[y] = reinterpret_cast<float*>(to.ml + at);
-          }
-        } else {
-          float* const part = p.join.parts + ((size_t)blockIdx.x * 2 + (sg.first ? 1 : 0)) * (kItemRows * (D + 2));
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            po[y] = part + (size_t)(kRows * tile + row0 + 8 * y) * D + 2 * qd;
-            pm[y] = part + kItemRows * D + kRows * tile + row0 + 8 * y;
+            if (whole) {
+              lstep = 1;
+              po[y] = sums.o + at * D + 2 * qd;
+              pm[y] = reinterpret_cast<float*>(sums.ml + at);
+            } else if (qd == 0 && row0 + 8 * y < rows) {
+              sums.ml[at] = kv_row_in_parts(blockIdx.x, followers);
+            }
           }
         }
 #pragma unroll 1
@@ -983,13 +994,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
           }
       }
       tc_fence_before();
-      if (!whole && sg.first && tid == 0) {
-        const long long last_u = sg.item_end - 1;  // the block that holds the item's last unit
-        long long b = ((last_u + 1) * n - 1) / U;
-        while (U * b / n > last_u) --b;
-        while (U * (b + 1) / n <= last_u) ++b;
-        *header = KvJoinHeader{(int)(b - blockIdx.x), rq.q0, sg.row0, sg.rows, sg.head, sg.req >= p.batch.requests};
-      }
+      if (!kShared && !whole && sg.first && tid == 0)
+        *header = KvJoinHeader{end_block() - (int)blockIdx.x, rq.q0, sg.row0, sg.rows, sg.head};
     }
   }
   tc_fence_before();

@@ -15,9 +15,9 @@
 // each.  Of a pair's channels both lie in one lane: for halves (i, i + rot / 2)
 // lane l holds chunks l and l + rot / 16, for neighbours 2 l and 2 l + 1; either
 // way its pairs are 8 l .. 8 l + 7, one piece of the table's row.  A lane takes
-// U rows one after another, of one token where heads allow it, so that weights
-// and the table's row are read once for all of them and their loads are under
-// way together.  A block's rows are all queries, all keys or all values.
+// up to eight rows one after another, of one token where heads allow it, so that
+// weights and the table's row are read once for all of them; a row is asked for
+// a turn ahead.  A block's rows are all queries, all keys or all values.
 #include <algorithm>
 
 #include "kv_codes.cuh"
@@ -25,7 +25,7 @@
 namespace tlq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kResident = 3;  // blocks of an SM (registers)
 
 struct Part {
   const __half* x;
@@ -46,6 +46,7 @@ struct RopeParams {
   float eps, inv_d;
   KvCache cache;
   const long long* slots;
+  int turns;  // rows of a lane
 };
 
 // Lane l's two chunks.
@@ -95,8 +96,8 @@ __device__ __forceinline__ void turn_of(const RopeTable& r, int l, const int (&a
   }
 }
 
-template <int D, int U>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+template <int D>
+__global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopeParams p) {
   constexpr int L = D / 16;  // lanes of a row
   pdl_launch_dependents();
   pdl_wait();
@@ -105,22 +106,23 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   while (kind < 2 && block >= p.part[kind].blocks) block -= p.part[kind++].blocks;
   const Part& part = p.part[kind];
   const int l = threadIdx.x % L;
-  const uint32_t first = (block * (kThreads / L) + threadIdx.x / L) * U;
+  const uint32_t first = (block * (kThreads / L) + threadIdx.x / L) * p.turns;
   const int rot = kind == 2 ? 0 : p.rope.rot;
   const bool turns = l * 16 < rot;
   const int2 ch = chunks_of<D>(l, rot, p.rope.neighbours);
 
-  // every lane of a warp takes part in all shuffles: rows past the end do the last one again
-  uint4 raw[U][2];
-  uint32_t tok[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const uint32_t row = min(first + u, part.rows - 1);
-    tok[u] = (uint32_t)divide((int)row, part.heads);
-    const uint4* src = reinterpret_cast<const uint4*>(part.x + tok[u] * part.ld + (row - tok[u] * part.heads.d) * D);
-    raw[u][0] = __ldg(src + ch.x);
-    raw[u][1] = __ldg(src + ch.y);
-  }
+  // A row is asked for a turn ahead.  Every lane of a warp takes part in all
+  // shuffles: rows past the end do the last one again.
+  uint4 raw[2];
+  uint32_t next_t;
+  auto fetch = [&](uint32_t row) {
+    row = min(row, part.rows - 1);
+    next_t = (uint32_t)divide((int)row, part.heads);
+    const uint4* src = reinterpret_cast<const uint4*>(part.x + next_t * part.ld + (row - next_t * part.heads.d) * D);
+    raw[0] = __ldg(src + ch.x);
+    raw[1] = __ldg(src + ch.y);
+  };
+  fetch(first);
   uint4 wraw[2];
   const bool normed = kind < 2 && part.weight != nullptr;
   if (normed) {
@@ -130,9 +132,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   float2 cs[8];  // of the token at hand
   bool there = true;
   uint32_t held = 0xffffffffu;
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const uint32_t row = min(first + u, part.rows - 1), t = tok[u];
+#pragma unroll 1
+  for (int u = 0; u < p.turns; ++u) {
+    const uint32_t row = min(first + u, part.rows - 1), t = next_t;
     const int head = (int)(row - t * part.heads.d);
     if (p.rope.rot && t != held) {
       held = t;
@@ -149,9 +151,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
     float2 x[2][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[0][i] = half2_at(raw[u][0], i);
-      x[1][i] = half2_at(raw[u][1], i);
+      x[0][i] = half2_at(raw[0], i);
+      x[1][i] = half2_at(raw[1], i);
     }
+    if (u + 1 < p.turns) fetch(first + u + 1);
     if (normed) {
       float s0 = chunk_squares(x[0]), s1 = chunk_squares(x[1]), sum;
       if (!p.rope.neighbours && rot == D) {
@@ -280,12 +283,18 @@ __global__ void table_kernel(const double* __restrict__ freq, float2* __restrict
   }
 }
 
-template <int D, int U>
-tlq_status launch_one(RopeParams& p, cudaStream_t stream) {
-  constexpr uint32_t per = kThreads / (D / 16) * U;
+template <int D>
+tlq_status launch_rows(RopeParams& p, cudaStream_t stream) {
+  constexpr uint32_t groups = kThreads / (D / 16);  // rows of a block at a time
+  long long rows = 0;
+  for (const Part& part : p.part) rows += part.rows;
+  // one turn each while they all fit the GPU at once, and up to eight
+  const long long wave = (long long)device_info().sms * kResident * groups;
+  p.turns = (int)std::min<long long>(8, (rows + wave - 1) / wave);
   uint32_t blocks = 0;
   for (Part& part : p.part) {
-    part.blocks = (part.rows + per - 1) / per;
+    const uint32_t per = groups * p.turns;
+    part.blocks = (uint32_t)(((long long)part.rows + per - 1) / per);
     blocks += part.blocks;
   }
   cudaLaunchConfig_t lc = {};
@@ -297,14 +306,7 @@ tlq_status launch_one(RopeParams& p, cudaStream_t stream) {
   at.val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = &at;
   lc.numAttrs = pdl_enabled() ? 1 : 0;
-  return cuda_error(cudaLaunchKernelEx(&lc, rope_kernel<D, U>, p), "rope: launch");
-}
-
-template <int D>
-tlq_status launch_rows(RopeParams& p, cudaStream_t stream) {
-  long long rows = 0;
-  for (const Part& part : p.part) rows += part.rows;
-  return rows * (D / 16) < 64ll * kThreads * device_info().sms / 8 ? launch_one<D, 1>(p, stream) : launch_one<D, 4>(p, stream);
+  return cuda_error(cudaLaunchKernelEx(&lc, rope_kernel<D>, p), "rope: launch");
 }
 
 }  // namespace

@@ -35,11 +35,12 @@ namespace tlq {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxBlocks = 8;        // of a cluster
 constexpr int kBins = 2048;
 constexpr int kOne = 43;             // the largest weight is 2^43
 constexpr float kOctaves = 40.0f;    // weights below 2^-40 of it count as none
 constexpr int kMaxSmem = 232448 - 1024;
-static_assert(kMaxVocab / 8 <= 1 << 17, "limbs of 15 bits of a block's values add up in 32");
+static_assert(kMaxVocab / kMaxBlocks <= 1 << 17, "limbs of 15 bits of a block's values add up in 32");
 
 // 2^(-j / 256) * 2^43, rounded: exp of -j ln 2 / 256 by its series in double.
 struct PowerTable {
@@ -109,6 +110,14 @@ __device__ __forceinline__ uint64_t weight_of(float x, float top, Exponent e, co
   return (v + ((1ull << n) >> 1)) >> n;
 }
 
+// x in [0, 1) as a fraction of 2^64 (bits below that are cut off).
+__device__ __forceinline__ uint64_t fraction_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const uint64_t m = (uint64_t)((b & 0x7fffffu) | 0x800000u) << 40;  // x = m * 2^(e - 126) * 2^-64
+  const int down = 126 - (int)(b >> 23);
+  return b < 0x800000u || down > 63 ? 0 : m >> down;
+}
+
 // Order-preserving whole numbers for FP32 values (-0 as +0).
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
@@ -125,12 +134,14 @@ struct Shared {
   uint64_t powers[256];
   uint64_t list[2][kList];               // candidates, of the cut by count and by mass (written by others)
   uint64_t list_mass[kList];             // their weights
-  uint64_t group_mass[8][kGroups];       // by block (written by others)
-  uint32_t group_count[8][kGroups];      // likewise
-  uint64_t mass[8];                      // likewise
-  uint32_t count[8], low[8], high[8];    // likewise
-  float top[8];                          // likewise
-  int top_at[8], bad[8];                 // likewise
+  uint64_t group_mass[kMaxBlocks][kGroups];   // by block (written by others)
+  uint32_t group_count[kMaxBlocks][kGroups];  // likewise
+  uint64_t fine_mass[kMaxBlocks][kGroupBins];
+  uint32_t fine_count[kMaxBlocks][kGroupBins];
+  uint64_t mass[kMaxBlocks];                      // likewise
+  uint32_t count[8], low[8], high[kMaxBlocks];    // likewise
+  float top[kMaxBlocks];                          // likewise
+  int top_at[8], bad[kMaxBlocks];                 // likewise
   uint64_t warp_mass[kWarps];
   uint32_t warp_count[kWarps];
   float warp_top[kWarps];
@@ -138,7 +149,7 @@ struct Shared {
   // what a search has found
   int bin;
   uint32_t before_count, bin_count, offset, pushed;
-  uint64_t before_mass, bin_mass, want_mass;
+  uint64_t before_mass, bin_mass;
   uint64_t cut, cut_mass;
   int found_index;                       // written by others
 };
@@ -186,79 +197,94 @@ __device__ __forceinline__ uint64_t block_scan(Shared& s, uint64_t mass) {
   return mass;
 }
 
-// The bin in which the running count reaches want_count or, with want_mass, the
-// running mass reaches that: by one warp, from the blocks' sums of 32 bins each
-// and then those bins themselves.  s.bin is -1 where all bins stay below.
+// Inclusive sums over a warp.
+__device__ __forceinline__ void warp_scan(uint64_t& m, uint32_t& c) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t x = __shfl_up_sync(0xffffffffu, m, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, c, o);
+    if ((threadIdx.x & 31) >= o) {
+      m += x;
+      c += y;
+    }
+  }
+}
+
+// The bin in which the running count reaches want_count or, with `counting`
+// false, the running mass reaches want_mass: from the blocks' sums of 32 bins
+// each, then those bins themselves, which a warp for each block fetches.  Every
+// warp goes through the sums by itself; one barrier.  The values before the
+// histogram's are in s.before_*.  s.bin is -1 where all bins stay below.
 __device__ __forceinline__ void find_bin(Shared& s, cg::cluster_group& cluster, int C, int rank, bool with_mass,
                                          bool counting, uint32_t want_count, uint64_t want_mass) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint64_t m[2] = {0, 0};
   uint32_t c[2] = {0, 0};
-  for (int o = 0; o < C; ++o)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      c[j] += s.group_count[o][2 * lane + j];
-      if (with_mass) m[j] += s.group_mass[o][2 * lane + j];
-    }
-  uint64_t pm = m[0] + m[1];
-  uint32_t pc = c[0] + c[1];
+  for (int o = 0; o < kMaxBlocks; ++o)
+    if (o < C) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t x = __shfl_up_sync(0xffffffffu, pm, o);
-    const uint32_t y = __shfl_up_sync(0xffffffffu, pc, o);
-    if (lane >= o) {
-      pm += x;
-      pc += y;
+      for (int j = 0; j < 2; ++j) {
+        c[j] += s.group_count[o][2 * lane + j];
+        if (with_mass) m[j] += s.group_mass[o][2 * lane + j];
+      }
     }
-  }
-  uint64_t base_m = s.before_mass;
-  uint32_t base_c = s.before_count;
+  uint64_t pm = m[0] + m[1], base_m = s.before_mass;
+  uint32_t pc = c[0] + c[1], base_c = s.before_count;
+  warp_scan(pm, pc);
   const uint32_t hit = __ballot_sync(0xffffffffu, counting ? base_c + pc >= want_count : base_m + pm >= want_mass);
-  if (!hit) {
-    if (lane == 0) s.bin = -1;
-    return;
-  }
-  const int from = __ffs(hit) - 1;
-  base_m += __shfl_sync(0xffffffffu, pm - m[0] - m[1], from);
-  base_c += __shfl_sync(0xffffffffu, pc - c[0] - c[1], from);
-  const uint64_t m0 = __shfl_sync(0xffffffffu, m[0], from);
-  const uint32_t c0 = __shfl_sync(0xffffffffu, c[0], from);
-  const bool second = counting ? base_c + c0 < want_count : base_m + m0 < want_mass;
-  if (second) {
-    base_m += m0;
-    base_c += c0;
-  }
-  const int bin = (2 * from + (second ? 1 : 0)) * kGroupBins + lane;
-  uint64_t bm = 0;
-  uint32_t bc = 0, offset = 0;
-  for (int o = 0; o < C; ++o) {
-    const Shared& of = *cluster.map_shared_rank(&s, o);
-    const uint32_t n = of.hist[0][bin];
-    if (o < rank) offset += n;
-    bc += n;
-    if (with_mass) bm += of.hist[1][bin] + ((uint64_t)of.hist[2][bin] << 15) + ((uint64_t)of.hist[3][bin] << 30);
-  }
-  pm = bm;
-  pc = bc;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t x = __shfl_up_sync(0xffffffffu, pm, o);
-    const uint32_t y = __shfl_up_sync(0xffffffffu, pc, o);
-    if (lane >= o) {
-      pm += x;
-      pc += y;
+  int first = -1;
+  if (hit) {
+    const int from = __ffs(hit) - 1;
+    base_m += __shfl_sync(0xffffffffu, pm - m[0] - m[1], from);
+    base_c += __shfl_sync(0xffffffffu, pc - c[0] - c[1], from);
+    const uint64_t m0 = __shfl_sync(0xffffffffu, m[0], from);
+    const uint32_t c0 = __shfl_sync(0xffffffffu, c[0], from);
+    const bool second = counting ? base_c + c0 < want_count : base_m + m0 < want_mass;
+    if (second) {
+      base_m += m0;
+      base_c += c0;
+    }
+    first = (2 * from + (second ? 1 : 0)) * kGroupBins;
+    if (warp < C) {
+      const Shared& of = *cluster.map_shared_rank(&s, warp);
+      const uint32_t n = of.hist[0][first + lane];
+      uint64_t x = 0;
+      if (with_mass)
+        x = of.hist[1][first + lane] + ((uint64_t)of.hist[2][first + lane] << 15) +
+            ((uint64_t)of.hist[3][first + lane] << 30);
+      s.fine_count[warp][lane] = n;
+      s.fine_mass[warp][lane] = x;
     }
   }
-  const uint32_t there = __ballot_sync(0xffffffffu, counting ? base_c + pc >= want_count : base_m + pm >= want_mass);
-  if (lane == __ffs(there) - 1) {
-    s.bin = bin;
-    s.before_mass = base_m + pm - bm;
-    s.before_count = base_c + pc - bc;
-    s.bin_mass = bm;
-    s.bin_count = bc;
-    s.offset = offset;
-    s.pushed = 0;
+  __syncthreads();
+  if (warp == 0) {
+    uint64_t bm = 0;
+    uint32_t bc = 0, offset = 0;
+#pragma unroll
+    for (int o = 0; o < kMaxBlocks; ++o)
+      if (o < C) {
+        if (o < rank) offset += s.fine_count[o][lane];
+        bc += s.fine_count[o][lane];
+        bm += s.fine_mass[o][lane];
+      }
+    pm = bm;
+    pc = bc;
+    warp_scan(pm, pc);
+    const uint32_t there = __ballot_sync(0xffffffffu, counting ? base_c + pc >= want_count : base_m + pm >= want_mass);
+    if (first < 0) {
+      if (lane == 0) s.bin = -1;
+    } else if (lane == __ffs(there) - 1) {
+      s.bin = first + lane;
+      s.before_mass = base_m + pm - bm;
+      s.before_count = base_c + pc - bc;
+      s.bin_mass = bm;
+      s.bin_count = bc;
+      s.offset = offset;
+      s.pushed = 0;
+    }
   }
+  __syncthreads();
 }
 
 template <class T, bool STAGED>
@@ -376,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   auto pair_of = [&](uint32_t key, int i) -> uint64_t { return ((uint64_t)key << 32) | (0xffffffffu - (uint32_t)(i0 + i)); };
 
   bool fresh = false;  // the histogram is that of all values
-  uint64_t limit_mass = 0;
+  uint64_t limit_mass = 0, want_mass = 0;
 #pragma unroll 1
   for (int pass = by_count ? 0 : 1; pass < (by_mass ? 2 : 1); ++pass) {
     const bool counting = pass == 0;
@@ -386,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       s.before_mass = 0;
       s.before_count = 0;
     }
+    __syncthreads();
 #pragma unroll 1
     for (bool first_level = true;; first_level = false) {
       if (!(first_level && fresh)) {
@@ -432,23 +459,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         cluster.sync();
         fresh = first_level;
       }
-      if (warp == 0) {
-        __syncwarp();
-        if (first_level && !counting) {
-          // the shortest run that reaches p of the mass: ceil(p * mass), of at least one value
-          uint64_t all = 0;
-          for (int o = 0; o < C; ++o) all += s.group_mass[o][lane] + s.group_mass[o][lane + 32];
+      if (first_level && !counting) {
+        // the shortest run that reaches p of the mass: ceil(p * mass), of at least one value
+        uint64_t all = limit_mass;
+        if (!all) {
+#pragma unroll
+          for (int o = 0; o < kMaxBlocks; ++o)
+            if (o < C) all += s.group_mass[o][lane] + s.group_mass[o][lane + 32];
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-          if (limit_mass) all = limit_mass;
-          const uint64_t frac = (uint64_t)((double)fmaxf(tp, 0.f) * 18446744073709551616.0);
-          const uint64_t want = __umul64hi(frac, all) + (frac * all != 0);
-          if (lane == 0) s.want_mass = want ? want : 1;
-          __syncwarp();
         }
-        find_bin(s, cluster, C, rank, by_mass, counting, (uint32_t)k, s.want_mass);
+        const uint64_t frac = fraction_of(fmaxf(tp, 0.f));
+        want_mass = max(1ull, (unsigned long long)(__umul64hi(frac, all) + (frac * all != 0)));
       }
-      __syncthreads();
+      find_bin(s, cluster, C, rank, by_mass, counting, (uint32_t)k, want_mass);
       const int found = s.bin;
       if (found < 0) break;  // fewer values with weight than that: nothing is cut
       const uint32_t in_bin = s.bin_count;
@@ -488,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
               m += s.list_mass[j];
               ++c;
             }
-          if (counting ? c + 1 == (uint32_t)k : m < s.want_mass && m + w >= s.want_mass) {
+          if (counting ? c + 1 == (uint32_t)k : m < want_mass && m + w >= want_mass) {
             s.cut = me;
             s.cut_mass = m + w;
           }
@@ -535,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         // one value, in_bin times: the index of the last that is needed
         const uint64_t each = s.bin_mass / in_bin;
         const uint32_t ties = counting ? (uint32_t)k - s.before_count
-                                       : (uint32_t)((s.want_mass - s.before_mass + each - 1) / each);
+                                       : (uint32_t)((want_mass - s.before_mass + each - 1) / each);
         const int seg = (n + kWarps - 1) / kWarps, end = min(n, (warp + 1) * seg);
         uint32_t c = 0;
         for (int i = warp * seg + lane; i < end; i += 32) c += key_of(at(i)) == key_low;
@@ -577,7 +601,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 
   // ---- the mass of what is kept, by warps' segments in order ----
   const float mp = p.min_p ? __ldg(p.min_p + row) : 0.f;
-  const uint64_t least = mp > 0.f ? (uint64_t)ceil(fmin((double)mp, 1.0) * 8796093022208.0) : 0;
+  uint64_t least = 0;  // ceil(min_p * 2^43)
+  if (mp >= 1.f) {
+    least = 1ull << kOne;
+  } else if (mp > 0.f) {
+    const uint64_t f = fraction_of(mp);
+    least = (f >> (64 - kOne)) + ((f & ((1ull << (64 - kOne)) - 1)) != 0);
+  }
   const uint32_t cut_key = (uint32_t)(cut >> 32);
   auto kept_weight = [&](int i) -> uint64_t {
     const float x = at(i);
@@ -604,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     total += s.mass[o];
   }
   const float u = fminf(fmaxf(__ldg(p.uniform + row), 0.f), 0.99999994f);  // a NaN counts as 0
-  const uint64_t target = __umul64hi((uint64_t)((double)u * 18446744073709551616.0), total);
+  const uint64_t target = __umul64hi(fraction_of(u), total);
   if (before <= target && target < before + all) {  // this block
     int w = 0;
     for (; w < kWarps - 1 && before + s.warp_mass[w] <= target; ++w) before += s.warp_mass[w];
@@ -658,7 +688,7 @@ tlq_status launch_one(const SampleParams& p, int rows, int blocks, size_t smem, 
 template <class T>
 tlq_status launch_as(SampleParams p, int rows, cudaStream_t stream) {
   int blocks = 1;
-  while (blocks < 8 && p.vocab > 4096 * blocks) blocks *= 2;
+  while (blocks < kMaxBlocks && p.vocab > 4096 * blocks) blocks *= 2;
   p.piece = (p.vocab + blocks - 1) / blocks;
   const size_t fixed = (sizeof(Shared) + 15) & ~size_t(15), staged = fixed + (size_t)p.piece * sizeof(T) + 16;
   return staged <= (size_t)kMaxSmem ? launch_one<T, true>(p, rows, blocks, staged, stream)

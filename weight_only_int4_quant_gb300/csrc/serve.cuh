@@ -302,8 +302,8 @@ struct SampleArgs {
 };
 tlq_status launch_sample(const SampleArgs& a, cudaStream_t stream);
 
-// Where the softmax's sums of each row go that is joined with others of the
-// same row afterwards: [tokens][q_heads] rows of O [D], and of m and l.
+// The softmax's sums of each row of a batch with a prefix: [tokens][q_heads] rows
+// of O [D], and of m and l; or, of a row that lies in parts, where these begin.
 struct KvRowSums {
   float* o;
   float2* ml;
@@ -311,6 +311,10 @@ struct KvRowSums {
 struct KvShared {
   KvRowSums own, prefix;
 };
+// (block that begins the row's item, -followers) in the place of (m, l): l is never negative.
+__device__ __forceinline__ float2 kv_row_in_parts(int block, int followers) {
+  return make_float2(__int_as_float(block), -(float)followers);
+}
 inline size_t kv_row_sums_bytes(long long rows, int head_dim) { return (size_t)rows * (head_dim + 2) * sizeof(float); }
 
 struct KvAttention {
@@ -332,7 +336,6 @@ struct KvJoinHeader {
   int row0;       // first (query, head) row of the item
   int rows;
   int head;       // key head
-  int prefix;     // the item is of the shared prefix
 };
 // The parts that one kernel leaves: two to a block, of the item it ends (0) and
 // of the one it begins (1).
@@ -362,12 +365,12 @@ size_t kv4_prefill_workspace(int head_dim);
 tlq_status launch_kv4_decode(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream);
 tlq_status launch_kv4_prefill(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream);
 tlq_status launch_kv4_join(const KvAttention& a, const KvJoin& few, const KvJoin& many, cudaStream_t stream);
-// The same three for a batch with a prefix: sums of rows go to a.shared, and
-// _merge puts the prefix's and a request's own together.
+// The same for a batch with a prefix: sums of rows go to a.shared, and _finish
+// puts a row's parts, the prefix's and its request's own, together.
 tlq_status launch_kv4_decode_shared(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream);
 tlq_status launch_kv4_prefill_shared(const KvAttention& a, int few_rows, void* ws, KvJoin* join, cudaStream_t stream);
-tlq_status launch_kv4_join_shared(const KvAttention& a, const KvJoin& few, const KvJoin& many, cudaStream_t stream);
-tlq_status launch_kv4_merge(const KvAttention& a, int few_rows, cudaStream_t stream);
+tlq_status launch_kv4_finish_shared(const KvAttention& a, int few_rows, const KvJoin& few, const KvJoin& many,
+                                    cudaStream_t stream);
 
 struct LoraArgs {
   const __half* x;

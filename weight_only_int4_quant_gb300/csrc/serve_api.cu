@@ -431,8 +431,7 @@ tlq_status tl_kv4_attention_prefix(const tl_kv4_cache* cache, const uint16_t* q,
   tlq_status ls = launch_kv4_decode_shared(a, few, at, &few_parts, s);
   if (ls == TLQ_OK && (long long)tokens * (q_heads / a.cache.heads) > few)
     ls = launch_kv4_prefill_shared(a, few, at + kv4_decode_workspace(d), &many_parts, s);
-  if (ls == TLQ_OK) ls = launch_kv4_join_shared(a, few_parts, many_parts, s);
-  return ls == TLQ_OK ? launch_kv4_merge(a, few, s) : ls;
+  return ls == TLQ_OK ? launch_kv4_finish_shared(a, few, few_parts, many_parts, s) : ls;
 }
 
 tlq_status tl_rope_table(const double* inv_freq, int64_t num_positions, int rot_dim, double scale, float* table,
