@@ -834,7 +834,7 @@ tlq_status tl_kv4_append_rope(const tl_kv4_cache* cache, const tl_rope* rope, co
  *   at which the running sum of the kept weights passes uniform times their
  *   sum; its log-probability is ln(w / that sum).  Weights below 2^-40 count as
  *   none.  They are held as whole numbers, 2^43 for the largest and each within
- *   about 2^-40 of it, so sums are exact whatever their order.
+ *   about 2^-39 of it, so sums are exact whatever their order.
  *
  *   logits       FP16 (fp16 = 1) or FP32 (0) [rows][vocab], row stride ld
  *                (elements); -infinity: a token that is not to be drawn.  A row

@@ -9,7 +9,7 @@
 // Which token that is depends on the last bits of long sums, so the weights are
 // whole numbers, 2^43 for the largest, and their sums exact: the same whatever
 // the order, and two rows differ only where the weights do.  A weight comes
-// within about 2^-40 of its value: the exponent in two FP32 numbers (x - max
+// within about 2^-39 of its value: the exponent in two FP32 numbers (x - max
 // exactly, times log2(e) / T), 2^(-j/256) from a table and a cubic for the rest.
 // FP64, the plain way, would take 30 times the arithmetic's time here (2
 // operations a clock and SM).
@@ -72,6 +72,8 @@ struct SampleParams {
   float* logprobs;
 };
 
+constexpr float kLn2 = 0.693147182f, kLn2Lo = -1.90465421e-9f;  // ln 2 in two FP32 numbers
+
 // log2(e) / T in two FP32 numbers.
 struct Exponent {
   float hi, lo;
@@ -85,29 +87,68 @@ __device__ __forceinline__ Exponent exponent_of(float t) {
   return e;
 }
 
-// exp((x - top) / T) * 2^43, or 0 below 2^-40.
-__device__ __forceinline__ uint64_t weight_of(float x, float top, Exponent e, const uint64_t* __restrict__ powers) {
-  const float d = __fsub_rn(x, top), back = __fsub_rn(d, x);
-  const float d_lo = __fadd_rn(__fsub_rn(x, __fsub_rn(d, back)), __fsub_rn(-top, back));
-  const float h = __fmul_rn(d, e.hi);
-  if (!(h >= -kOctaves)) return 0;
-  const float l = fmaf(d, e.hi, -h) + fmaf(d, e.lo, d_lo * e.hi);
-  // h = -k / 256 + r
-  const float kf = rintf(h * -256.0f);
-  const int k = (int)kf;
-  const float r = fmaf(kf, 1.0f / 256.0f, h);  // exact, |r| <= 2^-9
-  // z = 2^(r + l) - 1 in units of 2^-40: c1 r in two numbers, and the rest
-  const float c1 = 0.693147182f, c1_lo = -1.90465421e-9f, c2 = 0.240226507f, c3 = 0.0555041087f, c4 = 0.00961812911f;
-  const float zh = __fmul_rn(c1, r), rr = r + l;
-  const float zl = fmaf(c1, r, -zh) + fmaf(c1_lo, r, c1 * l) + rr * rr * fmaf(rr, fmaf(rr, c4, c3), c2);
-  const float a = __fadd_rn(__fmul_rn(zh, 2147483648.0f), 12582912.0f);  // units of 2^-31, a whole number
-  const float rest = __fsub_rn(__fmul_rn(zh, 2147483648.0f), __fsub_rn(a, 12582912.0f));
-  const float b = __fadd_rn(__fmul_rn(fmaf(zl, 2147483648.0f, rest), 512.0f), 12582912.0f);
-  const int z = (__float_as_int(a) - 0x4B400000) * 512 + (__float_as_int(b) - 0x4B400000);
-  const uint64_t power = powers[k & 255];
-  const int n = k >> 8;
-  const uint64_t v = power + (uint64_t)(((long long)((power + 2048) >> 12) * z + (1 << 27)) >> 28);
-  return (v + ((1ull << n) >> 1)) >> n;
+struct Row {
+  float top;
+  Exponent e;
+};
+
+// -h = (top - x) / T * log2(e), rounded: which bin x falls in goes by it alone.
+__device__ __forceinline__ float octaves_of(const Row& r, float x) { return __fmul_rn(__fsub_rn(x, r.top), -r.e.hi); }
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it leaves a whole number's bits
+constexpr int kMagicBits = 0x4B400000;
+// 64 bins to an octave, the last one up to kOctaves; kBins: no weight.
+__device__ __forceinline__ int bin_of_k(int k) { return min(k >> 2, kBins - 1); }
+__device__ __forceinline__ int first_bin(const Row& r, float x) {
+  const float o = octaves_of(r, x);
+  return o <= kOctaves ? bin_of_k(__float_as_int(fmaf(o, 256.0f, kMagic)) - kMagicBits) : kBins;
+}
+
+__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+
+// exp((x - top) / T) * 2^43 of two values, 0 below 2^-40, and their bins.  Two at
+// a time: the FP32 part is in packed operations (none of them a product that
+// goes into a plain sum, which the compiler would join).  The lowest bit is set
+// instead of rounding the last shift.
+__device__ __forceinline__ void weights_of(float x0, float x1, const Row& r, const uint64_t* __restrict__ powers,
+                                           uint64_t (&w)[2], int (&bin)[2]) {
+  // x - top = d + d_lo exactly (Knuth's two-sum)
+  const float2 x = make_float2(x0, x1), neg_top = pair(-r.top), minus = pair(-1.0f);
+  const float2 d = add2(x, neg_top), back = fma2(x, minus, d);  // d - x
+  const float2 d_lo = add2(add2(x, fma2(d, minus, back)), fma2(back, minus, neg_top));
+  // -h, and the rest l:  (x - top) log2(e) / T = h + l
+  const float2 e = pair(r.e.hi), nh = mul2(d, pair(-r.e.hi));
+  const float2 l = fma2(d_lo, e, fma2(d, pair(r.e.lo), fma2(d, e, nh)));
+  // h = -k / 256 - q
+  const float2 kb = fma2(nh, pair(256.0f), pair(kMagic));
+  const float2 q = fma2(add2(kb, pair(-kMagic)), pair(-1.0f / 256.0f), nh);  // exact, |q| <= 2^-9
+  // z = 2^(l - q) - 1: -c1 q in two numbers, and what is below 2^-17.  In units of
+  // 2^-31 the first is rounded to a whole number, all that is left to 1 / 256 of one.
+  const float2 nzh = mul2(q, pair(kLn2)), rr = fma2(q, minus, l);
+  float2 zl = fma2(q, pair(-kLn2), nzh);
+  zl = fma2(l, pair(kLn2), fma2(q, pair(-kLn2Lo), zl));
+  zl = fma2(mul2(rr, rr), fma2(rr, fma2(rr, pair(0.00961812911f), pair(0.0555041087f)), pair(0.240226507f)), zl);
+  const float2 up = pair(2147483648.0f);
+  const float2 a = fma2(nzh, pair(-2147483648.0f), pair(kMagic));
+  const float2 rest = fma2(nzh, pair(-2147483648.0f), fma2(a, minus, pair(kMagic)));
+  const float2 b = fma2(fma2(zl, up, rest), pair(256.0f), pair(kMagic));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = __float_as_int(i ? kb.y : kb.x) - kMagicBits;
+    const int z = __float_as_int(i ? a.y : a.x) * 256 + __float_as_int(i ? b.y : b.x) -
+                  (int)((unsigned)kMagicBits * 257u);  // units of 2^-39
+    const uint64_t power = powers[k & 255];
+    const uint64_t v = power + (uint64_t)(((long long)(int)(power >> 13) * z) >> 26);
+    const bool some = (i ? nh.y : nh.x) <= kOctaves;
+    w[i] = some ? (v >> (k >> 8)) | 1ull : 0;
+    bin[i] = some ? bin_of_k(k) : kBins;
+  }
+}
+
+__device__ __forceinline__ uint64_t weight_of(float x, const Row& r, const uint64_t* __restrict__ powers) {
+  uint64_t w[2];
+  int bin[2];
+  weights_of(x, x, r, powers, w, bin);
+  return w[0];
 }
 
 // x in [0, 1) as a fraction of 2^64 (bits below that are cut off).
@@ -156,17 +197,6 @@ struct Shared {
 
 __device__ __forceinline__ float value_of_key(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
-}
-
-struct Row {
-  float top;
-  Exponent e;
-  float scale;  // bins of an octave
-};
-
-__device__ __forceinline__ int first_bin(const Row& r, float x) {  // kBins: below every weight
-  const float t = (r.top - x) * r.scale;
-  return t < (float)kBins ? (int)t : kBins;
 }
 
 template <class T>
@@ -392,7 +422,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   Row r;
   r.top = top;
   r.e = exponent_of(t);
-  r.scale = fminf(r.e.hi, 1e30f) * ((float)kBins / kOctaves);
   const int k = p.top_k ? __ldg(p.top_k + row) : 0;
   const float tp = p.top_p ? __ldg(p.top_p + row) : 1.0f;
   const bool by_count = k > 0 && k < p.vocab, by_mass = tp < 1.0f;
@@ -420,21 +449,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           for (int i = tid; i < 4 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
           __syncthreads();
         }
-#pragma unroll 2
-        for (int i = tid; i < n; i += kThreads) {
-          const float x = at(i);
-          int b = first_bin(r, x);
-          if (!first_level) {
-            const uint32_t key = key_of(x);
-            b = b == bin && key >= key_low && key <= key_high ? (int)((key_high - key) >> shift) : kBins;
+        for (int i = tid; i < n; i += 2 * kThreads) {
+          const float x[2] = {at(i), i + kThreads < n ? at(i + kThreads) : -INFINITY};
+          uint64_t w[2] = {0, 0};
+          int bins[2];
+          if (by_mass) {
+            weights_of(x[0], x[1], r, s.powers, w, bins);
+          } else {
+            bins[0] = first_bin(r, x[0]);
+            bins[1] = first_bin(r, x[1]);
           }
-          if (b < kBins) {
-            atomicAdd(&s.hist[0][b], 1u);
-            if (by_mass) {
-              const uint64_t w = weight_of(x, r.top, r.e, s.powers);
-              atomicAdd(&s.hist[1][b], (uint32_t)w & 0x7fffu);
-              atomicAdd(&s.hist[2][b], (uint32_t)(w >> 15) & 0x7fffu);
-              atomicAdd(&s.hist[3][b], (uint32_t)(w >> 30));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            int b = bins[j];
+            if (!first_level) {
+              const uint32_t key = key_of(x[j]);
+              b = b == bin && key >= key_low && key <= key_high ? (int)((key_high - key) >> shift) : kBins;
+            }
+            if (b < kBins) {
+              atomicAdd(&s.hist[0][b], 1u);
+              if (by_mass) {
+                atomicAdd(&s.hist[1][b], (uint32_t)w[j] & 0x7fffu);
+                atomicAdd(&s.hist[2][b], (uint32_t)(w[j] >> 15) & 0x7fffu);
+                if (w[j] >> 30) atomicAdd(&s.hist[3][b], (uint32_t)(w[j] >> 30));
+              }
             }
           }
         }
@@ -500,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const uint64_t me = tid < (int)in_bin ? list[tid] : 0;
         uint64_t w = 0;
         if (tid < (int)in_bin) {
-          w = weight_of(value_of_key((uint32_t)(me >> 32)), r.top, r.e, s.powers);
+          w = weight_of(value_of_key((uint32_t)(me >> 32)), r, s.powers);
           s.list_mass[tid] = w;
         }
         __syncthreads();
@@ -609,17 +647,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     least = (f >> (64 - kOne)) + ((f & ((1ull << (64 - kOne)) - 1)) != 0);
   }
   const uint32_t cut_key = (uint32_t)(cut >> 32);
+  auto kept = [&](float x, int i) {
+    const uint32_t key = key_of(x);
+    return key > cut_key || (key == cut_key && pair_of(key, i) >= cut);
+  };
   auto kept_weight = [&](int i) -> uint64_t {
     const float x = at(i);
-    const uint32_t key = key_of(x);
-    if (key < cut_key || (key == cut_key && pair_of(key, i) < cut)) return 0;
-    const uint64_t w = weight_of(x, r.top, r.e, s.powers);
+    const uint64_t w = kept(x, i) ? weight_of(x, r, s.powers) : 0;
     return w >= least ? w : 0;
   };
   const int seg = (n + kWarps - 1) / kWarps;
   uint64_t m = 0;
-#pragma unroll 2
-  for (int i = warp * seg + lane; i < min(n, (warp + 1) * seg); i += 32) m += kept_weight(i);
+  for (int i = warp * seg + lane; i < min(n, (warp + 1) * seg); i += 64) {
+    float x[2] = {at(i), -INFINITY};
+    const bool two = i + 32 < min(n, (warp + 1) * seg);
+    if (two) x[1] = at(i + 32);
+    const bool keep[2] = {kept(x[0], i), two && kept(x[1], i + 32)};
+    if (keep[0] || keep[1]) {
+      uint64_t w[2];
+      int bins[2];
+      weights_of(x[0], x[1], r, s.powers, w, bins);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) m += keep[j] && w[j] >= least ? w[j] : 0;
+    }
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
   if (lane == 0) s.warp_mass[warp] = m;
@@ -655,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           if (p.logprobs) {
             // (x - top) / T - ln(sum of weights against the largest)
             const float d = at(i) - r.top, h = __fmul_rn(d, r.e.hi), l = fmaf(d, r.e.hi, -h) + d * r.e.lo;
-            const float rest = (float)(total - (1ull << kOne)) * 1.13686838e-13f;  // 2^-43
+            const float rest = (float)(total - (1ull << kOne)) * 1.13686838e-13f;  // 2^-43: the largest is among them
             p.logprobs[row] = (h + l) * 0.693147182f - log1pf(rest);
           }
           break;
