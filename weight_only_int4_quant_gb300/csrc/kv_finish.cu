@@ -15,6 +15,7 @@ namespace tlq {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kBatch = 8;  // parts whose loads are under way together
 
 // One row's parts on one side.
 struct RowParts {
@@ -63,26 +64,43 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const KvBatch batch, c
     const KvJoin &jo = own_many ? many : few, &jp = prefix_many ? many : few;
     const RowParts parts[2] = {row_parts<D>(shared.own, at, jo, (t * share + g) % jo.rows),
                                row_parts<D>(shared.prefix, at, jp, ((r.q0 + t) * share + g) % jp.rows)};
-    float m = -INFINITY;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-#pragma unroll 4
-      for (int i = 0; i < parts[s].n; ++i) m = fmaxf(m, parts[s].m[parts[s].at(i)]);
-    }
-    float l = 0.f, sum[8] = {};
+    float m = -INFINITY, l = 0.f, sum[8] = {};
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       float acc[8] = {};
-#pragma unroll 4
-      for (int i = 0; i < parts[s].n; ++i) {
-        const size_t o = parts[s].at(i);
-        const float w = exp2f(parts[s].m[o] - m);
-        const float4* src = reinterpret_cast<const float4*>(parts[s].o + o + ch);
-        const float4 a = src[0], b = src[1];
-        l = fmaf(w, parts[s].l[o], l);
-        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      // kBatch parts under way at a time, the sums moved to the greatest m so far
+      for (int i0 = 0; i0 < parts[s].n; i0 += kBatch) {
+        float pm[kBatch], pl[kBatch];
+        float4 a[kBatch], b[kBatch];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, x[k], acc[k]);
+        for (int i = 0; i < kBatch; ++i) {
+          const bool on = i0 + i < parts[s].n;
+          const size_t o = parts[s].at(on ? i0 + i : 0);
+          pm[i] = on ? parts[s].m[o] : -INFINITY;
+          pl[i] = on ? parts[s].l[o] : 0.f;
+          const float4* src = reinterpret_cast<const float4*>(parts[s].o + o + ch);
+          a[i] = on ? src[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+          b[i] = on ? src[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float next = m;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) next = fmaxf(next, pm[i]);
+        const float moved = exp2f(m - next);  // 0 before the first
+        m = next;
+        l *= moved;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          acc[k] *= moved;
+          sum[k] *= moved;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const float w = exp2f(pm[i] - m);
+          l = fmaf(w, pl[i], l);
+          const float x[8] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, x[k], acc[k]);
+        }
       }
       // the tensor-core kernel's channels lie as 0 4 1 5 2 6 3 7
       const bool permuted = s ? prefix_many : own_many;

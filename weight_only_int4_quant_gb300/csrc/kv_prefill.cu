@@ -386,8 +386,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   const int requests = kv_requests<kShared>(p.batch);
   const bool small = requests <= kThreads;
   if (small) {
-    for (int i = warp; i < requests; i += kThreads / 32) {
-      long long v = lane_units(kv_request_or_prefix<kShared>(p.batch, p.cache.page, i), lane, 32);
+    // short ones a thread to a request, those of many row tiles a warp each
+    long long v = 0;
+    bool many = false;
+    if (tid < requests) {
+      const KvRequest r = kv_request_or_prefix<kShared>(p.batch, p.cache.page, tid);
+      many = many_rows(p, r) > 4 * kItemRows;
+      if (!many) v = lane_units(r, 0, 1);
+      request_units[tid] = v;
+    }
+    uint32_t left = __ballot_sync(0xffffffffu, many);
+    while (left) {
+      const int i = (tid & ~31) + __ffs(left) - 1;
+      left &= left - 1;
+      v = lane_units(kv_request_or_prefix<kShared>(p.batch, p.cache.page, i), lane, 32);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if (lane == 0) request_units[i] = v;

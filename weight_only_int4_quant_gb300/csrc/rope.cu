@@ -115,12 +115,18 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
   // shuffles: rows past the end do the last one again.
   uint4 raw[2];
   uint32_t next_t;
+  int next_at[3] = {0, 0, 0};
+  long long next_slot = -1;
   auto fetch = [&](uint32_t row) {
     row = min(row, part.rows - 1);
     next_t = (uint32_t)divide((int)row, part.heads);
     const uint4* src = reinterpret_cast<const uint4*>(part.x + next_t * part.ld + (row - next_t * part.heads.d) * D);
     raw[0] = __ldg(src + ch.x);
     raw[1] = __ldg(src + ch.y);
+#pragma unroll
+    for (int a = 0; a < 3; ++a)
+      if (a < p.rope.axes) next_at[a] = __ldg(p.positions + a * p.ld_positions + next_t);
+    if (part.out == nullptr) next_slot = __ldg(p.slots + next_t);
   };
   fetch(first);
   uint4 wraw[2];
@@ -136,17 +142,11 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
   for (int u = 0; u < p.turns; ++u) {
     const uint32_t row = min(first + u, part.rows - 1), t = next_t;
     const int head = (int)(row - t * part.heads.d);
+    const long long slot = next_slot;
     if (p.rope.rot && t != held) {
       held = t;
-      int at[3] = {0, 0, 0};
-      there = true;
-#pragma unroll
-      for (int a = 0; a < 3; ++a)
-        if (a < p.rope.axes) {
-          at[a] = __ldg(p.positions + a * p.ld_positions + t);
-          there &= at[a] >= 0;
-        }
-      if (turns && there) turn_of(p.rope, l, at, cs);
+      there = next_at[0] >= 0 && next_at[1] >= 0 && next_at[2] >= 0;
+      if (turns && there) turn_of(p.rope, l, next_at, cs);
     }
     float2 x[2][4];
 #pragma unroll
@@ -255,7 +255,6 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
           word[k] = code_word_by_division(make_float4(a.x, a.y, b.x, b.y), make_float4(c.x, c.y, d.x, d.y), g.s, g.b);
         }
       }
-      const long long slot = __ldg(p.slots + t);
       if (mine && in_cache(p.cache, slot)) {
         const CodeRow out = code_row<D>(p.cache, slot, head, kind - 1);
         uint32_t* codes = reinterpret_cast<uint32_t*>(out.codes);
