@@ -44,6 +44,7 @@ struct RopeParams {
   long long ld_positions;
   Part part[3];  // queries, keys, values
   float eps, inv_d;
+  float one;  // 1: a sum as one * a + b is not joined with the products before it to one rounding
   KvCache cache;
   const long long* slots;
   int turns;  // rows of a lane
@@ -70,7 +71,7 @@ __device__ __forceinline__ float chunk_squares(const float2 (&x)[4]) {
 
 // cos and sin of a lane's pairs 8 l .. 8 l + 7: one piece of one row where they
 // are all of one axis; NaN past the table's end.
-__device__ __forceinline__ void turn_of(const RopeTable& r, int l, const int (&at)[3], float2 (&cs)[8]) {
+__device__ __forceinline__ void turn_of(const RopeTable& r, int l, const int (&at)[3], float2 (&co)[4], float2 (&si)[4]) {
   const int half = r.rot / 2, first = 8 * l, last = first + 7;
   auto axis = [&](int pair) { return pair < r.end0 ? at[0] : pair < r.end1 ? at[1] : at[2]; };
   if ((last < r.end0) | (first >= r.end0 && last < r.end1) | (first >= r.end1)) {
@@ -80,23 +81,25 @@ __device__ __forceinline__ void turn_of(const RopeTable& r, int l, const int (&a
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float4 v = __ldg(src + j);
-        cs[2 * j] = make_float2(v.x, v.y);
-        cs[2 * j + 1] = make_float2(v.z, v.w);
+        co[j] = make_float2(v.x, v.z);
+        si[j] = make_float2(v.y, v.w);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) cs[j] = make_float2(NAN, NAN);
+      for (int j = 0; j < 4; ++j) co[j] = si[j] = make_float2(NAN, NAN);
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int pos = axis(first + j);
-      cs[j] = pos < r.positions ? __ldg(r.table + (long long)pos * half + first + j) : make_float2(NAN, NAN);
+      const float2 v = pos < r.positions ? __ldg(r.table + (long long)pos * half + first + j) : make_float2(NAN, NAN);
+      (j & 1 ? co[j / 2].y : co[j / 2].x) = v.x;
+      (j & 1 ? si[j / 2].y : si[j / 2].x) = v.y;
     }
   }
 }
 
-template <int D>
+template <int D, bool CACHE>
 __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopeParams p) {
   constexpr int L = D / 16;  // lanes of a row
   pdl_launch_dependents();
@@ -115,18 +118,12 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
   // shuffles: rows past the end do the last one again.
   uint4 raw[2];
   uint32_t next_t;
-  int next_at[3] = {0, 0, 0};
-  long long next_slot = -1;
   auto fetch = [&](uint32_t row) {
     row = min(row, part.rows - 1);
     next_t = (uint32_t)divide((int)row, part.heads);
     const uint4* src = reinterpret_cast<const uint4*>(part.x + next_t * part.ld + (row - next_t * part.heads.d) * D);
     raw[0] = __ldg(src + ch.x);
     raw[1] = __ldg(src + ch.y);
-#pragma unroll
-    for (int a = 0; a < 3; ++a)
-      if (a < p.rope.axes) next_at[a] = __ldg(p.positions + a * p.ld_positions + next_t);
-    if (part.out == nullptr) next_slot = __ldg(p.slots + next_t);
   };
   fetch(first);
   uint4 wraw[2];
@@ -135,18 +132,25 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
     wraw[0] = __ldg(reinterpret_cast<const uint4*>(part.weight) + ch.x);
     wraw[1] = __ldg(reinterpret_cast<const uint4*>(part.weight) + ch.y);
   }
-  float2 cs[8];  // of the token at hand
+  float2 co[4], si[4];  // of the token at hand: pairs 2 j, 2 j + 1
+  const float2 one = make_float2(p.one, p.one), minus_one = make_float2(-p.one, -p.one);
   bool there = true;
   uint32_t held = 0xffffffffu;
 #pragma unroll 1
   for (int u = 0; u < p.turns; ++u) {
     const uint32_t row = min(first + u, part.rows - 1), t = next_t;
     const int head = (int)(row - t * part.heads.d);
-    const long long slot = next_slot;
     if (p.rope.rot && t != held) {
       held = t;
-      there = next_at[0] >= 0 && next_at[1] >= 0 && next_at[2] >= 0;
-      if (turns && there) turn_of(p.rope, l, next_at, cs);
+      int at[3] = {0, 0, 0};
+      there = true;
+#pragma unroll
+      for (int a = 0; a < 3; ++a)
+        if (a < p.rope.axes) {
+          at[a] = __ldg(p.positions + a * p.ld_positions + t);
+          there &= at[a] >= 0;
+        }
+      if (turns && there) turn_of(p.rope, l, at, co, si);
     }
     float2 x[2][4];
 #pragma unroll
@@ -186,19 +190,16 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 v = x[k][i], c = cs[4 * k + i];
-            x[k][i].x = __fsub_rn(__fmul_rn(v.x, c.x), __fmul_rn(v.y, c.y));
-            x[k][i].y = __fadd_rn(__fmul_rn(v.y, c.x), __fmul_rn(v.x, c.y));
+            const float2 v = x[k][i], cj = co[2 * k + i / 2], sj = si[2 * k + i / 2];
+            const float c = i & 1 ? cj.y : cj.x, n = i & 1 ? sj.y : sj.x;
+            x[k][i] = fma2(mul2(make_float2(v.y, v.x), make_float2(-n, n)), one, mul2(v, make_float2(c, c)));
           }
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 a = x[0][i], b = x[1][i];
-          const float2 c = make_float2(cs[2 * i].x, cs[2 * i + 1].x), s = make_float2(cs[2 * i].y, cs[2 * i + 1].y);
-          // sums by scalar operations: the compiler joins a packed product and sum to one rounding
-          const float2 ac = mul2(a, c), bs = mul2(b, s), bc = mul2(b, c), as = mul2(a, s);
-          x[0][i] = make_float2(__fsub_rn(ac.x, bs.x), __fsub_rn(ac.y, bs.y));
-          x[1][i] = make_float2(__fadd_rn(bc.x, as.x), __fadd_rn(bc.y, as.y));
+          const float2 a = x[0][i], b = x[1][i], c = co[i], s = si[i];
+          x[0][i] = fma2(mul2(b, s), minus_one, mul2(a, c));
+          x[1][i] = fma2(mul2(a, s), one, mul2(b, c));
         }
       }
     }
@@ -208,13 +209,13 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[k][i] = __floats2half2_rn(x[k][i].x, x[k][i].y);
     const bool mine = first + u < part.rows && there;
-    if (part.out != nullptr) {
+    if (!CACHE || part.out != nullptr) {
       if (mine) {
         uint4* dst = reinterpret_cast<uint4*>(part.out + t * part.ldo + head * D);
 #pragma unroll
         for (int k = 0; k < 2; ++k) dst[k ? ch.y : ch.x] = *reinterpret_cast<const uint4*>(h[k]);
       }
-    } else if constexpr (D <= 128) {
+    } else if constexpr (CACHE) {
       // least and greatest value of the row's first and second group of channels (of one group: of each half)
       const __half inf = __ushort_as_half((unsigned short)0x7C00), ninf = __ushort_as_half((unsigned short)0xFC00);
       __half2 lo2 = __half2half2(inf), hi2 = __half2half2(ninf);
@@ -255,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
           word[k] = code_word_by_division(make_float4(a.x, a.y, b.x, b.y), make_float4(c.x, c.y, d.x, d.y), g.s, g.b);
         }
       }
+      const long long slot = __ldg(p.slots + t);
       if (mine && in_cache(p.cache, slot)) {
         const CodeRow out = code_row<D>(p.cache, slot, head, kind - 1);
         uint32_t* codes = reinterpret_cast<uint32_t*>(out.codes);
@@ -282,7 +284,7 @@ __global__ void table_kernel(const double* __restrict__ freq, float2* __restrict
   }
 }
 
-template <int D>
+template <int D, bool CACHE>
 tlq_status launch_rows(RopeParams& p, cudaStream_t stream) {
   constexpr uint32_t groups = kThreads / (D / 16);  // rows of a block at a time
   long long rows = 0;
@@ -305,7 +307,7 @@ tlq_status launch_rows(RopeParams& p, cudaStream_t stream) {
   at.val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = &at;
   lc.numAttrs = pdl_enabled() ? 1 : 0;
-  return cuda_error(cudaLaunchKernelEx(&lc, rope_kernel<D>, p), "rope: launch");
+  return cuda_error(cudaLaunchKernelEx(&lc, rope_kernel<D, CACHE>, p), "rope: launch");
 }
 
 }  // namespace
@@ -325,10 +327,13 @@ tlq_status launch_rope(const RopeArgs& a, cudaStream_t stream) {
   }
   p.eps = a.eps;
   p.inv_d = 1.0f / (float)a.head_dim;
+  p.one = 1.0f;
   p.cache = a.cache;
   p.slots = a.slots;
-  return a.head_dim == 64 ? launch_rows<64>(p, stream)
-                          : a.head_dim == 128 ? launch_rows<128>(p, stream) : launch_rows<256>(p, stream);
+  if (a.slots != nullptr) return a.head_dim == 64 ? launch_rows<64, true>(p, stream) : launch_rows<128, true>(p, stream);
+  return a.head_dim == 64    ? launch_rows<64, false>(p, stream)
+         : a.head_dim == 128 ? launch_rows<128, false>(p, stream)
+                             : launch_rows<256, false>(p, stream);
 }
 
 tlq_status launch_rope_table(const double* freq, float* table, long long positions, int half, double scale,
