@@ -96,21 +96,26 @@ struct Row {
 __device__ __forceinline__ float octaves_of(const Row& r, float x) { return __fmul_rn(__fsub_rn(x, r.top), -r.e.hi); }
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it leaves a whole number's bits
 constexpr int kMagicBits = 0x4B400000;
-// 64 bins to an octave, the last one up to kOctaves; kBins: no weight.
-__device__ __forceinline__ int bin_of_k(int k) { return min(k >> 2, kBins - 1); }
+// A value's k: 256ths of an octave below the greatest; kNoStep: no weight.  64 bins
+// to an octave, the last one up to kOctaves; kBins: no weight.
+constexpr int kNoStep = 1 << 20;
+__device__ __forceinline__ int bin_of_k(int k) { return k == kNoStep ? kBins : min(k >> 2, kBins - 1); }
 __device__ __forceinline__ int first_bin(const Row& r, float x) {
   const float o = octaves_of(r, x);
-  return o <= kOctaves ? bin_of_k(__float_as_int(fmaf(o, 256.0f, kMagic)) - kMagicBits) : kBins;
+  return o <= kOctaves ? min((__float_as_int(fmaf(o, 256.0f, kMagic)) - kMagicBits) >> 2, kBins - 1) : kBins;
 }
+
+// The weight in the middle of a bin, the largest being 1.
+__device__ __forceinline__ float middle_of(int bin) { return exp2f(((float)bin + 0.5f) * (-1.0f / 64.0f)); }
 
 __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 
-// exp((x - top) / T) * 2^43 of two values, 0 below 2^-40, and their bins.  Two at
+// exp((x - top) / T) * 2^43 of two values, 0 below 2^-40, and their k.  Two at
 // a time: the FP32 part is in packed operations (none of them a product that
 // goes into a plain sum, which the compiler would join).  The lowest bit is set
 // instead of rounding the last shift.
 __device__ __forceinline__ void weights_of(float x0, float x1, const Row& r, const uint64_t* __restrict__ powers,
-                                           uint64_t (&w)[2], int (&bin)[2]) {
+                                           uint64_t (&w)[2], int (&step)[2]) {
   // x - top = d + d_lo exactly (Knuth's two-sum)
   const float2 x = make_float2(x0, x1), neg_top = pair(-r.top), minus = pair(-1.0f);
   const float2 d = add2(x, neg_top), back = fma2(x, minus, d);  // d - x
@@ -140,14 +145,14 @@ __device__ __forceinline__ void weights_of(float x0, float x1, const Row& r, con
     const uint64_t v = power + (uint64_t)(((long long)(int)(power >> 13) * z) >> 26);
     const bool some = (i ? nh.y : nh.x) <= kOctaves;
     w[i] = some ? (v >> (k >> 8)) | 1ull : 0;
-    bin[i] = some ? bin_of_k(k) : kBins;
+    step[i] = some ? k : kNoStep;
   }
 }
 
 __device__ __forceinline__ uint64_t weight_of(float x, const Row& r, const uint64_t* __restrict__ powers) {
   uint64_t w[2];
-  int bin[2];
-  weights_of(x, x, r, powers, w, bin);
+  int step[2];
+  weights_of(x, x, r, powers, w, step);
   return w[0];
 }
 
@@ -168,12 +173,18 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 constexpr int kGroups = 64, kGroupBins = kBins / kGroups;
 constexpr int kList = 512;  // candidates for a cut that are ranked one by one
 static_assert(kGroupBins == 32, "a lane to a bin");
+static_assert(kWarps >= kMaxBlocks && kList <= kThreads, "a warp to a block, a thread to a candidate");
+constexpr int kHeavyGroups = 12;  // groups whose weights are added up exactly beside the counts: 2^-6 and more
 
 // The state of a block; other blocks of its cluster write what is marked.
 struct Shared {
   uint32_t hist[4][kBins];               // counts, limbs (read by others)
   uint64_t powers[256];
   uint64_t list[2][kList];               // candidates, of the cut by count and by mass (written by others)
+  uint64_t local[kList];                 // this block's candidates
+  uint64_t sum[kMaxBlocks], above[kMaxBlocks], heavy[kMaxBlocks];  // by block (written by others)
+  float group_about[kMaxBlocks][kGroups];                          // likewise
+  uint32_t merged, base[kMaxBlocks];     // candidates of the cluster (counted by others), where this block's go
   uint64_t list_mass[kList];             // their weights
   uint64_t group_mass[kMaxBlocks][kGroups];   // by block (written by others)
   uint32_t group_count[kMaxBlocks][kGroups];  // likewise
@@ -183,7 +194,7 @@ struct Shared {
   uint32_t count[8], low[8], high[kMaxBlocks];    // likewise
   float top[kMaxBlocks];                          // likewise
   int top_at[8], bad[kMaxBlocks];                 // likewise
-  uint64_t warp_mass[kWarps];
+  uint64_t warp_mass[kWarps], warp_other[kWarps];
   uint32_t warp_count[kWarps];
   float warp_top[kWarps];
   int warp_at[kWarps], warp_bad[kWarps];
@@ -317,6 +328,125 @@ __device__ __forceinline__ void find_bin(Shared& s, cg::cluster_group& cluster, 
   __syncthreads();
 }
 
+// Sums over the block of up to two numbers; every thread gets them.
+__device__ __forceinline__ void block_sums(Shared& s, uint64_t& a, uint64_t& b) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) {
+    s.warp_mass[threadIdx.x >> 5] = a;
+    s.warp_other[threadIdx.x >> 5] = b;
+  }
+  __syncthreads();
+  a = b = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    a += s.warp_mass[w];
+    b += s.warp_other[w];
+  }
+}
+
+// ceil(p * mass), of at least one value.
+__device__ __forceinline__ uint64_t share_of(float p, uint64_t mass) {
+  const uint64_t frac = fraction_of(fmaxf(p, 0.f));
+  return max(1ull, (unsigned long long)(__umul64hi(frac, mass) + (frac * mass != 0)));
+}
+
+// About where the mass reaches p of the whole, from the counts: weights count as
+// those of their bins' middles, the heaviest groups' exactly.  The same in every
+// block.  upto: values of that bin's group, the groups before it and the one after.
+struct About {
+  int k, around;  // around: how many k on either side to look at (-1: too many values lie there)
+  int bin;
+  uint32_t upto;
+};
+__device__ __forceinline__ About find_about(Shared& s, cg::cluster_group& cluster, int C, float p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float a[2] = {0.f, 0.f};
+  uint32_t c[2] = {0, 0};
+  uint64_t heavy = 0;
+#pragma unroll
+  for (int o = 0; o < kMaxBlocks; ++o)
+    if (o < C) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        a[j] += s.group_about[o][2 * lane + j];
+        c[j] += s.group_count[o][2 * lane + j];
+      }
+      heavy += s.heavy[o];
+    }
+  // the exact sum of the heavy groups in the place of the estimate
+  float estimate = lane < kHeavyGroups / 2 ? a[0] + a[1] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) estimate += __shfl_xor_sync(0xffffffffu, estimate, o);
+  if (lane < kHeavyGroups / 2) {
+    const float f = (float)heavy * 1.13686838e-13f / estimate;  // 2^-43; the largest value is among them
+    a[0] *= f;
+    a[1] *= f;
+  }
+  float sum = a[0] + a[1];
+  uint32_t count = c[0] + c[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float x = __shfl_up_sync(0xffffffffu, sum, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, count, o);
+    if (lane >= o) {
+      sum += x;
+      count += y;
+    }
+  }
+  const float want = p * __shfl_sync(0xffffffffu, sum, 31);
+  const uint32_t hit = __ballot_sync(0xffffffffu, sum >= want) | 0x80000000u;
+  const int from = __ffs(hit) - 1;
+  const float before = __shfl_sync(0xffffffffu, sum - a[0] - a[1], from), first = __shfl_sync(0xffffffffu, a[0], from);
+  const bool second = before + first < want;
+  const int group = 2 * from + (second ? 1 : 0);
+  // values up to the group after it
+  const uint32_t through = __shfl_sync(0xffffffffu, count, from);
+  const uint32_t next = __shfl_sync(0xffffffffu, c[0], min(from + 1, 31));
+  const uint32_t upto = second ? through + (from < 31 ? next : 0) : through;
+  const float scale = group < kHeavyGroups ? (float)heavy * 1.13686838e-13f / estimate : 1.0f;
+  if (warp < C) s.fine_count[warp][lane] = cluster.map_shared_rank(&s, warp)->hist[0][group * kGroupBins + lane];
+  __syncthreads();
+  uint32_t n = 0;
+#pragma unroll
+  for (int o = 0; o < kMaxBlocks; ++o)
+    if (o < C) n += s.fine_count[o][lane];
+  float m = (float)n * middle_of(group * kGroupBins + lane) * scale;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float x = __shfl_up_sync(0xffffffffu, m, o);
+    if (lane >= o) m += x;
+  }
+  const float at = before + (second ? first : 0.f) + m;
+  const uint32_t there = __ballot_sync(0xffffffffu, at >= want) | 0x80000000u;
+  const int lane_of = __ffs(there) - 1, bin = group * kGroupBins + lane_of;
+  const float own = __shfl_sync(0xffffffffu, (float)n * middle_of(group * kGroupBins + lane) * scale, lane_of);
+  const float into = fminf(fmaxf((want - __shfl_sync(0xffffffffu, at, lane_of) + own) / own, 0.f), 0.999f);
+  const uint32_t in_bin = __shfl_sync(0xffffffffu, n, lane_of);
+  // the values looked at should fit the list: some 300
+  const int around = bin >= kBins - 1 ? -1 : in_bin * 5 <= 1200 ? 2 : in_bin * 3 <= 1400 ? 1 : in_bin <= 1600 ? 0 : -1;
+  return About{4 * bin + (int)(4.0f * into), around, bin, upto};
+}
+
+// What the blocks have collected in s.local goes into list[1] of block 0, or of
+// every block.  Ends with the cluster's barrier.
+__device__ __forceinline__ void merge_lists(Shared& s, cg::cluster_group& cluster, int blocks) {
+  __syncthreads();
+  const int n = (int)min(s.pushed, (uint32_t)kList);
+  if ((int)threadIdx.x < blocks)
+    s.base[threadIdx.x] = atomicAdd(&cluster.map_shared_rank(&s, threadIdx.x)->merged, s.pushed);
+  __syncthreads();
+  for (int o = 0; o < blocks; ++o) {
+    const uint32_t to = s.base[o] + threadIdx.x;
+    if ((int)threadIdx.x < n && to < (uint32_t)kList) cluster.map_shared_rank(&s, o)->list[1][to] = s.local[threadIdx.x];
+  }
+  cluster.sync();
+}
+
 template <class T, bool STAGED>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -328,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const long long row = blockIdx.x / C;
   pdl_launch_dependents();
   for (int i = tid; i < 256; i += kThreads) s.powers[i] = kPowers.v[i];
-  for (int i = tid; i < 4 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
+  for (int i = tid; i < kBins; i += kThreads) s.hist[0][i] = 0;
+  if (tid == 0) s.merged = s.pushed = 0;
   pdl_wait();
 
   const T* const base = static_cast<const T*>(p.logits) + row * p.ld;
@@ -430,10 +561,198 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   uint64_t cut = 0;
   auto pair_of = [&](uint32_t key, int i) -> uint64_t { return ((uint64_t)key << 32) | (0xffffffffu - (uint32_t)(i0 + i)); };
 
-  bool fresh = false;  // the histogram is that of all values
+  // ---- the counts of all values' bins ----
+  const float mp = p.min_p ? __ldg(p.min_p + row) : 0.f;
+  uint64_t least = 0;  // ceil(min_p * 2^43)
+  if (mp >= 1.f) {
+    least = 1ull << kOne;
+  } else if (mp > 0.f) {
+    const uint64_t f = fraction_of(mp);
+    least = (f >> (64 - kOne)) + ((f & ((1ull << (64 - kOne)) - 1)) != 0);
+  }
+  const float u = fminf(fmaxf(__ldg(p.uniform + row), 0.f), 0.99999994f);  // a NaN counts as 0
+  const int seg = (n + kWarps - 1) / kWarps;  // a warp's values
+  auto write_out = [&](int index, float x, uint64_t total) {
+    p.tokens[row] = index;
+    if (p.logprobs) {
+      // (x - top) / T - ln(sum of weights against the largest)
+      const float d = x - r.top, h = __fmul_rn(d, r.e.hi), l = fmaf(d, r.e.hi, -h) + d * r.e.lo;
+      const float rest = (float)(total - (1ull << kOne)) * 1.13686838e-13f;  // 2^-43: the largest is among them
+      p.logprobs[row] = (h + l) * 0.693147182f - log1pf(rest);
+    }
+  };
+  auto collect = [&](float x, int i) {
+    const uint32_t spot = atomicAdd(&s.pushed, 1u);
+    if (spot < (uint32_t)kList) s.local[spot] = pair_of(key_of(x), i);
+  };
+  // Block 0 has every value that may be kept in list[1] and does the rest alone:
+  // count_limit and, where by_mass, p of `mass` (0: of the first count_limit).
+  auto finish_list = [&](uint32_t count_limit, uint64_t mass) {
+    const int entries = (int)min(s.merged, (uint32_t)kList);
+    const uint64_t* const list = s.list[1];
+    const bool on = tid < entries;
+    const uint64_t me = on ? list[tid] : 0;
+    const float x = value_of_key((uint32_t)(me >> 32));
+    const uint64_t w = on ? weight_of(x, r, s.powers) : 0;
+    if (on) s.list_mass[tid] = w;
+    __syncthreads();
+    uint64_t before = 0;
+    uint32_t c = 0;
+    if (on)
+      for (int j = 0; j < entries; ++j)
+        if (list[j] > me) {
+          before += s.list_mass[j];
+          ++c;
+        }
+    bool keep = on && c < count_limit;
+    if (by_mass) {
+      if (mass == 0) {
+        uint64_t first = keep ? w : 0, none = 0;
+        block_sums(s, first, none);
+        mass = first;
+      }
+      keep = keep && before < share_of(tp, mass);
+    }
+    keep = keep && w >= least;
+    uint64_t total = keep ? w : 0, none = 0;
+    block_sums(s, total, none);
+    if (on) s.list_mass[tid] = keep ? w : 0;
+    __syncthreads();
+    const uint64_t target = __umul64hi(fraction_of(u), total);
+    if (keep && w > 0) {  // the kept ones of lower index
+      const uint32_t my = (uint32_t)me;  // falls with the index
+      uint64_t run = 0;
+      for (int j = 0; j < entries; ++j)
+        if ((uint32_t)list[j] > my) run += s.list_mass[j];
+      if (run <= target && target < run + w) write_out((int)(0xffffffffu - my), x, total);
+    }
+  };
+
+  bool summed = false;  // the kept weights of the warps' segments are in warp_mass
+  bool fresh = false;   // the histogram's counts are those of all values
+  if (by_count || by_mass) {
+    uint64_t heavy = 0;
+#pragma unroll 1
+    for (int i = tid; i < n; i += 2 * kThreads) {
+      const float x0 = at(i), x1 = i + kThreads < n ? at(i + kThreads) : -INFINITY;
+      const int b0 = first_bin(r, x0), b1 = first_bin(r, x1);
+      if (b0 < kBins) atomicAdd(&s.hist[0][b0], 1u);
+      if (b1 < kBins) atomicAdd(&s.hist[0][b1], 1u);
+      if (by_mass && min(b0, b1) < kHeavyGroups * kGroupBins) {
+        uint64_t w[2];
+        int bins[2];
+        weights_of(x0, x1, r, s.powers, w, bins);
+        heavy += (b0 < kHeavyGroups * kGroupBins ? w[0] : 0) + (b1 < kHeavyGroups * kGroupBins ? w[1] : 0);
+      }
+    }
+    uint64_t none = 0;
+    block_sums(s, heavy, none);  // its barriers are the histogram's too
+    if (tid < C) cluster.map_shared_rank(&s, tid)->heavy[rank] = heavy;
+    for (int g = warp; g < kGroups; g += kWarps) {
+      const uint32_t c = s.hist[0][g * kGroupBins + lane], all = __reduce_add_sync(0xffffffffu, c);
+      float m = (float)c * middle_of(g * kGroupBins + lane);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+      if (lane < C) {
+        Shared& to = *cluster.map_shared_rank(&s, lane);
+        to.group_count[rank][g] = all;
+        to.group_about[rank][g] = m;
+      }
+    }
+    if (tid == 0) {
+      s.before_mass = 0;
+      s.before_count = 0;
+    }
+    cluster.sync();
+    fresh = !by_mass;
+    if (by_count) {
+      // few enough: block 0 gets them all
+      find_bin(s, cluster, C, rank, false, true, (uint32_t)k, 0);
+      const int bin = s.bin;
+      if (bin >= 0 && s.before_count + s.bin_count <= (uint32_t)kList) {
+        for (int i = tid; i < n; i += kThreads) {
+          const float x = at(i);
+          if (first_bin(r, x) <= bin) collect(x, i);
+        }
+        merge_lists(s, cluster, 1);
+        if (rank == 0) finish_list((uint32_t)k, 0);
+        return;
+      }
+      cluster.sync();  // the histogram is read by all others until here
+    } else {
+      const About about = find_about(s, cluster, C, tp);
+      const bool few = about.upto <= (uint32_t)kList;
+      // few: all up to the end of the group after the bin's; else what lies around
+      // the estimate, and the exact sum above that
+      const int low = few ? 0 : about.k - about.around;
+      const int high = few ? 4 * (about.bin / kGroupBins + 2) * kGroupBins - 1 : about.k + about.around;
+      uint64_t all = 0, above = 0, m = 0;
+#pragma unroll 1
+      for (int i = warp * seg + lane; i < min(n, (warp + 1) * seg); i += 64) {
+        const float x[2] = {at(i), i + 32 < min(n, (warp + 1) * seg) ? at(i + 32) : -INFINITY};
+        uint64_t w[2];
+        int step[2];
+        weights_of(x[0], x[1], r, s.powers, w, step);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          all += w[j];
+          if (step[j] < low || (few && step[j] <= high)) {
+            above += w[j];
+            m += w[j] >= least ? w[j] : 0;
+          }
+          if (step[j] >= low && step[j] <= high) collect(x[j], i + 32 * j);
+        }
+      }
+      uint64_t my_all = all, my_above = above;
+      block_sums(s, my_all, my_above);
+      if (tid < C) {
+        Shared& to = *cluster.map_shared_rank(&s, tid);
+        to.sum[rank] = my_all;
+        to.above[rank] = my_above;
+      }
+      merge_lists(s, cluster, few ? 1 : C);
+      all = above = 0;
+      for (int o = 0; o < C; ++o) {
+        all += s.sum[o];
+        above += s.above[o];
+      }
+      const uint64_t want = share_of(tp, all);
+      if (few && above >= want) {  // above: all that is listed
+        if (rank == 0) finish_list(0xffffffffu, all);
+        return;
+      }
+      const uint64_t* const list = s.list[1];
+      const int entries = (int)min(s.merged, (uint32_t)kList);
+      const uint64_t me = tid < entries ? list[tid] : 0;
+      const uint64_t w = tid < entries ? weight_of(value_of_key((uint32_t)(me >> 32)), r, s.powers) : 0;
+      if (tid < entries) s.list_mass[tid] = w;
+      uint64_t listed = w, none2 = 0;
+      block_sums(s, listed, none2);
+      if (!few && s.merged <= (uint32_t)kList && above < want && above + listed >= want) {  // the cut is in the list
+        if (tid < entries) {
+          uint64_t before = above;
+          for (int j = 0; j < entries; ++j)
+            if (list[j] > me) before += s.list_mass[j];
+          if (before < want && before + w >= want) s.cut = me;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+        __syncthreads();
+        if (lane == 0) s.warp_mass[warp] = m;
+        __syncthreads();
+        cut = s.cut;
+        const int index = (int)(0xffffffffu - (uint32_t)me) - i0;
+        if (tid < entries && me >= cut && w >= least && index >= 0 && index < n)
+          atomicAdd(reinterpret_cast<unsigned long long*>(&s.warp_mass[index / seg]), (unsigned long long)w);
+        __syncthreads();
+        summed = true;
+      }
+    }
+  }
+
   uint64_t limit_mass = 0, want_mass = 0;
 #pragma unroll 1
-  for (int pass = by_count ? 0 : 1; pass < (by_mass ? 2 : 1); ++pass) {
+  for (int pass = by_count ? 0 : 1; !summed && pass < (by_mass ? 2 : 1); ++pass) {
     const bool counting = pass == 0;
     uint32_t key_low = 0, key_high = 0xffffffffu, shift = 0;
     int bin = -1;  // of all values' histogram, once it is known
@@ -445,10 +764,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll 1
     for (bool first_level = true;; first_level = false) {
       if (!(first_level && fresh)) {
-        if (!first_level || (pass > 0 && by_count)) {  // zero from the start on otherwise
-          for (int i = tid; i < 4 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
-          __syncthreads();
-        }
+        for (int i = tid; i < 4 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
+        __syncthreads();
         for (int i = tid; i < n; i += 2 * kThreads) {
           const float x[2] = {at(i), i + kThreads < n ? at(i + kThreads) : -INFINITY};
           uint64_t w[2] = {0, 0};
@@ -461,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            int b = bins[j];
+            int b = by_mass ? bin_of_k(bins[j]) : bins[j];
             if (!first_level) {
               const uint32_t key = key_of(x[j]);
               b = b == bin && key >= key_low && key <= key_high ? (int)((key_high - key) >> shift) : kBins;
@@ -498,7 +815,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         fresh = first_level;
       }
       if (first_level && !counting) {
-        // the shortest run that reaches p of the mass: ceil(p * mass), of at least one value
         uint64_t all = limit_mass;
         if (!all) {
 #pragma unroll
@@ -507,8 +823,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
         }
-        const uint64_t frac = fraction_of(fmaxf(tp, 0.f));
-        want_mass = max(1ull, (unsigned long long)(__umul64hi(frac, all) + (frac * all != 0)));
+        want_mass = share_of(tp, all);
       }
       find_bin(s, cluster, C, rank, by_mass, counting, (uint32_t)k, want_mass);
       const int found = s.bin;
@@ -530,7 +845,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           const uint32_t key = key_of(x);
           if (inside(x, key)) {
             const uint32_t spot = s.offset + atomicAdd(&s.pushed, 1u);
-            for (int o = 0; o < C; ++o) cluster.map_shared_rank(&s, o)->list[pass][spot] = pair_of(key, i);
+            if (spot < (uint32_t)kList)  // in_bin of them
+              for (int o = 0; o < C; ++o) cluster.map_shared_rank(&s, o)->list[pass][spot] = pair_of(key, i);
           }
         }
         cluster.sync();
@@ -638,14 +954,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   }
 
   // ---- the mass of what is kept, by warps' segments in order ----
-  const float mp = p.min_p ? __ldg(p.min_p + row) : 0.f;
-  uint64_t least = 0;  // ceil(min_p * 2^43)
-  if (mp >= 1.f) {
-    least = 1ull << kOne;
-  } else if (mp > 0.f) {
-    const uint64_t f = fraction_of(mp);
-    least = (f >> (64 - kOne)) + ((f & ((1ull << (64 - kOne)) - 1)) != 0);
-  }
   const uint32_t cut_key = (uint32_t)(cut >> 32);
   auto kept = [&](float x, int i) {
     const uint32_t key = key_of(x);
@@ -656,25 +964,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     const uint64_t w = kept(x, i) ? weight_of(x, r, s.powers) : 0;
     return w >= least ? w : 0;
   };
-  const int seg = (n + kWarps - 1) / kWarps;
-  uint64_t m = 0;
-  for (int i = warp * seg + lane; i < min(n, (warp + 1) * seg); i += 64) {
-    float x[2] = {at(i), -INFINITY};
-    const bool two = i + 32 < min(n, (warp + 1) * seg);
-    if (two) x[1] = at(i + 32);
-    const bool keep[2] = {kept(x[0], i), two && kept(x[1], i + 32)};
-    if (keep[0] || keep[1]) {
-      uint64_t w[2];
-      int bins[2];
-      weights_of(x[0], x[1], r, s.powers, w, bins);
+  if (!summed) {
+    uint64_t m = 0;
+    for (int i = warp * seg + lane; i < min(n, (warp + 1) * seg); i += 64) {
+      float x[2] = {at(i), -INFINITY};
+      const bool two = i + 32 < min(n, (warp + 1) * seg);
+      if (two) x[1] = at(i + 32);
+      const bool keep[2] = {kept(x[0], i), two && kept(x[1], i + 32)};
+      if (keep[0] || keep[1]) {
+        uint64_t w[2];
+        int bins[2];
+        weights_of(x[0], x[1], r, s.powers, w, bins);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) m += keep[j] && w[j] >= least ? w[j] : 0;
+        for (int j = 0; j < 2; ++j) m += keep[j] && w[j] >= least ? w[j] : 0;
+      }
     }
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-  if (lane == 0) s.warp_mass[warp] = m;
-  __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+    if (lane == 0) s.warp_mass[warp] = m;
+    __syncthreads();
+  }
   uint64_t all = 0;
   for (int w = 0; w < kWarps; ++w) all += s.warp_mass[w];
   if (tid < C) cluster.map_shared_rank(&s, tid)->mass[rank] = all;
@@ -684,7 +993,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (o < rank) before += s.mass[o];
     total += s.mass[o];
   }
-  const float u = fminf(fmaxf(__ldg(p.uniform + row), 0.f), 0.99999994f);  // a NaN counts as 0
   const uint64_t target = __umul64hi(fraction_of(u), total);
   if (before <= target && target < before + all) {  // this block
     int w = 0;
@@ -702,13 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const int i = begin + tid * each + j;
         const uint64_t wi = i < end ? kept_weight(i) : 0;
         if (target < upto + wi) {
-          p.tokens[row] = i0 + i;
-          if (p.logprobs) {
-            // (x - top) / T - ln(sum of weights against the largest)
-            const float d = at(i) - r.top, h = __fmul_rn(d, r.e.hi), l = fmaf(d, r.e.hi, -h) + d * r.e.lo;
-            const float rest = (float)(total - (1ull << kOne)) * 1.13686838e-13f;  // 2^-43: the largest is among them
-            p.logprobs[row] = (h + l) * 0.693147182f - log1pf(rest);
-          }
+          write_out(i0 + i, at(i), total);
           break;
         }
         upto += wi;
