@@ -15,6 +15,8 @@ import threading
 
 from .build import BINDING as _BINDING_PATH
 from .build import LIB as _LIB_PATH
+from .build import TENSORS as _TENSORS_PATH
+from .build import TENSORS_OF as _TENSORS_OF
 from .build import build as _build
 
 __all__ = [
@@ -221,7 +223,23 @@ def _load_binding(lib):
                   for f in ("tl_kv_plan", "tl_kv4_append", "tl_kv4_read", "tl_kv4_attention", "tl_lora_add")))
     module.bind_step(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                        for f in ("tl_qk_norm_rope", "tl_kv4_append_rope", "tl_sample", "tl_kv4_attention_prefix")))
+    _read_tensors(module)
     _short = module
+
+
+def _read_tensors(module):
+    """Lets the C API module read tensors past the interpreter (csrc/tensors.cpp),
+    where that was built for this very torch."""
+    import torch
+
+    try:
+        with open(_TENSORS_OF) as f:
+            if f.read() != torch.__version__:
+                return
+        tensors = ctypes.CDLL(_TENSORS_PATH)
+    except OSError:
+        return
+    module.read_tensors(ctypes.cast(tensors.tlq_tensor_read, ctypes.c_void_p).value, torch.Tensor, torch.nn.Parameter)
 
 
 def _raise_if(st: int):

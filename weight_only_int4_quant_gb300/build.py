@@ -1,12 +1,15 @@
 """Build libtlq.so (sm_103a) in-tree with nvcc: one object per .cu, compiled in
 parallel, then one shared-library link; beside it, with the C compiler, the
-Python module that shortens the serving calls (the library does without it
-where it cannot be built).  No cmake, no torch extension."""
+Python module that shortens the serving calls and its way to read torch's
+tensors (the library does without them where they cannot be built).  No cmake,
+no torch extension."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
+import re
 import subprocess
 import sysconfig
 import warnings
@@ -18,6 +21,9 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libtlq.so")
 # one file for each interpreter that uses the tree
 BINDING = os.path.join(BUILD, "_tlq_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+# how that module reads torch's tensors, for one version of torch (named in TENSORS_OF)
+TENSORS = os.path.join(BUILD, "_tlq_tensors" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+TENSORS_OF = TENSORS + ".torch"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-rdc=true", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -73,11 +79,47 @@ def build_binding(force: bool = False) -> bool:
     return True
 
 
+def build_tensors(force: bool = False) -> bool:
+    """TENSORS: csrc/tensors.cpp against the headers of the torch that is installed
+    (which is not imported).  Without them, or where it does not compile, the C
+    API module reads tensors through their attributes."""
+    src = os.path.join(CSRC, "tensors.cpp")
+    spec = importlib.util.find_spec("torch")
+    root = os.path.dirname(spec.origin) if spec and spec.origin else ""
+    if not os.path.exists(os.path.join(root, "include", "torch", "csrc", "autograd", "python_variable.h")):
+        return False
+    with open(os.path.join(root, "version.py")) as f:
+        version = re.search(r"__version__ = '([^']*)'", f.read()).group(1)
+    deps = [src, os.path.join(CSRC, "tensors.h"), os.path.abspath(__file__)]
+    if not force and _fresh(TENSORS, deps) and os.path.exists(TENSORS_OF) and open(TENSORS_OF).read() == version:
+        return True
+    tmp = TENSORS + ".tmp%d" % os.getpid()
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], cuda, CSRC]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-w", "-shared", "-fPIC"] + ["-I" + i for i in include] + \
+        [src, "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-ltorch_cpu"]
+    try:
+        done = subprocess.run(cmd, capture_output=True, text=True).returncode == 0
+    except OSError:
+        done = False
+    if not done:
+        for path in (TENSORS, TENSORS_OF):  # of an older source or another torch
+            if os.path.exists(path):
+                os.remove(path)
+        return False
+    os.replace(tmp, TENSORS)
+    with open(TENSORS_OF, "w") as f:
+        f.write(version)
+    return True
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile every kernel source for sm_103a and link libtlq.so; return its path."""
     os.makedirs(BUILD, exist_ok=True)
     build_binding(force)
     if not force and up_to_date():
+        build_tensors()
         return LIB
     nvcc = _nvcc()
     srcs = _sources()
@@ -92,8 +134,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError("nvcc failed for %s:\n%s\n%s" % (src, " ".join(cmd), r.stderr))
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(9, len(srcs) + 1)) as ex:
+        tensors = ex.submit(build_tensors, force)
         results = list(ex.map(compile_one, srcs))
+        tensors.result()
     if verbose:
         for _, log in results:
             print(log)

@@ -8,13 +8,16 @@
  * Python function of its name takes, reads what the tensors say of themselves
  * and calls the library; it returns the library's status, or -1 without having
  * called it when an argument is not as it should be (the Python function then
- * goes through its own checks, which name what is wrong).
+ * goes through its own checks, which name what is wrong).  Tensors are read
+ * through tensors.cpp where that was built for the torch in use, else through
+ * their attributes.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <string.h>
 
 #include "../../include/tlq.h"
+#include "tensors.h"
 
 #define FALLBACK (-1)
 
@@ -61,8 +64,31 @@ static int call_long(PyObject* o, PyObject* name, long long* out) {
   return !(*out == -1 && PyErr_Occurred());
 }
 
+/* The way past the interpreter, once read_tensors has been called: for torch's
+ * own two classes only (a subclass may answer for itself). */
+static int (*f_tensor)(PyObject*, tlq_tensor*);
+static PyTypeObject *tensor_class, *parameter_class;
+
+static int known(PyObject* t, tlq_tensor* x) {
+  return f_tensor && (Py_TYPE(t) == tensor_class || Py_TYPE(t) == parameter_class) && f_tensor(t, x);
+}
+
+static int type_of(PyObject* type) {
+  return type == t_f16 ? TLQ_TENSOR_F16
+         : type == t_f32 ? TLQ_TENSOR_F32
+         : type == t_i32 ? TLQ_TENSOR_I32
+         : type == t_i64 ? TLQ_TENSOR_I64
+                         : TLQ_TENSOR_U8;
+}
+
 /* Sizes (s_shape) or strides (s_stride) of a tensor of `dims` dimensions. */
 static int extents(PyObject* t, int strides, int dims, long long* out) {
+  tlq_tensor x;
+  if (known(t, &x)) {
+    if (x.dims != dims) return 0;
+    memcpy(out, strides ? x.step : x.size, dims * sizeof *out);
+    return 1;
+  }
   PyObject* v = strides ? PyObject_CallMethodNoArgs(t, s_stride) : PyObject_GetAttr(t, s_shape);
   if (!v || !PyTuple_Check(v) || PyTuple_GET_SIZE(v) != dims) {
     Py_XDECREF(v);
@@ -84,6 +110,13 @@ static int pointer(PyObject* t, void** p) {
 /* A contiguous CUDA tensor of one type; n >= 0: of that many elements, else
  * *n_out takes the number (if asked for). */
 static int flat(PyObject* t, PyObject* type, long long n, void** p, long long* n_out) {
+  tlq_tensor x;
+  if (known(t, &x)) {
+    if (x.type != type_of(type) || !x.contiguous || (n >= 0 && x.numel != n)) return 0;
+    if (n_out) *n_out = x.numel;
+    *p = x.data;
+    return 1;
+  }
   if (!attr_is(t, s_dtype, type) || !attr_is(t, s_is_cuda, Py_True)) return 0;
   PyObject* c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
   Py_XDECREF(c);
@@ -99,13 +132,24 @@ static int flat(PyObject* t, PyObject* type, long long n, void** p, long long* n
 /* Rows [tokens, a] (dims = 2) or [tokens, a, b] (dims = 3), contiguous but for
  * the token stride; at least one (whose stride says nothing). */
 static int rows(PyObject* t, int dims, long long a, long long b, void** p, int64_t* ld, long long* tokens) {
+  tlq_tensor x;
   long long size[3], step[3];
-  if (!attr_is(t, s_dtype, t_f16) || !attr_is(t, s_is_cuda, Py_True) || !extents(t, 0, dims, size) ||
-      !extents(t, 1, dims, step))
+  const int direct = known(t, &x);
+  if (direct) {
+    if (x.type != TLQ_TENSOR_F16 || x.dims != dims) return 0;
+    memcpy(size, x.size, dims * sizeof *size);
+    memcpy(step, x.step, dims * sizeof *step);
+  } else if (!attr_is(t, s_dtype, t_f16) || !attr_is(t, s_is_cuda, Py_True) || !extents(t, 0, dims, size) ||
+             !extents(t, 1, dims, step)) {
     return 0;
+  }
   if (size[0] < 1 || size[1] != a || (dims == 3 && (size[2] != b || step[1] != b)) || step[dims - 1] != 1) return 0;
   *ld = size[0] > 1 ? step[0] : (dims == 3 ? a * b : a);
   *tokens = size[0];
+  if (direct) {
+    *p = x.data;
+    return 1;
+  }
   return pointer(t, p);
 }
 
@@ -337,11 +381,17 @@ static int sample(PyObject* const* a, Py_ssize_t n) {
   /* logits, uniform, tokens, temperature, top_k, top_p, min_p, logprobs, stream */
   void *x, *uniform, *tokens, *temperature, *top_k, *top_p, *min_p, *logprobs, *s;
   long long size[2], step[2];
-  if (n != 9 || !extents(a[0], 0, 2, size) || !extents(a[0], 1, 2, step) || size[0] < 1 || step[1] != 1 ||
-      !attr_is(a[0], s_is_cuda, Py_True))
+  tlq_tensor logits;
+  if (n != 9 || !extents(a[0], 0, 2, size) || !extents(a[0], 1, 2, step) || size[0] < 1 || step[1] != 1)
     return FALLBACK;
-  const int half = attr_is(a[0], s_dtype, t_f16);
-  if ((!half && !attr_is(a[0], s_dtype, t_f32)) || !pointer(a[0], &x) || !flat(a[1], t_f32, size[0], &uniform, NULL) ||
+  if (known(a[0], &logits)) {
+    x = logits.data;
+  } else {
+    if (!attr_is(a[0], s_is_cuda, Py_True) || !pointer(a[0], &x)) return FALLBACK;
+    logits.type = attr_is(a[0], s_dtype, t_f16) ? TLQ_TENSOR_F16 : attr_is(a[0], s_dtype, t_f32) ? TLQ_TENSOR_F32 : 0;
+  }
+  const int half = logits.type == TLQ_TENSOR_F16;
+  if ((!half && logits.type != TLQ_TENSOR_F32) || !flat(a[1], t_f32, size[0], &uniform, NULL) ||
       !flat(a[2], t_i32, size[0], &tokens, NULL) || !flat_or_none(a[3], t_f32, size[0], &temperature) ||
       !flat_or_none(a[4], t_i32, size[0], &top_k) || !flat_or_none(a[5], t_f32, size[0], &top_p) ||
       !flat_or_none(a[6], t_f32, size[0], &min_p) || !flat_or_none(a[7], t_f32, size[0], &logprobs) ||
@@ -417,6 +467,19 @@ static PyObject* bind_step(PyObject* self, PyObject* args) {
   Py_RETURN_NONE;
 }
 
+/* read_tensors(the address of tlq_tensor_read, torch.Tensor, torch.nn.Parameter) */
+static PyObject* read_tensors(PyObject* self, PyObject* args) {
+  PyObject *f, *tensor, *parameter;
+  (void)self;
+  if (!PyArg_ParseTuple(args, "OO!O!", &f, &PyType_Type, &tensor, &PyType_Type, &parameter)) return NULL;
+  void* p = PyLong_AsVoidPtr(f);
+  if (PyErr_Occurred()) return NULL;
+  tensor_class = (PyTypeObject*)Py_NewRef(tensor);
+  parameter_class = (PyTypeObject*)Py_NewRef(parameter);
+  *(void**)&f_tensor = p;
+  Py_RETURN_NONE;
+}
+
 static PyMethodDef methods[] = {
     {"bind", bind, METH_VARARGS, "Torch's types and the library's entry points; once."},
     {"plan", (PyCFunction)(void (*)(void))py_plan, METH_FASTCALL, "tl_kv_plan"},
@@ -425,6 +488,7 @@ static PyMethodDef methods[] = {
     {"attention", (PyCFunction)(void (*)(void))py_attention, METH_FASTCALL, "tl_kv4_attention"},
     {"lora", (PyCFunction)(void (*)(void))py_lora, METH_FASTCALL, "tl_lora_add"},
     {"bind_step", bind_step, METH_VARARGS, "The entry points of a step's other calls; once, after bind."},
+    {"read_tensors", read_tensors, METH_VARARGS, "The way to read tensors past the interpreter; once."},
     {"norm_rope", (PyCFunction)(void (*)(void))py_norm_rope, METH_FASTCALL, "tl_qk_norm_rope"},
     {"append_rope", (PyCFunction)(void (*)(void))py_append_rope, METH_FASTCALL, "tl_kv4_append_rope"},
     {"sample", (PyCFunction)(void (*)(void))py_sample, METH_FASTCALL, "tl_sample"},

@@ -1,0 +1,40 @@
+// What a torch tensor says of itself, read from the tensor (torch's own headers)
+// instead of through the interpreter: five attribute calls take 0.3 us of a
+// serving call of 2, and such a call has up to eight tensors.  A shared library
+// beside the C API module, which is given the address of tlq_tensor_read; built
+// for one version of torch and used with no other.
+#include <Python.h>
+#include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
+
+extern "C" {
+
+#include "tensors.h"
+
+const char* tlq_torch_version(void) { return TORCH_VERSION; }
+
+// 1 if o (a torch.Tensor or Parameter, which the caller has made sure of) is a
+// strided CUDA tensor of up to four dimensions; *t is filled in.
+int tlq_tensor_read(PyObject* o, tlq_tensor* t) {
+  const at::Tensor& x = THPVariable_Unpack(o);
+  if (!x.defined() || !x.is_cuda() || x.layout() != at::kStrided || x.dim() > 4) return 0;
+  switch (x.scalar_type()) {
+    case at::kHalf: t->type = TLQ_TENSOR_F16; break;
+    case at::kFloat: t->type = TLQ_TENSOR_F32; break;
+    case at::kInt: t->type = TLQ_TENSOR_I32; break;
+    case at::kLong: t->type = TLQ_TENSOR_I64; break;
+    case at::kByte: t->type = TLQ_TENSOR_U8; break;
+    default: return 0;
+  }
+  t->dims = (int)x.dim();
+  for (int i = 0; i < t->dims; ++i) {
+    t->size[i] = x.sizes()[i];
+    t->step[i] = x.strides()[i];
+  }
+  t->numel = x.numel();
+  t->contiguous = x.is_contiguous();
+  t->data = x.data_ptr();
+  return 1;
+}
+
+}  // extern "C"
