@@ -53,12 +53,16 @@ __device__ __forceinline__ bool code_word(const float2 (&x)[4], float s, float b
   return far < s * (0.5f - 3.8147e-6f);
 }
 
-static __device__ __noinline__ uint32_t code_word_by_division(float4 lo, float4 hi, float s, float b) {
+__device__ __forceinline__ uint32_t code_word_by_divisions(float4 lo, float4 hi, float s, float b) {
   const float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) w |= (uint32_t)fminf(fmaxf(rintf((x[i] - b) / s), 0.0f), 15.0f) << (4 * i);
   return w;
+}
+// The same as a call, where it would crowd out the code around it.
+static __device__ __noinline__ uint32_t code_word_by_division(float4 lo, float4 hi, float s, float b) {
+  return code_word_by_divisions(lo, hi, s, b);
 }
 
 // x / 15 as IEEE division gives it: a correctly rounded reciprocal, the

@@ -152,6 +152,8 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
         }
       if (turns && there) turn_of(p.rope, l, at, co, si);
     }
+    long long slot = -1;
+    if (CACHE && part.out == nullptr) slot = __ldg(p.slots + t);
     float2 x[2][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -253,10 +255,9 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
           const GroupScale& g = (k ? ch.y : ch.x) >> gshift ? g1 : g0;
           const float2 a = __half22float2(h[k][0]), b = __half22float2(h[k][1]), c = __half22float2(h[k][2]),
                        d = __half22float2(h[k][3]);
-          word[k] = code_word_by_division(make_float4(a.x, a.y, b.x, b.y), make_float4(c.x, c.y, d.x, d.y), g.s, g.b);
+          word[k] = code_word_by_divisions(make_float4(a.x, a.y, b.x, b.y), make_float4(c.x, c.y, d.x, d.y), g.s, g.b);
         }
       }
-      const long long slot = __ldg(p.slots + t);
       if (mine && in_cache(p.cache, slot)) {
         const CodeRow out = code_row<D>(p.cache, slot, head, kind - 1);
         uint32_t* codes = reinterpret_cast<uint32_t*>(out.codes);
