@@ -232,3 +232,22 @@ def test_strided_rows(lib):
     wide = torch.full((71, 10, 128), 2.0, dtype=torch.float16, device="cuda")
     b.run(out=wide[:, 1:9])
     assert torch.equal(wide[:, 1:9], want) and (wide[:, 0] == 2).all() and (wide[:, 9] == 2).all()
+
+
+def test_contradicting_lengths_write_within_their_rows(lib):
+    """Requests whose queries overlap or run backwards: the numbers of such rows mean nothing, rows of sound
+    requests are what they are alone, and the rows of no request are left."""
+    b = Batch(lib, 700, [90, 120, 40, 30], [20, 60, 1, 1], 16, 4, 128, 128, 16)
+    want = b.run()
+    start = b.start.tolist()
+    out = torch.full((len(b.q) + 8, 16, 128), 9.0, dtype=torch.float16, device="cuda")[:len(b.q)]
+    for bad in ([0, 20, 10, 81, 82], [0, 50, 30, 81, 82], [5, 5, 80, 81, 82], [0, 90, 80, 81, 82], [-3, 20, 80, 81, 82],
+                [2 ** 31 - 1, -2 ** 31, 80, 81, 82]):
+        b.start[:] = torch.tensor(bad, dtype=torch.int32)
+        out.fill_(9.0)
+        b.run(out=out)
+        torch.cuda.synchronize()
+        assert torch.equal(out[81], want[81])  # the last request is sound in each
+    lib.tl_check_status()
+    b.start[:] = torch.tensor(start, dtype=torch.int32)
+    assert torch.equal(b.run(), want)

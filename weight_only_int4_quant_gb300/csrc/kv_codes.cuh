@@ -97,4 +97,46 @@ __device__ __forceinline__ GroupScale group_scale(__half low, __half high) {
   return g;
 }
 
+// A row's piece of 16 channels, one of D / 16 lanes side by side (GL to a group):
+// codes and parameters into the row's slot, unless `put` is false or the slot is
+// outside the cache.  All lanes of a warp take part.  next() is called once the
+// row is in registers.
+template <int D, int GL, class F>
+__device__ __forceinline__ void append_row(const KvCache& c, const uint4 (&raw)[2], bool put, long long slot, int head,
+                                           int part, int sub, F next) {
+  float2 x[8];
+  __half2 lo2, hi2;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint4& q = raw[i >> 2];
+    const uint32_t w = (i & 2) ? ((i & 1) ? q.w : q.z) : ((i & 1) ? q.y : q.x);
+    const __half2 h = *reinterpret_cast<const __half2*>(&w);
+    x[i] = __half22float2(h);
+    lo2 = i ? __hmin2_nan(lo2, h) : h;
+    hi2 = i ? __hmax2_nan(hi2, h) : h;
+  }
+  next();
+#pragma unroll
+  for (int o = 1; o < GL; o <<= 1) {
+    lo2 = __hmin2_nan(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
+    hi2 = __hmax2_nan(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+  }
+  const GroupScale g = group_scale(__hmin_nan(__low2half(lo2), __high2half(lo2)),
+                                   __hmax_nan(__low2half(hi2), __high2half(hi2)));
+  uint32_t word[2];
+  const float2 x0[4] = {x[0], x[1], x[2], x[3]}, x1[4] = {x[4], x[5], x[6], x[7]};
+  const bool sure0 = code_word(x0, g.s, g.b, g.inv, &word[0]), sure1 = code_word(x1, g.s, g.b, g.inv, &word[1]);
+  if (!(sure0 && sure1 && (g.top - g.b) * g.inv < 15.25f)) {
+    word[0] = code_word_by_division(make_float4(x[0].x, x[0].y, x[1].x, x[1].y),
+                                    make_float4(x[2].x, x[2].y, x[3].x, x[3].y), g.s, g.b);
+    word[1] = code_word_by_division(make_float4(x[4].x, x[4].y, x[5].x, x[5].y),
+                                    make_float4(x[6].x, x[6].y, x[7].x, x[7].y), g.s, g.b);
+  }
+  if (put && in_cache(c, slot)) {
+    const CodeRow out = code_row<D>(c, slot, head, part);
+    reinterpret_cast<uint2*>(out.codes)[sub] = make_uint2(word[0], word[1]);
+    if (sub % GL == 0) out.par[sub / GL] = g.pair;
+  }
+}
+
 }  // namespace tlq

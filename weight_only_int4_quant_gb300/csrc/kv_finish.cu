@@ -22,27 +22,37 @@ struct RowParts {
   const float *o, *m, *l;
   size_t f;  // floats of a part
   int n;
+  bool permuted;  // of the tensor-core kernel, whose channels lie as 0 4 1 5 2 6 3 7
   __device__ __forceinline__ size_t at(int i) const { return i ? (size_t)(2 * i - 1) * f : 0; }
 };
 
+// gr: the row among its request's (query, head) rows; many: which kernel takes
+// that request.  Where parts lie goes by what their kernel wrote, checked against
+// its blocks, so that lengths that contradict each other (requests whose queries
+// overlap) lead to no address outside the workspace.
 template <int D>
-__device__ __forceinline__ RowParts row_parts(const KvRowSums& sums, size_t row, const KvJoin& j, int item_row) {
+__device__ __forceinline__ RowParts row_parts(const KvRowSums& sums, size_t row, int gr, bool many, const KvJoin& few_parts,
+                                              const KvJoin& many_parts) {
   const float2 ml = sums.ml[row];
   RowParts r;
   if (ml.y < 0.f) {
-    const int block = __float_as_int(ml.x), R = j.rows;
+    const int mark = __float_as_int(ml.x), block = mark & (kPartsOfMany - 1), followers = (int)fminf(-ml.y, 1e6f);
+    r.permuted = mark & kPartsOfMany;
+    const KvJoin& j = r.permuted ? many_parts : few_parts;
+    const int R = j.rows, item_row = gr % max(R, 1);
     r.f = (size_t)R * (D + 2);  // a part: O [R][D], m [R], l [R]
     const float* first = j.parts + ((size_t)block * 2 + 1) * r.f;  // follower i at (block + i) * 2 parts
     r.o = first + (size_t)item_row * D;
     r.m = first + (size_t)R * D + item_row;
     r.l = r.m + R;
-    r.n = 1 + (int)-ml.y;
+    r.n = block + followers < j.blocks ? 1 + followers : 0;
   } else {
     r.f = 0;
     r.o = sums.o + row * D;
     r.m = &sums.ml[row].x;
     r.l = &sums.ml[row].y;
     r.n = 1;
+    r.permuted = many;
   }
   return r;
 }
@@ -61,9 +71,8 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const KvBatch batch, c
     const int row = (int)(e / (D / 8)), ch = (int)(e % (D / 8)) * 8;
     const int t = divide(row, by_heads), head = row - t * q_heads, g = head % share;
     const size_t at = (size_t)(r.q0 + t) * q_heads + head;
-    const KvJoin &jo = own_many ? many : few, &jp = prefix_many ? many : few;
-    const RowParts parts[2] = {row_parts<D>(shared.own, at, jo, (t * share + g) % jo.rows),
-                               row_parts<D>(shared.prefix, at, jp, ((r.q0 + t) * share + g) % jp.rows)};
+    const RowParts parts[2] = {row_parts<D>(shared.own, at, t * share + g, own_many, few, many),
+                               row_parts<D>(shared.prefix, at, (r.q0 + t) * share + g, prefix_many, few, many)};
     float m = -INFINITY, l = 0.f, sum[8] = {};
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -102,10 +111,8 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const KvBatch batch, c
           for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, x[k], acc[k]);
         }
       }
-      // the tensor-core kernel's channels lie as 0 4 1 5 2 6 3 7
-      const bool permuted = s ? prefix_many : own_many;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum[k] += permuted ? acc[((k & 3) << 1) + (k >> 2)] : acc[k];
+      for (int k = 0; k < 8; ++k) sum[k] += parts[s].permuted ? acc[((k & 3) << 1) + (k >> 2)] : acc[k];
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;  // no key seen: zeros
     uint32_t o[4];

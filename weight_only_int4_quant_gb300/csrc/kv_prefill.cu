@@ -970,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
               po[y] = sums.o + at * D + 2 * qd;
               pm[y] = reinterpret_cast<float*>(sums.ml + at);
             } else if (qd == 0 && row0 + 8 * y < rows) {
-              sums.ml[at] = kv_row_in_parts(blockIdx.x, followers);
+              sums.ml[at] = kv_row_in_parts(blockIdx.x | kPartsOfMany, followers);
             }
           }
         }

@@ -99,8 +99,10 @@ __device__ __forceinline__ void turn_of(const RopeTable& r, int l, const int (&a
   }
 }
 
-template <int D, bool CACHE>
+// GL: lanes of a group of the cache that keys and values go into; 0: there is none.
+template <int D, int GL>
 __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopeParams p) {
+  constexpr bool CACHE = GL > 0;
   constexpr int L = D / 16;  // lanes of a row
   pdl_launch_dependents();
   pdl_wait();
@@ -126,8 +128,26 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
     raw[1] = __ldg(src + ch.y);
   };
   fetch(first);
+  if constexpr (CACHE) {
+    if (kind == 2) {  // values: as they are
+#pragma unroll 1
+      for (int u = 0; u < p.turns; ++u) {
+        const uint32_t t = next_t;
+        const int head = (int)(min(first + u, part.rows - 1) - t * part.heads.d);
+        bool there = true;
+        if (p.rope.rot) {
+#pragma unroll
+          for (int a = 0; a < 3; ++a)
+            if (a < p.rope.axes) there &= __ldg(p.positions + a * p.ld_positions + t) >= 0;
+        }
+        append_row<D, GL>(p.cache, raw, first + u < part.rows && there, __ldg(p.slots + t), head, 1, l,
+                          [&]() { if (u + 1 < p.turns) fetch(first + u + 1); });
+      }
+      return;
+    }
+  }
   uint4 wraw[2];
-  const bool normed = kind < 2 && part.weight != nullptr;
+  const bool normed = part.weight != nullptr;
   if (normed) {
     wraw[0] = __ldg(reinterpret_cast<const uint4*>(part.weight) + ch.x);
     wraw[1] = __ldg(reinterpret_cast<const uint4*>(part.weight) + ch.y);
@@ -218,32 +238,63 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
         for (int k = 0; k < 2; ++k) dst[k ? ch.y : ch.x] = *reinterpret_cast<const uint4*>(h[k]);
       }
     } else if constexpr (CACHE) {
-      // least and greatest value of the row's first and second group of channels (of one group: of each half)
-      const __half inf = __ushort_as_half((unsigned short)0x7C00), ninf = __ushort_as_half((unsigned short)0xFC00);
-      __half2 lo2 = __half2half2(inf), hi2 = __half2half2(ninf);
-      const int gshift = p.cache.group == 64 ? 3 : 4;  // chunk to group
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const __half2 a = __hmin2_nan(__hmin2_nan(h[k][0], h[k][1]), __hmin2_nan(h[k][2], h[k][3]));
-        const __half2 b = __hmax2_nan(__hmax2_nan(h[k][0], h[k][1]), __hmax2_nan(h[k][2], h[k][3]));
-        const __half low = __hmin_nan(__low2half(a), __high2half(a)), high = __hmax_nan(__low2half(b), __high2half(b));
-        const bool g = (k ? ch.y : ch.x) >> gshift;
-        lo2 = __hmin2_nan(lo2, g ? __halves2half2(inf, low) : __halves2half2(low, inf));
-        hi2 = __hmax2_nan(hi2, g ? __halves2half2(ninf, high) : __halves2half2(high, ninf));
-      }
-#pragma unroll
-      for (int o = 1; o < L; o <<= 1) {
-        lo2 = __hmin2_nan(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
-        hi2 = __hmax2_nan(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
-      }
-      const GroupScale g0 = group_scale(__low2half(lo2), __low2half(hi2));
-      GroupScale g1 = g0;
-      if (D == 128 && gshift == 3) g1 = group_scale(__high2half(lo2), __high2half(hi2));
+      int2 at = ch;  // the chunks at hand
       uint32_t word[2];
+      GroupScale g0, g1;
+      constexpr bool two = GL < L;  // groups of a row
+      const bool split = two && !p.rope.neighbours && rot > 64;  // a lane's chunks are of two groups (some lanes')
+      if (!split || rot == 128) {
+        if (split) {
+          // lanes l and l ^ 4 exchange a chunk: then each has two of one group
+          const bool high = l >= 4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __half2 give = high ? h[0][i] : h[1][i];
+            const __half2 got = __shfl_xor_sync(0xffffffffu, give, 4);
+            h[0][i] = high ? got : h[0][i];
+            h[1][i] = high ? h[1][i] : got;
+          }
+          at = high ? make_int2(l + 4, l + 8) : make_int2(l, l + 4);
+        }
+        __half2 lo2 = h[0][0], hi2 = h[0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+          lo2 = __hmin2_nan(lo2, h[i >> 2][i & 3]);
+          hi2 = __hmax2_nan(hi2, h[i >> 2][i & 3]);
+        }
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1)
+          if (o < GL) {
+            lo2 = __hmin2_nan(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
+            hi2 = __hmax2_nan(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+          }
+        g0 = g1 = group_scale(__hmin_nan(__low2half(lo2), __high2half(lo2)), __hmax_nan(__low2half(hi2), __high2half(hi2)));
+      } else {
+        // least and greatest value of the row's first and second group
+        const __half inf = __ushort_as_half((unsigned short)0x7C00), ninf = __ushort_as_half((unsigned short)0xFC00);
+        __half2 lo2 = __half2half2(inf), hi2 = __half2half2(ninf);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const __half2 a = __hmin2_nan(__hmin2_nan(h[k][0], h[k][1]), __hmin2_nan(h[k][2], h[k][3]));
+          const __half2 b = __hmax2_nan(__hmax2_nan(h[k][0], h[k][1]), __hmax2_nan(h[k][2], h[k][3]));
+          const __half low = __hmin_nan(__low2half(a), __high2half(a)), high = __hmax_nan(__low2half(b), __high2half(b));
+          const bool g = (k ? at.y : at.x) >> 3;
+          lo2 = __hmin2_nan(lo2, g ? __halves2half2(inf, low) : __halves2half2(low, inf));
+          hi2 = __hmax2_nan(hi2, g ? __halves2half2(ninf, high) : __halves2half2(high, ninf));
+        }
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) {
+          lo2 = __hmin2_nan(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
+          hi2 = __hmax2_nan(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+        }
+        const GroupScale a = group_scale(__low2half(lo2), __low2half(hi2)), b = group_scale(__high2half(lo2), __high2half(hi2));
+        g0 = at.x >> 3 ? b : a;
+        g1 = at.y >> 3 ? b : a;
+      }
       bool sure = true;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const GroupScale& g = (k ? ch.y : ch.x) >> gshift ? g1 : g0;
+        const GroupScale& g = k ? g1 : g0;
         float2 y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = __half22float2(h[k][i]);
@@ -252,21 +303,21 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const RopePar
       if (!sure) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const GroupScale& g = (k ? ch.y : ch.x) >> gshift ? g1 : g0;
+          const GroupScale& g = k ? g1 : g0;
           const float2 a = __half22float2(h[k][0]), b = __half22float2(h[k][1]), c = __half22float2(h[k][2]),
                        d = __half22float2(h[k][3]);
           word[k] = code_word_by_divisions(make_float4(a.x, a.y, b.x, b.y), make_float4(c.x, c.y, d.x, d.y), g.s, g.b);
         }
       }
       if (mine && in_cache(p.cache, slot)) {
-        const CodeRow out = code_row<D>(p.cache, slot, head, kind - 1);
+        const CodeRow out = code_row<D>(p.cache, slot, head, 0);
         uint32_t* codes = reinterpret_cast<uint32_t*>(out.codes);
-        codes[ch.x] = word[0];
-        codes[ch.y] = word[1];
-        if (l == 0) {
-          out.par[0] = g0.pair;
-          if (D == 128 && gshift == 3) out.par[1] = g1.pair;
-        }
+        codes[at.x] = word[0];
+        codes[at.y] = word[1];
+        // a group's parameters are its first chunk's lane's to write
+        if (at.x == 0) out.par[0] = g0.pair;
+        if (two && at.x == 8) out.par[1] = g0.pair;
+        if (two && at.y == 8) out.par[1] = g1.pair;
       }
     }
   }
@@ -285,7 +336,7 @@ __global__ void table_kernel(const double* __restrict__ freq, float2* __restrict
   }
 }
 
-template <int D, bool CACHE>
+template <int D, int GL>
 tlq_status launch_rows(RopeParams& p, cudaStream_t stream) {
   constexpr uint32_t groups = kThreads / (D / 16);  // rows of a block at a time
   long long rows = 0;
@@ -308,7 +359,7 @@ tlq_status launch_rows(RopeParams& p, cudaStream_t stream) {
   at.val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = &at;
   lc.numAttrs = pdl_enabled() ? 1 : 0;
-  return cuda_error(cudaLaunchKernelEx(&lc, rope_kernel<D, CACHE>, p), "rope: launch");
+  return cuda_error(cudaLaunchKernelEx(&lc, rope_kernel<D, GL>, p), "rope: launch");
 }
 
 }  // namespace
@@ -331,10 +382,13 @@ tlq_status launch_rope(const RopeArgs& a, cudaStream_t stream) {
   p.one = 1.0f;
   p.cache = a.cache;
   p.slots = a.slots;
-  if (a.slots != nullptr) return a.head_dim == 64 ? launch_rows<64, true>(p, stream) : launch_rows<128, true>(p, stream);
-  return a.head_dim == 64    ? launch_rows<64, false>(p, stream)
-         : a.head_dim == 128 ? launch_rows<128, false>(p, stream)
-                             : launch_rows<256, false>(p, stream);
+  if (a.slots != nullptr)
+    return a.head_dim == 64      ? launch_rows<64, 4>(p, stream)
+           : a.cache.group == 64 ? launch_rows<128, 4>(p, stream)
+                                 : launch_rows<128, 8>(p, stream);
+  return a.head_dim == 64    ? launch_rows<64, 0>(p, stream)
+         : a.head_dim == 128 ? launch_rows<128, 0>(p, stream)
+                             : launch_rows<256, 0>(p, stream);
 }
 
 tlq_status launch_rope_table(const double* freq, float* table, long long positions, int half, double scale,

@@ -311,11 +311,13 @@ struct KvRowSums {
 struct KvShared {
   KvRowSums own, prefix;
 };
-// (block that begins the row's item, -followers) in the place of (m, l): l is never negative.
+inline size_t kv_row_sums_bytes(long long rows, int head_dim) { return (size_t)rows * (head_dim + 2) * sizeof(float); }
+// (block that begins the row's item and which kernel's, -followers) in the place
+// of (m, l): l is never negative.
+constexpr int kPartsOfMany = 1 << 30;
 __device__ __forceinline__ float2 kv_row_in_parts(int block, int followers) {
   return make_float2(__int_as_float(block), -(float)followers);
 }
-inline size_t kv_row_sums_bytes(long long rows, int head_dim) { return (size_t)rows * (head_dim + 2) * sizeof(float); }
 
 struct KvAttention {
   KvCache cache;
