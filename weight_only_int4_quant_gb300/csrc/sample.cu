@@ -178,7 +178,7 @@ constexpr int kHeavyGroups = 12;  // groups whose weights are added up exactly b
 
 // The state of a block; other blocks of its cluster write what is marked.
 struct Shared {
-  uint32_t hist[4][kBins];               // counts, limbs (read by others)
+  uint32_t hist[kBins];                  // counts (read by others)
   uint64_t powers[256];
   uint64_t list[2][kList];               // candidates, of the cut by count and by mass (written by others)
   uint64_t local[kList];                 // this block's candidates
@@ -238,6 +238,14 @@ __device__ __forceinline__ uint64_t block_scan(Shared& s, uint64_t mass) {
   return mass;
 }
 
+// The weights' limbs of the bins lie behind that (read by others), over the values,
+// which are read from global memory again once they are needed.
+constexpr size_t kFixed = (sizeof(Shared) + 15) & ~size_t(15);
+constexpr size_t kLimbBytes = 3 * kBins * sizeof(uint32_t);
+__device__ __forceinline__ uint32_t* limbs_of(Shared& s, int limb) {
+  return reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(&s) + kFixed) + limb * kBins;
+}
+
 // Inclusive sums over a warp.
 __device__ __forceinline__ void warp_scan(uint64_t& m, uint32_t& c) {
 #pragma unroll
@@ -288,12 +296,12 @@ __device__ __forceinline__ void find_bin(Shared& s, cg::cluster_group& cluster, 
     }
     first = (2 * from + (second ? 1 : 0)) * kGroupBins;
     if (warp < C) {
-      const Shared& of = *cluster.map_shared_rank(&s, warp);
-      const uint32_t n = of.hist[0][first + lane];
+      Shared& of = *cluster.map_shared_rank(&s, warp);
+      const uint32_t n = of.hist[first + lane];
       uint64_t x = 0;
       if (with_mass)
-        x = of.hist[1][first + lane] + ((uint64_t)of.hist[2][first + lane] << 15) +
-            ((uint64_t)of.hist[3][first + lane] << 30);
+        x = limbs_of(of, 0)[first + lane] + ((uint64_t)limbs_of(of, 1)[first + lane] << 15) +
+            ((uint64_t)limbs_of(of, 2)[first + lane] << 30);
       s.fine_count[warp][lane] = n;
       s.fine_mass[warp][lane] = x;
     }
@@ -409,7 +417,7 @@ __device__ __forceinline__ About find_about(Shared& s, cg::cluster_group& cluste
   const uint32_t next = __shfl_sync(0xffffffffu, c[0], min(from + 1, 31));
   const uint32_t upto = second ? through + (from < 31 ? next : 0) : through;
   const float scale = group < kHeavyGroups ? (float)heavy * 1.13686838e-13f / estimate : 1.0f;
-  if (warp < C) s.fine_count[warp][lane] = cluster.map_shared_rank(&s, warp)->hist[0][group * kGroupBins + lane];
+  if (warp < C) s.fine_count[warp][lane] = cluster.map_shared_rank(&s, warp)->hist[group * kGroupBins + lane];
   __syncthreads();
   uint32_t n = 0;
 #pragma unroll
@@ -427,8 +435,13 @@ __device__ __forceinline__ About find_about(Shared& s, cg::cluster_group& cluste
   const float own = __shfl_sync(0xffffffffu, (float)n * middle_of(group * kGroupBins + lane) * scale, lane_of);
   const float into = fminf(fmaxf((want - __shfl_sync(0xffffffffu, at, lane_of) + own) / own, 0.f), 0.999f);
   const uint32_t in_bin = __shfl_sync(0xffffffffu, n, lane_of);
-  // the values looked at should fit the list: some 300
-  const int around = bin >= kBins - 1 ? -1 : in_bin * 5 <= 1200 ? 2 : in_bin * 3 <= 1400 ? 1 : in_bin <= 1600 ? 0 : -1;
+  // some 128 values are looked at, by how densely they lie here: a cut outside of them
+  // costs the general way (15 to 40 us), more of them the ranking (200 us with 256 for 191
+  // in 256 rows of 100003; with 96 of them single rows of 200000 missed)
+  const uint32_t own_group = __shfl_sync(0xffffffffu, second ? c[1] : c[0], from);
+  const uint32_t after = __shfl_sync(0xffffffffu, second ? c[0] : c[1], second ? min(from + 1, 31) : from);
+  const float dense = fmaxf((float)in_bin * 0.25f, (float)max(own_group, after) * (1.0f / 128.0f));  // of a k
+  const int around = bin >= kBins - 1 || dense > 400.f ? -1 : (int)fminf(64.0f / fmaxf(dense, 1.0f), 64.0f);
   return About{4 * bin + (int)(4.0f * into), around, bin, upto};
 }
 
@@ -458,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const long long row = blockIdx.x / C;
   pdl_launch_dependents();
   for (int i = tid; i < 256; i += kThreads) s.powers[i] = kPowers.v[i];
-  for (int i = tid; i < kBins; i += kThreads) s.hist[0][i] = 0;
+  for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
   if (tid == 0) s.merged = s.pushed = 0;
   pdl_wait();
 
@@ -467,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const T* const mine = base + i0;
   // in shared memory the piece lies as it does to 16 bytes in global memory
   const int lead = (int)((reinterpret_cast<uintptr_t>(mine) & 15) / sizeof(T));
-  T* const stage = reinterpret_cast<T*>(smem_raw + ((sizeof(Shared) + 15) & ~size_t(15))) + lead;
+  T* const stage = reinterpret_cast<T*>(smem_raw + kFixed) + lead;
   auto at = [&](int i) -> float { return value_of<T>(STAGED ? stage[i] : mine[i]); };
 
   // ---- the piece into shared memory, its greatest value (lowest index first) ----
@@ -636,8 +649,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     for (int i = tid; i < n; i += 2 * kThreads) {
       const float x0 = at(i), x1 = i + kThreads < n ? at(i + kThreads) : -INFINITY;
       const int b0 = first_bin(r, x0), b1 = first_bin(r, x1);
-      if (b0 < kBins) atomicAdd(&s.hist[0][b0], 1u);
-      if (b1 < kBins) atomicAdd(&s.hist[0][b1], 1u);
+      if (b0 < kBins) atomicAdd(&s.hist[b0], 1u);
+      if (b1 < kBins) atomicAdd(&s.hist[b1], 1u);
       if (by_mass && min(b0, b1) < kHeavyGroups * kGroupBins) {
         uint64_t w[2];
         int bins[2];
@@ -649,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     block_sums(s, heavy, none);  // its barriers are the histogram's too
     if (tid < C) cluster.map_shared_rank(&s, tid)->heavy[rank] = heavy;
     for (int g = warp; g < kGroups; g += kWarps) {
-      const uint32_t c = s.hist[0][g * kGroupBins + lane], all = __reduce_add_sync(0xffffffffu, c);
+      const uint32_t c = s.hist[g * kGroupBins + lane], all = __reduce_add_sync(0xffffffffu, c);
       float m = (float)c * middle_of(g * kGroupBins + lane);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
@@ -750,6 +763,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
   }
 
+  // ---- the general way: histograms with the weights' exact sums ----
+  const bool spoiled = !summed && by_mass;  // the limbs go over the staged values
+  auto any = [&](int i) -> float { return STAGED && !spoiled ? value_of<T>(stage[i]) : value_of<T>(mine[i]); };
   uint64_t limit_mass = 0, want_mass = 0;
 #pragma unroll 1
   for (int pass = by_count ? 0 : 1; !summed && pass < (by_mass ? 2 : 1); ++pass) {
@@ -764,10 +780,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll 1
     for (bool first_level = true;; first_level = false) {
       if (!(first_level && fresh)) {
-        for (int i = tid; i < 4 * kBins; i += kThreads) (&s.hist[0][0])[i] = 0;
+        for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
+        if (by_mass)
+          for (int i = tid; i < 3 * kBins; i += kThreads) limbs_of(s, 0)[i] = 0;
         __syncthreads();
         for (int i = tid; i < n; i += 2 * kThreads) {
-          const float x[2] = {at(i), i + kThreads < n ? at(i + kThreads) : -INFINITY};
+          const float x[2] = {any(i), i + kThreads < n ? any(i + kThreads) : -INFINITY};
           uint64_t w[2] = {0, 0};
           int bins[2];
           if (by_mass) {
@@ -784,11 +802,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
               b = b == bin && key >= key_low && key <= key_high ? (int)((key_high - key) >> shift) : kBins;
             }
             if (b < kBins) {
-              atomicAdd(&s.hist[0][b], 1u);
+              atomicAdd(&s.hist[b], 1u);
               if (by_mass) {
-                atomicAdd(&s.hist[1][b], (uint32_t)w[j] & 0x7fffu);
-                atomicAdd(&s.hist[2][b], (uint32_t)(w[j] >> 15) & 0x7fffu);
-                if (w[j] >> 30) atomicAdd(&s.hist[3][b], (uint32_t)(w[j] >> 30));
+                atomicAdd(limbs_of(s, 0) + b, (uint32_t)w[j] & 0x7fffu);
+                atomicAdd(limbs_of(s, 1) + b, (uint32_t)(w[j] >> 15) & 0x7fffu);
+                if (w[j] >> 30) atomicAdd(limbs_of(s, 2) + b, (uint32_t)(w[j] >> 30));
               }
             }
           }
@@ -798,10 +816,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
         for (int g = warp; g < kGroups; g += kWarps) {
           const int b = g * kGroupBins + lane;
-          const uint32_t c = __reduce_add_sync(0xffffffffu, s.hist[0][b]);
+          const uint32_t c = __reduce_add_sync(0xffffffffu, s.hist[b]);
           uint64_t m = 0;
           if (by_mass) {
-            m = s.hist[1][b] + ((uint64_t)s.hist[2][b] << 15) + ((uint64_t)s.hist[3][b] << 30);
+            m = limbs_of(s, 0)[b] + ((uint64_t)limbs_of(s, 1)[b] << 15) + ((uint64_t)limbs_of(s, 2)[b] << 30);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
           }
@@ -841,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       if (in_bin <= (uint32_t)kList) {
         // every block gets all candidates and ranks them
         for (int i = tid; i < n; i += kThreads) {
-          const float x = at(i);
+          const float x = any(i);
           const uint32_t key = key_of(x);
           if (inside(x, key)) {
             const uint32_t spot = s.offset + atomicAdd(&s.pushed, 1u);
@@ -879,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       // the least and greatest key in there
       uint32_t low = 0xffffffffu, high = 0;
       for (int i = tid; i < n; i += kThreads) {
-        const float x = at(i);
+        const float x = any(i);
         const uint32_t key = key_of(x);
         if (inside(x, key)) {
           low = min(low, key);
@@ -916,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                                        : (uint32_t)((want_mass - s.before_mass + each - 1) / each);
         const int seg = (n + kWarps - 1) / kWarps, end = min(n, (warp + 1) * seg);
         uint32_t c = 0;
-        for (int i = warp * seg + lane; i < end; i += 32) c += key_of(at(i)) == key_low;
+        for (int i = warp * seg + lane; i < end; i += 32) c += key_of(any(i)) == key_low;
         c = __reduce_add_sync(0xffffffffu, c);
         __syncthreads();
         if (lane == 0) s.warp_count[warp] = c;
@@ -932,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         if (before < ties && before + c >= ties) {  // this warp
           uint32_t left = ties - before;
           for (int i = warp * seg; i < end; i += 32) {
-            const bool hit = i + lane < end && key_of(at(i + lane)) == key_low;
+            const bool hit = i + lane < end && key_of(any(i + lane)) == key_low;
             const uint32_t hits = __ballot_sync(0xffffffffu, hit);
             if ((uint32_t)__popc(hits) >= left) {
               const int spot = __fns(hits, 0, (int)left);
@@ -960,16 +978,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     return key > cut_key || (key == cut_key && pair_of(key, i) >= cut);
   };
   auto kept_weight = [&](int i) -> uint64_t {
-    const float x = at(i);
+    const float x = any(i);
     const uint64_t w = kept(x, i) ? weight_of(x, r, s.powers) : 0;
     return w >= least ? w : 0;
   };
   if (!summed) {
     uint64_t m = 0;
     for (int i = warp * seg + lane; i < min(n, (warp + 1) * seg); i += 64) {
-      float x[2] = {at(i), -INFINITY};
+      float x[2] = {any(i), -INFINITY};
       const bool two = i + 32 < min(n, (warp + 1) * seg);
-      if (two) x[1] = at(i + 32);
+      if (two) x[1] = any(i + 32);
       const bool keep[2] = {kept(x[0], i), two && kept(x[1], i + 32)};
       if (keep[0] || keep[1]) {
         uint64_t w[2];
@@ -1010,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const int i = begin + tid * each + j;
         const uint64_t wi = i < end ? kept_weight(i) : 0;
         if (target < upto + wi) {
-          write_out(i0 + i, at(i), total);
+          write_out(i0 + i, any(i), total);
           break;
         }
         upto += wi;
@@ -1038,14 +1056,34 @@ tlq_status launch_one(const SampleParams& p, int rows, int blocks, size_t smem, 
   return cuda_error(cudaLaunchKernelEx(&lc, sample_kernel<T, STAGED>, p), "sample: launch");
 }
 
+// How many blocks take a row: whichever needs the least time, as measured (top-p,
+// microseconds): each wave of rows 12 and 1.45 for every 1000 values of a block
+// where two blocks share an SM, 0.8 where they do not.  64 rows of 131072 FP16:
+// four blocks 60, eight (two waves) 75, two 65; 64 of 32000: 39, 50, 44; 256 of 100003
+// FP32: eight 234, four 237; 512 of 4000: one 28, two 42, four 77.
 template <class T>
 tlq_status launch_as(SampleParams p, int rows, cudaStream_t stream) {
-  int blocks = 1;
-  while (blocks < kMaxBlocks && p.vocab > 4096 * blocks) blocks *= 2;
-  p.piece = (p.vocab + blocks - 1) / blocks;
-  const size_t fixed = (sizeof(Shared) + 15) & ~size_t(15), staged = fixed + (size_t)p.piece * sizeof(T) + 16;
-  return staged <= (size_t)kMaxSmem ? launch_one<T, true>(p, rows, blocks, staged, stream)
-                                    : launch_one<T, false>(p, rows, blocks, fixed, stream);
+  const int sms = device_info().sms;
+  int blocks = 0;
+  size_t smem = 0;
+  double least = 0;
+  for (int b = 1; b <= kMaxBlocks; b *= 2) {
+    const size_t piece = (size_t)(p.vocab + b - 1) / b, need = kFixed + std::max(kLimbBytes, piece * sizeof(T) + 16);
+    if (need > (size_t)kMaxSmem) continue;
+    const int resident = need + 1024 <= (228u << 10) / 2 ? 2 : 1;
+    const long long at_once = std::max(1, sms / b * resident - (b > 2 ? 2 : 0));  // clusters that fit
+    const bool shared = resident == 2 && (long long)rows * b > sms;
+    const double time = (double)((rows + at_once - 1) / at_once) * (12.0 + (shared ? 1.45e-3 : 0.8e-3) * (double)piece);
+    if (blocks == 0 || time < least) {
+      blocks = b;
+      smem = need;
+      least = time;
+    }
+  }
+  p.piece = (p.vocab + std::max(blocks, 1) - 1) / std::max(blocks, 1);
+  if (blocks) return launch_one<T, true>(p, rows, blocks, smem, stream);
+  p.piece = (p.vocab + kMaxBlocks - 1) / kMaxBlocks;
+  return launch_one<T, false>(p, rows, kMaxBlocks, kFixed + kLimbBytes, stream);
 }
 
 }  // namespace
