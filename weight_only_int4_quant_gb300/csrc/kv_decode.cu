@@ -64,6 +64,9 @@ namespace tlq {
 namespace {
 
 constexpr bool kShared = TLQ_KV_SHARED_UNIT;
+// What beginning and ending an item costs, in stages, on the line of work.  With a
+// prefix the items are short (a request's own tokens).
+constexpr int kItemCost = kShared ? 1 : 0;
 
 constexpr int kStage = 128;  // tokens of a stage
 constexpr int kTile = 16;    // tokens of a matrix instruction
@@ -167,7 +170,7 @@ __device__ __forceinline__ ItemShape item_shape(const DecodeParams& p, const KvR
     // window + queries - 1 keys, wherever they lie in their stages
     span = (int)min((long long)r.len, (long long)p.window + queries + kStage);
   }
-  s.units = max(1, (span + kStage - 1) / kStage);
+  s.units = max(1, (span + kStage - 1) / kStage) + kItemCost;
   return s;
 }
 
@@ -202,6 +205,10 @@ struct Walk {
       const int item = (int)((u - req_u) / shape.units);
       const int c0 = (int)((u - req_u) - (long long)item * shape.units);
       const int c1 = (int)min((long long)shape.units, c0 + (u_end - u));
+      if (kItemCost > 0 && c1 <= kItemCost) {  // the share ends before the item's first stage
+        u += c1 - c0;
+        continue;
+      }
       const int row_blocks = shape.items / p.cache.heads;
       s->rq = rq;
       s->req = req;
@@ -214,9 +221,9 @@ struct Walk {
       s->all_hi = min(s->hi, rq.base + first_q + 1);
       s->all_lo = p.window > 0 ? rq.base + last_q - p.window + 1 : 0;
       const int stage = s->lo / kStage;
-      s->s0 = stage + c0;
-      s->s1 = min(stage + c1, (s->hi + kStage - 1) / kStage);
-      s->first = c0 == 0;
+      s->s0 = stage + max(0, c0 - kItemCost);
+      s->s1 = min(stage + c1 - kItemCost, (s->hi + kStage - 1) / kStage);
+      s->first = c0 <= kItemCost;
       s->last = c1 == shape.units;
       s->item_end = req_u + (long long)(item + 1) * shape.units;
       s->units = c1 - c0;
