@@ -15,7 +15,6 @@ namespace tlq {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 8;  // parts whose loads are under way together
 
 // One row's parts on one side.
 struct RowParts {
@@ -57,8 +56,9 @@ __device__ __forceinline__ RowParts row_parts(const KvRowSums& sums, size_t row,
   return r;
 }
 
-// The grid's x goes over requests, its y over their rows.
-template <int D>
+// The grid's x goes over requests, its y over their rows.  kBatch: parts whose
+// loads are under way together.
+template <int D, int kBatch>
 __global__ void __launch_bounds__(kThreads) finish_kernel(const KvBatch batch, const KvShared shared, const KvJoin few,
                                                           const KvJoin many, __half* out, long long ldo, int q_heads,
                                                           FastDiv by_heads, int share, int page, int few_rows) {
@@ -140,7 +140,12 @@ tlq_status launch_kv4_finish_shared(const KvAttention& a, int few_rows, const Kv
   at.val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = &at;
   lc.numAttrs = pdl_enabled() ? 1 : 0;
-  auto kernel = a.head_dim == 64 ? finish_kernel<64> : finish_kernel<128>;
+  // Rows of prompts lie in one or two parts, and there are many of them: fewer
+  // registers (992 queries: 337 us with four, 346 with eight).  Single tokens' lie in
+  // many: more under way (four requests: 11.2 us with eight, 11.8 with four).
+  const bool prompts = (long long)a.batch.max_q * (a.q_heads / a.cache.heads) > few_rows;
+  auto kernel = a.head_dim == 64 ? (prompts ? finish_kernel<64, 4> : finish_kernel<64, 8>)
+                                 : (prompts ? finish_kernel<128, 4> : finish_kernel<128, 8>);
   return cuda_error(cudaLaunchKernelEx(&lc, kernel, a.batch, a.shared, few, many, a.out, a.ldo, a.q_heads,
                                        fast_div((uint32_t)a.q_heads), a.q_heads / a.cache.heads, a.cache.page, few_rows),
                     "kv4 attention finish: launch");
