@@ -99,7 +99,7 @@ def test_many_rows(lib):
     compare(lib, x, u, **filters(700, g, "tkpm"))
 
 
-@pytest.mark.parametrize("vocab", [7, 1000, 70000])
+@pytest.mark.parametrize("vocab", [7, 1000, 70000, 1 << 20])
 def test_equal_logits(lib, vocab):
     """Every weight the same: sums are whole numbers and borders are hit exactly; ties go by index."""
     rows = 24
@@ -109,6 +109,7 @@ def test_equal_logits(lib, vocab):
     compare(lib, x, u, k=torch.arange(rows, dtype=torch.int32, device="cuda"))
     compare(lib, x, u, p=torch.arange(rows, device="cuda") / 16.0)
     compare(lib, x, u, p=torch.full((rows,), 0.5, device="cuda"), k=torch.full((rows,), 4, dtype=torch.int32, device="cuda"))
+    compare(lib, x, u, p=torch.full((rows,), 0.75, device="cuda"), k=torch.full((rows,), max(1, vocab * 2 // 3), dtype=torch.int32, device="cuda"))
     compare(lib, x, u, mp=torch.full((rows,), 1.0, device="cuda"))
 
 
@@ -221,3 +222,38 @@ def test_captured_on_other_streams_and_the_long_way(lib, monkeypatch):
             call(side)
         side.synchronize()
         assert (tokens.tolist(), logs.tolist()) == got
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("vocab", [3000, 150000])
+def test_many_kept(lib, vocab, half):
+    """top-k beyond a list's length, with and without top-p; cuts in a flat body, in a narrow peak and between two
+    far groups of values."""
+    g = torch.Generator("cuda").manual_seed(vocab)
+    flat = torch.rand(4, vocab, device="cuda", generator=g) * 1e-3
+    peak = torch.randn(4, vocab, device="cuda", generator=g) * 0.02
+    peak[:, 7] = 30.0
+    apart = torch.where(torch.rand(4, vocab, device="cuda", generator=g) < 0.01, 9.0, 0.0) + 0.3 * torch.randn(
+        4, vocab, device="cuda", generator=g)
+    x = torch.cat((flat, peak, apart))
+    x = x.half() if half else x
+    u = torch.rand(12, device="cuda", generator=g)
+    k = (vocab * torch.rand(12, device="cuda", generator=g)).int().clamp_min(600)
+    p = 0.05 + 0.94 * torch.rand(12, device="cuda", generator=g)
+    t = 0.5 + torch.rand(12, device="cuda", generator=g)
+    compare(lib, x, u, k=k)
+    compare(lib, x, u, p=p, t=t)
+    compare(lib, x, u, k=k, p=p, t=t)
+    compare(lib, x, u, k=k, p=p, mp=torch.full((12,), 0.3, device="cuda"))
+
+
+@pytest.mark.parametrize("vocab,rows", [(20000, 1), (20000, 40), (20000, 200), (5000, 90), (5000, 400), (65536, 30), (65536, 100)])
+def test_the_same_by_any_number_of_blocks(lib, vocab, rows):
+    """How many blocks take a row goes by the number of rows: the first rows are what they are alone."""
+    x, u, g = logits(rows, vocab, 4, True)
+    f = filters(rows, g, "tpm")
+    tokens, logs = lib.sample(x, u, f["t"], None, f["p"], f["mp"])
+    for i in (0, rows // 2, rows - 1):
+        one = slice(i, i + 1)
+        t, l = lib.sample(x[one], u[one], f["t"][one], None, f["p"][one], f["mp"][one])
+        assert t[0] == tokens[i] and torch.equal(l[0].nan_to_num(), logs[i].nan_to_num())

@@ -17,7 +17,16 @@
 // way its pairs are 8 l .. 8 l + 7, one piece of the table's row.  A lane takes
 // up to eight rows one after another, of one token where heads allow it, so that
 // weights and the table's row are read once for all of them; a row is asked for
-// a turn ahead.  A block's rows are all queries, all keys or all values.
+// a turn ahead.  A block's rows are all queries, all keys or all values; values go
+// the way of the plain append.
+//
+// 8192 tokens x 40 heads of 128 take 34.4 us (5.0 TB/s, three quarters of a copy's
+// rate): three blocks of 80 registers a thread to an SM keep 24 KB under way, and
+// four blocks spill (43 us).  Up to 4 rows to a lane take the append of 16001 tokens,
+// 32 / 8 heads, with its read from 113 us to 120, up to 16 from 111 to 115, up to 48 to
+// 125.  A ring of rows in shared memory, three ahead, is 5 % faster on that prompt and
+// 14 % slower on rows of 64 channels.
+// Few tokens are bound by latency (position, table row, head): 16 take 2.4 us.
 #include <algorithm>
 
 #include "kv_codes.cuh"
