@@ -257,3 +257,20 @@ def test_the_same_by_any_number_of_blocks(lib, vocab, rows):
         one = slice(i, i + 1)
         t, l = lib.sample(x[one], u[one], f["t"][one], None, f["p"][one], f["mp"][one])
         assert t[0] == tokens[i] and torch.equal(l[0].nan_to_num(), logs[i].nan_to_num())
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("kind", ["p", "tkpm"])
+@pytest.mark.parametrize("vocab", [7, 4003, 70001, 200003])
+def test_the_same_by_clusters_of_every_size(lib, vocab, kind, half):
+    """17 to 152 rows go from clusters of eight blocks down to single blocks, by way of seven, six, five and three."""
+    x, u, g = logits(152, vocab, 6, half)
+    f = filters(152, g, kind)
+    pick = lambda rows: [f[n][:rows] if f.get(n) is not None else None for n in ("t", "k", "p", "mp")]
+    want_t, want_l = [torch.cat(parts) for parts in zip(*(
+        lib.sample(x[i:i + 1], u[i:i + 1], *[None if f.get(n) is None else f[n][i:i + 1] for n in ("t", "k", "p", "mp")])
+        for i in range(152)))]
+    for rows in (17, 19, 21, 23, 26, 28, 33, 36, 40, 46, 50, 64, 76, 90, 100, 152):
+        t, l = lib.sample(x[:rows], u[:rows], *pick(rows))
+        assert torch.equal(t, want_t[:rows])
+        assert torch.equal(l.nan_to_num(), want_l[:rows].nan_to_num())

@@ -29,14 +29,16 @@
 // clocks each, bound them.
 // top-k, and few kept values: one block gets all that may be kept as a list.
 //
-// 256 rows of 100003 FP32, top-p: 191 us, 7 waves of clusters of eight blocks; of a
-// block's 27 us the exact weights (50 instructions a value, two values at a time)
-// take 6.6, counting 4.2, loading 3, the rest barriers of the cluster and short
-// phases of the block.  64 rows of 131072 FP16, all filters: 44 us.  One row of 32000:
-// 12.7 us, a chain of ten short phases.
+// 256 rows of 100003 FP32, top-p: 165 us, 6 waves of clusters of six blocks (clusters
+// of eight, 7 to 8 waves: 190).  Of 27 us of a block with 12500 values the exact
+// weights (50 instructions a value, two values at a time) take 6.6, counting 4.2,
+// loading 3, the rest barriers of the cluster and short phases of the block.  64 rows
+// of 131072 FP16, all filters: 43.5 us.  One row of 32000: 12.4 us, a chain of ten
+// short phases.
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "serve.cuh"
 
@@ -656,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   bool fresh = false;   // the histogram's counts are those of all values
   if (by_count || by_mass) {
     uint64_t heavy = 0;
-#pragma unroll 1
+#pragma unroll 2
     for (int i = tid; i < n; i += 2 * kThreads) {
       const float x0 = at(i), x1 = i + kThreads < n ? at(i + kThreads) : -INFINITY;
       const int b0 = first_bin(r, x0), b1 = first_bin(r, x1);
@@ -672,7 +674,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     uint64_t none = 0;
     block_sums(s, heavy, none);  // its barriers are the histogram's too
     if (tid < C) cluster.map_shared_rank(&s, tid)->heavy[rank] = heavy;
-    for (int g = warp; g < kGroups; g += kWarps) {
+#pragma unroll
+    for (int j = 0; j < kGroups / kWarps; ++j) {
+      const int g = warp + j * kWarps;
       const uint32_t c = s.hist[g * kGroupBins + lane], all = __reduce_add_sync(0xffffffffu, c);
       float m = (float)c * middle_of(g * kGroupBins + lane);
 #pragma unroll
@@ -1067,24 +1071,55 @@ tlq_status launch_one(const SampleParams& p, int rows, int blocks, size_t smem, 
   return cuda_error(cudaLaunchKernelEx(&lc, sample_kernel<T, STAGED>, p), "sample: launch");
 }
 
-// How many blocks take a row: whichever needs the least time, as measured (top-p,
-// microseconds): each wave of rows 12 and 1.45 for every 1000 values of a block
-// where two blocks share an SM, 0.8 where they do not.  64 rows of 131072 FP16:
-// four blocks 60, eight (two waves) 75, two 65; 64 of 32000: 39, 50, 44; 256 of 100003
-// FP32: eight 234, four 237; 512 of 4000: one 28, two 42, four 77.
+// Clusters of this many blocks that run at once, with one or two blocks to an SM;
+// asked once.  A cluster lies in one GPC, so it is not SMs / blocks: of 152 SMs
+// clusters of 1 to 8 get 152, 76, 46, 36, 28, 23, 15 and 15, and with two blocks to
+// an SM 304, 152, 97, 74, 58, 46, 38 and 36.
+constexpr size_t kSmemOfTwo = (228u << 10) / 2 - 1024;
+template <class T>
+int clusters_at_once(int blocks, int resident) {
+  static std::atomic<int> known[kMaxBlocks + 1][3];
+  int n = known[blocks][resident].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)blocks, 1, 1);
+  lc.blockDim = dim3(kThreads, 1, 1);
+  lc.dynamicSmemBytes = resident == 2 ? kSmemOfTwo : (size_t)kMaxSmem;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)blocks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  if (opt_in_smem<sample_kernel<T, true>>(kMaxSmem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, sample_kernel<T, true>, &lc) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return std::max(1, device_info().sms / blocks * resident);  // the launch reports what is wrong
+  }
+  known[blocks][resident].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// How many blocks take a row: whichever needs the least time by two lines fitted to
+// 50 measurements (top-p, rows of 32000 and more): a wave of rows takes 11.5 us and
+// 0.65 for every 1000 values of a block, or, where two blocks share an SM, 12 and
+// 1.22.  256 rows of 100003 FP32: six blocks 188 us, three 195, eight 218; 64 of
+// 131072 FP16: four 52, two 54, eight 68; 40 of 200000 FP32: six 66, five 72, eight
+// 80; 512 of 32000 FP16: one 102, two 116; 64 of 32000 FP16: four 39, two 44.
 template <class T>
 tlq_status launch_as(SampleParams p, int rows, cudaStream_t stream) {
   const int sms = device_info().sms;
   int blocks = 0;
   size_t smem = 0;
   double least = 0;
-  for (int b = 1; b <= kMaxBlocks; b *= 2) {
+  for (int b = 1; b <= kMaxBlocks; ++b) {
     const size_t piece = (size_t)(p.vocab + b - 1) / b, need = kFixed + std::max(kLimbBytes, piece * sizeof(T) + 16);
     if (need > (size_t)kMaxSmem) continue;
-    const int resident = need + 1024 <= (228u << 10) / 2 ? 2 : 1;
-    const long long at_once = std::max(1, sms / b * resident - (b > 2 ? 2 : 0));  // clusters that fit
+    const int resident = need <= kSmemOfTwo ? 2 : 1;
+    const long long at_once = clusters_at_once<T>(b, resident);
     const bool shared = resident == 2 && (long long)rows * b > sms;
-    const double time = (double)((rows + at_once - 1) / at_once) * (12.0 + (shared ? 1.45e-3 : 0.8e-3) * (double)piece);
+    const double time = (double)((rows + at_once - 1) / at_once) *
+                        (shared ? 12.0 + 1.22e-3 * (double)piece : 11.5 + 0.65e-3 * (double)piece);
     if (blocks == 0 || time < least) {
       blocks = b;
       smem = need;
