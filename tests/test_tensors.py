@@ -93,3 +93,29 @@ def test_the_same_as_by_attributes(lib, tmp_path):
             got.append((m.sample(x, s, t, None, None, None, None, None, None), t.tolist()))
         assert got[0] == got[1]
     torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_tensors_that_stand_for_others_are_refused(lib):
+    """Inside torch.func's transforms tensors have no storage: an error, not the end of the process."""
+    u = torch.rand(6, device="cuda")
+    logits = torch.randn(3, 6, 40, device="cuda")
+    tokens = torch.full((6,), -5, dtype=torch.int32, device="cuda")
+    rows = torch.randn(3, 6, 5, 64, device="cuda").half()
+    out = torch.zeros(6, 5, 64, dtype=torch.float16, device="cuda")
+
+    def draw(x):
+        lib.tl_sample(x, u, tokens)
+        return x.sum()
+
+    def norm(x):
+        lib.tl_qk_norm_rope(None, x, None, None, out, None)
+        return x.float().sum()
+
+    for f, x in ((draw, logits), (norm, rows)):
+        with pytest.raises(RuntimeError):
+            torch.func.vmap(f)(x)
+        with pytest.raises(RuntimeError):
+            torch.func.grad(f)(x[0])
+    torch.cuda.synchronize()
+    assert tokens.tolist() == [-5] * 6 and not out.any()

@@ -89,7 +89,10 @@ def build_tensors(force: bool = False) -> bool:
     if not os.path.exists(os.path.join(root, "include", "torch", "csrc", "autograd", "python_variable.h")):
         return False
     with open(os.path.join(root, "version.py")) as f:
-        version = re.search(r"__version__ = '([^']*)'", f.read()).group(1)
+        version = re.search(r"""__version__ = ['"]([^'"]*)""", f.read())
+    if not version:
+        return False
+    version = version.group(1)
     deps = [src, os.path.join(CSRC, "tensors.h"), os.path.abspath(__file__)]
     if not force and _fresh(TENSORS, deps) and os.path.exists(TENSORS_OF) and open(TENSORS_OF).read() == version:
         return True

@@ -14,8 +14,10 @@ extern "C" {
 const char* tlq_torch_version(void) { return TORCH_VERSION; }
 
 // 1 if o (a torch.Tensor or Parameter, which the caller has made sure of) is a
-// strided CUDA tensor of up to four dimensions; *t is filled in.
-int tlq_tensor_read(PyObject* o, tlq_tensor* t) {
+// strided CUDA tensor of up to four dimensions; *t is filled in.  Tensors that
+// stand for others (inside torch.func's transforms) have no storage and throw
+// when they are asked for it: 0, and their attributes then say what is wrong.
+int tlq_tensor_read(PyObject* o, tlq_tensor* t) try {
   const at::Tensor& x = THPVariable_Unpack(o);
   if (!x.defined() || !x.is_cuda() || x.layout() != at::kStrided || x.dim() > 4) return 0;
   switch (x.scalar_type()) {
@@ -35,6 +37,8 @@ int tlq_tensor_read(PyObject* o, tlq_tensor* t) {
   t->contiguous = x.is_contiguous();
   t->data = x.data_ptr();
   return 1;
+} catch (...) {
+  return 0;
 }
 
 }  // extern "C"
