@@ -1,5 +1,8 @@
 """Sampling against its definition in 64 bits: tokens are equal, log-probabilities to FP32's own rounding."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -8,6 +11,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 LEAST = 2.0 ** -40
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def plain(x, u, t=None, k=None, p=None, mp=None):
@@ -274,3 +278,25 @@ def test_the_same_by_clusters_of_every_size(lib, vocab, kind, half):
         t, l = lib.sample(x[:rows], u[:rows], *pick(rows))
         assert torch.equal(t, want_t[:rows])
         assert torch.equal(l.nan_to_num(), want_l[:rows].nan_to_num())
+
+
+FIRST = """
+import torch, weight_only_int4_quant_gb300 as lib
+lib.load()
+g = torch.Generator("cuda").manual_seed(3)
+x, u = torch.randn(40, 9000, device="cuda", generator=g), torch.rand(40, device="cuda", generator=g)
+p, tokens = torch.full((40,), 0.9, device="cuda"), torch.zeros(40, dtype=torch.int32, device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    lib.tl_sample(x, u, tokens, top_p=p)
+tokens.fill_(-7)
+graph.replay()
+assert torch.equal(tokens, lib.sample(x, u, top_p=p)[0])
+print("same")
+"""
+
+
+def test_a_first_call_may_be_captured(lib):
+    """What is asked of the device once may be asked while a stream is captured."""
+    r = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, cwd=ROOT)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr

@@ -1071,16 +1071,17 @@ tlq_status launch_one(const SampleParams& p, int rows, int blocks, size_t smem, 
   return cuda_error(cudaLaunchKernelEx(&lc, sample_kernel<T, STAGED>, p), "sample: launch");
 }
 
-// Clusters of this many blocks that run at once, with one or two blocks to an SM;
-// asked once.  A cluster lies in one GPC, so it is not SMs / blocks: of 152 SMs
-// clusters of 1 to 8 get 152, 76, 46, 36, 28, 23, 15 and 15, and with two blocks to
-// an SM 304, 152, 97, 74, 58, 46, 38 and 36.
+// Clusters of this many blocks that run at once, with one or two blocks to an SM
+// (of a kernel that is opted in to its shared memory); asked once for each number
+// of SMs.  A cluster lies in one GPC, so it is not SMs / blocks: of 152 SMs clusters
+// of 1 to 8 get 152, 76, 46, 36, 28, 23, 15 and 15, and with two blocks to an SM 304,
+// 152, 97, 74, 58, 46, 38 and 36.
 constexpr size_t kSmemOfTwo = (228u << 10) / 2 - 1024;
 template <class T>
 int clusters_at_once(int blocks, int resident) {
-  static std::atomic<int> known[kMaxBlocks + 1][3];
-  int n = known[blocks][resident].load(std::memory_order_relaxed);
-  if (n > 0) return n;
+  static std::atomic<int> known[kMaxBlocks + 1][3];  // SMs in the upper half, clusters in the lower
+  const int sms = device_info().sms, was = known[blocks][resident].load(std::memory_order_relaxed);
+  if (was >> 16 == sms) return was & 0xffff;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)blocks, 1, 1);
   lc.blockDim = dim3(kThreads, 1, 1);
@@ -1091,12 +1092,12 @@ int clusters_at_once(int blocks, int resident) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   lc.attrs = at;
   lc.numAttrs = 1;
-  if (opt_in_smem<sample_kernel<T, true>>(kMaxSmem) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, sample_kernel<T, true>, &lc) != cudaSuccess || n < 1) {
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, sample_kernel<T, true>, &lc) != cudaSuccess || n < 1 || n > 0xffff) {
     cudaGetLastError();
-    return std::max(1, device_info().sms / blocks * resident);  // the launch reports what is wrong
+    return std::max(1, sms / blocks * resident);  // the launch reports what is wrong
   }
-  known[blocks][resident].store(n, std::memory_order_relaxed);
+  known[blocks][resident].store(sms << 16 | n, std::memory_order_relaxed);
   return n;
 }
 
@@ -1108,6 +1109,8 @@ int clusters_at_once(int blocks, int resident) {
 // 80; 512 of 32000 FP16: one 102, two 116; 64 of 32000 FP16: four 39, two 44.
 template <class T>
 tlq_status launch_as(SampleParams p, int rows, cudaStream_t stream) {
+  const cudaError_t attr = opt_in_smem<sample_kernel<T, true>>(kMaxSmem);
+  if (attr != cudaSuccess) return cuda_error(attr, "sample: shared memory");
   const int sms = device_info().sms;
   int blocks = 0;
   size_t smem = 0;
