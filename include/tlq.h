@@ -730,9 +730,11 @@ size_t tl_kv4_attention_workspace_size(int q_heads, int heads, int head_dim, int
  *                 outside the cache counts as holding no tokens, and so do
  *                 those behind the table
  *   The other arguments, what is not written, and what a NaN does are as in
- *   tl_kv4_attention (without a window).  A batch whose queries are few (64
- *   rows of one key head, or any number where rows hold two groups) reads the
- *   prefix once for each 16 rows, from L2.
+ *   tl_kv4_attention (without a window).  A batch whose queries are few for the
+ *   prefix's table (a choice by both sizes; any where rows hold two groups)
+ *   reads the prefix once for each 8 or 16 rows of a key head, from L2; prompts
+ *   and long prefixes once for each 256.  prefix_pages is what the choice goes
+ *   by, so a table much longer than its prefix costs time.
  *   workspace     of tl_kv4_attention_prefix_workspace_size bytes or more
  *   Lengths are read on the GPU only, the prefix's too.  Deterministic.
  *   Returns as tl_kv4_attention.

@@ -11,6 +11,13 @@ pytestmark = pytest.mark.gpu
 U = 2.0 ** -11
 
 
+@pytest.fixture(autouse=True, params=[0, 30000], ids=["table", "long_table"])
+def spare(request, monkeypatch):
+    """Which kernels run goes by the table's length: 65 rows and more behind a short one by one kernel, behind a long
+    one by both."""
+    monkeypatch.setattr(Batch, "spare", request.param)
+
+
 def cached(blocks, ids, page, d, group, part):
     """Keys (0) or values (1) of pages in 64 bits: [heads, tokens, D]; a page outside the cache: None rows as NaN."""
     got = blocks[ids.clamp(0, blocks.shape[0] - 1)]
@@ -24,6 +31,8 @@ def cached(blocks, ids, page, d, group, part):
 
 
 class Batch:
+    spare = 0  # entries behind the prefix's own in the table that the kernels get
+
     def __init__(self, lib, prefix, lens, adds, hq, hkv, d, group, page, seed=0, spread=1.0):
         g = torch.Generator("cuda").manual_seed(seed)
         self.lib, self.page, self.d, self.group, self.hq, self.hkv = lib, page, d, group, hq, hkv
@@ -37,7 +46,9 @@ class Batch:
         v = torch.randn(tokens, hkv, d, device="cuda", generator=g) * torch.exp(torch.randn(tokens, hkv, 1, device="cuda", generator=g))
         lib.tl_kv4_append(self.cache, k.half(), v.half(), torch.arange(tokens, device="cuda"))
         i32 = dict(dtype=torch.int32, device="cuda")
-        self.prefix_len, self.prefix_table = torch.tensor([prefix], **i32), order[:shared].int().contiguous()
+        self.prefix_len, self.whole_table = torch.tensor([prefix], **i32), torch.full((shared + self.spare,), -1, **i32)
+        self.prefix_table = self.whole_table[:shared]
+        self.prefix_table[:] = order[:shared].int()
         self.table = torch.full((len(lens), max(need + [1]) + 1), -1, **i32)
         at = shared
         for i, n in enumerate(need):
@@ -55,7 +66,7 @@ class Batch:
         args = dict(workspace=self.cache.prefix_workspace(self.hq, self.q.shape[0], self.max_q))
         args.update(k)
         self.lib.tl_kv4_attention_prefix(self.cache, self.q, out, self.start, self.lens, self.table, self.prefix_len,
-                                         self.prefix_table, self.max_q, self.scale, **args)
+                                         self.whole_table, self.max_q, self.scale, **args)
         return out
 
     def exact(self):
@@ -236,9 +247,9 @@ def test_strided_rows(lib):
 
 def test_contradicting_lengths_write_within_their_rows(lib):
     """Requests whose queries overlap or run backwards: the numbers of such rows mean nothing, rows of sound
-    requests are what they are alone, and the rows of no request are left."""
+    requests are right (the work, and so the sums, may be split elsewhere), and the rows of no request are left."""
     b = Batch(lib, 700, [90, 120, 40, 30], [20, 60, 1, 1], 16, 4, 128, 128, 16)
-    want = b.run()
+    want, (exact, tol) = b.run(), b.exact()
     start = b.start.tolist()
     out = torch.full((len(b.q) + 8, 16, 128), 9.0, dtype=torch.float16, device="cuda")[:len(b.q)]
     for bad in ([0, 20, 10, 81, 82], [0, 50, 30, 81, 82], [5, 5, 80, 81, 82], [0, 90, 80, 81, 82], [-3, 20, 80, 81, 82],
@@ -247,7 +258,24 @@ def test_contradicting_lengths_write_within_their_rows(lib):
         out.fill_(9.0)
         b.run(out=out)
         torch.cuda.synchronize()
-        assert torch.equal(out[81], want[81])  # the last request is sound in each
+        assert ((out[81].double() - exact[81]).abs() <= tol[81] + 2.0 ** -24).all()  # the last request is sound in each
     lib.tl_check_status()
     b.start[:] = torch.tensor(start, dtype=torch.int32)
     assert torch.equal(b.run(), want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("adds", [[1] * 33, [2, 47, 1], [200, 3]])
+def test_both_ways(lib, d, adds, monkeypatch):
+    """The same batch by one kernel and by both: within both bounds, and any prefix length behind either table."""
+    lens = [a + 37 * i % 151 for i, a in enumerate(adds)]
+    got = []
+    for spare in (0, 30000):
+        monkeypatch.setattr(Batch, "spare", spare)
+        b = Batch(lib, 700, lens, adds, 8, 2, d, d, 16, seed=5)
+        for n in (700, 1, 129, 0, 640):
+            b.prefix_len.fill_(n)
+            got.append(b.check().double())
+        _, tol = b.exact()
+    for one, two in zip(got[:5], got[5:]):
+        assert ((one - two).abs() <= 4 * tol + 2.0 ** -22).all()

@@ -253,17 +253,17 @@ G = 1 << 36
 def prefix(d=128, group=128, t=2):
     c = tlq._KV4Cache(64 * M, 10, 4, d, 16, group)
     return lib.tl_kv4_attention_prefix(ctypes.byref(c), M, 1024, 8, 16 * M, 1024, 3 * M, 4 * M, 5 * M, 4, 6 * M, 7 * M, 9, 2, t,
-                                       1, 0.1, G, G, None)
+                                       t, 0.1, G, G, None)
 
 def sample(half, vocab):
     return lib.tl_sample(M, half, vocab, 1, vocab, G, None, None, None, None, 2 * G, None, None)
 
 for device in (0, 1, 5, 0):
     fake.fake_device(device)
-    for form in ((128, 128, 2), (128, 64, 8), (64, 64, 4), (128, 128, 600), (64, 64, 600)):
+    for form in ((128, 128, 2), (128, 64, 8), (64, 64, 4), (128, 128, 2000), (64, 64, 2000)):
         st = prefix(*form)
         assert st == tlq.TLQ_OK, (device, form, st, tlq.tl_last_error())
-        assert fake.fake_launches() == (3 if form[2] == 600 else 2), form
+        assert fake.fake_launches() == (3 if form[2] == 2000 else 2), form
     for half, vocab in ((1, 1), (1, 131072), (0, 200000), (0, 1 << 20)):
         st = sample(half, vocab)
         assert st == tlq.TLQ_OK and fake.fake_launches() == 1, (device, half, vocab, st, tlq.tl_last_error())

@@ -163,6 +163,29 @@ tlq_status check_attention(const AttentionCall& c, KvAttention* a, bool* empty) 
 // 246 us, where rows in one group take 68).
 int few_rows_of(const tl_kv4_cache& c) { return c.head_dim == c.group ? kFewRows : 0x7fffffff; }
 
+// Whether the few-rows kernel takes a batch with a prefix alone, whatever its rows.
+// By the tables' capacity, since lengths are known on the GPU only.  What 300
+// measured batches come to, in us: a stage of 128 tokens takes the few-rows kernel
+// 0.0037 for 8 rows of a key head of 128 and 0.0026 of 64, half as much again and
+// more in prompts (whose items are short, and count two stages more); the other
+// kernel 0.022 and 0.016 for 256 rows, and 17 and 15 for its launch, its search and
+// its first stage.  Key and query heads of 128, 64 tokens: 8 and 32 behind 256 19 us
+// for 35, behind 2048 34 for 39, behind 8190 78 for 47; 1 and 4 behind 8190 20 for 36.
+// A prompt of 100 tokens, 8 and 32 heads: behind 16 18 for 23, behind 2048 46 for 33.
+bool few_rows_alone(const KvAttention& a) {
+  if (a.head_dim != a.cache.group) return true;  // as in few_rows_of()
+  auto stages_of = [&](int pages) { return ((long long)pages * a.cache.page + 127) / 128; };
+  const long long share = a.q_heads / a.cache.heads, rows = a.batch.tokens * share;
+  if (rows <= kFewRows) return true;
+  const bool prompts = a.batch.max_q * share > kFewRows, small = a.head_dim == 64;
+  const double prefix = (double)stages_of(a.batch.prefix_pages) * a.cache.heads;
+  const double own = prompts ? (double)(stages_of(a.batch.ld_table) + 2) * a.cache.heads : 0.0;
+  const double here = (prompts ? (small ? 0.0045 : 0.0065) : (small ? 0.0026 : 0.0037)) * (prefix + own) *
+                      (double)((rows + 7) / 8);
+  const double there = (small ? 15.0 : 17.0) + (small ? 0.016 : 0.022) * prefix * (double)((rows + 255) / 256);
+  return here < there;
+}
+
 // Rows that may lie in others' gaps (columns of a fused projection's rows).
 struct RowSet {
   const void* p;
@@ -416,7 +439,7 @@ tlq_status tl_kv4_attention_prefix(const tl_kv4_cache* cache, const uint16_t* q,
                     workspace_bytes},
       &a, &empty);
   if (st != TLQ_OK || empty) return st;
-  const int few = few_rows_of(*cache), d = cache->head_dim;
+  const int d = cache->head_dim, few = few_rows_alone(a) ? 0x7fffffff : kFewRows;
   const long long rows = (long long)tokens * q_heads;
   uint8_t* at = static_cast<uint8_t*>(workspace);
   uint8_t* sums = at + ((attention_workspace(d) + 255) & ~size_t(255));
