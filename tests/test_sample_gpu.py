@@ -280,6 +280,32 @@ def test_the_same_by_clusters_of_every_size(lib, vocab, kind, half):
         assert torch.equal(l.nan_to_num(), want_l[:rows].nan_to_num())
 
 
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("vocab,t,k", [(5000, 0.02, 50), (60000, 0.03, 300), (5000, 0.3, 4000), (40000, 0.25, 39000),
+                                       (3, 0.01, 2), (700, 0.001, 699)])
+def test_fewer_with_weight_than_k(lib, vocab, t, k, half):
+    """Cold rows: what is within 2^-40 of the greatest is less than top_k, from one value to more than a list holds."""
+    x, u, g = logits(9, vocab, vocab + k, half)
+    f = dict(t=torch.full((9,), t, device="cuda"), k=torch.full((9,), k, dtype=torch.int32, device="cuda"))
+    weight = ((x.float() - x.float().amax(1, keepdim=True)) / t * math.log2(math.e) > -40).sum(1)
+    assert (weight < k).any()
+    compare(lib, x, u, **f)
+    compare(lib, x, u, **f, p=torch.rand(9, device="cuda", generator=g))
+    compare(lib, x, u, **f, p=torch.rand(9, device="cuda", generator=g), mp=0.1 * torch.rand(9, device="cuda", generator=g))
+
+
+@pytest.mark.parametrize("vocab", [3000, 70000])
+def test_kept_sets_of_every_size(lib, vocab):
+    """top_p's cut behind 1 to some hundreds of values: by a ranked list, and around an estimate."""
+    x, u, g = logits(96, vocab, 17, False)
+    t = torch.full((96,), 0.9, device="cuda")
+    ordered = torch.softmax(x.double() / 0.9, 1).sort(1, descending=True)[0].cumsum(1)
+    behind = (1.09 ** torch.arange(96, device="cuda")).long().clamp(1, vocab - 1)  # 1 .. 3400
+    behind = behind.clamp(max=vocab // 2)
+    p = ordered.gather(1, behind[:, None])[:, 0].float()
+    compare(lib, x, u, t=t, p=p)
+
+
 FIRST = """
 import torch, weight_only_int4_quant_gb300 as lib
 lib.load()

@@ -29,11 +29,11 @@
 // clocks each, bound them.
 // top-k, and few kept values: one block gets all that may be kept as a list.
 //
-// 256 rows of 100003 FP32, top-p: 165 us, 6 waves of clusters of six blocks (clusters
+// 256 rows of 100003 FP32, top-p: 164 us, 6 waves of clusters of six blocks (clusters
 // of eight, 7 to 8 waves: 190).  Of 27 us of a block with 12500 values the exact
 // weights (50 instructions a value, two values at a time) take 6.6, counting 4.2,
 // loading 3, the rest barriers of the cluster and short phases of the block.  64 rows
-// of 131072 FP16, all filters: 43.5 us.  One row of 32000: 12.4 us, a chain of ten
+// of 131072 FP16, all filters: 42 us.  One row of 32000: 12.4 us, a chain of ten
 // short phases.
 #include <cooperative_groups.h>
 
@@ -185,6 +185,10 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 
 constexpr int kGroups = 64, kGroupBins = kBins / kGroups;
 constexpr int kList = 512;  // candidates for a cut that are ranked one by one
+// Beyond this many a cut by mass is looked for around its estimate: each candidate is
+// compared with all others, so 420 of them take 13 us, 170 take 3, and that way takes 4
+// (60 batches of all kinds: 17.1 us in the mean with 128 or 192, 17.9 with 512).
+constexpr int kRanked = 192;
 static_assert(kGroupBins == 32, "a lane to a bin");
 static_assert(kWarps >= kMaxBlocks && kList <= kThreads, "a warp to a block, a thread to a candidate");
 constexpr int kHeavyGroups = 12;  // groups whose weights are added up exactly beside the counts: 2^-6 and more
@@ -697,19 +701,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       // few enough: block 0 gets them all
       find_bin(s, cluster, C, rank, false, true, (uint32_t)k, 0);
       const int bin = s.bin;
-      if (bin >= 0 && s.before_count + s.bin_count <= (uint32_t)kList) {
+      if (bin < 0 || s.before_count + s.bin_count <= (uint32_t)kList) {
+        // (bin < 0: fewer than k have weight)
         for (int i = tid; i < n; i += kThreads) {
           const float x = at(i);
-          if (first_bin(r, x) <= bin) collect(x, i);
+          if (first_bin(r, x) <= (bin < 0 ? kBins - 1 : bin)) collect(x, i);
         }
-        merge_lists(s, cluster, 1);
-        if (rank == 0) finish_list((uint32_t)k, 0);
-        return;
+        merge_lists(s, cluster, bin < 0 ? C : 1);
+        if (bin >= 0 || s.merged <= (uint32_t)kList) {
+          if (rank == 0) finish_list((uint32_t)k, 0);
+          return;
+        }
       }
       cluster.sync();  // the histogram is read by all others until here
     } else {
       const About about = find_about(s, cluster, C, tp);
-      const bool few = about.upto <= (uint32_t)kList;
+      const bool few = about.upto <= (uint32_t)kRanked;
       // few: all up to the end of the group after the bin's; else what lies around
       // the estimate, and the exact sum above that
       const int low = few ? 0 : about.k - about.around;
