@@ -382,10 +382,11 @@ __device__ __forceinline__ uint64_t share_of(float p, uint64_t mass) {
 
 // About where the mass reaches p of the whole, from the counts: weights count as
 // those of their bins' middles, the heaviest groups' exactly.  The same in every
-// block.  upto: values of that bin's group, the groups before it and the one after.
+// block.  upto: values of that bin's group, those before it and the next that has any
+// after it; end: the k there.
 struct About {
-  int k, around;  // around: how many k on either side to look at (-1: too many values lie there)
-  int bin;
+  int low, high;  // the k to look at (low > high: too many values lie there)
+  int end;
   uint32_t upto;
 };
 __device__ __forceinline__ About find_about(Shared& s, cg::cluster_group& cluster, int C, float p) {
@@ -429,10 +430,11 @@ __device__ __forceinline__ About find_about(Shared& s, cg::cluster_group& cluste
   const float before = __shfl_sync(0xffffffffu, sum - a[0] - a[1], from), first = __shfl_sync(0xffffffffu, a[0], from);
   const bool second = before + first < want;
   const int group = 2 * from + (second ? 1 : 0);
-  // values up to the group after it
-  const uint32_t through = __shfl_sync(0xffffffffu, count, from);
-  const uint32_t next = __shfl_sync(0xffffffffu, c[0], min(from + 1, 31));
-  const uint32_t upto = second ? through + (from < 31 ? next : 0) : through;
+  // the values up to the pair of groups after it that has any
+  const uint32_t through = __shfl_sync(0xffffffffu, second ? count : count - c[1], from);
+  const int last = __ffs(__ballot_sync(0xffffffffu, count > through) | 0x80000000u) - 1;
+  const uint32_t upto = __shfl_sync(0xffffffffu, count, last);
+  const int end = 4 * (2 * last + 2) * kGroupBins - 1;
   const float scale = group < kHeavyGroups ? (float)heavy * 1.13686838e-13f / estimate : 1.0f;
   if (warp < C) s.fine_count[warp][lane] = cluster.map_shared_rank(&s, warp)->hist[group * kGroupBins + lane];
   __syncthreads();
@@ -452,14 +454,17 @@ __device__ __forceinline__ About find_about(Shared& s, cg::cluster_group& cluste
   const float own = __shfl_sync(0xffffffffu, (float)n * middle_of(group * kGroupBins + lane) * scale, lane_of);
   const float into = fminf(fmaxf((want - __shfl_sync(0xffffffffu, at, lane_of) + own) / own, 0.f), 0.999f);
   const uint32_t in_bin = __shfl_sync(0xffffffffu, n, lane_of);
-  // some 128 values are looked at, by how densely they lie here: a cut outside of them
-  // costs the general way (15 to 40 us), more of them the ranking (200 us with 256 for 191
-  // in 256 rows of 100003; with 96 of them single rows of 200000 missed)
+  // some 110 values are looked at, by how densely they lie here, but half a k to either
+  // side at least: a cut outside of them costs the general way (15 to 40 us), more of
+  // them the ranking (200 us with 256 for 191 in 256 rows of 100003).  With whole k
+  // about the estimate's, 4 rows of 100 missed of 150000 values; now 1 of 3600.
   const uint32_t own_group = __shfl_sync(0xffffffffu, second ? c[1] : c[0], from);
   const uint32_t after = __shfl_sync(0xffffffffu, second ? c[0] : c[1], second ? min(from + 1, 31) : from);
   const float dense = fmaxf((float)in_bin * 0.25f, (float)max(own_group, after) * (1.0f / 128.0f));  // of a k
-  const int around = bin >= kBins - 1 || dense > 400.f ? -1 : (int)fminf(64.0f / fmaxf(dense, 1.0f), 64.0f);
-  return About{4 * bin + (int)(4.0f * into), around, bin, upto};
+  const float place = 4.0f * ((float)bin + into);
+  const float reach = fminf(fmaxf(52.0f / fmaxf(dense, 1.0f), dense < 200.f ? 0.5f : 0.f), 64.0f);
+  if (bin >= kBins - 1 || dense > 400.f) return About{1, 0, end, upto};
+  return About{(int)fmaxf(place - reach, 0.f), (int)(place + reach), end, upto};
 }
 
 // What the blocks have collected in s.local goes into list[1] of block 0, or of
@@ -717,10 +722,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     } else {
       const About about = find_about(s, cluster, C, tp);
       const bool few = about.upto <= (uint32_t)kRanked;
-      // few: all up to the end of the group after the bin's; else what lies around
+      // few: all up to the end of the next groups with values; else what lies around
       // the estimate, and the exact sum above that
-      const int low = few ? 0 : about.k - about.around;
-      const int high = few ? 4 * (about.bin / kGroupBins + 2) * kGroupBins - 1 : about.k + about.around;
+      const int low = few ? 0 : about.low;
+      const int high = few ? about.end : about.high;
       uint64_t all = 0, above = 0, m = 0;
 #pragma unroll 1
       for (int i = warp * seg + lane; i < min(n, (warp + 1) * seg); i += 64) {
