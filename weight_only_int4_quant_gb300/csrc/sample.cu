@@ -492,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long row = blockIdx.x / C;
   pdl_launch_dependents();
+  cluster_arrive();  // waited for before the first look at another block's memory
   for (int i = tid; i < 256; i += kThreads) s.powers[i] = kPowers.v[i];
   for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
   if (tid == 0) s.merged = s.pushed = 0;
@@ -551,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     s.warp_bad[warp] = bad;
   }
   __syncthreads();
+  cluster_wait();  // all blocks have begun: their shared memory is there
   if (tid < C) {
     for (int w = 0; w < kWarps; ++w) {
       if (s.warp_top[w] > top || (s.warp_top[w] == top && s.warp_at[w] < top_at)) {
