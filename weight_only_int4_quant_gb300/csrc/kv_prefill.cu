@@ -347,6 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   __shared__ PWalk walks[kThreads / 32];
   __shared__ PSegment segments[kThreads / 32];
   __shared__ long long request_units[kThreads];
+  __shared__ uint16_t long_requests[kThreads];  // those that a warp counts together
+  __shared__ int long_count;
 
   const int tid = threadIdx.x, warp = (int)uniform(tid >> 5), lane = tid & 31;
   pdl_launch_dependents();
@@ -368,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
       mbar_init(&bar->t_empty[i], 8);
     }
     fence_mbar_init();
+    long_count = 0;
   }
   if (warp == 0) tmem_alloc(&bar->tmem, 512);
   tc_fence_before();
@@ -388,20 +391,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_attention_kernel(const Pr
   const int requests = kv_requests<kShared>(p.batch);
   const bool small = requests <= kThreads;
   if (small) {
-    // short ones a thread to a request, those of many row tiles a warp each
-    long long v = 0;
-    bool many = false;
+    // short ones a thread to a request; those of many row tiles a warp each, dealt to
+    // all warps wherever they stand among the requests
     if (tid < requests) {
       const KvRequest r = kv_request_or_prefix<kShared>(p.batch, p.cache.page, tid);
-      many = many_rows(p, r) > 4 * kItemRows;
-      if (!many) v = lane_units(r, 0, 1);
-      request_units[tid] = v;
+      if (many_rows(p, r) > 4 * kItemRows)
+        long_requests[atomicAdd(&long_count, 1)] = (uint16_t)tid;  // in any order: each has its own sum
+      else
+        request_units[tid] = lane_units(r, 0, 1);
     }
-    uint32_t left = __ballot_sync(0xffffffffu, many);
-    while (left) {
-      const int i = (tid & ~31) + __ffs(left) - 1;
-      left &= left - 1;
-      v = lane_units(kv_request_or_prefix<kShared>(p.batch, p.cache.page, i), lane, 32);
+    __syncthreads();
+    for (int j = warp; j < long_count; j += kThreads / 32) {
+      const int i = long_requests[j];
+      long long v = lane_units(kv_request_or_prefix<kShared>(p.batch, p.cache.page, i), lane, 32);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if (lane == 0) request_units[i] = v;
