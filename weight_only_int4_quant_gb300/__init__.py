@@ -229,7 +229,8 @@ def _load_binding(lib):
 
 def _read_tensors(module):
     """Lets the C API module read tensors past the interpreter (csrc/tensors.cpp),
-    where that was built for this very torch."""
+    where that was built for this very torch: as the file beside it says and as it
+    says itself (a process may look while another builds)."""
     import torch
 
     try:
@@ -237,7 +238,10 @@ def _read_tensors(module):
             if f.read() != torch.__version__:
                 return
         tensors = ctypes.CDLL(_TENSORS_PATH)
-    except OSError:
+        tensors.tlq_torch_version.restype = ctypes.c_char_p
+    except (OSError, AttributeError):
+        return
+    if tensors.tlq_torch_version().decode().split("+")[0] != torch.__version__.split("+")[0]:
         return
     module.read_tensors(ctypes.cast(tensors.tlq_tensor_read, ctypes.c_void_p).value, torch.Tensor, torch.nn.Parameter)
 

@@ -111,9 +111,14 @@ def build_tensors(force: bool = False) -> bool:
             if os.path.exists(path):
                 os.remove(path)
         return False
+    # the version only ever stands beside the library it is of: it goes first and comes back last, whole
+    if os.path.exists(TENSORS_OF):
+        os.remove(TENSORS_OF)
     os.replace(tmp, TENSORS)
-    with open(TENSORS_OF, "w") as f:
+    tmp = TENSORS_OF + ".tmp%d" % os.getpid()
+    with open(tmp, "w") as f:
         f.write(version)
+    os.replace(tmp, TENSORS_OF)
     return True
 
 
