@@ -279,13 +279,14 @@ def _on(stream):
 
 
 def _result(stream, *tensors):
-    """Tensors allocated under _on(stream), for the caller: their memory goes
-    back only when the caller's stream is done with them too."""
+    """Tensors allocated under _on(stream) (or None), for the caller: their memory
+    goes back only when the caller's stream is done with them too."""
     if stream is not None:
         import torch
 
         for t in tensors:
-            t.record_stream(torch.cuda.current_stream())
+            if t is not None:
+                t.record_stream(torch.cuda.current_stream())
     return tensors[0] if len(tensors) == 1 else tensors
 
 
@@ -1132,12 +1133,12 @@ def rope_table(num_positions: int, inv_freq, scale: float = 1.0, stream=None):
 
 
 def qk_norm_rope(rope, q, k, positions, q_weight=None, k_weight=None, eps: float = 1e-6, stream=None):
-    """(q, k) normed and rotated, compact.  Tokens that are passed over hold zeros."""
+    """(q, k) normed and rotated, compact; either may be None, and then is in the
+    result.  Tokens that are passed over hold zeros."""
     import torch
 
     with _on(stream):
-        q_out = torch.zeros(q.shape, dtype=torch.float16, device=q.device)
-        k_out = torch.zeros(k.shape, dtype=torch.float16, device=k.device)
+        q_out, k_out = (None if x is None else torch.zeros(x.shape, dtype=torch.float16, device=x.device) for x in (q, k))
         tl_qk_norm_rope(rope, q, k, positions, q_out, k_out, q_weight, k_weight, eps, stream)
     return _result(stream, q_out, k_out)
 
