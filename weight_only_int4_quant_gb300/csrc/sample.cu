@@ -126,7 +126,7 @@ __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 // exp((x - top) / T) * 2^43 of two values, 0 below 2^-40, and their k.  Two at
 // a time: the FP32 part is in packed operations (none of them a product that
 // goes into a plain sum, which the compiler would join).  The lowest bit is set
-// instead of rounding the last shift.
+// instead of rounding the last shift, where there is one: the largest is 2^43.
 __device__ __forceinline__ void weights_of(float x0, float x1, const Row& r, const uint64_t* __restrict__ powers,
                                            uint64_t (&w)[2], int (&step)[2]) {
   // x - top = d + d_lo exactly (Knuth's two-sum)
@@ -157,7 +157,7 @@ __device__ __forceinline__ void weights_of(float x0, float x1, const Row& r, con
     const uint64_t power = powers[k & 255];
     const uint64_t v = power + (uint64_t)(((long long)(int)(power >> 13) * z) >> 26);
     const bool some = (i ? nh.y : nh.x) <= kOctaves;
-    w[i] = some ? (v >> (k >> 8)) | 1ull : 0;
+    w[i] = some ? (v >> (k >> 8)) | (uint32_t)min(k >> 8, 1) : 0;
     step[i] = some ? k : kNoStep;
   }
 }
