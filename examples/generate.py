@@ -3,7 +3,7 @@
     python examples/generate.py [--steps N]
 
 The common beginning goes into the cache once.  A step of all requests is then
-eight calls and no host copy of a length or a token:
+seven calls and no host copy of a length or a token:
 
     tl_kv_plan               tables, slots and positions of the requests' own tokens
     tl_quant_gemm_ws         the fused projection: queries, keys, values
@@ -40,7 +40,7 @@ class Model:
         near_one = lambda: (1 + 0.1 * torch.randn(head_dim, device="cuda", generator=self.gen)).half()  # noqa: E731
         self.q_weight, self.k_weight = near_one(), near_one()
         freq = 10000.0 ** (-torch.arange(0, head_dim, 2, device="cuda", dtype=torch.float64) / head_dim)
-        self.rope = tlq.Rope(tlq.rope_table(positions, freq))
+        self.turns = tlq.rope_table(positions, freq)
         self.cache = tlq.KV4Cache(pages, kv_heads, head_dim, page_size, group=head_dim)
         i32 = dict(dtype=torch.int32, device="cuda")
         self.table = torch.full((requests, pages), -1, **i32)
@@ -79,11 +79,14 @@ class Model:
         self.prefix_len = torch.tensor([n], dtype=torch.int32, device="cuda")
         self.prefix_table = self.order[:-(-n // p)].contiguous()
         self.free_pages = self.order[-(-n // p):].contiguous()
+        # own tokens lie behind the common ones: their positions count from a later row of the table, and what the
+        # plan marks as no token stays marked
+        rope, self.rope = tlq.Rope(self.turns), tlq.Rope(self.turns[n:])
         for at in range(0, n, len(self.rows)):
             pos = torch.arange(at, min(n, at + len(self.rows)), dtype=torch.int32, device="cuda")
             slots = self.prefix_table.long()[pos // p] * p + pos % p
             _, k, v = self.heads(self.embed[ids[at:at + len(pos)]])
-            tlq.tl_kv4_append_rope(self.cache, self.rope, k, v, pos, slots, self.k_weight, eps=EPS)
+            tlq.tl_kv4_append_rope(self.cache, rope, k, v, pos, slots, self.k_weight, eps=EPS)
 
     def step(self, ids, added, max_q, last, uniform, temperature, top_k, top_p):
         """Each request's next token, after its tokens of this step (ids, laid out request after request; last: the
@@ -96,9 +99,8 @@ class Model:
                        free_head=self.counts[was][2:3])
         self.cached = seq
         q, k, v = self.heads(self.embed[ids])
-        positions = self.token_pos[:t] + self.prefix_len  # own tokens lie behind the common ones
-        tlq.tl_kv4_append_rope(self.cache, self.rope, k, v, positions, self.slots[:t], self.k_weight, q, q, self.q_weight,
-                               EPS)
+        tlq.tl_kv4_append_rope(self.cache, self.rope, k, v, self.token_pos[:t], self.slots[:t], self.k_weight, q, q,
+                               self.q_weight, EPS)
         self.queries, mixed, out = q, self.mixed[:t], self.out[:t]
         tlq.tl_kv4_attention_prefix(self.cache, q, mixed, self.q_start, seq, self.table, self.prefix_len,
                                     self.prefix_table, max_q, self.head_dim ** -0.5, workspace=self.workspace)
