@@ -733,8 +733,9 @@ size_t tl_kv4_attention_workspace_size(int q_heads, int heads, int head_dim, int
  *   tl_kv4_attention (without a window).  A batch whose queries are few for the
  *   prefix's table (a choice by both sizes; any where rows hold two groups)
  *   reads the prefix once for each 8 or 16 rows of a key head, from L2; prompts
- *   and long prefixes once for each 256.  prefix_pages is what the choice goes
- *   by, so a table much longer than its prefix costs time.
+ *   and long prefixes once for each 256.  The choice goes by prefix_pages and,
+ *   in batches with prompts, by ld_table: tables much longer than what they hold
+ *   can cost time.
  *   workspace     of tl_kv4_attention_prefix_workspace_size bytes or more
  *   Lengths are read on the GPU only, the prefix's too.  Deterministic.
  *   Returns as tl_kv4_attention.
@@ -814,7 +815,9 @@ tlq_status tl_qk_norm_rope(const tl_rope* rope, const int32_t* positions, const 
  *   k, v, slots  as in tl_kv4_append;  the rest as in tl_qk_norm_rope.  A token
  *   with a negative position is passed over altogether, one whose slot is
  *   outside the cache brings its queries only; a position at or past
- *   num_positions gives a key that stands for NaN.
+ *   num_positions gives a key that stands for NaN.  Behind a shared prefix,
+ *   tl_kv_plan's positions count from the prefix on: a rope whose table begins
+ *   at the prefix's last row + 1 takes them as they are, its -1 too.
  *   Bit-exact; deterministic.  Returns as tl_kv4_append.
  */
 tlq_status tl_kv4_append_rope(const tl_kv4_cache* cache, const tl_rope* rope, const int32_t* positions,
@@ -835,8 +838,10 @@ tlq_status tl_kv4_append_rope(const tl_kv4_cache* cache, const tl_rope* rope, co
  *   the first is always kept.  The row's token is the first kept one, by index,
  *   at which the running sum of the kept weights passes uniform times their
  *   sum; its log-probability is ln(w / that sum).  Weights below 2^-40 count as
- *   none.  They are held as whole numbers, 2^43 for the largest and each within
- *   about 2^-39 of it, so sums are exact whatever their order.
+ *   none.  They are held as whole numbers, 2^43 for the largest: each to about
+ *   2^-39 of its own value and one unit, 2^-43 of the largest (min_p is compared
+ *   with these), so sums are exact whatever their order.  A difference x - max x
+ *   past FP32's range counts as -infinity.
  *
  *   logits       FP16 (fp16 = 1) or FP32 (0) [rows][vocab], row stride ld
  *                (elements); -infinity: a token that is not to be drawn.  A row

@@ -142,7 +142,7 @@ tlq_status launch_kv4_finish_shared(const KvAttention& a, int few_rows, const Kv
   lc.attrs = &at;
   lc.numAttrs = pdl_enabled() ? 1 : 0;
   // Rows of prompts lie in one or two parts, and there are many of them: fewer
-  // registers (992 queries: 337 us with four, 346 with eight).  Single tokens' lie in
+  // registers (992 queries: 329 us with four, 341 with eight).  Single tokens' lie in
   // many: more under way (four requests: 11.2 us with eight, 11.8 with four).
   const bool prompts = (long long)a.batch.max_q * (a.q_heads / a.cache.heads) > few_rows;
   auto kernel = a.head_dim == 64 ? (prompts ? finish_kernel<64, 4> : finish_kernel<64, 8>)

@@ -65,8 +65,8 @@ constexpr int kRows = 128;        // rows of a tile
 constexpr int kItemRows = 256;    // rows of an item: two tiles
 constexpr int kHalf = 64;         // tokens whose weights are handed over at once
 constexpr int kItemCost = kShared ? 6 : 2;  // what beginning and ending an item costs, in stages; with a
-                                            // prefix short items lie beside long ones (346 us with 6, 348 with 4,
-                                            // 358 with 2: 992 queries behind 12001 tokens)
+                                            // prefix short items lie beside long ones (329 us with 6, 332 with 4,
+                                            // 342 with 2: 992 queries behind 12001 tokens)
 constexpr int kCodeWarps = 3;     // warps that write the K and V tiles
 constexpr int kThreads = (8 + kCodeWarps + 1) * 32;
 constexpr float kHeadroom = 6.0f;   // a new reference puts the largest weight at 2^6

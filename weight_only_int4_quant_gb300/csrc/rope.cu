@@ -20,7 +20,7 @@
 // a turn ahead.  A block's rows are all queries, all keys or all values; values go
 // the way of the plain append.
 //
-// 8192 tokens x 40 heads of 128 take 34.4 us (5.0 TB/s, three quarters of a copy's
+// 8192 tokens x 40 heads of 128 take 34.2 us (5.0 TB/s, three quarters of a copy's
 // rate): three blocks of 80 registers a thread to an SM keep 24 KB under way, and
 // four blocks spill (43 us).  Up to 4 rows to a lane take the append of 16001 tokens,
 // 32 / 8 heads, with its read from 113 us to 120, up to 16 from 111 to 115, up to 48 to

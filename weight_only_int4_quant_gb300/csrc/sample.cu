@@ -9,8 +9,10 @@
 // Which token that is depends on the last bits of long sums, so the weights are
 // whole numbers, 2^43 for the largest, and their sums exact: the same whatever
 // the order, and two rows differ only where the weights do.  A weight comes
-// within about 2^-39 of its value: the exponent in two FP32 numbers (x - max
-// exactly, times log2(e) / T), 2^(-j/256) from a table and a cubic for the rest.
+// within about 2^-39 of its value (the exponent in two FP32 numbers: x - max
+// exactly, times log2(e) / T; 2^(-j/256) from a table and a cubic for the rest),
+// and then to a whole number: one of 2^-20 is good to 2^-23, one of 2^-40 to an
+// eighth, in sums that are 2^43 at least.
 // FP64, the plain way, would take 30 times the arithmetic's time here (2
 // operations a clock and SM).
 //
@@ -29,12 +31,12 @@
 // clocks each, bound them.
 // top-k, and few kept values: one block gets all that may be kept as a list.
 //
-// 256 rows of 100003 FP32, top-p: 164 us, 6 waves of clusters of six blocks (clusters
-// of eight, 7 to 8 waves: 190).  Of 27 us of a block with 12500 values the exact
+// 256 rows of 100003 FP32, temperature and top-p: 166 us, 6 waves of clusters of six
+// blocks.  Of 27 us of a block with 12500 values (of eight to a row) the exact
 // weights (50 instructions a value, two values at a time) take 6.6, counting 4.2,
 // loading 3, the rest barriers of the cluster and short phases of the block.  64 rows
-// of 131072 FP16, all filters: 42 us.  One row of 32000: 12.4 us, a chain of ten
-// short phases.
+// of 131072 FP16, all filters: 41 to 46 us.  One row of 32000: 10 to 15 us by its
+// values, a chain of ten short phases.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -1118,9 +1120,11 @@ int clusters_at_once(int blocks, int resident) {
 // How many blocks take a row: whichever needs the least time by two lines fitted to
 // 50 measurements (top-p, rows of 32000 and more): a wave of rows takes 11.5 us and
 // 0.65 for every 1000 values of a block, or, where two blocks share an SM, 12 and
-// 1.22.  256 rows of 100003 FP32: six blocks 188 us, three 195, eight 218; 64 of
-// 131072 FP16: four 52, two 54, eight 68; 40 of 200000 FP32: six 66, five 72, eight
-// 80; 512 of 32000 FP16: one 102, two 116; 64 of 32000 FP16: four 39, two 44.
+// 1.22.  By blocks to a row, top-p of 0.85 to 0.99, the first being the choice: 256
+// rows of 100003 FP32 six 201 us, three 212, seven 225, eight 231; 64 of 131072 FP16
+// four 61, two 65, eight 74; 40 of 200000 FP32 six 75, five 83, eight 91; 512 of
+// 32000 FP16 one 108, two 118; 64 of 32000 FP16 four 26, three 30, two 35; one of
+// 32000 eight 16, four 18, one 37.
 template <class T>
 tlq_status launch_as(SampleParams p, int rows, cudaStream_t stream) {
   const cudaError_t attr = opt_in_smem<sample_kernel<T, true>>(kMaxSmem);
