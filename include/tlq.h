@@ -817,7 +817,7 @@ tlq_status tl_qk_norm_rope(const tl_rope* rope, const int32_t* positions, const 
  *   outside the cache brings its queries only; a position at or past
  *   num_positions gives a key that stands for NaN.  Behind a shared prefix,
  *   tl_kv_plan's positions count from the prefix on: a rope whose table begins
- *   at the prefix's last row + 1 takes them as they are, its -1 too.
+ *   at the row behind the prefix's last takes them as they are, its -1 too.
  *   Bit-exact; deterministic.  Returns as tl_kv4_append.
  */
 tlq_status tl_kv4_append_rope(const tl_kv4_cache* cache, const tl_rope* rope, const int32_t* positions,
